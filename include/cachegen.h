@@ -340,6 +340,187 @@ cg_status cg_int8_encode(const void *kv, int64_t rows, int32_t channels, void *q
 cg_status cg_int8_decode(const void *q, const float *scales, int64_t rows, int32_t channels,
                          void *kv_out, cg_stream_t stream);
 
+/* A KV cache held in 4 bits, in pages, that attention reads directly: for
+ * serving from a cache that stays compressed on the GPU. It takes the rows
+ * that cg_decode restores (kv[l][0] and kv[l][1] are its k and v) or that a
+ * model has just computed, and gives them back for cg_encode. These calls
+ * are additions of this library; the pages describe none of them.
+ *
+ *   quantise   per (token, head) row of head_size channels and group of
+ *              `group` channels: lo = min x, hi = max x,
+ *              s = bf16_rne(fp32(fp32(hi - lo) / 15));
+ *              n = min(15, round_half_even(fp32(fp32(x - lo) / s))),
+ *              n = 0 where s = 0                        (4 bits, s and lo bf16)
+ *   value      x^ = lo + s n; cg_int4_load gives bf16_rne(fp32(lo + fp32(s n)))
+ *   attention  out_i = sum_j p_ij v^_j, p_i = softmax over the visible j of
+ *              scale q_i . k^_j. Query i of a request with n queries and m
+ *              cached tokens (its own among them) stands at position
+ *              x = m - n + i and sees j when j <= x and (window == 0 or
+ *              x - j < window or j < sinks). A query that sees nothing gets 0.
+ *
+ * Layout. data is [num_layers][num_pages][num_heads][page_tokens / 16] blobs
+ * of 16 tokens; a blob of head size D with g = D / group is 16 (D + 8 g) bytes:
+ *   K codes   [16 tokens][D/2]: channel c in byte c%32/8 * D/8 + c/32 * 4 + c%8/2
+ *   K params  [16 tokens][g] of (s, lo), two bf16
+ *   V codes   [8 token pairs][D]: channel c of token 2p + b in byte
+ *             c%32/4 * D/8 + c/32 * 4 + 2 b + c%4/2
+ *   V params  as K params
+ * with the even channel of a byte in its low half: the words that one thread
+ * of a matrix instruction needs lie side by side, and a head's tokens of a
+ * page come in one bulk copy. Slot s of a layer is token s % page_tokens of
+ * page s / page_tokens.
+ *
+ * status: 16 bytes (16-byte aligned) that the caller clears once; a call sets
+ * the first word when it meets an error on the device and it has none yet.
+ * Read it with cg_last_device_error(NULL, status, ...). Calls never clear it,
+ * so it costs a call nothing and one read covers many calls.
+ *
+ * Limits (CG_ERR_UNSUPPORTED): head_size 64 or 128, group 32, 64 or 128 and
+ * at most head_size, page_tokens a multiple of 16 up to 1024, num_layers *
+ * num_pages * num_heads and num_pages * page_tokens below 2^31. data must be
+ * 256-byte aligned. */
+typedef struct cg_int4_cache {
+    void *data;
+    void *status;
+    int32_t num_layers;
+    int32_t num_pages;
+    int32_t page_tokens;
+    int32_t num_heads;
+    int32_t head_size;
+    int32_t group;
+} cg_int4_cache;
+
+/* Bytes of a cache's data (its data and status pointers are not looked at).
+ * Host only. */
+cg_status cg_int4_cache_bytes(const cg_int4_cache *cache, size_t *bytes);
+
+/* K and V rows: bf16 [layers][tokens][num_heads][head_size] with strides in
+ * elements, channels contiguous; both pointers 16-byte aligned and every
+ * stride a multiple of 8. A layer of cg_decode's output has k = kv[l][0],
+ * v = kv[l][1], a layer stride of 2*T*C, a token stride of C and a head
+ * stride of head_size. */
+typedef struct cg_kv_rows {
+    void *k;
+    void *v;
+    int64_t k_layer_stride, k_token_stride, k_head_stride;
+    int64_t v_layer_stride, v_token_stride, v_head_stride;
+} cg_kv_rows;
+
+/* cg_int4_store: quantise rows of `layers` layers into layers [first_layer,
+ * first_layer + layers) of the cache: token t goes to slot slots[t] (device,
+ * int32 [tokens]) of every layer. Slot -1 skips the token (padding); any
+ * other slot outside the cache is skipped with CG_ERR_CORRUPT in status. Two
+ * tokens of one call must not have the same slot (which of their parts stay
+ * is then undefined). A group with inf or NaN, or whose hi - lo overflows,
+ * sets CG_ERR_NONFINITE and is stored as zeros.
+ *
+ * cg_int4_load: the other way, into rows. Slot -1 gives zeros, any other slot
+ * outside the cache zeros and CG_ERR_CORRUPT. The same slot may occur often.
+ *
+ * Both are asynchronous on stream, in one launch. */
+cg_status cg_int4_store(const cg_int4_cache *cache, int32_t first_layer, int32_t layers,
+                        const cg_kv_rows *rows, const int32_t *slots, int64_t tokens,
+                        cg_stream_t stream);
+cg_status cg_int4_load(const cg_int4_cache *cache, int32_t first_layer, int32_t layers,
+                       const cg_kv_rows *rows, const int32_t *slots, int64_t tokens,
+                       cg_stream_t stream);
+
+/* Most requests of one cg_pages_grow or cg_int4_attention call. */
+#define CG_MAX_REQUESTS 8192
+
+/* Pages and slots for the new tokens of a batch, worked out on the GPU from
+ * the requests' lengths, so that a serving loop (or a captured graph) needs
+ * no host round trip. Request r holds lens[r] tokens in ceil(lens[r] /
+ * page_tokens) pages, whose ids stand in row r of block_table (int32, rows
+ * table_stride elements apart, table_width entries); counts[r] tokens are new.
+ * The pages that they need beyond those are taken from the end of the list
+ * free_pages[0 .. *free_count): the k-th page needed, by request and then by
+ * position, is free_pages[*free_count - 1 - k]. The call writes
+ *   block_table  the ids of the pages taken; no other entry
+ *   cu_out       int32 [requests + 1]: exclusive prefix sum of counts
+ *   lens_out     int32 [requests]: lens + counts (may be lens itself)
+ *   free_count_out  int32 [1]: pages left (may be free_count itself)
+ *   slots_out    int32 [tokens]: the slot of each new token, requests one
+ *                after the other; -1 from cu_out[requests] on
+ *   status       16 bytes, 16-byte aligned, always written: CG_OK, or
+ *                CG_ERR_INVALID_ARG   a negative length or count
+ *                CG_ERR_CAPACITY      too few free pages, a table row or
+ *                                     slots_out too short
+ *                CG_ERR_CORRUPT       free_count outside [0, free_capacity]
+ *                                     or a page id outside [0, num_pages)
+ * With an error nothing is taken: block_table is as it was, lens_out and
+ * free_count_out repeat their inputs, cu_out is 0 and slots_out is -1 (a page
+ * id outside the cache in block_table is the exception: only its tokens'
+ * slots are -1). No other two arrays may overlap. Asynchronous on stream. */
+typedef struct cg_page_batch {
+    int32_t *block_table;
+    int64_t table_stride;
+    int32_t table_width;
+    int32_t requests;
+    const int32_t *lens;
+    const int32_t *counts;
+    const int32_t *free_pages;
+    const int32_t *free_count;
+    int32_t free_capacity;
+    int32_t num_pages;
+    int32_t page_tokens;
+    int32_t *cu_out;
+    int32_t *lens_out;
+    int32_t *free_count_out;
+    int32_t *slots_out;
+    int64_t tokens;
+    void *status;
+} cg_page_batch;
+
+cg_status cg_pages_grow(const cg_page_batch *batch, cg_stream_t stream);
+
+/* Attention of new tokens over one layer of the cache (the formula above).
+ * Their K and V must have been stored before. q and out are bf16 [tokens]
+ * [q_heads][head_size] with strides in elements (multiples of 8, pointers
+ * 16-byte aligned); query head h reads KV head h / (q_heads / num_heads).
+ * cu_q (int32 [requests + 1]), kv_lens (int32 [requests]) and block_table
+ * are device arrays as cg_pages_grow leaves them: request r owns the rows
+ * [cu_q[r], cu_q[r+1]) of q and out, which may be none; rows from
+ * cu_q[requests] on are left as they were. max_q_len: no request has more
+ * rows than this (0: not known); a call for few rows launches less with it.
+ * Table entries of pages in which no query of the request sees a token are
+ * not read.
+ *
+ * Errors found on the device, in the cache's status: CG_ERR_CORRUPT for a
+ * cu_q that is not ascending within [0, tokens], a negative kv_len or one
+ * beyond table_width pages (the request's rows are left as they were), and
+ * for a page id outside the cache (its tokens count as not visible);
+ * CG_ERR_INVALID_ARG for a request with more than max_q_len rows (left as
+ * they were); CG_ERR_TIMEOUT when a bounded wait ran out.
+ *
+ * workspace (device, 256-byte aligned, the size that
+ * cg_int4_attention_workspace gives; data and status pointers, q, out and
+ * the device arrays are not looked at there) is scratch: calls that may
+ * overlap need one each. Asynchronous on stream. */
+typedef struct cg_attention {
+    const void *q;
+    int64_t q_token_stride, q_head_stride;
+    void *out;
+    int64_t out_token_stride, out_head_stride;
+    const int32_t *cu_q;
+    const int32_t *kv_lens;
+    const int32_t *block_table;
+    int64_t table_stride;
+    int32_t table_width;
+    int32_t requests;
+    int32_t tokens;
+    int32_t q_heads;
+    int32_t max_q_len;
+    int32_t window;
+    int32_t sinks;
+    float scale;
+} cg_attention;
+
+cg_status cg_int4_attention_workspace(const cg_int4_cache *cache, const cg_attention *args,
+                                      size_t *bytes);
+cg_status cg_int4_attention(const cg_int4_cache *cache, int32_t layer, const cg_attention *args,
+                            void *workspace, size_t workspace_bytes, cg_stream_t stream);
+
 /* Per-kernel timing, for profiling. When enabled, each kernel that
  * cg_encode/cg_decode enqueue is bracketed by two CUDA events on the launch
  * stream (up to max_launches kernels are recorded; later ones are not).

@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as ct
+import functools
 import os
 import threading
 from dataclasses import dataclass
@@ -51,6 +52,39 @@ class cg_encoded(ct.Structure):
 
 class cg_kernel_profile(ct.Structure):
     _fields_ = [("kernel", ct.c_char_p), ("launches", ct.c_int64), ("total_ms", ct.c_double)]
+
+
+class cg_int4_cache(ct.Structure):
+    _fields_ = [("data", ct.c_void_p), ("status", ct.c_void_p), ("num_layers", ct.c_int32),
+                ("num_pages", ct.c_int32), ("page_tokens", ct.c_int32), ("num_heads", ct.c_int32),
+                ("head_size", ct.c_int32), ("group", ct.c_int32)]
+
+
+class cg_kv_rows(ct.Structure):
+    _fields_ = [("k", ct.c_void_p), ("v", ct.c_void_p)] + \
+        [(n, ct.c_int64) for n in ("k_layer_stride", "k_token_stride", "k_head_stride",
+                                   "v_layer_stride", "v_token_stride", "v_head_stride")]
+
+
+class cg_page_batch(ct.Structure):
+    _fields_ = [("block_table", ct.c_void_p), ("table_stride", ct.c_int64),
+                ("table_width", ct.c_int32), ("requests", ct.c_int32),
+                ("lens", ct.c_void_p), ("counts", ct.c_void_p), ("free_pages", ct.c_void_p),
+                ("free_count", ct.c_void_p), ("free_capacity", ct.c_int32),
+                ("num_pages", ct.c_int32), ("page_tokens", ct.c_int32),
+                ("cu_out", ct.c_void_p), ("lens_out", ct.c_void_p),
+                ("free_count_out", ct.c_void_p), ("slots_out", ct.c_void_p),
+                ("tokens", ct.c_int64), ("status", ct.c_void_p)]
+
+
+class cg_attention(ct.Structure):
+    _fields_ = [("q", ct.c_void_p), ("q_token_stride", ct.c_int64), ("q_head_stride", ct.c_int64),
+                ("out", ct.c_void_p), ("out_token_stride", ct.c_int64),
+                ("out_head_stride", ct.c_int64), ("cu_q", ct.c_void_p), ("kv_lens", ct.c_void_p),
+                ("block_table", ct.c_void_p), ("table_stride", ct.c_int64),
+                ("table_width", ct.c_int32), ("requests", ct.c_int32), ("tokens", ct.c_int32),
+                ("q_heads", ct.c_int32), ("max_q_len", ct.c_int32), ("window", ct.c_int32),
+                ("sinks", ct.c_int32), ("scale", ct.c_float)]
 
 
 class CacheGenError(RuntimeError):
@@ -128,6 +162,16 @@ def _open(path: str) -> ct.CDLL:
                                         ct.POINTER(u64), P]),
         "cg_int8_encode": (st, [P, ct.c_int64, ct.c_int32, P, P, P, P]),
         "cg_int8_decode": (st, [P, P, ct.c_int64, ct.c_int32, P, P]),
+        "cg_int4_cache_bytes": (st, [ct.POINTER(cg_int4_cache), ct.POINTER(sz)]),
+        "cg_int4_store": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, ct.c_int32,
+                               ct.POINTER(cg_kv_rows), P, ct.c_int64, P]),
+        "cg_int4_load": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, ct.c_int32,
+                              ct.POINTER(cg_kv_rows), P, ct.c_int64, P]),
+        "cg_pages_grow": (st, [ct.POINTER(cg_page_batch), P]),
+        "cg_int4_attention_workspace": (st, [ct.POINTER(cg_int4_cache), ct.POINTER(cg_attention),
+                                             ct.POINTER(sz)]),
+        "cg_int4_attention": (st, [ct.POINTER(cg_int4_cache), ct.c_int32,
+                                   ct.POINTER(cg_attention), P, sz, P]),
         "cg_profile_enable": (st, [P, ct.c_int32]),
         "cg_profile_read": (st, [P, ct.POINTER(cg_kernel_profile), ct.c_int32,
                                  ct.POINTER(ct.c_int32)]),
@@ -543,3 +587,287 @@ class Codec:
         cg_deserialize(codec.plan, host_in, enc.bytestream, enc.lengths, enc.cdf, enc.amax,
                        stream)
         return codec, enc
+
+
+# ---------------------------------------------- paged cache held in 4 bits
+
+def _on_device(fn):
+    """Run a method or function of the paged cache on the stream given as
+    stream= (its temporaries and outputs are then allocated there too)."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+class _Launch:
+    """The current stream of a device, with that device made current while
+    the call is enqueued."""
+    __slots__ = ("device", "back")
+
+    def __init__(self, device):
+        self.device = device
+
+    def __enter__(self):
+        import torch
+        now = torch.cuda.current_device()
+        self.back = now if now != self.device.index else None
+        if self.back is not None:
+            torch.cuda.set_device(self.device)
+        return torch.cuda.current_stream(self.device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            import torch
+            torch.cuda.set_device(self.back)
+
+
+def _need(cond, what: str):
+    if not cond:
+        raise ValueError(what)
+
+
+def _ints(t, device, shape, what: str):
+    """A contiguous int32 tensor of the given shape on the device."""
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and
+          tuple(t.shape) == shape and t.is_contiguous(),
+          f"{what} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+
+
+def _table(t, device, what: str):
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and
+          t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1) and
+          (t.stride(0) >= t.shape[1] or t.shape[0] <= 1),
+          f"{what} must be an int32 tensor [requests, pages] on {device}, a row's entries adjacent")
+
+
+def _stride(t, dim: int) -> int:
+    return t.stride(dim) if t.shape[dim] > 1 else 0
+
+
+def _bf16_rows(t, device, shape, what: str, written: bool):
+    """A bf16 tensor [.., head_size] of the given shape whose rows the
+    kernels can read (and, when written, that do not overlap)."""
+    import torch
+    _need(isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.device == device and
+          tuple(t.shape) == shape, f"{what} must be a bf16 tensor of shape {list(shape)} on {device}")
+    if t.numel() == 0:
+        return
+    _need(t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and
+          all(s % 8 == 0 for s, n in zip(t.stride()[:-1], shape) if n > 1),
+          f"{what}: channels must be adjacent, rows 16-byte aligned")
+    if written:
+        # each dimension steps over everything inside the smaller ones
+        inner = t.shape[-1]
+        for s, n in sorted((s, n) for s, n in zip(t.stride()[:-1], shape) if n > 1):
+            _need(s >= inner, f"{what}: rows overlap")
+            inner = s * (n - 1) + inner
+
+
+@dataclass
+class PagePlan:
+    """What grow_pages found: tensors on the device."""
+    slots: "object"        # int32 [tokens], -1 behind the last request
+    cu: "object"           # int32 [requests + 1]
+    lens: "object"         # int32 [requests], with the new tokens
+    free_count: "object"   # int32 [1]
+    status: "object"       # uint8 [16]
+
+    def check(self):
+        """Wait for the current stream; raise if the pages could not be had."""
+        import torch
+        with torch.cuda.device(self.status.device):
+            st, _ = cg_last_device_error(None, self.status)
+        _check(st, "cg_pages_grow (device)")
+
+
+@_on_device
+def grow_pages(block_table, lens, counts, free_pages, free_count, page_tokens: int, tokens: int,
+               num_pages: int | None = None, out: PagePlan | None = None) -> PagePlan:
+    """Pages and slots of a batch's new tokens (cg_pages_grow in
+    include/cachegen.h). block_table int32 [requests, width] gets the ids of
+    the pages taken; lens and counts are int32 [requests] (tokens held, tokens
+    new); free_pages int32 [capacity] holds free_count (int32 [1]) free page
+    ids, taken from its end. ``tokens`` is the length of the slot map (at
+    least the sum of counts; the rest of it is -1). With ``num_pages`` page
+    ids are checked against the cache's size. ``out`` reuses the buffers of an
+    earlier plan; its lens and free_count may be the lens and free_count passed
+    in (a captured decode loop then advances in place). Enqueues and returns:
+    the caller's own check is PagePlan.check()."""
+    import torch
+    _need(isinstance(lens, torch.Tensor) and lens.is_cuda, "lens must be a CUDA tensor")
+    dev = lens.device
+    n = lens.shape[0] if lens.dim() == 1 else -1
+    _ints(lens, dev, (n,), "lens")
+    _ints(counts, dev, (n,), "counts")
+    _table(block_table, dev, "block_table")
+    _need(block_table.shape[0] == n, "block_table must have one row per request")
+    _ints(free_pages, dev, (free_pages.numel(),), "free_pages")
+    _ints(free_count, dev, (1,), "free_count")
+    tokens = int(tokens)
+    _need(tokens >= 0 and page_tokens > 0, "tokens must not be negative, page_tokens positive")
+    if out is None:
+        e = functools.partial(torch.empty, dtype=torch.int32, device=dev)
+        out = PagePlan(e(tokens), e(n + 1), e(n), e(1),
+                       torch.empty(16, dtype=torch.uint8, device=dev))
+    else:
+        _ints(out.slots, dev, (tokens,), "out.slots")
+        _ints(out.cu, dev, (n + 1,), "out.cu")
+        _ints(out.lens, dev, (n,), "out.lens")
+        _ints(out.free_count, dev, (1,), "out.free_count")
+        _check_status_buffer(out.status, "grow_pages")
+    if num_pages is None:
+        num_pages = 0x7FFFFFFF // page_tokens
+    b = cg_page_batch(block_table.data_ptr(), block_table.stride(0) if n > 1 else
+                      block_table.shape[1], block_table.shape[1], n, lens.data_ptr(),
+                      counts.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
+                      free_pages.shape[0], num_pages, page_tokens, out.cu.data_ptr(),
+                      out.lens.data_ptr(), out.free_count.data_ptr(), out.slots.data_ptr(), tokens,
+                      out.status.data_ptr())
+    with _Launch(dev) as s:
+        _check(load().cg_pages_grow(ct.byref(b), s), "cg_pages_grow")
+    return out
+
+
+class Int4Cache:
+    """A paged KV cache held in 4 bits, and the attention that reads it
+    (cg_int4_* in include/cachegen.h, which defines the format). ``data`` is
+    the cache's bytes, uint8 of any shape (made, and zeroed, if not given).
+
+    Calls enqueue on the current stream (or on stream=) and return; errors
+    that the GPU finds are kept until check() raises them. Calls that touch
+    the same slots, one of them a store, must be ordered by the caller."""
+
+    def __init__(self, num_layers, num_pages, page_tokens, num_heads, head_size, group=32,
+                 data=None, device="cuda"):
+        import torch
+        self._c = cg_int4_cache(0, 0, num_layers, num_pages, page_tokens, num_heads, head_size,
+                                group)
+        self._ref = ct.byref(self._c)
+        n = ct.c_size_t(0)
+        _check(load().cg_int4_cache_bytes(self._ref, ct.byref(n)), "cg_int4_cache_bytes")
+        self.nbytes = n.value
+        if data is None:
+            data = torch.zeros(self.nbytes, dtype=torch.uint8, device=device)
+        _need(isinstance(data, torch.Tensor) and data.is_cuda and data.dtype == torch.uint8 and
+              data.is_contiguous() and data.numel() == self.nbytes,
+              f"data must be a contiguous uint8 CUDA tensor of {self.nbytes} bytes")
+        self.data, self.device = data, data.device
+        self.status = torch.zeros(16, dtype=torch.uint8, device=self.device)
+        self._c.data, self._c.status = data.data_ptr(), self.status.data_ptr()
+        self.num_layers, self.num_pages, self.page_tokens = num_layers, num_pages, page_tokens
+        self.num_heads, self.head_size, self.group = num_heads, head_size, group
+
+    def _rows(self, k, v, tokens, layers, written):
+        shape = (tokens, self.num_heads, self.head_size)
+        if layers is not None:
+            shape = (layers,) + shape
+        _bf16_rows(k, self.device, shape, "k", written)
+        _bf16_rows(v, self.device, shape, "v", written)
+        ks = [_stride(k, i) for i in range(k.dim() - 1)]
+        vs = [_stride(v, i) for i in range(v.dim() - 1)]
+        if layers is None:
+            ks, vs = [0] + ks, [0] + vs
+        return cg_kv_rows(k.data_ptr(), v.data_ptr(), *ks, *vs)
+
+    @_on_device
+    def store(self, k, v, slots, layer: int = 0) -> None:
+        """Quantise rows k, v (bf16 [tokens, heads, head_size] into one layer,
+        or [layers, tokens, heads, head_size] into layers from ``layer`` on;
+        kv[:, 0] and kv[:, 1] of Codec.decode's output fit) into the slots
+        (int32 [tokens]; -1 skips a token, no other slot may occur twice)."""
+        _need(k.dim() in (3, 4) and k.shape == v.shape,
+              "k and v must have the same shape, [tokens, heads, head_size] with or without layers")
+        tokens, layers = k.shape[-3], k.shape[0] if k.dim() == 4 else None
+        rows = self._rows(k, v, tokens, layers, False)
+        _ints(slots, self.device, (tokens,), "slots")
+        with _Launch(self.device) as s:
+            _check(load().cg_int4_store(self._ref, layer, 1 if layers is None else layers,
+                                        ct.byref(rows), slots.data_ptr(), tokens, s),
+                   "cg_int4_store")
+
+    @_on_device
+    def load(self, slots, layer: int = 0, layers: int | None = None, k_out=None, v_out=None):
+        """The bf16 rows of the slots: (k, v) as [tokens, heads, head_size] of
+        one layer, or [layers, tokens, heads, head_size]. Slot -1 gives zeros.
+        k_out, v_out take the rows in place (halves of a KV blob for
+        Codec.encode, say)."""
+        import torch
+        tokens = slots.shape[0] if slots.dim() == 1 else -1
+        _ints(slots, self.device, (tokens,), "slots")
+        shape = (tokens, self.num_heads, self.head_size)
+        if layers is not None:
+            _need(layers >= 0, "layers must not be negative")
+            shape = (layers,) + shape
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+        rows = self._rows(k_out, v_out, tokens, layers, True)
+        with _Launch(self.device) as s:
+            _check(load().cg_int4_load(self._ref, layer, 1 if layers is None else layers,
+                                       ct.byref(rows), slots.data_ptr(), tokens, s),
+                   "cg_int4_load")
+        return k_out, v_out
+
+    @_on_device
+    def attention(self, q, cu_q, kv_lens, block_table, layer: int = 0, window: int = 0,
+                  sinks: int = 0, scale: float | None = None, max_q_len: int | None = None,
+                  out=None):
+        """Attention of the new tokens' queries q (bf16 [tokens, q_heads,
+        head_size]) over a layer of the cache: request r owns the rows
+        cu_q[r]:cu_q[r + 1] and sees its first kv_lens[r] tokens through row r of
+        block_table, causally; with ``window`` only the last ``window`` of
+        them and the first ``sinks``. scale defaults to head_size ** -0.5.
+        max_q_len, the most rows that any request has, spares launches when it
+        is small. Returns out, like q; rows from cu_q[-1] on are not written."""
+        import torch
+        dev = self.device
+        _need(q.dim() == 3, "q must be [tokens, q_heads, head_size]")
+        tokens, q_heads = q.shape[0], q.shape[1]
+        _need(q_heads > 0 and q_heads % self.num_heads == 0,
+              f"q_heads must be a multiple of {self.num_heads}")
+        shape = (tokens, q_heads, self.head_size)
+        _bf16_rows(q, dev, shape, "q", False)
+        n = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+        _ints(kv_lens, dev, (n,), "kv_lens")
+        _ints(cu_q, dev, (n + 1,), "cu_q")
+        _table(block_table, dev, "block_table")
+        _need(block_table.shape[0] == n, "block_table must have one row per request")
+        if out is None:
+            out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        else:
+            _bf16_rows(out, dev, shape, "out", True)
+        width = block_table.shape[1]
+        a = cg_attention(q.data_ptr(), _stride(q, 0), _stride(q, 1), out.data_ptr(),
+                         _stride(out, 0), _stride(out, 1), cu_q.data_ptr(), kv_lens.data_ptr(),
+                         block_table.data_ptr(), block_table.stride(0) if n > 1 else width, width,
+                         n, tokens, q_heads, max_q_len or 0, window, sinks,
+                         self.head_size ** -0.5 if scale is None else scale)
+        L = load()
+        with _Launch(dev) as s:
+            need = ct.c_size_t(0)
+            _check(L.cg_int4_attention_workspace(self._ref, ct.byref(a), ct.byref(need)),
+                   "cg_int4_attention_workspace")
+            # one per call, from the current stream's pool: calls on other
+            # streams and captured graphs never share one
+            ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
+            _check(L.cg_int4_attention(self._ref, layer, ct.byref(a), _ptr(ws), need.value, s),
+                   "cg_int4_attention")
+        return out
+
+    def check(self):
+        """Wait for the current stream; raise the first error that the GPU
+        found in this cache's calls since the last check, and clear it."""
+        import torch
+        with torch.cuda.device(self.device):
+            st, _ = cg_last_device_error(None, self.status)
+            if st != CG_OK:
+                self.status.zero_()
+        _check(st, "Int4Cache (device)")

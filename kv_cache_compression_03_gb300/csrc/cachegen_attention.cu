@@ -10,18 +10,11 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "cg_int4.h"
+#include "cg_attention.h"
 
 namespace {
 
 constexpr int kThreads = 128;
-
-struct AttnArgs {
-    const uint8_t *layer;
-    void *status;
-    int32_t num_pages, page_tokens, heads;
-    cg_attention a;
-};
 
 // The request of a query row: last r with cu[r] <= t. False where cu does
 // not place t in one valid request.
@@ -60,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) k_attention_rows(AttnArgs p)
     const int t = (int)(row / a.q_heads), qh = (int)(row % a.q_heads);
     const int h = qh / (a.q_heads / p.heads);
     int r, n, i;
-    if (!request_of(p, t, &r, &n, &i))
+    if (!request_of(p, t, &r, &n, &i) || n * p.ratio <= p.few_rows)
         return;
     const int kv = a.kv_lens[r];
     if (kv < 0 || (int64_t)kv > (int64_t)a.table_width * p.page_tokens) {
@@ -149,6 +142,15 @@ cg_status check_sizes(const cg_int4_cache *c, const cg_attention *a)
     return CG_OK;
 }
 
+constexpr int kFewRows = 64;
+
+// Most rows of one KV head that a request can have (query heads times tokens).
+int64_t max_rows(const cg_int4_cache *c, const cg_attention *a)
+{
+    const int n = a->max_q_len > 0 && a->max_q_len < a->tokens ? a->max_q_len : a->tokens;
+    return (int64_t)n * (a->q_heads / c->num_heads);
+}
+
 }  // namespace
 
 extern "C" cg_status cg_int4_attention_workspace(const cg_int4_cache *c, const cg_attention *a,
@@ -159,7 +161,8 @@ extern "C" cg_status cg_int4_attention_workspace(const cg_int4_cache *c, const c
     const cg_status st = check_sizes(c, a);
     if (st != CG_OK)
         return st;
-    *bytes = 0;
+    const int64_t rows = max_rows(c, a);
+    *bytes = attn_few_workspace(c->head_size, (int)(rows < kFewRows ? rows : kFewRows));
     return CG_OK;
 }
 
@@ -197,13 +200,21 @@ extern "C" cg_status cg_int4_attention(const cg_int4_cache *c, int32_t layer,
     p.num_pages = c->num_pages;
     p.page_tokens = c->page_tokens;
     p.heads = c->num_heads;
+    p.ratio = a->q_heads / c->num_heads;
+    p.few_rows = kFewRows;
+    p.scale2 = a->scale * 1.4426950408889634f;
     p.a = *a;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t rows = (int64_t)a->tokens * a->q_heads;
-    const unsigned grid = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
-    const cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
-        k_attention_rows<decltype(blob)><<<grid, kThreads, 0, s>>>(p);
-        return cudaGetLastError();
-    });
+    const int64_t most = max_rows(c, a);
+    cudaError_t err = attn_few_launch(p, c->head_size, c->group,
+                                      (int)(most < kFewRows ? most : kFewRows), workspace, s);
+    if (err == cudaSuccess && most > kFewRows) {
+        const int64_t rows = (int64_t)a->tokens * a->q_heads;
+        const unsigned grid = (unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32));
+        err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
+            k_attention_rows<decltype(blob)><<<grid, kThreads, 0, s>>>(p);
+            return cudaGetLastError();
+        });
+    }
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

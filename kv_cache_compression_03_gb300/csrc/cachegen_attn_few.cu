@@ -1,0 +1,767 @@
+// Attention over the 4-bit cache for few query rows per KV head: single
+// tokens and a few drafted ones (up to 64 rows: query heads of the KV head
+// times new tokens). Bound by HBM: D + 8 D/G bytes per token and head are read
+// once, and the work on them has to keep pace with that.
+//
+// Mathematics. With k^ = lo + s n, q.k^ = sum_g s_g (q.n)_g + lo_g (sum q)_g, and
+// sum_t p_t v^_t = sum_t (p_t s_t) (n_t - 8) + sum_t p_t (lo_t + 8 s_t): the matrix
+// instructions take the codes themselves as bf16, which hold them exactly, and
+// the group's parameters meet one score or one probability, not every value.
+// A code becomes bf16 by one masked or into the mantissa of 128 (K: 128 + n)
+// or of 16 (V: 16 + n); the offsets come off exactly: for K through the
+// accumulator's start, -128 sum q, for V through a product with ones, which
+// sums the same rounded p s that the codes met. Roundings: p s to bf16 (2^-8
+// relative); scores, sums and the running maximum stay in fp32.
+//
+// Tiles. mma.sync m16n8k16 with the tokens (K) or channels (V) as the 16 rows
+// and 8 query rows as columns, so 4 or 8 query heads fill an instruction that
+// is idle to 15/16 with queries as rows. One warp takes a blob of 16 tokens at
+// a time, alone: its own ring of bulk copies, its own running maximum and sum,
+// no block barrier in the loop. The cache's layout puts the words that a
+// thread of the instruction needs side by side: a blob's codes come in 16-byte
+// shared loads without bank conflicts.
+//
+// Split. The batch's blobs, in the order request, KV head, row tile, token,
+// are one line that the blocks cut into equal pieces, whatever the lengths.
+// A piece that holds a (request, head, tile) whole writes its output; cut ones
+// write their maximum, sum and accumulator, and a second kernel joins them in
+// the order of the tokens, so results do not depend on timing.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cg_attention.h"
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kStages = 4;       // blobs in flight per warp (a power of two)
+constexpr int kMinPiece = kWarps;   // blobs of a block, at least
+constexpr float kNone = -INFINITY;
+
+// ---------------------------------------------------------------- schedule
+
+// The blobs that a request's rows can see: [0, sink) and [sink + skip, ..),
+// nb of them (at least 1, so that every row gets its output).
+struct Span {
+    int32_t nb, sink, skip;
+};
+
+__device__ __forceinline__ Span span_of(const AttnArgs &p, const AttnRequest &q)
+{
+    const int32_t end = (q.kv + 15) / 16;
+    Span s = {end, 0, 0};
+    if (p.a.window > 0) {
+        const int64_t low = (int64_t)q.kv - q.nq + 1 - p.a.window;   // the first row's
+        if (low > 0) {
+            const int32_t first = (int32_t)(low / 16);
+            const int64_t sb = ((int64_t)p.a.sinks + 15) / 16;
+            s.sink = sb < first ? (int32_t)sb : first;
+            s.skip = first - s.sink;
+            s.nb = end - s.skip;
+        }
+    }
+    if (s.nb < 1)
+        s.nb = 1;
+    return s;
+}
+
+template <int RU>
+__device__ __forceinline__ int64_t work_of(const AttnArgs &p, int r, AttnRequest *q, uint32_t *error)
+{
+    if (!attn_request(p, r, q, error) || q->rows > p.few_rows)
+        return 0;
+    return (int64_t)((q->rows + RU - 1) / RU) * p.heads * span_of(p, *q).nb;
+}
+
+struct Place {   // a point of the line
+    int32_t r;        // request (requests: past the end)
+    int64_t off;      // blobs from the request's start
+};
+
+// Block-wide: the line's length, the blobs of a piece, and the place of
+// piece `piece` plus `plus`. Block 0 of the main kernel reports bad requests.
+template <int RU>
+__device__ Place schedule(const AttnArgs &p, int pieces, int piece, int plus, bool report,
+                          int64_t *total_out, int64_t *chunk_out)
+{
+    __shared__ int64_t warp_sum[kWarps];
+    __shared__ Place found;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const bool once = p.a.requests <= kThreads;
+    int64_t total = 0, chunk = 0, want = -1;
+    if (tid == 0)
+        found = {p.a.requests, 0};
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t carry = 0;
+        for (int r0 = 0; r0 < p.a.requests; r0 += kThreads) {
+            const int r = r0 + tid;
+            int64_t w = 0;
+            if (r < p.a.requests) {
+                AttnRequest q;
+                uint32_t error;
+                w = work_of<RU>(p, r, &q, &error);
+                if (report && pass == 0 && error != CG_OK)
+                    int4_set_status(p.status, error);
+            }
+            int64_t inc = w;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+                if (lane >= d)
+                    inc += o;
+            }
+            if (lane == 31)
+                warp_sum[warp] = inc;
+            __syncthreads();
+            int64_t before = carry, sum = carry;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                if (i < warp)
+                    before += warp_sum[i];
+                sum += warp_sum[i];
+            }
+            __syncthreads();
+            carry = sum;
+            if (pass == 0 && once) {
+                total = sum;
+                chunk = (total + pieces - 1) / pieces;
+                if (chunk < kMinPiece)
+                    chunk = kMinPiece;
+                want = piece * chunk + plus;
+            }
+            const int64_t start = before + inc - w;
+            if (want >= start && want < start + w)
+                found = {r, want - start};
+        }
+        if (pass == 0) {
+            total = carry;
+            chunk = (total + pieces - 1) / pieces;
+            if (chunk < kMinPiece)
+                chunk = kMinPiece;
+            want = piece * chunk + plus;
+            if (once)
+                break;
+        }
+    }
+    __syncthreads();
+    const Place at = found;
+    *total_out = total;
+    *chunk_out = chunk;
+    return at;
+}
+
+// A (request, head, row tile) and the stretch of its blobs in this piece.
+struct Unit {
+    int32_t r, h, rt, tiles;
+    AttnRequest q;
+    Span span;
+    int32_t b0, b1;
+};
+
+// Finds the unit at a place; `left` blobs of the piece remain.
+template <int RU>
+__device__ __forceinline__ void unit_at(const AttnArgs &p, Place at, int64_t left, Unit *u)
+{
+    uint32_t error;
+    attn_request(p, at.r, &u->q, &error);
+    u->r = at.r;
+    u->span = span_of(p, u->q);
+    u->tiles = (u->q.rows + RU - 1) / RU;
+    const int32_t i = (int32_t)(at.off / u->span.nb);
+    u->h = i / u->tiles;
+    u->rt = i - u->h * u->tiles;
+    u->b0 = (int32_t)(at.off - (int64_t)i * u->span.nb);
+    const int64_t end = u->b0 + left;
+    u->b1 = end < u->span.nb ? (int32_t)end : u->span.nb;
+}
+
+// The next unit of the line (the caller knows that there is one).
+template <int RU>
+__device__ __forceinline__ void unit_next(const AttnArgs &p, int64_t left, Unit *u)
+{
+    if (++u->rt == u->tiles) {
+        u->rt = 0;
+        if (++u->h == p.heads) {
+            u->h = 0;
+            uint32_t error;
+            while (++u->r < p.a.requests && work_of<RU>(p, u->r, &u->q, &error) == 0)
+                ;
+            if (u->r >= p.a.requests) {   // not reached while blobs are left
+                u->b0 = u->b1 = 0;
+                return;
+            }
+            u->span = span_of(p, u->q);
+            u->tiles = (u->q.rows + RU - 1) / RU;
+        }
+    }
+    u->b0 = 0;
+    u->b1 = left < u->span.nb ? (int32_t)left : u->span.nb;
+}
+
+// A warp's stretch of a unit's blobs in this piece.
+__device__ __forceinline__ void warp_range(const Unit &u, int warp, int *b, int *e)
+{
+    const int n = u.b1 - u.b0;
+    *b = u.b0 + (int)((int64_t)n * warp / kWarps);
+    *e = u.b0 + (int)((int64_t)n * (warp + 1) / kWarps);
+}
+
+// ------------------------------------------------------------ instructions
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Codes i and i + 4 of a word as the bf16 pair (128 + n, 128 + n).
+__device__ __forceinline__ uint32_t codes128(uint32_t w, int i)
+{
+    return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+}
+
+// Codes i and i + 4 of a word as the bf16 pair (16 + n, 16 + n).
+__device__ __forceinline__ uint32_t codes16(uint32_t w, int i)
+{
+    return ((i == 0 ? w << 3 : w >> (4 * i - 3)) & 0x00780078u) | 0x41804180u;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
+{
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+}
+
+// ---------------------------------------------------------------- workspace
+
+// Partial results: [block][2] of { float o[RU][D]; float m[RU]; float l[RU]; }.
+// Slot 0 of a block belongs to a unit that began in an earlier block, slot 1
+// to one that goes on in the next.
+template <int D, int RU>
+constexpr int kPartFloats = RU *(D + 2);
+
+// ------------------------------------------------------------- main kernel
+
+template <typename B, int NT>
+struct FewShared {
+    static constexpr int RU = 8 * NT;
+    uint8_t ring[kWarps][kStages][B::kBytes];
+    float merge[kWarps][RU][B::kD / NT];   // one of NT parts of the channels
+    float m[kWarps][RU], l[kWarps][RU];
+    uint64_t full[kWarps][kStages];
+    uint32_t bad[kWarps][kStages];         // the blob's page id was outside the cache
+};
+
+template <typename B, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(AttnArgs p, float *parts)
+{
+    using S = FewShared<B, NT>;
+    constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG, RU = S::RU;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    S &sm = *reinterpret_cast<S *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    if (lane == 0)
+        for (int i = 0; i < kStages; ++i)
+            bar_init(&sm.full[warp][i], 1);
+    bar_init_fence();
+    int64_t total, chunk;
+    const Place at = schedule<RU>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
+    const int64_t begin = blockIdx.x * chunk;
+    if (begin >= total)
+        return;
+    const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
+
+    const int bpp = p.page_tokens / 16;
+    // ---- the warp's feeder (lane 0 issues; all lanes keep its state)
+    Unit fu;
+    unit_at<RU>(p, at, count, &fu);
+    int64_t f_pos = fu.b1 - fu.b0;   // blobs of the piece up to the end of the feeder's unit
+    int f_b, f_e;
+    warp_range(fu, warp, &f_b, &f_e);
+    int f_in = 0, f_page = 0;
+    bool f_jump = true;              // the page has to be looked up again
+    uint32_t issued = 0;
+    auto feed = [&]() {
+        // one more blob into the ring, if the piece has one for this warp
+        while (f_b >= f_e) {
+            if (f_pos >= count)
+                return;
+            unit_next<RU>(p, count - f_pos, &fu);
+            f_pos += fu.b1 - fu.b0;
+            warp_range(fu, warp, &f_b, &f_e);
+            f_jump = true;
+        }
+        const int ab = f_b < fu.span.sink ? f_b : f_b + fu.span.skip;
+        if (f_jump || f_b == fu.span.sink) {
+            f_page = ab / bpp;
+            f_in = ab - f_page * bpp;
+            f_jump = false;
+        }
+        const int st = issued & (kStages - 1);
+        if (lane == 0) {
+            int id = -1;
+            if (fu.q.kv > 0)
+                id = p.a.block_table[fu.r * p.a.table_stride + f_page];
+            const bool ok = id >= 0 && id < p.num_pages;
+            sm.bad[warp][st] = !ok;
+            if (ok) {
+                const uint8_t *src = p.layer + (((size_t)id * p.heads + fu.h) * bpp + f_in) * B::kBytes;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_expect(&sm.full[warp][st], B::kBytes);
+                bulk_copy(sm.ring[warp][st], src, B::kBytes, &sm.full[warp][st]);
+            } else {
+                if (fu.q.kv > 0)
+                    int4_set_status(p.status, CG_ERR_CORRUPT);
+                bar_arrive(&sm.full[warp][st]);
+            }
+        }
+        ++issued;
+        ++f_b;
+        if (++f_in == bpp) {
+            f_in = 0;
+            ++f_page;
+        }
+    };
+    __syncwarp();
+    for (int i = 0; i < kStages; ++i)
+        feed();
+
+    bool alive = true;               // no wait has run out
+    uint32_t used = 0;
+    Unit u;
+    unit_at<RU>(p, at, count, &u);
+    int64_t pos = 0;
+    for (;;) {
+        // ---- queries: column g of row tile nt is row rt * RU + 8 nt + g
+        const int row_base = u.rt * RU;
+        uint32_t qf[NT][NW][4];
+        float qs[NT][NG][2];         // sums of q per group, rows 2t and 2t + 1
+        int x[NT][2];                // their positions (-1: no such row)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int row = row_base + 8 * nt + g;
+            const bool there = row < u.q.rows;
+            const int qt = there ? row / p.ratio : 0, qh = u.h * p.ratio + (there ? row - qt * p.ratio : 0);
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.a.q) +
+                                     (int64_t)(u.q.row0 + qt) * p.a.q_token_stride + qh * p.a.q_head_stride;
+            float sum[NG] = {};
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const uint4 v = there ? *reinterpret_cast<const uint4 *>(q + 32 * w + 8 * t)
+                                      : make_uint4(0, 0, 0, 0);
+                // channels i and i + 4 side by side, as the codes of a word come
+                qf[nt][w][0] = __byte_perm(v.x, v.z, 0x5410);
+                qf[nt][w][1] = __byte_perm(v.x, v.z, 0x7632);
+                qf[nt][w][2] = __byte_perm(v.y, v.w, 0x5410);
+                qf[nt][w][3] = __byte_perm(v.y, v.w, 0x7632);
+                sum[w / WPG] += par_s(v.x) + par_lo(v.x) + par_s(v.y) + par_lo(v.y) + par_s(v.z) +
+                                par_lo(v.z) + par_s(v.w) + par_lo(v.w);
+            }
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
+                sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
+                qs[nt][i][0] = __shfl_sync(0xFFFFFFFFu, sum[i], 8 * t);
+                qs[nt][i][1] = __shfl_sync(0xFFFFFFFFu, sum[i], 8 * t + 4);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int rr = row_base + 8 * nt + 2 * t + j;
+                x[nt][j] = rr < u.q.rows ? u.q.kv - u.q.nq + rr / p.ratio : -1;
+            }
+        }
+        // positions of the tile's first and last row: blobs that both see whole need no mask
+        const int last_row = (row_base + RU < u.q.rows ? row_base + RU : u.q.rows) - 1;
+        const int x_lo = u.q.kv - u.q.nq + row_base / p.ratio;
+        const int x_hi = u.q.kv - u.q.nq + last_row / p.ratio;
+        const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
+
+        float o[NW * 2][NT][4] = {};
+        float ones[NG][NT][4] = {};
+        float mid[NG][NT][2] = {};
+        float m[NT][2], l[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            for (int j = 0; j < 2; ++j) {
+                m[nt][j] = kNone;
+                l[nt][j] = 0.0f;
+            }
+
+        int b, e;
+        warp_range(u, warp, &b, &e);
+        for (; b < e; ++b) {
+            const int st = used & (kStages - 1);
+            if (alive &&
+                !__all_sync(0xFFFFFFFFu, bar_wait(&sm.full[warp][st], (used / kStages) & 1))) {
+                alive = false;
+                int4_set_status(p.status, CG_ERR_TIMEOUT);
+            }
+            ++used;
+            if (alive && !sm.bad[warp][st]) {
+                const uint8_t *blob = sm.ring[warp][st];
+                const int tok = 16 * (b < u.span.sink ? b : b + u.span.skip);
+                // ---- scores of tokens g and g + 8 with rows 2t and 2t + 1
+                uint32_t k0[NW], k1[NW], kp0[NG], kp1[NG];
+                load_words(k0, blob + B::kKCodes + g * (D / 2) + t * (D / 8));
+                load_words(k1, blob + B::kKCodes + (g + 8) * (D / 2) + t * (D / 8));
+                load_words(kp0, blob + B::kKParams + g * 4 * NG);
+                load_words(kp1, blob + B::kKParams + (g + 8) * 4 * NG);
+                float z[NT][4] = {};
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    float acc[NT][4];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            acc[nt][j] = -128.0f * qs[nt][gi][j & 1];
+#pragma unroll
+                    for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            const uint32_t a0 = codes128(k0[w], i), a1 = codes128(k1[w], i);
+                            const uint32_t a2 = codes128(k0[w], i + 1), a3 = codes128(k1[w], i + 1);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
+                        }
+                    const float s0 = par_s(kp0[gi]), l0 = par_lo(kp0[gi]);
+                    const float s1 = par_s(kp1[gi]), l1 = par_lo(kp1[gi]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            z[nt][j] = fmaf(s0, acc[nt][j], fmaf(l0, qs[nt][gi][j], z[nt][j]));
+                            z[nt][2 + j] = fmaf(s1, acc[nt][2 + j], fmaf(l1, qs[nt][gi][j], z[nt][2 + j]));
+                        }
+                }
+                uint32_t vp0[NG], vp1[NG];
+                load_words(vp0, blob + B::kVParams + g * 4 * NG);
+                load_words(vp1, blob + B::kVParams + (g + 8) * 4 * NG);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        z[nt][j] *= p.scale2;
+                const bool whole = tok + 15 <= x_lo && (x_hi - tok < window || tok + 15 < p.a.sinks);
+                if (!whole) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int at_tok = tok + g + (j >= 2 ? 8 : 0), xr = x[nt][j & 1];
+                            const bool sees = at_tok <= xr && (xr - at_tok < window || at_tok < p.a.sinks);
+                            z[nt][j] = sees ? z[nt][j] : kNone;
+                        }
+                    // parameters behind the last token may be anything
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) {
+                        vp0[gi] = tok + g < u.q.kv ? vp0[gi] : 0;
+                        vp1[gi] = tok + g + 8 < u.q.kv ? vp1[gi] : 0;
+                    }
+                }
+                // ---- running maximum: raised only when a score exceeds it by 2^8, so
+                // that probabilities stay below 2^8 and rescaling is rare
+                bool raise = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        raise |= fmaxf(z[nt][j], z[nt][2 + j]) > m[nt][j] + 8.0f;
+                if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            float mx = fmaxf(z[nt][j], z[nt][2 + j]);
+#pragma unroll
+                            for (int d = 4; d < 32; d <<= 1)
+                                mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+                            mx = fmaxf(mx, m[nt][j]);
+                            const float f = m[nt][j] == kNone ? 0.0f : exp2_fast(m[nt][j] - mx);
+                            m[nt][j] = mx;
+                            l[nt][j] *= f;
+#pragma unroll
+                            for (int c = 0; c < NW * 2; ++c) {
+                                o[c][nt][j] *= f;
+                                o[c][nt][2 + j] *= f;
+                            }
+#pragma unroll
+                            for (int gi = 0; gi < NG; ++gi) {
+                                ones[gi][nt][j] *= f;
+                                mid[gi][nt][j] *= f;
+                            }
+                        }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float base = m[nt][j] == kNone ? 0.0f : m[nt][j];
+                        z[nt][j] = exp2_fast(z[nt][j] - base);
+                        z[nt][2 + j] = exp2_fast(z[nt][2 + j] - base);
+                        l[nt][j] += z[nt][j] + z[nt][2 + j];
+                    }
+                // ---- values
+                uint32_t v0[NW], v1[NW];
+                load_words(v0, blob + B::kVCodes + t * D + g * (D / 8));
+                load_words(v1, blob + B::kVCodes + (t + 4) * D + g * (D / 8));
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    const float s0 = par_s(vp0[gi]), s1 = par_s(vp1[gi]);
+                    const float c0 = fmaf(8.0f, s0, par_lo(vp0[gi])), c1 = fmaf(8.0f, s1, par_lo(vp1[gi]));
+                    uint32_t pf[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            mid[gi][nt][j] += fmaf(z[nt][j], c0, z[nt][2 + j] * c1);
+                        pf[nt][0] = transpose8x8(pack_bf16(z[nt][0] * s0, z[nt][1] * s0));
+                        pf[nt][1] = transpose8x8(pack_bf16(z[nt][2] * s1, z[nt][3] * s1));
+                        mma16816(ones[gi][nt], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u,
+                                 pf[nt][0], pf[nt][1]);
+                    }
+#pragma unroll
+                    for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            const uint32_t a0 = codes16(v0[w], i), a1 = codes16(v0[w], i + 1);
+                            const uint32_t a2 = codes16(v1[w], i), a3 = codes16(v1[w], i + 1);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+                                mma16816(o[w * 2 + i / 2][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                        }
+                }
+            }
+            __syncwarp();   // every lane has read the stage
+            if (alive)
+                feed();
+        }
+
+        // ---- the warps' results of this unit, joined in shared memory
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) {
+                    l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], d);
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi)
+                        mid[gi][nt][j] += __shfl_xor_sync(0xFFFFFFFFu, mid[gi][nt][j], d);
+                }
+                if (g == 0) {
+                    sm.m[warp][8 * nt + 2 * t + j] = m[nt][j];
+                    sm.l[warp][8 * nt + 2 * t + j] = l[nt][j];
+                }
+            }
+        __syncthreads();
+        const bool from_before = u.b0 > 0, goes_on = u.b1 < u.span.nb;
+        float *part = parts + ((size_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * kPartFloats<D, RU>;
+        const int rows_here = last_row - row_base + 1;
+        float f[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float mx = kNone;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    mx = fmaxf(mx, sm.m[w][8 * nt + 2 * t + j]);
+                // without a maximum the sum is 0, or NaN for a query with NaN
+                f[nt][j] = m[nt][j] == kNone ? l[nt][j] : exp2_fast(m[nt][j] - mx);
+            }
+        constexpr int kPartW = NW / NT;   // words (32 channels) of a pass
+#pragma unroll
+        for (int pass = 0; pass < NT; ++pass) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int w = 0; w < kPartW; ++w) {
+                        const int ww = pass * kPartW + w, gi = ww / WPG;
+                        const float off = mid[gi][nt][j] - 24.0f * ones[gi][nt][j];
+                        const float4 v = make_float4((o[2 * ww][nt][j] + off) * f[nt][j],
+                                                     (o[2 * ww][nt][2 + j] + off) * f[nt][j],
+                                                     (o[2 * ww + 1][nt][j] + off) * f[nt][j],
+                                                     (o[2 * ww + 1][nt][2 + j] + off) * f[nt][j]);
+                        *reinterpret_cast<float4 *>(&sm.merge[warp][8 * nt + 2 * t + j][32 * w + 4 * g]) = v;
+                    }
+            __syncthreads();
+            constexpr int kQuads = D / NT / 4;   // float4 per row
+            for (int i = tid; i < rows_here * kQuads; i += kThreads) {
+                const int row = i / kQuads, c = (i - row * kQuads) * 4;
+                float mx = kNone, ls = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    mx = fmaxf(mx, sm.m[w][row]);
+                float4 sum = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float4 v = *reinterpret_cast<const float4 *>(&sm.merge[w][row][c]);
+                    sum.x += v.x;
+                    sum.y += v.y;
+                    sum.z += v.z;
+                    sum.w += v.w;
+                    const float mw = sm.m[w][row];
+                    ls += mw == kNone ? sm.l[w][row] : sm.l[w][row] * exp2_fast(mw - mx);
+                }
+                const int ch = pass * (D / NT) + c;
+                if (from_before || goes_on) {
+                    *reinterpret_cast<float4 *>(part + row * D + ch) = sum;
+                    if (pass == 0 && c == 0) {
+                        part[RU * D + row] = mx;
+                        part[RU * D + RU + row] = ls;
+                    }
+                } else {
+                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                    const int rr = row_base + row, qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                                         (int64_t)(u.q.row0 + qt) * p.a.out_token_stride +
+                                         qh * p.a.out_head_stride + ch;
+                    *reinterpret_cast<uint2 *>(out) =
+                        make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+                }
+            }
+            __syncthreads();
+        }
+        pos += u.b1 - u.b0;
+        if (pos >= count)
+            break;
+        unit_next<RU>(p, count - pos, &u);
+    }
+    // a wait that ran out: the copies still in flight must land before the block's memory goes
+    if (!alive)
+        for (; used < issued; ++used)
+            bar_wait(&sm.full[warp][used & (kStages - 1)], (used / kStages) & 1);
+}
+
+// ------------------------------------------------------------------- joining
+
+// Block c joins the unit that begins in block c of the main kernel and goes
+// on behind it, if there is one.
+template <int D, int RU>
+__global__ void __launch_bounds__(kThreads) k_attention_join(AttnArgs p, int pieces, const float *parts)
+{
+    int64_t total, chunk;
+    const int c = blockIdx.x;
+    // where the next piece starts: inside the unit, if one goes on
+    const Place at = schedule<RU>(p, pieces, c + 1, 0, false, &total, &chunk);
+    const int64_t border = (c + 1) * chunk;
+    if (border >= total)
+        return;
+    Unit u;
+    unit_at<RU>(p, at, 1, &u);
+    if (u.b0 == 0 || u.b0 > chunk)
+        return;   // begins at the border, or before block c
+    const int64_t end = border - u.b0 + u.span.nb;
+    const int last = (int)((end + chunk - 1) / chunk) - 1;   // the block that holds its end
+    const int row_base = u.rt * RU;
+    const int rows_here = (row_base + RU < u.q.rows ? row_base + RU : u.q.rows) - row_base;
+    constexpr int kQuads = D / 4;
+    for (int i = threadIdx.x; i < rows_here * kQuads; i += kThreads) {
+        const int row = i / kQuads, ch = (i - row * kQuads) * 4;
+        float m = kNone, l = 0.0f;
+        float4 sum = make_float4(0, 0, 0, 0);
+        for (int k = c; k <= last; ++k) {
+            const float *part = parts + ((size_t)k * 2 + (k == c ? 1 : 0)) * kPartFloats<D, RU>;
+            const float mk = part[RU * D + row], lk = part[RU * D + RU + row];
+            const float4 v = *reinterpret_cast<const float4 *>(part + row * D + ch);
+            if (mk == kNone) {
+                l += lk;
+                continue;
+            }
+            const float mn = fmaxf(m, mk), f = m == kNone ? 0.0f : exp2_fast(m - mn), e = exp2_fast(mk - mn);
+            m = mn;
+            l = l * f + lk * e;
+            sum.x = sum.x * f + v.x * e;
+            sum.y = sum.y * f + v.y * e;
+            sum.z = sum.z * f + v.z * e;
+            sum.w = sum.w * f + v.w * e;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int rr = row_base + row, qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                             (int64_t)(u.q.row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride + ch;
+        *reinterpret_cast<uint2 *>(out) =
+            make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+    }
+}
+
+// Row tiles of 8 or 16 query rows, by the most rows that a request can have.
+int tile_rows(int max_rows) { return max_rows <= 8 ? 8 : 16; }
+
+template <typename B, int NT>
+cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
+{
+    using Sh = FewShared<B, NT>;
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(k_attention_few<B, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)sizeof(Sh));
+    if (err != cudaSuccess)
+        return err;
+    int blocks = (NT == 1 ? 2 : 1) * sms;
+    if (blocks > kFewMaxBlocks)
+        blocks = kFewMaxBlocks;
+    k_attention_few<B, NT><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
+    k_attention_join<B::kD, 8 * NT><<<blocks, kThreads, 0, s>>>(p, blocks, parts);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_few_workspace(int head_size, int max_rows)
+{
+    const int ru = tile_rows(max_rows);
+    return (size_t)kFewMaxBlocks * 2 * ru * (head_size + 2) * sizeof(float);
+}
+
+cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max_rows, void *ws,
+                            cudaStream_t s)
+{
+    float *parts = static_cast<float *>(ws);
+    return int4_dispatch(head_size, group, [&](auto blob) {
+        using B = decltype(blob);
+        return tile_rows(max_rows) == 8 ? launch<B, 1>(p, parts, s) : launch<B, 2>(p, parts, s);
+    });
+}

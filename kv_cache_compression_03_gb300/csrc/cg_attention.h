@@ -1,0 +1,109 @@
+// Shared by the attention kernels of the 4-bit cache.
+#pragma once
+
+#include "cg_int4.h"
+
+struct AttnArgs {
+    const uint8_t *layer;   // the cache's bytes of one layer
+    void *status;
+    int32_t num_pages, page_tokens, heads, ratio;   // ratio: query heads per KV head
+    int32_t few_rows;       // requests with up to this many rows per KV head go to the
+                            // kernel for few rows
+    float scale2;           // scale * log2(e)
+    cg_attention a;
+};
+
+// One request's rows and tokens.
+struct AttnRequest {
+    int32_t row0, nq, kv;   // first query row, query rows, cached tokens
+    int32_t rows;           // nq * ratio: rows of one KV head
+};
+
+// False for a request without rows and for an invalid one, which *error
+// then names.
+__device__ __forceinline__ bool attn_request(const AttnArgs &p, int r, AttnRequest *q,
+                                             uint32_t *error)
+{
+    const int32_t c0 = p.a.cu_q[r], c1 = p.a.cu_q[r + 1], kv = p.a.kv_lens[r];
+    *error = CG_OK;
+    if (c0 < 0 || c1 < c0 || c1 > p.a.tokens || kv < 0 ||
+        (int64_t)kv > (int64_t)p.a.table_width * p.page_tokens)
+        *error = CG_ERR_CORRUPT;
+    else if (p.a.max_q_len > 0 && c1 - c0 > p.a.max_q_len)
+        *error = CG_ERR_INVALID_ARG;
+    q->row0 = c0;
+    q->nq = c1 - c0;
+    q->kv = kv;
+    q->rows = q->nq * p.ratio;   // at most tokens * q_heads, which fits
+    return *error == CG_OK && c1 > c0;
+}
+
+// ------------------------------------------------------ barriers and copies
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p)
+{
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+__device__ __forceinline__ void bar_init(uint64_t *bar, uint32_t count)
+{
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bar_init_fence()
+{
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
+                 "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t bytes,
+                                          uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(smem_addr(dst)),
+        "l"(src), "r"(bytes), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Polls before a wait gives up; each may suspend the thread for a while.
+constexpr uint32_t kBarWaitLimit = 1u << 20;
+
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
+{
+    const uint32_t at = smem_addr(bar);
+    for (uint32_t i = 0; i < kBarWaitLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(at), "r"(parity)
+            : "memory");
+        if (done)
+            return true;
+    }
+    return false;
+}
+
+// ------------------------------------------------------------------ launches
+
+// Most blocks of the kernel for few rows, whose partial results the
+// workspace holds.
+constexpr int kFewMaxBlocks = 320;
+
+size_t attn_few_workspace(int head_size, int max_rows);
+cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max_rows, void *ws,
+                            cudaStream_t s);

@@ -7,11 +7,15 @@
 // sum_t p_t v^_t = sum_t (p_t s_t) (n_t - 8) + sum_t p_t (lo_t + 8 s_t): the matrix
 // instructions take the codes themselves as bf16, which hold them exactly, and
 // the group's parameters meet one score or one probability, not every value.
-// A code becomes bf16 by one masked or into the mantissa of 128 (K: 128 + n)
-// or of 16 (V: 16 + n); the offsets come off exactly: for K through the
-// accumulator's start, -128 sum q, for V through a product with ones, which
-// sums the same rounded p s that the codes met. Roundings: p s to bf16 (2^-8
-// relative); scores, sums and the running maximum stay in fp32.
+// A code becomes bf16 by one mask: a bf16 whose bits are 0 .. 255 (a subnormal
+// or the first binade) is those bits times 2^-133, so the codes of bits 0..3 are
+// n 2^-133 and those of bits 4..7 are n 2^-129 where they lie. The powers of two
+// come off exactly: queries are scaled per row (and by 1/16 at the channels
+// of the upper codes) so that their largest is near 2^126, p s by 2^110 (less
+// where a large s would overflow), and results by the inverse. Sum p s 8 is taken
+// by a product with a constant matrix, from the same rounded p s that the codes
+// met. Roundings: p s to bf16 (2^-8 relative); scores, sums and the running
+// maximum stay in fp32.
 //
 // Tiles. mma.sync m16n8k16 with the tokens (K) or channels (V) as the 16 rows
 // and 8 query rows as columns, so 4 or 8 query heads fill an instruction that
@@ -35,11 +39,12 @@
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 4;       // blobs in flight per warp (a power of two)
 constexpr int kMinPiece = kWarps;   // blobs of a block, at least
-constexpr float kNone = -INFINITY;
+constexpr float kNone = -3.0e38f;   // no maximum yet; finite, so that differences are numbers
+constexpr int kStartExp = 110;      // exponent that p s starts with
 
 // ---------------------------------------------------------------- schedule
 
@@ -235,16 +240,17 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
-// Codes i and i + 4 of a word as the bf16 pair (128 + n, 128 + n).
-__device__ __forceinline__ uint32_t codes128(uint32_t w, int i)
+// Codes i and i + 4 of a word as a bf16 pair: n 2^-133 for even i, n 2^-129 for
+// odd i (bf16 bits 0 .. 255 count in steps of 2^-133).
+__device__ __forceinline__ uint32_t codes_of(uint32_t w, int i)
 {
-    return ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    return (i < 2 ? w : w >> 8) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
 }
+constexpr uint32_t kEight = 0x00080008u;   // 8 2^-133, twice
 
-// Codes i and i + 4 of a word as the bf16 pair (16 + n, 16 + n).
-__device__ __forceinline__ uint32_t codes16(uint32_t w, int i)
+__device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
 {
-    return ((i == 0 ? w << 3 : w >> (4 * i - 3)) & 0x00780078u) | 0x41804180u;
+    return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
 template <int N>
@@ -286,7 +292,7 @@ struct FewShared {
 };
 
 template <typename B, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(AttnArgs p, float *parts)
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(AttnArgs p, float *parts)
 {
     using S = FewShared<B, NT>;
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG, RU = S::RU;
@@ -307,40 +313,49 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
 
     const int bpp = p.page_tokens / 16;
-    // ---- the warp's feeder (lane 0 issues; all lanes keep its state)
+    // ---- the warp's feeder: copies a few blobs ahead of the warp, through the same units.
+    // Each lane holds one page id of the 32 from f_p0 on.
+    const uint32_t page_bytes = (uint32_t)p.heads * bpp * B::kBytes;
     Unit fu;
     unit_at<RU>(p, at, count, &fu);
     int64_t f_pos = fu.b1 - fu.b0;   // blobs of the piece up to the end of the feeder's unit
-    int f_b, f_e;
+    int f_b, f_e, f_in = 0, f_page = 0, f_p0 = -64, f_id = -1;
     warp_range(fu, warp, &f_b, &f_e);
-    int f_in = 0, f_page = 0;
-    bool f_jump = true;              // the page has to be looked up again
+    bool f_jump = true;              // the page has to be worked out again
     uint32_t issued = 0;
     auto feed = [&]() {
         // one more blob into the ring, if the piece has one for this warp
-        while (f_b >= f_e) {
-            if (f_pos >= count)
-                return;
-            unit_next<RU>(p, count - f_pos, &fu);
-            f_pos += fu.b1 - fu.b0;
-            warp_range(fu, warp, &f_b, &f_e);
+        if (f_b >= f_e) {
+            do {
+                if (f_pos >= count)
+                    return;
+                unit_next<RU>(p, count - f_pos, &fu);
+                f_pos += fu.b1 - fu.b0;
+                warp_range(fu, warp, &f_b, &f_e);
+            } while (f_b >= f_e);
             f_jump = true;
+            f_p0 = -64;
         }
-        const int ab = f_b < fu.span.sink ? f_b : f_b + fu.span.skip;
         if (f_jump || f_b == fu.span.sink) {
+            const int ab = f_b < fu.span.sink ? f_b : f_b + fu.span.skip;
             f_page = ab / bpp;
             f_in = ab - f_page * bpp;
             f_jump = false;
         }
+        if ((unsigned)(f_page - f_p0) >= 32u) {
+            f_p0 = f_page;
+            f_id = f_page + lane < p.a.table_width && fu.q.kv > 0
+                       ? p.a.block_table[fu.r * p.a.table_stride + f_page + lane]
+                       : -1;
+        }
+        const int id = __shfl_sync(0xFFFFFFFFu, f_id, f_page - f_p0);
         const int st = issued & (kStages - 1);
         if (lane == 0) {
-            int id = -1;
-            if (fu.q.kv > 0)
-                id = p.a.block_table[fu.r * p.a.table_stride + f_page];
-            const bool ok = id >= 0 && id < p.num_pages;
+            const bool ok = (unsigned)id < (unsigned)p.num_pages;
             sm.bad[warp][st] = !ok;
             if (ok) {
-                const uint8_t *src = p.layer + (((size_t)id * p.heads + fu.h) * bpp + f_in) * B::kBytes;
+                const uint8_t *src = p.layer + (uint64_t)(uint32_t)id * page_bytes +
+                                     (uint32_t)(fu.h * bpp + f_in) * B::kBytes;
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_expect(&sm.full[warp][st], B::kBytes);
                 bulk_copy(sm.ring[warp][st], src, B::kBytes, &sm.full[warp][st]);
@@ -370,8 +385,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
         // ---- queries: column g of row tile nt is row rt * RU + 8 nt + g
         const int row_base = u.rt * RU;
         uint32_t qf[NT][NW][4];
-        float qs[NT][NG][2];         // sums of q per group, rows 2t and 2t + 1
-        int x[NT][2];                // their positions (-1: no such row)
+        float qs[NT][NG][2];         // scale2 times the sums of q per group, rows 2t and 2t + 1
+        float rho[NT][2];            // scale2 over the power of two in qf
+        int x[NT][2];                // positions of rows 2t and 2t + 1 (-1: no such row)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = row_base + 8 * nt + g;
@@ -379,25 +395,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
             const int qt = there ? row / p.ratio : 0, qh = u.h * p.ratio + (there ? row - qt * p.ratio : 0);
             const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.a.q) +
                                      (int64_t)(u.q.row0 + qt) * p.a.q_token_stride + qh * p.a.q_head_stride;
+            uint4 v[NW];
+            uint32_t top = 0;        // largest |q| of the row (as bf16 bits, in both halves)
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                v[w] = there ? *reinterpret_cast<const uint4 *>(q + 32 * w + 8 * t) : make_uint4(0, 0, 0, 0);
+                top = __vmaxu2(top, v[w].x & 0x7FFF7FFFu);
+                top = __vmaxu2(top, v[w].y & 0x7FFF7FFFu);
+                top = __vmaxu2(top, v[w].z & 0x7FFF7FFFu);
+                top = __vmaxu2(top, v[w].w & 0x7FFF7FFFu);
+            }
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            // exact: |q| 2^fe stays below 2^127; small rows (and 0) take the largest factor
+            int fe = 126 - ((int)(top >> 7) - 127);
+            fe = fe < 127 ? fe : 127;
+            const float up = pow2(fe), up16 = pow2(fe - 4);
+            // scale2 2^(133 - fe) in two steps: the power alone may pass 2^127
+            const float back = p.scale2 * pow2(66) * pow2(67 - fe);
             float sum[NG] = {};
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const uint4 v = there ? *reinterpret_cast<const uint4 *>(q + 32 * w + 8 * t)
-                                      : make_uint4(0, 0, 0, 0);
+                const uint4 c = v[w];
                 // channels i and i + 4 side by side, as the codes of a word come
-                qf[nt][w][0] = __byte_perm(v.x, v.z, 0x5410);
-                qf[nt][w][1] = __byte_perm(v.x, v.z, 0x7632);
-                qf[nt][w][2] = __byte_perm(v.y, v.w, 0x5410);
-                qf[nt][w][3] = __byte_perm(v.y, v.w, 0x7632);
-                sum[w / WPG] += par_s(v.x) + par_lo(v.x) + par_s(v.y) + par_lo(v.y) + par_s(v.z) +
-                                par_lo(v.z) + par_s(v.w) + par_lo(v.w);
+                qf[nt][w][0] = pack_bf16(par_s(c.x) * up, par_s(c.z) * up);
+                qf[nt][w][1] = pack_bf16(par_lo(c.x) * up16, par_lo(c.z) * up16);
+                qf[nt][w][2] = pack_bf16(par_s(c.y) * up, par_s(c.w) * up);
+                qf[nt][w][3] = pack_bf16(par_lo(c.y) * up16, par_lo(c.w) * up16);
+                sum[w / WPG] += par_s(c.x) + par_lo(c.x) + par_s(c.y) + par_lo(c.y) + par_s(c.z) +
+                                par_lo(c.z) + par_s(c.w) + par_lo(c.w);
             }
+            rho[nt][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t);
+            rho[nt][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
                 sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
-                qs[nt][i][0] = __shfl_sync(0xFFFFFFFFu, sum[i], 8 * t);
-                qs[nt][i][1] = __shfl_sync(0xFFFFFFFFu, sum[i], 8 * t + 4);
+                qs[nt][i][0] = p.scale2 * __shfl_sync(0xFFFFFFFFu, sum[i], 8 * t);
+                qs[nt][i][1] = p.scale2 * __shfl_sync(0xFFFFFFFFu, sum[i], 8 * t + 4);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -415,6 +451,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
         float ones[NG][NT][4] = {};
         float mid[NG][NT][2] = {};
         float m[NT][2], l[NT][2];
+        int ve = kStartExp;          // p s is taken times 2^ve
+        float vup = pow2(kStartExp), s_most = pow2(118 - kStartExp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             for (int j = 0; j < 2; ++j) {
@@ -441,21 +479,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
                 load_words(k1, blob + B::kKCodes + (g + 8) * (D / 2) + t * (D / 8));
                 load_words(kp0, blob + B::kKParams + g * 4 * NG);
                 load_words(kp1, blob + B::kKParams + (g + 8) * 4 * NG);
-                float z[NT][4] = {};
+                float z[NT][4] = {}, zl[NT][4] = {};
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
-                    float acc[NT][4];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            acc[nt][j] = -128.0f * qs[nt][gi][j & 1];
+                    float acc[NT][4] = {};
 #pragma unroll
                     for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
 #pragma unroll
                         for (int i = 0; i < 4; i += 2) {
-                            const uint32_t a0 = codes128(k0[w], i), a1 = codes128(k1[w], i);
-                            const uint32_t a2 = codes128(k0[w], i + 1), a3 = codes128(k1[w], i + 1);
+                            const uint32_t a0 = codes_of(k0[w], i), a1 = codes_of(k1[w], i);
+                            const uint32_t a2 = codes_of(k0[w], i + 1), a3 = codes_of(k1[w], i + 1);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
                                 mma16816(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
@@ -466,8 +499,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            z[nt][j] = fmaf(s0, acc[nt][j], fmaf(l0, qs[nt][gi][j], z[nt][j]));
-                            z[nt][2 + j] = fmaf(s1, acc[nt][2 + j], fmaf(l1, qs[nt][gi][j], z[nt][2 + j]));
+                            z[nt][j] = fmaf(s0, acc[nt][j], z[nt][j]);
+                            z[nt][2 + j] = fmaf(s1, acc[nt][2 + j], z[nt][2 + j]);
+                            zl[nt][j] = fmaf(l0, qs[nt][gi][j], zl[nt][j]);
+                            zl[nt][2 + j] = fmaf(l1, qs[nt][gi][j], zl[nt][2 + j]);
                         }
                 }
                 uint32_t vp0[NG], vp1[NG];
@@ -477,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        z[nt][j] *= p.scale2;
+                        z[nt][j] = fmaf(z[nt][j], rho[nt][j & 1], zl[nt][j]);
                 const bool whole = tok + 15 <= x_lo && (x_hi - tok < window || tok + 15 < p.a.sinks);
                 if (!whole) {
 #pragma unroll
@@ -486,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
                         for (int j = 0; j < 4; ++j) {
                             const int at_tok = tok + g + (j >= 2 ? 8 : 0), xr = x[nt][j & 1];
                             const bool sees = at_tok <= xr && (xr - at_tok < window || at_tok < p.a.sinks);
-                            z[nt][j] = sees ? z[nt][j] : kNone;
+                            z[nt][j] = sees ? z[nt][j] : -INFINITY;
                         }
                     // parameters behind the last token may be anything
 #pragma unroll
@@ -497,13 +532,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
                 }
                 // ---- running maximum: raised only when a score exceeds it by 2^8, so
                 // that probabilities stay below 2^8 and rescaling is rare
-                bool raise = false;
+                float over = z[0][0] - m[0][0];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        raise |= fmaxf(z[nt][j], z[nt][2 + j]) > m[nt][j] + 8.0f;
-                if (__any_sync(0xFFFFFFFFu, raise)) {
+                    for (int j = 0; j < 4; ++j)
+                        over = fmaxf(over, z[nt][j] - m[nt][j & 1]);
+                if (__any_sync(0xFFFFFFFFu, over > 8.0f)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -513,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
                             for (int d = 4; d < 32; d <<= 1)
                                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
                             mx = fmaxf(mx, m[nt][j]);
-                            const float f = m[nt][j] == kNone ? 0.0f : exp2_fast(m[nt][j] - mx);
+                            const float f = exp2_fast(m[nt][j] - mx);
                             m[nt][j] = mx;
                             l[nt][j] *= f;
 #pragma unroll
@@ -528,14 +563,40 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
                             }
                         }
                 }
+                // p s 2^ve has to stay below 2^127 (p is at most 2^8)
+                float s_sum = 0.0f;
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi)
+                    s_sum += par_s(vp0[gi]) + par_s(vp1[gi]);
+                if (__any_sync(0xFFFFFFFFu, s_sum > s_most)) {
+                    float top = fminf(s_sum, 3.0e38f);
+#pragma unroll
+                    for (int d = 1; d < 32; d <<= 1)
+                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    const int e = 117 - ((int)(__float_as_uint(top) >> 23) - 127);   // top < 2^(118 - e)
+                    const float f = ve - e > 126 ? 0.0f : pow2(e - ve);
+                    ve = e;
+                    vup = pow2(e);
+                    s_most = pow2(118 - e < 127 ? 118 - e : 127);
+#pragma unroll
+                    for (int c = 0; c < NW * 2; ++c)
+                        for (int nt = 0; nt < NT; ++nt)
+                            for (int j = 0; j < 4; ++j)
+                                o[c][nt][j] *= f;
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi)
+                        for (int nt = 0; nt < NT; ++nt)
+                            for (int j = 0; j < 2; ++j)
+                                ones[gi][nt][j] *= f;
+                }
+                float ps[NT][4];     // p 2^ve
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float base = m[nt][j] == kNone ? 0.0f : m[nt][j];
-                        z[nt][j] = exp2_fast(z[nt][j] - base);
-                        z[nt][2 + j] = exp2_fast(z[nt][2 + j] - base);
-                        l[nt][j] += z[nt][j] + z[nt][2 + j];
+                    for (int j = 0; j < 4; ++j) {
+                        z[nt][j] = exp2_fast(z[nt][j] - m[nt][j & 1]);
+                        ps[nt][j] = z[nt][j] * vup;
+                        l[nt][j & 1] += z[nt][j];
                     }
                 // ---- values
                 uint32_t v0[NW], v1[NW];
@@ -551,17 +612,16 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
 #pragma unroll
                         for (int j = 0; j < 2; ++j)
                             mid[gi][nt][j] += fmaf(z[nt][j], c0, z[nt][2 + j] * c1);
-                        pf[nt][0] = transpose8x8(pack_bf16(z[nt][0] * s0, z[nt][1] * s0));
-                        pf[nt][1] = transpose8x8(pack_bf16(z[nt][2] * s1, z[nt][3] * s1));
-                        mma16816(ones[gi][nt], 0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u,
-                                 pf[nt][0], pf[nt][1]);
+                        pf[nt][0] = transpose8x8(pack_bf16(ps[nt][0] * s0, ps[nt][1] * s0));
+                        pf[nt][1] = transpose8x8(pack_bf16(ps[nt][2] * s1, ps[nt][3] * s1));
+                        mma16816(ones[gi][nt], kEight, kEight, kEight, kEight, pf[nt][0], pf[nt][1]);
                     }
 #pragma unroll
                     for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
 #pragma unroll
                         for (int i = 0; i < 4; i += 2) {
-                            const uint32_t a0 = codes16(v0[w], i), a1 = codes16(v0[w], i + 1);
-                            const uint32_t a2 = codes16(v1[w], i), a3 = codes16(v1[w], i + 1);
+                            const uint32_t a0 = codes_of(v0[w], i), a1 = codes_of(v0[w], i + 1);
+                            const uint32_t a2 = codes_of(v1[w], i), a3 = codes_of(v1[w], i + 1);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
                                 mma16816(o[w * 2 + i / 2][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
@@ -603,10 +663,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     mx = fmaxf(mx, sm.m[w][8 * nt + 2 * t + j]);
-                // without a maximum the sum is 0, or NaN for a query with NaN
-                f[nt][j] = m[nt][j] == kNone ? l[nt][j] : exp2_fast(m[nt][j] - mx);
+                f[nt][j] = exp2_fast(m[nt][j] - mx);
             }
         constexpr int kPartW = NW / NT;   // words (32 channels) of a pass
+        // 2^(133 - ve) in two steps: codes and p s had 2^-133 and 2^ve
+        const float down0 = pow2(66), down1 = pow2(67 - (ve < -59 ? -59 : ve));
 #pragma unroll
         for (int pass = 0; pass < NT; ++pass) {
 #pragma unroll
@@ -616,11 +677,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
 #pragma unroll
                     for (int w = 0; w < kPartW; ++w) {
                         const int ww = pass * kPartW + w, gi = ww / WPG;
-                        const float off = mid[gi][nt][j] - 24.0f * ones[gi][nt][j];
-                        const float4 v = make_float4((o[2 * ww][nt][j] + off) * f[nt][j],
-                                                     (o[2 * ww][nt][2 + j] + off) * f[nt][j],
-                                                     (o[2 * ww + 1][nt][j] + off) * f[nt][j],
-                                                     (o[2 * ww + 1][nt][2 + j] + off) * f[nt][j]);
+                        const float off = mid[gi][nt][j], eight = ones[gi][nt][j];
+                        float4 v;    // channels 4g .. 4g + 3; the upper codes counted 16-fold
+                        v.x = (o[2 * ww][nt][j] - eight) * down0 * down1;
+                        v.y = (fmaf(o[2 * ww][nt][2 + j], 0.0625f, -eight)) * down0 * down1;
+                        v.z = (o[2 * ww + 1][nt][j] - eight) * down0 * down1;
+                        v.w = (fmaf(o[2 * ww + 1][nt][2 + j], 0.0625f, -eight)) * down0 * down1;
+                        v = make_float4((v.x + off) * f[nt][j], (v.y + off) * f[nt][j],
+                                        (v.z + off) * f[nt][j], (v.w + off) * f[nt][j]);
                         *reinterpret_cast<float4 *>(&sm.merge[warp][8 * nt + 2 * t + j][32 * w + 4 * g]) = v;
                     }
             __syncthreads();
@@ -640,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 2 : 1) k_attention_few(Att
                     sum.z += v.z;
                     sum.w += v.w;
                     const float mw = sm.m[w][row];
-                    ls += mw == kNone ? sm.l[w][row] : sm.l[w][row] * exp2_fast(mw - mx);
+                    ls += sm.l[w][row] * exp2_fast(mw - mx);
                 }
                 const int ch = pass * (D / NT) + c;
                 if (from_before || goes_on) {
@@ -703,11 +767,7 @@ __global__ void __launch_bounds__(kThreads) k_attention_join(AttnArgs p, int pie
             const float *part = parts + ((size_t)k * 2 + (k == c ? 1 : 0)) * kPartFloats<D, RU>;
             const float mk = part[RU * D + row], lk = part[RU * D + RU + row];
             const float4 v = *reinterpret_cast<const float4 *>(part + row * D + ch);
-            if (mk == kNone) {
-                l += lk;
-                continue;
-            }
-            const float mn = fmaxf(m, mk), f = m == kNone ? 0.0f : exp2_fast(m - mn), e = exp2_fast(mk - mn);
+            const float mn = fmaxf(m, mk), f = exp2_fast(m - mn), e = exp2_fast(mk - mn);
             m = mn;
             l = l * f + lk * e;
             sum.x = sum.x * f + v.x * e;
@@ -740,7 +800,7 @@ cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
                                    (int)sizeof(Sh));
     if (err != cudaSuccess)
         return err;
-    int blocks = (NT == 1 ? 2 : 1) * sms;
+    int blocks = (NT == 1 ? 3 : 2) * sms;
     if (blocks > kFewMaxBlocks)
         blocks = kFewMaxBlocks;
     k_attention_few<B, NT><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);

@@ -102,7 +102,7 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
 
 // Most blocks of the kernel for few rows, whose partial results the
 // workspace holds.
-constexpr int kFewMaxBlocks = 320;
+constexpr int kFewMaxBlocks = 480;
 
 size_t attn_few_workspace(int head_size, int max_rows);
 cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max_rows, void *ws,

@@ -11,10 +11,12 @@
 // or the first binade) is those bits times 2^-133, so the codes of bits 0..3 are
 // n 2^-133 and those of bits 4..7 are n 2^-129 where they lie. The powers of two
 // come off exactly: queries are scaled per row (and by 1/16 at the channels
-// of the upper codes) so that their largest is near 2^126, p s by 2^110 (less
-// where a large s would overflow), and results by the inverse. Sum p s 8 is taken
-// by a product with a constant matrix, from the same rounded p s that the codes
-// met. Roundings: p s to bf16 (2^-8 relative); scores, sums and the running
+// of the upper codes) so that their largest is near 2^126, p by 2^90 (less where
+// a large s or lo would overflow), and results by the inverse. What is summed
+// beside the codes is summed by matrix instructions too: lo (sum q) with sum q
+// in two or three bf16 parts (16 bits at least), sum p s, sum p lo, sum p and
+// sum p s 8 as rows of one small accumulator. Roundings: p to bf16, for every sum
+// alike, and p s to bf16 (2^-8 relative each); scores, sums and the running
 // maximum stay in fp32.
 //
 // Tiles. mma.sync m16n8k16 with the tokens (K) or channels (V) as the 16 rows
@@ -42,9 +44,9 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStages = 4;       // blobs in flight per warp (a power of two)
-constexpr int kMinPiece = kWarps;   // blobs of a block, at least
+constexpr int kMinPiece = 4 * kWarps;   // blobs of a block, at least
 constexpr float kNone = -3.0e38f;   // no maximum yet; finite, so that differences are numbers
-constexpr int kStartExp = 110;      // exponent that p s starts with
+constexpr int kStartExp = 90;       // p is taken times 2^90 at first
 
 // ---------------------------------------------------------------- schedule
 
@@ -226,6 +228,25 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same into a fresh accumulator.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                               uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
+// Product of bf16 pairs, rounded to bf16.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t c;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
 {
     uint32_t y;
@@ -385,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
         // ---- queries: column g of row tile nt is row rt * RU + 8 nt + g
         const int row_base = u.rt * RU;
         uint32_t qf[NT][NW][4];
-        float qs[NT][NG][2];         // scale2 times the sums of q per group, rows 2t and 2t + 1
+        uint32_t qs[NT][2];          // scale2 times the sum of q in group t % NG, as parts of
+                                     // which the product with (s, lo) takes the lo half
         float rho[NT][2];            // scale2 over the power of two in qf
         int x[NT][2];                // positions of rows 2t and 2t + 1 (-1: no such row)
 #pragma unroll
@@ -428,12 +450,30 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             }
             rho[nt][0] = __shfl_sync(0xFFFFFFFFu, back, 8 * t);
             rho[nt][1] = __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4);
+            float mine = 0.0f;       // of group t % NG, whole row
 #pragma unroll
             for (int i = 0; i < NG; ++i) {
                 sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
                 sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
-                qs[nt][i][0] = p.scale2 * __shfl_sync(0xFFFFFFFFu, sum[i], 8 * t);
-                qs[nt][i][1] = p.scale2 * __shfl_sync(0xFFFFFFFFu, sum[i], 8 * t + 4);
+                if (t % NG == i)
+                    mine = p.scale2 * sum[i];
+            }
+            uint32_t part[4] = {0, 0, 0, 0};   // high halves: mine, in descending parts
+#pragma unroll
+            for (int i = 0; i < 3; ++i) {
+                part[i] = pack_bf16(0.0f, mine);
+                mine -= par_lo(part[i]);
+            }
+            if (NG == 4) {
+                qs[nt][0] = part[0];
+                qs[nt][1] = part[1];
+            } else {
+                qs[nt][0] = part[0];
+#pragma unroll
+                for (int i = 1; i < 4; ++i)
+                    if (t / NG == i)
+                        qs[nt][0] = part[i];
+                qs[nt][1] = NG == 2 && t < 2 ? part[2] : 0;
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -448,17 +488,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
         const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
 
         float o[NW * 2][NT][4] = {};
-        float ones[NG][NT][4] = {};
-        float mid[NG][NT][2] = {};
-        float m[NT][2], l[NT][2];
-        int ve = kStartExp;          // p s is taken times 2^ve
-        float vup = pow2(kStartExp), s_most = pow2(118 - kStartExp);
+        // rows of 16: g < NG sum p s_g, NG + g sum p lo_g, 8 + g sum p s_g 8 2^-133, 15 sum p
+        float aux[NT][4] = {};
+        uint32_t eight[NG];          // the rows 8 + g
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi)
+            eight[gi] = g == gi ? kEight : 0;
+        const uint32_t ones = g == 7 ? 0x3F803F80u : 0;
+        const uint32_t par_sel = g < NG ? 0x5410u : 0x7632u;   // s or lo of two words
+        const uint32_t par_keep = g < 2 * NG ? 0xFFFFFFFFu : 0;
+        const int par_at = B::kVParams + 2 * t * 4 * NG + (g % NG) * 4;
+        float m[NT][2];              // running maximum of the scores, less ve
+        int ve = kStartExp;          // p is taken times 2^ve
+        float limit = 8.0f + kStartExp;
+        uint32_t par_bias = 0x80008000u - ((101 - kStartExp + 127) << 7) * 0x10001u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            for (int j = 0; j < 2; ++j) {
-                m[nt][j] = kNone;
-                l[nt][j] = 0.0f;
-            }
+            m[nt][0] = m[nt][1] = kNone;
 
         int b, e;
         warp_range(u, warp, &b, &e);
@@ -479,10 +525,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 load_words(k1, blob + B::kKCodes + (g + 8) * (D / 2) + t * (D / 8));
                 load_words(kp0, blob + B::kKParams + g * 4 * NG);
                 load_words(kp1, blob + B::kKParams + (g + 8) * 4 * NG);
-                float z[NT][4] = {}, zl[NT][4] = {};
+                float z[NT][4] = {}, zl[NT][4];
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
-                    float acc[NT][4] = {};
+                    float acc[NT][4];
 #pragma unroll
                     for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
 #pragma unroll
@@ -491,28 +537,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                             const uint32_t a2 = codes_of(k0[w], i + 1), a3 = codes_of(k1[w], i + 1);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16816(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
+                                if (w == gi * WPG && i == 0)
+                                    mma16816_first(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
+                                else
+                                    mma16816(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
                         }
-                    const float s0 = par_s(kp0[gi]), l0 = par_lo(kp0[gi]);
-                    const float s1 = par_s(kp1[gi]), l1 = par_lo(kp1[gi]);
+                    const float s0 = par_s(kp0[gi]), s1 = par_s(kp1[gi]);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            z[nt][j] = fmaf(s0, acc[nt][j], z[nt][j]);
-                            z[nt][2 + j] = fmaf(s1, acc[nt][2 + j], z[nt][2 + j]);
-                            zl[nt][j] = fmaf(l0, qs[nt][gi][j], zl[nt][j]);
-                            zl[nt][2 + j] = fmaf(l1, qs[nt][gi][j], zl[nt][2 + j]);
+                            z[nt][j] = gi ? fmaf(s0, acc[nt][j], z[nt][j]) : s0 * acc[nt][j];
+                            z[nt][2 + j] = gi ? fmaf(s1, acc[nt][2 + j], z[nt][2 + j]) : s1 * acc[nt][2 + j];
                         }
                 }
-                uint32_t vp0[NG], vp1[NG];
-                load_words(vp0, blob + B::kVParams + g * 4 * NG);
-                load_words(vp1, blob + B::kVParams + (g + 8) * 4 * NG);
+                {
+                    const uint32_t a0 = *reinterpret_cast<const uint32_t *>(blob + B::kKParams +
+                                                                            (g * NG + t % NG) * 4);
+                    const uint32_t a1 = *reinterpret_cast<const uint32_t *>(blob + B::kKParams +
+                                                                            ((g + 8) * NG + t % NG) * 4);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816_first(zl[nt], a0, a1, a0, a1, qs[nt][0], qs[nt][1]);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         z[nt][j] = fmaf(z[nt][j], rho[nt][j & 1], zl[nt][j]);
+                // rows of the V parameters: s or lo of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
+                uint32_t va[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t *at = blob + par_at + i * 8 * 4 * NG;
+                    va[i] = __byte_perm(*reinterpret_cast<const uint32_t *>(at),
+                                        *reinterpret_cast<const uint32_t *>(at + 4 * NG), par_sel) &
+                            par_keep;
+                }
                 const bool whole = tok + 15 <= x_lo && (x_hi - tok < window || tok + 15 < p.a.sinks);
                 if (!whole) {
 #pragma unroll
@@ -525,9 +586,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                         }
                     // parameters behind the last token may be anything
 #pragma unroll
-                    for (int gi = 0; gi < NG; ++gi) {
-                        vp0[gi] = tok + g < u.q.kv ? vp0[gi] : 0;
-                        vp1[gi] = tok + g + 8 < u.q.kv ? vp1[gi] : 0;
+                    for (int i = 0; i < 2; ++i) {
+                        const int first = tok + 2 * t + 8 * i;
+                        va[i] &= first + 1 < u.q.kv ? 0xFFFFFFFFu : first < u.q.kv ? 0xFFFFu : 0u;
                     }
                 }
                 // ---- running maximum: raised only when a score exceeds it by 2^8, so
@@ -538,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         over = fmaxf(over, z[nt][j] - m[nt][j & 1]);
-                if (__any_sync(0xFFFFFFFFu, over > 8.0f)) {
+                if (__any_sync(0xFFFFFFFFu, over > limit)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -547,74 +608,69 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1)
                                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-                            mx = fmaxf(mx, m[nt][j]);
+                            mx = fmaxf(mx - (float)ve, m[nt][j]);
                             const float f = exp2_fast(m[nt][j] - mx);
                             m[nt][j] = mx;
-                            l[nt][j] *= f;
 #pragma unroll
                             for (int c = 0; c < NW * 2; ++c) {
                                 o[c][nt][j] *= f;
                                 o[c][nt][2 + j] *= f;
                             }
-#pragma unroll
-                            for (int gi = 0; gi < NG; ++gi) {
-                                ones[gi][nt][j] *= f;
-                                mid[gi][nt][j] *= f;
-                            }
+                            aux[nt][j] *= f;
+                            aux[nt][2 + j] *= f;
                         }
                 }
-                // p s 2^ve has to stay below 2^127 (p is at most 2^8)
-                float s_sum = 0.0f;
-#pragma unroll
-                for (int gi = 0; gi < NG; ++gi)
-                    s_sum += par_s(vp0[gi]) + par_s(vp1[gi]);
-                if (__any_sync(0xFFFFFFFFu, s_sum > s_most)) {
-                    float top = fminf(s_sum, 3.0e38f);
+                // sums of p s and p lo have to stay finite: p is at most 2^(ve + 8), s and |lo|
+                // below 2^(101 - ve), and 2^16 tokens of a warp reach 2^125
+                const uint32_t va_top = __vmaxu2(va[0] & 0x7FFF7FFFu, va[1] & 0x7FFF7FFFu);
+                if (__any_sync(0xFFFFFFFFu, (va_top + par_bias) & 0x80008000u)) {
+                    uint32_t top = max(va_top & 0xFFFFu, va_top >> 16);
 #pragma unroll
                     for (int d = 1; d < 32; d <<= 1)
-                        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    const int e = 117 - ((int)(__float_as_uint(top) >> 23) - 127);   // top < 2^(118 - e)
-                    const float f = ve - e > 126 ? 0.0f : pow2(e - ve);
-                    ve = e;
-                    vup = pow2(e);
-                    s_most = pow2(118 - e < 127 ? 118 - e : 127);
+                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                    const int e = 100 - ((int)(top >> 7) - 127);   // top < 2^(101 - e)
+                    const float f = pow2(e - ve);
 #pragma unroll
-                    for (int c = 0; c < NW * 2; ++c)
-                        for (int nt = 0; nt < NT; ++nt)
-                            for (int j = 0; j < 4; ++j)
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                            for (int c = 0; c < NW * 2; ++c)
                                 o[c][nt][j] *= f;
+                            aux[nt][j] *= f;
+                        }
 #pragma unroll
-                    for (int gi = 0; gi < NG; ++gi)
-                        for (int nt = 0; nt < NT; ++nt)
-                            for (int j = 0; j < 2; ++j)
-                                ones[gi][nt][j] *= f;
-                }
-                float ps[NT][4];     // p 2^ve
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        z[nt][j] = exp2_fast(z[nt][j] - m[nt][j & 1]);
-                        ps[nt][j] = z[nt][j] * vup;
-                        l[nt][j & 1] += z[nt][j];
+                        for (int j = 0; j < 2; ++j)
+                            m[nt][j] += (float)(ve - e);
                     }
+                    ve = e;
+                    limit = 8.0f + (float)e;
+                    par_bias = 0x80008000u - (uint32_t)min((101 - e + 127) << 7, 0x7F80) * 0x10001u;
+                }
+                uint32_t pf[NT][2];  // p as the other factor: row g, tokens 2t, 2t + 1 (+ 8)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        z[nt][j] = exp2_fast(z[nt][j] - m[nt][j & 1]);
+                    pf[nt][0] = transpose8x8(pack_bf16(z[nt][0], z[nt][1]));
+                    pf[nt][1] = transpose8x8(pack_bf16(z[nt][2], z[nt][3]));
+                    mma16816(aux[nt], va[0], ones, va[1], ones, pf[nt][0], pf[nt][1]);
+                }
                 // ---- values
                 uint32_t v0[NW], v1[NW];
                 load_words(v0, blob + B::kVCodes + t * D + g * (D / 8));
                 load_words(v1, blob + B::kVCodes + (t + 4) * D + g * (D / 8));
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
-                    const float s0 = par_s(vp0[gi]), s1 = par_s(vp1[gi]);
-                    const float c0 = fmaf(8.0f, s0, par_lo(vp0[gi])), c1 = fmaf(8.0f, s1, par_lo(vp1[gi]));
-                    uint32_t pf[NT][2];
+                    const uint32_t s0 = __shfl_sync(0xFFFFFFFFu, va[0], 4 * gi + t);
+                    const uint32_t s1 = __shfl_sync(0xFFFFFFFFu, va[1], 4 * gi + t);
+                    uint32_t ps[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            mid[gi][nt][j] += fmaf(z[nt][j], c0, z[nt][2 + j] * c1);
-                        pf[nt][0] = transpose8x8(pack_bf16(ps[nt][0] * s0, ps[nt][1] * s0));
-                        pf[nt][1] = transpose8x8(pack_bf16(ps[nt][2] * s1, ps[nt][3] * s1));
-                        mma16816(ones[gi][nt], kEight, kEight, kEight, kEight, pf[nt][0], pf[nt][1]);
+                        ps[nt][0] = mul_bf16x2(pf[nt][0], s0);
+                        ps[nt][1] = mul_bf16x2(pf[nt][1], s1);
+                        mma16816(aux[nt], 0, eight[gi], 0, eight[gi], ps[nt][0], ps[nt][1]);
                     }
 #pragma unroll
                     for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
@@ -624,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                             const uint32_t a2 = codes_of(v1[w], i), a3 = codes_of(v1[w], i + 1);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt)
-                                mma16816(o[w * 2 + i / 2][nt], a0, a1, a2, a3, pf[nt][0], pf[nt][1]);
+                                mma16816(o[w * 2 + i / 2][nt], a0, a1, a2, a3, ps[nt][0], ps[nt][1]);
                         }
                 }
             }
@@ -634,20 +690,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
         }
 
         // ---- the warps' results of this unit, joined in shared memory
+        const float down = pow2(-ve);
+        float off[NT][NG][2], ex[NT][NG][2];   // sum p (lo + 8 s); sum p s 8, as o counts it
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int d = 4; d < 32; d <<= 1) {
-                    l[nt][j] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], d);
-#pragma unroll
-                    for (int gi = 0; gi < NG; ++gi)
-                        mid[gi][nt][j] += __shfl_xor_sync(0xFFFFFFFFu, mid[gi][nt][j], d);
+                for (int gi = 0; gi < NG; ++gi) {
+                    off[nt][gi][j] = (8.0f * __shfl_sync(0xFFFFFFFFu, aux[nt][j], 4 * gi + t) +
+                                      __shfl_sync(0xFFFFFFFFu, aux[nt][j], 4 * (NG + gi) + t)) * down;
+                    ex[nt][gi][j] = __shfl_sync(0xFFFFFFFFu, aux[nt][2 + j], 4 * gi + t);
                 }
-                if (g == 0) {
+                m[nt][j] += (float)ve;
+                if (g == 7) {
                     sm.m[warp][8 * nt + 2 * t + j] = m[nt][j];
-                    sm.l[warp][8 * nt + 2 * t + j] = l[nt][j];
+                    sm.l[warp][8 * nt + 2 * t + j] = aux[nt][2 + j] * down;
                 }
             }
         __syncthreads();
@@ -666,8 +724,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 f[nt][j] = exp2_fast(m[nt][j] - mx);
             }
         constexpr int kPartW = NW / NT;   // words (32 channels) of a pass
-        // 2^(133 - ve) in two steps: codes and p s had 2^-133 and 2^ve
-        const float down0 = pow2(66), down1 = pow2(67 - (ve < -59 ? -59 : ve));
+        const float down0 = pow2(66), down1 = pow2(67 - ve);   // 2^(133 - ve) in two steps
 #pragma unroll
         for (int pass = 0; pass < NT; ++pass) {
 #pragma unroll
@@ -677,14 +734,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 #pragma unroll
                     for (int w = 0; w < kPartW; ++w) {
                         const int ww = pass * kPartW + w, gi = ww / WPG;
-                        const float off = mid[gi][nt][j], eight = ones[gi][nt][j];
+                        const float e8 = ex[nt][gi][j], add = off[nt][gi][j];
                         float4 v;    // channels 4g .. 4g + 3; the upper codes counted 16-fold
-                        v.x = (o[2 * ww][nt][j] - eight) * down0 * down1;
-                        v.y = (fmaf(o[2 * ww][nt][2 + j], 0.0625f, -eight)) * down0 * down1;
-                        v.z = (o[2 * ww + 1][nt][j] - eight) * down0 * down1;
-                        v.w = (fmaf(o[2 * ww + 1][nt][2 + j], 0.0625f, -eight)) * down0 * down1;
-                        v = make_float4((v.x + off) * f[nt][j], (v.y + off) * f[nt][j],
-                                        (v.z + off) * f[nt][j], (v.w + off) * f[nt][j]);
+                        v.x = (o[2 * ww][nt][j] - e8) * down0 * down1;
+                        v.y = (fmaf(o[2 * ww][nt][2 + j], 0.0625f, -e8)) * down0 * down1;
+                        v.z = (o[2 * ww + 1][nt][j] - e8) * down0 * down1;
+                        v.w = (fmaf(o[2 * ww + 1][nt][2 + j], 0.0625f, -e8)) * down0 * down1;
+                        v = make_float4((v.x + add) * f[nt][j], (v.y + add) * f[nt][j],
+                                        (v.z + add) * f[nt][j], (v.w + add) * f[nt][j]);
                         *reinterpret_cast<float4 *>(&sm.merge[warp][8 * nt + 2 * t + j][32 * w + 4 * g]) = v;
                     }
             __syncthreads();
@@ -758,29 +815,50 @@ __global__ void __launch_bounds__(kThreads) k_attention_join(AttnArgs p, int pie
     const int last = (int)((end + chunk - 1) / chunk) - 1;   // the block that holds its end
     const int row_base = u.rt * RU;
     const int rows_here = (row_base + RU < u.q.rows ? row_base + RU : u.q.rows) - row_base;
+    // weights of the parts: 2^(m - max m), and the sums that they give
+    extern __shared__ float weight[];   // [RU][parts]
+    __shared__ float inv[RU];
+    const int n = last - c + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int row = warp; row < rows_here; row += kWarps) {
+        float mx = kNone, l = 0.0f;
+        for (int k = lane; k < n; k += 32)
+            mx = fmaxf(mx, parts[((size_t)(c + k) * 2 + (k == 0)) * kPartFloats<D, RU> + RU * D + row]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+        for (int k = lane; k < n; k += 32) {
+            const float *part = parts + ((size_t)(c + k) * 2 + (k == 0)) * kPartFloats<D, RU> + RU * D;
+            const float e = exp2_fast(part[row] - mx);
+            weight[row * n + k] = e;
+            l = fmaf(part[RU + row], e, l);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        if (lane == 0)
+            inv[row] = l == 0.0f ? 0.0f : 1.0f / l;
+    }
+    __syncthreads();
     constexpr int kQuads = D / 4;
     for (int i = threadIdx.x; i < rows_here * kQuads; i += kThreads) {
         const int row = i / kQuads, ch = (i - row * kQuads) * 4;
-        float m = kNone, l = 0.0f;
         float4 sum = make_float4(0, 0, 0, 0);
-        for (int k = c; k <= last; ++k) {
-            const float *part = parts + ((size_t)k * 2 + (k == c ? 1 : 0)) * kPartFloats<D, RU>;
-            const float mk = part[RU * D + row], lk = part[RU * D + RU + row];
-            const float4 v = *reinterpret_cast<const float4 *>(part + row * D + ch);
-            const float mn = fmaxf(m, mk), f = exp2_fast(m - mn), e = exp2_fast(mk - mn);
-            m = mn;
-            l = l * f + lk * e;
-            sum.x = sum.x * f + v.x * e;
-            sum.y = sum.y * f + v.y * e;
-            sum.z = sum.z * f + v.z * e;
-            sum.w = sum.w * f + v.w * e;
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float4 v = *reinterpret_cast<const float4 *>(
+                parts + ((size_t)(c + k) * 2 + (k == 0)) * kPartFloats<D, RU> + row * D + ch);
+            const float e = weight[row * n + k];
+            sum.x = fmaf(v.x, e, sum.x);
+            sum.y = fmaf(v.y, e, sum.y);
+            sum.z = fmaf(v.z, e, sum.z);
+            sum.w = fmaf(v.w, e, sum.w);
         }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const float f = inv[row];
         const int rr = row_base + row, qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
         __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
                              (int64_t)(u.q.row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride + ch;
         *reinterpret_cast<uint2 *>(out) =
-            make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
+            make_uint2(pack_bf16(sum.x * f, sum.y * f), pack_bf16(sum.z * f, sum.w * f));
     }
 }
 
@@ -804,7 +882,7 @@ cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
     if (blocks > kFewMaxBlocks)
         blocks = kFewMaxBlocks;
     k_attention_few<B, NT><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
-    k_attention_join<B::kD, 8 * NT><<<blocks, kThreads, 0, s>>>(p, blocks, parts);
+    k_attention_join<B::kD, 8 * NT><<<blocks, kThreads, 8 * NT * blocks * sizeof(float), s>>>(p, blocks, parts);
     return cudaGetLastError();
 }
 

@@ -43,7 +43,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;       // blobs in flight per warp (a power of two)
+constexpr int kRing = 4;         // blobs in a warp's ring
 constexpr int kMinPiece = 4 * kWarps;   // blobs of a block, at least
 constexpr float kNone = -3.0e38f;   // no maximum yet; finite, so that differences are numbers
 constexpr int kStartExp = 90;       // p is taken times 2^90 at first
@@ -302,14 +302,17 @@ constexpr int kPartFloats = RU *(D + 2);
 
 // ------------------------------------------------------------- main kernel
 
+// HB: blobs that a warp takes in one step. Two give its schedulers two
+// independent chains and halve what a step costs besides (waits, votes, the
+// next copy); with 16 rows (NT = 2) there are registers for one.
 template <typename B, int NT>
 struct FewShared {
-    static constexpr int RU = 8 * NT;
-    uint8_t ring[kWarps][kStages][B::kBytes];
+    static constexpr int RU = 8 * NT, HB = NT == 1 ? 2 : 1, kStages = kRing / HB;
+    uint8_t ring[kWarps][kStages][HB * B::kBytes];
     float merge[kWarps][RU][B::kD / NT];   // one of NT parts of the channels
     float m[kWarps][RU], l[kWarps][RU];
     uint64_t full[kWarps][kStages];
-    uint32_t bad[kWarps][kStages];         // the blob's page id was outside the cache
+    uint32_t there[kWarps][kStages];       // which blobs of the step were copied
 };
 
 template <typename B, int NT>
@@ -317,11 +320,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 {
     using S = FewShared<B, NT>;
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG, RU = S::RU;
+    constexpr int HB = S::HB, kStages = S::kStages;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
 
+    // the joining kernel's blocks may come up as this one's leave
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (lane == 0)
         for (int i = 0; i < kStages; ++i)
             bar_init(&sm.full[warp][i], 1);
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
     bool f_jump = true;              // the page has to be worked out again
     uint32_t issued = 0;
     auto feed = [&]() {
-        // one more blob into the ring, if the piece has one for this warp
+        // the next step's blobs into the ring, if the piece has more for this warp
         if (f_b >= f_e) {
             do {
                 if (f_pos >= count)
@@ -357,41 +363,57 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             f_jump = true;
             f_p0 = -64;
         }
-        if (f_jump || f_b == fu.span.sink) {
-            const int ab = f_b < fu.span.sink ? f_b : f_b + fu.span.skip;
-            f_page = ab / bpp;
-            f_in = ab - f_page * bpp;
-            f_jump = false;
+        const uint8_t *src[HB];
+        uint32_t there = 0;
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+            src[i] = nullptr;
+            if (f_b >= f_e)
+                break;
+            if (f_jump || f_b == fu.span.sink) {
+                const int ab = f_b < fu.span.sink ? f_b : f_b + fu.span.skip;
+                f_page = ab / bpp;
+                f_in = ab - f_page * bpp;
+                f_jump = false;
+            }
+            if ((unsigned)(f_page - f_p0) >= 32u) {
+                f_p0 = f_page;
+                f_id = f_page + lane < p.a.table_width && fu.q.kv > 0
+                           ? p.a.block_table[fu.r * p.a.table_stride + f_page + lane]
+                           : -1;
+            }
+            const int id = __shfl_sync(0xFFFFFFFFu, f_id, f_page - f_p0);
+            if ((unsigned)id < (unsigned)p.num_pages)
+                there |= 1u << i;
+            else if (fu.q.kv > 0 && lane == 0)
+                int4_set_status(p.status, CG_ERR_CORRUPT);
+            src[i] = p.layer + (uint64_t)(uint32_t)id * page_bytes + (uint32_t)(fu.h * bpp + f_in) * B::kBytes;
+            ++f_b;
+            if (++f_in == bpp) {
+                f_in = 0;
+                ++f_page;
+            }
         }
-        if ((unsigned)(f_page - f_p0) >= 32u) {
-            f_p0 = f_page;
-            f_id = f_page + lane < p.a.table_width && fu.q.kv > 0
-                       ? p.a.block_table[fu.r * p.a.table_stride + f_page + lane]
-                       : -1;
-        }
-        const int id = __shfl_sync(0xFFFFFFFFu, f_id, f_page - f_p0);
         const int st = issued & (kStages - 1);
         if (lane == 0) {
-            const bool ok = (unsigned)id < (unsigned)p.num_pages;
-            sm.bad[warp][st] = !ok;
-            if (ok) {
-                const uint8_t *src = p.layer + (uint64_t)(uint32_t)id * page_bytes +
-                                     (uint32_t)(fu.h * bpp + f_in) * B::kBytes;
+            uint64_t *bar = &sm.full[warp][st];
+            sm.there[warp][st] = there;
+            if (there) {
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                bar_expect(&sm.full[warp][st], B::kBytes);
-                bulk_copy(sm.ring[warp][st], src, B::kBytes, &sm.full[warp][st]);
+                bar_expect(bar, __popc(there) * B::kBytes);
+                if (HB == 2 && there == 3 && src[HB - 1] == src[0] + B::kBytes) {
+                    bulk_copy(sm.ring[warp][st], src[0], HB * B::kBytes, bar);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < HB; ++i)
+                        if (there >> i & 1)
+                            bulk_copy(sm.ring[warp][st] + i * B::kBytes, src[i], B::kBytes, bar);
+                }
             } else {
-                if (fu.q.kv > 0)
-                    int4_set_status(p.status, CG_ERR_CORRUPT);
-                bar_arrive(&sm.full[warp][st]);
+                bar_arrive(bar);
             }
         }
         ++issued;
-        ++f_b;
-        if (++f_in == bpp) {
-            f_in = 0;
-            ++f_page;
-        }
     };
     __syncwarp();
     for (int i = 0; i < kStages; ++i)
@@ -508,7 +530,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 
         int b, e;
         warp_range(u, warp, &b, &e);
-        for (; b < e; ++b) {
+        for (; b < e; b += HB) {
             const int st = used & (kStages - 1);
             if (alive &&
                 !__all_sync(0xFFFFFFFFu, bar_wait(&sm.full[warp][st], (used / kStages) & 1))) {
@@ -516,95 +538,116 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 int4_set_status(p.status, CG_ERR_TIMEOUT);
             }
             ++used;
-            if (alive && !sm.bad[warp][st]) {
-                const uint8_t *blob = sm.ring[warp][st];
-                const int tok = 16 * (b < u.span.sink ? b : b + u.span.skip);
-                // ---- scores of tokens g and g + 8 with rows 2t and 2t + 1
-                uint32_t k0[NW], k1[NW], kp0[NG], kp1[NG];
-                load_words(k0, blob + B::kKCodes + g * (D / 2) + t * (D / 8));
-                load_words(k1, blob + B::kKCodes + (g + 8) * (D / 2) + t * (D / 8));
-                load_words(kp0, blob + B::kKParams + g * 4 * NG);
-                load_words(kp1, blob + B::kKParams + (g + 8) * 4 * NG);
-                float z[NT][4] = {}, zl[NT][4];
+            const uint32_t there = sm.there[warp][st];
+            if (alive && there) {
+                const uint8_t *ring = sm.ring[warp][st];
+                float z[HB][NT][4];
+                uint32_t va[HB][2];
+                int tok[HB];
+                bool whole = true;
 #pragma unroll
-                for (int gi = 0; gi < NG; ++gi) {
-                    float acc[NT][4];
+                for (int hb = 0; hb < HB; ++hb) {
+                    const uint8_t *blob = ring + hb * B::kBytes;
+                    // ---- scores of tokens g and g + 8 with rows 2t and 2t + 1
+                    uint32_t k0[NW], k1[NW], kp0[NG], kp1[NG];
+                    load_words(k0, blob + B::kKCodes + g * (D / 2) + t * (D / 8));
+                    load_words(k1, blob + B::kKCodes + (g + 8) * (D / 2) + t * (D / 8));
+                    load_words(kp0, blob + B::kKParams + g * 4 * NG);
+                    load_words(kp1, blob + B::kKParams + (g + 8) * 4 * NG);
+                    float zl[NT][4];
 #pragma unroll
-                    for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+                    for (int gi = 0; gi < NG; ++gi) {
+                        float acc[NT][4];
 #pragma unroll
-                        for (int i = 0; i < 4; i += 2) {
-                            const uint32_t a0 = codes_of(k0[w], i), a1 = codes_of(k1[w], i);
-                            const uint32_t a2 = codes_of(k0[w], i + 1), a3 = codes_of(k1[w], i + 1);
+                        for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                if (w == gi * WPG && i == 0)
-                                    mma16816_first(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
-                                else
-                                    mma16816(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
-                        }
-                    const float s0 = par_s(kp0[gi]), s1 = par_s(kp1[gi]);
+                            for (int i = 0; i < 4; i += 2) {
+                                const uint32_t a0 = codes_of(k0[w], i), a1 = codes_of(k1[w], i);
+                                const uint32_t a2 = codes_of(k0[w], i + 1), a3 = codes_of(k1[w], i + 1);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                                for (int nt = 0; nt < NT; ++nt)
+                                    if (w == gi * WPG && i == 0)
+                                        mma16816_first(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
+                                    else
+                                        mma16816(acc[nt], a0, a1, a2, a3, qf[nt][w][i], qf[nt][w][i + 1]);
+                            }
+                        const float s0 = par_s(kp0[gi]), s1 = par_s(kp1[gi]);
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            z[nt][j] = gi ? fmaf(s0, acc[nt][j], z[nt][j]) : s0 * acc[nt][j];
-                            z[nt][2 + j] = gi ? fmaf(s1, acc[nt][2 + j], z[nt][2 + j]) : s1 * acc[nt][2 + j];
-                        }
-                }
-                {
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                z[hb][nt][j] = gi ? fmaf(s0, acc[nt][j], z[hb][nt][j]) : s0 * acc[nt][j];
+                                z[hb][nt][2 + j] =
+                                    gi ? fmaf(s1, acc[nt][2 + j], z[hb][nt][2 + j]) : s1 * acc[nt][2 + j];
+                            }
+                    }
                     const uint32_t a0 = *reinterpret_cast<const uint32_t *>(blob + B::kKParams +
                                                                             (g * NG + t % NG) * 4);
                     const uint32_t a1 = *reinterpret_cast<const uint32_t *>(blob + B::kKParams +
                                                                             ((g + 8) * NG + t % NG) * 4);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
                         mma16816_first(zl[nt], a0, a1, a0, a1, qs[nt][0], qs[nt][1]);
-                }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        z[nt][j] = fmaf(z[nt][j], rho[nt][j & 1], zl[nt][j]);
-                // rows of the V parameters: s or lo of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
-                uint32_t va[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint8_t *at = blob + par_at + i * 8 * 4 * NG;
-                    va[i] = __byte_perm(*reinterpret_cast<const uint32_t *>(at),
-                                        *reinterpret_cast<const uint32_t *>(at + 4 * NG), par_sel) &
-                            par_keep;
-                }
-                const bool whole = tok + 15 <= x_lo && (x_hi - tok < window || tok + 15 < p.a.sinks);
-                if (!whole) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int at_tok = tok + g + (j >= 2 ? 8 : 0), xr = x[nt][j & 1];
-                            const bool sees = at_tok <= xr && (xr - at_tok < window || at_tok < p.a.sinks);
-                            z[nt][j] = sees ? z[nt][j] : -INFINITY;
-                        }
-                    // parameters behind the last token may be anything
+                        for (int j = 0; j < 4; ++j)
+                            z[hb][nt][j] = fmaf(z[hb][nt][j], rho[nt][j & 1], zl[nt][j]);
+                    }
+                    // rows of the V parameters: s or lo of tokens 2t, 2t + 1 and 2t + 8, 2t + 9
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int first = tok + 2 * t + 8 * i;
-                        va[i] &= first + 1 < u.q.kv ? 0xFFFFFFFFu : first < u.q.kv ? 0xFFFFu : 0u;
+                        const uint8_t *at = blob + par_at + i * 8 * 4 * NG;
+                        va[hb][i] = __byte_perm(*reinterpret_cast<const uint32_t *>(at),
+                                                *reinterpret_cast<const uint32_t *>(at + 4 * NG), par_sel) &
+                                    par_keep;
+                    }
+                    // a blob that was not copied lies behind every row
+                    const int vb = b + hb;
+                    tok[hb] = there >> hb & 1 ? 16 * (vb < u.span.sink ? vb : vb + u.span.skip) : 0x7FFFFFC0;
+                    whole &= tok[hb] + 15 <= x_lo && (x_hi - tok[hb] < window || tok[hb] + 15 < p.a.sinks);
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int hb = 0; hb < HB; ++hb) {
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int at_tok = tok[hb] + g + (j >= 2 ? 8 : 0), xr = x[nt][j & 1];
+                                const bool sees =
+                                    at_tok <= xr && (xr - at_tok < window || at_tok < p.a.sinks);
+                                z[hb][nt][j] = sees ? z[hb][nt][j] : -INFINITY;
+                            }
+                        // parameters behind the last token may be anything
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int first = tok[hb] + 2 * t + 8 * i;
+                            va[hb][i] &= first + 1 < u.q.kv ? 0xFFFFFFFFu : first < u.q.kv ? 0xFFFFu : 0u;
+                        }
                     }
                 }
-                // ---- running maximum: raised only when a score exceeds it by 2^8, so
-                // that probabilities stay below 2^8 and rescaling is rare
-                float over = z[0][0] - m[0][0];
+                // ---- the running maximum is raised only when a score exceeds it by 2^8: p stays
+                // below 2^(ve + 8) and rescaling is rare. Sums of p s and p lo have to stay finite
+                // too: s and |lo| below 2^(101 - ve), and 2^16 tokens of a warp reach 2^125.
+                float over = z[0][0][0] - m[0][0];
+                uint32_t va_top = 0;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int hb = 0; hb < HB; ++hb) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        over = fmaxf(over, z[nt][j] - m[nt][j & 1]);
-                if (__any_sync(0xFFFFFFFFu, over > limit)) {
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            over = fmaxf(over, z[hb][nt][j] - m[nt][j & 1]);
+                    va_top = __vmaxu2(va_top, __vmaxu2(va[hb][0] & 0x7FFF7FFFu, va[hb][1] & 0x7FFF7FFFu));
+                }
+                const bool raise = over > limit, large = (va_top + par_bias) & 0x80008000u;
+                if (__any_sync(0xFFFFFFFFu, raise || large)) {
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
-                            float mx = fmaxf(z[nt][j], z[nt][2 + j]);
+                            float mx = fmaxf(z[0][nt][j], z[0][nt][2 + j]);
+                            if (HB == 2)
+                                mx = fmaxf(mx, fmaxf(z[HB - 1][nt][j], z[HB - 1][nt][2 + j]));
 #pragma unroll
                             for (int d = 4; d < 32; d <<= 1)
                                 mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
@@ -619,69 +662,70 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                             aux[nt][j] *= f;
                             aux[nt][2 + j] *= f;
                         }
-                }
-                // sums of p s and p lo have to stay finite: p is at most 2^(ve + 8), s and |lo|
-                // below 2^(101 - ve), and 2^16 tokens of a warp reach 2^125
-                const uint32_t va_top = __vmaxu2(va[0] & 0x7FFF7FFFu, va[1] & 0x7FFF7FFFu);
-                if (__any_sync(0xFFFFFFFFu, (va_top + par_bias) & 0x80008000u)) {
-                    uint32_t top = max(va_top & 0xFFFFu, va_top >> 16);
+                    if (__any_sync(0xFFFFFFFFu, large)) {
+                        uint32_t top = max(va_top & 0xFFFFu, va_top >> 16);
 #pragma unroll
-                    for (int d = 1; d < 32; d <<= 1)
-                        top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                    const int e = 100 - ((int)(top >> 7) - 127);   // top < 2^(101 - e)
-                    const float f = pow2(e - ve);
+                        for (int d = 1; d < 32; d <<= 1)
+                            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+                        const int e = 100 - ((int)(top >> 7) - 127);   // top < 2^(101 - e)
+                        const float f = pow2(e - ve);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                                for (int c = 0; c < NW * 2; ++c)
+                                    o[c][nt][j] *= f;
+                                aux[nt][j] *= f;
+                            }
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                m[nt][j] += (float)(ve - e);
+                        }
+                        ve = e;
+                        limit = 8.0f + (float)e;
+                        par_bias = 0x80008000u - (uint32_t)min((101 - e + 127) << 7, 0x7F80) * 0x10001u;
+                    }
+                }
+#pragma unroll
+                for (int hb = 0; hb < HB; ++hb) {
+                    const uint8_t *blob = ring + hb * B::kBytes;
+                    uint32_t pf[NT][2];  // p as the other factor: row g, tokens 2t, 2t + 1 (+ 8)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = 0; j < 4; ++j)
+                            z[hb][nt][j] = exp2_fast(z[hb][nt][j] - m[nt][j & 1]);
+                        pf[nt][0] = transpose8x8(pack_bf16(z[hb][nt][0], z[hb][nt][1]));
+                        pf[nt][1] = transpose8x8(pack_bf16(z[hb][nt][2], z[hb][nt][3]));
+                        mma16816(aux[nt], va[hb][0], ones, va[hb][1], ones, pf[nt][0], pf[nt][1]);
+                    }
+                    // ---- values
+                    uint32_t v0[NW], v1[NW];
+                    load_words(v0, blob + B::kVCodes + t * D + g * (D / 8));
+                    load_words(v1, blob + B::kVCodes + (t + 4) * D + g * (D / 8));
 #pragma unroll
-                            for (int c = 0; c < NW * 2; ++c)
-                                o[c][nt][j] *= f;
-                            aux[nt][j] *= f;
+                    for (int gi = 0; gi < NG; ++gi) {
+                        const uint32_t s0 = __shfl_sync(0xFFFFFFFFu, va[hb][0], 4 * gi + t);
+                        const uint32_t s1 = __shfl_sync(0xFFFFFFFFu, va[hb][1], 4 * gi + t);
+                        uint32_t ps[NT][2];
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            ps[nt][0] = mul_bf16x2(pf[nt][0], s0);
+                            ps[nt][1] = mul_bf16x2(pf[nt][1], s1);
+                            mma16816(aux[nt], 0, eight[gi], 0, eight[gi], ps[nt][0], ps[nt][1]);
                         }
 #pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                            m[nt][j] += (float)(ve - e);
+                        for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+#pragma unroll
+                            for (int i = 0; i < 4; i += 2) {
+                                const uint32_t a0 = codes_of(v0[w], i), a1 = codes_of(v0[w], i + 1);
+                                const uint32_t a2 = codes_of(v1[w], i), a3 = codes_of(v1[w], i + 1);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma16816(o[w * 2 + i / 2][nt], a0, a1, a2, a3, ps[nt][0], ps[nt][1]);
+                            }
                     }
-                    ve = e;
-                    limit = 8.0f + (float)e;
-                    par_bias = 0x80008000u - (uint32_t)min((101 - e + 127) << 7, 0x7F80) * 0x10001u;
-                }
-                uint32_t pf[NT][2];  // p as the other factor: row g, tokens 2t, 2t + 1 (+ 8)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        z[nt][j] = exp2_fast(z[nt][j] - m[nt][j & 1]);
-                    pf[nt][0] = transpose8x8(pack_bf16(z[nt][0], z[nt][1]));
-                    pf[nt][1] = transpose8x8(pack_bf16(z[nt][2], z[nt][3]));
-                    mma16816(aux[nt], va[0], ones, va[1], ones, pf[nt][0], pf[nt][1]);
-                }
-                // ---- values
-                uint32_t v0[NW], v1[NW];
-                load_words(v0, blob + B::kVCodes + t * D + g * (D / 8));
-                load_words(v1, blob + B::kVCodes + (t + 4) * D + g * (D / 8));
-#pragma unroll
-                for (int gi = 0; gi < NG; ++gi) {
-                    const uint32_t s0 = __shfl_sync(0xFFFFFFFFu, va[0], 4 * gi + t);
-                    const uint32_t s1 = __shfl_sync(0xFFFFFFFFu, va[1], 4 * gi + t);
-                    uint32_t ps[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        ps[nt][0] = mul_bf16x2(pf[nt][0], s0);
-                        ps[nt][1] = mul_bf16x2(pf[nt][1], s1);
-                        mma16816(aux[nt], 0, eight[gi], 0, eight[gi], ps[nt][0], ps[nt][1]);
-                    }
-#pragma unroll
-                    for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
-#pragma unroll
-                        for (int i = 0; i < 4; i += 2) {
-                            const uint32_t a0 = codes_of(v0[w], i), a1 = codes_of(v0[w], i + 1);
-                            const uint32_t a2 = codes_of(v1[w], i), a3 = codes_of(v1[w], i + 1);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                mma16816(o[w * 2 + i / 2][nt], a0, a1, a2, a3, ps[nt][0], ps[nt][1]);
-                        }
                 }
             }
             __syncwarp();   // every lane has read the stage
@@ -815,6 +859,7 @@ __global__ void __launch_bounds__(kThreads) k_attention_join(AttnArgs p, int pie
     const int last = (int)((end + chunk - 1) / chunk) - 1;   // the block that holds its end
     const int row_base = u.rt * RU;
     const int rows_here = (row_base + RU < u.q.rows ? row_base + RU : u.q.rows) - row_base;
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // for the main kernel's parts
     // weights of the parts: 2^(m - max m), and the sums that they give
     extern __shared__ float weight[];   // [RU][parts]
     __shared__ float inv[RU];
@@ -882,8 +927,23 @@ cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
     if (blocks > kFewMaxBlocks)
         blocks = kFewMaxBlocks;
     k_attention_few<B, NT><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
-    k_attention_join<B::kD, 8 * NT><<<blocks, kThreads, 8 * NT * blocks * sizeof(float), s>>>(p, blocks, parts);
-    return cudaGetLastError();
+    err = cudaGetLastError();
+    if (err != cudaSuccess)
+        return err;
+    // launched while the main kernel still runs: its own schedule is worked out
+    // meanwhile, and it waits for the main kernel before it reads the parts
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = 8 * NT * blocks * sizeof(float);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_attention_join<B::kD, 8 * NT>, p, blocks,
+                              static_cast<const float *>(parts));
 }
 
 }  // namespace

@@ -312,7 +312,6 @@ struct FewShared {
     float merge[kWarps][RU][B::kD / NT];   // one of NT parts of the channels
     float m[kWarps][RU], l[kWarps][RU];
     uint64_t full[kWarps][kStages];
-    uint32_t there[kWarps][kStages];       // which blobs of the step were copied
 };
 
 template <typename B, int NT>
@@ -330,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (lane == 0)
         for (int i = 0; i < kStages; ++i)
-            bar_init(&sm.full[warp][i], 1);
+            bar_init(&sm.full[warp][i], HB);   // one arrival per blob of the step
     bar_init_fence();
     int64_t total, chunk;
     const Place at = schedule<RU>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
@@ -340,79 +339,57 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
 
     const int bpp = p.page_tokens / 16;
-    // ---- the warp's feeder: copies a few blobs ahead of the warp, through the same units.
-    // Each lane holds one page id of the 32 from f_p0 on.
-    const uint32_t page_bytes = (uint32_t)p.heads * bpp * B::kBytes;
+    // ---- the warp's feeder: copies some steps ahead of the warp, through the same units.
+    // Up to 32 blobs of the stretch are looked up at once, one by each lane, which then
+    // issues its own blob's copy.
     Unit fu;
     unit_at<RU>(p, at, count, &fu);
     int64_t f_pos = fu.b1 - fu.b0;   // blobs of the piece up to the end of the feeder's unit
-    int f_b, f_e, f_in = 0, f_page = 0, f_p0 = -64, f_id = -1;
+    int f_b, f_e;                    // blobs of the stretch not looked up yet
     warp_range(fu, warp, &f_b, &f_e);
-    bool f_jump = true;              // the page has to be worked out again
+    int f_i = 0, f_n = 0;            // blobs issued and looked up of the current 32
+    uint32_t f_off = 0, f_ok = 0;    // the lane's blob (in 128-byte units of the layer); valid lanes
     uint32_t issued = 0;
+    uint32_t ahead = 0;              // which blobs of the steps in flight are there, HB bits a step
     auto feed = [&]() {
-        // the next step's blobs into the ring, if the piece has more for this warp
-        if (f_b >= f_e) {
-            do {
+        ahead >>= HB;
+        if (f_i >= f_n) {
+            while (f_b >= f_e) {
                 if (f_pos >= count)
                     return;
                 unit_next<RU>(p, count - f_pos, &fu);
                 f_pos += fu.b1 - fu.b0;
                 warp_range(fu, warp, &f_b, &f_e);
-            } while (f_b >= f_e);
-            f_jump = true;
-            f_p0 = -64;
-        }
-        const uint8_t *src[HB];
-        uint32_t there = 0;
-#pragma unroll
-        for (int i = 0; i < HB; ++i) {
-            src[i] = nullptr;
-            if (f_b >= f_e)
-                break;
-            if (f_jump || f_b == fu.span.sink) {
-                const int ab = f_b < fu.span.sink ? f_b : f_b + fu.span.skip;
-                f_page = ab / bpp;
-                f_in = ab - f_page * bpp;
-                f_jump = false;
             }
-            if ((unsigned)(f_page - f_p0) >= 32u) {
-                f_p0 = f_page;
-                f_id = f_page + lane < p.a.table_width && fu.q.kv > 0
-                           ? p.a.block_table[fu.r * p.a.table_stride + f_page + lane]
-                           : -1;
+            f_i = 0;
+            f_n = f_e - f_b < 32 ? f_e - f_b : 32;
+            int id = -1;
+            if (lane < f_n && fu.q.kv > 0) {
+                const int vb = f_b + lane, ab = vb < fu.span.sink ? vb : vb + fu.span.skip;
+                const int page = ab / bpp;
+                id = p.a.block_table[fu.r * p.a.table_stride + page];
+                if ((unsigned)id >= (unsigned)p.num_pages)
+                    int4_set_status(p.status, CG_ERR_CORRUPT);
+                // at most num_pages * heads * page_tokens / 16 blobs: below 2^32 such units (cg_int4.h)
+                f_off = (((uint32_t)id * p.heads + fu.h) * bpp + (ab - page * bpp)) * (B::kBytes / 128);
             }
-            const int id = __shfl_sync(0xFFFFFFFFu, f_id, f_page - f_p0);
-            if ((unsigned)id < (unsigned)p.num_pages)
-                there |= 1u << i;
-            else if (fu.q.kv > 0 && lane == 0)
-                int4_set_status(p.status, CG_ERR_CORRUPT);
-            src[i] = p.layer + (uint64_t)(uint32_t)id * page_bytes + (uint32_t)(fu.h * bpp + f_in) * B::kBytes;
-            ++f_b;
-            if (++f_in == bpp) {
-                f_in = 0;
-                ++f_page;
-            }
+            f_ok = __ballot_sync(0xFFFFFFFFu, (unsigned)id < (unsigned)p.num_pages);
+            f_b += f_n;
         }
         const int st = issued & (kStages - 1);
-        if (lane == 0) {
+        if ((unsigned)(lane - f_i) < (unsigned)HB) {
             uint64_t *bar = &sm.full[warp][st];
-            sm.there[warp][st] = there;
-            if (there) {
+            if (f_ok >> lane & 1) {
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                bar_expect(bar, __popc(there) * B::kBytes);
-                if (HB == 2 && there == 3 && src[HB - 1] == src[0] + B::kBytes) {
-                    bulk_copy(sm.ring[warp][st], src[0], HB * B::kBytes, bar);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < HB; ++i)
-                        if (there >> i & 1)
-                            bulk_copy(sm.ring[warp][st] + i * B::kBytes, src[i], B::kBytes, bar);
-                }
+                bar_expect(bar, B::kBytes);
+                bulk_copy(sm.ring[warp][st] + (lane - f_i) * B::kBytes, p.layer + (uint64_t)f_off * 128,
+                          B::kBytes, bar);
             } else {
                 bar_arrive(bar);
             }
         }
+        ahead |= (f_ok >> f_i & ((1u << HB) - 1)) << (HB * (kStages - 1));
+        f_i += HB;
         ++issued;
     };
     __syncwarp();
@@ -538,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 int4_set_status(p.status, CG_ERR_TIMEOUT);
             }
             ++used;
-            const uint32_t there = sm.there[warp][st];
+            const uint32_t there = ahead & ((1u << HB) - 1);
             if (alive && there) {
                 const uint8_t *ring = sm.ring[warp][st];
                 float z[HB][NT][4];
@@ -597,8 +574,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                     for (int i = 0; i < 2; ++i) {
                         const uint8_t *at = blob + par_at + i * 8 * 4 * NG;
                         va[hb][i] = __byte_perm(*reinterpret_cast<const uint32_t *>(at),
-                                                *reinterpret_cast<const uint32_t *>(at + 4 * NG), par_sel) &
-                                    par_keep;
+                                                *reinterpret_cast<const uint32_t *>(at + 4 * NG), par_sel);
+                        if (NG < 4)
+                            va[hb][i] &= par_keep;
                     }
                     // a blob that was not copied lies behind every row
                     const int vb = b + hb;

@@ -61,6 +61,10 @@ inline cg_status int4_check_shape(const cg_int4_cache *c)
         (int64_t)c->num_layers * c->num_pages >= limit ||
         (int64_t)c->num_layers * c->num_pages * c->num_heads >= limit)
         return CG_ERR_UNSUPPORTED;
+    // one layer in 128-byte units (every blob is whole ones) counts in 32 bits: below 512 GiB
+    if ((int64_t)c->num_pages * c->num_heads >= 2 * limit / (c->page_tokens / 16) /
+                                                   (int4_blob_bytes(c->head_size, c->group) / 128))
+        return CG_ERR_UNSUPPORTED;
     return CG_OK;
 }
 

@@ -17,7 +17,7 @@ LIB = os.path.join(OUT_DIR, "libcachegen.so")
 
 SOURCES = ["cachegen_kernels.cu", "cachegen_api.cu", "cachegen_noalloc.cu", "cachegen_int8.cu",
            "cachegen_int4.cu", "cachegen_pages.cu", "cachegen_attention.cu",
-           "cachegen_attn_few.cu"]
+           "cachegen_attn_few.cu", "cachegen_attn_many.cu"]
 HEADERS = [os.path.join(CSRC, "cg_internal.h"), os.path.join(CSRC, "cg_int4.h"),
            os.path.join(CSRC, "cg_attention.h"),
            os.path.join(INCLUDE, "cachegen.h")]

@@ -1,0 +1,693 @@
+// Attention over the 4-bit cache for many query rows (prompts, chunks of
+// them): tensor-core bound, 4 D flops per query head and visible pair.
+//
+// One block per 256 rows of a (request, KV head), rows being the head's query
+// heads of one token after another: the group shares its K and V. Per tile of
+// 128 tokens, S = Q K^T and O += P V by tcgen05.mma (128 x 128 x 16, bf16 in, fp32
+// accumulators in tensor memory), two row tiles of 128 in turn, so that the
+// softmax of one runs under the products of the other:
+//   warps 0-3, 4-7   softmax of row tile 0, 1: a thread owns a row. It reads S
+//                    from tensor memory, keeps the running maximum and sum
+//                    and writes P as bf16 over S, where the next product reads
+//                    it. O is rescaled in place, only when a maximum rises by
+//                    more than 2^8.
+//   warps 8-10       K: 4-bit codes to bf16 rows in shared memory
+//   warps 11-14      V: the same, transposed (channels as rows)
+//   warp 15          one thread issues all products
+// Codes are expanded once per 256 rows, beside 2 x 2 x 128 x 128 x 128 products.
+// K rows keep the channel order in which a word's codes come apart (0 4 1 5 2 6
+// 3 7 of each eight); Q is laid out alike. V's words hold a pair of tokens each, as
+// the transposed rows need them.
+//
+// Roundings: k^ and v^ = lo + s n to bf16 (one rounding, 2^-8 relative), p to
+// bf16; scores, sums and O in fp32.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cg_attention.h"
+
+namespace {
+
+constexpr int kSoftWarps = 8, kKWarps = 3, kVWarps = 4;   // 16 warps in all: 128 registers
+constexpr int kWarps = kSoftWarps + kKWarps + kVWarps + 1;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRows = 256;       // of a block
+constexpr int kTile = 128;       // tokens
+constexpr int kBlobs = kTile / 16;
+constexpr float kNone = -3.0e38f;
+
+// ------------------------------------------------------------ instructions
+
+// Descriptor of a shared-memory operand: K-major rows of 128 bytes, 128-byte
+// swizzle, 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t at)
+{
+    return (uint64_t)((at >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)64 << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// bf16 x bf16 -> fp32, both operands K-major, M = 128.
+__host__ __device__ constexpr uint32_t mma_desc(int n)
+{
+    return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+
+// The barrier is arrived on once all products issued so far are done.
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_fence_before()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_fence_after()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// 32 columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld32(float (&v)[32], uint32_t at)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"f"(v[0]),
+        "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
+        "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]),
+        "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::
+            "r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(at)
+        : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// lo + s n for the codes i and i + 4 of a word, rounded once: n comes exact out
+// of the mantissa of 128 + n.
+__device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32_t lo)
+{
+    const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t n, y;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(x), "r"(0x43004300u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(n), "r"(s), "r"(lo));
+    return y;
+}
+
+template <int N>
+__device__ __forceinline__ void load_or_zero(uint32_t (&w)[N], const uint8_t *p, bool there)
+{
+    if constexpr (N == 1) {
+        w[0] = there ? *reinterpret_cast<const uint32_t *>(p) : 0;
+    } else if constexpr (N == 2) {
+        const uint2 v = there ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0, 0);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        const uint4 v = there ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+}
+
+// ------------------------------------------------------------------ schedule
+
+template <int D>
+struct ManyShared {
+    uint8_t q[2][kTile * D * 2];
+    uint8_t k[2][kTile * D * 2];
+    uint8_t v[2][kTile * D * 2];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
+    int64_t warp_sum[kWarps];
+    uint32_t tmem;
+    int32_t found_r;
+    int64_t found_off;
+    uint32_t gave_up;    // a wait ran out: everyone leaves
+    uint32_t bad_page;   // a page id of the unit is outside the cache
+};
+
+// Waits that end: false once this wait or another one of the block ran out.
+__device__ __forceinline__ bool wait_or_leave(uint64_t *bar, uint32_t parity, uint32_t *gave_up,
+                                              void *status)
+{
+    const uint32_t at = smem_addr(bar);
+    for (uint32_t i = 0; i < kBarWaitLimit; ++i) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(at), "r"(parity)
+            : "memory");
+        if (done)
+            return true;
+        if (*reinterpret_cast<volatile uint32_t *>(gave_up))
+            return false;
+    }
+    *reinterpret_cast<volatile uint32_t *>(gave_up) = 1;
+    int4_set_status(status, CG_ERR_TIMEOUT);
+    return false;
+}
+
+__device__ __forceinline__ int64_t units_of(const AttnArgs &p, int r, AttnRequest *q)
+{
+    uint32_t error;
+    if (!attn_request(p, r, q, &error) || q->rows <= p.few_rows)
+        return 0;
+    return (int64_t)((q->rows + kRows - 1) / kRows) * p.heads;
+}
+
+// Block-wide: the request that unit `want` belongs to, in sm.found_r
+// (requests: past the last unit), and the unit's number within it.
+template <typename S>
+__device__ void find_unit(const AttnArgs &p, S &sm, int64_t want)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0)
+        sm.found_r = p.a.requests;
+    int64_t carry = 0;
+    for (int r0 = 0; r0 < p.a.requests; r0 += kThreads) {
+        const int r = r0 + tid;
+        AttnRequest q;
+        const int64_t w = r < p.a.requests ? units_of(p, r, &q) : 0;
+        int64_t inc = w;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+            if (lane >= d)
+                inc += o;
+        }
+        if (lane == 31)
+            sm.warp_sum[warp] = inc;
+        __syncthreads();
+        int64_t before = carry;
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp)
+                before += sm.warp_sum[i];
+            carry += sm.warp_sum[i];
+        }
+        const int64_t start = before + inc - w;
+        if (want >= start && want < start + w) {
+            sm.found_r = r;
+            sm.found_off = want - start;
+        }
+        __syncthreads();
+    }
+}
+
+// Visible blob vb of a unit is blob vb or, behind the first tokens, vb + skip.
+struct Stretch {
+    int32_t nb, sink, skip;
+    __device__ __forceinline__ int32_t blob(int32_t vb) const { return vb < sink ? vb : vb + skip; }
+};
+
+// -------------------------------------------------------------------- kernel
+
+template <typename B>
+__global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
+{
+    constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
+    constexpr int kQSub = kTile * 128;           // bytes of a 64-channel part of a Q or K tile
+    constexpr int kVSub = D * 128;               // bytes of a 64-token part of a V tile
+    constexpr uint32_t kO = 256;                 // tensor memory: S0, S1 at 0, 128; O0, O1 at 256, 384
+    using S = ManyShared<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    S &sm = *reinterpret_cast<S *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sm.k_full[i], 32 * kKWarps);
+            bar_init(&sm.v_full[i], 32 * kVWarps);
+            bar_init(&sm.p_full[i], 128);
+            bar_init(&sm.k_empty[i], 1);
+            bar_init(&sm.v_empty[i], 1);
+            bar_init(&sm.s_full[i], 1);
+        }
+        bar_init_fence();
+        sm.gave_up = 0;
+    }
+    if (warp == kWarps - 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
+                         smem_addr(&sm.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tmem_fence_before();
+    }
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sm.tmem;
+    const int bpp = p.page_tokens / 16;
+    const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
+    // exponents in powers of two; a negative scale goes into Q, so that the largest score is
+    // the largest product
+    const float sc = fmaxf(fabsf(p.scale2), 1.2e-38f);
+    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+
+    uint32_t tiles_done = 0;             // K and V tiles of earlier units
+    uint32_t s_done[2] = {0, 0};         // uses of s_full, p_full is used one less per unit
+    uint32_t p_done[2] = {0, 0};
+    bool alive = true;
+    for (int64_t unit = blockIdx.x;; unit += gridDim.x) {
+        find_unit(p, sm, unit);
+        if (sm.found_r >= p.a.requests)
+            break;
+        const int r = sm.found_r;
+        AttnRequest q;
+        uint32_t error;
+        attn_request(p, r, &q, &error);
+        const int row_tiles = (q.rows + kRows - 1) / kRows;
+        // the last rows, which see most, first
+        const int rt = row_tiles - 1 - (int)(sm.found_off / p.heads);
+        const int h = (int)(sm.found_off % p.heads);
+        const int row0 = rt * kRows, rows = min(kRows, q.rows - row0);
+        const int tiles_q = rows > 128 ? 2 : 1;
+        // positions of the unit's first and last row, and the blobs that they see
+        const int x0 = q.kv - q.nq;
+        const int x_first = x0 + row0 / p.ratio, x_last = x0 + (row0 + rows - 1) / p.ratio;
+        Stretch st;
+        {
+            const int end = x_last < 0 ? 0 : x_last / 16 + 1;
+            st = {end, 0, 0};
+            const int64_t low = (int64_t)x_first + 1 - window;
+            if (p.a.window > 0 && low > 0) {
+                const int first = (int)(low / 16);
+                const int64_t sb = ((int64_t)p.a.sinks + 15) / 16;
+                st.sink = sb < first ? (int)sb : first;
+                st.skip = first - st.sink;
+                st.nb = end - st.skip;
+            }
+        }
+        const int n = (st.nb + kBlobs - 1) / kBlobs;   // tiles (0: nothing is seen)
+        const int32_t *table = p.a.block_table + r * p.a.table_stride;
+
+        // ---- Q into shared memory, and a look at the page ids
+        if (tid == 0)
+            sm.bad_page = 0;
+        __syncthreads();
+        for (int i = tid; i < tiles_q * 128 * (D / 8); i += kThreads) {
+            const int row = i / (D / 8), c = i % (D / 8), rr = row0 + row;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < rows) {
+                const int qt = rr / p.ratio, qh = h * p.ratio + rr - qt * p.ratio;
+                v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) +
+                                                     (int64_t)(q.row0 + qt) * p.a.q_token_stride +
+                                                     qh * p.a.q_head_stride + 8 * c);
+            }
+            const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip,
+                                       __byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
+            const int in = row & 127;
+            *reinterpret_cast<uint4 *>(sm.q[row >> 7] + (c >> 3) * kQSub + in * 128 + (((c & 7) ^ (in & 7)) << 4)) = o;
+        }
+        for (int vb = tid; vb < st.nb; vb += kThreads) {
+            const int id = table[st.blob(vb) / bpp];
+            if ((unsigned)id >= (unsigned)p.num_pages) {
+                sm.bad_page = 1;
+                int4_set_status(p.status, CG_ERR_CORRUPT);
+            }
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();
+        const bool bad_page = sm.bad_page;
+
+        if (warp < kSoftWarps) {
+            // ================================================== softmax of a row
+            const int i = warp >> 2, row = 32 * (warp & 3) + lane, rr = row0 + 128 * i + row;
+            if (i < tiles_q) {
+                const uint32_t lane_at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+                const uint32_t s_at = lane_at + 128 * i, o_at = lane_at + kO + 128 * i;
+                const int x = rr < q.rows ? x0 + rr / p.ratio : -1;
+                const int last_row = min(row0 + 128 * i + 128, q.rows) - 1;
+                const int x_lo = x0 + (row0 + 128 * i) / p.ratio, x_hi = x0 + last_row / p.ratio;
+                float m = kNone, l = 0.0f;
+                for (int j = 0; j < n && alive; ++j) {
+                    alive = wait_or_leave(&sm.s_full[i], s_done[i] & 1, &sm.gave_up, p.status);
+                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    ++s_done[i];
+                    if (!alive)
+                        break;
+                    tmem_fence_after();
+                    const int vb0 = j * kBlobs;
+                    const int t0 = 16 * st.blob(vb0), t1 = 16 * st.blob(vb0 + kBlobs - 1) + 15;
+                    const bool whole = !bad_page && vb0 + kBlobs <= st.nb && t1 <= x_lo &&
+                                       (x_hi - t0 < window || t1 < p.a.sinks);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float s[32];
+                        tmem_ld32(s, s_at + 32 * c);
+                        tmem_wait_ld();
+                        if (!whole) {
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                const int vb = vb0 + 2 * c + b;
+                                bool there = vb < st.nb;
+                                if (there && bad_page)
+                                    there = (unsigned)table[st.blob(vb) / bpp] < (unsigned)p.num_pages;
+                                const int tok = 16 * st.blob(vb);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const int at = tok + e;
+                                    const bool sees = there && at <= x && (x - at < window || at < p.a.sinks);
+                                    s[16 * b + e] = sees ? s[16 * b + e] : -INFINITY;
+                                }
+                            }
+                            tmem_st32(s_at + 32 * c, s);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            mx = fmaxf(mx, s[e]);
+                    }
+                    if (!whole)
+                        tmem_wait_st();
+                    mx *= sc;
+                    if (__any_sync(0xFFFFFFFFu, mx > m + 8.0f)) {
+                        const float mn = fmaxf(mx, m), f = exp2_fast(m - mn);
+                        m = mn;
+                        l *= f;
+                        if (j > 0) {
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                float o[32];
+                                tmem_ld32(o, o_at + 32 * c);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    o[e] *= f;
+                                tmem_st32(o_at + 32 * c, o);
+                            }
+                        }
+                    }
+                    float sum = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        float s[32];
+                        uint32_t pk[16];
+                        tmem_ld32(s, s_at + 32 * c);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            s[e] = exp2_fast(fmaf(s[e], sc, -m));
+                            sum += s[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            pk[e] = pack_bf16(s[2 * e], s[2 * e + 1]);
+                        tmem_st16(s_at + 16 * c, pk);   // over columns already read
+                    }
+                    l += sum;
+                    tmem_wait_st();
+                    tmem_fence_before();
+                    bar_arrive(&sm.p_full[i]);
+                }
+                if (alive && n > 0) {
+                    alive = wait_or_leave(&sm.s_full[i], s_done[i] & 1, &sm.gave_up, p.status);
+                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    ++s_done[i];
+                    tmem_fence_after();
+                }
+                if (alive) {
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    const int qt = rr / p.ratio, qh = h * p.ratio + rr - qt * p.ratio;
+                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                                         (int64_t)(q.row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride;
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float o[32];
+                        if (n > 0) {
+                            tmem_ld32(o, o_at + 32 * c);
+                            tmem_wait_ld();
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = 0.0f;
+                        }
+                        if (rr < q.rows) {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8)
+                                *reinterpret_cast<uint4 *>(out + 32 * c + e) =
+                                    make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv),
+                                               pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                               pack_bf16(o[e + 4] * inv, o[e + 5] * inv),
+                                               pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+                        }
+                    }
+                }
+                tmem_fence_before();
+            }
+        } else if (warp < kSoftWarps + kKWarps) {
+            // ============================================================ K tiles
+            // A warp takes 8 tokens (half a blob) at a time: lane t + 4 k has words t of token
+            // (k & 1) * 4 + (k >> 1), so that eight lanes' 16-byte stores meet all banks
+            constexpr int kItems = (2 * kBlobs + kKWarps - 1) / kKWarps;
+            const int wi = warp - kSoftWarps, t = lane & 3, k8 = lane >> 2;
+            const int half_tok = (k8 & 1) * 4 + (k8 >> 1);
+            for (int j = 0; j < n && alive; ++j) {
+                uint32_t code[kItems][NW], par[kItems][NG];
+#pragma unroll
+                for (int u = 0; u < kItems; ++u) {
+                    const int item = wi + kKWarps * u, vb = j * kBlobs + (item >> 1);
+                    const int tok = 8 * (item & 1) + half_tok;
+                    int id = -1, ab = 0;
+                    if (item < 2 * kBlobs && vb < st.nb) {
+                        ab = st.blob(vb);
+                        id = table[ab / bpp];
+                    }
+                    const bool there = (unsigned)id < (unsigned)p.num_pages;
+                    const uint8_t *blob = p.layer + (((size_t)(there ? id : 0) * p.heads + h) * bpp + ab % bpp) *
+                                                        B::kBytes;
+                    load_or_zero(code[u], blob + B::kKCodes + tok * (D / 2) + t * (D / 8), there);
+                    load_or_zero(par[u], blob + B::kKParams + tok * 4 * NG, there);
+                }
+                const uint32_t use = tiles_done + j, sl = use & 1;
+                alive = wait_or_leave(&sm.k_empty[sl], (use >> 1 & 1) ^ 1, &sm.gave_up, p.status);
+                if (!alive)
+                    break;
+#pragma unroll
+                for (int u = 0; u < kItems; ++u) {
+                    const int item = wi + kKWarps * u, row = 8 * item + half_tok;
+                    if (item >= 2 * kBlobs)
+                        break;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        const uint32_t pw = par[u][w / WPG];
+                        const uint32_t s2 = __byte_perm(pw, pw, 0x1010), lo2 = __byte_perm(pw, pw, 0x3232);
+                        const uint4 o = make_uint4(expand(code[u][w], 0, s2, lo2), expand(code[u][w], 1, s2, lo2),
+                                                   expand(code[u][w], 2, s2, lo2), expand(code[u][w], 3, s2, lo2));
+                        const int c = 4 * w + t;
+                        *reinterpret_cast<uint4 *>(sm.k[sl] + (c >> 3) * kQSub + row * 128 +
+                                                   (((c & 7) ^ (row & 7)) << 4)) = o;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(&sm.k_full[sl]);
+            }
+        } else if (warp < kSoftWarps + kKWarps + kVWarps) {
+            // ============================================================ V tiles
+            // A thread takes half a blob (8 tokens: pairs 4 hf .. 4 hf + 3) at words g: channels
+            // 32 w + 4 g + i; eight lanes with the same g store to different 16-byte columns
+            const int wi = warp - kSoftWarps - kKWarps;
+            const int pg = 8 * (wi & 1) + (lane & 7), g = 4 * (wi >> 1) + (lane >> 3), hf = pg & 1;
+            for (int j = 0; j < n && alive; ++j) {
+                uint32_t code[4][NW], par[8][NG];
+                const int vb = j * kBlobs + (pg >> 1);
+                int id = -1, ab = 0;
+                if (vb < st.nb) {
+                    ab = st.blob(vb);
+                    id = table[ab / bpp];
+                }
+                const bool there = (unsigned)id < (unsigned)p.num_pages;
+                const uint8_t *blob = p.layer + (((size_t)(there ? id : 0) * p.heads + h) * bpp + ab % bpp) * B::kBytes;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    load_or_zero(code[u], blob + B::kVCodes + (4 * hf + u) * D + g * (D / 8), there);
+                // tokens that are not there get 0, whatever the cache holds in their place
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    load_or_zero(par[u], blob + B::kVParams + (8 * hf + u) * 4 * NG,
+                                 there && 16 * ab + 8 * hf + u < q.kv);
+                const uint32_t use = tiles_done + j, sl = use & 1;
+                alive = wait_or_leave(&sm.v_empty[sl], (use >> 1 & 1) ^ 1, &sm.gave_up, p.status);
+                if (!alive)
+                    break;
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    uint32_t s2[4], lo2[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        s2[u] = __byte_perm(par[2 * u][gi], par[2 * u + 1][gi], 0x5410);
+                        lo2[u] = __byte_perm(par[2 * u][gi], par[2 * u + 1][gi], 0x7632);
+                    }
+#pragma unroll
+                    for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 o = make_uint4(expand(code[0][w], i, s2[0], lo2[0]),
+                                                       expand(code[1][w], i, s2[1], lo2[1]),
+                                                       expand(code[2][w], i, s2[2], lo2[2]),
+                                                       expand(code[3][w], i, s2[3], lo2[3]));
+                            const int row = 32 * w + 4 * g + i;
+                            *reinterpret_cast<uint4 *>(sm.v[sl] + (pg >> 3) * kVSub + row * 128 +
+                                                       (((pg & 7) ^ (row & 7)) << 4)) = o;
+                        }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(&sm.v_full[sl]);
+            }
+        } else if (lane == 0 && n > 0) {
+            // ========================================================== products
+            const uint32_t q_at = smem_addr(sm.q[0]), k_at = smem_addr(sm.k[0]), v_at = smem_addr(sm.v[0]);
+            auto scores = [&](int i, uint32_t sl) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * kQSub + (kk & 3) * 32;
+                    mma_ss(tmem + 128 * i, smem_desc(q_at + i * (kTile * D * 2) + off),
+                           smem_desc(k_at + sl * (kTile * D * 2) + off), mma_desc(kTile), kk > 0);
+                }
+                mma_commit(&sm.s_full[i]);
+            };
+            uint32_t use = tiles_done;
+            alive = wait_or_leave(&sm.k_full[use & 1], use >> 1 & 1, &sm.gave_up, p.status);
+            if (alive) {
+                tmem_fence_after();
+                for (int i = 0; i < tiles_q; ++i)
+                    scores(i, use & 1);
+                mma_commit(&sm.k_empty[use & 1]);
+            }
+            for (int j = 0; j < n && alive; ++j, ++use) {
+                const uint32_t sl = use & 1, nx = use + 1;
+                for (int i = 0; i < tiles_q && alive; ++i) {
+                    alive = wait_or_leave(&sm.p_full[i], p_done[i] & 1, &sm.gave_up, p.status);
+                    ++p_done[i];
+                    if (alive && i == 0)
+                        alive = wait_or_leave(&sm.v_full[sl], use >> 1 & 1, &sm.gave_up, p.status);
+                    if (alive && i == 0 && j + 1 < n)
+                        alive = wait_or_leave(&sm.k_full[nx & 1], nx >> 1 & 1, &sm.gave_up, p.status);
+                    if (!alive)
+                        break;
+                    tmem_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_ts(tmem + kO + 128 * i, tmem + 128 * i + 8 * kk,
+                               smem_desc(v_at + sl * (kTile * D * 2) + (kk >> 2) * kVSub + (kk & 3) * 32),
+                               mma_desc(D), j > 0 || kk > 0);
+                    if (i + 1 == tiles_q)
+                        mma_commit(&sm.v_empty[sl]);
+                    if (j + 1 < n)
+                        scores(i, nx & 1);
+                    else
+                        mma_commit(&sm.s_full[i]);   // O is complete
+                }
+                if (alive && j + 1 < n)
+                    mma_commit(&sm.k_empty[nx & 1]);
+            }
+        }
+        tiles_done += n;
+        __syncwarp();
+        __syncthreads();
+        alive = sm.gave_up == 0;
+        if (!alive)
+            break;
+    }
+    // products still in flight (after a wait that ran out) end before the memory goes
+    if (warp == kWarps - 1) {
+        if (!alive && lane == 0) {
+            bar_init(&sm.k_full[0], 1);
+            bar_init_fence();
+            mma_commit(&sm.k_full[0]);
+            bar_wait(&sm.k_full[0], 0);
+        }
+        __syncwarp();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    if (warp == kWarps - 1) {
+        tmem_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <typename B>
+cudaError_t launch(const AttnArgs &p, cudaStream_t s)
+{
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess)
+        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int smem = (int)sizeof(ManyShared<B::kD>);
+    if (err == cudaSuccess)
+        err = cudaFuncSetAttribute(k_attention_many<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess)
+        return err;
+    // units that there can be: full row tiles, and one short one per request with more than
+    // few_rows rows
+    const int64_t rows = (int64_t)p.a.tokens * p.ratio;
+    int64_t units = rows / kRows + 1;
+    const int64_t requests = rows / (p.few_rows + 1);
+    units += requests < p.a.requests ? requests : p.a.requests;
+    units *= p.heads;
+    k_attention_many<B><<<(unsigned)(units < sms ? units : sms), kThreads, smem, s>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, cudaStream_t s)
+{
+    return int4_dispatch(head_size, group, [&](auto blob) { return launch<decltype(blob)>(p, s); });
+}

@@ -107,3 +107,4 @@ constexpr int kFewMaxBlocks = 480;
 size_t attn_few_workspace(int head_size, int max_rows);
 cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max_rows, void *ws,
                             cudaStream_t s);
+cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, cudaStream_t s);

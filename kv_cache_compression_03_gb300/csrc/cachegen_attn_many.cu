@@ -13,7 +13,7 @@
 //                    more than 2^8.
 //   warps 8-10       K: 4-bit codes to bf16 rows in shared memory
 //   warps 11-14      V: the same, transposed (channels as rows)
-//   warp 15          one thread issues all products
+//   warp 15          one thread issues all products; the warp finds the next unit
 // Codes are expanded once per 256 rows, beside 2 x 2 x 128 x 128 x 128 products.
 // K rows keep the channel order in which a word's codes come apart (0 4 1 5 2 6
 // 3 7 of each eight); Q is laid out alike. V's words hold a pair of tokens each, as
@@ -30,9 +30,13 @@
 
 namespace {
 
-constexpr int kSoftWarps = 8, kKWarps = 3, kVWarps = 4;   // 16 warps in all: 128 registers
+constexpr int kSoftWarps = 8, kKWarps = 3, kVWarps = 4;
 constexpr int kWarps = kSoftWarps + kKWarps + kVWarps + 1;
 constexpr int kThreads = 32 * kWarps;
+// registers of a softmax thread (a row of S in them) and of the others: 256 of each share
+// the 512 * 128 that the block starts with
+constexpr int kSoftRegs = 184, kOtherRegs = 72;
+static_assert(kSoftRegs + kOtherRegs <= 2 * 128, "more registers than the block has");
 constexpr int kRows = 256;       // of a block
 constexpr int kTile = 128;       // tokens
 constexpr int kBlobs = kTile / 16;
@@ -94,7 +98,7 @@ __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 32 columns of the warp's 32 lanes.
-__device__ __forceinline__ void tmem_ld32(float (&v)[32], uint32_t at)
+__device__ __forceinline__ void tmem_ld32(float *v, uint32_t at)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
@@ -107,18 +111,6 @@ __device__ __forceinline__ void tmem_ld32(float (&v)[32], uint32_t at)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32])
-{
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"f"(v[0]),
-        "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]),
-        "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]),
-        "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(at)
-        : "memory");
-}
-
 __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16])
 {
     asm volatile(
@@ -127,6 +119,37 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&v)[16])
         "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(at)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t (&v)[16], uint32_t at)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(at)
+        : "memory");
+}
+
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -167,18 +190,28 @@ __device__ __forceinline__ void load_or_zero(uint32_t (&w)[N], const uint8_t *p,
 
 // ------------------------------------------------------------------ schedule
 
+// 256 rows of a (request, KV head) and the blobs that they see: [0, sink) and
+// [sink + skip, ..), nb of them in n tiles of 8.
+struct Unit {
+    int32_t there;        // 0: no more units
+    int32_t r, h, q_row0; // request, KV head, the request's first query row
+    int32_t rows, row0;   // rows of the request's KV head, first row of the unit
+    int32_t tiles_q;      // row tiles of 128: 1 or 2
+    int32_t x0, kv;       // position of the request's first query row; its tokens
+    int32_t n, nb, sink, skip;
+    int32_t bad_page;     // a page id is outside the cache
+    __device__ __forceinline__ int32_t blob(int32_t vb) const { return vb < sink ? vb : vb + skip; }
+};
+
 template <int D>
 struct ManyShared {
     uint8_t q[2][kTile * D * 2];
     uint8_t k[2][kTile * D * 2];
     uint8_t v[2][kTile * D * 2];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
-    int64_t warp_sum[kWarps];
+    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
+    Unit unit[2];
     uint32_t tmem;
-    int32_t found_r;
-    int64_t found_off;
     uint32_t gave_up;    // a wait ran out: everyone leaves
-    uint32_t bad_page;   // a page id of the unit is outside the cache
 };
 
 // Waits that end: false once this wait or another one of the block ran out.
@@ -204,27 +237,28 @@ __device__ __forceinline__ bool wait_or_leave(uint64_t *bar, uint32_t parity, ui
     return false;
 }
 
-__device__ __forceinline__ int64_t units_of(const AttnArgs &p, int r, AttnRequest *q)
+__device__ __forceinline__ int32_t units_of(const AttnArgs &p, int r, AttnRequest *q)
 {
     uint32_t error;
-    if (!attn_request(p, r, q, &error) || q->rows <= p.few_rows)
+    if (r >= p.a.requests || !attn_request(p, r, q, &error) || q->rows <= p.few_rows)
         return 0;
-    return (int64_t)((q->rows + kRows - 1) / kRows) * p.heads;
+    return (q->rows + kRows - 1) / kRows * p.heads;   // at most tokens * q_heads
 }
 
-// Block-wide: the request that unit `want` belongs to, in sm.found_r
-// (requests: past the last unit), and the unit's number within it.
-template <typename S>
-__device__ void find_unit(const AttnArgs &p, S &sm, int64_t want)
+// One warp: unit `want` of the batch into *u. It goes on from where the last
+// call stood (32 requests from *r0 on, `*before` units ahead of them).
+__device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t want, int *r0, int64_t *before, Unit *u)
 {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid == 0)
-        sm.found_r = p.a.requests;
-    int64_t carry = 0;
-    for (int r0 = 0; r0 < p.a.requests; r0 += kThreads) {
-        const int r = r0 + tid;
+    const int lane = threadIdx.x & 31;
+    for (;; *r0 += 32) {
+        if (*r0 >= p.a.requests) {
+            if (lane == 0)
+                u->there = 0;
+            __syncwarp();
+            return;
+        }
         AttnRequest q;
-        const int64_t w = r < p.a.requests ? units_of(p, r, &q) : 0;
+        const int w = units_of(p, *r0 + lane, &q);
         int64_t inc = w;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -232,29 +266,47 @@ __device__ void find_unit(const AttnArgs &p, S &sm, int64_t want)
             if (lane >= d)
                 inc += o;
         }
-        if (lane == 31)
-            sm.warp_sum[warp] = inc;
-        __syncthreads();
-        int64_t before = carry;
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp)
-                before += sm.warp_sum[i];
-            carry += sm.warp_sum[i];
+        const int64_t start = *before + inc - w;
+        const uint32_t mine = __ballot_sync(0xFFFFFFFFu, want >= start && want < start + w);
+        if (mine == 0) {
+            *before += __shfl_sync(0xFFFFFFFFu, inc, 31);
+            continue;
         }
-        const int64_t start = before + inc - w;
-        if (want >= start && want < start + w) {
-            sm.found_r = r;
-            sm.found_off = want - start;
+        const int src = __ffs(mine) - 1;
+        const int off = __shfl_sync(0xFFFFFFFFu, (int)(want - start), src);
+        const int r = *r0 + src;
+        units_of(p, r, &q);
+        // the last rows, which see most, first
+        const int tile = (q.rows + kRows - 1) / kRows - 1 - off / p.heads;
+        const int row0 = tile * kRows, rows = min(kRows, q.rows - row0), x0 = q.kv - q.nq;
+        const int x_first = x0 + row0 / p.ratio, x_last = x0 + (row0 + rows - 1) / p.ratio;
+        const int end = x_last < 0 ? 0 : x_last / 16 + 1;
+        int sink = 0, skip = 0;
+        const int64_t low = (int64_t)x_first + 1 - p.a.window;
+        if (p.a.window > 0 && low > 0) {
+            const int first = (int)(low / 16);
+            const int64_t sb = ((int64_t)p.a.sinks + 15) / 16;
+            sink = sb < first ? (int)sb : first;
+            skip = first - sink;
         }
-        __syncthreads();
+        const int nb = end - skip, bpp = p.page_tokens / 16;
+        bool bad = false;
+        for (int vb = lane; vb < nb; vb += 32) {
+            const int ab = vb < sink ? vb : vb + skip;
+            const int id = p.a.block_table[r * p.a.table_stride + ab / bpp];
+            bad |= (unsigned)id >= (unsigned)p.num_pages;
+        }
+        bad = __any_sync(0xFFFFFFFFu, bad);
+        if (lane == 0) {
+            if (bad)
+                int4_set_status(p.status, CG_ERR_CORRUPT);
+            *u = {1,  r, off % p.heads, q.row0, q.rows, row0, rows > 128 ? 2 : 1,
+                  x0, q.kv, (nb + kBlobs - 1) / kBlobs, nb, sink, skip, bad};
+        }
+        __syncwarp();
+        return;
     }
 }
-
-// Visible blob vb of a unit is blob vb or, behind the first tokens, vb + skip.
-struct Stretch {
-    int32_t nb, sink, skip;
-    __device__ __forceinline__ int32_t blob(int32_t vb) const { return vb < sink ? vb : vb + skip; }
-};
 
 // -------------------------------------------------------------------- kernel
 
@@ -279,142 +331,108 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
             bar_init(&sm.v_empty[i], 1);
             bar_init(&sm.s_full[i], 1);
         }
+        bar_init(&sm.q_full, 128 * 2);
         bar_init_fence();
         sm.gave_up = 0;
     }
+    int u_r0 = 0;                // the last warp's place in the batch
+    int64_t u_before = 0, u_next = blockIdx.x;
     if (warp == kWarps - 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_addr(&sm.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        find_unit(p, u_next, &u_r0, &u_before, &sm.unit[0]);
         tmem_fence_before();
     }
     __syncthreads();
     tmem_fence_after();
     const uint32_t tmem = sm.tmem;
     const int bpp = p.page_tokens / 16;
-    const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
-    // exponents in powers of two; a negative scale goes into Q, so that the largest score is
-    // the largest product
-    const float sc = fmaxf(fabsf(p.scale2), 1.2e-38f);
-    const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
-
-    uint32_t tiles_done = 0;             // K and V tiles of earlier units
-    uint32_t s_done[2] = {0, 0};         // uses of s_full, p_full is used one less per unit
-    uint32_t p_done[2] = {0, 0};
+    uint32_t tiles_done = 0;     // K and V tiles of earlier units
     bool alive = true;
-    for (int64_t unit = blockIdx.x;; unit += gridDim.x) {
-        find_unit(p, sm, unit);
-        if (sm.found_r >= p.a.requests)
-            break;
-        const int r = sm.found_r;
-        AttnRequest q;
-        uint32_t error;
-        attn_request(p, r, &q, &error);
-        const int row_tiles = (q.rows + kRows - 1) / kRows;
-        // the last rows, which see most, first
-        const int rt = row_tiles - 1 - (int)(sm.found_off / p.heads);
-        const int h = (int)(sm.found_off % p.heads);
-        const int row0 = rt * kRows, rows = min(kRows, q.rows - row0);
-        const int tiles_q = rows > 128 ? 2 : 1;
-        // positions of the unit's first and last row, and the blobs that they see
-        const int x0 = q.kv - q.nq;
-        const int x_first = x0 + row0 / p.ratio, x_last = x0 + (row0 + rows - 1) / p.ratio;
-        Stretch st;
-        {
-            const int end = x_last < 0 ? 0 : x_last / 16 + 1;
-            st = {end, 0, 0};
-            const int64_t low = (int64_t)x_first + 1 - window;
-            if (p.a.window > 0 && low > 0) {
-                const int first = (int)(low / 16);
-                const int64_t sb = ((int64_t)p.a.sinks + 15) / 16;
-                st.sink = sb < first ? (int)sb : first;
-                st.skip = first - st.sink;
-                st.nb = end - st.skip;
-            }
-        }
-        const int n = (st.nb + kBlobs - 1) / kBlobs;   // tiles (0: nothing is seen)
-        const int32_t *table = p.a.block_table + r * p.a.table_stride;
 
-        // ---- Q into shared memory, and a look at the page ids
-        if (tid == 0)
-            sm.bad_page = 0;
-        __syncthreads();
-        for (int i = tid; i < tiles_q * 128 * (D / 8); i += kThreads) {
-            const int row = i / (D / 8), c = i % (D / 8), rr = row0 + row;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < rows) {
-                const int qt = rr / p.ratio, qh = h * p.ratio + rr - qt * p.ratio;
-                v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) +
-                                                     (int64_t)(q.row0 + qt) * p.a.q_token_stride +
-                                                     qh * p.a.q_head_stride + 8 * c);
+    if (warp < kSoftWarps) {
+        // ===================================================== softmax of a row
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+        // exponents in powers of two; a negative scale goes into Q, so that the largest score
+        // is the largest product
+        const float sc = fmaxf(fabsf(p.scale2), 1.2e-38f);
+        const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+        const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
+        const int i = warp >> 2, row = 32 * (warp & 3) + lane;
+        const uint32_t lane_at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t s_at = lane_at + 128 * i, o_at = lane_at + kO + 128 * i;
+        uint32_t s_done = 0;
+        for (int un = 0;; un ^= 1) {
+            const Unit &u = sm.unit[un];
+            if (!u.there)
+                break;
+            // ---- the row tile's queries into shared memory
+            for (int e = tid & 127; e < 128 * (D / 8); e += 128) {
+                const int in = e / (D / 8), c = e % (D / 8), rr = u.row0 + 128 * i + in;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (rr < u.rows) {
+                    const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
+                    v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) +
+                                                         (int64_t)(u.q_row0 + qt) * p.a.q_token_stride +
+                                                         qh * p.a.q_head_stride + 8 * c);
+                }
+                *reinterpret_cast<uint4 *>(sm.q[i] + (c >> 3) * kQSub + in * 128 + (((c & 7) ^ (in & 7)) << 4)) =
+                    make_uint4(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip,
+                               __byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
             }
-            const uint4 o = make_uint4(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip,
-                                       __byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
-            const int in = row & 127;
-            *reinterpret_cast<uint4 *>(sm.q[row >> 7] + (c >> 3) * kQSub + in * 128 + (((c & 7) ^ (in & 7)) << 4)) = o;
-        }
-        for (int vb = tid; vb < st.nb; vb += kThreads) {
-            const int id = table[st.blob(vb) / bpp];
-            if ((unsigned)id >= (unsigned)p.num_pages) {
-                sm.bad_page = 1;
-                int4_set_status(p.status, CG_ERR_CORRUPT);
-            }
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncthreads();
-        const bool bad_page = sm.bad_page;
-
-        if (warp < kSoftWarps) {
-            // ================================================== softmax of a row
-            const int i = warp >> 2, row = 32 * (warp & 3) + lane, rr = row0 + 128 * i + row;
-            if (i < tiles_q) {
-                const uint32_t lane_at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-                const uint32_t s_at = lane_at + 128 * i, o_at = lane_at + kO + 128 * i;
-                const int x = rr < q.rows ? x0 + rr / p.ratio : -1;
-                const int last_row = min(row0 + 128 * i + 128, q.rows) - 1;
-                const int x_lo = x0 + (row0 + 128 * i) / p.ratio, x_hi = x0 + last_row / p.ratio;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            bar_arrive(&sm.q_full);
+            if (i < u.tiles_q) {
+                const int rr = u.row0 + 128 * i + row;
+                const int x = rr < u.rows ? u.x0 + rr / p.ratio : -1;
+                const int last_row = min(u.row0 + 128 * i + 128, u.rows) - 1;
+                const int x_lo = u.x0 + (u.row0 + 128 * i) / p.ratio, x_hi = u.x0 + last_row / p.ratio;
                 float m = kNone, l = 0.0f;
-                for (int j = 0; j < n && alive; ++j) {
-                    alive = wait_or_leave(&sm.s_full[i], s_done[i] & 1, &sm.gave_up, p.status);
+                for (int j = 0; j < u.n; ++j) {
+                    alive = wait_or_leave(&sm.s_full[i], s_done & 1, &sm.gave_up, p.status);
                     alive = __all_sync(0xFFFFFFFFu, alive);
-                    ++s_done[i];
+                    ++s_done;
                     if (!alive)
                         break;
                     tmem_fence_after();
+                    float s[kTile];
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        tmem_ld32(s + 32 * c, s_at + 32 * c);
                     const int vb0 = j * kBlobs;
-                    const int t0 = 16 * st.blob(vb0), t1 = 16 * st.blob(vb0 + kBlobs - 1) + 15;
-                    const bool whole = !bad_page && vb0 + kBlobs <= st.nb && t1 <= x_lo &&
+                    const int t0 = 16 * u.blob(vb0), t1 = 16 * u.blob(vb0 + kBlobs - 1) + 15;
+                    const bool whole = !u.bad_page && vb0 + kBlobs <= u.nb && t1 <= x_lo &&
                                        (x_hi - t0 < window || t1 < p.a.sinks);
+                    tmem_wait_ld();
+                    if (!whole) {
+#pragma unroll
+                        for (int b = 0; b < kBlobs; ++b) {
+                            const int vb = vb0 + b;
+                            bool there = vb < u.nb;
+                            if (there && u.bad_page)
+                                there = (unsigned)p.a.block_table[u.r * p.a.table_stride + u.blob(vb) / bpp] <
+                                        (unsigned)p.num_pages;
+                            const int tok = 16 * u.blob(vb);
+                            // of the blob's 16 tokens the row sees those below `end`, from `low` on or below `sink`
+                            const int end = there ? x + 1 - tok : 0;
+                            const int64_t low64 = (int64_t)x + 1 - window - tok;
+                            const int low = low64 < 0 ? 0 : (int)min(low64, (int64_t)16);
+                            const int sink = p.a.sinks - tok;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                s[16 * b + e] = e < end && (e >= low || e < sink) ? s[16 * b + e] : -INFINITY;
+                        }
+                    }
                     float mx = -INFINITY;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        tmem_ld32(s, s_at + 32 * c);
-                        tmem_wait_ld();
-                        if (!whole) {
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                const int vb = vb0 + 2 * c + b;
-                                bool there = vb < st.nb;
-                                if (there && bad_page)
-                                    there = (unsigned)table[st.blob(vb) / bpp] < (unsigned)p.num_pages;
-                                const int tok = 16 * st.blob(vb);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const int at = tok + e;
-                                    const bool sees = there && at <= x && (x - at < window || at < p.a.sinks);
-                                    s[16 * b + e] = sees ? s[16 * b + e] : -INFINITY;
-                                }
-                            }
-                            tmem_st32(s_at + 32 * c, s);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            mx = fmaxf(mx, s[e]);
+                    for (int e = 0; e < kTile; e += 8) {
+                        const float a = fmaxf(fmaxf(s[e], s[e + 1]), s[e + 2]);
+                        const float b = fmaxf(fmaxf(s[e + 3], s[e + 4]), s[e + 5]);
+                        mx = fmaxf(fmaxf(mx, a), b);
+                        mx = fmaxf(fmaxf(mx, s[e + 6]), s[e + 7]);
                     }
-                    if (!whole)
-                        tmem_wait_st();
                     mx *= sc;
                     if (__any_sync(0xFFFFFFFFu, mx > m + 8.0f)) {
                         const float mn = fmaxf(mx, m), f = exp2_fast(m - mn);
@@ -422,120 +440,133 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                         l *= f;
                         if (j > 0) {
 #pragma unroll 1
-                            for (int c = 0; c < D / 32; ++c) {
-                                float o[32];
-                                tmem_ld32(o, o_at + 32 * c);
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(o, o_at + 16 * c);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    o[e] *= f;
-                                tmem_st32(o_at + 32 * c, o);
+                                for (int e = 0; e < 16; ++e)
+                                    o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                tmem_st16(o_at + 16 * c, o);
                             }
                         }
                     }
-                    float sum = 0.0f;
+                    float2 sum = make_float2(0.0f, 0.0f);
+                    const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        float s[32];
                         uint32_t pk[16];
-                        tmem_ld32(s, s_at + 32 * c);
-                        tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            s[e] = exp2_fast(fmaf(s[e], sc, -m));
-                            sum += s[e];
+                        for (int e = 0; e < 16; ++e) {
+                            float2 z = fma2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, m2);
+                            z.x = exp2_fast(z.x);
+                            z.y = exp2_fast(z.y);
+                            sum = add2(sum, z);
+                            pk[e] = pack_bf16(z.x, z.y);
                         }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            pk[e] = pack_bf16(s[2 * e], s[2 * e + 1]);
-                        tmem_st16(s_at + 16 * c, pk);   // over columns already read
+                        tmem_st16(s_at + 16 * c, pk);
                     }
-                    l += sum;
+                    l += sum.x + sum.y;
                     tmem_wait_st();
                     tmem_fence_before();
                     bar_arrive(&sm.p_full[i]);
                 }
-                if (alive && n > 0) {
-                    alive = wait_or_leave(&sm.s_full[i], s_done[i] & 1, &sm.gave_up, p.status);
+                if (alive && u.n > 0) {
+                    alive = wait_or_leave(&sm.s_full[i], s_done & 1, &sm.gave_up, p.status);
                     alive = __all_sync(0xFFFFFFFFu, alive);
-                    ++s_done[i];
+                    ++s_done;
                     tmem_fence_after();
                 }
                 if (alive) {
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    const int qt = rr / p.ratio, qh = h * p.ratio + rr - qt * p.ratio;
+                    const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
                     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
-                                         (int64_t)(q.row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride;
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        float o[32];
-                        if (n > 0) {
-                            tmem_ld32(o, o_at + 32 * c);
-                            tmem_wait_ld();
-                        } else {
+                                         (int64_t)(u.q_row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride;
+                    float o[D];
+                    if (u.n > 0) {
 #pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                o[e] = 0.0f;
-                        }
-                        if (rr < q.rows) {
+                        for (int c = 0; c < D / 32; ++c)
+                            tmem_ld32(o + 32 * c, o_at + 32 * c);
+                        tmem_wait_ld();
+                    } else {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 8)
-                                *reinterpret_cast<uint4 *>(out + 32 * c + e) =
-                                    make_uint4(pack_bf16(o[e] * inv, o[e + 1] * inv),
-                                               pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                               pack_bf16(o[e + 4] * inv, o[e + 5] * inv),
-                                               pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-                        }
+                        for (int e = 0; e < D; ++e)
+                            o[e] = 0.0f;
+                    }
+                    if (rr < u.rows) {
+#pragma unroll
+                        for (int e = 0; e < D; e += 8)
+                            *reinterpret_cast<uint4 *>(out + e) = make_uint4(
+                                pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
+                                pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
                     }
                 }
                 tmem_fence_before();
             }
-        } else if (warp < kSoftWarps + kKWarps) {
+            __syncthreads();
+            if (sm.gave_up)
+                break;
+        }
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp < kSoftWarps + kKWarps) {
             // ============================================================ K tiles
             // A warp takes 8 tokens (half a blob) at a time: lane t + 4 k has words t of token
             // (k & 1) * 4 + (k >> 1), so that eight lanes' 16-byte stores meet all banks
             constexpr int kItems = (2 * kBlobs + kKWarps - 1) / kKWarps;
             const int wi = warp - kSoftWarps, t = lane & 3, k8 = lane >> 2;
             const int half_tok = (k8 & 1) * 4 + (k8 >> 1);
-            for (int j = 0; j < n && alive; ++j) {
-                uint32_t code[kItems][NW], par[kItems][NG];
-#pragma unroll
-                for (int u = 0; u < kItems; ++u) {
-                    const int item = wi + kKWarps * u, vb = j * kBlobs + (item >> 1);
-                    const int tok = 8 * (item & 1) + half_tok;
-                    int id = -1, ab = 0;
-                    if (item < 2 * kBlobs && vb < st.nb) {
-                        ab = st.blob(vb);
-                        id = table[ab / bpp];
-                    }
-                    const bool there = (unsigned)id < (unsigned)p.num_pages;
-                    const uint8_t *blob = p.layer + (((size_t)(there ? id : 0) * p.heads + h) * bpp + ab % bpp) *
-                                                        B::kBytes;
-                    load_or_zero(code[u], blob + B::kKCodes + tok * (D / 2) + t * (D / 8), there);
-                    load_or_zero(par[u], blob + B::kKParams + tok * 4 * NG, there);
-                }
-                const uint32_t use = tiles_done + j, sl = use & 1;
-                alive = wait_or_leave(&sm.k_empty[sl], (use >> 1 & 1) ^ 1, &sm.gave_up, p.status);
-                if (!alive)
+            for (int un = 0;; un ^= 1) {
+                const Unit &u = sm.unit[un];
+                if (!u.there)
                     break;
+                const int32_t *table = p.a.block_table + u.r * p.a.table_stride;
+                const int n = u.n, nb = u.nb, h = u.h;
+                for (int j = 0; j < n; ++j) {
+                    uint32_t code[kItems][NW], par[kItems][NG];
 #pragma unroll
-                for (int u = 0; u < kItems; ++u) {
-                    const int item = wi + kKWarps * u, row = 8 * item + half_tok;
-                    if (item >= 2 * kBlobs)
+                    for (int it = 0; it < kItems; ++it) {
+                        const int item = wi + kKWarps * it, vb = j * kBlobs + (item >> 1);
+                        const int tok = 8 * (item & 1) + half_tok;
+                        int id = -1, ab = 0;
+                        if (item < 2 * kBlobs && vb < nb) {
+                            ab = u.blob(vb);
+                            id = table[ab / bpp];
+                        }
+                        const bool there = (unsigned)id < (unsigned)p.num_pages;
+                        const uint8_t *blob =
+                            p.layer + (((size_t)(there ? id : 0) * p.heads + h) * bpp + ab % bpp) * B::kBytes;
+                        load_or_zero(code[it], blob + B::kKCodes + tok * (D / 2) + t * (D / 8), there);
+                        load_or_zero(par[it], blob + B::kKParams + tok * 4 * NG, there);
+                    }
+                    const uint32_t use = tiles_done + j, sl = use & 1;
+                    if (!wait_or_leave(&sm.k_empty[sl], (use >> 1 & 1) ^ 1, &sm.gave_up, p.status))
                         break;
 #pragma unroll
-                    for (int w = 0; w < NW; ++w) {
-                        const uint32_t pw = par[u][w / WPG];
-                        const uint32_t s2 = __byte_perm(pw, pw, 0x1010), lo2 = __byte_perm(pw, pw, 0x3232);
-                        const uint4 o = make_uint4(expand(code[u][w], 0, s2, lo2), expand(code[u][w], 1, s2, lo2),
-                                                   expand(code[u][w], 2, s2, lo2), expand(code[u][w], 3, s2, lo2));
-                        const int c = 4 * w + t;
-                        *reinterpret_cast<uint4 *>(sm.k[sl] + (c >> 3) * kQSub + row * 128 +
-                                                   (((c & 7) ^ (row & 7)) << 4)) = o;
+                    for (int it = 0; it < kItems; ++it) {
+                        const int item = wi + kKWarps * it, at = 8 * item + half_tok;
+                        if (item >= 2 * kBlobs)
+                            break;
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) {
+                            const uint32_t pw = par[it][w / WPG];
+                            const uint32_t s2 = __byte_perm(pw, pw, 0x1010), lo2 = __byte_perm(pw, pw, 0x3232);
+                            const uint4 o =
+                                make_uint4(expand(code[it][w], 0, s2, lo2), expand(code[it][w], 1, s2, lo2),
+                                           expand(code[it][w], 2, s2, lo2), expand(code[it][w], 3, s2, lo2));
+                            const int c = 4 * w + t;
+                            *reinterpret_cast<uint4 *>(sm.k[sl] + (c >> 3) * kQSub + at * 128 +
+                                                       (((c & 7) ^ (at & 7)) << 4)) = o;
+                        }
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    bar_arrive(&sm.k_full[sl]);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                bar_arrive(&sm.k_full[sl]);
+                tiles_done += n;
+                __syncwarp();
+                __syncthreads();
+                if (sm.gave_up)
+                    break;
             }
         } else if (warp < kSoftWarps + kKWarps + kVWarps) {
             // ============================================================ V tiles
@@ -543,116 +574,139 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
             // 32 w + 4 g + i; eight lanes with the same g store to different 16-byte columns
             const int wi = warp - kSoftWarps - kKWarps;
             const int pg = 8 * (wi & 1) + (lane & 7), g = 4 * (wi >> 1) + (lane >> 3), hf = pg & 1;
-            for (int j = 0; j < n && alive; ++j) {
-                uint32_t code[4][NW], par[8][NG];
-                const int vb = j * kBlobs + (pg >> 1);
-                int id = -1, ab = 0;
-                if (vb < st.nb) {
-                    ab = st.blob(vb);
-                    id = table[ab / bpp];
-                }
-                const bool there = (unsigned)id < (unsigned)p.num_pages;
-                const uint8_t *blob = p.layer + (((size_t)(there ? id : 0) * p.heads + h) * bpp + ab % bpp) * B::kBytes;
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    load_or_zero(code[u], blob + B::kVCodes + (4 * hf + u) * D + g * (D / 8), there);
-                // tokens that are not there get 0, whatever the cache holds in their place
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    load_or_zero(par[u], blob + B::kVParams + (8 * hf + u) * 4 * NG,
-                                 there && 16 * ab + 8 * hf + u < q.kv);
-                const uint32_t use = tiles_done + j, sl = use & 1;
-                alive = wait_or_leave(&sm.v_empty[sl], (use >> 1 & 1) ^ 1, &sm.gave_up, p.status);
-                if (!alive)
+            for (int un = 0;; un ^= 1) {
+                const Unit &u = sm.unit[un];
+                if (!u.there)
                     break;
-#pragma unroll
-                for (int gi = 0; gi < NG; ++gi) {
-                    uint32_t s2[4], lo2[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        s2[u] = __byte_perm(par[2 * u][gi], par[2 * u + 1][gi], 0x5410);
-                        lo2[u] = __byte_perm(par[2 * u][gi], par[2 * u + 1][gi], 0x7632);
+                const int32_t *table = p.a.block_table + u.r * p.a.table_stride;
+                const int n = u.n, nb = u.nb, h = u.h, kv = u.kv;
+                for (int j = 0; j < n; ++j) {
+                    uint32_t code[4][NW], par[8][NG];
+                    const int vb = j * kBlobs + (pg >> 1);
+                    int id = -1, ab = 0;
+                    if (vb < nb) {
+                        ab = u.blob(vb);
+                        id = table[ab / bpp];
                     }
+                    const bool there = (unsigned)id < (unsigned)p.num_pages;
+                    const uint8_t *blob =
+                        p.layer + (((size_t)(there ? id : 0) * p.heads + h) * bpp + ab % bpp) * B::kBytes;
 #pragma unroll
-                    for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+                    for (int e = 0; e < 4; ++e)
+                        load_or_zero(code[e], blob + B::kVCodes + (4 * hf + e) * D + g * (D / 8), there);
+                    // tokens that are not there get 0, whatever the cache holds in their place
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const uint4 o = make_uint4(expand(code[0][w], i, s2[0], lo2[0]),
-                                                       expand(code[1][w], i, s2[1], lo2[1]),
-                                                       expand(code[2][w], i, s2[2], lo2[2]),
-                                                       expand(code[3][w], i, s2[3], lo2[3]));
-                            const int row = 32 * w + 4 * g + i;
-                            *reinterpret_cast<uint4 *>(sm.v[sl] + (pg >> 3) * kVSub + row * 128 +
-                                                       (((pg & 7) ^ (row & 7)) << 4)) = o;
+                    for (int e = 0; e < 8; ++e)
+                        load_or_zero(par[e], blob + B::kVParams + (8 * hf + e) * 4 * NG,
+                                     there && 16 * ab + 8 * hf + e < kv);
+                    const uint32_t use = tiles_done + j, sl = use & 1;
+                    if (!wait_or_leave(&sm.v_empty[sl], (use >> 1 & 1) ^ 1, &sm.gave_up, p.status))
+                        break;
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) {
+                        uint32_t s2[4], lo2[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            s2[e] = __byte_perm(par[2 * e][gi], par[2 * e + 1][gi], 0x5410);
+                            lo2[e] = __byte_perm(par[2 * e][gi], par[2 * e + 1][gi], 0x7632);
                         }
+#pragma unroll
+                        for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const uint4 o = make_uint4(
+                                    expand(code[0][w], c, s2[0], lo2[0]), expand(code[1][w], c, s2[1], lo2[1]),
+                                    expand(code[2][w], c, s2[2], lo2[2]), expand(code[3][w], c, s2[3], lo2[3]));
+                                const int at = 32 * w + 4 * g + c;
+                                *reinterpret_cast<uint4 *>(sm.v[sl] + (pg >> 3) * kVSub + at * 128 +
+                                                           (((pg & 7) ^ (at & 7)) << 4)) = o;
+                            }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    bar_arrive(&sm.v_full[sl]);
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                bar_arrive(&sm.v_full[sl]);
+                tiles_done += n;
+                __syncwarp();
+                __syncthreads();
+                if (sm.gave_up)
+                    break;
             }
-        } else if (lane == 0 && n > 0) {
+        } else {
             // ========================================================== products
             const uint32_t q_at = smem_addr(sm.q[0]), k_at = smem_addr(sm.k[0]), v_at = smem_addr(sm.v[0]);
             auto scores = [&](int i, uint32_t sl) {
+                const uint64_t a = smem_desc(q_at + i * (kTile * D * 2)), b = smem_desc(k_at + sl * (kTile * D * 2));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * kQSub + (kk & 3) * 32;
-                    mma_ss(tmem + 128 * i, smem_desc(q_at + i * (kTile * D * 2) + off),
-                           smem_desc(k_at + sl * (kTile * D * 2) + off), mma_desc(kTile), kk > 0);
+                    const uint32_t off = ((kk >> 2) * kQSub + (kk & 3) * 32) >> 4;
+                    mma_ss(tmem + 128 * i, a + off, b + off, mma_desc(kTile), kk > 0);
                 }
                 mma_commit(&sm.s_full[i]);
             };
-            uint32_t use = tiles_done;
-            alive = wait_or_leave(&sm.k_full[use & 1], use >> 1 & 1, &sm.gave_up, p.status);
-            if (alive) {
-                tmem_fence_after();
-                for (int i = 0; i < tiles_q; ++i)
-                    scores(i, use & 1);
-                mma_commit(&sm.k_empty[use & 1]);
-            }
-            for (int j = 0; j < n && alive; ++j, ++use) {
-                const uint32_t sl = use & 1, nx = use + 1;
-                for (int i = 0; i < tiles_q && alive; ++i) {
-                    alive = wait_or_leave(&sm.p_full[i], p_done[i] & 1, &sm.gave_up, p.status);
-                    ++p_done[i];
-                    if (alive && i == 0)
-                        alive = wait_or_leave(&sm.v_full[sl], use >> 1 & 1, &sm.gave_up, p.status);
-                    if (alive && i == 0 && j + 1 < n)
-                        alive = wait_or_leave(&sm.k_full[nx & 1], nx >> 1 & 1, &sm.gave_up, p.status);
-                    if (!alive)
-                        break;
-                    tmem_fence_after();
+            uint32_t p_done[2] = {0, 0}, units = 0;
+            for (int un = 0;; un ^= 1) {
+                const Unit &u = sm.unit[un];
+                if (!u.there)
+                    break;
+                const int n = u.n, tiles_q = u.tiles_q;
+                if (lane == 0) {
+                    alive = wait_or_leave(&sm.q_full, units & 1, &sm.gave_up, p.status);
+                    uint32_t use = tiles_done;
+                    if (alive && n > 0) {
+                        alive = wait_or_leave(&sm.k_full[use & 1], use >> 1 & 1, &sm.gave_up, p.status);
+                        if (alive) {
+                            tmem_fence_after();
+                            for (int i = 0; i < tiles_q; ++i)
+                                scores(i, use & 1);
+                            mma_commit(&sm.k_empty[use & 1]);
+                        }
+                    }
+                    for (int j = 0; j < n && alive; ++j, ++use) {
+                        const uint32_t sl = use & 1, nx = use + 1;
+                        for (int i = 0; i < tiles_q; ++i) {
+                            alive = wait_or_leave(&sm.p_full[i], p_done[i] & 1, &sm.gave_up, p.status);
+                            ++p_done[i];
+                            if (alive && i == 0)
+                                alive = wait_or_leave(&sm.v_full[sl], use >> 1 & 1, &sm.gave_up, p.status);
+                            if (alive && i == 0 && j + 1 < n)
+                                alive = wait_or_leave(&sm.k_full[nx & 1], nx >> 1 & 1, &sm.gave_up, p.status);
+                            if (!alive)
+                                break;
+                            tmem_fence_after();
+                            const uint64_t b = smem_desc(v_at + sl * (kTile * D * 2));
 #pragma unroll
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_ts(tmem + kO + 128 * i, tmem + 128 * i + 8 * kk,
-                               smem_desc(v_at + sl * (kTile * D * 2) + (kk >> 2) * kVSub + (kk & 3) * 32),
-                               mma_desc(D), j > 0 || kk > 0);
-                    if (i + 1 == tiles_q)
-                        mma_commit(&sm.v_empty[sl]);
-                    if (j + 1 < n)
-                        scores(i, nx & 1);
-                    else
-                        mma_commit(&sm.s_full[i]);   // O is complete
+                            for (int kk = 0; kk < kTile / 16; ++kk)
+                                mma_ts(tmem + kO + 128 * i, tmem + 128 * i + 8 * kk,
+                                       b + (((kk >> 2) * kVSub + (kk & 3) * 32) >> 4), mma_desc(D), j > 0 || kk > 0);
+                            if (i + 1 == tiles_q)
+                                mma_commit(&sm.v_empty[sl]);
+                            if (j + 1 < n)
+                                scores(i, nx & 1);
+                            else
+                                mma_commit(&sm.s_full[i]);   // O is complete
+                        }
+                        if (alive && j + 1 < n)
+                            mma_commit(&sm.k_empty[nx & 1]);
+                    }
                 }
-                if (alive && j + 1 < n)
-                    mma_commit(&sm.k_empty[nx & 1]);
+                __syncwarp();
+                tiles_done += n;
+                ++units;
+                u_next += gridDim.x;
+                find_unit(p, u_next, &u_r0, &u_before, &sm.unit[un ^ 1]);
+                __syncthreads();
+                if (sm.gave_up)
+                    break;
             }
+            // products still in flight (after a wait that ran out) end before the memory goes
+            if (sm.gave_up && lane == 0) {
+                bar_init(&sm.q_full, 1);
+                bar_init_fence();
+                mma_commit(&sm.q_full);
+                bar_wait(&sm.q_full, 0);
+            }
+            __syncwarp();
         }
-        tiles_done += n;
-        __syncwarp();
-        __syncthreads();
-        alive = sm.gave_up == 0;
-        if (!alive)
-            break;
-    }
-    // products still in flight (after a wait that ran out) end before the memory goes
-    if (warp == kWarps - 1) {
-        if (!alive && lane == 0) {
-            bar_init(&sm.k_full[0], 1);
-            bar_init_fence();
-            mma_commit(&sm.k_full[0]);
-            bar_wait(&sm.k_full[0], 0);
-        }
-        __syncwarp();
     }
     tmem_fence_before();
     __syncthreads();

@@ -33,10 +33,6 @@ namespace {
 constexpr int kSoftWarps = 8, kKWarps = 3, kVWarps = 4;
 constexpr int kWarps = kSoftWarps + kKWarps + kVWarps + 1;
 constexpr int kThreads = 32 * kWarps;
-// registers of a softmax thread (a row of S in them) and of the others: 256 of each share
-// the 512 * 128 that the block starts with
-constexpr int kSoftRegs = 184, kOtherRegs = 72;
-static_assert(kSoftRegs + kOtherRegs <= 2 * 128, "more registers than the block has");
 constexpr int kRows = 256;       // of a block
 constexpr int kTile = 128;       // tokens
 constexpr int kBlobs = kTile / 16;
@@ -45,12 +41,11 @@ constexpr float kNone = -3.0e38f;
 // ------------------------------------------------------------ instructions
 
 // Descriptor of a shared-memory operand: K-major rows of 128 bytes, 128-byte
-// swizzle, 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t at)
-{
-    return (uint64_t)((at >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)64 << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
+// swizzle, 8-row groups 1024 bytes apart. Only the low word, with the address,
+// varies; it is passed as 32 bits, so that a product takes few registers over to
+// the uniform file (what the issuing thread spends its time on).
+constexpr uint32_t kDescHigh = 64u | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t smem_desc(uint32_t at) { return (at >> 4 & 0x3FFF) | 1u << 16; }
 
 // bf16 x bf16 -> fp32, both operands K-major, M = 128.
 __host__ __device__ constexpr uint32_t mma_desc(int n)
@@ -58,21 +53,21 @@ __host__ __device__ constexpr uint32_t mma_desc(int n)
     return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh)
         : "memory");
 }
 
@@ -129,6 +124,18 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&v)[16], uint32_t at)
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(at)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32])
+{
+    uint32_t a[16], b[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        a[e] = __float_as_uint(v[e]);
+        b[e] = __float_as_uint(v[16 + e]);
+    }
+    tmem_st16(at, a);
+    tmem_st16(at + 16, b);
 }
 
 // Pairs of fp32 in one instruction.
@@ -190,6 +197,8 @@ __device__ __forceinline__ void load_or_zero(uint32_t (&w)[N], const uint8_t *p,
 
 // ------------------------------------------------------------------ schedule
 
+constexpr int kUnits = 4;   // units known at a time
+
 // 256 rows of a (request, KV head) and the blobs that they see: [0, sink) and
 // [sink + skip, ..), nb of them in n tiles of 8.
 struct Unit {
@@ -199,7 +208,6 @@ struct Unit {
     int32_t tiles_q;      // row tiles of 128: 1 or 2
     int32_t x0, kv;       // position of the request's first query row; its tokens
     int32_t n, nb, sink, skip;
-    int32_t bad_page;     // a page id is outside the cache
     __device__ __forceinline__ int32_t blob(int32_t vb) const { return vb < sink ? vb : vb + skip; }
 };
 
@@ -208,8 +216,11 @@ struct ManyShared {
     uint8_t q[2][kTile * D * 2];
     uint8_t k[2][kTile * D * 2];
     uint8_t v[2][kTile * D * 2];
-    uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2];
-    Unit unit[2];
+    uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
+        o_full[2], last;
+    uint64_t u_full[kUnits], u_empty[kUnits];
+    Unit unit[kUnits];
+    uint32_t bad[4];     // of the last tiles: blobs whose page id is outside the cache
     uint32_t tmem;
     uint32_t gave_up;    // a wait ran out: everyone leaves
 };
@@ -219,19 +230,10 @@ __device__ __forceinline__ bool wait_or_leave(uint64_t *bar, uint32_t parity, ui
                                               void *status)
 {
     const uint32_t at = smem_addr(bar);
-    for (uint32_t i = 0; i < kBarWaitLimit; ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(at), "r"(parity)
-            : "memory");
-        if (done)
-            return true;
-        if (*reinterpret_cast<volatile uint32_t *>(gave_up))
-            return false;
-    }
+    if (bar_poll(at, parity) || bar_wait_long(at, parity, gave_up))
+        return true;
+    if (*reinterpret_cast<volatile uint32_t *>(gave_up))
+        return false;
     *reinterpret_cast<volatile uint32_t *>(gave_up) = 1;
     int4_set_status(status, CG_ERR_TIMEOUT);
     return false;
@@ -289,24 +291,39 @@ __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t want, int *
             sink = sb < first ? (int)sb : first;
             skip = first - sink;
         }
-        const int nb = end - skip, bpp = p.page_tokens / 16;
-        bool bad = false;
-        for (int vb = lane; vb < nb; vb += 32) {
-            const int ab = vb < sink ? vb : vb + skip;
-            const int id = p.a.block_table[r * p.a.table_stride + ab / bpp];
-            bad |= (unsigned)id >= (unsigned)p.num_pages;
-        }
-        bad = __any_sync(0xFFFFFFFFu, bad);
-        if (lane == 0) {
-            if (bad)
-                int4_set_status(p.status, CG_ERR_CORRUPT);
-            *u = {1,  r, off % p.heads, q.row0, q.rows, row0, rows > 128 ? 2 : 1,
-                  x0, q.kv, (nb + kBlobs - 1) / kBlobs, nb, sink, skip, bad};
-        }
+        const int nb = end - skip;
+        if (lane == 0)
+            *u = {1,  r,    off % p.heads,                q.row0, q.rows, row0, rows > 128 ? 2 : 1,
+                  x0, q.kv, (nb + kBlobs - 1) / kBlobs, nb,     sink,   skip};
         __syncwarp();
         return;
     }
 }
+
+// The page ids of a tile's blobs, one by each of eight lanes (in every eight),
+// read a tile before its codes are and two before they are used.
+struct Lookup {
+    int32_t id, blob;
+    // starts reading the id of the lane's blob in tile j
+    __device__ __forceinline__ void start(const Unit &u, const int32_t *table, int bpp, int j)
+    {
+        const int vb = j * kBlobs + (threadIdx.x & 7);
+        id = -1;
+        blob = 0;
+        if (vb < u.nb) {
+            blob = u.blob(vb);
+            id = table[blob / bpp];
+        }
+    }
+    // the lane's blob in 128-byte units of the layer (it fits, cg_int4.h), ~0 if it is not there
+    template <typename B>
+    __device__ __forceinline__ uint32_t place(const AttnArgs &p, int h, int bpp) const
+    {
+        if ((unsigned)id >= (unsigned)p.num_pages)
+            return ~0u;
+        return (((uint32_t)id * p.heads + h) * bpp + blob % bpp) * (B::kBytes / 128);
+    }
+};
 
 // -------------------------------------------------------------------- kernel
 
@@ -316,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
     constexpr int kQSub = kTile * 128;           // bytes of a 64-channel part of a Q or K tile
     constexpr int kVSub = D * 128;               // bytes of a 64-token part of a V tile
-    constexpr uint32_t kO = 256;                 // tensor memory: S0, S1 at 0, 128; O0, O1 at 256, 384
+    // all 512 columns of tensor memory, so they start at 0: S0, S1, O0, O1
+    constexpr uint32_t kS = 0, kO = 256;
     using S = ManyShared<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
@@ -330,109 +348,118 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
             bar_init(&sm.k_empty[i], 1);
             bar_init(&sm.v_empty[i], 1);
             bar_init(&sm.s_full[i], 1);
+            bar_init(&sm.o_full[i], 1);
         }
-        bar_init(&sm.q_full, 128 * 2);
+        bar_init(&sm.last, 1);
+        for (int i = 0; i < kUnits; ++i) {
+            bar_init(&sm.u_full[i], 1);
+            bar_init(&sm.u_empty[i], kWarps);
+        }
+        bar_init(&sm.q_full, 32 * kVWarps);
+        bar_init(&sm.q_empty, 1);
         bar_init_fence();
         sm.gave_up = 0;
     }
-    int u_r0 = 0;                // the last warp's place in the batch
-    int64_t u_before = 0, u_next = blockIdx.x;
     if (warp == kWarps - 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
                          smem_addr(&sm.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        find_unit(p, u_next, &u_r0, &u_before, &sm.unit[0]);
         tmem_fence_before();
     }
     __syncthreads();
     tmem_fence_after();
-    const uint32_t tmem = sm.tmem;
+    if (sm.tmem != 0 && tid == 0)   // never: the block took all of it
+        int4_set_status(p.status, CG_ERR_CUDA);
     const int bpp = p.page_tokens / 16;
+    // Every role walks the block's units on its own and meets the others at the barriers only,
+    // so that the next unit's queries, keys and values come in under the last one's products.
+    uint32_t un = 0;             // units begun
     uint32_t tiles_done = 0;     // K and V tiles of earlier units
-    bool alive = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {   // one thread's view
+        return wait_or_leave(bar, parity, &sm.gave_up, p.status);
+    };
+    auto wait_all = [&](uint64_t *bar, uint32_t parity) {   // the warp's
+        return __all_sync(0xFFFFFFFFu, wait_or_leave(bar, parity, &sm.gave_up, p.status));
+    };
+    auto next_unit = [&]() -> const Unit * {   // the warp's next unit, or none
+        if (!wait_all(&sm.u_full[un % kUnits], un / kUnits & 1))
+            return nullptr;
+        const Unit *u = &sm.unit[un % kUnits];
+        return u->there ? u : nullptr;
+    };
+    auto unit_over = [&](int n) {
+        tiles_done += n;
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&sm.u_empty[un % kUnits]);
+        ++un;
+    };
 
     if (warp < kSoftWarps) {
         // ===================================================== softmax of a row
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         // exponents in powers of two; a negative scale goes into Q, so that the largest score
         // is the largest product
         const float sc = fmaxf(fabsf(p.scale2), 1.2e-38f);
-        const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
         const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
-        const int i = warp >> 2, row = 32 * (warp & 3) + lane;
-        const uint32_t lane_at = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-        const uint32_t s_at = lane_at + 128 * i, o_at = lane_at + kO + 128 * i;
-        uint32_t s_done = 0;
-        for (int un = 0;; un ^= 1) {
-            const Unit &u = sm.unit[un];
-            if (!u.there)
-                break;
-            // ---- the row tile's queries into shared memory
-            for (int e = tid & 127; e < 128 * (D / 8); e += 128) {
-                const int in = e / (D / 8), c = e % (D / 8), rr = u.row0 + 128 * i + in;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (rr < u.rows) {
-                    const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
-                    v = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(p.a.q) +
-                                                         (int64_t)(u.q_row0 + qt) * p.a.q_token_stride +
-                                                         qh * p.a.q_head_stride + 8 * c);
-                }
-                *reinterpret_cast<uint4 *>(sm.q[i] + (c >> 3) * kQSub + in * 128 + (((c & 7) ^ (in & 7)) << 4)) =
-                    make_uint4(__byte_perm(v.x, v.z, 0x5410) ^ flip, __byte_perm(v.x, v.z, 0x7632) ^ flip,
-                               __byte_perm(v.y, v.w, 0x5410) ^ flip, __byte_perm(v.y, v.w, 0x7632) ^ flip);
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            bar_arrive(&sm.q_full);
+        const int i = warp >> 2;
+        const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t s_at = lane_at + kS + 128 * i, o_at = lane_at + kO + 128 * i;
+        uint32_t s_done = 0, o_done = 0;
+        while (const Unit *up = next_unit()) {
+            const Unit &u = *up;
+            const int n = u.n;
             if (i < u.tiles_q) {
-                const int rr = u.row0 + 128 * i + row;
+                const int rr = u.row0 + 128 * i + 32 * (warp & 3) + lane;
                 const int x = rr < u.rows ? u.x0 + rr / p.ratio : -1;
                 const int last_row = min(u.row0 + 128 * i + 128, u.rows) - 1;
                 const int x_lo = u.x0 + (u.row0 + 128 * i) / p.ratio, x_hi = u.x0 + last_row / p.ratio;
                 float m = kNone, l = 0.0f;
-                for (int j = 0; j < u.n; ++j) {
-                    alive = wait_or_leave(&sm.s_full[i], s_done & 1, &sm.gave_up, p.status);
-                    alive = __all_sync(0xFFFFFFFFu, alive);
+                bool alive = true;
+                for (int j = 0; j < n; ++j) {
+                    alive = wait_all(&sm.s_full[i], s_done & 1);
                     ++s_done;
                     if (!alive)
                         break;
                     tmem_fence_after();
-                    float s[kTile];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        tmem_ld32(s + 32 * c, s_at + 32 * c);
                     const int vb0 = j * kBlobs;
                     const int t0 = 16 * u.blob(vb0), t1 = 16 * u.blob(vb0 + kBlobs - 1) + 15;
-                    const bool whole = !u.bad_page && vb0 + kBlobs <= u.nb && t1 <= x_lo &&
+                    const uint32_t bad = *reinterpret_cast<volatile uint32_t *>(&sm.bad[(tiles_done + j) & 3]);
+                    const bool whole = bad == 0 && vb0 + kBlobs <= u.nb && t1 <= x_lo &&
                                        (x_hi - t0 < window || t1 < p.a.sinks);
-                    tmem_wait_ld();
-                    if (!whole) {
-#pragma unroll
-                        for (int b = 0; b < kBlobs; ++b) {
-                            const int vb = vb0 + b;
-                            bool there = vb < u.nb;
-                            if (there && u.bad_page)
-                                there = (unsigned)p.a.block_table[u.r * p.a.table_stride + u.blob(vb) / bpp] <
-                                        (unsigned)p.num_pages;
-                            const int tok = 16 * u.blob(vb);
-                            // of the blob's 16 tokens the row sees those below `end`, from `low` on or below `sink`
-                            const int end = there ? x + 1 - tok : 0;
-                            const int64_t low64 = (int64_t)x + 1 - window - tok;
-                            const int low = low64 < 0 ? 0 : (int)min(low64, (int64_t)16);
-                            const int sink = p.a.sinks - tok;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                s[16 * b + e] = e < end && (e >= low || e < sink) ? s[16 * b + e] : -INFINITY;
-                        }
-                    }
+                    // S is read twice, 32 columns at a time: rolled loops, because the roles of the
+                    // block run side by side and have to share the instruction caches
                     float mx = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        float s[32];
+                        tmem_ld32(s, s_at + 32 * c);
+                        tmem_wait_ld();
+                        if (!whole) {
 #pragma unroll
-                    for (int e = 0; e < kTile; e += 8) {
-                        const float a = fmaxf(fmaxf(s[e], s[e + 1]), s[e + 2]);
-                        const float b = fmaxf(fmaxf(s[e + 3], s[e + 4]), s[e + 5]);
+                            for (int b = 0; b < 2; ++b) {
+                                const int vb = vb0 + 2 * c + b, tok = 16 * u.blob(vb);
+                                // of the blob's 16 tokens the row sees those below `end`, from `low` on or below `sink`
+                                const int end = vb < u.nb && !(bad >> (2 * c + b) & 1) ? x + 1 - tok : 0;
+                                const int64_t low64 = (int64_t)x + 1 - window - tok;
+                                const int low = low64 < 0 ? 0 : (int)min(low64, (int64_t)16);
+                                const int sink = p.a.sinks - tok;
+#pragma unroll
+                                for (int e = 0; e < 16; ++e)
+                                    s[16 * b + e] = e < end && (e >= low || e < sink) ? s[16 * b + e] : -INFINITY;
+                            }
+                            tmem_st32(s_at + 32 * c, s);
+                        }
+                        float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
+#pragma unroll
+                        for (int e = 4; e < 32; e += 4) {
+                            a = fmaxf(fmaxf(a, s[e]), s[e + 1]);
+                            b = fmaxf(fmaxf(b, s[e + 2]), s[e + 3]);
+                        }
                         mx = fmaxf(fmaxf(mx, a), b);
-                        mx = fmaxf(fmaxf(mx, s[e + 6]), s[e + 7]);
                     }
+                    if (!whole)
+                        tmem_wait_st();
                     mx *= sc;
                     if (__any_sync(0xFFFFFFFFu, mx > m + 8.0f)) {
                         const float mn = fmaxf(mx, m), f = exp2_fast(m - mn);
@@ -453,257 +480,347 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                     }
                     float2 sum = make_float2(0.0f, 0.0f);
                     const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
+                        float s[32];
                         uint32_t pk[16];
+                        tmem_ld32(s, s_at + 32 * c);
+                        tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            float2 z = fma2(make_float2(s[32 * c + 2 * e], s[32 * c + 2 * e + 1]), sc2, m2);
+                            float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), sc2, m2);
                             z.x = exp2_fast(z.x);
                             z.y = exp2_fast(z.y);
                             sum = add2(sum, z);
                             pk[e] = pack_bf16(z.x, z.y);
                         }
-                        tmem_st16(s_at + 16 * c, pk);
+                        tmem_st16(s_at + 16 * c, pk);   // over columns already read
                     }
                     l += sum.x + sum.y;
                     tmem_wait_st();
                     tmem_fence_before();
                     bar_arrive(&sm.p_full[i]);
                 }
-                if (alive && u.n > 0) {
-                    alive = wait_or_leave(&sm.s_full[i], s_done & 1, &sm.gave_up, p.status);
-                    alive = __all_sync(0xFFFFFFFFu, alive);
-                    ++s_done;
+                if (alive && n > 0) {
+                    alive = wait_all(&sm.o_full[i], o_done & 1);
+                    ++o_done;
                     tmem_fence_after();
                 }
-                if (alive) {
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
-                    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
-                                         (int64_t)(u.q_row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride;
-                    float o[D];
-                    if (u.n > 0) {
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c)
-                            tmem_ld32(o + 32 * c, o_at + 32 * c);
+                if (!alive)
+                    break;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
+                __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                                     (int64_t)(u.q_row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    if (n > 0) {
+                        tmem_ld32(o, o_at + 32 * c);
                         tmem_wait_ld();
                     } else {
 #pragma unroll
-                        for (int e = 0; e < D; ++e)
+                        for (int e = 0; e < 32; ++e)
                             o[e] = 0.0f;
                     }
                     if (rr < u.rows) {
 #pragma unroll
-                        for (int e = 0; e < D; e += 8)
-                            *reinterpret_cast<uint4 *>(out + e) = make_uint4(
+                        for (int e = 0; e < 32; e += 8)
+                            *reinterpret_cast<uint4 *>(out + 32 * c + e) = make_uint4(
                                 pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
                                 pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
                     }
                 }
-                tmem_fence_before();
+                tmem_fence_before();   // the next unit's first p_full orders these reads before its O
             }
-            __syncthreads();
-            if (sm.gave_up)
-                break;
+            unit_over(n);
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp < kSoftWarps + kKWarps) {
             // ============================================================ K tiles
             // A warp takes 8 tokens (half a blob) at a time: lane t + 4 k has words t of token
-            // (k & 1) * 4 + (k >> 1), so that eight lanes' 16-byte stores meet all banks
-            constexpr int kItems = (2 * kBlobs + kKWarps - 1) / kKWarps;
+            // (k & 1) * 4 + (k >> 1), so that eight lanes' 16-byte stores meet all banks. The first
+            // of the warps also finds the units, one ahead.
+            constexpr int kItems = (2 * kBlobs + kKWarps - 1) / kKWarps, kAhead = 3;   // items on their way
+            static_assert(kItems % kAhead == 0, "an item keeps its place");
             const int wi = warp - kSoftWarps, t = lane & 3, k8 = lane >> 2;
             const int half_tok = (k8 & 1) * 4 + (k8 >> 1);
-            for (int un = 0;; un ^= 1) {
-                const Unit &u = sm.unit[un];
-                if (!u.there)
-                    break;
+            int u_r0 = 0;
+            int64_t u_before = 0;
+            auto find = [&](uint32_t which) {
+                const uint32_t slot = which % kUnits;
+                if (!wait_all(&sm.u_empty[slot], (which / kUnits & 1) ^ 1))
+                    return;
+                find_unit(p, blockIdx.x + (int64_t)which * gridDim.x, &u_r0, &u_before, &sm.unit[slot]);
+                if (lane == 0)
+                    bar_arrive(&sm.u_full[slot]);
+                __syncwarp();
+            };
+            if (wi == 0)
+                find(0);
+            while (const Unit *up = next_unit()) {
+                const Unit &u = *up;
                 const int32_t *table = p.a.block_table + u.r * p.a.table_stride;
-                const int n = u.n, nb = u.nb, h = u.h;
+                const int n = u.n, h = u.h;
+                uint32_t code[kAhead][NW], par[kAhead][NG];   // item it in place it % kAhead
+                Lookup look = {-1, 0};
+                uint32_t now, then;  // the lane's blob of this tile and the next
+                uint32_t bad;        // this tile's blobs whose page id is outside the cache
+                auto load = [&](uint32_t place, int k, int it) {
+                    const int item = wi + kKWarps * it, tok = 8 * (item & 1) + half_tok;
+                    const uint32_t at = __shfl_sync(0xFFFFFFFFu, place, item >> 1 & 7);
+                    const bool there = item < 2 * kBlobs && at != ~0u;
+                    const uint8_t *blob = p.layer + (uint64_t)at * 128;
+                    load_or_zero(code[k], blob + B::kKCodes + tok * (D / 2) + t * (D / 8), there);
+                    load_or_zero(par[k], blob + B::kKParams + tok * 4 * NG, there);
+                };
+                auto is_bad = [&](uint32_t place, int j) {
+                    return __ballot_sync(0xFFFFFFFFu, place == ~0u && j * kBlobs + (lane & 7) < u.nb) & 0xFFu;
+                };
+                look.start(u, table, bpp, 0);
+                now = look.place<B>(p, h, bpp);
+                bad = is_bad(now, 0);
+                look.start(u, table, bpp, 1);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    load(now, k, k);
+                if (wi == 0 && n == 0)
+                    find(un + 1);
                 for (int j = 0; j < n; ++j) {
-                    uint32_t code[kItems][NW], par[kItems][NG];
-#pragma unroll
-                    for (int it = 0; it < kItems; ++it) {
-                        const int item = wi + kKWarps * it, vb = j * kBlobs + (item >> 1);
-                        const int tok = 8 * (item & 1) + half_tok;
-                        int id = -1, ab = 0;
-                        if (item < 2 * kBlobs && vb < nb) {
-                            ab = u.blob(vb);
-                            id = table[ab / bpp];
-                        }
-                        const bool there = (unsigned)id < (unsigned)p.num_pages;
-                        const uint8_t *blob =
-                            p.layer + (((size_t)(there ? id : 0) * p.heads + h) * bpp + ab % bpp) * B::kBytes;
-                        load_or_zero(code[it], blob + B::kKCodes + tok * (D / 2) + t * (D / 8), there);
-                        load_or_zero(par[it], blob + B::kKParams + tok * 4 * NG, there);
-                    }
                     const uint32_t use = tiles_done + j, sl = use & 1;
-                    if (!wait_or_leave(&sm.k_empty[sl], (use >> 1 & 1) ^ 1, &sm.gave_up, p.status))
+                    if (!wait_all(&sm.k_empty[sl], (use >> 1 & 1) ^ 1))
                         break;
+                    if (wi == 0 && lane == 0) {
+                        *reinterpret_cast<volatile uint32_t *>(&sm.bad[use & 3]) = bad;
+                        if (bad)
+                            int4_set_status(p.status, CG_ERR_CORRUPT);
+                    }
+                    then = look.place<B>(p, h, bpp);
+                    bad = is_bad(then, j + 1);
+                    look.start(u, table, bpp, j + 2);
+#pragma unroll 1
+                    for (int round = 0; round < kItems; round += kAhead) {
 #pragma unroll
-                    for (int it = 0; it < kItems; ++it) {
-                        const int item = wi + kKWarps * it, at = 8 * item + half_tok;
-                        if (item >= 2 * kBlobs)
-                            break;
+                        for (int k = 0; k < kAhead; ++k) {
+                            const int item = wi + kKWarps * (round + k), at = 8 * item + half_tok;
+                            uint32_t cd[NW], pw[NG];
 #pragma unroll
-                        for (int w = 0; w < NW; ++w) {
-                            const uint32_t pw = par[it][w / WPG];
-                            const uint32_t s2 = __byte_perm(pw, pw, 0x1010), lo2 = __byte_perm(pw, pw, 0x3232);
-                            const uint4 o =
-                                make_uint4(expand(code[it][w], 0, s2, lo2), expand(code[it][w], 1, s2, lo2),
-                                           expand(code[it][w], 2, s2, lo2), expand(code[it][w], 3, s2, lo2));
-                            const int c = 4 * w + t;
-                            *reinterpret_cast<uint4 *>(sm.k[sl] + (c >> 3) * kQSub + at * 128 +
-                                                       (((c & 7) ^ (at & 7)) << 4)) = o;
+                            for (int w = 0; w < NW; ++w)
+                                cd[w] = code[k][w];
+#pragma unroll
+                            for (int gi = 0; gi < NG; ++gi)
+                                pw[gi] = par[k][gi];
+                            const bool same = round + kAhead < kItems;   // the next one in this place: of this tile?
+                            load(same ? now : then, k, same ? round + kAhead + k : k);
+                            if (item < 2 * kBlobs) {
+#pragma unroll
+                                for (int w = 0; w < NW; ++w) {
+                                    const uint32_t q = pw[w / WPG];
+                                    const uint32_t s2 = __byte_perm(q, q, 0x1010), lo2 = __byte_perm(q, q, 0x3232);
+                                    const uint4 o = make_uint4(expand(cd[w], 0, s2, lo2), expand(cd[w], 1, s2, lo2),
+                                                               expand(cd[w], 2, s2, lo2), expand(cd[w], 3, s2, lo2));
+                                    const int c = 4 * w + t;
+                                    *reinterpret_cast<uint4 *>(sm.k[sl] + (c >> 3) * kQSub + at * 128 +
+                                                               (((c & 7) ^ (at & 7)) << 4)) = o;
+                                }
+                            }
                         }
                     }
+                    now = then;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     bar_arrive(&sm.k_full[sl]);
+                    if (wi == 0 && j == 0)
+                        find(un + 1);
                 }
-                tiles_done += n;
-                __syncwarp();
-                __syncthreads();
-                if (sm.gave_up)
-                    break;
+                unit_over(n);
             }
         } else if (warp < kSoftWarps + kKWarps + kVWarps) {
-            // ============================================================ V tiles
-            // A thread takes half a blob (8 tokens: pairs 4 hf .. 4 hf + 3) at words g: channels
-            // 32 w + 4 g + i; eight lanes with the same g store to different 16-byte columns
-            const int wi = warp - kSoftWarps - kKWarps;
-            const int pg = 8 * (wi & 1) + (lane & 7), g = 4 * (wi >> 1) + (lane >> 3), hf = pg & 1;
-            for (int un = 0;; un ^= 1) {
-                const Unit &u = sm.unit[un];
-                if (!u.there)
-                    break;
+            // ================================================== queries and V tiles
+            // A thread takes words (g, w) of half a blob's 4 token pairs at a time: channels 32 w + 4 g
+            // + i. Eight lanes with the same g and w store to different 16-byte columns.
+            // kAhead words are on their way while one is expanded.
+            constexpr int kAhead = 2;
+            static_assert(NW % kAhead == 0 && 16 * 8 == 32 * kVWarps, "one (pg, g0) to a thread");
+            const int wi = warp - kSoftWarps - kKWarps, vt = 32 * wi + lane;
+            const int pg = 8 * (wi & 1) + (lane & 7), hf = pg & 1, g0 = 4 * (wi >> 1) + (lane >> 3);
+            const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+            while (const Unit *up = next_unit()) {
+                const Unit &u = *up;
                 const int32_t *table = p.a.block_table + u.r * p.a.table_stride;
-                const int n = u.n, nb = u.nb, h = u.h, kv = u.kv;
-                for (int j = 0; j < n; ++j) {
-                    uint32_t code[4][NW], par[8][NG];
-                    const int vb = j * kBlobs + (pg >> 1);
-                    int id = -1, ab = 0;
-                    if (vb < nb) {
-                        ab = u.blob(vb);
-                        id = table[ab / bpp];
+                const int n = u.n, h = u.h, kv = u.kv;
+                Lookup look = {-1, 0};
+                look.start(u, table, bpp, 0);
+                if (!wait_all(&sm.q_empty, (un & 1) ^ 1))   // the last unit's scores are done
+                    break;
+                {
+                    constexpr int kC = D / 8, kStep = 32 * kVWarps / kC;   // rows apart
+                    const int c = vt % kC;
+                    int in = vt / kC;
+                    int qt = (u.row0 + in) / p.ratio, qr = (u.row0 + in) - qt * p.ratio;
+                    const int step_t = kStep / p.ratio, step_r = kStep - step_t * p.ratio;
+                    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.a.q) +
+                                             (int64_t)u.q_row0 * p.a.q_token_stride +
+                                             (int64_t)h * p.ratio * p.a.q_head_stride + 8 * c;
+                    const int end = 128 * u.tiles_q, rows = u.rows - u.row0;
+                    while (in < end) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            v[e] = in + e * kStep < rows
+                                       ? *reinterpret_cast<const uint4 *>(q + qt * p.a.q_token_stride +
+                                                                          qr * p.a.q_head_stride)
+                                       : make_uint4(0, 0, 0, 0);
+                            qt += step_t;
+                            qr += step_r;
+                            if (qr >= p.ratio) {
+                                qr -= p.ratio;
+                                ++qt;
+                            }
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e, in += kStep)
+                            *reinterpret_cast<uint4 *>(sm.q[in >> 7] + (c >> 3) * kQSub + (in & 127) * 128 +
+                                                       (((c & 7) ^ (in & 7)) << 4)) =
+                                make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410) ^ flip,
+                                           __byte_perm(v[e].x, v[e].z, 0x7632) ^ flip,
+                                           __byte_perm(v[e].y, v[e].w, 0x5410) ^ flip,
+                                           __byte_perm(v[e].y, v[e].w, 0x7632) ^ flip);
                     }
-                    const bool there = (unsigned)id < (unsigned)p.num_pages;
-                    const uint8_t *blob =
-                        p.layer + (((size_t)(there ? id : 0) * p.heads + h) * bpp + ab % bpp) * B::kBytes;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    bar_arrive(&sm.q_full);
+                }
+                uint32_t code[kAhead][4], par[kAhead][8];   // word w of (pg, g0) in place w % kAhead
+                struct Half {        // the thread's half blob in a tile
+                    uint32_t at;
+                    int left;        // tokens of it that are there
+                } now, then;
+                auto take = [&](Half &f) {
+                    f.at = __shfl_sync(0xFFFFFFFFu, look.place<B>(p, h, bpp), pg >> 1);
+                    const int blob = __shfl_sync(0xFFFFFFFFu, look.blob, pg >> 1);
+                    f.left = f.at == ~0u ? 0 : kv - 16 * blob - 8 * hf;
+                };
+                auto load = [&](const Half &f, int k, int w) {
+                    const uint8_t *blob = p.layer + (uint64_t)f.at * 128;
+                    const uint32_t *c = reinterpret_cast<const uint32_t *>(blob + B::kVCodes + 4 * hf * D +
+                                                                           g0 * (D / 8)) + w;
+                    const uint32_t *q = reinterpret_cast<const uint32_t *>(blob + B::kVParams) + 8 * hf * NG + w / WPG;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        load_or_zero(code[e], blob + B::kVCodes + (4 * hf + e) * D + g * (D / 8), there);
+                        code[k][e] = f.left > 0 ? c[e * (D / 4)] : 0;
                     // tokens that are not there get 0, whatever the cache holds in their place
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        load_or_zero(par[e], blob + B::kVParams + (8 * hf + e) * 4 * NG,
-                                     there && 16 * ab + 8 * hf + e < kv);
+                        par[k][e] = e < f.left ? q[e * NG] : 0;
+                };
+                take(now);
+                look.start(u, table, bpp, 1);
+#pragma unroll
+                for (int k = 0; k < kAhead; ++k)
+                    load(now, k, k);
+                for (int j = 0; j < n; ++j) {
                     const uint32_t use = tiles_done + j, sl = use & 1;
-                    if (!wait_or_leave(&sm.v_empty[sl], (use >> 1 & 1) ^ 1, &sm.gave_up, p.status))
+                    if (!wait_all(&sm.v_empty[sl], (use >> 1 & 1) ^ 1))
                         break;
+                    take(then);      // of tile j + 1
+                    look.start(u, table, bpp, j + 2);
+#pragma unroll 1
+                    for (int round = 0; round < NW; round += kAhead) {
 #pragma unroll
-                    for (int gi = 0; gi < NG; ++gi) {
-                        uint32_t s2[4], lo2[4];
+                        for (int k = 0; k < kAhead; ++k) {
+                            uint32_t s2[4], lo2[4], cd[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            s2[e] = __byte_perm(par[2 * e][gi], par[2 * e + 1][gi], 0x5410);
-                            lo2[e] = __byte_perm(par[2 * e][gi], par[2 * e + 1][gi], 0x7632);
-                        }
-#pragma unroll
-                        for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+                            for (int e = 0; e < 4; ++e) {
+                                s2[e] = __byte_perm(par[k][2 * e], par[k][2 * e + 1], 0x5410);
+                                lo2[e] = __byte_perm(par[k][2 * e], par[k][2 * e + 1], 0x7632);
+                                cd[e] = code[k][e];
+                            }
+                            const bool same = round + kAhead < NW;
+                            load(same ? now : then, k, same ? round + kAhead + k : k);
 #pragma unroll
                             for (int c = 0; c < 4; ++c) {
-                                const uint4 o = make_uint4(
-                                    expand(code[0][w], c, s2[0], lo2[0]), expand(code[1][w], c, s2[1], lo2[1]),
-                                    expand(code[2][w], c, s2[2], lo2[2]), expand(code[3][w], c, s2[3], lo2[3]));
-                                const int at = 32 * w + 4 * g + c;
-                                *reinterpret_cast<uint4 *>(sm.v[sl] + (pg >> 3) * kVSub + at * 128 +
-                                                           (((pg & 7) ^ (at & 7)) << 4)) = o;
+                                const uint4 o =
+                                    make_uint4(expand(cd[0], c, s2[0], lo2[0]), expand(cd[1], c, s2[1], lo2[1]),
+                                               expand(cd[2], c, s2[2], lo2[2]), expand(cd[3], c, s2[3], lo2[3]));
+                                const int row = 32 * (round + k) + 4 * g0 + c;
+                                *reinterpret_cast<uint4 *>(sm.v[sl] + (pg >> 3) * kVSub + row * 128 +
+                                                           (((pg & 7) ^ (row & 7)) << 4)) = o;
                             }
+                        }
                     }
+                    now = then;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     bar_arrive(&sm.v_full[sl]);
                 }
-                tiles_done += n;
-                __syncwarp();
-                __syncthreads();
-                if (sm.gave_up)
-                    break;
+                unit_over(n);
             }
         } else {
             // ========================================================== products
             const uint32_t q_at = smem_addr(sm.q[0]), k_at = smem_addr(sm.k[0]), v_at = smem_addr(sm.v[0]);
             auto scores = [&](int i, uint32_t sl) {
-                const uint64_t a = smem_desc(q_at + i * (kTile * D * 2)), b = smem_desc(k_at + sl * (kTile * D * 2));
-#pragma unroll
+                const uint32_t a = smem_desc(q_at + i * (kTile * D * 2)), b = smem_desc(k_at + sl * (kTile * D * 2));
+#pragma unroll 1
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * kQSub + (kk & 3) * 32) >> 4;
-                    mma_ss(tmem + 128 * i, a + off, b + off, mma_desc(kTile), kk > 0);
+                    mma_ss(kS + 128 * i, a + off, b + off, mma_desc(kTile), kk > 0);
                 }
                 mma_commit(&sm.s_full[i]);
             };
-            uint32_t p_done[2] = {0, 0}, units = 0;
-            for (int un = 0;; un ^= 1) {
-                const Unit &u = sm.unit[un];
-                if (!u.there)
-                    break;
-                const int n = u.n, tiles_q = u.tiles_q;
+            uint32_t p_done = 0;     // parity of each row tile's p_full
+            while (const Unit *up = next_unit()) {
+                const int n = up->n, tiles_q = up->tiles_q;
                 if (lane == 0) {
-                    alive = wait_or_leave(&sm.q_full, units & 1, &sm.gave_up, p.status);
+                    bool alive = wait(&sm.q_full, un & 1);
                     uint32_t use = tiles_done;
+                    if (n == 0)
+                        bar_arrive(&sm.q_empty);
+                    else if (alive)
+                        alive = wait(&sm.k_full[use & 1], use >> 1 & 1);
                     if (alive && n > 0) {
-                        alive = wait_or_leave(&sm.k_full[use & 1], use >> 1 & 1, &sm.gave_up, p.status);
-                        if (alive) {
-                            tmem_fence_after();
-                            for (int i = 0; i < tiles_q; ++i)
-                                scores(i, use & 1);
-                            mma_commit(&sm.k_empty[use & 1]);
-                        }
+                        tmem_fence_after();
+                        scores(0, use & 1);
+                        if (tiles_q > 1)
+                            scores(1, use & 1);
+                        mma_commit(&sm.k_empty[use & 1]);
+                        if (n == 1)
+                            mma_commit(&sm.q_empty);
                     }
                     for (int j = 0; j < n && alive; ++j, ++use) {
                         const uint32_t sl = use & 1, nx = use + 1;
+                        const uint32_t b = smem_desc(v_at + sl * (kTile * D * 2));
+#pragma unroll 1
                         for (int i = 0; i < tiles_q; ++i) {
-                            alive = wait_or_leave(&sm.p_full[i], p_done[i] & 1, &sm.gave_up, p.status);
-                            ++p_done[i];
+                            alive = wait(&sm.p_full[i], p_done >> i & 1);
+                            p_done ^= 1u << i;
                             if (alive && i == 0)
-                                alive = wait_or_leave(&sm.v_full[sl], use >> 1 & 1, &sm.gave_up, p.status);
+                                alive = wait(&sm.v_full[sl], use >> 1 & 1);
                             if (alive && i == 0 && j + 1 < n)
-                                alive = wait_or_leave(&sm.k_full[nx & 1], nx >> 1 & 1, &sm.gave_up, p.status);
+                                alive = wait(&sm.k_full[nx & 1], nx >> 1 & 1);
                             if (!alive)
                                 break;
                             tmem_fence_after();
-                            const uint64_t b = smem_desc(v_at + sl * (kTile * D * 2));
-#pragma unroll
+#pragma unroll 1
                             for (int kk = 0; kk < kTile / 16; ++kk)
-                                mma_ts(tmem + kO + 128 * i, tmem + 128 * i + 8 * kk,
+                                mma_ts(kO + 128 * i, kS + 128 * i + 8 * kk,
                                        b + (((kk >> 2) * kVSub + (kk & 3) * 32) >> 4), mma_desc(D), j > 0 || kk > 0);
                             if (i + 1 == tiles_q)
                                 mma_commit(&sm.v_empty[sl]);
                             if (j + 1 < n)
                                 scores(i, nx & 1);
                             else
-                                mma_commit(&sm.s_full[i]);   // O is complete
+                                mma_commit(&sm.o_full[i]);
                         }
                         if (alive && j + 1 < n)
                             mma_commit(&sm.k_empty[nx & 1]);
+                        if (alive && j + 2 == n)
+                            mma_commit(&sm.q_empty);
                     }
                 }
-                __syncwarp();
-                tiles_done += n;
-                ++units;
-                u_next += gridDim.x;
-                find_unit(p, u_next, &u_r0, &u_before, &sm.unit[un ^ 1]);
-                __syncthreads();
-                if (sm.gave_up)
-                    break;
+                unit_over(n);
             }
             // products still in flight (after a wait that ran out) end before the memory goes
             if (sm.gave_up && lane == 0) {
-                bar_init(&sm.q_full, 1);
-                bar_init_fence();
-                mma_commit(&sm.q_full);
-                bar_wait(&sm.q_full, 0);
+                mma_commit(&sm.last);
+                bar_wait(&sm.last, 0);
             }
             __syncwarp();
         }
@@ -712,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
     __syncthreads();
     if (warp == kWarps - 1) {
         tmem_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
     }
 }
 

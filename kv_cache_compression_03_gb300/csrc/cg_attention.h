@@ -78,24 +78,45 @@ __device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t b
         : "memory");
 }
 
-// Polls before a wait gives up; each may suspend the thread for a while.
-constexpr uint32_t kBarWaitLimit = 1u << 20;
+// A wait gives up after a second. *leave (if given) is looked at as well: set,
+// the wait ends at once. Each poll may suspend the thread for a while.
+constexpr uint64_t kBarWaitNs = 1000000000ull;
+
+__device__ __forceinline__ bool bar_poll(uint32_t at, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(at), "r"(parity)
+        : "memory");
+    return done;
+}
+
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+
+__device__ __forceinline__ bool bar_wait_long(uint32_t at, uint32_t parity, volatile uint32_t *leave)
+{
+    const uint64_t start = now_ns();
+    do {
+        if (bar_poll(at, parity))
+            return true;
+        if (leave != nullptr && *leave)
+            return false;
+    } while (now_ns() - start < kBarWaitNs);
+    return false;
+}
 
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
 {
     const uint32_t at = smem_addr(bar);
-    for (uint32_t i = 0; i < kBarWaitLimit; ++i) {
-        uint32_t done;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(done)
-            : "r"(at), "r"(parity)
-            : "memory");
-        if (done)
-            return true;
-    }
-    return false;
+    return bar_poll(at, parity) || bar_wait_long(at, parity, nullptr);
 }
 
 // ------------------------------------------------------------------ launches

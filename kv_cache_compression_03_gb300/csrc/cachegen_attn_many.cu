@@ -71,6 +71,15 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         : "memory");
 }
 
+// One lane of the warp, chosen in a way that the compiler knows to be one lane:
+// the branch that it takes then needs no care for others at each product.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one;
+}
+
 // The barrier is arrived on once all products issued so far are done.
 __device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
@@ -758,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
             const uint32_t q_at = smem_addr(sm.q[0]), k_at = smem_addr(sm.k[0]), v_at = smem_addr(sm.v[0]);
             auto scores = [&](int i, uint32_t sl) {
                 const uint32_t a = smem_desc(q_at + i * (kTile * D * 2)), b = smem_desc(k_at + sl * (kTile * D * 2));
-#pragma unroll 1
+#pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * kQSub + (kk & 3) * 32) >> 4;
                     mma_ss(kS + 128 * i, a + off, b + off, mma_desc(kTile), kk > 0);
@@ -768,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
             uint32_t p_done = 0;     // parity of each row tile's p_full
             while (const Unit *up = next_unit()) {
                 const int n = up->n, tiles_q = up->tiles_q;
-                if (lane == 0) {
+                if (elect_one()) {
                     bool alive = wait(&sm.q_full, un & 1);
                     uint32_t use = tiles_done;
                     if (n == 0)
@@ -798,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                             if (!alive)
                                 break;
                             tmem_fence_after();
-#pragma unroll 1
+#pragma unroll
                             for (int kk = 0; kk < kTile / 16; ++kk)
                                 mma_ts(kO + 128 * i, kS + 128 * i + 8 * kk,
                                        b + (((kk >> 2) * kVSub + (kk & 3) * 32) >> 4), mma_desc(D), j > 0 || kk > 0);

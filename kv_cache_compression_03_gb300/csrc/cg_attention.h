@@ -103,14 +103,20 @@ __device__ __forceinline__ uint64_t now_ns()
 
 __device__ __forceinline__ bool bar_wait_long(uint32_t at, uint32_t parity, volatile uint32_t *leave)
 {
-    const uint64_t start = now_ns();
-    do {
+    uint64_t start = 0;
+    for (uint32_t i = 0;; ++i) {
         if (bar_poll(at, parity))
             return true;
+        if ((i & 63) != 63)   // the clock is looked at now and then
+            continue;
         if (leave != nullptr && *leave)
             return false;
-    } while (now_ns() - start < kBarWaitNs);
-    return false;
+        const uint64_t now = now_ns();
+        if (start == 0)
+            start = now;
+        else if (now - start > kBarWaitNs)
+            return false;
+    }
 }
 
 __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)

@@ -15,8 +15,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as ct
-import functools
 import os
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -163,15 +163,14 @@ def _open(path: str) -> ct.CDLL:
         "cg_int8_encode": (st, [P, ct.c_int64, ct.c_int32, P, P, P, P]),
         "cg_int8_decode": (st, [P, P, ct.c_int64, ct.c_int32, P, P]),
         "cg_int4_cache_bytes": (st, [ct.POINTER(cg_int4_cache), ct.POINTER(sz)]),
-        "cg_int4_store": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, ct.c_int32,
-                               ct.POINTER(cg_kv_rows), P, ct.c_int64, P]),
-        "cg_int4_load": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, ct.c_int32,
-                              ct.POINTER(cg_kv_rows), P, ct.c_int64, P]),
-        "cg_pages_grow": (st, [ct.POINTER(cg_page_batch), P]),
-        "cg_int4_attention_workspace": (st, [ct.POINTER(cg_int4_cache), ct.POINTER(cg_attention),
-                                             ct.POINTER(sz)]),
-        "cg_int4_attention": (st, [ct.POINTER(cg_int4_cache), ct.c_int32,
-                                   ct.POINTER(cg_attention), P, sz, P]),
+        # the structs of rows, batches and attention calls come as packed bytes
+        "cg_int4_store": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, ct.c_int32, P, P,
+                               ct.c_int64, P]),
+        "cg_int4_load": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, ct.c_int32, P, P,
+                              ct.c_int64, P]),
+        "cg_pages_grow": (st, [P, P]),
+        "cg_int4_attention_workspace": (st, [ct.POINTER(cg_int4_cache), P, ct.POINTER(sz)]),
+        "cg_int4_attention": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, P, P, sz, P]),
         "cg_profile_enable": (st, [P, ct.c_int32]),
         "cg_profile_read": (st, [P, ct.POINTER(cg_kernel_profile), ct.c_int32,
                                  ct.POINTER(ct.c_int32)]),
@@ -590,38 +589,44 @@ class Codec:
 
 
 # ---------------------------------------------- paged cache held in 4 bits
+# These calls run once per layer and decode step, where a microsecond of Python
+# is a microsecond of the step: checks are written out on plain tuples, and the
+# structs of the C calls are packed in one go (their layout is asserted here).
 
-def _on_device(fn):
-    """Run a method or function of the paged cache on the stream given as
-    stream= (its temporaries and outputs are then allocated there too)."""
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        import torch
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
+_ROWS = struct.Struct("@PPqqqqqq")
+_BATCH = struct.Struct("@PqiiPPPPiiiPPPPqP")
+_ATTENTION = struct.Struct("@PqqPqqPPPqiiiiiiif")
+assert _ROWS.size == ct.sizeof(cg_kv_rows) and _BATCH.size == ct.sizeof(cg_page_batch) and \
+    -(-_ATTENTION.size // 8) * 8 == ct.sizeof(cg_attention)
+
+
+def _on_stream(stream, fn, *args, **kw):
+    """fn(*args, **kw) with `stream` current: its temporaries and outputs are
+    then that stream's too."""
+    import torch
+    with torch.cuda.stream(stream):
+        return fn(*args, **kw)
 
 
 class _Launch:
-    """The current stream of a device, with that device made current while
-    the call is enqueued."""
-    __slots__ = ("device", "back")
+    """The current stream of a device (its index), with that device made
+    current while a call is enqueued."""
+    __slots__ = ("index", "back")
 
-    def __init__(self, device):
-        self.device = device
+    def __init__(self, index):
+        self.index = index
 
     def __enter__(self):
         import torch
-        now = torch.cuda.current_device()
-        self.back = now if now != self.device.index else None
-        if self.back is not None:
-            torch.cuda.set_device(self.device)
-        return torch.cuda.current_stream(self.device).cuda_stream
+        now = torch._C._cuda_getDevice()
+        self.back = -1
+        if now != self.index:
+            torch.cuda.set_device(self.index)
+            self.back = now
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        if self.back is not None:
+        if self.back >= 0:
             import torch
             torch.cuda.set_device(self.back)
 
@@ -631,43 +636,52 @@ def _need(cond, what: str):
         raise ValueError(what)
 
 
-def _ints(t, device, shape, what: str):
-    """A contiguous int32 tensor of the given shape on the device."""
+def _ints(t, device, shape, what: str) -> int:
+    """The address of a contiguous int32 tensor of the given shape on the device."""
     import torch
-    _need(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and
-          tuple(t.shape) == shape and t.is_contiguous(),
-          f"{what} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape and
+            t.device == device and t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+    return t.data_ptr()
 
 
 def _table(t, device, what: str):
+    """(requests, entries of a row, elements between rows) of a block table."""
     import torch
-    _need(isinstance(t, torch.Tensor) and t.dtype == torch.int32 and t.device == device and
-          t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1) and
-          (t.stride(0) >= t.shape[1] or t.shape[0] <= 1),
-          f"{what} must be an int32 tensor [requests, pages] on {device}, a row's entries adjacent")
-
-
-def _stride(t, dim: int) -> int:
-    return t.stride(dim) if t.shape[dim] > 1 else 0
+    if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device and t.dim() == 2:
+        n, width = t.shape
+        s0, s1 = t.stride()
+        if (s1 == 1 or width <= 1) and (s0 >= width or n <= 1):
+            return n, width, s0 if n > 1 else width
+    raise ValueError(f"{what} must be an int32 tensor [requests, pages] on {device}, a row's "
+                     f"entries adjacent")
 
 
 def _bf16_rows(t, device, shape, what: str, written: bool):
-    """A bf16 tensor [.., head_size] of the given shape whose rows the
-    kernels can read (and, when written, that do not overlap)."""
+    """(address, strides but the last) of a bf16 tensor [.., head_size] of the
+    given shape whose rows the kernels can read (and, when written, that do
+    not overlap). A dimension of one element counts stride 0."""
     import torch
-    _need(isinstance(t, torch.Tensor) and t.dtype == torch.bfloat16 and t.device == device and
-          tuple(t.shape) == shape, f"{what} must be a bf16 tensor of shape {list(shape)} on {device}")
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and
+            t.device == device):
+        raise ValueError(f"{what} must be a bf16 tensor of shape {list(shape)} on {device}")
+    ptr, strides = t.data_ptr(), t.stride()
+    last = strides[-1]
+    strides = [s if n > 1 else 0 for s, n in zip(strides[:-1], shape)]
     if t.numel() == 0:
-        return
-    _need(t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and
-          all(s % 8 == 0 for s, n in zip(t.stride()[:-1], shape) if n > 1),
-          f"{what}: channels must be adjacent, rows 16-byte aligned")
+        return ptr, strides
+    bits = ptr >> 1
+    for s in strides:
+        bits |= s
+    if last != 1 or bits & 7:
+        raise ValueError(f"{what}: channels must be adjacent, rows 16-byte aligned")
     if written:
         # each dimension steps over everything inside the smaller ones
-        inner = t.shape[-1]
-        for s, n in sorted((s, n) for s, n in zip(t.stride()[:-1], shape) if n > 1):
+        inner = shape[-1]
+        for s, n in sorted((s, n) for s, n in zip(strides, shape) if n > 1):
             _need(s >= inner, f"{what}: rows overlap")
-            inner = s * (n - 1) + inner
+            inner += s * (n - 1)
+    return ptr, strides
 
 
 @dataclass
@@ -687,9 +701,8 @@ class PagePlan:
         _check(st, "cg_pages_grow (device)")
 
 
-@_on_device
 def grow_pages(block_table, lens, counts, free_pages, free_count, page_tokens: int, tokens: int,
-               num_pages: int | None = None, out: PagePlan | None = None) -> PagePlan:
+               num_pages: int | None = None, out: PagePlan | None = None, stream=None) -> PagePlan:
     """Pages and slots of a batch's new tokens (cg_pages_grow in
     include/cachegen.h). block_table int32 [requests, width] gets the ids of
     the pages taken; lens and counts are int32 [requests] (tokens held, tokens
@@ -700,38 +713,40 @@ def grow_pages(block_table, lens, counts, free_pages, free_count, page_tokens: i
     earlier plan; its lens and free_count may be the lens and free_count passed
     in (a captured decode loop then advances in place). Enqueues and returns:
     the caller's own check is PagePlan.check()."""
+    if stream is not None:
+        return _on_stream(stream, grow_pages, block_table, lens, counts, free_pages, free_count,
+                          page_tokens, tokens, num_pages, out)
     import torch
     _need(isinstance(lens, torch.Tensor) and lens.is_cuda, "lens must be a CUDA tensor")
     dev = lens.device
     n = lens.shape[0] if lens.dim() == 1 else -1
-    _ints(lens, dev, (n,), "lens")
-    _ints(counts, dev, (n,), "counts")
-    _table(block_table, dev, "block_table")
-    _need(block_table.shape[0] == n, "block_table must have one row per request")
-    _ints(free_pages, dev, (free_pages.numel(),), "free_pages")
-    _ints(free_count, dev, (1,), "free_count")
+    lens_at, counts_at = _ints(lens, dev, (n,), "lens"), _ints(counts, dev, (n,), "counts")
+    rows, width, stride = _table(block_table, dev, "block_table")
+    _need(rows == n, "block_table must have one row per request")
+    capacity = free_pages.numel()
+    free_at = _ints(free_pages, dev, (capacity,), "free_pages")
+    nfree_at = _ints(free_count, dev, (1,), "free_count")
     tokens = int(tokens)
     _need(tokens >= 0 and page_tokens > 0, "tokens must not be negative, page_tokens positive")
     if out is None:
-        e = functools.partial(torch.empty, dtype=torch.int32, device=dev)
-        out = PagePlan(e(tokens), e(n + 1), e(n), e(1),
-                       torch.empty(16, dtype=torch.uint8, device=dev))
+        e, i32 = torch.empty, torch.int32
+        out = PagePlan(e(tokens, dtype=i32, device=dev), e(n + 1, dtype=i32, device=dev),
+                       e(n, dtype=i32, device=dev), e(1, dtype=i32, device=dev),
+                       e(16, dtype=torch.uint8, device=dev))
     else:
         _ints(out.slots, dev, (tokens,), "out.slots")
         _ints(out.cu, dev, (n + 1,), "out.cu")
         _ints(out.lens, dev, (n,), "out.lens")
         _ints(out.free_count, dev, (1,), "out.free_count")
         _check_status_buffer(out.status, "grow_pages")
-    if num_pages is None:
-        num_pages = 0x7FFFFFFF // page_tokens
-    b = cg_page_batch(block_table.data_ptr(), block_table.stride(0) if n > 1 else
-                      block_table.shape[1], block_table.shape[1], n, lens.data_ptr(),
-                      counts.data_ptr(), free_pages.data_ptr(), free_count.data_ptr(),
-                      free_pages.shape[0], num_pages, page_tokens, out.cu.data_ptr(),
-                      out.lens.data_ptr(), out.free_count.data_ptr(), out.slots.data_ptr(), tokens,
-                      out.status.data_ptr())
-    with _Launch(dev) as s:
-        _check(load().cg_pages_grow(ct.byref(b), s), "cg_pages_grow")
+        _need(out.status.device == dev, "out.status must be on the same device")
+    b = _BATCH.pack(block_table.data_ptr(), stride, width, n, lens_at, counts_at, free_at, nfree_at,
+                    capacity, 0x7FFFFFFF // page_tokens if num_pages is None else num_pages,
+                    page_tokens, out.cu.data_ptr(), out.lens.data_ptr(), out.free_count.data_ptr(),
+                    out.slots.data_ptr(), tokens, out.status.data_ptr())
+    with _Launch(dev.index) as s:
+        st = (_lib or load()).cg_pages_grow(b, s)
+    _check(st, "cg_pages_grow")
     return out
 
 
@@ -768,39 +783,40 @@ class Int4Cache:
         shape = (tokens, self.num_heads, self.head_size)
         if layers is not None:
             shape = (layers,) + shape
-        _bf16_rows(k, self.device, shape, "k", written)
-        _bf16_rows(v, self.device, shape, "v", written)
-        ks = [_stride(k, i) for i in range(k.dim() - 1)]
-        vs = [_stride(v, i) for i in range(v.dim() - 1)]
+        k_at, ks = _bf16_rows(k, self.device, shape, "k", written)
+        v_at, vs = _bf16_rows(v, self.device, shape, "v", written)
         if layers is None:
-            ks, vs = [0] + ks, [0] + vs
-        return cg_kv_rows(k.data_ptr(), v.data_ptr(), *ks, *vs)
+            return _ROWS.pack(k_at, v_at, 0, *ks, 0, *vs)
+        return _ROWS.pack(k_at, v_at, *ks, *vs)
 
-    @_on_device
-    def store(self, k, v, slots, layer: int = 0) -> None:
+    def store(self, k, v, slots, layer: int = 0, stream=None) -> None:
         """Quantise rows k, v (bf16 [tokens, heads, head_size] into one layer,
         or [layers, tokens, heads, head_size] into layers from ``layer`` on;
         kv[:, 0] and kv[:, 1] of Codec.decode's output fit) into the slots
         (int32 [tokens]; -1 skips a token, no other slot may occur twice)."""
-        _need(k.dim() in (3, 4) and k.shape == v.shape,
-              "k and v must have the same shape, [tokens, heads, head_size] with or without layers")
-        tokens, layers = k.shape[-3], k.shape[0] if k.dim() == 4 else None
+        if stream is not None:
+            return _on_stream(stream, self.store, k, v, slots, layer)
+        shape = k.shape
+        _need(len(shape) in (3, 4), "k must be [tokens, heads, head_size], with or without layers")
+        tokens, layers = shape[-3], shape[0] if len(shape) == 4 else None
         rows = self._rows(k, v, tokens, layers, False)
-        _ints(slots, self.device, (tokens,), "slots")
-        with _Launch(self.device) as s:
-            _check(load().cg_int4_store(self._ref, layer, 1 if layers is None else layers,
-                                        ct.byref(rows), slots.data_ptr(), tokens, s),
-                   "cg_int4_store")
+        at = _ints(slots, self.device, (tokens,), "slots")
+        with _Launch(self.device.index) as s:
+            st = (_lib or load()).cg_int4_store(self._ref, layer, 1 if layers is None else layers,
+                                                rows, at, tokens, s)
+        _check(st, "cg_int4_store")
 
-    @_on_device
-    def load(self, slots, layer: int = 0, layers: int | None = None, k_out=None, v_out=None):
+    def load(self, slots, layer: int = 0, layers: int | None = None, k_out=None, v_out=None,
+             stream=None):
         """The bf16 rows of the slots: (k, v) as [tokens, heads, head_size] of
         one layer, or [layers, tokens, heads, head_size]. Slot -1 gives zeros.
         k_out, v_out take the rows in place (halves of a KV blob for
         Codec.encode, say)."""
+        if stream is not None:
+            return _on_stream(stream, self.load, slots, layer, layers, k_out, v_out)
         import torch
         tokens = slots.shape[0] if slots.dim() == 1 else -1
-        _ints(slots, self.device, (tokens,), "slots")
+        at = _ints(slots, self.device, (tokens,), "slots")
         shape = (tokens, self.num_heads, self.head_size)
         if layers is not None:
             _need(layers >= 0, "layers must not be negative")
@@ -810,16 +826,15 @@ class Int4Cache:
         if v_out is None:
             v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
         rows = self._rows(k_out, v_out, tokens, layers, True)
-        with _Launch(self.device) as s:
-            _check(load().cg_int4_load(self._ref, layer, 1 if layers is None else layers,
-                                       ct.byref(rows), slots.data_ptr(), tokens, s),
-                   "cg_int4_load")
+        with _Launch(self.device.index) as s:
+            st = (_lib or load()).cg_int4_load(self._ref, layer, 1 if layers is None else layers,
+                                               rows, at, tokens, s)
+        _check(st, "cg_int4_load")
         return k_out, v_out
 
-    @_on_device
     def attention(self, q, cu_q, kv_lens, block_table, layer: int = 0, window: int = 0,
                   sinks: int = 0, scale: float | None = None, max_q_len: int | None = None,
-                  out=None):
+                  out=None, stream=None):
         """Attention of the new tokens' queries q (bf16 [tokens, q_heads,
         head_size]) over a layer of the cache: request r owns the rows
         cu_q[r]:cu_q[r + 1] and sees its first kv_lens[r] tokens through row r of
@@ -827,39 +842,42 @@ class Int4Cache:
         them and the first ``sinks``. scale defaults to head_size ** -0.5.
         max_q_len, the most rows that any request has, spares launches when it
         is small. Returns out, like q; rows from cu_q[-1] on are not written."""
+        if stream is not None:
+            return _on_stream(stream, self.attention, q, cu_q, kv_lens, block_table, layer, window,
+                              sinks, scale, max_q_len, out)
         import torch
-        dev = self.device
-        _need(q.dim() == 3, "q must be [tokens, q_heads, head_size]")
-        tokens, q_heads = q.shape[0], q.shape[1]
+        dev, D = self.device, self.head_size
+        shape = q.shape
+        _need(len(shape) == 3, "q must be [tokens, q_heads, head_size]")
+        tokens, q_heads, _ = shape
         _need(q_heads > 0 and q_heads % self.num_heads == 0,
               f"q_heads must be a multiple of {self.num_heads}")
-        shape = (tokens, q_heads, self.head_size)
-        _bf16_rows(q, dev, shape, "q", False)
-        n = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
-        _ints(kv_lens, dev, (n,), "kv_lens")
-        _ints(cu_q, dev, (n + 1,), "cu_q")
-        _table(block_table, dev, "block_table")
-        _need(block_table.shape[0] == n, "block_table must have one row per request")
+        shape = (tokens, q_heads, D)
+        q_at, (qs0, qs1) = _bf16_rows(q, dev, shape, "q", False)
+        n, width, stride = _table(block_table, dev, "block_table")
+        lens_at = _ints(kv_lens, dev, (n,), "kv_lens (one entry per row of block_table)")
+        cu_at = _ints(cu_q, dev, (n + 1,), "cu_q")
         if out is None:
             out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+            out_at, os0, os1 = out.data_ptr(), q_heads * D, D
         else:
-            _bf16_rows(out, dev, shape, "out", True)
-        width = block_table.shape[1]
-        a = cg_attention(q.data_ptr(), _stride(q, 0), _stride(q, 1), out.data_ptr(),
-                         _stride(out, 0), _stride(out, 1), cu_q.data_ptr(), kv_lens.data_ptr(),
-                         block_table.data_ptr(), block_table.stride(0) if n > 1 else width, width,
-                         n, tokens, q_heads, max_q_len or 0, window, sinks,
-                         self.head_size ** -0.5 if scale is None else scale)
-        L = load()
-        with _Launch(dev) as s:
-            need = ct.c_size_t(0)
-            _check(L.cg_int4_attention_workspace(self._ref, ct.byref(a), ct.byref(need)),
-                   "cg_int4_attention_workspace")
+            out_at, (os0, os1) = _bf16_rows(out, dev, shape, "out", True)
+        a = _ATTENTION.pack(q_at, qs0, qs1, out_at, os0, os1, cu_at, lens_at,
+                            block_table.data_ptr(), stride, width, n, tokens, q_heads,
+                            max_q_len or 0, window, sinks, D ** -0.5 if scale is None else scale)
+        L = _lib or load()
+        need = ct.c_size_t(0)
+        _check(L.cg_int4_attention_workspace(self._ref, a, ct.byref(need)),
+               "cg_int4_attention_workspace")
+        size, ws, ws_at = need.value, None, None
+        if size:
             # one per call, from the current stream's pool: calls on other
             # streams and captured graphs never share one
-            ws = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
-            _check(L.cg_int4_attention(self._ref, layer, ct.byref(a), _ptr(ws), need.value, s),
-                   "cg_int4_attention")
+            ws = torch.empty(size, dtype=torch.uint8, device=dev)
+            ws_at = ws.data_ptr()
+        with _Launch(dev.index) as s:
+            st = L.cg_int4_attention(self._ref, layer, a, ws_at, size, s)
+        _check(st, "cg_int4_attention")
         return out
 
     def check(self):

@@ -8,6 +8,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "cg_attention.h"
 
 namespace {
@@ -39,6 +41,23 @@ int64_t max_rows(const cg_int4_cache *c, const cg_attention *a)
 }
 
 }  // namespace
+
+cudaError_t attn_sm_count(int *sms)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess)
+        return err;
+    const bool keep = dev >= 0 && dev < 64;
+    *sms = keep ? known[dev].load(std::memory_order_relaxed) : 0;
+    if (*sms == 0) {
+        err = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+        if (err == cudaSuccess && keep)
+            known[dev].store(*sms, std::memory_order_relaxed);
+    }
+    return err;
+}
 
 extern "C" cg_status cg_int4_attention_workspace(const cg_int4_cache *c, const cg_attention *a,
                                                  size_t *bytes)

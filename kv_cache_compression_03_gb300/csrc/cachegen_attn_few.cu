@@ -892,10 +892,8 @@ template <typename B, int NT>
 cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
 {
     using Sh = FewShared<B, NT>;
-    int dev = 0, sms = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess)
-        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    cudaError_t err = attn_sm_count(&sms);
     if (err == cudaSuccess)
         err = cudaFuncSetAttribute(k_attention_few<B, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)sizeof(Sh));

@@ -33,6 +33,7 @@ namespace {
 constexpr int kSoftWarps = 8, kKWarps = 3, kVWarps = 4;
 constexpr int kWarps = kSoftWarps + kKWarps + kVWarps + 1;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kKAhead = 3, kVAhead = 4;   // of a thread's loads, so many are on their way
 constexpr int kRows = 256;       // of a block
 constexpr int kTile = 128;       // tokens
 constexpr int kBlobs = kTile / 16;
@@ -550,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
             // A warp takes 8 tokens (half a blob) at a time: lane t + 4 k has words t of token
             // (k & 1) * 4 + (k >> 1), so that eight lanes' 16-byte stores meet all banks. The first
             // of the warps also finds the units, one ahead.
-            constexpr int kItems = (2 * kBlobs + kKWarps - 1) / kKWarps, kAhead = 3;   // items on their way
+            constexpr int kItems = (2 * kBlobs + kKWarps - 1) / kKWarps, kAhead = kKAhead;   // items on their way
             static_assert(kItems % kAhead == 0, "an item keeps its place");
             const int wi = warp - kSoftWarps, t = lane & 3, k8 = lane >> 2;
             const int half_tok = (k8 & 1) * 4 + (k8 >> 1);
@@ -648,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
             // A thread takes words (g, w) of half a blob's 4 token pairs at a time: channels 32 w + 4 g
             // + i. Eight lanes with the same g and w store to different 16-byte columns.
             // kAhead words are on their way while one is expanded.
-            constexpr int kAhead = 2;
+            constexpr int kAhead = NW < kVAhead ? NW : kVAhead;
             static_assert(NW % kAhead == 0 && 16 * 8 == 32 * kVWarps, "one (pg, g0) to a thread");
             const int wi = warp - kSoftWarps - kKWarps, vt = 32 * wi + lane;
             const int pg = 8 * (wi & 1) + (lane & 7), hf = pg & 1, g0 = 4 * (wi >> 1) + (lane >> 3);
@@ -845,10 +846,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
 template <typename B>
 cudaError_t launch(const AttnArgs &p, cudaStream_t s)
 {
-    int dev = 0, sms = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err == cudaSuccess)
-        err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    int sms = 0;
+    cudaError_t err = attn_sm_count(&sms);
     const int smem = (int)sizeof(ManyShared<B::kD>);
     if (err == cudaSuccess)
         err = cudaFuncSetAttribute(k_attention_many<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -127,6 +127,9 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
 
 // ------------------------------------------------------------------ launches
 
+// SM count of the current device, looked up once per device.
+cudaError_t attn_sm_count(int *sms);
+
 // Most blocks of the kernel for few rows, whose partial results the
 // workspace holds.
 constexpr int kFewMaxBlocks = 480;

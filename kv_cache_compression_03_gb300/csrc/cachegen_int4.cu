@@ -1,9 +1,12 @@
 // Store and load of the 4-bit paged cache (cg_int4_store, cg_int4_load).
 //
 // Per (token, head) row and group of G channels, lo = min x, s = bf16((max x
-// - lo) / 15), n = min(15, rne((x - lo) / s)); the value is lo + s n.
-// A thread owns 8 channels (16 bytes of bf16, one word of codes); the G / 8
-// threads of a group reduce its range with shuffles.
+// - lo) / 15), n = min(15, rne((x - lo) / s)); the value is lo + s n. Both are
+// streams (4 D bytes of bf16 against D + 8 D / G in the cache per token and head)
+// bound by HBM; what has to keep pace is the work per value.
+//
+// A block takes up to 16 tokens of one layer, all heads. Where each token lies
+// is worked out once, in shared memory, so that the rest is adds.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -14,146 +17,327 @@
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxTile = 16;   // tokens of a block
+constexpr int kEnoughBlocks = 304;   // two on each of 152 SMs
 
 struct RowArgs {
     uint8_t *data;
     void *status;
     size_t layer_bytes;   // one layer of the cache
-    int32_t num_slots, page_tokens, heads;
+    int32_t num_slots, page_tokens, heads, tile;
     uint16_t *k, *v;      // bf16 bits
     int64_t kl, kt, kh, vl, vt, vh;
     const int32_t *slots;
     int64_t tokens;
 };
 
-// Address of the blob that holds a slot of head h, and the token in it.
+// Where the block's tokens lie: the blob of head 0, and the token in it (-1: a
+// slot that is skipped). Blobs of the next heads follow at head_bytes().
+struct Tile {
+    uint8_t *blob[kMaxTile];
+    int32_t tok[kMaxTile];
+};
+
 template <typename B>
-__device__ __forceinline__ uint8_t *blob_of(const RowArgs &a, int layer, int slot, int h, int *tok)
+__device__ __forceinline__ uint32_t head_bytes(const RowArgs &a)
 {
-    const int page = slot / a.page_tokens, in = slot - page * a.page_tokens;
-    *tok = in & 15;
-    const size_t blobs = a.page_tokens / 16;
-    return a.data + (size_t)layer * a.layer_bytes +
-           (((size_t)page * a.heads + h) * blobs + (in >> 4)) * B::kBytes;
+    return (uint32_t)(a.page_tokens / 16) * B::kBytes;
 }
+
+template <typename B>
+__device__ __forceinline__ int find_tile(const RowArgs &a, Tile &tile)
+{
+    const int64_t first = (int64_t)blockIdx.x * a.tile;
+    const int n = (int)(a.tokens - first < a.tile ? a.tokens - first : a.tile);
+    if (threadIdx.x < n) {
+        const int slot = a.slots[first + threadIdx.x];
+        int tok = -1;
+        if (slot >= 0 && slot < a.num_slots) {
+            const int page = slot / a.page_tokens, in = slot - page * a.page_tokens;
+            tok = in & 15;
+            tile.blob[threadIdx.x] = a.data + blockIdx.y * a.layer_bytes +
+                                     (size_t)page * a.heads * head_bytes<B>(a) + (in >> 4) * B::kBytes;
+        } else if (slot != -1) {
+            int4_set_status(a.status, CG_ERR_CORRUPT);
+        }
+        tile.tok[threadIdx.x] = tok;
+    }
+    __syncthreads();
+    return n;
+}
+
+// A thread's walk over (token, row) pairs, `rows` rows to a token, a fixed
+// number of pairs apart.
+struct Walk {
+    int token, row, step_token, step_row, rows;
+    __device__ __forceinline__ Walk(int at, int step, int rows_)
+    {
+        rows = rows_;
+        token = at / rows;
+        row = at - token * rows;
+        step_token = step / rows;
+        step_row = step - step_token * rows;
+    }
+    __device__ __forceinline__ void next()
+    {
+        token += step_token;
+        row += step_row;
+        if (row >= rows) {
+            row -= rows;
+            ++token;
+        }
+    }
+};
 
 __device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
+__device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b)
+{
+    uint32_t c;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
+{
+    uint32_t c;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
+// bf16(fp32(range / 15)). range (1 / 15) is within two last bits of the quotient,
+// which only matters where that is next to a border of the rounding to bf16
+// (low half 0x8000); there, and for tiny ranges, it is divided.
+__device__ __forceinline__ float scale_of(float range)
+{
+    float q = range * (1.0f / 15.0f);
+    const uint32_t near = ((__float_as_uint(q) & 0xFFFFu) - 0x7FFCu);
+    if (near <= 8u || q < 0x1p-100f)
+        q = __fdiv_rn(range, 15.0f);
+    return __bfloat162float(__float2bfloat16_rn(q));
+}
+
+// Codes of 8 values: n = rne(d / s), d = x - lo. n0 = rne(d (1 / s)) is n or, next
+// to a tie, its neighbour; e = d - n0 s is exact (both are multiples of d's last
+// bit and e is below s), so |e| against s / 2 decides, with n even where they are
+// equal. (The fp32 quotient of the definition rounds to k + 1/2 only where d / s is
+// k + 1/2: 2 d - (2 k + 1) s is 0 or at least two last bits of d, more than half a
+// last bit of the quotient times s.) So no division per value: a handful of
+// multiply-adds, and the correction only in warps that have a value at a tie.
+__device__ __forceinline__ uint32_t codes_of_row(const float (&x)[8], float lo, float s)
+{
+    constexpr float kMagic = 12582912.0f;   // 1.5 2^23: adding it rounds to whole numbers
+    constexpr uint32_t kMagicBits = 0x4B400000u;
+    float inv;   // n0 may be off by one next to a tie, so this need not be exact
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    const float h = 0.5f * s;
+    float r[8], e[8], top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float d = __fsub_rn(x[j], lo);
+        r[j] = __fmaf_rn(d, inv, kMagic);
+        e[j] = __fmaf_rn(__fsub_rn(kMagic, r[j]), s, d);
+        top = fmaxf(top, fabsf(e[j]));
+    }
+    if (top >= 0.9999f * h) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t bits = __float_as_uint(r[j]);
+            // |e| > h, or = h with n0 odd
+            if (fabsf(e[j]) > __uint_as_float(__float_as_uint(h) - (bits & 1u)))
+                r[j] = __uint_as_float(e[j] < 0.0f ? bits - 1u : bits + 1u);
+        }
+    }
+    uint32_t code = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        code += (__float_as_uint(r[j]) - kMagicBits) << (4 * j);
+    return code;
+}
+
+// The same by division, where s is too small for the above (its last bit, or its
+// reciprocal, would leave fp32's normal range).
+__device__ __noinline__ uint32_t codes_of_tiny_row(const float (&x)[8], float lo, float s)
+{
+    uint32_t code = 0;
+    for (int j = 0; j < 8; ++j)
+        code |= (uint32_t)min(15, __float2int_rn(__fdiv_rn(__fsub_rn(x[j], lo), s))) << (4 * j);
+    return code;
+}
+
+// A thread takes 8 channels (16 bytes of bf16, one word of codes); the G / 8
+// threads of a group reduce its range with shuffles.
 template <typename B>
 __global__ void __launch_bounds__(kThreads) k_int4_store(RowArgs a)
 {
-    constexpr int kChunks = B::kD / 8;   // threads of a row
-    const int64_t per_token = (int64_t)2 * a.heads * kChunks;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t tok_i = i / per_token;
-    const int r = (int)(i - tok_i * per_token);
-    const int chunk = r % kChunks, h = r / kChunks % a.heads, is_v = r / kChunks / a.heads;
-    const int layer = blockIdx.y;
-    const bool there = tok_i < a.tokens;
-    const int slot = there ? a.slots[tok_i] : -1;
-    const bool ok = slot >= 0 && slot < a.num_slots;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (ok) {
-        const uint16_t *src = is_v ? a.v + layer * a.vl + tok_i * a.vt + h * a.vh
-                                   : a.k + layer * a.kl + tok_i * a.kt + h * a.kh;
-        w = __ldcs(reinterpret_cast<const uint4 *>(src) + chunk);
-    } else if (slot < -1 || slot >= a.num_slots) {
-        int4_set_status(a.status, CG_ERR_CORRUPT);
-    }
-    const float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y),
-                        bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
-    float lo = x[0], hi = x[0], any = 0.0f;
+    __shared__ Tile tile;
+    constexpr int kChunks = B::kD / 8, kRowsAtOnce = kThreads / kChunks;
+    const int n = find_tile<B>(a, tile);
+    const int chunk = threadIdx.x % kChunks, w32 = chunk / 4, part = chunk % 4;
+    const int64_t first = (int64_t)blockIdx.x * a.tile;
+    const uint16_t *k = a.k + blockIdx.y * a.kl + first * a.kt + 8 * chunk;
+    const uint16_t *v = a.v + blockIdx.y * a.vl + first * a.vt + 8 * chunk;
+    const uint32_t per_head = head_bytes<B>(a);
+    const int total = n * 2 * a.heads;
+    Walk at(threadIdx.x / kChunks, kRowsAtOnce, 2 * a.heads);
+    for (int i = threadIdx.x / kChunks; i - threadIdx.x / kChunks < total; i += kRowsAtOnce, at.next()) {
+        const bool is_v = at.row >= a.heads;
+        const int h = is_v ? at.row - a.heads : at.row;
+        const int tok = i < total ? tile.tok[at.token] : -1;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (tok >= 0)
+            w = __ldcs(reinterpret_cast<const uint4 *>(is_v ? v + at.token * a.vt + h * a.vh
+                                                            : k + at.token * a.kt + h * a.kh));
+        const float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y),
+                            bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
+        // the range two channels at a time; a NaN stays one through both
+        uint32_t lo2 = min2(min2(w.x, w.y), min2(w.z, w.w)), hi2 = max2(max2(w.x, w.y), max2(w.z, w.w));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        lo = fminf(lo, x[j]);
-        hi = fmaxf(hi, x[j]);
-        any = fmaf(x[j], 0.0f, any);   // NaN once a value is inf or NaN
-    }
-#pragma unroll
-    for (int m = 1; m < B::kG / 8; m <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, m));
-        any += __shfl_xor_sync(0xFFFFFFFFu, any, m);
-    }
-    if (!ok)
-        return;
-    float s = __bfloat162float(__float2bfloat16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.0f)));
-    if (any != 0.0f || isinf(s)) {     // any is 0 or NaN
-        int4_set_status(a.status, CG_ERR_NONFINITE);
-        s = lo = 0.0f;
-    }
-    uint32_t code = 0;
-    if (s > 0.0f) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int n = min(15, __float2int_rn(__fdiv_rn(__fsub_rn(x[j], lo), s)));
-            code |= (uint32_t)n << (4 * j);
+        for (int m = 1; m < B::kG / 8; m <<= 1) {
+            lo2 = min2(lo2, __shfl_xor_sync(0xFFFFFFFFu, lo2, m));
+            hi2 = max2(hi2, __shfl_xor_sync(0xFFFFFFFFu, hi2, m));
         }
-    }
-    int tok;
-    uint8_t *blob = blob_of<B>(a, layer, slot, h, &tok);
-    const int w32 = chunk / 4, part = chunk % 4;
-    if (!is_v) {
-        *reinterpret_cast<uint32_t *>(blob + B::kKCodes + tok * (B::kD / 2) +
-                                      part * (B::kD / 8) + w32 * 4) = code;
-    } else {
-        uint8_t *p = blob + B::kVCodes + (tok >> 1) * B::kD + 2 * part * (B::kD / 8) + w32 * 4 +
-                     2 * (tok & 1);
-        *reinterpret_cast<uint16_t *>(p) = (uint16_t)code;
-        *reinterpret_cast<uint16_t *>(p + B::kD / 8) = (uint16_t)(code >> 16);
-    }
-    if (chunk % (B::kG / 8) == 0) {
-        const int g = chunk / (B::kG / 8);
-        *reinterpret_cast<uint32_t *>(blob + (is_v ? B::kVParams : B::kKParams) +
-                                      (tok * B::kGroups + g) * 4) = pack_bf16(s, lo);
+        if (tok < 0)
+            continue;
+        lo2 = min2(lo2, __byte_perm(lo2, lo2, 0x1032));
+        hi2 = max2(hi2, __byte_perm(hi2, hi2, 0x1032));
+        float lo = bf_lo(lo2), s = scale_of(__fsub_rn(bf_lo(hi2), lo));
+        if (!(s < INFINITY)) {   // inf or NaN in the group, or hi - lo overflows
+            int4_set_status(a.status, CG_ERR_NONFINITE);
+            s = lo = 0.0f;
+        }
+        uint32_t code = 0;
+        if (s >= 0x1p-100f && s <= 0x1p120f)
+            code = codes_of_row(x, lo, s);
+        else if (s > 0.0f)
+            code = codes_of_tiny_row(x, lo, s);
+        uint8_t *blob = tile.blob[at.token] + h * per_head;
+        if (!is_v) {
+            *reinterpret_cast<uint32_t *>(blob + B::kKCodes + tok * (B::kD / 2) + part * (B::kD / 8) + w32 * 4) =
+                code;
+        } else {
+            uint8_t *p = blob + B::kVCodes + (tok >> 1) * B::kD + 2 * part * (B::kD / 8) + w32 * 4 + 2 * (tok & 1);
+            *reinterpret_cast<uint16_t *>(p) = (uint16_t)code;
+            *reinterpret_cast<uint16_t *>(p + B::kD / 8) = (uint16_t)(code >> 16);
+        }
+        if (chunk % (B::kG / 8) == 0)
+            *reinterpret_cast<uint32_t *>(blob + (is_v ? B::kVParams : B::kKParams) +
+                                          (tok * B::kGroups + chunk / (B::kG / 8)) * 4) = pack_bf16(s, lo);
     }
 }
 
+// lo + s n for the codes i and i + 4 of a word. n comes exact out of the mantissa
+// of 128 + n, and one rounding to bf16 gives what fp32 and then bf16 would: s n
+// has 12 bits, so where the sum does not fit fp32, s n is far below half a last
+// bit of lo.
+__device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32_t lo)
+{
+    const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    uint32_t n, y;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(x), "r"(0x43004300u));
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(n), "r"(s), "r"(lo));
+    return y;
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
+{
+    if constexpr (N == 1) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else if constexpr (N == 2) {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+    } else {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        w[0] = v.x;
+        w[1] = v.y;
+        w[2] = v.z;
+        w[3] = v.w;
+    }
+}
+
+// K: four threads to a row, each the words of its eighth channels (16 bytes of
+// codes at D = 128, 16-byte stores). V: eight threads to a row and two tokens at
+// a time, since the cache keeps pairs of tokens in one word; where the tokens are
+// no pair each reads its own half.
 template <typename B>
 __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
 {
-    constexpr int kChunks = B::kD / 8;
-    const int64_t per_token = (int64_t)2 * a.heads * kChunks;
-    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t tok_i = i / per_token;
-    if (tok_i >= a.tokens)
-        return;
-    const int r = (int)(i - tok_i * per_token);
-    const int chunk = r % kChunks, h = r / kChunks % a.heads, is_v = r / kChunks / a.heads;
-    const int layer = blockIdx.y;
-    const int slot = a.slots[tok_i];
-    uint4 out = make_uint4(0, 0, 0, 0);
-    if (slot >= 0 && slot < a.num_slots) {
-        int tok;
-        const uint8_t *blob = blob_of<B>(a, layer, slot, h, &tok);
-        const int w32 = chunk / 4, part = chunk % 4;
-        uint32_t code;
-        if (!is_v) {
-            code = *reinterpret_cast<const uint32_t *>(blob + B::kKCodes + tok * (B::kD / 2) +
-                                                       part * (B::kD / 8) + w32 * 4);
-        } else {
-            const uint8_t *p = blob + B::kVCodes + (tok >> 1) * B::kD + 2 * part * (B::kD / 8) +
-                               w32 * 4 + 2 * (tok & 1);
-            code = *reinterpret_cast<const uint16_t *>(p) |
-                   (uint32_t)*reinterpret_cast<const uint16_t *>(p + B::kD / 8) << 16;
-        }
-        const uint32_t par = *reinterpret_cast<const uint32_t *>(
-            blob + (is_v ? B::kVParams : B::kKParams) +
-            (tok * B::kGroups + chunk / (B::kG / 8)) * 4);
-        const float s = par_s(par), lo = par_lo(par);
-        float y[8];
+    __shared__ Tile tile;
+    constexpr int NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
+    const int n = find_tile<B>(a, tile);
+    const int64_t first = (int64_t)blockIdx.x * a.tile;
+    uint16_t *k = a.k + blockIdx.y * a.kl + first * a.kt, *v = a.v + blockIdx.y * a.vl + first * a.vt;
+    const uint32_t per_head = head_bytes<B>(a);
+    {
+        const int t = threadIdx.x & 3;
+        Walk at(threadIdx.x / 4, kThreads / 4, a.heads);
+        for (; at.token < n; at.next()) {
+            const int tok = tile.tok[at.token];
+            uint16_t *dst = k + at.token * a.kt + at.row * a.kh + 8 * t;
+            if (tok < 0) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            y[j] = __fadd_rn(lo, __fmul_rn(s, (float)((code >> (4 * j)) & 15u)));
-        out = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]),
-                         pack_bf16(y[6], y[7]));
-    } else if (slot != -1) {
-        int4_set_status(a.status, CG_ERR_CORRUPT);
+                for (int w = 0; w < NW; ++w)
+                    __stcs(reinterpret_cast<uint4 *>(dst + 32 * w), make_uint4(0, 0, 0, 0));
+                continue;
+            }
+            const uint8_t *blob = tile.blob[at.token] + at.row * per_head;
+            uint32_t code[NW], par[NG];
+            load_words(code, blob + B::kKCodes + tok * (B::kD / 2) + t * (B::kD / 8));
+            load_words(par, blob + B::kKParams + tok * 4 * NG);
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                const uint32_t q = par[w / WPG], s = __byte_perm(q, q, 0x1010), lo = __byte_perm(q, q, 0x3232);
+                const uint32_t y0 = expand(code[w], 0, s, lo), y1 = expand(code[w], 1, s, lo);
+                const uint32_t y2 = expand(code[w], 2, s, lo), y3 = expand(code[w], 3, s, lo);
+                __stcs(reinterpret_cast<uint4 *>(dst + 32 * w),
+                       make_uint4(__byte_perm(y0, y1, 0x5410), __byte_perm(y2, y3, 0x5410),
+                                  __byte_perm(y0, y1, 0x7632), __byte_perm(y2, y3, 0x7632)));
+            }
+        }
     }
-    uint16_t *dst = is_v ? a.v + layer * a.vl + tok_i * a.vt + h * a.vh
-                         : a.k + layer * a.kl + tok_i * a.kt + h * a.kh;
-    __stcs(reinterpret_cast<uint4 *>(dst) + chunk, out);
+    {
+        const int g = threadIdx.x & 7;
+        Walk at(threadIdx.x / 8, kThreads / 8, a.heads);
+        for (; 2 * at.token < n; at.next()) {
+            const int t0 = 2 * at.token, t1 = t0 + 1 < n ? t0 + 1 : t0;
+            const int tok0 = tile.tok[t0], tok1 = tile.tok[t1];
+            const bool pair = t1 > t0 && tok0 >= 0 && !(tok0 & 1) && tok1 == tok0 + 1 && tile.blob[t0] == tile.blob[t1];
+            uint16_t *dst = v + t0 * a.vt + at.row * a.vh + 4 * g;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (e == 1 && (pair || t1 == t0))
+                    break;
+                const int tok = e ? tok1 : tok0;
+                uint16_t *to = dst + (e ? a.vt : 0);
+                if (tok < 0) {
+#pragma unroll
+                    for (int w = 0; w < NW; ++w)
+                        __stcs(reinterpret_cast<uint2 *>(to + 32 * w), make_uint2(0, 0));
+                    continue;
+                }
+                const uint8_t *blob = tile.blob[e ? t1 : t0] + at.row * per_head;
+                uint32_t code[NW], par0[NG], par1[NG];
+                load_words(code, blob + B::kVCodes + (tok >> 1) * B::kD + g * (B::kD / 8));
+                load_words(par0, blob + B::kVParams + (tok & ~1) * 4 * NG);
+                load_words(par1, blob + B::kVParams + (tok | 1) * 4 * NG);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    const uint32_t s = __byte_perm(par0[w / WPG], par1[w / WPG], 0x5410);
+                    const uint32_t lo = __byte_perm(par0[w / WPG], par1[w / WPG], 0x7632);
+                    const uint32_t y0 = expand(code[w], 0, s, lo), y1 = expand(code[w], 1, s, lo);
+                    const uint32_t y2 = expand(code[w], 2, s, lo), y3 = expand(code[w], 3, s, lo);
+                    const uint2 even = make_uint2(__byte_perm(y0, y1, 0x5410), __byte_perm(y2, y3, 0x5410));
+                    const uint2 odd = make_uint2(__byte_perm(y0, y1, 0x7632), __byte_perm(y2, y3, 0x7632));
+                    __stcs(reinterpret_cast<uint2 *>(to + 32 * w), tok & 1 ? odd : even);
+                    if (pair)
+                        __stcs(reinterpret_cast<uint2 *>(to + a.vt + 32 * w), odd);
+                }
+            }
+        }
+    }
 }
 
 // Checks of both calls; *work is false where there is nothing to do.
@@ -178,11 +362,12 @@ cg_status check_rows(const cg_int4_cache *c, int32_t first_layer, int32_t layers
     if (rows->k == nullptr || rows->v == nullptr || slots == nullptr ||
         !int4_aligned(rows->k, 16) || !int4_aligned(rows->v, 16) || !int4_aligned(slots, 4))
         return CG_ERR_INVALID_ARG;
-    // the grid's limits: 2^31 - 1 blocks, 65,535 layers
-    const int64_t threads = tokens * 2 * c->num_heads * (c->head_size / 8);
-    if (tokens >= ((int64_t)1 << 31) || (threads + kThreads - 1) / kThreads >= ((int64_t)1 << 31) ||
-        layers > 65535)
+    if (tokens >= ((int64_t)1 << 31) || layers > 65535)   // the grid's limits
         return CG_ERR_UNSUPPORTED;
+    // 16 tokens to a block, fewer where that would leave SMs idle
+    a->tile = kMaxTile;
+    while (a->tile > 1 && (tokens + a->tile - 1) / a->tile * layers < kEnoughBlocks)
+        a->tile /= 2;
     a->layer_bytes = (size_t)c->num_pages * int4_page_bytes(c);
     a->data = static_cast<uint8_t *>(c->data) + (size_t)first_layer * a->layer_bytes;
     a->status = c->status;
@@ -202,10 +387,9 @@ cg_status check_rows(const cg_int4_cache *c, int32_t first_layer, int32_t layers
     return CG_OK;
 }
 
-dim3 row_grid(const cg_int4_cache *c, int32_t layers, int64_t tokens)
+dim3 row_grid(const RowArgs &a, int32_t layers)
 {
-    const int64_t threads = tokens * 2 * c->num_heads * (c->head_size / 8);
-    return dim3((unsigned)((threads + kThreads - 1) / kThreads), (unsigned)layers);
+    return dim3((unsigned)((a.tokens + a.tile - 1) / a.tile), (unsigned)layers);
 }
 
 }  // namespace
@@ -231,7 +415,7 @@ extern "C" cg_status cg_int4_store(const cg_int4_cache *c, int32_t first_layer, 
     if (st != CG_OK || !work)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid = row_grid(c, layers, tokens);
+    const dim3 grid = row_grid(a, layers);
     const cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
         k_int4_store<decltype(blob)><<<grid, kThreads, 0, s>>>(a);
         return cudaGetLastError();
@@ -249,7 +433,7 @@ extern "C" cg_status cg_int4_load(const cg_int4_cache *c, int32_t first_layer, i
     if (st != CG_OK || !work)
         return st;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const dim3 grid = row_grid(c, layers, tokens);
+    const dim3 grid = row_grid(a, layers);
     const cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
         k_int4_load<decltype(blob)><<<grid, kThreads, 0, s>>>(a);
         return cudaGetLastError();

@@ -3,10 +3,10 @@
 //
 // Two prefix sums over the requests (new tokens, pages needed) place every
 // new token and page. The sums run in one block, so nothing waits on another
-// block and the in-place outputs have one writer; that block also hands out
-// the pages. Slots of small batches are filled by the same block, those of
-// larger ones by a second launch over the tokens. The call is bound by
-// launch and barrier latency, not by its few bytes.
+// block and the in-place outputs have one writer. Pages and slots of small
+// batches are filled by the same block; larger ones take two more launches, over
+// the pages and over the slots, with the sums of pages left for them in the slot
+// map. The call is bound by launch and barrier latency, not by its few bytes.
 
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -18,7 +18,8 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSlotThreads = 256;
-constexpr int kFewTokens = 8192;   // slots that the first block fills itself
+constexpr int kSlotTile = 4 * kSlotThreads;   // slots of a block of the second launch
+constexpr int kFewTokens = CG_MAX_REQUESTS;   // slots that the first block fills itself
 
 struct Sum {
     int64_t tokens, pages;
@@ -62,11 +63,11 @@ __device__ __forceinline__ int slot_of(const cg_page_batch &b, int32_t page, int
 }
 
 // Dynamic shared memory: cu[requests + 1], base[requests + 1] (exclusive
-// sums of the new tokens and of the pages needed).
+// sums of the new tokens and of the pages needed), held[requests] (pages).
 __global__ void __launch_bounds__(kThreads) k_pages_grow(cg_page_batch b)
 {
     extern __shared__ int32_t smem[];
-    int32_t *cu = smem, *base = smem + b.requests + 1;
+    int32_t *cu = smem, *base = cu + b.requests + 1, *held = base + b.requests + 1;
     __shared__ Sum warp_sum[kWarps];
     __shared__ uint32_t error;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -79,76 +80,83 @@ __global__ void __launch_bounds__(kThreads) k_pages_grow(cg_page_batch b)
     __syncthreads();
     if (tid == 0 && (nfree < 0 || nfree > b.free_capacity))
         atomicCAS(&error, 0u, (uint32_t)CG_ERR_CORRUPT);
-    Sum carry = {0, 0};
-    for (int r0 = 0; r0 < b.requests; r0 += kThreads) {
-        const int r = r0 + tid;
-        Sum v = {0, 0};
-        if (r < b.requests) {
+    // a thread's requests lie together: one scan over the threads places them all
+    constexpr int kMost = (CG_MAX_REQUESTS + kThreads - 1) / kThreads;
+    const int each = (b.requests + kThreads - 1) / kThreads;
+    int32_t tokens[kMost], pages[kMost];
+    Sum v = {0, 0};
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int r = tid * each + i;
+        tokens[i] = pages[i] = 0;
+        if (i < each && r < b.requests) {
             const int64_t len = b.lens[r], n = b.counts[r];
             if (len < 0 || n < 0) {
                 atomicCAS(&error, 0u, (uint32_t)CG_ERR_INVALID_ARG);
             } else {
-                const int64_t all = (len + n + P - 1) / P;
+                const int64_t all = (len + n + P - 1) / P, have = (len + P - 1) / P;
                 if (all > b.table_width || len + n > INT32_MAX)
                     atomicCAS(&error, 0u, (uint32_t)CG_ERR_CAPACITY);
-                v.tokens = n;
-                v.pages = all - (len + P - 1) / P;
+                tokens[i] = (int32_t)n;
+                pages[i] = (int32_t)(all - have);
+                held[r] = (int32_t)have;
+                v.tokens += n;
+                v.pages += all - have;
             }
         }
-        const Sum own = v;
-        v = warp_scan(v, lane);
-        if (lane == 31)
-            warp_sum[warp] = v;
-        __syncthreads();
-        Sum before = carry, total = carry;
-        for (int i = 0; i < kWarps; ++i) {
-            const Sum s = warp_sum[i];
-            if (i < warp) {
-                before.tokens += s.tokens;
-                before.pages += s.pages;
-            }
-            total.tokens += s.tokens;
-            total.pages += s.pages;
+    }
+    const Sum own = v;
+    v = warp_scan(v, lane);
+    if (lane == 31)
+        warp_sum[warp] = v;
+    __syncthreads();
+    const Sum warps = warp_scan(warp_sum[lane], lane);   // every warp for itself
+    Sum total = {__shfl_sync(0xFFFFFFFFu, warps.tokens, 31), __shfl_sync(0xFFFFFFFFu, warps.pages, 31)};
+    const int64_t wt = __shfl_sync(0xFFFFFFFFu, warps.tokens, (warp + 31) & 31);
+    const int64_t wp = __shfl_sync(0xFFFFFFFFu, warps.pages, (warp + 31) & 31);
+    int64_t tok = v.tokens - own.tokens + (warp ? wt : 0), page = v.pages - own.pages + (warp ? wp : 0);
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int r = tid * each + i;
+        if (i < each && r < b.requests) {   // past an int the call fails below
+            cu[r] = (int32_t)tok;
+            base[r] = (int32_t)page;
+            tok += tokens[i];
+            page += pages[i];
         }
-        __syncthreads();
-        if (r < b.requests) {   // past an int the call fails below
-            cu[r] = (int32_t)(before.tokens + v.tokens - own.tokens);
-            base[r] = (int32_t)(before.pages + v.pages - own.pages);
-        }
-        carry = total;
     }
     if (tid == 0) {
-        cu[b.requests] = (int32_t)carry.tokens;
-        base[b.requests] = (int32_t)carry.pages;
-        if (carry.tokens > b.tokens || carry.pages > nfree)
+        cu[b.requests] = (int32_t)total.tokens;
+        base[b.requests] = (int32_t)total.pages;
+        if (total.tokens > b.tokens || total.pages > nfree)
             atomicCAS(&error, 0u, (uint32_t)CG_ERR_CAPACITY);
     }
     __syncthreads();
     const uint32_t err = error;
     const int32_t ntok = err ? 0 : cu[b.requests], npage = err ? 0 : base[b.requests];
-    // pages taken
-    for (int32_t k = tid; k < npage; k += kThreads) {
-        const int r = last_at_most(base, b.requests, k);
-        const int32_t held = (b.lens[r] + P - 1) / P;
-        const int32_t id = b.free_pages[nfree - 1 - k];
-        if (id < 0 || id >= b.num_pages)
-            int4_set_status(b.status, CG_ERR_CORRUPT);
-        b.block_table[r * b.table_stride + held + (k - base[r])] = id;
-    }
-    // slots, where this block fills them
-    if (b.tokens <= kFewTokens)
+    if (b.tokens <= kFewTokens) {
+        for (int32_t k = tid; k < npage; k += kThreads) {
+            const int32_t id = b.free_pages[nfree - 1 - k];
+            const int r = last_at_most(base, b.requests, k);
+            if (id < 0 || id >= b.num_pages)
+                int4_set_status(b.status, CG_ERR_CORRUPT);
+            b.block_table[r * b.table_stride + held[r] + (k - base[r])] = id;
+        }
         for (int32_t t = tid; t < b.tokens; t += kThreads) {
             int slot = -1;
             if (t < ntok) {
                 const int r = last_at_most(cu, b.requests, t);
-                const int32_t len = b.lens[r], x = len + (t - cu[r]);
-                const int32_t held = (len + P - 1) / P, at = x / P;
-                const int32_t page = at < held ? b.block_table[r * b.table_stride + at]
-                                               : b.free_pages[nfree - 1 - (base[r] + at - held)];
-                slot = slot_of(b, page, x);
+                const int32_t x = b.lens[r] + (t - cu[r]), at = x / P;
+                const int32_t id = at < held[r] ? b.block_table[r * b.table_stride + at]
+                                                : b.free_pages[nfree - 1 - (base[r] + at - held[r])];
+                slot = slot_of(b, id, x);
             }
             b.slots_out[t] = slot;
         }
+    } else {   // more slots than requests: room for the sums
+        for (int r = tid; r <= b.requests; r += kThreads)
+            b.slots_out[r] = err ? 0 : base[r];
+    }
     __syncthreads();   // lens_out may be lens, free_count_out free_count
     for (int r = tid; r < b.requests; r += kThreads) {
         const int32_t len = b.lens[r];
@@ -163,20 +171,50 @@ __global__ void __launch_bounds__(kThreads) k_pages_grow(cg_page_batch b)
     }
 }
 
+// Pages of a large batch: the sums stand in slots_out, the lengths are the new
+// ones, and the list ends where it did before the pages were taken.
+__global__ void __launch_bounds__(kSlotThreads) k_page_ids(cg_page_batch b)
+{
+    const int32_t *base = b.slots_out;
+    const int32_t npage = base[b.requests], nfree = *b.free_count_out + npage;
+    for (int64_t k = (int64_t)blockIdx.x * kSlotThreads + threadIdx.x; k < npage;
+         k += (int64_t)gridDim.x * kSlotThreads) {
+        const int32_t id = b.free_pages[nfree - 1 - k];
+        const int r = last_at_most(base, b.requests, (int32_t)k);
+        const int32_t len = b.lens_out[r] - (b.cu_out[r + 1] - b.cu_out[r]);
+        const int32_t held = (len + b.page_tokens - 1) / b.page_tokens;
+        if (id < 0 || id >= b.num_pages)
+            int4_set_status(b.status, CG_ERR_CORRUPT);
+        b.block_table[r * b.table_stride + held + (k - base[r])] = id;
+    }
+}
+
 // Slots of a large batch, once the tables are complete; lens_out is lens +
-// counts (cu_out all zero after an error, so nothing is read then).
+// counts (cu_out all zero after an error, so nothing is read then). A block's
+// slots belong to few requests: two searches find the first and the last.
 __global__ void __launch_bounds__(kSlotThreads) k_page_slots(cg_page_batch b)
 {
-    const int64_t t = (int64_t)blockIdx.x * kSlotThreads + threadIdx.x;
-    if (t >= b.tokens)
-        return;
-    int slot = -1;
-    if (t < b.cu_out[b.requests]) {
-        const int r = last_at_most(b.cu_out, b.requests, (int32_t)t);
-        const int32_t x = b.lens_out[r] - (b.cu_out[r + 1] - (int32_t)t);
-        slot = slot_of(b, b.block_table[r * b.table_stride + x / b.page_tokens], x);
+    __shared__ int range[2];
+    const int64_t t0 = (int64_t)blockIdx.x * kSlotTile;
+    const int32_t ntok = b.cu_out[b.requests];
+    const int64_t end = t0 + kSlotTile < b.tokens ? t0 + kSlotTile : b.tokens;
+    if (threadIdx.x < 64 && (threadIdx.x & 31) == 0 && t0 < ntok)
+        range[threadIdx.x >> 5] =
+            last_at_most(b.cu_out, b.requests, threadIdx.x ? (int32_t)(end < ntok ? end - 1 : ntok - 1) : (int32_t)t0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSlotTile / kSlotThreads; ++i) {
+        const int64_t t = t0 + i * kSlotThreads + threadIdx.x;
+        if (t >= end)
+            break;
+        int slot = -1;
+        if (t < ntok) {
+            const int r = range[0] + last_at_most(b.cu_out + range[0], range[1] - range[0] + 1, (int32_t)t);
+            const int32_t x = b.lens_out[r] - (b.cu_out[r + 1] - (int32_t)t);
+            slot = slot_of(b, b.block_table[r * b.table_stride + x / b.page_tokens], x);
+        }
+        b.slots_out[t] = slot;
     }
-    b.slots_out[t] = slot;
 }
 
 }  // namespace
@@ -206,14 +244,18 @@ extern "C" cg_status cg_pages_grow(const cg_page_batch *b, cg_stream_t stream)
         if (!int4_aligned(p, 4))
             return CG_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int smem = 2 * (b->requests + 1) * (int)sizeof(int32_t);
+    const int smem = (3 * b->requests + 2) * (int)sizeof(int32_t);
     if (smem > 48 * 1024 - 2048 &&
         cudaFuncSetAttribute(k_pages_grow, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
             cudaSuccess)
         return CG_ERR_CUDA;
     k_pages_grow<<<1, kThreads, smem, s>>>(*b);
-    if (b->tokens > kFewTokens)
-        k_page_slots<<<(unsigned)((b->tokens + kSlotThreads - 1) / kSlotThreads), kSlotThreads, 0,
+    if (b->tokens > kFewTokens) {
+        // pages that there can be, two to a thread
+        const int64_t pages = b->tokens / b->page_tokens + b->requests;
+        k_page_ids<<<(unsigned)(pages / (2 * kSlotThreads) + 1), kSlotThreads, 0, s>>>(*b);
+        k_page_slots<<<(unsigned)((b->tokens + kSlotTile - 1) / kSlotTile), kSlotThreads, 0,
                        s>>>(*b);
+    }
     return cudaGetLastError() == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

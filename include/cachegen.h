@@ -396,7 +396,7 @@ cg_status cg_int4_cache_bytes(const cg_int4_cache *cache, size_t *bytes);
 
 /* K and V rows: bf16 [layers][tokens][num_heads][head_size] with strides in
  * elements, channels contiguous; both pointers 16-byte aligned and every
- * stride a multiple of 8. A layer of cg_decode's output has k = kv[l][0],
+ * stride a multiple of 8 (the head strides below 2^31). A layer of cg_decode's output has k = kv[l][0],
  * v = kv[l][1], a layer stride of 2*T*C, a token stride of C and a head
  * stride of head_size. */
 typedef struct cg_kv_rows {

@@ -26,14 +26,17 @@ struct RowArgs {
     size_t layer_bytes;   // one layer of the cache
     int32_t num_slots, page_tokens, heads, tile;
     uint16_t *k, *v;      // bf16 bits
-    int64_t kl, kt, kh, vl, vt, vh;
+    int64_t kl, kt, vl, vt;
+    int32_t kh, vh;
     const int32_t *slots;
     int64_t tokens;
 };
 
-// Where the block's tokens lie: the blob of head 0, and the token in it (-1: a
-// slot that is skipped). Blobs of the next heads follow at head_bytes().
+// Where the block's tokens lie: their rows of head 0, the blob of head 0, and the
+// token in it (-1: a slot that is skipped). Blobs of the next heads follow at
+// head_bytes().
 struct Tile {
+    uint16_t *row[2][kMaxTile];   // K, V
     uint8_t *blob[kMaxTile];
     int32_t tok[kMaxTile];
 };
@@ -51,6 +54,8 @@ __device__ __forceinline__ int find_tile(const RowArgs &a, Tile &tile)
     const int n = (int)(a.tokens - first < a.tile ? a.tokens - first : a.tile);
     if (threadIdx.x < n) {
         const int slot = a.slots[first + threadIdx.x];
+        tile.row[0][threadIdx.x] = a.k + blockIdx.y * a.kl + (first + threadIdx.x) * a.kt;
+        tile.row[1][threadIdx.x] = a.v + blockIdx.y * a.vl + (first + threadIdx.x) * a.vt;
         int tok = -1;
         if (slot >= 0 && slot < a.num_slots) {
             const int page = slot / a.page_tokens, in = slot - page * a.page_tokens;
@@ -143,10 +148,11 @@ __device__ __forceinline__ uint32_t codes_of_row(const float (&x)[8], float lo, 
     if (top >= 0.9999f * h) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
+            // one to the side of e where |e| > h, or = h with n0 odd
             const uint32_t bits = __float_as_uint(r[j]);
-            // |e| > h, or = h with n0 odd
-            if (fabsf(e[j]) > __uint_as_float(__float_as_uint(h) - (bits & 1u)))
-                r[j] = __uint_as_float(e[j] < 0.0f ? bits - 1u : bits + 1u);
+            const bool off = fabsf(e[j]) > __uint_as_float(__float_as_uint(h) - (bits & 1u));
+            const uint32_t side = 1u | (uint32_t)(__float_as_int(e[j]) >> 31);
+            r[j] = __uint_as_float(bits + (off ? side : 0u));
         }
     }
     uint32_t code = 0;
@@ -158,9 +164,10 @@ __device__ __forceinline__ uint32_t codes_of_row(const float (&x)[8], float lo, 
 
 // The same by division, where s is too small for the above (its last bit, or its
 // reciprocal, would leave fp32's normal range).
-__device__ __noinline__ uint32_t codes_of_tiny_row(const float (&x)[8], float lo, float s)
+__device__ __forceinline__ uint32_t codes_of_tiny_row(const float (&x)[8], float lo, float s)
 {
     uint32_t code = 0;
+#pragma unroll
     for (int j = 0; j < 8; ++j)
         code |= (uint32_t)min(15, __float2int_rn(__fdiv_rn(__fsub_rn(x[j], lo), s))) << (4 * j);
     return code;
@@ -175,9 +182,6 @@ __global__ void __launch_bounds__(kThreads) k_int4_store(RowArgs a)
     constexpr int kChunks = B::kD / 8, kRowsAtOnce = kThreads / kChunks;
     const int n = find_tile<B>(a, tile);
     const int chunk = threadIdx.x % kChunks, w32 = chunk / 4, part = chunk % 4;
-    const int64_t first = (int64_t)blockIdx.x * a.tile;
-    const uint16_t *k = a.k + blockIdx.y * a.kl + first * a.kt + 8 * chunk;
-    const uint16_t *v = a.v + blockIdx.y * a.vl + first * a.vt + 8 * chunk;
     const uint32_t per_head = head_bytes<B>(a);
     const int total = n * 2 * a.heads;
     Walk at(threadIdx.x / kChunks, kRowsAtOnce, 2 * a.heads);
@@ -187,8 +191,8 @@ __global__ void __launch_bounds__(kThreads) k_int4_store(RowArgs a)
         const int tok = i < total ? tile.tok[at.token] : -1;
         uint4 w = make_uint4(0, 0, 0, 0);
         if (tok >= 0)
-            w = __ldcs(reinterpret_cast<const uint4 *>(is_v ? v + at.token * a.vt + h * a.vh
-                                                            : k + at.token * a.kt + h * a.kh));
+            w = __ldcs(reinterpret_cast<const uint4 *>(tile.row[is_v][at.token] +
+                                                       (int64_t)h * (is_v ? a.vh : a.kh)) + chunk);
         const float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y),
                             bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
         // the range two channels at a time; a NaN stays one through both
@@ -268,15 +272,13 @@ __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
     __shared__ Tile tile;
     constexpr int NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
     const int n = find_tile<B>(a, tile);
-    const int64_t first = (int64_t)blockIdx.x * a.tile;
-    uint16_t *k = a.k + blockIdx.y * a.kl + first * a.kt, *v = a.v + blockIdx.y * a.vl + first * a.vt;
     const uint32_t per_head = head_bytes<B>(a);
     {
         const int t = threadIdx.x & 3;
         Walk at(threadIdx.x / 4, kThreads / 4, a.heads);
         for (; at.token < n; at.next()) {
             const int tok = tile.tok[at.token];
-            uint16_t *dst = k + at.token * a.kt + at.row * a.kh + 8 * t;
+            uint16_t *dst = tile.row[0][at.token] + (int64_t)at.row * a.kh + 8 * t;
             if (tok < 0) {
 #pragma unroll
                 for (int w = 0; w < NW; ++w)
@@ -305,13 +307,13 @@ __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
             const int t0 = 2 * at.token, t1 = t0 + 1 < n ? t0 + 1 : t0;
             const int tok0 = tile.tok[t0], tok1 = tile.tok[t1];
             const bool pair = t1 > t0 && tok0 >= 0 && !(tok0 & 1) && tok1 == tok0 + 1 && tile.blob[t0] == tile.blob[t1];
-            uint16_t *dst = v + t0 * a.vt + at.row * a.vh + 4 * g;
+            const int64_t in_row = (int64_t)at.row * a.vh + 4 * g;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 if (e == 1 && (pair || t1 == t0))
                     break;
                 const int tok = e ? tok1 : tok0;
-                uint16_t *to = dst + (e ? a.vt : 0);
+                uint16_t *to = tile.row[1][e ? t1 : t0] + in_row;
                 if (tok < 0) {
 #pragma unroll
                     for (int w = 0; w < NW; ++w)
@@ -333,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
                     const uint2 odd = make_uint2(__byte_perm(y0, y1, 0x7632), __byte_perm(y2, y3, 0x7632));
                     __stcs(reinterpret_cast<uint2 *>(to + 32 * w), tok & 1 ? odd : even);
                     if (pair)
-                        __stcs(reinterpret_cast<uint2 *>(to + a.vt + 32 * w), odd);
+                        __stcs(reinterpret_cast<uint2 *>(tile.row[1][t1] + in_row + 32 * w), odd);
                 }
             }
         }
@@ -376,12 +378,14 @@ cg_status check_rows(const cg_int4_cache *c, int32_t first_layer, int32_t layers
     a->heads = c->num_heads;
     a->k = static_cast<uint16_t *>(rows->k);
     a->v = static_cast<uint16_t *>(rows->v);
+    if (strides[2] > INT32_MAX || strides[5] > INT32_MAX)
+        return CG_ERR_UNSUPPORTED;
     a->kl = strides[0];
     a->kt = strides[1];
-    a->kh = strides[2];
+    a->kh = (int32_t)strides[2];
     a->vl = strides[3];
     a->vt = strides[4];
-    a->vh = strides[5];
+    a->vh = (int32_t)strides[5];
     a->slots = slots;
     a->tokens = tokens;
     return CG_OK;

@@ -67,8 +67,13 @@ extern "C" cg_status cg_int4_attention_workspace(const cg_int4_cache *c, const c
     const cg_status st = check_sizes(c, a);
     if (st != CG_OK)
         return st;
+    // the two kernels run one after the other and share it
     const int64_t rows = max_rows(c, a);
     *bytes = attn_few_workspace(c->head_size, (int)(rows < kFewRows ? rows : kFewRows));
+    if (rows > kFewRows) {
+        const size_t many = attn_many_workspace(c->head_size);
+        *bytes = many > *bytes ? many : *bytes;
+    }
     return CG_OK;
 }
 
@@ -115,6 +120,6 @@ extern "C" cg_status cg_int4_attention(const cg_int4_cache *c, int32_t layer,
     cudaError_t err = attn_few_launch(p, c->head_size, c->group,
                                       (int)(most < kFewRows ? most : kFewRows), workspace, s);
     if (err == cudaSuccess && most > kFewRows)
-        err = attn_many_launch(p, c->head_size, c->group, s);
+        err = attn_many_launch(p, c->head_size, c->group, workspace, s);
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

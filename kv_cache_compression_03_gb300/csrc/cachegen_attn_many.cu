@@ -209,15 +209,22 @@ __device__ __forceinline__ void load_or_zero(uint32_t (&w)[N], const uint8_t *p,
 
 constexpr int kUnits = 4;   // units known at a time
 
-// 256 rows of a (request, KV head) and the blobs that they see: [0, sink) and
-// [sink + skip, ..), nb of them in n tiles of 8.
+// 256 rows of a (request, KV head), and of the blobs that they see ([0, sink) and
+// [sink + skip, ..), nb of them) those of one piece, from v0 on in n tiles of 8.
+// Where there are fewer units than blocks, each is cut into pieces along its
+// tokens, an item to a block, whose results a second kernel joins.
 struct Unit {
-    int32_t there;        // 0: no more units
+    int32_t there;        // 0: no more items
+    int32_t item, parts;  // the item's number; how many the unit is cut into
     int32_t r, h, q_row0; // request, KV head, the request's first query row
     int32_t rows, row0;   // rows of the request's KV head, first row of the unit
     int32_t tiles_q;      // row tiles of 128: 1 or 2
     int32_t x0, kv;       // position of the request's first query row; its tokens
     int32_t n, nb, sink, skip;
+    int32_t v0;           // the piece's first visible blob
+    // With one row tile in a cut unit the two softmax groups take turns at the tiles of tokens,
+    // each with a maximum, a sum and an accumulator of its own.
+    __device__ __forceinline__ bool turns() const { return tiles_q == 1 && parts > 1; }
     __device__ __forceinline__ int32_t blob(int32_t vb) const { return vb < sink ? vb : vb + skip; }
 };
 
@@ -232,8 +239,24 @@ struct ManyShared {
     Unit unit[kUnits];
     uint32_t bad[4];     // of the last tiles: blobs whose page id is outside the cache
     uint32_t tmem;
+    int32_t units;       // of the whole batch
     uint32_t gave_up;    // a wait ran out: everyone leaves
 };
+
+// Most blocks, hence most items of a batch that is cut.
+constexpr int kMaxBlocks = 160;
+
+// Workspace: how the batch was cut, the units, and of each item 256 rows of
+// { float o[D] }, then { float m }, { float l }. Where the softmax groups take
+// turns, rows 128 .. 255 are the second group's results for rows 0 .. 127.
+struct ManyWork {
+    int32_t *cut;        // units, pieces of each
+    Unit *heads;
+    float *parts;
+};
+
+template <int D>
+constexpr size_t kPartFloats = (size_t)kRows * (D + 2);
 
 // Waits that end: false once this wait or another one of the block ran out.
 __device__ __forceinline__ bool wait_or_leave(uint64_t *bar, uint32_t parity, uint32_t *gave_up,
@@ -259,9 +282,12 @@ __device__ __forceinline__ int32_t units_of(const AttnArgs &p, int r, AttnReques
 
 // One warp: unit `want` of the batch into *u. It goes on from where the last
 // call stood (32 requests from *r0 on, `*before` units ahead of them).
-__device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t want, int *r0, int64_t *before, Unit *u)
+__device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t item, int split, int *r0, int64_t *before,
+                                          Unit *u, Unit *heads)
 {
     const int lane = threadIdx.x & 31;
+    const int64_t want = item / split;
+    const int piece = (int)(item - want * split);
     for (;; *r0 += 32) {
         if (*r0 >= p.a.requests) {
             if (lane == 0)
@@ -301,10 +327,18 @@ __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t want, int *
             sink = sb < first ? (int)sb : first;
             skip = first - sink;
         }
-        const int nb = end - skip;
-        if (lane == 0)
-            *u = {1,  r,    off % p.heads,                q.row0, q.rows, row0, rows > 128 ? 2 : 1,
-                  x0, q.kv, (nb + kBlobs - 1) / kBlobs, nb,     sink,   skip};
+        const int nb = end - skip, n = (nb + kBlobs - 1) / kBlobs;
+        // at least two tiles to a piece; the pieces behind the last are empty
+        const int parts = min(split, max(n / 2, 1));
+        const int t0 = piece < parts ? (int)((int64_t)n * piece / parts) : 0;
+        const int t1 = piece < parts ? (int)((int64_t)n * (piece + 1) / parts) : 0;
+        if (lane == 0) {
+            const Unit found = {piece < parts ? 1 : 2, (int)item, parts, r, off % p.heads, q.row0, q.rows, row0,
+                                rows > 128 ? 2 : 1, x0, q.kv, t1 - t0, nb, sink, skip, t0 * kBlobs};
+            *u = found;
+            if (split > 1 && piece == 0)
+                heads[want] = found;
+        }
         __syncwarp();
         return;
     }
@@ -317,7 +351,7 @@ struct Lookup {
     // starts reading the id of the lane's blob in tile j
     __device__ __forceinline__ void start(const Unit &u, const int32_t *table, int bpp, int j)
     {
-        const int vb = j * kBlobs + (threadIdx.x & 7);
+        const int vb = u.v0 + j * kBlobs + (threadIdx.x & 7);
         id = -1;
         blob = 0;
         if (vb < u.nb) {
@@ -338,7 +372,7 @@ struct Lookup {
 // -------------------------------------------------------------------- kernel
 
 template <typename B>
-__global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
+__global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, ManyWork work)
 {
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
     constexpr int kQSub = kTile * 128;           // bytes of a 64-channel part of a Q or K tile
@@ -369,6 +403,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
         bar_init(&sm.q_empty, 1);
         bar_init_fence();
         sm.gave_up = 0;
+        sm.units = 0;
+    }
+    __syncthreads();
+    {
+        int64_t mine = 0;
+        for (int r = tid; r < p.a.requests; r += kThreads) {
+            AttnRequest q;
+            mine += units_of(p, r, &q);
+        }
+        // only whether there are fewer than blocks matters
+        const int few = __reduce_add_sync(0xFFFFFFFFu, (int)min(mine, (int64_t)(1 << 20)));
+        if (lane == 0)
+            atomicAdd(&sm.units, few);
     }
     if (warp == kWarps - 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(
@@ -381,6 +428,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
     tmem_fence_after();
     if (sm.tmem != 0 && tid == 0)   // never: the block took all of it
         int4_set_status(p.status, CG_ERR_CUDA);
+    const int split = sm.units > 0 && sm.units < gridDim.x ? gridDim.x / sm.units : 1;
+    if (blockIdx.x == 0 && tid == 0) {
+        work.cut[0] = sm.units;
+        work.cut[1] = split;
+    }
     const int bpp = p.page_tokens / 16;
     // Every role walks the block's units on its own and meets the others at the barriers only,
     // so that the next unit's queries, keys and values come in under the last one's products.
@@ -396,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
         if (!wait_all(&sm.u_full[un % kUnits], un / kUnits & 1))
             return nullptr;
         const Unit *u = &sm.unit[un % kUnits];
-        return u->there ? u : nullptr;
+        return u->there == 1 ? u : nullptr;   // (a piece that is empty is a block's only item)
     };
     auto unit_over = [&](int n) {
         tiles_done += n;
@@ -419,20 +471,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
         while (const Unit *up = next_unit()) {
             const Unit &u = *up;
             const int n = u.n;
-            if (i < u.tiles_q) {
-                const int rr = u.row0 + 128 * i + 32 * (warp & 3) + lane;
+            const bool turns = u.turns();
+            const int tile = turns ? 0 : i, first = turns ? i : 0, step = turns ? 2 : 1;
+            if (tile < u.tiles_q) {
+                const int rr = u.row0 + 128 * tile + 32 * (warp & 3) + lane;
                 const int x = rr < u.rows ? u.x0 + rr / p.ratio : -1;
-                const int last_row = min(u.row0 + 128 * i + 128, u.rows) - 1;
-                const int x_lo = u.x0 + (u.row0 + 128 * i) / p.ratio, x_hi = u.x0 + last_row / p.ratio;
+                const int last_row = min(u.row0 + 128 * tile + 128, u.rows) - 1;
+                const int x_lo = u.x0 + (u.row0 + 128 * tile) / p.ratio, x_hi = u.x0 + last_row / p.ratio;
                 float m = kNone, l = 0.0f;
                 bool alive = true;
-                for (int j = 0; j < n; ++j) {
+                for (int j = first; j < n; j += step) {
                     alive = wait_all(&sm.s_full[i], s_done & 1);
                     ++s_done;
                     if (!alive)
                         break;
                     tmem_fence_after();
-                    const int vb0 = j * kBlobs;
+                    const int vb0 = u.v0 + j * kBlobs;
                     const int t0 = 16 * u.blob(vb0), t1 = 16 * u.blob(vb0 + kBlobs - 1) + 15;
                     const uint32_t bad = *reinterpret_cast<volatile uint32_t *>(&sm.bad[(tiles_done + j) & 3]);
                     const bool whole = bad == 0 && vb0 + kBlobs <= u.nb && t1 <= x_lo &&
@@ -475,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                         const float mn = fmaxf(mx, m), f = exp2_fast(m - mn);
                         m = mn;
                         l *= f;
-                        if (j > 0) {
+                        if (j > first) {
 #pragma unroll 1
                             for (int c = 0; c < D / 16; ++c) {
                                 uint32_t o[16];
@@ -511,7 +565,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                     tmem_fence_before();
                     bar_arrive(&sm.p_full[i]);
                 }
-                if (alive && n > 0) {
+                const bool any = n > first;
+                if (alive && any) {
                     alive = wait_all(&sm.o_full[i], o_done & 1);
                     ++o_done;
                     tmem_fence_after();
@@ -522,10 +577,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                 const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
                                      (int64_t)(u.q_row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride;
+                float *part = work.parts + u.item * kPartFloats<D>;
+                const int part_row = 128 * i + 32 * (warp & 3) + lane;
+                if (u.parts > 1) {
+                    part[(size_t)kRows * D + part_row] = m;
+                    part[(size_t)kRows * (D + 1) + part_row] = l;
+                }
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     float o[32];
-                    if (n > 0) {
+                    if (any) {
                         tmem_ld32(o, o_at + 32 * c);
                         tmem_wait_ld();
                     } else {
@@ -533,7 +594,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                         for (int e = 0; e < 32; ++e)
                             o[e] = 0.0f;
                     }
-                    if (rr < u.rows) {
+                    if (rr >= u.rows)
+                        continue;
+                    if (u.parts > 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(part + (size_t)part_row * D + 32 * c + e) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8)
                             *reinterpret_cast<uint4 *>(out + 32 * c + e) = make_uint4(
@@ -561,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                 const uint32_t slot = which % kUnits;
                 if (!wait_all(&sm.u_empty[slot], (which / kUnits & 1) ^ 1))
                     return;
-                find_unit(p, blockIdx.x + (int64_t)which * gridDim.x, &u_r0, &u_before, &sm.unit[slot]);
+                find_unit(p, blockIdx.x + (int64_t)which * gridDim.x, split, &u_r0, &u_before, &sm.unit[slot],
+                          work.heads);
                 if (lane == 0)
                     bar_arrive(&sm.u_full[slot]);
                 __syncwarp();
@@ -585,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
                     load_or_zero(par[k], blob + B::kKParams + tok * 4 * NG, there);
                 };
                 auto is_bad = [&](uint32_t place, int j) {
-                    return __ballot_sync(0xFFFFFFFFu, place == ~0u && j * kBlobs + (lane & 7) < u.nb) & 0xFFu;
+                    return __ballot_sync(0xFFFFFFFFu, place == ~0u && u.v0 + j * kBlobs + (lane & 7) < u.nb) & 0xFFu;
                 };
                 look.start(u, table, bpp, 0);
                 now = look.place<B>(p, h, bpp);
@@ -766,8 +835,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
         } else {
             // ========================================================== products
             const uint32_t q_at = smem_addr(sm.q[0]), k_at = smem_addr(sm.k[0]), v_at = smem_addr(sm.v[0]);
-            auto scores = [&](int i, uint32_t sl) {
-                const uint32_t a = smem_desc(q_at + i * (kTile * D * 2)), b = smem_desc(k_at + sl * (kTile * D * 2));
+            // S of accumulator i: row tile `rows` with the K tile in place sl
+            auto scores = [&](int i, int rows, uint32_t sl) {
+                const uint32_t a = smem_desc(q_at + rows * (kTile * D * 2)), b = smem_desc(k_at + sl * (kTile * D * 2));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = ((kk >> 2) * kQSub + (kk & 3) * 32) >> 4;
@@ -778,50 +848,67 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
             uint32_t p_done = 0;     // parity of each row tile's p_full
             while (const Unit *up = next_unit()) {
                 const int n = up->n, tiles_q = up->tiles_q;
+                const bool turns = up->turns();
                 if (elect_one()) {
+                    // O of accumulator i, with the V tile of the t-th tile of all
+                    auto values = [&](int i, uint32_t t, bool add) {
+                        const uint32_t b = smem_desc(v_at + (t & 1) * (kTile * D * 2));
+#pragma unroll
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            mma_ts(kO + 128 * i, kS + 128 * i + 8 * kk, b + (((kk >> 2) * kVSub + (kk & 3) * 32) >> 4),
+                                   mma_desc(D), add || kk > 0);
+                    };
+                    auto k_there = [&](uint32_t t) { return wait(&sm.k_full[t & 1], t >> 1 & 1); };
+                    auto v_there = [&](uint32_t t) { return wait(&sm.v_full[t & 1], t >> 1 & 1); };
+                    auto p_there = [&](int i) {
+                        const bool ok = wait(&sm.p_full[i], p_done >> i & 1);
+                        p_done ^= 1u << i;
+                        return ok;
+                    };
                     bool alive = wait(&sm.q_full, un & 1);
-                    uint32_t use = tiles_done;
-                    if (n == 0)
-                        bar_arrive(&sm.q_empty);
-                    else if (alive)
-                        alive = wait(&sm.k_full[use & 1], use >> 1 & 1);
-                    if (alive && n > 0) {
+                    const uint32_t t0 = tiles_done;
+                    // the first scores of both accumulators
+                    const int head = turns ? min(n, 2) : min(n, 1);
+                    for (int j = 0; j < head && alive; ++j) {
+                        alive = k_there(t0 + j);
+                        if (!alive)
+                            break;
                         tmem_fence_after();
-                        scores(0, use & 1);
-                        if (tiles_q > 1)
-                            scores(1, use & 1);
-                        mma_commit(&sm.k_empty[use & 1]);
-                        if (n == 1)
+                        scores(turns ? j : 0, 0, (t0 + j) & 1);
+                        if (!turns && tiles_q > 1)
+                            scores(1, 1, (t0 + j) & 1);
+                        mma_commit(&sm.k_empty[(t0 + j) & 1]);
+                    }
+                    if (n <= head) {   // no more scores
+                        if (n == 0)
+                            bar_arrive(&sm.q_empty);
+                        else if (alive)
                             mma_commit(&sm.q_empty);
                     }
-                    for (int j = 0; j < n && alive; ++j, ++use) {
-                        const uint32_t sl = use & 1, nx = use + 1;
-                        const uint32_t b = smem_desc(v_at + sl * (kTile * D * 2));
-#pragma unroll 1
-                        for (int i = 0; i < tiles_q; ++i) {
-                            alive = wait(&sm.p_full[i], p_done >> i & 1);
-                            p_done ^= 1u << i;
-                            if (alive && i == 0)
-                                alive = wait(&sm.v_full[sl], use >> 1 & 1);
-                            if (alive && i == 0 && j + 1 < n)
-                                alive = wait(&sm.k_full[nx & 1], nx >> 1 & 1);
+                    for (int j = 0; j < n && alive; ++j) {
+                        const uint32_t t = t0 + j, nx = t + head;   // nx: the next tile of this accumulator
+                        const bool more = j + head < n;
+                        for (int k = 0; k < (turns ? 1 : tiles_q); ++k) {
+                            const int i = turns ? j & 1 : k;
+                            alive = p_there(i);
+                            if (alive && k == 0)
+                                alive = v_there(t);
+                            if (alive && k == 0 && more)
+                                alive = k_there(nx);
                             if (!alive)
                                 break;
                             tmem_fence_after();
-#pragma unroll
-                            for (int kk = 0; kk < kTile / 16; ++kk)
-                                mma_ts(kO + 128 * i, kS + 128 * i + 8 * kk,
-                                       b + (((kk >> 2) * kVSub + (kk & 3) * 32) >> 4), mma_desc(D), j > 0 || kk > 0);
-                            if (i + 1 == tiles_q)
-                                mma_commit(&sm.v_empty[sl]);
-                            if (j + 1 < n)
-                                scores(i, nx & 1);
+                            values(i, t, j >= head);
+                            if (turns || k + 1 == tiles_q)
+                                mma_commit(&sm.v_empty[t & 1]);
+                            if (more)
+                                scores(i, turns ? 0 : i, nx & 1);
                             else
                                 mma_commit(&sm.o_full[i]);
                         }
-                        if (alive && j + 1 < n)
+                        if (alive && more)
                             mma_commit(&sm.k_empty[nx & 1]);
-                        if (alive && j + 2 == n)
+                        if (alive && j + head + 1 == n)
                             mma_commit(&sm.q_empty);
                     }
                 }
@@ -843,8 +930,74 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p)
     }
 }
 
+// ------------------------------------------------------------------- joining
+
+// A few rows of a unit that was cut: the parts' accumulators, weighted by
+// 2^(m - max m); the weights first, so that the rest is independent loads.
+constexpr int kJoinRows = 16, kJoinThreads = 128;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p, ManyWork work)
+{
+    __shared__ float weight[kJoinRows][2 * kMaxBlocks];
+    __shared__ float inv[kJoinRows];
+    if (work.cut[1] == 1 || blockIdx.x >= work.cut[0])
+        return;
+    const Unit u = work.heads[blockIdx.x];
+    const int row0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, min(kRows, u.rows - u.row0) - row0);
+    if (u.parts == 1 || rows <= 0)
+        return;
+    const int each = u.turns() ? 2 : 1, n = u.parts * each;
+    // part k of row `row` of the block: its results stand in this row of the item
+    const float *first = work.parts + u.item * kPartFloats<D>;
+    auto part_of = [&](int k) { return first + (k / each) * kPartFloats<D>; };
+    auto row_of = [&](int k, int row) { return row0 + row + 128 * (k % each); };
+    const int lane = threadIdx.x & 31;
+    for (int row = threadIdx.x >> 5; row < rows; row += kJoinThreads / 32) {
+        float mx = kNone, l = 0.0f;
+        for (int k = lane; k < n; k += 32)
+            mx = fmaxf(mx, part_of(k)[(size_t)kRows * D + row_of(k, row)]);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+        for (int k = lane; k < n; k += 32) {
+            const float *stats = part_of(k) + (size_t)kRows * D + row_of(k, row);
+            const float f = exp2_fast(stats[0] - mx);
+            weight[row][k] = f;
+            l = fmaf(stats[kRows], f, l);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+        if (lane == 0)
+            inv[row] = l == 0.0f ? 0.0f : 1.0f / l;
+    }
+    __syncthreads();
+    constexpr int kQuads = D / 4;
+    for (int e = threadIdx.x; e < rows * kQuads; e += kJoinThreads) {
+        const int row = e / kQuads, ch = e % kQuads * 4;
+        float4 sum = make_float4(0, 0, 0, 0);
+#pragma unroll 8
+        for (int k = 0; k < n; ++k) {
+            const float4 v = *reinterpret_cast<const float4 *>(part_of(k) + (size_t)row_of(k, row) * D + ch);
+            const float f = weight[row][k];
+            sum.x = fmaf(v.x, f, sum.x);
+            sum.y = fmaf(v.y, f, sum.y);
+            sum.z = fmaf(v.z, f, sum.z);
+            sum.w = fmaf(v.w, f, sum.w);
+        }
+        const int rr = u.row0 + row0 + row, qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
+        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
+                             (int64_t)(u.q_row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride + ch;
+        *reinterpret_cast<uint2 *>(out) =
+            make_uint2(pack_bf16(sum.x * inv[row], sum.y * inv[row]), pack_bf16(sum.z * inv[row], sum.w * inv[row]));
+    }
+}
+
+constexpr size_t kHeadBytes = 256 + (sizeof(Unit) * kMaxBlocks + 255) / 256 * 256;
+
 template <typename B>
-cudaError_t launch(const AttnArgs &p, cudaStream_t s)
+cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
 {
     int sms = 0;
     cudaError_t err = attn_sm_count(&sms);
@@ -853,20 +1006,26 @@ cudaError_t launch(const AttnArgs &p, cudaStream_t s)
         err = cudaFuncSetAttribute(k_attention_many<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess)
         return err;
-    // units that there can be: full row tiles, and one short one per request with more than
-    // few_rows rows
-    const int64_t rows = (int64_t)p.a.tokens * p.ratio;
-    int64_t units = rows / kRows + 1;
-    const int64_t requests = rows / (p.few_rows + 1);
-    units += requests < p.a.requests ? requests : p.a.requests;
-    units *= p.heads;
-    k_attention_many<B><<<(unsigned)(units < sms ? units : sms), kThreads, smem, s>>>(p);
-    return cudaGetLastError();
+    const ManyWork work = {reinterpret_cast<int32_t *>(ws), reinterpret_cast<Unit *>(ws + 256),
+                           reinterpret_cast<float *>(ws + kHeadBytes)};
+    k_attention_many<B><<<sms < kMaxBlocks ? sms : kMaxBlocks, kThreads, smem, s>>>(p, work);
+    err = cudaGetLastError();
+    if (err == cudaSuccess) {
+        k_attention_many_join<B::kD><<<dim3(kMaxBlocks, kRows / kJoinRows), kJoinThreads, 0, s>>>(p, work);
+        err = cudaGetLastError();
+    }
+    return err;
 }
 
 }  // namespace
 
-cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, cudaStream_t s)
+size_t attn_many_workspace(int head_size)
 {
-    return int4_dispatch(head_size, group, [&](auto blob) { return launch<decltype(blob)>(p, s); });
+    return kHeadBytes + kMaxBlocks * (size_t)kRows * (head_size + 2) * sizeof(float);
+}
+
+cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, void *ws, cudaStream_t s)
+{
+    return int4_dispatch(head_size, group,
+                         [&](auto blob) { return launch<decltype(blob)>(p, static_cast<uint8_t *>(ws), s); });
 }

@@ -137,4 +137,5 @@ constexpr int kFewMaxBlocks = 480;
 size_t attn_few_workspace(int head_size, int max_rows);
 cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max_rows, void *ws,
                             cudaStream_t s);
-cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, cudaStream_t s);
+size_t attn_many_workspace(int head_size);
+cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, void *ws, cudaStream_t s);

@@ -11,9 +11,10 @@
 //                    and writes P as bf16 over S, where the next product reads
 //                    it. O is rescaled in place, only when a maximum rises by
 //                    more than 2^8.
-//   warps 8-10       K: 4-bit codes to bf16 rows in shared memory
-//   warps 11-14      V: the same, transposed (channels as rows)
-//   warp 15          one thread issues all products; the warp finds the next unit
+//   warps 8-13       4-bit codes to bf16 tiles in shared memory, a blob of 16 tokens
+//                    at a time: K as rows of tokens, V transposed (rows of channels)
+//   warp 14          finds the units and copies their blobs into a ring
+//   warp 15          one thread issues all products
 // Codes are expanded once per 256 rows, beside 2 x 2 x 128 x 128 x 128 products.
 // K rows keep the channel order in which a word's codes come apart (0 4 1 5 2 6
 // 3 7 of each eight); Q is laid out alike. V's words hold a pair of tokens each, as
@@ -30,10 +31,10 @@
 
 namespace {
 
-constexpr int kSoftWarps = 8, kKWarps = 3, kVWarps = 4;
-constexpr int kWarps = kSoftWarps + kKWarps + kVWarps + 1;
+constexpr int kSoftWarps = 8, kExpandWarps = 6;
+constexpr int kWarps = kSoftWarps + kExpandWarps + 2;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kKAhead = 3, kVAhead = 4;   // of a thread's loads, so many are on their way
+constexpr int kRing = 2 * kExpandWarps;   // blobs copied ahead: two for each of those warps
 constexpr int kRows = 256;       // of a block
 constexpr int kTile = 128;       // tokens
 constexpr int kBlobs = kTile / 16;
@@ -188,16 +189,16 @@ __device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32
 }
 
 template <int N>
-__device__ __forceinline__ void load_or_zero(uint32_t (&w)[N], const uint8_t *p, bool there)
+__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
 {
     if constexpr (N == 1) {
-        w[0] = there ? *reinterpret_cast<const uint32_t *>(p) : 0;
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
     } else if constexpr (N == 2) {
-        const uint2 v = there ? *reinterpret_cast<const uint2 *>(p) : make_uint2(0, 0);
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
         w[0] = v.x;
         w[1] = v.y;
     } else {
-        const uint4 v = there ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
         w[0] = v.x;
         w[1] = v.y;
         w[2] = v.z;
@@ -207,7 +208,8 @@ __device__ __forceinline__ void load_or_zero(uint32_t (&w)[N], const uint8_t *p,
 
 // ------------------------------------------------------------------ schedule
 
-constexpr int kUnits = 4;   // units known at a time
+constexpr int kUnits = 4;       // units known at a time
+constexpr int kBadTiles = 16;   // more than the copies can be ahead of the softmax
 
 // 256 rows of a (request, KV head), and of the blobs that they see ([0, sink) and
 // [sink + skip, ..), nb of them) those of one piece, from v0 on in n tiles of 8.
@@ -228,16 +230,18 @@ struct Unit {
     __device__ __forceinline__ int32_t blob(int32_t vb) const { return vb < sink ? vb : vb + skip; }
 };
 
-template <int D>
+template <typename B>
 struct ManyShared {
-    uint8_t q[2][kTile * D * 2];
-    uint8_t k[2][kTile * D * 2];
-    uint8_t v[2][kTile * D * 2];
+    uint8_t q[2][kTile * B::kD * 2];
+    uint8_t k[2][kTile * B::kD * 2];
+    uint8_t v[2][kTile * B::kD * 2];
+    uint8_t ring[kRing][B::kBytes];
     uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
         o_full[2], last;
-    uint64_t u_full[kUnits], u_empty[kUnits];
+    uint64_t u_full[kUnits], u_empty[kUnits], raw_full[kRing], raw_empty[kRing];
     Unit unit[kUnits];
-    uint32_t bad[4];     // of the last tiles: blobs whose page id is outside the cache
+    uint32_t raw_there[kRing];   // the blob was copied
+    uint32_t bad[kBadTiles];     // of the last tiles: blobs whose page id is outside the cache
     uint32_t tmem;
     int32_t units;       // of the whole batch
     uint32_t gave_up;    // a wait ran out: everyone leaves
@@ -344,31 +348,6 @@ __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t item, int s
     }
 }
 
-// The page ids of a tile's blobs, one by each of eight lanes (in every eight),
-// read a tile before its codes are and two before they are used.
-struct Lookup {
-    int32_t id, blob;
-    // starts reading the id of the lane's blob in tile j
-    __device__ __forceinline__ void start(const Unit &u, const int32_t *table, int bpp, int j)
-    {
-        const int vb = u.v0 + j * kBlobs + (threadIdx.x & 7);
-        id = -1;
-        blob = 0;
-        if (vb < u.nb) {
-            blob = u.blob(vb);
-            id = table[blob / bpp];
-        }
-    }
-    // the lane's blob in 128-byte units of the layer (it fits, cg_int4.h), ~0 if it is not there
-    template <typename B>
-    __device__ __forceinline__ uint32_t place(const AttnArgs &p, int h, int bpp) const
-    {
-        if ((unsigned)id >= (unsigned)p.num_pages)
-            return ~0u;
-        return (((uint32_t)id * p.heads + h) * bpp + blob % bpp) * (B::kBytes / 128);
-    }
-};
-
 // -------------------------------------------------------------------- kernel
 
 template <typename B>
@@ -379,15 +358,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
     constexpr int kVSub = D * 128;               // bytes of a 64-token part of a V tile
     // all 512 columns of tensor memory, so they start at 0: S0, S1, O0, O1
     constexpr uint32_t kS = 0, kO = 256;
-    using S = ManyShared<D>;
+    using S = ManyShared<B>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            bar_init(&sm.k_full[i], 32 * kKWarps);
-            bar_init(&sm.v_full[i], 32 * kVWarps);
+            bar_init(&sm.k_full[i], kBlobs);
+            bar_init(&sm.v_full[i], kBlobs);
             bar_init(&sm.p_full[i], 128);
             bar_init(&sm.k_empty[i], 1);
             bar_init(&sm.v_empty[i], 1);
@@ -399,7 +378,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
             bar_init(&sm.u_full[i], 1);
             bar_init(&sm.u_empty[i], kWarps);
         }
-        bar_init(&sm.q_full, 32 * kVWarps);
+        for (int i = 0; i < kRing; ++i) {
+            bar_init(&sm.raw_full[i], 1);
+            bar_init(&sm.raw_empty[i], 1);
+        }
+        bar_init(&sm.q_full, kExpandWarps);
         bar_init(&sm.q_empty, 1);
         bar_init_fence();
         sm.gave_up = 0;
@@ -488,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                     tmem_fence_after();
                     const int vb0 = u.v0 + j * kBlobs;
                     const int t0 = 16 * u.blob(vb0), t1 = 16 * u.blob(vb0 + kBlobs - 1) + 15;
-                    const uint32_t bad = *reinterpret_cast<volatile uint32_t *>(&sm.bad[(tiles_done + j) & 3]);
+                    const uint32_t bad = *reinterpret_cast<volatile uint32_t *>(&sm.bad[(tiles_done + j) % kBadTiles]);
                     const bool whole = bad == 0 && vb0 + kBlobs <= u.nb && t1 <= x_lo &&
                                        (x_hi - t0 < window || t1 < p.a.sinks);
                     // S is read twice, 32 columns at a time: rolled loops, because the roles of the
@@ -596,17 +579,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                     }
                     if (rr >= u.rows)
                         continue;
+                    // column 8 i + g is channel 4 g + i, as V's rows are
                     if (u.parts > 1) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(part + (size_t)part_row * D + 32 * c + e) =
-                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                        for (int g = 0; g < 8; ++g)
+                            *reinterpret_cast<float4 *>(part + (size_t)part_row * D + 32 * c + 4 * g) =
+                                make_float4(o[g], o[8 + g], o[16 + g], o[24 + g]);
                     } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            *reinterpret_cast<uint4 *>(out + 32 * c + e) = make_uint4(
-                                pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                                pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
+                        for (int g = 0; g < 8; g += 2)
+                            *reinterpret_cast<uint4 *>(out + 32 * c + 4 * g) = make_uint4(
+                                pack_bf16(o[g] * inv, o[8 + g] * inv), pack_bf16(o[16 + g] * inv, o[24 + g] * inv),
+                                pack_bf16(o[g + 1] * inv, o[9 + g] * inv), pack_bf16(o[17 + g] * inv, o[25 + g] * inv));
                     }
                 }
                 tmem_fence_before();   // the next unit's first p_full orders these reads before its O
@@ -614,137 +598,37 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
             unit_over(n);
         }
     } else {
-        if (warp < kSoftWarps + kKWarps) {
-            // ============================================================ K tiles
-            // A warp takes 8 tokens (half a blob) at a time: lane t + 4 k has words t of token
-            // (k & 1) * 4 + (k >> 1), so that eight lanes' 16-byte stores meet all banks. The first
-            // of the warps also finds the units, one ahead.
-            constexpr int kItems = (2 * kBlobs + kKWarps - 1) / kKWarps, kAhead = kKAhead;   // items on their way
-            static_assert(kItems % kAhead == 0, "an item keeps its place");
+        if (warp < kSoftWarps + kExpandWarps) {
+            // ======================================================= queries, K and V tiles
+            // Blobs go round the warps. K: 8 tokens at a time, lane t + 4 k has words t of token
+            // (k & 1) * 4 + (k >> 1). V: 4 pairs of tokens at a time, lane g + 8 w has the words
+            // (g, w), channels 32 w + 4 g + i, which become rows 32 w + 8 i + g. Either way eight
+            // lanes' 16-byte stores meet all banks.
             const int wi = warp - kSoftWarps, t = lane & 3, k8 = lane >> 2;
             const int half_tok = (k8 & 1) * 4 + (k8 >> 1);
-            int u_r0 = 0;
-            int64_t u_before = 0;
-            auto find = [&](uint32_t which) {
-                const uint32_t slot = which % kUnits;
-                if (!wait_all(&sm.u_empty[slot], (which / kUnits & 1) ^ 1))
-                    return;
-                find_unit(p, blockIdx.x + (int64_t)which * gridDim.x, split, &u_r0, &u_before, &sm.unit[slot],
-                          work.heads);
-                if (lane == 0)
-                    bar_arrive(&sm.u_full[slot]);
-                __syncwarp();
-            };
-            if (wi == 0)
-                find(0);
-            while (const Unit *up = next_unit()) {
-                const Unit &u = *up;
-                const int32_t *table = p.a.block_table + u.r * p.a.table_stride;
-                const int n = u.n, h = u.h;
-                uint32_t code[kAhead][NW], par[kAhead][NG];   // item it in place it % kAhead
-                Lookup look = {-1, 0};
-                uint32_t now, then;  // the lane's blob of this tile and the next
-                uint32_t bad;        // this tile's blobs whose page id is outside the cache
-                auto load = [&](uint32_t place, int k, int it) {
-                    const int item = wi + kKWarps * it, tok = 8 * (item & 1) + half_tok;
-                    const uint32_t at = __shfl_sync(0xFFFFFFFFu, place, item >> 1 & 7);
-                    const bool there = item < 2 * kBlobs && at != ~0u;
-                    const uint8_t *blob = p.layer + (uint64_t)at * 128;
-                    load_or_zero(code[k], blob + B::kKCodes + tok * (D / 2) + t * (D / 8), there);
-                    load_or_zero(par[k], blob + B::kKParams + tok * 4 * NG, there);
-                };
-                auto is_bad = [&](uint32_t place, int j) {
-                    return __ballot_sync(0xFFFFFFFFu, place == ~0u && u.v0 + j * kBlobs + (lane & 7) < u.nb) & 0xFFu;
-                };
-                look.start(u, table, bpp, 0);
-                now = look.place<B>(p, h, bpp);
-                bad = is_bad(now, 0);
-                look.start(u, table, bpp, 1);
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    load(now, k, k);
-                if (wi == 0 && n == 0)
-                    find(un + 1);
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t use = tiles_done + j, sl = use & 1;
-                    if (!wait_all(&sm.k_empty[sl], (use >> 1 & 1) ^ 1))
-                        break;
-                    if (wi == 0 && lane == 0) {
-                        *reinterpret_cast<volatile uint32_t *>(&sm.bad[use & 3]) = bad;
-                        if (bad)
-                            int4_set_status(p.status, CG_ERR_CORRUPT);
-                    }
-                    then = look.place<B>(p, h, bpp);
-                    bad = is_bad(then, j + 1);
-                    look.start(u, table, bpp, j + 2);
-#pragma unroll 1
-                    for (int round = 0; round < kItems; round += kAhead) {
-#pragma unroll
-                        for (int k = 0; k < kAhead; ++k) {
-                            const int item = wi + kKWarps * (round + k), at = 8 * item + half_tok;
-                            uint32_t cd[NW], pw[NG];
-#pragma unroll
-                            for (int w = 0; w < NW; ++w)
-                                cd[w] = code[k][w];
-#pragma unroll
-                            for (int gi = 0; gi < NG; ++gi)
-                                pw[gi] = par[k][gi];
-                            const bool same = round + kAhead < kItems;   // the next one in this place: of this tile?
-                            load(same ? now : then, k, same ? round + kAhead + k : k);
-                            if (item < 2 * kBlobs) {
-#pragma unroll
-                                for (int w = 0; w < NW; ++w) {
-                                    const uint32_t q = pw[w / WPG];
-                                    const uint32_t s2 = __byte_perm(q, q, 0x1010), lo2 = __byte_perm(q, q, 0x3232);
-                                    const uint4 o = make_uint4(expand(cd[w], 0, s2, lo2), expand(cd[w], 1, s2, lo2),
-                                                               expand(cd[w], 2, s2, lo2), expand(cd[w], 3, s2, lo2));
-                                    const int c = 4 * w + t;
-                                    *reinterpret_cast<uint4 *>(sm.k[sl] + (c >> 3) * kQSub + at * 128 +
-                                                               (((c & 7) ^ (at & 7)) << 4)) = o;
-                                }
-                            }
-                        }
-                    }
-                    now = then;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    bar_arrive(&sm.k_full[sl]);
-                    if (wi == 0 && j == 0)
-                        find(un + 1);
-                }
-                unit_over(n);
-            }
-        } else if (warp < kSoftWarps + kKWarps + kVWarps) {
-            // ================================================== queries and V tiles
-            // A thread takes words (g, w) of half a blob's 4 token pairs at a time: channels 32 w + 4 g
-            // + i. Eight lanes with the same g and w store to different 16-byte columns.
-            // kAhead words are on their way while one is expanded.
-            constexpr int kAhead = NW < kVAhead ? NW : kVAhead;
-            static_assert(NW % kAhead == 0 && 16 * 8 == 32 * kVWarps, "one (pg, g0) to a thread");
-            const int wi = warp - kSoftWarps - kKWarps, vt = 32 * wi + lane;
-            const int pg = 8 * (wi & 1) + (lane & 7), hf = pg & 1, g0 = 4 * (wi >> 1) + (lane >> 3);
+            const int g = lane & 7, vw = (lane >> 3) % NW, v_half = NW == 2 ? lane >> 4 : 0;
             const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+            uint32_t seq = 0;            // blobs of earlier units
             while (const Unit *up = next_unit()) {
                 const Unit &u = *up;
-                const int32_t *table = p.a.block_table + u.r * p.a.table_stride;
-                const int n = u.n, h = u.h, kv = u.kv;
-                Lookup look = {-1, 0};
-                look.start(u, table, bpp, 0);
-                if (!wait_all(&sm.q_empty, (un & 1) ^ 1))   // the last unit's scores are done
-                    break;
-                {
-                    constexpr int kC = D / 8, kStep = 32 * kVWarps / kC;   // rows apart
-                    const int c = vt % kC;
+                const int n = u.n;
+                auto queries = [&]() {   // false: a wait ran out
+                    if (!wait_all(&sm.q_empty, (un & 1) ^ 1))   // the last unit's scores are done
+                        return false;
+                    constexpr int kC = D / 8, kStep = 32 * kExpandWarps / kC;   // rows apart
+                    const int vt = 32 * wi + lane, c = vt % kC;
                     int in = vt / kC;
                     int qt = (u.row0 + in) / p.ratio, qr = (u.row0 + in) - qt * p.ratio;
                     const int step_t = kStep / p.ratio, step_r = kStep - step_t * p.ratio;
                     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.a.q) +
                                              (int64_t)u.q_row0 * p.a.q_token_stride +
-                                             (int64_t)h * p.ratio * p.a.q_head_stride + 8 * c;
+                                             (int64_t)u.h * p.ratio * p.a.q_head_stride + 8 * c;
                     const int end = 128 * u.tiles_q, rows = u.rows - u.row0;
+#pragma unroll 1
                     while (in < end) {
-                        uint4 v[8];
+                        uint4 v[4];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
+                        for (int e = 0; e < 4; ++e) {
                             v[e] = in + e * kStep < rows
                                        ? *reinterpret_cast<const uint4 *>(q + qt * p.a.q_token_stride +
                                                                           qr * p.a.q_head_stride)
@@ -757,81 +641,171 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                             }
                         }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e, in += kStep)
-                            *reinterpret_cast<uint4 *>(sm.q[in >> 7] + (c >> 3) * kQSub + (in & 127) * 128 +
-                                                       (((c & 7) ^ (in & 7)) << 4)) =
-                                make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410) ^ flip,
-                                           __byte_perm(v[e].x, v[e].z, 0x7632) ^ flip,
-                                           __byte_perm(v[e].y, v[e].w, 0x5410) ^ flip,
-                                           __byte_perm(v[e].y, v[e].w, 0x7632) ^ flip);
+                        for (int e = 0; e < 4; ++e, in += kStep)
+                            if (in < end)
+                                *reinterpret_cast<uint4 *>(sm.q[in >> 7] + (c >> 3) * kQSub + (in & 127) * 128 +
+                                                           (((c & 7) ^ (in & 7)) << 4)) =
+                                    make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410) ^ flip,
+                                               __byte_perm(v[e].x, v[e].z, 0x7632) ^ flip,
+                                               __byte_perm(v[e].y, v[e].w, 0x5410) ^ flip,
+                                               __byte_perm(v[e].y, v[e].w, 0x7632) ^ flip);
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    bar_arrive(&sm.q_full);
-                }
-                uint32_t code[kAhead][4], par[kAhead][8];   // word w of (pg, g0) in place w % kAhead
-                struct Half {        // the thread's half blob in a tile
-                    uint32_t at;
-                    int left;        // tokens of it that are there
-                } now, then;
-                auto take = [&](Half &f) {
-                    f.at = __shfl_sync(0xFFFFFFFFu, look.place<B>(p, h, bpp), pg >> 1);
-                    const int blob = __shfl_sync(0xFFFFFFFFu, look.blob, pg >> 1);
-                    f.left = f.at == ~0u ? 0 : kv - 16 * blob - 8 * hf;
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(&sm.q_full);
+                    return true;
                 };
-                auto load = [&](const Half &f, int k, int w) {
-                    const uint8_t *blob = p.layer + (uint64_t)f.at * 128;
-                    const uint32_t *c = reinterpret_cast<const uint32_t *>(blob + B::kVCodes + 4 * hf * D +
-                                                                           g0 * (D / 8)) + w;
-                    const uint32_t *q = reinterpret_cast<const uint32_t *>(blob + B::kVParams) + 8 * hf * NG + w / WPG;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        code[k][e] = f.left > 0 ? c[e * (D / 4)] : 0;
-                    // tokens that are not there get 0, whatever the cache holds in their place
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        par[k][e] = e < f.left ? q[e * NG] : 0;
-                };
-                take(now);
-                look.start(u, table, bpp, 1);
-#pragma unroll
-                for (int k = 0; k < kAhead; ++k)
-                    load(now, k, k);
-                for (int j = 0; j < n; ++j) {
-                    const uint32_t use = tiles_done + j, sl = use & 1;
-                    if (!wait_all(&sm.v_empty[sl], (use >> 1 & 1) ^ 1))
+                bool have_q = false, alive = true;
+                int b = (int)((wi + kExpandWarps - seq % kExpandWarps) % kExpandWarps);
+                for (; b < n * kBlobs && alive; b += kExpandWarps) {
+                    if (!have_q && b >= kBlobs) {   // after the first tile, which can be begun without
+                        have_q = true;
+                        if (!(alive = queries()))
+                            break;
+                    }
+                    const uint32_t use = tiles_done + (uint32_t)b / kBlobs, sl = use & 1, at = seq + b;
+                    const uint32_t slot = at % kRing;
+                    const int in_tile = b % kBlobs;
+                    alive = wait_all(&sm.raw_full[slot], at / kRing & 1) &&
+                            wait_all(&sm.k_empty[sl], (use >> 1 & 1) ^ 1);
+                    if (!alive)
                         break;
-                    take(then);      // of tile j + 1
-                    look.start(u, table, bpp, j + 2);
-#pragma unroll 1
-                    for (int round = 0; round < NW; round += kAhead) {
+                    const uint8_t *blob = sm.ring[slot];
+                    const bool there = sm.raw_there[slot];
 #pragma unroll
-                        for (int k = 0; k < kAhead; ++k) {
-                            uint32_t s2[4], lo2[4], cd[4];
+                    for (int a = 0; a < 2; ++a) {
+                        const int tok = 8 * a + half_tok, row = 16 * in_tile + tok;
+                        uint32_t code[NW], par[NG];
+                        load_words(code, blob + B::kKCodes + tok * (D / 2) + t * (D / 8));
+                        load_words(par, blob + B::kKParams + tok * 4 * NG);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                s2[e] = __byte_perm(par[k][2 * e], par[k][2 * e + 1], 0x5410);
-                                lo2[e] = __byte_perm(par[k][2 * e], par[k][2 * e + 1], 0x7632);
-                                cd[e] = code[k][e];
-                            }
-                            const bool same = round + kAhead < NW;
-                            load(same ? now : then, k, same ? round + kAhead + k : k);
+                        for (int w = 0; w < NW; ++w) {
+                            const uint32_t q = par[w / WPG];
+                            const uint32_t s2 = __byte_perm(q, q, 0x1010), lo2 = __byte_perm(q, q, 0x3232);
+                            uint4 o = make_uint4(expand(code[w], 0, s2, lo2), expand(code[w], 1, s2, lo2),
+                                                 expand(code[w], 2, s2, lo2), expand(code[w], 3, s2, lo2));
+                            if (!there)
+                                o = make_uint4(0, 0, 0, 0);
+                            const int c = 4 * w + t;
+                            *reinterpret_cast<uint4 *>(sm.k[sl] + (c >> 3) * kQSub + row * 128 +
+                                                       (((c & 7) ^ (row & 7)) << 4)) = o;
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(&sm.k_full[sl]);
+                    alive = wait_all(&sm.v_empty[sl], (use >> 1 & 1) ^ 1);
+                    if (!alive)
+                        break;
+                    // tokens that are not there get 0, whatever the cache holds in their place
+                    const int left = there ? u.kv - 16 * u.blob(u.v0 + b) : 0;
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const uint4 o =
-                                    make_uint4(expand(cd[0], c, s2[0], lo2[0]), expand(cd[1], c, s2[1], lo2[1]),
-                                               expand(cd[2], c, s2[2], lo2[2]), expand(cd[3], c, s2[3], lo2[3]));
-                                const int row = 32 * (round + k) + 4 * g0 + c;
-                                *reinterpret_cast<uint4 *>(sm.v[sl] + (pg >> 3) * kVSub + row * 128 +
-                                                           (((pg & 7) ^ (row & 7)) << 4)) = o;
+                    for (int a = 0; a < (NW == 2 ? 1 : 2); ++a) {
+                        const int hf = NW == 2 ? v_half : a, chunk = 2 * in_tile + hf;
+                        uint32_t code[4], s2[4], lo2[4];
+                        const uint32_t *par = reinterpret_cast<const uint32_t *>(blob + B::kVParams) + 8 * hf * NG +
+                                              vw / WPG;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            code[e] = *reinterpret_cast<const uint32_t *>(blob + B::kVCodes + (4 * hf + e) * D +
+                                                                          g * (D / 8) + 4 * vw);
+                            const int tok = 8 * hf + 2 * e;
+                            const uint32_t p0 = tok < left ? par[2 * e * NG] : 0;
+                            const uint32_t p1 = tok + 1 < left ? par[(2 * e + 1) * NG] : 0;
+                            s2[e] = __byte_perm(p0, p1, 0x5410);
+                            lo2[e] = __byte_perm(p0, p1, 0x7632);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int row = 32 * vw + 8 * i + g;
+                            *reinterpret_cast<uint4 *>(sm.v[sl] + (chunk >> 3) * kVSub + row * 128 +
+                                                       (((chunk & 7) ^ (row & 7)) << 4)) =
+                                make_uint4(expand(code[0], i, s2[0], lo2[0]), expand(code[1], i, s2[1], lo2[1]),
+                                           expand(code[2], i, s2[2], lo2[2]), expand(code[3], i, s2[3], lo2[3]));
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {
+                        bar_arrive(&sm.v_full[sl]);
+                        bar_arrive(&sm.raw_empty[slot]);
+                    }
+                }
+                if (alive && !have_q)
+                    queries();
+                seq += n * kBlobs;
+                unit_over(n);
+            }
+        } else if (warp == kSoftWarps + kExpandWarps) {
+            // ======================================================= units, copies
+            int u_r0 = 0;
+            int64_t u_before = 0;
+            uint32_t issued = 0;         // blobs
+            auto find = [&](uint32_t which) {
+                const uint32_t slot = which % kUnits;
+                if (!wait_all(&sm.u_empty[slot], (which / kUnits & 1) ^ 1))
+                    return;
+                find_unit(p, blockIdx.x + (int64_t)which * gridDim.x, split, &u_r0, &u_before, &sm.unit[slot],
+                          work.heads);
+                if (lane == 0)
+                    bar_arrive(&sm.u_full[slot]);
+                __syncwarp();
+            };
+            find(0);
+            while (const Unit *up = next_unit()) {
+                const Unit &u = *up;
+                const int32_t *table = p.a.block_table + u.r * p.a.table_stride;
+                const int n = u.n;
+                bool alive = true;
+                for (int b0 = 0; b0 < n * kBlobs && alive; b0 += 32) {
+                    // 32 blobs (four tiles) are looked up at once, one by each lane
+                    const int vb = u.v0 + b0 + lane;
+                    const bool wanted = b0 + lane < n * kBlobs && vb < u.nb;
+                    const int blob = wanted ? u.blob(vb) : 0, page = blob / bpp;
+                    const int id = wanted ? table[page] : -1;
+                    const bool there = (unsigned)id < (unsigned)p.num_pages;
+                    const uint32_t bad = __ballot_sync(0xFFFFFFFFu, wanted && !there);
+                    if (bad && lane == 0)
+                        int4_set_status(p.status, CG_ERR_CORRUPT);
+                    // in 128-byte units of the layer (it fits, cg_int4.h)
+                    const uint32_t place = there ? (((uint32_t)id * p.heads + u.h) * bpp + (blob - page * bpp)) *
+                                                       (B::kBytes / 128)
+                                                 : 0;
+                    const int count = min(32, n * kBlobs - b0);
+                    for (int k = 0; k < count && alive; ++k) {
+                        const uint32_t slot = issued % kRing;
+                        alive = wait_all(&sm.raw_empty[slot], (issued / kRing & 1) ^ 1);
+                        if (!alive)
+                            break;
+                        ++issued;
+                        if (lane == k) {
+                            if (k % kBlobs == 0)
+                                *reinterpret_cast<volatile uint32_t *>(
+                                    &sm.bad[(tiles_done + (b0 + k) / kBlobs) % kBadTiles]) = bad >> k & 0xFFu;
+                            sm.raw_there[slot] = there;
+                            if (there) {
+                                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                                bar_expect(&sm.raw_full[slot], B::kBytes);
+                                bulk_copy(sm.ring[slot], p.layer + (uint64_t)place * 128, B::kBytes,
+                                          &sm.raw_full[slot]);
+                            } else {
+                                bar_arrive(&sm.raw_full[slot]);
                             }
                         }
                     }
-                    now = then;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    bar_arrive(&sm.v_full[sl]);
+                    if (b0 == 0)
+                        find(un + 1);
                 }
+                if (n == 0)
+                    find(un + 1);
                 unit_over(n);
             }
+            // after a wait that ran out: the copies in flight land before the block's memory goes
+            if (sm.gave_up)
+                for (uint32_t at = issued < kRing ? 0 : issued - kRing; at < issued; ++at)
+                    bar_wait(&sm.raw_full[at % kRing], at / kRing & 1);
         } else {
             // ========================================================== products
             const uint32_t q_at = smem_addr(sm.q[0]), k_at = smem_addr(sm.k[0]), v_at = smem_addr(sm.v[0]);
@@ -893,14 +867,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                             alive = p_there(i);
                             if (alive && k == 0)
                                 alive = v_there(t);
-                            if (alive && k == 0 && more)
-                                alive = k_there(nx);
                             if (!alive)
                                 break;
                             tmem_fence_after();
                             values(i, t, j >= head);
                             if (turns || k + 1 == tiles_q)
                                 mma_commit(&sm.v_empty[t & 1]);
+                            // only now: a warp that expands tile nx may have to write V where tile t lies
+                            // before it comes to the last of nx's K
+                            if (more && k == 0 && !(alive = k_there(nx)))
+                                break;
                             if (more)
                                 scores(i, turns ? 0 : i, nx & 1);
                             else
@@ -1001,7 +977,7 @@ cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
 {
     int sms = 0;
     cudaError_t err = attn_sm_count(&sms);
-    const int smem = (int)sizeof(ManyShared<B::kD>);
+    const int smem = (int)sizeof(ManyShared<B>);
     if (err == cudaSuccess)
         err = cudaFuncSetAttribute(k_attention_many<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess)

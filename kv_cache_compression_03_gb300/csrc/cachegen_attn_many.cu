@@ -137,18 +137,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&v)[16], uint32_t at)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t at, const float (&v)[32])
-{
-    uint32_t a[16], b[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) {
-        a[e] = __float_as_uint(v[e]);
-        b[e] = __float_as_uint(v[16 + e]);
-    }
-    tmem_st16(at, a);
-    tmem_st16(at + 16, b);
-}
-
 // Pairs of fp32 in one instruction.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
@@ -476,34 +464,43 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                                        (x_hi - t0 < window || t1 < p.a.sinks);
                     // S is read twice, 32 columns at a time: rolled loops, because the roles of the
                     // block run side by side and have to share the instruction caches
+                    constexpr int C = 32;
                     float mx = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        tmem_ld32(s, s_at + 32 * c);
+                    for (int c = 0; c < kTile / C; ++c) {
+                        float s[C];
+#pragma unroll
+                        for (int k = 0; k < C / 32; ++k)
+                            tmem_ld32(s + 32 * k, s_at + C * c + 32 * k);
                         tmem_wait_ld();
                         if (!whole) {
 #pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                const int vb = vb0 + 2 * c + b, tok = 16 * u.blob(vb);
+                            for (int b = 0; b < C / 16; ++b) {
+                                const int in = C / 16 * c + b, vb = vb0 + in, tok = 16 * u.blob(vb);
                                 // of the blob's 16 tokens the row sees those below `end`, from `low` on or below `sink`
-                                const int end = vb < u.nb && !(bad >> (2 * c + b) & 1) ? x + 1 - tok : 0;
+                                const int end = vb < u.nb && !(bad >> in & 1) ? x + 1 - tok : 0;
                                 const int64_t low64 = (int64_t)x + 1 - window - tok;
                                 const int low = low64 < 0 ? 0 : (int)min(low64, (int64_t)16);
                                 const int sink = p.a.sinks - tok;
+                                uint32_t back[16];
 #pragma unroll
-                                for (int e = 0; e < 16; ++e)
+                                for (int e = 0; e < 16; ++e) {
                                     s[16 * b + e] = e < end && (e >= low || e < sink) ? s[16 * b + e] : -INFINITY;
+                                    back[e] = __float_as_uint(s[16 * b + e]);
+                                }
+                                tmem_st16(s_at + C * c + 16 * b, back);
                             }
-                            tmem_st32(s_at + 32 * c, s);
                         }
-                        float a = fmaxf(s[0], s[1]), b = fmaxf(s[2], s[3]);
+                        float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-                        for (int e = 4; e < 32; e += 4) {
-                            a = fmaxf(fmaxf(a, s[e]), s[e + 1]);
-                            b = fmaxf(fmaxf(b, s[e + 2]), s[e + 3]);
-                        }
-                        mx = fmaxf(fmaxf(mx, a), b);
+                        for (int e = 4; e + 8 <= C; e += 8)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                top[k] = fmaxf(fmaxf(top[k], s[e + 2 * k]), s[e + 2 * k + 1]);
+#pragma unroll
+                        for (int e = C - 4; e < C; ++e)
+                            top[e & 3] = fmaxf(top[e & 3], s[e]);
+                        mx = fmaxf(fmaxf(mx, fmaxf(top[0], top[1])), fmaxf(top[2], top[3]));
                     }
                     if (!whole)
                         tmem_wait_st();
@@ -525,24 +522,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                             }
                         }
                     }
-                    float2 sum = make_float2(0.0f, 0.0f);
+                    float2 sum = make_float2(0.0f, 0.0f), sum_b = sum;
                     const float2 sc2 = make_float2(sc, sc), m2 = make_float2(-m, -m);
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        float s[32];
-                        uint32_t pk[16];
-                        tmem_ld32(s, s_at + 32 * c);
+                    for (int c = 0; c < kTile / C; ++c) {
+                        float s[C];
+#pragma unroll
+                        for (int k = 0; k < C / 32; ++k)
+                            tmem_ld32(s + 32 * k, s_at + C * c + 32 * k);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            float2 z = fma2(make_float2(s[2 * e], s[2 * e + 1]), sc2, m2);
-                            z.x = exp2_fast(z.x);
-                            z.y = exp2_fast(z.y);
-                            sum = add2(sum, z);
-                            pk[e] = pack_bf16(z.x, z.y);
+                        for (int k = 0; k < C / 32; ++k) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                float2 z = fma2(make_float2(s[32 * k + 2 * e], s[32 * k + 2 * e + 1]), sc2, m2);
+                                z.x = exp2_fast(z.x);
+                                z.y = exp2_fast(z.y);
+                                if (e & 1)
+                                    sum_b = add2(sum_b, z);
+                                else
+                                    sum = add2(sum, z);
+                                pk[e] = pack_bf16(z.x, z.y);
+                            }
+                            tmem_st16(s_at + C / 2 * c + 16 * k, pk);   // over columns already read
                         }
-                        tmem_st16(s_at + 16 * c, pk);   // over columns already read
                     }
+                    sum = add2(sum, sum_b);
                     l += sum.x + sum.y;
                     tmem_wait_st();
                     tmem_fence_before();

@@ -593,6 +593,7 @@ class Codec:
 # is a microsecond of the step: checks are written out on plain tuples, and the
 # structs of the C calls are packed in one go (their layout is asserted here).
 
+_torch = None   # the module, once one of these calls needs it
 _ROWS = struct.Struct("@PPqqqqqq")
 _BATCH = struct.Struct("@PqiiPPPPiiiPPPPqP")
 _ATTENTION = struct.Struct("@PqqPqqPPPqiiiiiiif")
@@ -600,11 +601,17 @@ assert _ROWS.size == ct.sizeof(cg_kv_rows) and _BATCH.size == ct.sizeof(cg_page_
     -(-_ATTENTION.size // 8) * 8 == ct.sizeof(cg_attention)
 
 
+def _need_torch():
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _on_stream(stream, fn, *args, **kw):
     """fn(*args, **kw) with `stream` current: its temporaries and outputs are
     then that stream's too."""
-    import torch
-    with torch.cuda.stream(stream):
+    with (_torch or _need_torch()).cuda.stream(stream):
         return fn(*args, **kw)
 
 
@@ -617,18 +624,18 @@ class _Launch:
         self.index = index
 
     def __enter__(self):
-        import torch
-        now = torch._C._cuda_getDevice()
-        self.back = -1
+        C = _torch._C
+        now = C._cuda_getDevice()
         if now != self.index:
-            torch.cuda.set_device(self.index)
+            _torch.cuda.set_device(self.index)
             self.back = now
-        return torch._C._cuda_getCurrentRawStream(self.index)
+        else:
+            self.back = -1
+        return C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.back >= 0:
-            import torch
-            torch.cuda.set_device(self.back)
+            _torch.cuda.set_device(self.back)
 
 
 def _need(cond, what: str):
@@ -638,7 +645,7 @@ def _need(cond, what: str):
 
 def _ints(t, device, shape, what: str) -> int:
     """The address of a contiguous int32 tensor of the given shape on the device."""
-    import torch
+    torch = _torch or _need_torch()
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.shape == shape and
             t.device == device and t.is_contiguous()):
         raise ValueError(f"{what} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
@@ -647,7 +654,7 @@ def _ints(t, device, shape, what: str) -> int:
 
 def _table(t, device, what: str):
     """(requests, entries of a row, elements between rows) of a block table."""
-    import torch
+    torch = _torch or _need_torch()
     if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device and t.dim() == 2:
         n, width = t.shape
         s0, s1 = t.stride()
@@ -661,7 +668,7 @@ def _bf16_rows(t, device, shape, what: str, written: bool):
     """(address, strides but the last) of a bf16 tensor [.., head_size] of the
     given shape whose rows the kernels can read (and, when written, that do
     not overlap). A dimension of one element counts stride 0."""
-    import torch
+    torch = _torch or _need_torch()
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and
             t.device == device):
         raise ValueError(f"{what} must be a bf16 tensor of shape {list(shape)} on {device}")
@@ -716,7 +723,7 @@ def grow_pages(block_table, lens, counts, free_pages, free_count, page_tokens: i
     if stream is not None:
         return _on_stream(stream, grow_pages, block_table, lens, counts, free_pages, free_count,
                           page_tokens, tokens, num_pages, out)
-    import torch
+    torch = _torch or _need_torch()
     _need(isinstance(lens, torch.Tensor) and lens.is_cuda, "lens must be a CUDA tensor")
     dev = lens.device
     n = lens.shape[0] if lens.dim() == 1 else -1
@@ -761,7 +768,7 @@ class Int4Cache:
 
     def __init__(self, num_layers, num_pages, page_tokens, num_heads, head_size, group=32,
                  data=None, device="cuda"):
-        import torch
+        torch = _torch or _need_torch()
         self._c = cg_int4_cache(0, 0, num_layers, num_pages, page_tokens, num_heads, head_size,
                                 group)
         self._ref = ct.byref(self._c)
@@ -814,18 +821,25 @@ class Int4Cache:
         Codec.encode, say)."""
         if stream is not None:
             return _on_stream(stream, self.load, slots, layer, layers, k_out, v_out)
-        import torch
+        torch = _torch
         tokens = slots.shape[0] if slots.dim() == 1 else -1
         at = _ints(slots, self.device, (tokens,), "slots")
-        shape = (tokens, self.num_heads, self.head_size)
+        H, D = self.num_heads, self.head_size
+        shape = (tokens, H, D)
         if layers is not None:
             _need(layers >= 0, "layers must not be negative")
             shape = (layers,) + shape
-        if k_out is None:
+        if k_out is None and v_out is None:   # what is made here needs no check
             k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        if v_out is None:
             v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-        rows = self._rows(k_out, v_out, tokens, layers, True)
+            strides = (tokens * H * D, H * D, D)
+            rows = _ROWS.pack(k_out.data_ptr(), v_out.data_ptr(), *strides, *strides)
+        else:
+            if k_out is None:
+                k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            if v_out is None:
+                v_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
+            rows = self._rows(k_out, v_out, tokens, layers, True)
         with _Launch(self.device.index) as s:
             st = (_lib or load()).cg_int4_load(self._ref, layer, 1 if layers is None else layers,
                                                rows, at, tokens, s)
@@ -845,13 +859,12 @@ class Int4Cache:
         if stream is not None:
             return _on_stream(stream, self.attention, q, cu_q, kv_lens, block_table, layer, window,
                               sinks, scale, max_q_len, out)
-        import torch
-        dev, D = self.device, self.head_size
+        torch, dev, D = _torch, self.device, self.head_size
         shape = q.shape
         _need(len(shape) == 3, "q must be [tokens, q_heads, head_size]")
         tokens, q_heads, _ = shape
-        _need(q_heads > 0 and q_heads % self.num_heads == 0,
-              f"q_heads must be a multiple of {self.num_heads}")
+        if q_heads <= 0 or q_heads % self.num_heads:
+            raise ValueError(f"q_heads must be a multiple of {self.num_heads}")
         shape = (tokens, q_heads, D)
         q_at, (qs0, qs1) = _bf16_rows(q, dev, shape, "q", False)
         n, width, stride = _table(block_table, dev, "block_table")

@@ -31,7 +31,12 @@ cg_status check_sizes(const cg_int4_cache *c, const cg_attention *a)
     return CG_OK;
 }
 
-constexpr int kFewRows = 64;
+// Requests with up to this many rows per KV head go to the kernel for few rows,
+// which works on 16 at a time and reads the tokens again for each 16; the other
+// expands them once for up to 256. Four requests at 128K, 64 rows: 193 us there,
+// 159 us here; 64 at 1K, 64 rows: 153 and 92; eight at 16K, 20 rows: 110 and 161;
+// 64 at 1K, 32 rows: 85 and 89.
+constexpr int kFewRows = 48;
 
 // Most rows of one KV head that a request can have (query heads times tokens).
 int64_t max_rows(const cg_int4_cache *c, const cg_attention *a)

@@ -86,78 +86,104 @@ __device__ __forceinline__ int64_t work_of(const AttnArgs &p, int r, AttnRequest
 struct Place {   // a point of the line
     int32_t r;        // request (requests: past the end)
     int64_t off;      // blobs from the request's start
+    AttnRequest q;
 };
+
+__device__ __forceinline__ int64_t piece_of(int64_t total, int pieces)
+{
+    // (64-bit division is slow, and seldom needed)
+    const int64_t up = total + pieces - 1;
+    const int64_t chunk = up >> 32 ? up / pieces : (int64_t)((uint32_t)up / (uint32_t)pieces);
+    return chunk < kMinPiece ? kMinPiece : chunk;
+}
 
 // Block-wide: the line's length, the blobs of a piece, and the place of
 // piece `piece` plus `plus`. Block 0 of the main kernel reports bad requests.
 template <int RU>
-__device__ Place schedule(const AttnArgs &p, int pieces, int piece, int plus, bool report,
-                          int64_t *total_out, int64_t *chunk_out)
+__device__ __forceinline__ Place schedule(const AttnArgs &p, int pieces, int piece, int plus, bool report,
+                                          int64_t *total_out, int64_t *chunk_out)
 {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    auto work_at = [&](int r, AttnRequest *q, bool say) -> int64_t {
+        if (r >= p.a.requests)
+            return 0;
+        uint32_t error;
+        const int64_t w = work_of<RU>(p, r, q, &error);
+        if (say && error != CG_OK)
+            int4_set_status(p.status, error);
+        return w;
+    };
+    auto scan = [&](int64_t w) {
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, w, d);
+            if (lane >= d)
+                w += o;
+        }
+        return w;
+    };
+    if (p.a.requests <= 32) {   // each warp for itself
+        Place at = {p.a.requests, 0, {0, 0, 0, 0}};
+        const int64_t w = work_at(lane, &at.q, report && warp == 0), inc = scan(w);
+        *total_out = __shfl_sync(0xFFFFFFFFu, inc, 31);
+        *chunk_out = piece_of(*total_out, pieces);
+        const int64_t want = piece * *chunk_out + plus, start = inc - w;
+        const uint32_t mine = __ballot_sync(0xFFFFFFFFu, want >= start && want < start + w);
+        if (mine) {
+            const int src = __ffs(mine) - 1;
+            at.r = src;
+            at.off = __shfl_sync(0xFFFFFFFFu, want - start, src);
+            at.q.row0 = __shfl_sync(0xFFFFFFFFu, at.q.row0, src);
+            at.q.nq = __shfl_sync(0xFFFFFFFFu, at.q.nq, src);
+            at.q.kv = __shfl_sync(0xFFFFFFFFu, at.q.kv, src);
+            at.q.rows = __shfl_sync(0xFFFFFFFFu, at.q.rows, src);
+        }
+        return at;
+    }
     __shared__ int64_t warp_sum[kWarps];
     __shared__ Place found;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const bool once = p.a.requests <= kThreads;
     int64_t total = 0, chunk = 0, want = -1;
     if (tid == 0)
-        found = {p.a.requests, 0};
+        found.r = p.a.requests;
     for (int pass = 0; pass < 2; ++pass) {
         int64_t carry = 0;
         for (int r0 = 0; r0 < p.a.requests; r0 += kThreads) {
             const int r = r0 + tid;
-            int64_t w = 0;
-            if (r < p.a.requests) {
-                AttnRequest q;
-                uint32_t error;
-                w = work_of<RU>(p, r, &q, &error);
-                if (report && pass == 0 && error != CG_OK)
-                    int4_set_status(p.status, error);
-            }
-            int64_t inc = w;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-                if (lane >= d)
-                    inc += o;
-            }
+            AttnRequest q;
+            const int64_t w = work_at(r, &q, report && pass == 0), inc = scan(w);
             if (lane == 31)
                 warp_sum[warp] = inc;
             __syncthreads();
-            int64_t before = carry, sum = carry;
+            int64_t before = carry;
 #pragma unroll
             for (int i = 0; i < kWarps; ++i) {
                 if (i < warp)
                     before += warp_sum[i];
-                sum += warp_sum[i];
+                carry += warp_sum[i];
             }
             __syncthreads();
-            carry = sum;
             if (pass == 0 && once) {
-                total = sum;
-                chunk = (total + pieces - 1) / pieces;
-                if (chunk < kMinPiece)
-                    chunk = kMinPiece;
+                total = carry;
+                chunk = piece_of(total, pieces);
                 want = piece * chunk + plus;
             }
             const int64_t start = before + inc - w;
             if (want >= start && want < start + w)
-                found = {r, want - start};
+                found = {r, want - start, q};
         }
         if (pass == 0) {
-            total = carry;
-            chunk = (total + pieces - 1) / pieces;
-            if (chunk < kMinPiece)
-                chunk = kMinPiece;
-            want = piece * chunk + plus;
             if (once)
                 break;
+            total = carry;
+            chunk = piece_of(total, pieces);
+            want = piece * chunk + plus;
         }
     }
     __syncthreads();
-    const Place at = found;
     *total_out = total;
     *chunk_out = chunk;
-    return at;
+    return found;
 }
 
 // A (request, head, row tile) and the stretch of its blobs in this piece.
@@ -170,14 +196,13 @@ struct Unit {
 
 // Finds the unit at a place; `left` blobs of the piece remain.
 template <int RU>
-__device__ __forceinline__ void unit_at(const AttnArgs &p, Place at, int64_t left, Unit *u)
+__device__ __forceinline__ void unit_at(const AttnArgs &p, const Place &at, int64_t left, Unit *u)
 {
-    uint32_t error;
-    attn_request(p, at.r, &u->q, &error);
+    u->q = at.q;
     u->r = at.r;
     u->span = span_of(p, u->q);
     u->tiles = (u->q.rows + RU - 1) / RU;
-    const int32_t i = (int32_t)(at.off / u->span.nb);
+    const int32_t i = at.off >> 31 ? (int32_t)(at.off / u->span.nb) : (int32_t)at.off / u->span.nb;
     u->h = i / u->tiles;
     u->rt = i - u->h * u->tiles;
     u->b0 = (int32_t)(at.off - (int64_t)i * u->span.nb);
@@ -342,8 +367,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
     // ---- the warp's feeder: copies some steps ahead of the warp, through the same units.
     // Up to 32 blobs of the stretch are looked up at once, one by each lane, which then
     // issues its own blob's copy.
-    Unit fu;
-    unit_at<RU>(p, at, count, &fu);
+    Unit first;
+    unit_at<RU>(p, at, count, &first);
+    Unit fu = first;
     int64_t f_pos = fu.b1 - fu.b0;   // blobs of the piece up to the end of the feeder's unit
     int f_b, f_e;                    // blobs of the stretch not looked up yet
     warp_range(fu, warp, &f_b, &f_e);
@@ -398,8 +424,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 
     bool alive = true;               // no wait has run out
     uint32_t used = 0;
-    Unit u;
-    unit_at<RU>(p, at, count, &u);
+    Unit u = first;
     int64_t pos = 0;
     for (;;) {
         // ---- queries: column g of row tile nt is row rt * RU + 8 nt + g

@@ -11,10 +11,10 @@
 //                    and writes P as bf16 over S, where the next product reads
 //                    it. O is rescaled in place, only when a maximum rises by
 //                    more than 2^8.
-//   warps 8-13       4-bit codes to bf16 tiles in shared memory, a blob of 16 tokens
+//   warps 8-15       4-bit codes to bf16 tiles in shared memory, a blob of 16 tokens
 //                    at a time: K as rows of tokens, V transposed (rows of channels)
-//   warp 14          finds the units and copies their blobs into a ring
-//   warp 15          one thread issues all products
+//   warp 16          finds the units and copies their blobs into a ring, four lanes at once
+//   warp 17          one thread issues all products
 // Codes are expanded once per 256 rows, beside 2 x 2 x 128 x 128 x 128 products.
 // K rows keep the channel order in which a word's codes come apart (0 4 1 5 2 6
 // 3 7 of each eight); Q is laid out alike. V's words hold a pair of tokens each, as
@@ -31,10 +31,11 @@
 
 namespace {
 
-constexpr int kSoftWarps = 8, kExpandWarps = 6;
+constexpr int kSoftWarps = 8, kExpandWarps = 8;
 constexpr int kWarps = kSoftWarps + kExpandWarps + 2;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRing = 2 * kExpandWarps;   // blobs copied ahead: two for each of those warps
+constexpr int kRing = 12;   // blobs copied ahead
+constexpr int kIssue = 4;        // of those, copied at once
 constexpr int kRows = 256;       // of a block
 constexpr int kTile = 128;       // tokens
 constexpr int kBlobs = kTile / 16;
@@ -687,12 +688,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         load_words(par, blob + B::kKParams + tok * 4 * NG);
 #pragma unroll
                         for (int w = 0; w < NW; ++w) {
-                            const uint32_t q = par[w / WPG];
+                            const uint32_t q = there ? par[w / WPG] : 0;   // (0 + 0 n)
                             const uint32_t s2 = __byte_perm(q, q, 0x1010), lo2 = __byte_perm(q, q, 0x3232);
-                            uint4 o = make_uint4(expand(code[w], 0, s2, lo2), expand(code[w], 1, s2, lo2),
+                            const uint4 o = make_uint4(expand(code[w], 0, s2, lo2), expand(code[w], 1, s2, lo2),
                                                  expand(code[w], 2, s2, lo2), expand(code[w], 3, s2, lo2));
-                            if (!there)
-                                o = make_uint4(0, 0, 0, 0);
                             const int c = 4 * w + t;
                             *reinterpret_cast<uint4 *>(sm.k[sl] + (c >> 3) * kQSub + row * 128 +
                                                        (((c & 7) ^ (row & 7)) << 4)) = o;
@@ -780,16 +779,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                                                        (B::kBytes / 128)
                                                  : 0;
                     const int count = min(32, n * kBlobs - b0);
-                    for (int k = 0; k < count && alive; ++k) {
-                        const uint32_t slot = issued % kRing;
-                        alive = wait_all(&sm.raw_empty[slot], (issued / kRing & 1) ^ 1);
+                    // kIssue at a time: as many lanes wait for a place in the ring each, and copy
+                    for (int k = 0; k < count; k += kIssue) {
+                        const uint32_t at = issued + lane % kIssue, slot = at % kRing;
+                        alive = wait_all(&sm.raw_empty[slot], (at / kRing & 1) ^ 1);
                         if (!alive)
                             break;
-                        ++issued;
-                        if (lane == k) {
-                            if (k % kBlobs == 0)
+                        issued += kIssue;
+                        if ((unsigned)(lane - k) < kIssue) {
+                            if (lane % kBlobs == 0)
                                 *reinterpret_cast<volatile uint32_t *>(
-                                    &sm.bad[(tiles_done + (b0 + k) / kBlobs) % kBadTiles]) = bad >> k & 0xFFu;
+                                    &sm.bad[(tiles_done + (b0 + lane) / kBlobs) % kBadTiles]) = bad >> lane & 0xFFu;
                             sm.raw_there[slot] = there;
                             if (there) {
                                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -800,6 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                                 bar_arrive(&sm.raw_full[slot]);
                             }
                         }
+                        __syncwarp();
                     }
                     if (b0 == 0)
                         find(un + 1);

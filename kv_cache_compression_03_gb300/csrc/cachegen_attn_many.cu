@@ -225,7 +225,7 @@ struct ManyShared {
     uint8_t k[2][kTile * B::kD * 2];
     uint8_t v[2][kTile * B::kD * 2];
     uint8_t ring[kRing][B::kBytes];
-    uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2],
+    uint64_t q_full, q_empty, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_half[2], p_full[2],
         o_full[2], last;
     uint64_t u_full[kUnits], u_empty[kUnits], raw_full[kRing], raw_empty[kRing];
     Unit unit[kUnits];
@@ -356,6 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
         for (int i = 0; i < 2; ++i) {
             bar_init(&sm.k_full[i], kBlobs);
             bar_init(&sm.v_full[i], kBlobs);
+            bar_init(&sm.p_half[i], 128);
             bar_init(&sm.p_full[i], 128);
             bar_init(&sm.k_empty[i], 1);
             bar_init(&sm.v_empty[i], 1);
@@ -547,6 +548,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                                 pk[e] = pack_bf16(z.x, z.y);
                             }
                             tmem_st16(s_at + C / 2 * c + 16 * k, pk);   // over columns already read
+                        }
+                        if (c == kTile / C / 2 - 1) {   // the products of half the tile may begin
+                            tmem_wait_st();
+                            tmem_fence_before();
+                            bar_arrive(&sm.p_half[i]);
                         }
                     }
                     sum = add2(sum, sum_b);
@@ -832,12 +838,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                 const bool turns = up->turns();
                 if (elect_one()) {
                     // O of accumulator i, with the V tile of the t-th tile of all
-                    auto values = [&](int i, uint32_t t, bool add) {
-                        const uint32_t b = smem_desc(v_at + (t & 1) * (kTile * D * 2));
+                    auto values = [&](int i, int half, uint32_t t, bool add) {
+                        const uint32_t b = smem_desc(v_at + (t & 1) * (kTile * D * 2) + half * kVSub);
 #pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_ts(kO + 128 * i, kS + 128 * i + 8 * kk, b + (((kk >> 2) * kVSub + (kk & 3) * 32) >> 4),
-                                   mma_desc(D), add || kk > 0);
+                        for (int kk = 0; kk < kTile / 32; ++kk)
+                            mma_ts(kO + 128 * i, kS + 128 * i + 32 * half + 8 * kk, b + (kk * 32 >> 4), mma_desc(D),
+                                   add || kk > 0);
                     };
                     auto k_there = [&](uint32_t t) { return wait(&sm.k_full[t & 1], t >> 1 & 1); };
                     auto v_there = [&](uint32_t t) { return wait(&sm.v_full[t & 1], t >> 1 & 1); };
@@ -845,6 +851,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         const bool ok = wait(&sm.p_full[i], p_done >> i & 1);
                         p_done ^= 1u << i;
                         return ok;
+                    };
+                    auto half_there = [&](int i) {
+                        return wait(&sm.p_half[i], p_done >> i & 1);
                     };
                     bool alive = wait(&sm.q_full, un & 1);
                     const uint32_t t0 = tiles_done;
@@ -871,13 +880,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         const bool more = j + head < n;
                         for (int k = 0; k < (turns ? 1 : tiles_q); ++k) {
                             const int i = turns ? j & 1 : k;
-                            alive = p_there(i);
+                            alive = half_there(i);
                             if (alive && k == 0)
                                 alive = v_there(t);
                             if (!alive)
                                 break;
                             tmem_fence_after();
-                            values(i, t, j >= head);
+                            values(i, 0, t, j >= head);
+                            if (!(alive = p_there(i)))
+                                break;
+                            tmem_fence_after();
+                            values(i, 1, t, true);
                             if (turns || k + 1 == tiles_q)
                                 mma_commit(&sm.v_empty[t & 1]);
                             // only now: a warp that expands tile nx may have to write V where tile t lies

@@ -348,7 +348,7 @@ cg_status cg_int8_decode(const void *q, const float *scales, int64_t rows, int32
  *
  *   quantise   per (token, head) row of head_size channels and group of
  *              `group` channels: lo = min x, hi = max x,
- *              s = bf16_rne(fp32(fp32(hi - lo) / 15));
+ *              s = bf16_rne(fp32(fp32(hi - lo) * fp32(1 / 15)));
  *              n = min(15, round_half_even(fp32(fp32(x - lo) / s))),
  *              n = 0 where s = 0                        (4 bits, s and lo bf16)
  *   value      x^ = lo + s n; cg_int4_load gives bf16_rne(fp32(lo + fp32(s n)))

@@ -1,7 +1,7 @@
 // Store and load of the 4-bit paged cache (cg_int4_store, cg_int4_load).
 //
 // Per (token, head) row and group of G channels, lo = min x, s = bf16((max x
-// - lo) / 15), n = min(15, rne((x - lo) / s)); the value is lo + s n. Both are
+// - lo) (1 / 15)), n = min(15, rne((x - lo) / s)); the value is lo + s n. Both are
 // streams (4 D bytes of bf16 against D + 8 D / G in the cache per token and head)
 // bound by HBM; what has to keep pace is the work per value.
 //
@@ -111,16 +111,12 @@ __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b)
     return c;
 }
 
-// bf16(fp32(range / 15)). range (1 / 15) is within two last bits of the quotient,
-// which only matters where that is next to a border of the rounding to bf16
-// (low half 0x8000); there, and for tiny ranges, it is divided.
+// bf16(fp32(range (1 / 15))), 1 / 15 in fp32: the format takes the product, which every
+// device rounds alike, and not the quotient. The two are within two last bits of fp32, so
+// s is the same but for one range in about 2^14, next to a border of the rounding to bf16.
 __device__ __forceinline__ float scale_of(float range)
 {
-    float q = range * (1.0f / 15.0f);
-    const uint32_t near = ((__float_as_uint(q) & 0xFFFFu) - 0x7FFCu);
-    if (near <= 8u || q < 0x1p-100f)
-        q = __fdiv_rn(range, 15.0f);
-    return __bfloat162float(__float2bfloat16_rn(q));
+    return __bfloat162float(__float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f)));
 }
 
 // Codes of 8 values: n = rne(d / s), d = x - lo. n0 = rne(d (1 / s)) is n or, next

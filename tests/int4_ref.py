@@ -27,7 +27,8 @@ def quantise(x, group):
     y = np.asarray(x, dtype=np.float32).reshape(x.shape[:-1] + (x.shape[-1] // group, group))
     with np.errstate(all="ignore"):
         lo, hi = y.min(-1), y.max(-1)
-        s = bf16_round(((hi - lo).astype(np.float32) / np.float32(15.0)).astype(np.float32))
+        # the format multiplies by 1 / 15 in fp32 (and does not divide)
+        s = bf16_round(((hi - lo).astype(np.float32) * (np.float32(1.0) / np.float32(15.0))).astype(np.float32))
         bad = ~np.isfinite(y).all(-1) | ~np.isfinite(s)
         s, lo = np.where(bad, np.float32(0), s), np.where(bad, np.float32(0), lo)
         d = (y - lo[..., None]).astype(np.float32)

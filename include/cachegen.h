@@ -377,7 +377,8 @@ cg_status cg_int8_decode(const void *q, const float *scales, int64_t rows, int32
  *
  * Limits (CG_ERR_UNSUPPORTED): head_size 64 or 128, group 32, 64 or 128 and
  * at most head_size, page_tokens a multiple of 16 up to 1024, num_layers *
- * num_pages * num_heads and num_pages * page_tokens below 2^31. data must be
+ * num_pages * num_heads and num_pages * page_tokens below 2^31, one layer's
+ * bytes below 2^39. data must be
  * 256-byte aligned. */
 typedef struct cg_int4_cache {
     void *data;
@@ -396,9 +397,9 @@ cg_status cg_int4_cache_bytes(const cg_int4_cache *cache, size_t *bytes);
 
 /* K and V rows: bf16 [layers][tokens][num_heads][head_size] with strides in
  * elements, channels contiguous; both pointers 16-byte aligned and every
- * stride a multiple of 8 (the head strides below 2^31). A layer of cg_decode's output has k = kv[l][0],
- * v = kv[l][1], a layer stride of 2*T*C, a token stride of C and a head
- * stride of head_size. */
+ * stride a multiple of 8 (the head strides below 2^31). A layer of
+ * cg_decode's output has k = kv[l][0], v = kv[l][1], a layer stride of 2*T*C, a
+ * token stride of C and a head stride of head_size. */
 typedef struct cg_kv_rows {
     void *k;
     void *v;
@@ -411,8 +412,8 @@ typedef struct cg_kv_rows {
  * int32 [tokens]) of every layer. Slot -1 skips the token (padding); any
  * other slot outside the cache is skipped with CG_ERR_CORRUPT in status. Two
  * tokens of one call must not have the same slot (which of their parts stay
- * is then undefined). A group with inf or NaN, or whose hi - lo overflows,
- * sets CG_ERR_NONFINITE and is stored as zeros.
+ * is then undefined). A group with inf or NaN, or whose hi - lo or largest
+ * value lo + 15 s overflows, sets CG_ERR_NONFINITE and is stored as zeros.
  *
  * cg_int4_load: the other way, into rows. Slot -1 gives zeros, any other slot
  * outside the cache zeros and CG_ERR_CORRUPT. The same slot may occur often.
@@ -450,8 +451,8 @@ cg_status cg_int4_load(const cg_int4_cache *cache, int32_t first_layer, int32_t 
  *                                     or a page id outside [0, num_pages)
  * With an error nothing is taken: block_table is as it was, lens_out and
  * free_count_out repeat their inputs, cu_out is 0 and slots_out is -1 (a page
- * id outside the cache in block_table is the exception: only its tokens'
- * slots are -1). No other two arrays may overlap. Asynchronous on stream. */
+ * id outside the cache, in block_table or taken from free_pages, is the
+ * exception: only its tokens' slots are -1). No other two arrays may overlap. Asynchronous on stream. */
 typedef struct cg_page_batch {
     int32_t *block_table;
     int64_t table_stride;
@@ -492,6 +493,8 @@ cg_status cg_pages_grow(const cg_page_batch *batch, cg_stream_t stream);
  * for a page id outside the cache (its tokens count as not visible);
  * CG_ERR_INVALID_ARG for a request with more than max_q_len rows (left as
  * they were); CG_ERR_TIMEOUT when a bounded wait ran out.
+ *
+ * out must not overlap q or the cache.
  *
  * workspace (device, 256-byte aligned, the size that
  * cg_int4_attention_workspace gives; data and status pointers, q, out and

@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kThreads) k_int4_store(RowArgs a)
         lo2 = min2(lo2, __byte_perm(lo2, lo2, 0x1032));
         hi2 = max2(hi2, __byte_perm(hi2, hi2, 0x1032));
         float lo = bf_lo(lo2), s = scale_of(__fsub_rn(bf_lo(hi2), lo));
-        if (!(s < INFINITY)) {   // inf or NaN in the group, or hi - lo overflows
+        // inf or NaN in the group, or hi - lo overflows, or the largest value would round to inf
+        if (!(__fmaf_rn(15.0f, s, lo) < 0x1.FFp127f)) {
             int4_set_status(a.status, CG_ERR_NONFINITE);
             s = lo = 0.0f;
         }

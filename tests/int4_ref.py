@@ -29,7 +29,8 @@ def quantise(x, group):
         lo, hi = y.min(-1), y.max(-1)
         # the format multiplies by 1 / 15 in fp32 (and does not divide)
         s = bf16_round(((hi - lo).astype(np.float32) * (np.float32(1.0) / np.float32(15.0))).astype(np.float32))
-        bad = ~np.isfinite(y).all(-1) | ~np.isfinite(s)
+        top = (lo.astype(np.float64) + 15.0 * s.astype(np.float64)).astype(np.float32)
+        bad = ~np.isfinite(y).all(-1) | ~np.isfinite(s) | ~(top < 2.0 ** 128 - 2.0 ** 119)   # rounds to inf from there on
         s, lo = np.where(bad, np.float32(0), s), np.where(bad, np.float32(0), lo)
         d = (y - lo[..., None]).astype(np.float32)
         n = np.rint((d / s[..., None]).astype(np.float32))

@@ -118,6 +118,26 @@ def test_store_reports_what_it_cannot_hold(bad):
     got.check()                         # raised once, then cleared
 
 
+def test_store_reports_values_that_round_to_infinity():
+    """lo + 15 s past bf16's largest value: the group is refused, so that no stored value is infinite."""
+    rows = np.zeros((3, 1, 64), np.float32)
+    # a range of 254.25 or 254.75 2^120 has s = 17 2^120: 255.75 2^120 rounds to 2^128, 255.25 2^120 does not
+    rows[0, :, :32], rows[1, :, :32] = 0.75 * 2.0 ** 120, 0.25 * 2.0 ** 120
+    rows[:2, :, 9] = 255 * 2.0 ** 120
+    rows[2, :, 5] = 3.0e38
+    rows = ref.bf16_round(rows)
+    n, s, lo = ref.quantise(rows, 32)
+    assert s[0, 0, 0] == 0 and s[1, 0, 0] == 17 * 2.0 ** 120 and s[2, 0, 0] > 0
+    want, got = _pair(1, 1, 16, 1, 64, 32)
+    got.store(_dev(rows), _dev(rows), _ints([0, 1, 2]))
+    want.store(0, rows, rows, [0, 1, 2])
+    _same_bytes(want, got)
+    assert torch.isfinite(got.load(_ints([0, 1, 2]))[0].float()).all()
+    with pytest.raises(cg.CacheGenError) as e:
+        got.check()
+    assert e.value.status == cg.CG_ERR_NONFINITE
+
+
 def test_store_and_load_report_slots_outside_the_cache():
     rng = np.random.default_rng(4)
     k, v = _rand(rng, 3, 1, 64), _rand(rng, 3, 1, 64)
@@ -473,6 +493,111 @@ def test_attention_without_rows_or_requests():
     got.attention(torch.ones_like(keep), _ints([0, 0]), _ints([5]), _ints([[0]]), out=keep)
     assert bool((keep == 2.0).all())
     got.check()
+
+
+@pytest.mark.parametrize("n", [32, 33, 128, 129, 700, 8192])
+def test_attention_of_many_requests(n):
+    """Schedules within a warp, within a block and in two passes."""
+    rng = np.random.default_rng(n)
+    nkv = rng.integers(0, 60 if n < 1000 else 20, n)
+    nq = rng.integers(0, 3, n)
+    _run(rng, nq.tolist(), nkv.tolist(), 1, 2, 64, 64, 16, most=2)
+    _run(rng, nq.tolist(), nkv.tolist(), 2, 1, 128, 128, 16, window=21, sinks=1)
+
+
+@pytest.mark.parametrize("n", [31, 33, 140])
+def test_attention_of_many_requests_with_many_rows(n):
+    """Units of both kernels side by side, more of them than blocks."""
+    rng = np.random.default_rng(n)
+    nq = rng.choice([0, 1, 30, 40, 130], n, p=[0.1, 0.2, 0.3, 0.3, 0.1])
+    nkv = nq + rng.integers(0, 50, n)
+    _run(rng, nq.tolist(), nkv.tolist(), 2, 2, 64, 32, 16)
+
+
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32)])
+@pytest.mark.parametrize("nq,window,sinks", [(13, 0, 0), (33, 0, 0), (64, 0, 0), (65, 700, 9), (13, 1000, 0)])
+def test_attention_of_few_units_is_cut_along_the_tokens(dim, group, nq, window, sinks):
+    """One and two row tiles of long requests: pieces, joined by the second kernel."""
+    _run(np.random.default_rng(nq), [nq, nq], [3100, 2055], 1, 4, dim, group, 32, window, sinks, most=nq)
+
+
+@pytest.mark.parametrize("nq", [1, 40])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_attention_keeps_a_row_that_is_not_finite_to_itself(bad, nq):
+    rng = np.random.default_rng(11)
+    nkv, page, heads, ratio, dim = [75, 200], 16, 1, 4, 128
+    table, pages = _batch(rng, [nq, nq], nkv, page)
+    want, got = _filled(rng, nkv, table, pages, page, heads, dim, 32)
+    cu = np.array([0, nq, 2 * nq])
+    q = _rand(rng, 2 * nq, heads * ratio, dim)
+    o, tol = ref.attention(want, 0, q, cu, nkv, table, 0, 0, dim ** -0.5)
+    q[nq, 2, 7] = bad
+    out = got.attention(_dev(q), _ints(cu), _ints(nkv), _ints(table))
+    keep = np.ones(q.shape[:2], bool)
+    keep[nq, 2] = False
+    assert torch.isnan(out[nq, 2].float()).all()
+    _check_attention(out[torch.from_numpy(keep).cuda()], o[keep], tol[keep])
+    got.check()
+
+
+def test_attention_graphs_and_streams_side_by_side():
+    """Two captured graphs and eager calls, on three streams at once, prompts and single tokens: the
+    same bits as alone. Lengths change between replays."""
+    rng = np.random.default_rng(12)
+    heads, ratio, dim, group, page = 2, 4, 128, 64, 16
+    nq, nkv = [1, 2, 70, 200, 13], [900, 40, 300, 200, 2500]
+    table, pages = _batch(rng, nq, nkv, page)
+    want, got = _filled(rng, nkv, table, pages, page, heads, dim, group)
+    cu = np.concatenate([[0], np.cumsum(nq)])
+    q, tab, cu_t = _dev(_rand(rng, int(cu[-1]), heads * ratio, dim)), _ints(table), _ints(cu)
+    shorter = [m - d for m, d in zip(nkv, [300, 3, 41, 0, 1000])]
+    alone = [got.attention(q, cu_t, _ints(l), tab) for l in (nkv, shorter)]
+    _check_attention(alone[1], *ref.attention(want, 0, _np(q), cu, shorter, table, 0, 0, dim ** -0.5))
+    lens = [_ints(nkv), _ints(nkv)]
+    graphs, outs, streams = [], [], [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[i]):
+            outs.append(got.attention(q, cu_t, lens[i], tab))
+        graphs.append(g)
+    for turn in range(6):
+        lens[turn % 2].copy_(_ints(shorter if turn < 3 else nkv))
+        now = [torch.equal(l.cpu(), _ints(nkv).cpu()) for l in lens]
+        torch.cuda.synchronize()
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                graphs[i].replay()
+        eager = got.attention(q, cu_t, lens[0], tab, stream=streams[2])
+        torch.cuda.synchronize()
+        for i in range(2):
+            assert torch.equal(outs[i], alone[0 if now[i] else 1])
+        assert torch.equal(eager, outs[0])
+    got.check()
+
+
+def test_offsets_past_32_bits():
+    """A layer of 5 GB whose pages in use lie at its end: the same results as in a small cache."""
+    rng = np.random.default_rng(13)
+    heads, ratio, dim, group, page, pages = 8, 2, 128, 32, 1024, 4000
+    big = cg.Int4Cache(1, pages, page, heads, dim, group,
+                       data=torch.empty(pages * page // 16 * heads * 2560, dtype=torch.uint8, device="cuda"))
+    small = cg.Int4Cache(1, 5, page, heads, dim, group)
+    n = 3 * page + 77
+    k, v = _dev(_rand(rng, n, heads, dim)), _dev(_rand(rng, n, heads, dim))
+    ids = {small: [2, 0, 4, 1], big: [3999, 3, 3997, 3998]}
+    x, got = np.arange(n), {}
+    nq = [1, 40, 3]
+    cu, lens = _ints([0, 1, 41, 44]), _ints([n, n - 5, 2 * page + 1])
+    q = _dev(_rand(rng, 44, heads * ratio, dim))
+    for c, page_ids in ids.items():
+        slots = _ints(np.array(page_ids)[x // page] * page + x % page)
+        c.store(k, v, slots)
+        table = _ints([page_ids] * 3)
+        got[c] = c.load(slots) + (c.attention(q, cu, lens, table, max_q_len=max(nq)),)
+        c.check()
+    for a, b in zip(got[small], got[big]):
+        assert torch.equal(a, b)
 
 
 # ---------------------------------------------------------------- together

@@ -33,10 +33,10 @@ cg_status check_sizes(const cg_int4_cache *c, const cg_attention *a)
 
 // Requests with up to this many rows per KV head go to the kernel for few rows,
 // which works on 16 at a time and reads the tokens again for each 16; the other
-// expands them once for up to 256. Four requests at 128K, 64 rows: 193 us there,
-// 159 us here; 64 at 1K, 64 rows: 153 and 92; eight at 16K, 20 rows: 110 and 161;
-// 64 at 1K, 32 rows: 85 and 89.
-constexpr int kFewRows = 48;
+// expands them once for up to 256. Here and there, 8 KV heads of 128: 20 rows,
+// eight requests at 16K, 116 us and 127 us; 32 rows, four at 128K, 389 and 427,
+// 64 at 1K, 86 and 82; 48 rows, four at 128K, 569 and 428, 16 at 2K, 62 and 44.
+constexpr int kFewRows = 32;
 
 // Most rows of one KV head that a request can have (query heads times tokens).
 int64_t max_rows(const cg_int4_cache *c, const cg_attention *a)

@@ -1,5 +1,5 @@
 // Attention over the 4-bit cache for few query rows per KV head: single
-// tokens and a few drafted ones (up to 64 rows: query heads of the KV head
+// tokens and a few drafted ones (up to 32 rows: query heads of the KV head
 // times new tokens). Bound by HBM: D + 8 D/G bytes per token and head are read
 // once, and the work on them has to keep pace with that.
 //

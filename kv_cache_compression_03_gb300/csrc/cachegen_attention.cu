@@ -45,6 +45,13 @@ int64_t max_rows(const cg_int4_cache *c, const cg_attention *a)
     return (int64_t)n * (a->q_heads / c->num_heads);
 }
 
+// The workspace's part for the kernel for few rows.
+size_t few_bytes(const cg_int4_cache *c, int64_t rows)
+{
+    const size_t n = attn_few_workspace(c->head_size, (int)(rows < kFewRows ? rows : kFewRows));
+    return (n + 255) / 256 * 256;
+}
+
 }  // namespace
 
 cudaError_t attn_sm_count(int *sms)
@@ -72,13 +79,11 @@ extern "C" cg_status cg_int4_attention_workspace(const cg_int4_cache *c, const c
     const cg_status st = check_sizes(c, a);
     if (st != CG_OK)
         return st;
-    // the two kernels run one after the other and share it
+    // a part each: the two kernels may run side by side
     const int64_t rows = max_rows(c, a);
-    *bytes = attn_few_workspace(c->head_size, (int)(rows < kFewRows ? rows : kFewRows));
-    if (rows > kFewRows) {
-        const size_t many = attn_many_workspace(c->head_size);
-        *bytes = many > *bytes ? many : *bytes;
-    }
+    *bytes = few_bytes(c, rows);
+    if (rows > kFewRows)
+        *bytes += attn_many_workspace(c->head_size);
     return CG_OK;
 }
 
@@ -125,6 +130,7 @@ extern "C" cg_status cg_int4_attention(const cg_int4_cache *c, int32_t layer,
     cudaError_t err = attn_few_launch(p, c->head_size, c->group,
                                       (int)(most < kFewRows ? most : kFewRows), workspace, s);
     if (err == cudaSuccess && most > kFewRows)
-        err = attn_many_launch(p, c->head_size, c->group, workspace, s);
+        err = attn_many_launch(p, c->head_size, c->group,
+                               static_cast<uint8_t *>(workspace) + few_bytes(c, most), s);
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

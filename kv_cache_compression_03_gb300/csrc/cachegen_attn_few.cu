@@ -361,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
     const int g = lane >> 2, t = lane & 3;
 
     // the joining kernel's blocks may come up as this one's leave
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_next();
     if (lane == 0)
         for (int i = 0; i < kStages; ++i)
             bar_init(&sm.full[warp][i], HB);   // one arrival per blob of the step
@@ -865,22 +865,22 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 template <int D, int RU>
 __global__ void __launch_bounds__(kThreads) k_attention_join(AttnArgs p, int pieces, const float *parts)
 {
+    grid_next();
     int64_t total, chunk;
     const int c = blockIdx.x;
     // where the next piece starts: inside the unit, if one goes on
     const Place at = schedule<RU>(p, pieces, c + 1, 0, false, &total, &chunk);
     const int64_t border = (c + 1) * chunk;
-    if (border >= total)
-        return;
     Unit u;
-    unit_at<RU>(p, at, 1, &u);
-    if (u.b0 == 0 || u.b0 > chunk)
-        return;   // begins at the border, or before block c
+    if (border < total)
+        unit_at<RU>(p, at, 1, &u);
+    grid_wait();   // for the main kernel's parts
+    if (border >= total || u.b0 == 0 || u.b0 > chunk)
+        return;   // nothing there, or begins at the border, or before block c
     const int64_t end = border - u.b0 + u.span.nb;
     const int last = (int)((end + chunk - 1) / chunk) - 1;   // the block that holds its end
     const int row_base = u.rt * RU;
     const int rows_here = (row_base + RU < u.q.rows ? row_base + RU : u.q.rows) - row_base;
-    asm volatile("griddepcontrol.wait;" ::: "memory");   // for the main kernel's parts
     // weights of the parts: 2^(m - max m), and the sums that they give
     extern __shared__ float weight[];   // [RU][parts]
     __shared__ float inv[RU];
@@ -951,18 +951,8 @@ cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
         return err;
     // launched while the main kernel still runs: its own schedule is worked out
     // meanwhile, and it waits for the main kernel before it reads the parts
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = 8 * NT * blocks * sizeof(float);
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_attention_join<B::kD, 8 * NT>, p, blocks,
-                              static_cast<const float *>(parts));
+    return launch_under(k_attention_join<B::kD, 8 * NT>, dim3(blocks), kThreads, 8 * NT * blocks * sizeof(float), s,
+                        p, blocks, parts);
 }
 
 }  // namespace

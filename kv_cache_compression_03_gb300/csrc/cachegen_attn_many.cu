@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
     S &sm = *reinterpret_cast<S *>(smem_raw);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
+    grid_next();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             bar_init(&sm.k_full[i], kBlobs);
@@ -924,69 +925,75 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
         tmem_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");
     }
+    grid_wait();
 }
 
 // ------------------------------------------------------------------- joining
 
-// A few rows of a unit that was cut: the parts' accumulators, weighted by
-// 2^(m - max m); the weights first, so that the rest is independent loads.
-constexpr int kJoinRows = 16, kJoinThreads = 128;
+// Rows of units that were cut, a warp to a row: the parts' accumulators, weighted by
+// 2^(m - max m), in the order of the parts.
+constexpr int kJoinBlocks = 608, kJoinThreads = 128;   // four blocks on each of 152 SMs
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p, ManyWork work)
 {
-    __shared__ float weight[kJoinRows][2 * kMaxBlocks];
-    __shared__ float inv[kJoinRows];
-    if (work.cut[1] == 1 || blockIdx.x >= work.cut[0])
+    constexpr int kC = D / 32;   // channels of a lane
+    grid_wait();
+    if (work.cut[1] == 1)
         return;
-    const Unit u = work.heads[blockIdx.x];
-    const int row0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, min(kRows, u.rows - u.row0) - row0);
-    if (u.parts == 1 || rows <= 0)
-        return;
-    const int each = u.turns() ? 2 : 1, n = u.parts * each;
-    // part k of row `row` of the block: its results stand in this row of the item
-    const float *first = work.parts + u.item * kPartFloats<D>;
-    auto part_of = [&](int k) { return first + (k / each) * kPartFloats<D>; };
-    auto row_of = [&](int k, int row) { return row0 + row + 128 * (k % each); };
-    const int lane = threadIdx.x & 31;
-    for (int row = threadIdx.x >> 5; row < rows; row += kJoinThreads / 32) {
-        float mx = kNone, l = 0.0f;
+    const int lane = threadIdx.x & 31, rows = work.cut[0] * kRows;   // fewer units than blocks
+    for (int at = (blockIdx.x * kJoinThreads + threadIdx.x) >> 5; at < rows; at += kJoinBlocks * kJoinThreads / 32) {
+        const Unit &u = work.heads[at / kRows];
+        const int row = at % kRows, rr = u.row0 + row;
+        if (u.parts == 1 || rr >= u.rows)
+            continue;
+        const int each = u.turns() ? 2 : 1, n = u.parts * each;
+        // part k: its item, and its row there
+        const float *first = work.parts + u.item * kPartFloats<D>;
+        auto part_of = [&](int k) { return first + (k / each) * kPartFloats<D>; };
+        auto row_of = [&](int k) { return row + 128 * (k % each); };
+        float mx = kNone;
         for (int k = lane; k < n; k += 32)
-            mx = fmaxf(mx, part_of(k)[(size_t)kRows * D + row_of(k, row)]);
+            mx = fmaxf(mx, part_of(k)[(size_t)kRows * D + row_of(k)]);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-        for (int k = lane; k < n; k += 32) {
-            const float *stats = part_of(k) + (size_t)kRows * D + row_of(k, row);
-            const float f = exp2_fast(stats[0] - mx);
-            weight[row][k] = f;
-            l = fmaf(stats[kRows], f, l);
+        float l = 0.0f, sum[kC] = {};
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            float f = 0.0f;
+            if (k0 + lane < n) {
+                const float *stats = part_of(k0 + lane) + (size_t)kRows * D + row_of(k0 + lane);
+                f = exp2_fast(stats[0] - mx);
+                l = fmaf(stats[kRows], f, l);
+            }
+            const int here = min(32, n - k0);
+#pragma unroll 8
+            for (int k = 0; k < here; ++k) {
+                const float *o = part_of(k0 + k) + (size_t)row_of(k0 + k) * D + kC * lane;
+                const float w = __shfl_sync(0xFFFFFFFFu, f, k);
+                float v[kC];
+                if constexpr (kC == 4)
+                    *reinterpret_cast<float4 *>(v) = *reinterpret_cast<const float4 *>(o);
+                else
+                    *reinterpret_cast<float2 *>(v) = *reinterpret_cast<const float2 *>(o);
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    sum[c] = fmaf(v[c], w, sum[c]);
+            }
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1)
             l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-        if (lane == 0)
-            inv[row] = l == 0.0f ? 0.0f : 1.0f / l;
-    }
-    __syncthreads();
-    constexpr int kQuads = D / 4;
-    for (int e = threadIdx.x; e < rows * kQuads; e += kJoinThreads) {
-        const int row = e / kQuads, ch = e % kQuads * 4;
-        float4 sum = make_float4(0, 0, 0, 0);
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
-            const float4 v = *reinterpret_cast<const float4 *>(part_of(k) + (size_t)row_of(k, row) * D + ch);
-            const float f = weight[row][k];
-            sum.x = fmaf(v.x, f, sum.x);
-            sum.y = fmaf(v.y, f, sum.y);
-            sum.z = fmaf(v.z, f, sum.z);
-            sum.w = fmaf(v.w, f, sum.w);
-        }
-        const int rr = u.row0 + row0 + row, qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
-        __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
-                             (int64_t)(u.q_row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride + ch;
-        *reinterpret_cast<uint2 *>(out) =
-            make_uint2(pack_bf16(sum.x * inv[row], sum.y * inv[row]), pack_bf16(sum.z * inv[row], sum.w * inv[row]));
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
+        uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.a.out) +
+                                                     (int64_t)(u.q_row0 + qt) * p.a.out_token_stride +
+                                                     qh * p.a.out_head_stride + kC * lane);
+        if constexpr (kC == 4)
+            *reinterpret_cast<uint2 *>(out) =
+                make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
+        else
+            *out = pack_bf16(sum[0] * inv, sum[1] * inv);
     }
 }
 
@@ -1004,12 +1011,10 @@ cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
         return err;
     const ManyWork work = {reinterpret_cast<int32_t *>(ws), reinterpret_cast<Unit *>(ws + 256),
                            reinterpret_cast<float *>(ws + kHeadBytes)};
-    k_attention_many<B><<<sms < kMaxBlocks ? sms : kMaxBlocks, kThreads, smem, s>>>(p, work);
-    err = cudaGetLastError();
-    if (err == cudaSuccess) {
-        k_attention_many_join<B::kD><<<dim3(kMaxBlocks, kRows / kJoinRows), kJoinThreads, 0, s>>>(p, work);
-        err = cudaGetLastError();
-    }
+    // under the kernels for few rows: it works on other rows, with a workspace of its own
+    err = launch_under(k_attention_many<B>, dim3(sms < kMaxBlocks ? sms : kMaxBlocks), kThreads, smem, s, p, work);
+    if (err == cudaSuccess)
+        err = launch_under(k_attention_many_join<B::kD>, dim3(kJoinBlocks), kJoinThreads, 0, s, p, work);
     return err;
 }
 

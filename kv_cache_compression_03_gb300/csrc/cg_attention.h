@@ -127,6 +127,32 @@ __device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity)
 
 // ------------------------------------------------------------------ launches
 
+// A call's kernels come up under one another (programmatic stream serialization). The
+// next one may start from here on.
+__device__ __forceinline__ void grid_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Waits until the one before has ended and its results are there. Every kernel that was
+// launched so waits before it ends, in every block, so that what follows the call in the
+// stream follows all of its kernels.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... Params, typename... Args>
+cudaError_t launch_under(void (*kernel)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                         Args... args)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 // SM count of the current device, looked up once per device.
 cudaError_t attn_sm_count(int *sms);
 

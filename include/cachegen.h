@@ -378,7 +378,7 @@ cg_status cg_int8_decode(const void *q, const float *scales, int64_t rows, int32
  * Limits (CG_ERR_UNSUPPORTED): head_size 64 or 128, group 32, 64 or 128 and
  * at most head_size, page_tokens a multiple of 16 up to 1024, num_layers *
  * num_pages * num_heads and num_pages * page_tokens below 2^31, one layer's
- * bytes below 2^39. data must be
+ * bytes below 2^39, a page's below 2^32. data must be
  * 256-byte aligned. */
 typedef struct cg_int4_cache {
     void *data;
@@ -494,7 +494,8 @@ cg_status cg_pages_grow(const cg_page_batch *batch, cg_stream_t stream);
  * CG_ERR_INVALID_ARG for a request with more than max_q_len rows (left as
  * they were); CG_ERR_TIMEOUT when a bounded wait ran out.
  *
- * out must not overlap q or the cache.
+ * out must not overlap q or the cache. Sums are in fp32: scores have to stay
+ * below 2^127 there, and V values below 2^96 where a request has many rows.
  *
  * workspace (device, 256-byte aligned, the size that
  * cg_int4_attention_workspace gives; data and status pointers, q, out and

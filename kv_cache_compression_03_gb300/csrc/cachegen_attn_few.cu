@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
         float m[NT][2];              // running maximum of the scores, less ve
         int ve = kStartExp;          // p is taken times 2^ve
         float limit = 8.0f + kStartExp;
-        uint32_t par_bias = 0x80008000u - ((101 - kStartExp + 127) << 7) * 0x10001u;
+        uint32_t par_bias = 0x80008000u - ((96 - kStartExp + 127) << 7) * 0x10001u;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
             m[nt][0] = m[nt][1] = kNone;
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 }
                 // ---- the running maximum is raised only when a score exceeds it by 2^8: p stays
                 // below 2^(ve + 8) and rescaling is rare. Sums of p s and p lo have to stay finite
-                // too: s and |lo| below 2^(101 - ve), and 2^16 tokens of a warp reach 2^125.
+                // too: s and |lo| below 2^(96 - ve), and 2^21 tokens of a warp reach 2^125.
                 float over = z[0][0][0] - m[0][0];
                 uint32_t va_top = 0;
 #pragma unroll
@@ -688,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 #pragma unroll
                         for (int d = 1; d < 32; d <<= 1)
                             top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
-                        const int e = 100 - ((int)(top >> 7) - 127);   // top < 2^(101 - e)
+                        const int e = 95 - ((int)(top >> 7) - 127);   // top < 2^(96 - e)
                         const float f = pow2(e - ve);
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                         }
                         ve = e;
                         limit = 8.0f + (float)e;
-                        par_bias = 0x80008000u - (uint32_t)min((101 - e + 127) << 7, 0x7F80) * 0x10001u;
+                        par_bias = 0x80008000u - (uint32_t)min((96 - e + 127) << 7, 0x7F80) * 0x10001u;
                     }
                 }
 #pragma unroll

@@ -65,6 +65,9 @@ inline cg_status int4_check_shape(const cg_int4_cache *c)
     if ((int64_t)c->num_pages * c->num_heads >= 2 * limit / (c->page_tokens / 16) /
                                                    (int4_blob_bytes(c->head_size, c->group) / 128))
         return CG_ERR_UNSUPPORTED;
+    // so do the bytes of a page
+    if ((int64_t)c->num_heads * (c->page_tokens / 16) * int4_blob_bytes(c->head_size, c->group) >= 2 * limit)
+        return CG_ERR_UNSUPPORTED;
     return CG_OK;
 }
 

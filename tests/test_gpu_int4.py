@@ -302,14 +302,14 @@ def _batch(rng, nq, nkv, page, spare=3):
     return table, pages
 
 
-def _filled(rng, nkv, table, pages, page, heads, dim, group, layers=1, layer=0, scale=1.0):
+def _filled(rng, nkv, table, pages, page, heads, dim, group, layers=1, layer=0, scale=1.0, vscale=1.0):
     """A cache whose other places hold bytes that are no numbers."""
     want, got = _pair(layers, pages, page, heads, dim, group, fill=0xFF)
     for r, m in enumerate(nkv):
         x = np.arange(m)
         slots = table[r][x // page] * page + x % page
         k = ref.bf16_round(_rand(rng, m, heads, dim) * np.exp(0.7 * rng.standard_normal((heads, dim))) * scale)
-        want.store(layer, k, ref.bf16_round(_rand(rng, m, heads, dim) + 0.5), slots)
+        want.store(layer, k, ref.bf16_round((_rand(rng, m, heads, dim) + 0.5) * np.float32(vscale)), slots)
     _copy(want, got)
     return want, got
 
@@ -322,9 +322,9 @@ def _check_attention(out, want, tol):
 
 
 def _run(rng, nq, nkv, heads, ratio, dim, group, page, window=0, sinks=0, scale=None, most=None,
-         kscale=1.0, qscale=1.0):
+         kscale=1.0, qscale=1.0, vscale=1.0):
     table, pages = _batch(rng, nq, nkv, page)
-    want, got = _filled(rng, nkv, table, pages, page, heads, dim, group, scale=kscale)
+    want, got = _filled(rng, nkv, table, pages, page, heads, dim, group, scale=kscale, vscale=vscale)
     cu = np.concatenate([[0], np.cumsum(nq)])
     T = int(cu[-1])
     q = _rand(rng, T + 2, heads * ratio, dim, scale=qscale)
@@ -397,6 +397,12 @@ def test_attention_scales(scale, nq):
 @pytest.mark.parametrize("kscale,qscale", [(1e-30, 1.0), (1e4, 1e-4), (1e-4, 1e4), (1e30, 1e-30)])
 def test_attention_of_large_and_small_values(kscale, qscale, nq):
     _run(np.random.default_rng(5), [nq, nq], [80, 300], 1, 4, 128, 64, 16, kscale=kscale, qscale=qscale)
+
+
+@pytest.mark.parametrize("nq", [1, 80])
+@pytest.mark.parametrize("power", [-100, 5, 20, 90])
+def test_attention_of_large_and_small_values_of_v(power, nq):
+    _run(np.random.default_rng(14), [nq, nq], [90, 700], 1, 4, 128, 32, 16, vscale=2.0 ** power)
 
 
 def test_attention_layers_strides_and_other_streams():

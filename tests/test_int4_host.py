@@ -43,7 +43,8 @@ BAD_SHAPES = [(dict(num_layers=0), cg.CG_ERR_INVALID_ARG), (dict(num_pages=-1), 
               (dict(head_size=96), cg.CG_ERR_UNSUPPORTED), (dict(group=16), cg.CG_ERR_UNSUPPORTED),
               (dict(head_size=64, group=128), cg.CG_ERR_UNSUPPORTED),
               (dict(num_pages=1 << 27), cg.CG_ERR_UNSUPPORTED),
-              (dict(num_layers=1 << 15, num_pages=1 << 14), cg.CG_ERR_UNSUPPORTED)]
+              (dict(num_layers=1 << 15, num_pages=1 << 14), cg.CG_ERR_UNSUPPORTED),
+              (dict(num_layers=1, num_pages=1, num_heads=1 << 22), cg.CG_ERR_UNSUPPORTED)]
 BAD_POINTERS = [(dict(data=0), cg.CG_ERR_INVALID_ARG), (dict(data=FAKE + 128), cg.CG_ERR_INVALID_ARG),
                 (dict(status=0), cg.CG_ERR_INVALID_ARG), (dict(status=FAKE + 8), cg.CG_ERR_INVALID_ARG)]
 

@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                                 pack_bf16(o[g + 1] * inv, o[9 + g] * inv), pack_bf16(o[17 + g] * inv, o[25 + g] * inv));
                     }
                 }
-                tmem_fence_before();   // the next unit's first p_full orders these reads before its O
+                tmem_fence_before();   // the next unit's first p_half orders these reads before its O
             }
             unit_over(n);
         }

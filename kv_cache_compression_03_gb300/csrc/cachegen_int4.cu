@@ -9,10 +9,11 @@
 // is worked out once, in shared memory, so that the rest is adds.
 //
 // Measured (8 heads of 128, groups of 32): load of 16384 tokens x 32 layers at the copy
-// rate, 6.8 TB/s; store of as many 820 us, 3.4 TB/s, bound by instruction issue (3.2 of
-// 4 a cycle): 195 instructions for the 8 values of a thread, after the division per value, the
-// one per group and the addresses of each row were taken out of it (3115 us for both
-// directions before, 1227 now). 64 tokens of one layer: 4.7 us for both.
+// rate, 6.8 TB/s; store of as many 635 us, 4.4 TB/s, bound by instruction issue (3.2 of 4 a
+// cycle): 149 instructions for 8 values. What took it there from 2.4 ms: no division per value
+// or per row, pairs of fp32 in one instruction (820 -> 778 us), a head's K and V rows read at
+// once by the same threads (-> 667), six blocks on an SM at 40 registers (-> 635; seven spill).
+// 64 tokens of one layer: 4.9 us for store and load.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -125,6 +126,27 @@ __device__ __forceinline__ float scale_of(float range)
     return __bfloat162float(__float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f)));
 }
 
+// Pairs of fp32 in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // Codes of 8 values: n = rne(d / s), d = x - lo. n0 = rne(d (1 / s)) is n or, next
 // to a tie, its neighbour; e = d - n0 s is exact (both are multiples of d's last
 // bit and e is below s), so |e| against s / 2 decides, with n even where they are
@@ -140,12 +162,15 @@ __device__ __forceinline__ uint32_t codes_of_row(const float (&x)[8], float lo, 
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
     const float h = 0.5f * s;
     float r[8], e[8], top = 0.0f;
+    const float2 lo2 = make_float2(-lo, -lo), inv2 = make_float2(inv, inv), s2 = make_float2(s, s);
+    const float2 magic2 = make_float2(kMagic, kMagic), one2 = make_float2(-1.0f, -1.0f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float d = __fsub_rn(x[j], lo);
-        r[j] = __fmaf_rn(d, inv, kMagic);
-        e[j] = __fmaf_rn(__fsub_rn(kMagic, r[j]), s, d);
-        top = fmaxf(top, fabsf(e[j]));
+    for (int j = 0; j < 8; j += 2) {
+        const float2 d = add2(make_float2(x[j], x[j + 1]), lo2), n = fma2(d, inv2, magic2);
+        const float2 f = fma2(fma2(n, one2, magic2), s2, d);
+        r[j] = n.x, r[j + 1] = n.y;
+        e[j] = f.x, e[j + 1] = f.y;
+        top = fmaxf(fmaxf(top, fabsf(f.x)), fabsf(f.y));
     }
     if (top >= 0.9999f * h) {
 #pragma unroll
@@ -157,10 +182,11 @@ __device__ __forceinline__ uint32_t codes_of_row(const float (&x)[8], float lo, 
             r[j] = __uint_as_float(bits + (off ? side : 0u));
         }
     }
-    uint32_t code = 0;
+    // each r's bits are kMagicBits + n
+    uint32_t code = 0u - kMagicBits * 0x11111111u;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-        code += (__float_as_uint(r[j]) - kMagicBits) << (4 * j);
+        code += __float_as_uint(r[j]) << (4 * j);
     return code;
 }
 
@@ -175,62 +201,70 @@ __device__ __forceinline__ uint32_t codes_of_tiny_row(const float (&x)[8], float
     return code;
 }
 
-// A thread takes 8 channels (16 bytes of bf16, one word of codes); the G / 8
-// threads of a group reduce its range with shuffles.
+// A thread's 8 channels (16 bytes of bf16, one word of codes) of a row; the G / 8
+// threads of a group reduce its range with shuffles. tok < 0: no row.
+template <typename B, bool kIsV>
+__device__ __forceinline__ void store_row(const uint4 &w, int tok, int chunk, uint8_t *blob, void *status)
+{
+    const int w32 = chunk / 4, part = chunk % 4;
+    const float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y),
+                        bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
+    // the range two channels at a time; a NaN stays one through both
+    uint32_t lo2 = min2(min2(w.x, w.y), min2(w.z, w.w)), hi2 = max2(max2(w.x, w.y), max2(w.z, w.w));
+#pragma unroll
+    for (int m = 1; m < B::kG / 8; m <<= 1) {
+        lo2 = min2(lo2, __shfl_xor_sync(0xFFFFFFFFu, lo2, m));
+        hi2 = max2(hi2, __shfl_xor_sync(0xFFFFFFFFu, hi2, m));
+    }
+    if (tok < 0)
+        return;
+    lo2 = min2(lo2, __byte_perm(lo2, lo2, 0x1032));
+    hi2 = max2(hi2, __byte_perm(hi2, hi2, 0x1032));
+    float lo = bf_lo(lo2), s = scale_of(__fsub_rn(bf_lo(hi2), lo));
+    // inf or NaN in the group, or hi - lo overflows, or the largest value would round to inf
+    if (!(__fmaf_rn(15.0f, s, lo) < 0x1.FFp127f)) {
+        int4_set_status(status, CG_ERR_NONFINITE);
+        s = lo = 0.0f;
+    }
+    uint32_t code = 0;
+    if (s >= 0x1p-100f && s <= 0x1p120f)
+        code = codes_of_row(x, lo, s);
+    else if (s > 0.0f)
+        code = codes_of_tiny_row(x, lo, s);
+    if (!kIsV) {
+        *reinterpret_cast<uint32_t *>(blob + B::kKCodes + tok * (B::kD / 2) + part * (B::kD / 8) + w32 * 4) = code;
+    } else {
+        uint8_t *p = blob + B::kVCodes + (tok >> 1) * B::kD + 2 * part * (B::kD / 8) + w32 * 4 + 2 * (tok & 1);
+        *reinterpret_cast<uint16_t *>(p) = (uint16_t)code;
+        *reinterpret_cast<uint16_t *>(p + B::kD / 8) = (uint16_t)(code >> 16);
+    }
+    if (chunk % (B::kG / 8) == 0)
+        *reinterpret_cast<uint32_t *>(blob + (kIsV ? B::kVParams : B::kKParams) +
+                                      (tok * B::kGroups + chunk / (B::kG / 8)) * 4) = pack_bf16(s, lo);
+}
+
+// D / 8 threads to a head's K row and then its V row, both read at once.
 template <typename B>
-__global__ void __launch_bounds__(kThreads) k_int4_store(RowArgs a)
+__global__ void __launch_bounds__(kThreads, 6) k_int4_store(RowArgs a)
 {
     __shared__ Tile tile;
     constexpr int kChunks = B::kD / 8, kRowsAtOnce = kThreads / kChunks;
     const int n = find_tile<B>(a, tile);
-    const int chunk = threadIdx.x % kChunks, w32 = chunk / 4, part = chunk % 4;
+    const int chunk = threadIdx.x % kChunks;
     const uint32_t per_head = head_bytes<B>(a);
-    const int total = n * 2 * a.heads;
-    Walk at(threadIdx.x / kChunks, kRowsAtOnce, 2 * a.heads);
+    const int total = n * a.heads;
+    Walk at(threadIdx.x / kChunks, kRowsAtOnce, a.heads);
     for (int i = threadIdx.x / kChunks; i - threadIdx.x / kChunks < total; i += kRowsAtOnce, at.next()) {
-        const bool is_v = at.row >= a.heads;
-        const int h = is_v ? at.row - a.heads : at.row;
         const int tok = i < total ? tile.tok[at.token] : -1;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (tok >= 0)
-            w = __ldcs(reinterpret_cast<const uint4 *>(tile.row[is_v][at.token] +
-                                                       (int64_t)h * (is_v ? a.vh : a.kh)) + chunk);
-        const float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y),
-                            bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
-        // the range two channels at a time; a NaN stays one through both
-        uint32_t lo2 = min2(min2(w.x, w.y), min2(w.z, w.w)), hi2 = max2(max2(w.x, w.y), max2(w.z, w.w));
-#pragma unroll
-        for (int m = 1; m < B::kG / 8; m <<= 1) {
-            lo2 = min2(lo2, __shfl_xor_sync(0xFFFFFFFFu, lo2, m));
-            hi2 = max2(hi2, __shfl_xor_sync(0xFFFFFFFFu, hi2, m));
+        uint4 k = make_uint4(0, 0, 0, 0), v = k;
+        uint8_t *blob = nullptr;
+        if (tok >= 0) {
+            k = __ldcs(reinterpret_cast<const uint4 *>(tile.row[0][at.token] + (int64_t)at.row * a.kh) + chunk);
+            v = __ldcs(reinterpret_cast<const uint4 *>(tile.row[1][at.token] + (int64_t)at.row * a.vh) + chunk);
+            blob = tile.blob[at.token] + at.row * per_head;
         }
-        if (tok < 0)
-            continue;
-        lo2 = min2(lo2, __byte_perm(lo2, lo2, 0x1032));
-        hi2 = max2(hi2, __byte_perm(hi2, hi2, 0x1032));
-        float lo = bf_lo(lo2), s = scale_of(__fsub_rn(bf_lo(hi2), lo));
-        // inf or NaN in the group, or hi - lo overflows, or the largest value would round to inf
-        if (!(__fmaf_rn(15.0f, s, lo) < 0x1.FFp127f)) {
-            int4_set_status(a.status, CG_ERR_NONFINITE);
-            s = lo = 0.0f;
-        }
-        uint32_t code = 0;
-        if (s >= 0x1p-100f && s <= 0x1p120f)
-            code = codes_of_row(x, lo, s);
-        else if (s > 0.0f)
-            code = codes_of_tiny_row(x, lo, s);
-        uint8_t *blob = tile.blob[at.token] + h * per_head;
-        if (!is_v) {
-            *reinterpret_cast<uint32_t *>(blob + B::kKCodes + tok * (B::kD / 2) + part * (B::kD / 8) + w32 * 4) =
-                code;
-        } else {
-            uint8_t *p = blob + B::kVCodes + (tok >> 1) * B::kD + 2 * part * (B::kD / 8) + w32 * 4 + 2 * (tok & 1);
-            *reinterpret_cast<uint16_t *>(p) = (uint16_t)code;
-            *reinterpret_cast<uint16_t *>(p + B::kD / 8) = (uint16_t)(code >> 16);
-        }
-        if (chunk % (B::kG / 8) == 0)
-            *reinterpret_cast<uint32_t *>(blob + (is_v ? B::kVParams : B::kKParams) +
-                                          (tok * B::kGroups + chunk / (B::kG / 8)) * 4) = pack_bf16(s, lo);
+        store_row<B, false>(k, tok, chunk, blob, a.status);
+        store_row<B, true>(v, tok, chunk, blob, a.status);
     }
 }
 

@@ -498,8 +498,8 @@ cg_status cg_pages_grow(const cg_page_batch *batch, cg_stream_t stream);
  * below 2^127 there, and V values below 2^96 where a request has many rows.
  *
  * workspace (device, 256-byte aligned, the size that
- * cg_int4_attention_workspace gives; data and status pointers, q, out and
- * the device arrays are not looked at there) is scratch: calls that may
+ * cg_int4_attention_workspace gives from the cache's shape, tokens, q_heads and
+ * max_q_len; it looks at no pointer) is scratch: calls that may
  * overlap need one each. Asynchronous on stream. */
 typedef struct cg_attention {
     const void *q;

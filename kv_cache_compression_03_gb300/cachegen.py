@@ -785,6 +785,7 @@ class Int4Cache:
         self._c.data, self._c.status = data.data_ptr(), self.status.data_ptr()
         self.num_layers, self.num_pages, self.page_tokens = num_layers, num_pages, page_tokens
         self.num_heads, self.head_size, self.group = num_heads, head_size, group
+        self._sizes = {}   # workspace of attention calls, by their rows
 
     def _rows(self, k, v, tokens, layers, written):
         shape = (tokens, self.num_heads, self.head_size)
@@ -879,10 +880,16 @@ class Int4Cache:
                             block_table.data_ptr(), stride, width, n, tokens, q_heads,
                             max_q_len or 0, window, sinks, D ** -0.5 if scale is None else scale)
         L = _lib or load()
-        need = ct.c_size_t(0)
-        _check(L.cg_int4_attention_workspace(self._ref, a, ct.byref(need)),
-               "cg_int4_attention_workspace")
-        size, ws, ws_at = need.value, None, None
+        # the size depends on the most rows that a request can have per KV head, and on the cache
+        rows = (min(max_q_len, tokens) if max_q_len else tokens) * q_heads // self.num_heads
+        size, ws, ws_at = self._sizes.get(rows), None, None
+        if size is None:
+            need = ct.c_size_t(0)
+            _check(L.cg_int4_attention_workspace(self._ref, a, ct.byref(need)),
+                   "cg_int4_attention_workspace")
+            if len(self._sizes) >= 1024:
+                self._sizes.clear()
+            size = self._sizes[rows] = need.value
         if size:
             # one per call, from the current stream's pool: calls on other
             # streams and captured graphs never share one

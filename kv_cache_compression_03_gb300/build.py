@@ -90,8 +90,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 
 def build_test_variant(name: str, defines) -> str:
-    """A library compiled with test-only macros (cachegen_kernels.cu names
-    them: each forces a rarely taken path, an exact fallback or a bounded
+    """A library compiled with test-only macros (cachegen_kernels.cu and
+    cg_attention.h name them: each forces a rarely taken path, an exact fallback or a bounded
     wait that runs out), in _build/<name>/. For the tests; the product
     library never sets them."""
     return _build_into(os.path.join(OUT_DIR, name), tuple(defines))

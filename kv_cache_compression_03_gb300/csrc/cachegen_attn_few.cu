@@ -552,12 +552,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
         warp_range(u, warp, &b, &e);
         for (; b < e; b += HB) {
             const int st = used & (kStages - 1);
-            if (alive &&
-                !__all_sync(0xFFFFFFFFu, bar_wait(&sm.full[warp][st], (used / kStages) & 1))) {
-                alive = false;
-                int4_set_status(p.status, CG_ERR_TIMEOUT);
+            if (alive) {
+                const bool give_up = kTestTimeout && used == 1;
+                if (give_up || !__all_sync(0xFFFFFFFFu, bar_wait(&sm.full[warp][st], (used / kStages) & 1))) {
+                    alive = false;   // `used` stays: the first step not waited for
+                    int4_set_status(p.status, CG_ERR_TIMEOUT);
+                } else {
+                    ++used;
+                }
             }
-            ++used;
             const uint32_t there = ahead & ((1u << HB) - 1);
             if (alive && there) {
                 const uint8_t *ring = sm.ring[warp][st];
@@ -860,7 +863,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             break;
         unit_next<RU>(p, count - pos, &u);
     }
-    // a wait that ran out: the copies still in flight must land before the block's memory goes
+    // a wait that ran out: the copies still in flight, of the steps from that one on, must
+    // land before the block's memory goes
     if (!alive)
         for (; used < issued; ++used)
             bar_wait(&sm.full[warp][used & (kStages - 1)], (used / kStages) & 1);

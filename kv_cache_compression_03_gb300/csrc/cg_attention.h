@@ -82,6 +82,15 @@ __device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t b
 // the wait ends at once. Each poll may suspend the thread for a while.
 constexpr uint64_t kBarWaitNs = 1000000000ull;
 
+// Test builds (CG_TEST_ATTN_TIMEOUT) give up chosen waits at once, with copies and
+// products in flight that are all valid and complete: what a block does then must be
+// right in the product build too, where no test can make a wait run out.
+#ifdef CG_TEST_ATTN_TIMEOUT
+constexpr bool kTestTimeout = true;
+#else
+constexpr bool kTestTimeout = false;
+#endif
+
 __device__ __forceinline__ bool bar_poll(uint32_t at, uint32_t parity)
 {
     uint32_t done;

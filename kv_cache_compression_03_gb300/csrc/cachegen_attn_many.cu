@@ -272,12 +272,14 @@ struct ManyWork {
 template <int D>
 constexpr size_t kPartFloats = (size_t)kRows * (D + 2);
 
-// Waits that end: false once this wait or another one of the block ran out.
+// Waits that end: false once this wait or another one of the block ran out. The role that
+// gets false leaves for good: the other ones then wait for arrivals that do not come, until
+// they leave too, and no barrier is ever taken for a phase that it is not in.
 __device__ __forceinline__ bool wait_or_leave(uint64_t *bar, uint32_t parity, uint32_t *gave_up,
-                                              void *status)
+                                              void *status, bool at_once = false)
 {
     const uint32_t at = smem_addr(bar);
-    if (bar_poll(at, parity) || bar_wait_long(at, parity, gave_up))
+    if (!at_once && (bar_poll(at, parity) || bar_wait_long(at, parity, gave_up)))
         return true;
     if (*reinterpret_cast<volatile uint32_t *>(gave_up))
         return false;
@@ -434,12 +436,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
     // so that the next unit's queries, keys and values come in under the last one's products.
     uint32_t un = 0;             // units begun
     uint32_t tiles_done = 0;     // K and V tiles of earlier units
-    auto wait = [&](uint64_t *bar, uint32_t parity) {   // one thread's view
-        return wait_or_leave(bar, parity, &sm.gave_up, p.status);
+    auto wait = [&](uint64_t *bar, uint32_t parity, bool at_once = false) {   // one thread's view
+        return wait_or_leave(bar, parity, &sm.gave_up, p.status, at_once);
     };
-    auto wait_all = [&](uint64_t *bar, uint32_t parity) {   // the warp's
-        return __all_sync(0xFFFFFFFFu, wait_or_leave(bar, parity, &sm.gave_up, p.status));
+    auto wait_all = [&](uint64_t *bar, uint32_t parity, bool at_once = false) {   // the warp's
+        return __all_sync(0xFFFFFFFFu, wait_or_leave(bar, parity, &sm.gave_up, p.status, at_once));
     };
+    // test builds: which role of this block gives up
+    auto gives_up = [&](uint32_t role) { return kTestTimeout && blockIdx.x % 4 == role; };
+    uint32_t issued = 0;         // blobs whose copies the copying warp has issued
     auto next_unit = [&]() -> const Unit * {   // the warp's next unit, or none
         if (!wait_all(&sm.u_full[un % kUnits], un / kUnits & 1))
             return nullptr;
@@ -477,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                 float m = kNone, l = 0.0f;
                 bool alive = true;
                 for (int j = first; j < n; j += step) {
-                    alive = wait_all(&sm.s_full[i], s_done & 1);
+                    alive = wait_all(&sm.s_full[i], s_done & 1, gives_up(0) && s_done == 1);
                     ++s_done;
                     if (!alive)
                         break;
@@ -726,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                     // the barrier's parity would say the same as when this one is there: so first, that
                     // this one was issued, which it is only into a place that was read.
                     alive = __all_sync(0xFFFFFFFFu, blob_issued(slot, at)) &&
-                            wait_all(&sm.raw_full[slot], at / kRing & 1) &&
+                            wait_all(&sm.raw_full[slot], at / kRing & 1, gives_up(1) && at == 5) &&
                             wait_all(&sm.k_empty[sl], (use >> 1 & 1) ^ 1);
                     if (!alive)
                         break;
@@ -791,7 +796,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                     }
                 }
                 if (alive && !have_q)
-                    queries();
+                    alive = queries();
+                if (!alive)
+                    break;
                 seq += n * kBlobs;
                 unit_over(n);
             }
@@ -799,18 +806,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
             // ======================================================= units, copies
             int u_r0 = 0;
             int64_t u_before = 0;
-            uint32_t issued = 0;         // blobs
-            auto find = [&](uint32_t which) {
+            auto find = [&](uint32_t which) {   // false: a wait ran out
                 const uint32_t slot = which % kUnits;
                 if (!wait_all(&sm.u_empty[slot], (which / kUnits & 1) ^ 1))
-                    return;
+                    return false;
                 find_unit(p, blockIdx.x + (int64_t)which * gridDim.x, split, &u_r0, &u_before, &sm.unit[slot],
                           work.heads);
                 if (lane == 0)
                     bar_arrive(&sm.u_full[slot]);
                 __syncwarp();
+                return true;
             };
-            find(0);
+            find(0);   // a place that was never used: no wait
             while (const Unit *up = next_unit()) {
                 const Unit &u = *up;
                 const int32_t *table = p.a.block_table + u.r * p.a.table_stride;
@@ -834,7 +841,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                     // kIssue at a time: as many lanes wait for a place in the ring each, and copy
                     for (int k = 0; k < count; k += kIssue) {
                         const uint32_t at = issued + lane % kIssue, slot = at % kRing;
-                        alive = wait_all(&sm.raw_empty[slot], (at / kRing & 1) ^ 1);
+                        alive = wait_all(&sm.raw_empty[slot], (at / kRing & 1) ^ 1, gives_up(2) && issued == kRing);
                         if (!alive)
                             break;
                         issued += kIssue;
@@ -854,17 +861,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         }
                         __syncwarp();
                     }
-                    if (b0 == 0)
-                        find(un + 1);
+                    if (b0 == 0 && alive)
+                        alive = find(un + 1);
                 }
                 if (n == 0)
-                    find(un + 1);
+                    alive = find(un + 1);
+                if (!alive)
+                    break;
                 unit_over(n);
             }
-            // after a wait that ran out: the copies in flight land before the block's memory goes
-            if (sm.gave_up)
-                for (uint32_t at = issued < kRing ? 0 : issued - kRing; at < issued; ++at)
-                    bar_wait(&sm.raw_full[at % kRing], at / kRing & 1);
         } else {
             // ========================================================== products
             const uint32_t q_at = smem_addr(sm.q[0]), k_at = smem_addr(sm.k[0]), v_at = smem_addr(sm.v[0]);
@@ -882,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
             while (const Unit *up = next_unit()) {
                 const int n = up->n, tiles_q = up->tiles_q;
                 const bool turns = up->turns();
+                bool left = false;       // a wait ran out
                 if (elect_one()) {
                     // O of accumulator i, with the V tile of the t-th tile of all
                     auto values = [&](int i, int half, uint32_t t, bool add) {
@@ -898,8 +904,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         p_done ^= 1u << i;
                         return ok;
                     };
-                    auto half_there = [&](int i) {
-                        return wait(&sm.p_half[i], p_done >> i & 1);
+                    auto half_there = [&](int i, bool at_once) {
+                        return wait(&sm.p_half[i], p_done >> i & 1, at_once);
                     };
                     bool alive = wait(&sm.q_full, un & 1);
                     const uint32_t t0 = tiles_done;
@@ -926,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         const bool more = j + head < n;
                         for (int k = 0; k < (turns ? 1 : tiles_q); ++k) {
                             const int i = turns ? j & 1 : k;
-                            alive = half_there(i);
+                            alive = half_there(i, gives_up(3) && t == 1);
                             if (alive && k == 0)
                                 alive = v_there(t);
                             if (!alive)
@@ -953,19 +959,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         if (alive && j + head + 1 == n)
                             mma_commit(&sm.q_empty);
                     }
+                    left = !alive;
                 }
+                if (__any_sync(0xFFFFFFFFu, left))
+                    break;
                 unit_over(n);
             }
-            // products still in flight (after a wait that ran out) end before the memory goes
-            if (sm.gave_up && lane == 0) {
+        }
+    }
+    tmem_fence_before();
+    __syncthreads();
+    // Every role has left, so nothing is issued any more. After a wait that ran out, whichever
+    // role it was, what is in flight ends before shared and tensor memory go.
+    if (sm.gave_up) {
+        if (warp == kSoftWarps + kExpandWarps) {
+            for (uint32_t at = issued < kRing ? 0 : issued - kRing; at < issued; ++at)
+                bar_wait(&sm.raw_full[at % kRing], at / kRing & 1);
+        } else if (warp == kWarps - 1) {
+            if (elect_one()) {   // the thread that issued the products
                 mma_commit(&sm.last);
                 bar_wait(&sm.last, 0);
             }
             __syncwarp();
         }
+        __syncthreads();
     }
-    tmem_fence_before();
-    __syncthreads();
     if (warp == kWarps - 1) {
         tmem_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(sm.tmem) : "memory");

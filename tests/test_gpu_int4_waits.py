@@ -21,7 +21,9 @@ def variant():
 
 
 # Single tokens: every warp gives up its second step, with more behind it than its ring holds.
-@pytest.mark.parametrize("nq,ratio", [(1, 4), (1, 16)])
+# 64 and 16 rows of a KV head, 256: the softmax, an expanding warp, the copying warp or the
+# issuing thread, by the block; one row tile in turns, and two, both cut into pieces.
+@pytest.mark.parametrize("nq,ratio", [(1, 4), (1, 16), (16, 4), (64, 4)])
 @pytest.mark.parametrize("dim,group", [(128, 32), (64, 64)])
 def test_a_wait_that_runs_out_is_reported(variant, nq, ratio, dim, group):
     rng = np.random.default_rng(nq)

@@ -495,7 +495,9 @@ cg_status cg_pages_grow(const cg_page_batch *batch, cg_stream_t stream);
  * they were); CG_ERR_TIMEOUT when a bounded wait ran out.
  *
  * out must not overlap q or the cache. Sums are in fp32: scores have to stay
- * below 2^127 there, and V values below 2^96 where a request has many rows.
+ * below 2^127 there, and V values below 2^96 where a request has more than 32
+ * rows per KV head (query heads of it times new tokens), below 2^126 where it
+ * has fewer.
  *
  * workspace (device, 256-byte aligned, the size that
  * cg_int4_attention_workspace gives from the cache's shape, tokens, q_heads and

@@ -11,8 +11,10 @@
 // or the first binade) is those bits times 2^-133, so the codes of bits 0..3 are
 // n 2^-133 and those of bits 4..7 are n 2^-129 where they lie. The powers of two
 // come off exactly: queries are scaled per row (and by 1/16 at the channels
-// of the upper codes) so that their largest is near 2^126, p by 2^90 (less where
-// a large s or lo would overflow), and results by the inverse. What is summed
+// of the upper codes) so that their largest is near 2^126, p by 2^ve: 2^90, less where
+// a large s or lo would overflow. Results keep their factor through both joins, so that
+// no sum of p times a value leaves fp32's range whatever the value, and lose it together
+// with sum p. What is summed
 // beside the codes is summed by matrix instructions too: lo (sum q) with sum q
 // in two or three bf16 parts (16 bits at least), sum p s, sum p lo, sum p and
 // sum p s 8 as rows of one small accumulator, with p in two bf16 parts as well.
@@ -337,11 +339,15 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
 
 // ---------------------------------------------------------------- workspace
 
-// Partial results: [block][2] of { float o[RU][D]; float m[RU]; float l[RU]; }.
-// Slot 0 of a block belongs to a unit that began in an earlier block, slot 1
-// to one that goes on in the next.
+// Partial results: [block][2] of { float o[RU][D]; float4 (m, l, ve, unused)[RU]; },
+// o times 2^(ve - kRoom). Slot 0 of a block belongs to a unit that began in an earlier
+// block, slot 1 to one that goes on in the next.
 template <int D, int RU>
-constexpr int kPartFloats = RU *(D + 2);
+constexpr int kPartFloats = RU *(D + 4);
+
+// A warp's sums stay below 2^128 (see where the maximum is raised); four warps and up to
+// kFewMaxBlocks parts are added with factors of at most 1.
+constexpr int kRoom = 16;
 
 // ------------------------------------------------------------- main kernel
 
@@ -354,6 +360,7 @@ struct FewShared {
     uint8_t ring[kWarps][kStages][HB * B::kBytes];
     float merge[kWarps][RU][B::kD / NT];   // one of NT parts of the channels
     float m[kWarps][RU], l[kWarps][RU];
+    int32_t ve[kWarps];
     uint64_t full[kWarps][kStages];
 };
 
@@ -651,7 +658,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 }
                 // ---- the running maximum is raised only when a score exceeds it by 2^8: p stays
                 // below 2^(ve + 8) and rescaling is rare. Sums of p s and p lo have to stay finite
-                // too: s and |lo| below 2^(96 - ve), and 2^21 tokens of a warp reach 2^125.
+                // too: s and |lo| below 2^(96 - ve), and 2^21 tokens of a warp reach 2^125. (What
+                // 2^-ve would make of them is not formed before they are divided by sum p.)
                 float over = z[0][0][0] - m[0][0];
                 uint32_t va_top = 0;
 #pragma unroll
@@ -767,15 +775,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 
         // ---- the warps' results of this unit, joined in shared memory
         const float down = pow2(-ve);
-        float off[NT][NG][2], ex[NT][NG][2];   // sum p (lo + 8 s); sum p s 8, as o counts it
+        float off[NT][NG][2], ex[NT][NG][2];   // sum p (lo + 8 s) 2^-kRoom; sum p s 8, as o counts it
+        if (lane == 0)
+            sm.ve[warp] = ve;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
-                    off[nt][gi][j] = (8.0f * __shfl_sync(0xFFFFFFFFu, aux[nt][j], 4 * gi + t) +
-                                      __shfl_sync(0xFFFFFFFFu, aux[nt][j], 4 * (NG + gi) + t)) * down;
+                    const float ps = __shfl_sync(0xFFFFFFFFu, aux[nt][j], 4 * gi + t);
+                    const float pl = __shfl_sync(0xFFFFFFFFu, aux[nt][j], 4 * (NG + gi) + t);
+                    off[nt][gi][j] = fmaf(ps, pow2(3 - kRoom), pl * pow2(-kRoom));
                     ex[nt][gi][j] = __shfl_sync(0xFFFFFFFFu, aux[nt][2 + j], 4 * gi + t);
                 }
                 m[nt][j] += (float)ve;
@@ -788,6 +799,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
         const bool from_before = u.b0 > 0, goes_on = u.b1 < u.span.nb;
         float *part = parts + ((size_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * kPartFloats<D, RU>;
         const int rows_here = last_row - row_base + 1;
+        // the warps' results come to the least of their factors
+        int v_least = ve;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            v_least = min(v_least, sm.ve[w]);
+        const float level = pow2(v_least - ve);
         float f[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -797,10 +814,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
                     mx = fmaxf(mx, sm.m[w][8 * nt + 2 * t + j]);
-                f[nt][j] = exp2_fast(m[nt][j] - mx);
+                f[nt][j] = exp2_fast(m[nt][j] - mx) * level;
             }
         constexpr int kPartW = NW / NT;   // words (32 channels) of a pass
-        const float down0 = pow2(66), down1 = pow2(67 - ve);   // 2^(133 - ve) in two steps
+        const float up = pow2(133 - kRoom);
 #pragma unroll
         for (int pass = 0; pass < NT; ++pass) {
 #pragma unroll
@@ -812,10 +829,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                         const int ww = pass * kPartW + w, gi = ww / WPG;
                         const float e8 = ex[nt][gi][j], add = off[nt][gi][j];
                         float4 v;    // channels 4g .. 4g + 3; the upper codes counted 16-fold
-                        v.x = (o[2 * ww][nt][j] - e8) * down0 * down1;
-                        v.y = (fmaf(o[2 * ww][nt][2 + j], 0.0625f, -e8)) * down0 * down1;
-                        v.z = (o[2 * ww + 1][nt][j] - e8) * down0 * down1;
-                        v.w = (fmaf(o[2 * ww + 1][nt][2 + j], 0.0625f, -e8)) * down0 * down1;
+                        v.x = (o[2 * ww][nt][j] - e8) * up;
+                        v.y = (fmaf(o[2 * ww][nt][2 + j], 0.0625f, -e8)) * up;
+                        v.z = (o[2 * ww + 1][nt][j] - e8) * up;
+                        v.w = (fmaf(o[2 * ww + 1][nt][2 + j], 0.0625f, -e8)) * up;
                         v = make_float4((v.x + add) * f[nt][j], (v.y + add) * f[nt][j],
                                         (v.z + add) * f[nt][j], (v.w + add) * f[nt][j]);
                         *reinterpret_cast<float4 *>(&sm.merge[warp][8 * nt + 2 * t + j][32 * w + 4 * g]) = v;
@@ -843,11 +860,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 if (from_before || goes_on) {
                     *reinterpret_cast<float4 *>(part + row * D + ch) = sum;
                     if (pass == 0 && c == 0) {
-                        part[RU * D + row] = mx;
-                        part[RU * D + RU + row] = ls;
+                        reinterpret_cast<float4 *>(part + RU * D)[row] = make_float4(mx, ls, (float)v_least, 0.0f);
                     }
                 } else {
-                    const float inv = ls == 0.0f ? 0.0f : 1.0f / ls;
+                    const float inv = ls == 0.0f ? 0.0f : pow2(kRoom - v_least) / ls;
                     const int rr = row_base + row, qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
                     __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
                                          (int64_t)(u.q.row0 + qt) * p.a.out_token_stride +
@@ -875,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 // Block c joins the unit that begins in block c of the main kernel and goes
 // on behind it, if there is one.
 template <int D, int RU>
-__global__ void __launch_bounds__(kThreads) k_attention_join(AttnArgs p, int pieces, const float *parts)
+__global__ void __launch_bounds__(kThreads, 8) k_attention_join(AttnArgs p, int pieces, const float *parts)
 {
     grid_next();
     int64_t total, chunk;
@@ -893,28 +909,37 @@ __global__ void __launch_bounds__(kThreads) k_attention_join(AttnArgs p, int pie
     const int last = (int)((end + chunk - 1) / chunk) - 1;   // the block that holds its end
     const int row_base = u.rt * RU;
     const int rows_here = (row_base + RU < u.q.rows ? row_base + RU : u.q.rows) - row_base;
-    // weights of the parts: 2^(m - max m), and the sums that they give
+    // weights of the parts: 2^(m - max m), to the least of their factors, and the sums that they give
     extern __shared__ float weight[];   // [RU][parts]
     __shared__ float inv[RU];
     const int n = last - c + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    auto stats = [&](int k, int row) {
+        const float *part = parts + ((size_t)(c + k) * 2 + (k == 0)) * kPartFloats<D, RU>;
+        return reinterpret_cast<const float4 *>(part + RU * D)[row];
+    };
     for (int row = warp; row < rows_here; row += kWarps) {
-        float mx = kNone, l = 0.0f;
-        for (int k = lane; k < n; k += 32)
-            mx = fmaxf(mx, parts[((size_t)(c + k) * 2 + (k == 0)) * kPartFloats<D, RU> + RU * D + row]);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+        float mx = kNone, l = 0.0f, least = (float)kStartExp;
         for (int k = lane; k < n; k += 32) {
-            const float *part = parts + ((size_t)(c + k) * 2 + (k == 0)) * kPartFloats<D, RU> + RU * D;
-            const float e = exp2_fast(part[row] - mx);
-            weight[row * n + k] = e;
-            l = fmaf(part[RU + row], e, l);
+            const float4 part = stats(k, row);
+            mx = fmaxf(mx, part.x);
+            least = fminf(least, part.z);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
+            least = fminf(least, __shfl_xor_sync(0xFFFFFFFFu, least, d));
+        }
+        for (int k = lane; k < n; k += 32) {
+            const float4 part = stats(k, row);
+            const float e = exp2_fast(part.x - mx);
+            weight[row * n + k] = e * pow2((int)(least - part.z));
+            l = fmaf(part.y, e, l);
         }
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1)
             l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
         if (lane == 0)
-            inv[row] = l == 0.0f ? 0.0f : 1.0f / l;
+            inv[row] = l == 0.0f ? 0.0f : pow2(kRoom - (int)least) / l;
     }
     __syncthreads();
     constexpr int kQuads = D / 4;
@@ -972,7 +997,7 @@ cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
 size_t attn_few_workspace(int head_size, int max_rows)
 {
     const int ru = tile_rows(max_rows);
-    return (size_t)kFewMaxBlocks * 2 * ru * (head_size + 2) * sizeof(float);
+    return (size_t)kFewMaxBlocks * 2 * ru * (head_size + 4) * sizeof(float);
 }
 
 cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max_rows, void *ws,

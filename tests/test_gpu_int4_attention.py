@@ -122,3 +122,45 @@ def test_a_query_finds_its_token(nq, nkv, ratio, window, sinks, dim):
     out = _out(got, q, cu, nkv, table, window=window, sinks=sinks, scale=scale)
     # p s, p and the result to bf16: 2^-8 of 8, three times
     assert np.abs(out - o)[clear].max() <= 3 * 8 * bounds.U + 0.01
+
+
+@pytest.mark.parametrize("dim,group,ratio", [(128, 32, 4), (64, 64, 4), (128, 64, 16)])
+@pytest.mark.parametrize("power", [96, 112, 122])
+def test_large_values_of_v(dim, group, ratio, power):
+    """Few rows: equal scores, so that the sum of p V passes fp32's range long before V does."""
+    rng = np.random.default_rng(power)
+    heads, page, nq, nkv = 2, 32, [1, 2, 1, 1], [256, 700, 9001, 70000]
+    table, pages = _batch(rng, nq, nkv, page)
+    want, got = _pair(1, pages, page, heads, dim, group, fill=0xFF)
+    for r, m in enumerate(nkv):
+        x = np.arange(m)
+        v = bounds.whole_numbers(rng, m, heads, dim, group=group) * np.float32(2.0 ** power)
+        want.store(0, _rand(rng, m, heads, dim), v, table[r][x // page] * page + x % page)
+    _copy(want, got)
+    cu = np.concatenate([[0], np.cumsum(nq)])
+    out = _out(got, np.zeros((5, heads * ratio, dim), np.float32), cu, nkv, table, max_q_len=2)
+    o, tol = bounds.counted(want, 0, cu, nkv, table, 0, 0, heads, ratio)
+    assert np.isfinite(out).all() and (np.abs(out - o) <= tol).all()
+
+
+@pytest.mark.parametrize("dim,group,ratio", [(128, 32, 4), (64, 64, 16)])
+def test_values_of_v_of_every_size_side_by_side(dim, group, ratio):
+    """Stretches of tokens at 1, 2^20, 2^60 and 2^120: warps and parts come together with factors
+    of their own. Under the window a request sees one or two of the sizes."""
+    rng = np.random.default_rng(dim)
+    heads, page, window = 1, 16, 700
+    nq, nkv = [1] * 6, [900, 2000, 2900, 3900, 1300, 60]
+    powers = [0, 20, 60, 120]
+    table, pages = _batch(rng, nq, nkv, page)
+    want, got = _pair(1, pages, page, heads, dim, group, fill=0xFF)
+    for r, m in enumerate(nkv):
+        x = np.arange(m)
+        v = _rand(rng, m, heads, dim) * np.exp2(np.array(powers)[x // 1000])[:, None, None]
+        want.store(0, _rand(rng, m, heads, dim), ref.bf16_round(v.astype(np.float32)), table[r][x // page] * page + x % page)
+    _copy(want, got)
+    cu = np.arange(7)
+    q = _rand(rng, 6, heads * ratio, dim)
+    for w in (0, window):
+        out = _out(got, q, cu, nkv, table, window=w, max_q_len=1)
+        o, most, _ = bounds.attention(want, 0, q, cu, nkv, table, w, 0, dim ** -0.5)
+        assert np.isfinite(out).all() and (np.abs(out - o) <= most).all()

@@ -269,9 +269,12 @@ __global__ void __launch_bounds__(kThreads, 6) k_int4_store(RowArgs a)
 }
 
 // lo + s n for the codes i and i + 4 of a word. n comes exact out of the mantissa
-// of 128 + n, and one rounding to bf16 gives what fp32 and then bf16 would: s n
-// has 12 bits, so where the sum does not fit fp32, s n is far below half a last
-// bit of lo.
+// of 128 + n, s n has 12 bits, and one rounding to bf16 gives what the format's two (to fp32,
+// then to bf16) give wherever fp32 holds the sum, and where s n is far below half a last bit
+// of lo. What is left is a lo that fp32 drops next to an s n halfway between two bf16
+// values, which is then rounded to the even one: the rows with such a group, which data
+// hardly has, are found by tiny_lo() and written once more by load_twice_rounded().
+// (Both roundings for every code: 254 -> 318 us for 32768 tokens, 40 layers of 2 heads.)
 __device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32_t lo)
 {
     const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
@@ -279,6 +282,16 @@ __device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32
     asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(x), "r"(0x43004300u));
     asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(n), "r"(s), "r"(lo));
     return y;
+}
+
+// Not 0 where lo != 0 is at most half a last bit of fp32 at 15 s: 2^20 |lo| < s, for pairs.
+__device__ __forceinline__ uint32_t tiny_lo(uint32_t s, uint32_t lo)
+{
+    const uint32_t size = lo & 0x7FFF7FFFu;
+    uint32_t big, less;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(big) : "r"(size), "r"(0x49804980u));
+    asm("set.lt.u32.bf16x2 %0, %1, %2;" : "=r"(less) : "r"(big), "r"(s));   // all bits of a half
+    return less & size;
 }
 
 template <int N>
@@ -299,6 +312,40 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
     }
 }
 
+// The block's rows as k_int4_load writes them, by the same threads, with both roundings. A
+// loop of few registers: it is there for correctness alone.
+template <typename B>
+__device__ __forceinline__ void load_twice_rounded(const RowArgs &a, const Tile &tile, int n)
+{
+#pragma unroll 1
+    for (int v = 0; v < 2; ++v) {
+        const int per_row = v ? 8 : 4, chan = v ? 4 : 8;   // threads of a row, channels of a word
+        const int g = threadIdx.x % per_row;
+        // V's threads take two tokens at a time
+        Walk at(threadIdx.x / per_row, kThreads / per_row, a.heads);
+#pragma unroll 1
+        for (; (v + 1) * at.token < n; at.next())
+#pragma unroll 1
+            for (int t = (v + 1) * at.token; t < (v + 1) * (at.token + 1) && t < n; ++t) {
+                const int tok = tile.tok[t];
+                if (tok < 0)
+                    continue;
+                const uint8_t *blob = tile.blob[t] + at.row * head_bytes<B>(a);
+                const uint8_t *codes = blob + (v ? B::kVCodes + (tok >> 1) * B::kD + 2 * (tok & 1)
+                                                 : B::kKCodes + tok * (B::kD / 2)) + g * (B::kD / 8);
+                const uint8_t *pars = blob + (v ? B::kVParams : B::kKParams) + tok * 4 * B::kGroups;
+                uint16_t *to = tile.row[v][t] + (int64_t)at.row * (v ? a.vh : a.kh) + chan * g;
+#pragma unroll 1
+                for (int i = 0; i < B::kWords * chan; ++i) {
+                    const int w = i / chan, c = i - w * chan;
+                    const uint32_t code = codes[4 * w + c / 2] >> (4 * (c & 1)) & 15u;
+                    const uint32_t q = *reinterpret_cast<const uint32_t *>(pars + 4 * (32 * w / B::kG));
+                    to[32 * w + c] = (uint16_t)pack_bf16(__fmaf_rn((float)code, par_s(q), par_lo(q)), 0.0f);
+                }
+            }
+    }
+}
+
 // K: four threads to a row, each the words of its eighth channels (16 bytes of
 // codes at D = 128, 16-byte stores). V: eight threads to a row and two tokens at
 // a time, since the cache keeps pairs of tokens in one word; where the tokens are
@@ -310,6 +357,7 @@ __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
     constexpr int NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
     const int n = find_tile<B>(a, tile);
     const uint32_t per_head = head_bytes<B>(a);
+    uint32_t tiny = 0;
     {
         const int t = threadIdx.x & 3;
         Walk at(threadIdx.x / 4, kThreads / 4, a.heads);
@@ -329,6 +377,7 @@ __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const uint32_t q = par[w / WPG], s = __byte_perm(q, q, 0x1010), lo = __byte_perm(q, q, 0x3232);
+                tiny |= tiny_lo(s, lo);
                 const uint32_t y0 = expand(code[w], 0, s, lo), y1 = expand(code[w], 1, s, lo);
                 const uint32_t y2 = expand(code[w], 2, s, lo), y3 = expand(code[w], 3, s, lo);
                 __stcs(reinterpret_cast<uint4 *>(dst + 32 * w),
@@ -366,6 +415,7 @@ __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
                 for (int w = 0; w < NW; ++w) {
                     const uint32_t s = __byte_perm(par0[w / WPG], par1[w / WPG], 0x5410);
                     const uint32_t lo = __byte_perm(par0[w / WPG], par1[w / WPG], 0x7632);
+                    tiny |= tiny_lo(s, lo);
                     const uint32_t y0 = expand(code[w], 0, s, lo), y1 = expand(code[w], 1, s, lo);
                     const uint32_t y2 = expand(code[w], 2, s, lo), y3 = expand(code[w], 3, s, lo);
                     const uint2 even = make_uint2(__byte_perm(y0, y1, 0x5410), __byte_perm(y2, y3, 0x5410));
@@ -377,6 +427,8 @@ __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
             }
         }
     }
+    if (tiny)
+        load_twice_rounded<B>(a, tile, n);
 }
 
 // Checks of both calls; *work is false where there is nothing to do.

@@ -669,3 +669,28 @@ def test_a_restored_cache_is_attended_and_grown():
     again = c2.decode(c2.encode(blob))
     step64 = blob.float().abs().amax((3, 4), keepdim=True) / 7      # half a step of the 16-bin layers
     assert bool(((again.float() - blob.float()).abs() <= step64).all())
+
+
+@pytest.mark.parametrize("dim,group", FORMATS)
+def test_load_rounds_to_fp32_and_then_to_bf16(dim, group):
+    """|lo| so small that fp32 drops it next to s n, which lies halfway between two bf16 values
+    for some codes: the format's value is then the even one, not the one on lo's side."""
+    top = 1 + np.arange(128) / 128                        # a binade of bf16: every mantissa of s
+    rows = np.arange(group) % 16 / 15 * top[:, None, None]
+    rows = np.tile(rows.astype(np.float32), (1, 1, dim // group))
+    lo = ref.bf16_round(np.float32([-2.0 ** -30, 2.0 ** -30, -1.5 * 2.0 ** -40, 2.0 ** -22]))[np.arange(128) % 4]
+    rows[:, :, ::group] = lo[:, None, None]
+    rows[:, :, 16::group] = np.maximum(lo, rows[:, 0, 1])[:, None, None]
+    rows = ref.bf16_round(rows)
+    back = rows[::-1].copy()
+    for slots in (np.arange(128), np.random.default_rng(group).permutation(128)):
+        want, got = _pair(1, 8, 16, 1, dim, group)
+        got.store(_dev(rows), _dev(back), _ints(slots))
+        want.store(0, rows, back, slots)
+        _same_bytes(want, got)
+        k, v, _ = want.values(0, slots)
+        for w, l in zip((k, v), got.load(_ints(slots))):
+            assert np.array_equal(ref.bits(_np(l)), ref.bits(ref.bf16_round(w.astype(np.float32))))
+    # where one rounding would give others: fp32 drops lo and s n is halfway
+    half = (np.float32(k).view(np.uint32) & 0xFFFF) == 0x8000
+    assert (half & (np.float32(k).astype(np.float64) != k)).sum() > 50

@@ -494,10 +494,10 @@ cg_status cg_pages_grow(const cg_page_batch *batch, cg_stream_t stream);
  * CG_ERR_INVALID_ARG for a request with more than max_q_len rows (left as
  * they were); CG_ERR_TIMEOUT when a bounded wait ran out.
  *
- * out must not overlap q or the cache. Sums are in fp32: scores have to stay
- * below 2^127 there, and V values below 2^96 where a request has more than 32
- * rows per KV head (query heads of it times new tokens), below 2^126 where it
- * has fewer.
+ * out must not overlap q or the cache. Sums are in fp32: q, k and scale q
+ * have to stay below 2^120, scores (and the sums of their terms' sizes) below
+ * 2^100, and V values below 2^96 where a request has more than 32 rows per KV
+ * head (query heads of it times new tokens), below 2^126 where it has fewer.
  *
  * workspace (device, 256-byte aligned, the size that
  * cg_int4_attention_workspace gives from the cache's shape, tokens, q_heads and

@@ -187,6 +187,37 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// Product of bf16 pairs, rounded to bf16.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t c;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
+// The scale (in powers of two) as a factor of Q and one of the scores. Q takes its sign, so
+// that the largest score is the largest product, and a scale of 0 (masked products are -inf;
+// what is not finite times 0 stays so), and the power of two of one below 2^-24, so that no
+// q.k overflows whose score is below 2^100. Exact, unless q 2^e is below bf16's normal range.
+constexpr float kSmallScale = 0x1p-24f;
+
+__device__ __forceinline__ uint32_t q_factor(float scale2)   // a bf16, twice
+{
+    const uint32_t bits = __float_as_uint(scale2), sign = bits >> 16 & 0x8000u;
+    const uint32_t e = max(bits >> 23 & 0xFF, 1u);           // (subnormal ones go by 2^-126)
+    const uint32_t f = scale2 == 0.0f ? 0u : sign | (fabsf(scale2) < kSmallScale ? e << 7 : 0x3F80u);
+    return f | f << 16;
+}
+
+__device__ __forceinline__ float soft_scale(float scale2)
+{
+    const float a = fabsf(scale2);
+    if (a >= kSmallScale)
+        return a;
+    const uint32_t e = max(__float_as_uint(a) >> 23, 1u);
+    return a == 0.0f ? 1.0f : a * __uint_as_float((254u - e) << 23);
+}
+
 // lo + s n for the codes i and i + 4 of a word, rounded once: n comes exact out
 // of the mantissa of 128 + n.
 __device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32_t lo)
@@ -461,9 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
 
     if (warp < kSoftWarps) {
         // ===================================================== softmax of a row
-        // exponents in powers of two; a negative scale goes into Q, so that the largest score
-        // is the largest product
-        const float sc = fmaxf(fabsf(p.scale2), 1.2e-38f);
+        // exponents in powers of two; what q_factor puts into Q does not come here
+        const float sc = soft_scale(p.scale2);
         const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
         const int i = warp >> 2;
         const uint32_t lane_at = (uint32_t)(32 * (warp & 3)) << 16;
@@ -648,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
             const int wi = warp - kSoftWarps, t = lane & 3, k8 = lane >> 2;
             const int half_tok = (k8 & 1) * 4 + (k8 >> 1);
             const int g = lane & 7, vw = (lane >> 3) % NW, v_half = NW == 2 ? lane >> 4 : 0;
-            const uint32_t flip = p.scale2 < 0.0f ? 0x80008000u : 0u;
+            const uint32_t factor = q_factor(p.scale2);
             auto blob_issued = [&](uint32_t slot, uint32_t at) {   // false: a wait ran out
                 const volatile uint32_t *blob = &sm.raw_blob[slot];
                 uint64_t start = 0;
@@ -705,10 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                             if (in < end)
                                 *reinterpret_cast<uint4 *>(sm.q[in >> 7] + (c >> 3) * kQSub + (in & 127) * 128 +
                                                            (((c & 7) ^ (in & 7)) << 4)) =
-                                    make_uint4(__byte_perm(v[e].x, v[e].z, 0x5410) ^ flip,
-                                               __byte_perm(v[e].x, v[e].z, 0x7632) ^ flip,
-                                               __byte_perm(v[e].y, v[e].w, 0x5410) ^ flip,
-                                               __byte_perm(v[e].y, v[e].w, 0x7632) ^ flip);
+                                    make_uint4(mul_bf16x2(__byte_perm(v[e].x, v[e].z, 0x5410), factor),
+                                               mul_bf16x2(__byte_perm(v[e].x, v[e].z, 0x7632), factor),
+                                               mul_bf16x2(__byte_perm(v[e].y, v[e].w, 0x5410), factor),
+                                               mul_bf16x2(__byte_perm(v[e].y, v[e].w, 0x7632), factor));
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();

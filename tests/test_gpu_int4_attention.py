@@ -10,6 +10,7 @@ torch = pytest.importorskip("torch")
 
 import int4_bounds as bounds  # noqa: E402
 import int4_ref as ref  # noqa: E402
+from kv_cache_compression_03_gb300 import cachegen as cg  # noqa: E402
 
 from test_gpu_int4 import FORMATS, _batch, _copy, _dev, _filled, _ints, _np, _pair, _rand  # noqa: E402
 
@@ -164,3 +165,37 @@ def test_values_of_v_of_every_size_side_by_side(dim, group, ratio):
         out = _out(got, q, cu, nkv, table, window=w, max_q_len=1)
         o, most, _ = bounds.attention(want, 0, q, cu, nkv, table, w, 0, dim ** -0.5)
         assert np.isfinite(out).all() and (np.abs(out - o) <= most).all()
+
+
+# ordinary scores whose scale and whose products q.k are not
+SCALES = [(0.0, 2.0 ** 60, 2.0 ** 58), (2.0 ** 70, 1.0, 2.0 ** -74), (-2.0 ** 100, 2.0 ** -54, 2.0 ** -50),
+          (2.0 ** -100, 2.0 ** 30, 2.0 ** 67), (2.0 ** -126, 2.0 ** 22, 2.0 ** 101)]
+
+
+def _scales(nq, ratio, scale, kscale, qscale):
+    rng = np.random.default_rng(nq)
+    nkv, page, heads, dim, group = [90, 700], 16, 2, 128, 32
+    table, pages = _batch(rng, [nq] * 2, nkv, page)
+    want, got = _filled(rng, nkv, table, pages, page, heads, dim, group, scale=kscale)
+    cu = [0, nq, 2 * nq]
+    q = _rand(rng, 2 * nq, heads * ratio, dim, scale=qscale)
+    out = _out(got, q, cu, nkv, table, scale=scale)
+    bounds.check(out, *bounds.attention(want, 0, q, cu, nkv, table, 0, 0, scale))
+
+
+@pytest.mark.parametrize("scale,kscale,qscale", SCALES)
+def test_scales_of_every_size_many_rows(scale, kscale, qscale):
+    _scales(90, 2, scale, kscale, qscale)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_a_scale_of_zero_keeps_what_is_not_finite(bad):
+    q = torch.ones(80, 2, 64, dtype=torch.bfloat16, device="cuda")
+    q[7, 1, 3] = bad
+    cache = cg.Int4Cache(1, 10, 16, 1, 64, 64)
+    cache.store(torch.ones(100, 1, 64, dtype=torch.bfloat16, device="cuda"),
+                torch.ones(100, 1, 64, dtype=torch.bfloat16, device="cuda"), _ints(range(100)))
+    for n in (80, 1):
+        out = cache.attention(q[7:7 + n] if n == 1 else q, _ints([0, n]), _ints([100]), _ints([range(10)]), scale=0.0)
+        at = 0 if n == 1 else 7
+        assert torch.isnan(out[at, 1]).all() and bool((out[at, 0] == 1).all()) and not torch.isnan(out[at + 1:]).any()

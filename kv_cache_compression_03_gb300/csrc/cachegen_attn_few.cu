@@ -483,8 +483,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             int fe = 126 - ((int)(top >> 7) - 127);
             fe = fe < 127 ? fe : 127;
             const float up = pow2(fe), up16 = pow2(fe - 4);
-            // scale2 2^(133 - fe) in two steps: the power alone may pass 2^127
-            const float back = p.scale2 * pow2(66) * pow2(67 - fe);
+            // scale2 2^(133 - fe) in two steps, both upwards: the power alone may pass 2^127, and what
+            // lies between passes fp32's range only where the result does
+            const float back = p.scale2 * pow2((133 - fe) >> 1) * pow2((134 - fe) >> 1);
             float sum[NG] = {};
 #pragma unroll
             for (int w = 0; w < NW; ++w) {

@@ -199,3 +199,9 @@ def test_a_scale_of_zero_keeps_what_is_not_finite(bad):
         out = cache.attention(q[7:7 + n] if n == 1 else q, _ints([0, n]), _ints([100]), _ints([range(10)]), scale=0.0)
         at = 0 if n == 1 else 7
         assert torch.isnan(out[at, 1]).all() and bool((out[at, 0] == 1).all()) and not torch.isnan(out[at + 1:]).any()
+
+
+@pytest.mark.parametrize("nq,ratio", [(1, 4), (3, 8)])
+@pytest.mark.parametrize("scale,kscale,qscale", SCALES)
+def test_scales_of_every_size_few_rows(scale, kscale, qscale, nq, ratio):
+    _scales(nq, ratio, scale, kscale, qscale)

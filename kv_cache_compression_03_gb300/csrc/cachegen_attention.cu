@@ -14,6 +14,8 @@
 
 namespace {
 
+constexpr float kLog2E = 1.4426950408889634f;   // scores are taken in powers of two
+
 // The call's sizes (not its pointers).
 cg_status check_sizes(const cg_int4_cache *c, const cg_attention *a)
 {
@@ -22,7 +24,7 @@ cg_status check_sizes(const cg_int4_cache *c, const cg_attention *a)
         return st;
     if (a->requests < 0 || a->tokens < 0 || a->q_heads <= 0 || a->q_heads % c->num_heads != 0 ||
         a->max_q_len < 0 || a->window < 0 || a->sinks < 0 || a->table_width < 0 ||
-        a->table_stride < a->table_width || !isfinite(a->scale))
+        a->table_stride < a->table_width || !isfinite(a->scale * kLog2E))
         return CG_ERR_INVALID_ARG;
     if (a->requests > CG_MAX_REQUESTS ||
         (int64_t)a->table_width * c->page_tokens >= ((int64_t)1 << 31) ||
@@ -123,7 +125,7 @@ extern "C" cg_status cg_int4_attention(const cg_int4_cache *c, int32_t layer,
     p.heads = c->num_heads;
     p.ratio = a->q_heads / c->num_heads;
     p.few_rows = kFewRows;
-    p.scale2 = a->scale * 1.4426950408889634f;
+    p.scale2 = a->scale * kLog2E;
     p.a = *a;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int64_t most = max_rows(c, a);

@@ -197,3 +197,10 @@ def test_binding_checks_rows():
             cg._bf16_rows(bad, CPU, (5, 6, 64), "x", False)
     with pytest.raises(ValueError):
         cg._bf16_rows(x, torch.device("cuda", 0), (5, 6, 64), "x", False)
+
+
+def test_attention_refuses_a_scale_whose_powers_of_two_overflow(lib):
+    """Scores are taken times log2 e."""
+    n = ct.c_size_t(0)
+    for scale, code in ((3.0e38, cg.CG_ERR_INVALID_ARG), (-2.4e38, cg.CG_ERR_INVALID_ARG), (2.3e38, cg.CG_OK)):
+        assert lib.cg_int4_attention_workspace(ct.byref(_cache()), ct.byref(_args(scale=scale)), ct.byref(n)) == code

@@ -498,6 +498,9 @@ cg_status cg_pages_grow(const cg_page_batch *batch, cg_stream_t stream);
  * have to stay below 2^120, scores (and the sums of their terms' sizes) below
  * 2^100, and V values below 2^96 where a request has more than 32 rows per KV
  * head (query heads of it times new tokens), below 2^126 where it has fewer.
+ * There, codes are summed in units that end at 2^-106 of 1, or of the KV head's
+ * largest value v where that is above 32: small V values have an error of up to
+ * 2^-108 max(1, v) times the tokens besides that of the roundings.
  *
  * workspace (device, 256-byte aligned, the size that
  * cg_int4_attention_workspace gives from the cache's shape, tokens, q_heads and

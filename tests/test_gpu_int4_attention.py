@@ -205,3 +205,47 @@ def test_a_scale_of_zero_keeps_what_is_not_finite(bad):
 @pytest.mark.parametrize("scale,kscale,qscale", SCALES)
 def test_scales_of_every_size_few_rows(scale, kscale, qscale, nq, ratio):
     _scales(nq, ratio, scale, kscale, qscale)
+
+
+# 2^-149 is fp32's last bit; 2^-149 2^(133 - 90) a step of 16 tokens, 2^-110 a token, and room for
+# the four products and sums of a step that each may round
+def _small_v(tokens, largest=1.0):
+    return tokens * 2.0 ** -108 * max(1.0, largest)
+
+
+@pytest.mark.parametrize("dim,group,ratio", [(128, 32, 4), (64, 64, 16)])
+@pytest.mark.parametrize("power", [-60, -80, -90, -98, -120])
+def test_small_values_of_v(dim, group, ratio, power):
+    """Few rows: at 2^-80 the roundings are all there is, further down there is an error that the
+    header states."""
+    rng = np.random.default_rng(-power)
+    heads, page, nq, nkv = 2, 32, [1, 2, 1], [60, 700, 4000]
+    table, pages = _batch(rng, nq, nkv, page)
+    want, got = _filled(rng, nkv, table, pages, page, heads, dim, group, vscale=2.0 ** power)
+    cu = np.concatenate([[0], np.cumsum(nq)])
+    q = _rand(rng, 4, heads * ratio, dim)
+    out = _out(got, q, cu, nkv, table, max_q_len=2)
+    o, most, mean = bounds.attention(want, 0, q, cu, nkv, table, 0, 0, dim ** -0.5)
+    if power >= -80:
+        bounds.check(out, o, most, mean)
+    more = np.repeat([_small_v(m) for m in nkv], nq)[:, None, None]
+    assert (np.abs(out - o) <= most + more).all()
+
+
+def test_groups_of_v_of_different_size():
+    """A group near 2^70 beside groups near 1: the small ones keep their bits."""
+    rng = np.random.default_rng(1)
+    heads, ratio, page, nkv, dim, group = 1, 4, 16, [50, 3000], 128, 32
+    table, pages = _batch(rng, [1, 1], nkv, page)
+    want, got = _pair(1, pages, page, heads, dim, group, fill=0xFF)
+    for r, m in enumerate(nkv):
+        x = np.arange(m)
+        v = _rand(rng, m, heads, dim)
+        v[:, :, 32:64] *= np.float32(2.0 ** 70)
+        want.store(0, _rand(rng, m, heads, dim), ref.bf16_round(v), table[r][x // page] * page + x % page)
+    _copy(want, got)
+    q = _rand(rng, 2, ratio, dim)
+    out = _out(got, q, [0, 1, 2], nkv, table, max_q_len=1)
+    o, most, _ = bounds.attention(want, 0, q, [0, 1, 2], nkv, table, 0, 0, dim ** -0.5)
+    more = np.array([_small_v(m, 2.0 ** 73) for m in nkv])[:, None, None]
+    assert (np.abs(out - o) <= most + more).all()

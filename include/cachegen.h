@@ -373,7 +373,8 @@ cg_status cg_int8_decode(const void *q, const float *scales, int64_t rows, int32
  * status: 16 bytes (16-byte aligned) that the caller clears once; a call sets
  * the first word when it meets an error on the device and it has none yet.
  * Read it with cg_last_device_error(NULL, status, ...). Calls never clear it,
- * so it costs a call nothing and one read covers many calls.
+ * so it costs a call nothing and one read covers many calls;
+ * cg_int4_take_error reads and clears it in one step.
  *
  * Limits (CG_ERR_UNSUPPORTED): head_size 64 or 128, group 32, 64 or 128 and
  * at most head_size, page_tokens a multiple of 16 up to 1024, num_layers *
@@ -394,6 +395,13 @@ typedef struct cg_int4_cache {
 /* Bytes of a cache's data (its data and status pointers are not looked at).
  * Host only. */
 cg_status cg_int4_cache_bytes(const cg_int4_cache *cache, size_t *bytes);
+
+/* Moves the error in the cache's status, if any, to result (device, 16 bytes,
+ * 16-byte aligned; read it with cg_last_device_error(NULL, result, ...)) and
+ * leaves none, in one step on the device: an error that a call on another
+ * stream meets meanwhile is in this result or stays for the next.
+ * Asynchronous on stream. */
+cg_status cg_int4_take_error(const cg_int4_cache *cache, void *result, cg_stream_t stream);
 
 /* K and V rows: bf16 [layers][tokens][num_heads][head_size] with strides in
  * elements, channels contiguous; both pointers 16-byte aligned and every

@@ -163,6 +163,7 @@ def _open(path: str) -> ct.CDLL:
         "cg_int8_encode": (st, [P, ct.c_int64, ct.c_int32, P, P, P, P]),
         "cg_int8_decode": (st, [P, P, ct.c_int64, ct.c_int32, P, P]),
         "cg_int4_cache_bytes": (st, [ct.POINTER(cg_int4_cache), ct.POINTER(sz)]),
+        "cg_int4_take_error": (st, [ct.POINTER(cg_int4_cache), P, P]),
         # the structs of rows, batches and attention calls come as packed bytes
         "cg_int4_store": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, ct.c_int32, P, P,
                                ct.c_int64, P]),
@@ -902,10 +903,13 @@ class Int4Cache:
 
     def check(self):
         """Wait for the current stream; raise the first error that the GPU
-        found in this cache's calls since the last check, and clear it."""
+        found in this cache's calls since the last check. It is read and cleared
+        in one step: what calls on other streams meet later stays for the next
+        check."""
         import torch
         with torch.cuda.device(self.device):
-            st, _ = cg_last_device_error(None, self.status)
-            if st != CG_OK:
-                self.status.zero_()
+            result = torch.empty(16, dtype=torch.uint8, device=self.device)
+            _check(load().cg_int4_take_error(self._ref, result.data_ptr(), _stream_handle()),
+                   "cg_int4_take_error")
+            st, _ = cg_last_device_error(None, result)
         _check(st, "Int4Cache (device)")

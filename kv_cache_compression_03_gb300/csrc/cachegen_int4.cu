@@ -431,6 +431,11 @@ __global__ void __launch_bounds__(kThreads) k_int4_load(RowArgs a)
         load_twice_rounded<B>(a, tile, n);
 }
 
+__global__ void k_int4_take_error(uint32_t *status, uint4 *result)
+{
+    *result = make_uint4(atomicExch(status, 0u), 0, 0, 0);
+}
+
 // Checks of both calls; *work is false where there is nothing to do.
 cg_status check_rows(const cg_int4_cache *c, int32_t first_layer, int32_t layers,
                      const cg_kv_rows *rows, const int32_t *slots, int64_t tokens, RowArgs *a,
@@ -496,6 +501,18 @@ extern "C" cg_status cg_int4_cache_bytes(const cg_int4_cache *c, size_t *bytes)
         return st;
     *bytes = (size_t)c->num_layers * c->num_pages * int4_page_bytes(c);
     return CG_OK;
+}
+
+extern "C" cg_status cg_int4_take_error(const cg_int4_cache *c, void *result, cg_stream_t stream)
+{
+    const cg_status st = int4_check(c);
+    if (st != CG_OK)
+        return st;
+    if (result == nullptr || !int4_aligned(result, 16))
+        return CG_ERR_INVALID_ARG;
+    k_int4_take_error<<<1, 1, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        static_cast<uint32_t *>(c->status), static_cast<uint4 *>(result));
+    return cudaGetLastError() == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }
 
 extern "C" cg_status cg_int4_store(const cg_int4_cache *c, int32_t first_layer, int32_t layers,

@@ -694,3 +694,29 @@ def test_load_rounds_to_fp32_and_then_to_bf16(dim, group):
     # where one rounding would give others: fp32 drops lo and s n is halfway
     half = (np.float32(k).view(np.uint32) & 0xFFFF) == 0x8000
     assert (half & (np.float32(k).astype(np.float64) != k)).sum() > 50
+
+
+def test_check_keeps_an_error_that_comes_while_it_reads(monkeypatch):
+    """A store on another stream meets an error after check() has read the first one."""
+    _, got = _pair(1, 2, 16, 1, 64, 64)
+    k = torch.ones(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    got.store(k, k, _ints([99]))
+    read, other = cg.cg_last_device_error, torch.cuda.Stream()
+    bad = torch.full_like(k, float("nan"))
+    slot = _ints([3])
+
+    def read_and_then_store(*args):
+        st = read(*args)
+        got.store(bad, k, slot, stream=other)
+        other.synchronize()
+        return st
+
+    with monkeypatch.context() as m:
+        m.setattr(cg, "cg_last_device_error", read_and_then_store)
+        with pytest.raises(cg.CacheGenError) as e:
+            got.check()
+        assert e.value.status == cg.CG_ERR_CORRUPT
+    with pytest.raises(cg.CacheGenError) as e:
+        got.check()
+    assert e.value.status == cg.CG_ERR_NONFINITE
+    got.check()

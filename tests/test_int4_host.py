@@ -204,3 +204,11 @@ def test_attention_refuses_a_scale_whose_powers_of_two_overflow(lib):
     n = ct.c_size_t(0)
     for scale, code in ((3.0e38, cg.CG_ERR_INVALID_ARG), (-2.4e38, cg.CG_ERR_INVALID_ARG), (2.3e38, cg.CG_OK)):
         assert lib.cg_int4_attention_workspace(ct.byref(_cache()), ct.byref(_args(scale=scale)), ct.byref(n)) == code
+
+
+def test_take_error_refusals(lib):
+    f, inv = lib.cg_int4_take_error, cg.CG_ERR_INVALID_ARG
+    for kw, code in BAD_SHAPES + BAD_POINTERS:
+        assert f(ct.byref(_cache(**kw)), FAKE, None) == code, kw
+    assert f(None, FAKE, None) == inv and f(ct.byref(_cache()), None, None) == inv
+    assert f(ct.byref(_cache()), FAKE + 8, None) == inv

@@ -611,9 +611,20 @@ def _need_torch():
 
 def _on_stream(stream, fn, *args, **kw):
     """fn(*args, **kw) with `stream` current: its temporaries and outputs are
-    then that stream's too."""
-    with (_torch or _need_torch()).cuda.stream(stream):
-        return fn(*args, **kw)
+    then that stream's too. The tensors passed in (and the cache's own) may be
+    another stream's: their memory is not handed out again before the call on
+    this one has ended, however soon the caller drops them."""
+    torch = _torch or _need_torch()
+    with torch.cuda.stream(stream):
+        res = fn(*args, **kw)
+    owner = getattr(fn, "__self__", None)
+    used = [owner.data, owner.status] if owner is not None else []
+    for a in args:
+        used += [a.slots, a.cu, a.lens, a.free_count, a.status] if isinstance(a, PagePlan) else [a]
+    for t in used:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    return res
 
 
 class _Launch:
@@ -720,7 +731,9 @@ def grow_pages(block_table, lens, counts, free_pages, free_count, page_tokens: i
     ids are checked against the cache's size. ``out`` reuses the buffers of an
     earlier plan; its lens and free_count may be the lens and free_count passed
     in (a captured decode loop then advances in place). Enqueues and returns:
-    the caller's own check is PagePlan.check()."""
+    the caller's own check is PagePlan.check(). With ``stream`` the call runs
+    there; what made its inputs on another stream must be ordered before it by
+    the caller (stream.wait_stream)."""
     if stream is not None:
         return _on_stream(stream, grow_pages, block_table, lens, counts, free_pages, free_count,
                           page_tokens, tokens, num_pages, out)
@@ -765,7 +778,9 @@ class Int4Cache:
 
     Calls enqueue on the current stream (or on stream=) and return; errors
     that the GPU finds are kept until check() raises them. Calls that touch
-    the same slots, one of them a store, must be ordered by the caller."""
+    the same slots, one of them a store, must be ordered by the caller, and so
+    must a call with stream= and what made its inputs on another stream
+    (stream.wait_stream); the inputs may be dropped once the call has returned."""
 
     def __init__(self, num_layers, num_pages, page_tokens, num_heads, head_size, group=32,
                  data=None, device="cuda"):

@@ -720,3 +720,51 @@ def test_check_keeps_an_error_that_comes_while_it_reads(monkeypatch):
         got.check()
     assert e.value.status == cg.CG_ERR_NONFINITE
     got.check()
+
+
+def test_inputs_may_be_dropped_while_another_stream_reads_them():
+    """Calls with stream= that wait behind other work there: memory of inputs that the caller has
+    dropped is not handed out again before they have run."""
+    rng = np.random.default_rng(15)
+    n, heads, dim, page = 4096, 2, 128, 64
+    got, other = cg.Int4Cache(1, n // page, page, heads, dim, 32), torch.cuda.Stream()
+    k, v, q = (_dev(_rand(rng, n, heads * m, dim)) for m in (1, 1, 4))
+    slots, table, lens = _ints(rng.permutation(n)), _ints([rng.permutation(n // page)] * n), _ints(rng.integers(1, n, n))
+    cu = _ints(np.arange(n + 1))
+
+    def pages(stream=None, args=None):
+        a = args or make()
+        return cg.grow_pages(*a, 16, 70000, stream=stream)
+
+    def make():
+        return (torch.full((n, 300), -1, dtype=torch.int32, device="cuda"), torch.zeros_like(lens), lens // 256,
+                torch.arange(n * 2, dtype=torch.int32, device="cuda").flip(0), _ints([n * 2]))
+
+    got.store(k, v, slots)
+    want = got.load(slots) + (got.attention(q, cu, lens, table, max_q_len=1),)
+    plan = pages()
+    bytes_ = got.data.clone()
+    torch.cuda.synchronize()
+
+    def later(call, *args, **kw):
+        """call on copies of args that are dropped at once, their memory taken by other tensors."""
+        copies = [a.clone() for a in args]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(other):
+            torch.cuda._sleep(100_000_000)
+        res = call(*copies, stream=other, **kw)
+        copies.clear()
+        junk = [torch.full_like(a, 3) for _ in range(3) for a in args]
+        torch.cuda.synchronize()
+        del junk
+        return res
+
+    assert torch.equal(later(got.attention, q, cu, lens, table, max_q_len=1), want[2])
+    for a, b in zip(later(got.load, slots), want):
+        assert torch.equal(a, b)
+    got.data.zero_()
+    later(got.store, k, v, slots)
+    assert torch.equal(got.data, bytes_)
+    p = later(lambda *a, stream: pages(stream, a), *make())
+    assert p.slots.tolist() == plan.slots.tolist() and p.cu.tolist() == plan.cu.tolist()
+    got.check(), p.check()

@@ -679,11 +679,15 @@ def _table(t, device, what: str):
 def _bf16_rows(t, device, shape, what: str, written: bool):
     """(address, strides but the last) of a bf16 tensor [.., head_size] of the
     given shape whose rows the kernels can read (and, when written, that do
-    not overlap). A dimension of one element counts stride 0."""
+    not overlap). A dimension of one element counts stride 0. No gradient flows
+    through the cache: a tensor that autograd would follow is refused."""
     torch = _torch or _need_torch()
     if not (isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.shape == shape and
             t.device == device):
         raise ValueError(f"{what} must be a bf16 tensor of shape {list(shape)} on {device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires grad, and no gradient flows through the cache: pass "
+                         f"{what}.detach(), or call under torch.no_grad()")
     ptr, strides = t.data_ptr(), t.stride()
     last = strides[-1]
     strides = [s if n > 1 else 0 for s, n in zip(strides[:-1], shape)]
@@ -776,7 +780,8 @@ class Int4Cache:
     (cg_int4_* in include/cachegen.h, which defines the format). ``data`` is
     the cache's bytes, uint8 of any shape (made, and zeroed, if not given).
 
-    Calls enqueue on the current stream (or on stream=) and return; errors
+    For serving: no gradient flows through the cache, and rows that require one
+    are refused. Calls enqueue on the current stream (or on stream=) and return; errors
     that the GPU finds are kept until check() raises them. Calls that touch
     the same slots, one of them a store, must be ordered by the caller, and so
     must a call with stream= and what made its inputs on another stream

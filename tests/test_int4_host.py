@@ -212,3 +212,16 @@ def test_take_error_refusals(lib):
         assert f(ct.byref(_cache(**kw)), FAKE, None) == code, kw
     assert f(None, FAKE, None) == inv and f(ct.byref(_cache()), None, None) == inv
     assert f(ct.byref(_cache()), FAKE + 8, None) == inv
+
+
+@pytest.mark.parametrize("written", [False, True])
+def test_binding_refuses_rows_whose_gradient_would_be_lost(written):
+    x = torch.zeros(5, 6, 64, dtype=torch.bfloat16, requires_grad=True)
+    for t in (x, x * 2, x[:, :3]):
+        with pytest.raises(ValueError, match="requires grad"):
+            cg._bf16_rows(t, CPU, tuple(t.shape), "q", written)
+        cg._bf16_rows(t.detach(), CPU, tuple(t.shape), "q", written)
+        with torch.no_grad():
+            cg._bf16_rows(t, CPU, tuple(t.shape), "q", written)
+        with torch.inference_mode():
+            cg._bf16_rows(t, CPU, tuple(t.shape), "q", written)

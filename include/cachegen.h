@@ -457,6 +457,8 @@ cg_status cg_int4_load(const cg_int4_cache *cache, int32_t first_layer, int32_t 
  *                                     slots_out too short
  *                CG_ERR_CORRUPT       free_count outside [0, free_capacity]
  *                                     or a page id outside [0, num_pages)
+ *                of several the greatest code (a page id counts where there
+ *                is no other error)
  * With an error nothing is taken: block_table is as it was, lens_out and
  * free_count_out repeat their inputs, cu_out is 0 and slots_out is -1 (a page
  * id outside the cache, in block_table or taken from free_pages, is the

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) k_pages_grow(cg_page_batch b)
     extern __shared__ int32_t smem[];
     int32_t *cu = smem, *base = cu + b.requests + 1, *held = base + b.requests + 1;
     __shared__ Sum warp_sum[kWarps];
-    __shared__ uint32_t error;
+    __shared__ uint32_t error;   // the greatest code of several, whichever is found first
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t P = b.page_tokens;
     const int32_t nfree = *b.free_count;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(kThreads) k_pages_grow(cg_page_batch b)
     }
     __syncthreads();
     if (tid == 0 && (nfree < 0 || nfree > b.free_capacity))
-        atomicCAS(&error, 0u, (uint32_t)CG_ERR_CORRUPT);
+        atomicMax(&error, (uint32_t)CG_ERR_CORRUPT);
     // a thread's requests lie together: one scan over the threads places them all
     constexpr int kMost = (CG_MAX_REQUESTS + kThreads - 1) / kThreads;
     const int each = (b.requests + kThreads - 1) / kThreads;
@@ -94,11 +94,11 @@ __global__ void __launch_bounds__(kThreads) k_pages_grow(cg_page_batch b)
         if (i < each && r < b.requests) {
             const int64_t len = b.lens[r], n = b.counts[r];
             if (len < 0 || n < 0) {
-                atomicCAS(&error, 0u, (uint32_t)CG_ERR_INVALID_ARG);
+                atomicMax(&error, (uint32_t)CG_ERR_INVALID_ARG);
             } else {
                 const int64_t all = (len + n + P - 1) / P, have = (len + P - 1) / P;
                 if (all > b.table_width || len + n > INT32_MAX)
-                    atomicCAS(&error, 0u, (uint32_t)CG_ERR_CAPACITY);
+                    atomicMax(&error, (uint32_t)CG_ERR_CAPACITY);
                 tokens[i] = (int32_t)n;
                 pages[i] = (int32_t)(all - have);
                 held[r] = (int32_t)have;
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) k_pages_grow(cg_page_batch b)
         cu[b.requests] = (int32_t)total.tokens;
         base[b.requests] = (int32_t)total.pages;
         if (total.tokens > b.tokens || total.pages > nfree)
-            atomicCAS(&error, 0u, (uint32_t)CG_ERR_CAPACITY);
+            atomicMax(&error, (uint32_t)CG_ERR_CAPACITY);
     }
     __syncthreads();
     const uint32_t err = error;

@@ -768,3 +768,28 @@ def test_inputs_may_be_dropped_while_another_stream_reads_them():
     p = later(lambda *a, stream: pages(stream, a), *make())
     assert p.slots.tolist() == plan.slots.tolist() and p.cu.tolist() == plan.cu.tolist()
     got.check(), p.check()
+
+
+@pytest.mark.parametrize("n", [40, 3000])
+def test_grow_pages_reports_the_same_of_several_errors(n):
+    """Whichever thread meets its error first: the greatest code."""
+    rng = np.random.default_rng(n)
+    for wrong, code in (("negative, narrow", cg.CG_ERR_CAPACITY), ("negative, list", cg.CG_ERR_CORRUPT),
+                        ("negative, pages", cg.CG_ERR_CAPACITY), ("narrow, list", cg.CG_ERR_CORRUPT),
+                        ("pages, list", cg.CG_ERR_CORRUPT), ("negative, narrow, pages, list", cg.CG_ERR_CORRUPT)):
+        for _ in range(4):
+            at = rng.permutation(n)
+            lens, counts, nfree = np.full(n, 5), np.full(n, 1), 8
+            if "negative" in wrong:
+                lens[at[0]] = -1
+            if "narrow" in wrong:
+                lens[at[1]] = 100
+            if "pages" in wrong:
+                counts[at[2]], nfree = 40, 1
+            if "list" in wrong:
+                nfree = 9 if "pages" not in wrong else -1
+            p = cg.grow_pages(_ints(np.zeros((n, 4))), _ints(lens), _ints(counts), _ints(range(8)), _ints([nfree]), 16,
+                              n + 40)
+            with pytest.raises(cg.CacheGenError) as e:
+                p.check()
+            assert e.value.status == code, wrong

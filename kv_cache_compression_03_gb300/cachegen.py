@@ -655,6 +655,13 @@ def _need(cond, what: str):
         raise ValueError(what)
 
 
+def _int32(x, what: str) -> int:
+    """x, an int that a 32-bit argument holds (ctypes would cut a larger one off)."""
+    if not -0x80000000 <= x <= 0x7FFFFFFF:
+        raise ValueError(f"{what} must fit 32 bits")
+    return x
+
+
 def _ints(t, device, shape, what: str) -> int:
     """The address of a contiguous int32 tensor of the given shape on the device."""
     torch = _torch or _need_torch()
@@ -765,10 +772,13 @@ def grow_pages(block_table, lens, counts, free_pages, free_count, page_tokens: i
         _ints(out.free_count, dev, (1,), "out.free_count")
         _check_status_buffer(out.status, "grow_pages")
         _need(out.status.device == dev, "out.status must be on the same device")
-    b = _BATCH.pack(block_table.data_ptr(), stride, width, n, lens_at, counts_at, free_at, nfree_at,
-                    capacity, 0x7FFFFFFF // page_tokens if num_pages is None else num_pages,
-                    page_tokens, out.cu.data_ptr(), out.lens.data_ptr(), out.free_count.data_ptr(),
-                    out.slots.data_ptr(), tokens, out.status.data_ptr())
+    try:
+        b = _BATCH.pack(block_table.data_ptr(), stride, width, n, lens_at, counts_at, free_at,
+                        nfree_at, capacity, 0x7FFFFFFF // page_tokens if num_pages is None else num_pages,
+                        page_tokens, out.cu.data_ptr(), out.lens.data_ptr(), out.free_count.data_ptr(),
+                        out.slots.data_ptr(), tokens, out.status.data_ptr())
+    except struct.error as e:
+        raise ValueError(f"a number does not fit its type: {e}") from None
     with _Launch(dev.index) as s:
         st = (_lib or load()).cg_pages_grow(b, s)
     _check(st, "cg_pages_grow")
@@ -790,6 +800,8 @@ class Int4Cache:
     def __init__(self, num_layers, num_pages, page_tokens, num_heads, head_size, group=32,
                  data=None, device="cuda"):
         torch = _torch or _need_torch()
+        for x in (num_layers, num_pages, page_tokens, num_heads, head_size, group):
+            _int32(x, "a cache's sizes")
         self._c = cg_int4_cache(0, 0, num_layers, num_pages, page_tokens, num_heads, head_size,
                                 group)
         self._ref = ct.byref(self._c)
@@ -828,6 +840,7 @@ class Int4Cache:
         shape = k.shape
         _need(len(shape) in (3, 4), "k must be [tokens, heads, head_size], with or without layers")
         tokens, layers = shape[-3], shape[0] if len(shape) == 4 else None
+        _int32(layer, "layer")
         rows = self._rows(k, v, tokens, layers, False)
         at = _ints(slots, self.device, (tokens,), "slots")
         with _Launch(self.device.index) as s:
@@ -846,10 +859,11 @@ class Int4Cache:
         torch = _torch
         tokens = slots.shape[0] if slots.dim() == 1 else -1
         at = _ints(slots, self.device, (tokens,), "slots")
+        _int32(layer, "layer")
         H, D = self.num_heads, self.head_size
         shape = (tokens, H, D)
         if layers is not None:
-            _need(layers >= 0, "layers must not be negative")
+            _need(_int32(layers, "layers") >= 0, "layers must not be negative")
             shape = (layers,) + shape
         if k_out is None and v_out is None:   # what is made here needs no check
             k_out = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
@@ -884,6 +898,7 @@ class Int4Cache:
         torch, dev, D = _torch, self.device, self.head_size
         shape = q.shape
         _need(len(shape) == 3, "q must be [tokens, q_heads, head_size]")
+        _int32(layer, "layer")
         tokens, q_heads, _ = shape
         if q_heads <= 0 or q_heads % self.num_heads:
             raise ValueError(f"q_heads must be a multiple of {self.num_heads}")
@@ -897,9 +912,12 @@ class Int4Cache:
             out_at, os0, os1 = out.data_ptr(), q_heads * D, D
         else:
             out_at, (os0, os1) = _bf16_rows(out, dev, shape, "out", True)
-        a = _ATTENTION.pack(q_at, qs0, qs1, out_at, os0, os1, cu_at, lens_at,
-                            block_table.data_ptr(), stride, width, n, tokens, q_heads,
-                            max_q_len or 0, window, sinks, D ** -0.5 if scale is None else scale)
+        try:
+            a = _ATTENTION.pack(q_at, qs0, qs1, out_at, os0, os1, cu_at, lens_at,
+                                block_table.data_ptr(), stride, width, n, tokens, q_heads,
+                                max_q_len or 0, window, sinks, D ** -0.5 if scale is None else scale)
+        except struct.error as e:
+            raise ValueError(f"a number does not fit its type: {e}") from None
         L = _lib or load()
         # the size depends on the most rows that a request can have per KV head, and on the cache
         rows = (min(max_q_len, tokens) if max_q_len else tokens) * q_heads // self.num_heads

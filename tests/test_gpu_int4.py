@@ -793,3 +793,20 @@ def test_grow_pages_reports_the_same_of_several_errors(n):
             with pytest.raises(cg.CacheGenError) as e:
                 p.check()
             assert e.value.status == code, wrong
+
+
+def test_numbers_past_32_bits_are_refused_and_not_cut_off():
+    _, got = _pair(1, 2, 16, 1, 64, 64)
+    k = torch.ones(1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    one, table = _ints([1]), _ints([[0]])
+    for call in (lambda: got.store(k, k, one, layer=2 ** 32), lambda: got.load(one, layer=2 ** 32),
+                 lambda: got.load(one, layers=2 ** 32 + 1), lambda: got.attention(k, _ints([0, 1]), one, table, layer=2 ** 32),
+                 lambda: got.attention(k, _ints([0, 1]), one, table, window=2 ** 40),
+                 lambda: cg.grow_pages(table, one, one, one, one, 2 ** 33, 1)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(cg.CacheGenError) as e:      # fp32's infinity
+        got.attention(k, _ints([0, 1]), one, table, scale=1e39)
+    assert e.value.status == cg.CG_ERR_INVALID_ARG
+    assert not got.data.any()
+    got.check()

@@ -225,3 +225,16 @@ def test_binding_refuses_rows_whose_gradient_would_be_lost(written):
             cg._bf16_rows(t, CPU, tuple(t.shape), "q", written)
         with torch.inference_mode():
             cg._bf16_rows(t, CPU, tuple(t.shape), "q", written)
+
+
+def test_binding_refuses_numbers_that_their_type_does_not_hold():
+    """ctypes would take 2^32 + 1 layers for one, and 2^32 for layer 0."""
+    for x in (2 ** 31, -2 ** 31 - 1, 2 ** 32):
+        with pytest.raises(ValueError, match="32 bits"):
+            cg._int32(x, "layer")
+    assert cg._int32(2 ** 31 - 1, "layer") == 2 ** 31 - 1
+    for i in range(6):
+        sizes = [1, 2, 16, 1, 64, 32]
+        sizes[i] += 2 ** 32
+        with pytest.raises(ValueError, match="32 bits"):
+            cg.Int4Cache(*sizes, device="cpu")

@@ -249,3 +249,20 @@ def test_groups_of_v_of_different_size():
     o, most, _ = bounds.attention(want, 0, q, [0, 1, 2], nkv, table, 0, 0, dim ** -0.5)
     more = np.array([_small_v(m, 2.0 ** 73) for m in nkv])[:, None, None]
     assert (np.abs(out - o) <= most + more).all()
+
+
+@pytest.mark.parametrize("nq,nkv,ratio,page", [([1, 3], [500, 1333], 40, 16), ([1, 1], [700, 20], 300, 1024),
+                                               ([2, 1, 5], [3, 2000, 40], 33, 1024), ([1, 2], [5000, 3000], 11, 1024),
+                                               ([7], [2049], 129, 112)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 5)])
+def test_many_query_heads_and_large_pages(nq, nkv, ratio, page, window, sinks):
+    """A token's query heads fill row tiles alone, or end inside one; pages larger than a tile."""
+    rng = np.random.default_rng(ratio)
+    heads, dim, group = 1, 64, 64
+    table, pages = _batch(rng, nq, nkv, page)
+    want, got = _filled(rng, nkv, table, pages, page, heads, dim, group)
+    cu = np.concatenate([[0], np.cumsum(nq)])
+    q = _rand(rng, int(cu[-1]), heads * ratio, dim)
+    for most in (None, max(nq), 1000):
+        out = _out(got, q, cu, nkv, table, window=window, sinks=sinks, max_q_len=most)
+        bounds.check(out, *bounds.attention(want, 0, q, cu, nkv, table, window, sinks, dim ** -0.5))

@@ -40,8 +40,8 @@
 // the order of the tokens, so results do not depend on timing.
 //
 // Measured (8 KV heads of 128, 32 query heads, groups of 32): 64 requests of 6K tokens
-// on average 110 us, 4.6 TB/s where a copy reaches 6.8 (a floor of 74 us); 32 requests
-// under a window of 4096 tokens 47 us; one request of 128K 48 us; the smallest call 12.7 us, of which the two
+// on average 111 us, 4.6 TB/s where a copy reaches 6.8 (a floor of 74 us); 32 requests
+// under a window of 4096 tokens 47 us; one request of 128K 46 us; the smallest call 12.6 us, of which the two
 // launches make most. Issue slots are busy for 53 % of the time with 12 warps on an SM (168
 // registers each), which wait on the chain codes -> scores -> p -> values of their own blob
 // most. Rows 9 to 16 take 16 columns and 8 warps an SM; a third or fourth such tile would read

@@ -21,21 +21,24 @@
 // 3 7 of each eight); Q is laid out alike. V's words hold a pair of tokens each, as
 // the transposed rows need them. Tensor memory is full: two S, two O, 128 columns each.
 //
-// Fewer units than blocks: each is cut along its tokens, and a second kernel joins
-// the pieces in their order; with one row tile the softmax groups take turns at the
-// tiles of tokens.
+// At most half as many units as blocks: each is cut along its tokens, and a second kernel
+// joins the pieces in their order; with one row tile the softmax groups take turns at the
+// tiles of tokens. More units are dealt to the blocks in turns, the longest first.
 //
 // Roundings: k^ and v^ = lo + s n to bf16 (one rounding, 2^-8 relative at most), p to
 // bf16: the products need 16-bit operands, and bf16 keeps the range of s and lo. Against
-// 64 bits the error is 0.003 of the result, 0.0017 of which the rounding of the result
-// makes anyway. Scores, sums and O stay in fp32.
+// 64 bits the error is 0.0026 to 0.0039 of the result (prompt 0.0034, drafts 0.0038; the largest
+// part is k^'s, which moves scores), where rounding the result alone gives 0.0017. Scores,
+// sums and O stay in fp32.
 //
-// Measured (8 KV heads of 128, 32 query heads, groups of 32): a prompt of 8192 tokens 556 us,
-// 990 TFLOP/s, the tensor pipe active for 48 % of the time (its floor at 1909 TFLOP/s is
+// Measured (8 KV heads of 128, 32 query heads, groups of 32): a prompt of 8192 tokens 547 us,
+// 1005 TFLOP/s, the tensor pipe active for 48 % of the time (its floor at 1909 TFLOP/s is
 // 288 us); four drafted tokens of each of four requests at 128K tokens (2 KV heads, 32 query
-// heads, groups of 64) 116 us, 1.25 TB/s. A tile of 128 tokens takes 4400 cycles: a softmax of 2700 (two reads of S, 1000 for the
+// heads, groups of 64) 116 us, 1.25 TB/s. A tile of 128 tokens takes 4300 cycles: a softmax of 2700 (two reads of S, 1000 for the
 // maximum and 1500 for the exponentials) and the products of both row tiles, 4 x 512, which
-// the chain S -> P -> O -> next S of each row tile overlaps only in part. What was tried
+// the chain S -> P -> O -> next S of each row tile overlaps only in part. The kernel's time is
+// that of its longest block: 250 tiles of the 8192-token prompt where the mean is 219, 66
+// where it is 56 of a 2048-token chunk under a window of 4096 tokens. What was tried
 // against that and is slower: tiles of 64 tokens with the next S ready beforehand (650 us),
 // one pass over S that raises the maximum as it goes (594), 64 columns at a time (625: spills),
 // V kept in registers until the next K is written (583). Six expanding warps: 601 us; one blob

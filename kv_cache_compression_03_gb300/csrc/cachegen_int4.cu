@@ -8,8 +8,8 @@
 // A block takes up to 16 tokens of one layer, all heads. Where each token lies
 // is worked out once, in shared memory, so that the rest is adds.
 //
-// Measured (8 heads of 128, groups of 32): load of 16384 tokens x 32 layers at the copy
-// rate, 6.8 TB/s; store of as many 635 us, 4.4 TB/s, bound by instruction issue (3.2 of 4 a
+// Measured (8 heads of 128, groups of 32): load of 16384 tokens x 32 layers 404 us, at the copy
+// rate, 6.8 TB/s; store of as many 634 us, 4.4 TB/s, bound by instruction issue (3.2 of 4 a
 // cycle): 149 instructions for 8 values. What took it there from 2.4 ms: no division per value
 // or per row, pairs of fp32 in one instruction (820 -> 778 us), a head's K and V rows read at
 // once by the same threads (-> 667), six blocks on an SM at 40 registers (-> 635; seven spill).

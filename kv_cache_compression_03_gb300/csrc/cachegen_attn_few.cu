@@ -278,14 +278,6 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Product of bf16 pairs, rounded to bf16.
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t c;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-    return c;
-}
-
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c)
 {
     uint32_t d;
@@ -300,13 +292,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
     return y;
 }
 
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Codes i and i + 4 of a word as a bf16 pair: n 2^-133 for even i, n 2^-129 for
 // odd i (bf16 bits 0 .. 255 count in steps of 2^-133).
 __device__ __forceinline__ uint32_t codes_of(uint32_t w, int i)
@@ -318,24 +303,6 @@ constexpr uint32_t kEight = 0x00080008u;   // 8 2^-133, twice
 __device__ __forceinline__ float pow2(int e)   // -126 <= e <= 127
 {
     return __uint_as_float((uint32_t)(e + 127) << 23);
-}
-
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
-{
-    if constexpr (N == 1) {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
-    }
 }
 
 // ---------------------------------------------------------------- workspace

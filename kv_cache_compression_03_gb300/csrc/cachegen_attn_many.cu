@@ -162,42 +162,6 @@ __device__ __forceinline__ void tmem_ld16(uint32_t (&v)[16], uint32_t at)
         : "memory");
 }
 
-// Pairs of fp32 in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Product of bf16 pairs, rounded to bf16.
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
-{
-    uint32_t c;
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-    return c;
-}
-
 // The scale (in powers of two) as a factor of Q and one of the scores. Q takes its sign, so
 // that the largest score is the largest product, and a scale of 0 (masked products are -inf;
 // what is not finite times 0 stays so), and the power of two of one below 2^-24, so that no
@@ -219,35 +183,6 @@ __device__ __forceinline__ float soft_scale(float scale2)
         return a;
     const uint32_t e = max(__float_as_uint(a) >> 23, 1u);
     return a == 0.0f ? 1.0f : a * __uint_as_float((254u - e) << 23);
-}
-
-// lo + s n for the codes i and i + 4 of a word, rounded once: n comes exact out
-// of the mantissa of 128 + n.
-__device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32_t lo)
-{
-    const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    uint32_t n, y;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(x), "r"(0x43004300u));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(n), "r"(s), "r"(lo));
-    return y;
-}
-
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
-{
-    if constexpr (N == 1) {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
-    }
 }
 
 // ------------------------------------------------------------------ schedule

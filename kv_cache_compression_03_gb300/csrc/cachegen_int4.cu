@@ -126,27 +126,6 @@ __device__ __forceinline__ float scale_of(float range)
     return __bfloat162float(__float2bfloat16_rn(__fmul_rn(range, 1.0f / 15.0f)));
 }
 
-// Pairs of fp32 in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b)
-{
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // Codes of 8 values: n = rne(d / s), d = x - lo. n0 = rne(d (1 / s)) is n or, next
 // to a tie, its neighbour; e = d - n0 s is exact (both are multiples of d's last
 // bit and e is below s), so |e| against s / 2 decides, with n even where they are
@@ -268,22 +247,14 @@ __global__ void __launch_bounds__(kThreads, 6) k_int4_store(RowArgs a)
     }
 }
 
-// lo + s n for the codes i and i + 4 of a word. n comes exact out of the mantissa
-// of 128 + n, s n has 12 bits, and one rounding to bf16 gives what the format's two (to fp32,
-// then to bf16) give wherever fp32 holds the sum, and where s n is far below half a last bit
-// of lo. What is left is a lo that fp32 drops next to an s n halfway between two bf16
-// values, which is then rounded to the even one: the rows with such a group, which data
-// hardly has, are found by tiny_lo() and written once more by load_twice_rounded().
-// (Both roundings for every code: 254 -> 318 us for 32768 tokens, 40 layers of 2 heads.)
-__device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32_t lo)
-{
-    const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    uint32_t n, y;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(x), "r"(0x43004300u));
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(n), "r"(s), "r"(lo));
-    return y;
-}
-
+// Load expands codes with one rounding (expand). s n has 12 bits, and one rounding to bf16
+// gives what the format's two (to fp32, then to bf16) give wherever fp32 holds the sum, and
+// where s n is far below half a last bit of lo. What is left is a lo that fp32 drops next to
+// an s n halfway between two bf16 values, which is then rounded to the even one: the rows
+// with such a group, which data hardly has, are found by tiny_lo() and written once more by
+// load_twice_rounded(). (Both roundings for every code: 254 -> 318 us for 32768 tokens, 40
+// layers of 2 heads.)
+//
 // Not 0 where lo != 0 is at most half a last bit of fp32 at 15 s: 2^20 |lo| < s, for pairs.
 __device__ __forceinline__ uint32_t tiny_lo(uint32_t s, uint32_t lo)
 {
@@ -292,24 +263,6 @@ __device__ __forceinline__ uint32_t tiny_lo(uint32_t s, uint32_t lo)
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(big) : "r"(size), "r"(0x49804980u));
     asm("set.lt.u32.bf16x2 %0, %1, %2;" : "=r"(less) : "r"(big), "r"(s));   // all bits of a half
     return less & size;
-}
-
-template <int N>
-__device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
-{
-    if constexpr (N == 1) {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    } else if constexpr (N == 2) {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-    } else {
-        const uint4 v = *reinterpret_cast<const uint4 *>(p);
-        w[0] = v.x;
-        w[1] = v.y;
-        w[2] = v.z;
-        w[3] = v.w;
-    }
 }
 
 // The block's rows as k_int4_load writes them, by the same threads, with both roundings. A

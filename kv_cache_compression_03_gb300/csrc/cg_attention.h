@@ -38,6 +38,23 @@ __device__ __forceinline__ bool attn_request(const AttnArgs &p, int r, AttnReque
     return *error == CG_OK && c1 > c0;
 }
 
+// ------------------------------------------------------------- instructions
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Product of bf16 pairs, rounded to bf16.
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t c;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+    return c;
+}
+
 // ------------------------------------------------------ barriers and copies
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p)

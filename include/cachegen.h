@@ -543,6 +543,163 @@ cg_status cg_int4_attention_workspace(const cg_int4_cache *cache, const cg_atten
 cg_status cg_int4_attention(const cg_int4_cache *cache, int32_t layer, const cg_attention *args,
                             void *workspace, size_t workspace_bytes, cg_stream_t stream);
 
+/* The same where every request begins with the same cached tokens (an instruction
+ * or a document that a batch shares): the first shared_tokens of each request's tokens
+ * lie in the same pages, the first shared_tokens / page_tokens entries of its row of
+ * block_table. They are read once for all queries, by way of the first row of
+ * block_table; the other rows' entries there are not read. kv_lens counts the shared
+ * tokens too. The result is that of cg_int4_attention but for the order of fp32 sums.
+ *
+ * shared_tokens is a multiple of page_tokens and window is 0 (CG_ERR_INVALID_ARG; what
+ * of the first tokens is in a window depends on the query); shared_tokens = 0 is
+ * cg_int4_attention. A request whose new tokens do not all lie behind the shared ones
+ * sets CG_ERR_INVALID_ARG in the cache's status (its rows are left as they were).
+ * A page id outside the cache among the shared ones hides its tokens from every query.
+ * The workspace holds tokens * q_heads * (head_size + 2) floats more. */
+cg_status cg_int4_attention_shared_workspace(const cg_int4_cache *cache, const cg_attention *args,
+                                             int32_t shared_tokens, size_t *bytes);
+cg_status cg_int4_attention_shared(const cg_int4_cache *cache, int32_t layer,
+                                   const cg_attention *args, int32_t shared_tokens,
+                                   void *workspace, size_t workspace_bytes, cg_stream_t stream);
+
+/* Eviction: a cache that is kept to a budget by the attention that its tokens get.
+ * cg_int4_weigh sums the attention weights of every token, cg_choose_tokens picks the
+ * tokens of each head that stay, cg_int4_compact moves them to the front of their
+ * request's pages, and cg_pages_release gives the pages behind them back to the list
+ * that cg_pages_grow takes from. A request's heads (and layers) may keep different
+ * tokens, but equally many. Positions count what is in the cache: what attention and
+ * its masks call token j is from then on the j-th token that stayed.
+ *
+ * cg_int4_weigh, over one layer:
+ *   out[r][h][j] = in[r][h][j] + sum_i sum_g p_igj   for j < kv_lens[r],
+ * where p_ig is the softmax of cg_int4_attention for query i of request r and query head
+ * g, over the request's new tokens i and the query heads g of KV head h. A token that a
+ * query does not see gets 0 from it. Elements from kv_lens[r] on are left as they were.
+ * p is computed in fp32, the sum over i and g in an order that does not depend on timing.
+ *
+ * args are those of cg_int4_attention (out and its strides are not looked at), with
+ * the same limits and device errors; a kv_len beyond width is CG_ERR_CORRUPT. in (NULL:
+ * zeros) and out have rows of width floats, elements adjacent, strides in elements; in
+ * may be out (with the same strides) and otherwise must not overlap it. Rows of out must not
+ * overlap, nor out q or the cache. workspace as for attention; its size depends on the
+ * cache's shape, tokens, requests, q_heads, max_q_len and width. */
+typedef struct cg_token_weights {
+    const float *in;
+    float *out;
+    int64_t in_request_stride, in_head_stride;
+    int64_t out_request_stride, out_head_stride;
+    int32_t width;
+} cg_token_weights;
+
+cg_status cg_int4_weigh_workspace(const cg_int4_cache *cache, const cg_attention *args,
+                                  const cg_token_weights *weights, size_t *bytes);
+cg_status cg_int4_weigh(const cg_int4_cache *cache, int32_t layer, const cg_attention *args,
+                        const cg_token_weights *weights, void *workspace, size_t workspace_bytes,
+                        cg_stream_t stream);
+
+/* cg_choose_tokens: of each row of weights (float [layers][requests][heads], rows of
+ * width floats, elements adjacent, strides in elements) the tokens that stay. Of a request
+ * with m = lens[r] tokens the first `sinks` and the last `recent` stay, and of the
+ * others those with the greatest weights, min(m, budget) in all; of equal weights the
+ * lower token, and NaN is below every other weight.
+ *   kept      int32 [layers][requests][heads][budget], contiguous: the tokens that
+ *             stay, ascending; -1 behind the last
+ *   lens_out  int32 [requests]: min(m, budget) (may be lens itself)
+ *   status    16 bytes, 16-byte aligned, always written: CG_OK, or CG_ERR_CORRUPT for a
+ *             length that is negative or beyond width (its row of kept is -1,
+ *             lens_out repeats it)
+ * sinks + recent must not exceed budget (CG_ERR_INVALID_ARG). No other two arrays may
+ * overlap. Limits (CG_ERR_UNSUPPORTED): CG_MAX_REQUESTS requests, layers * requests *
+ * heads below 2^31. Asynchronous on stream. */
+typedef struct cg_token_choice {
+    const float *weights;
+    int64_t layer_stride, request_stride, head_stride;
+    int32_t layers, requests, heads, width;
+    const int32_t *lens;
+    int32_t budget, recent, sinks;
+    int32_t *kept;
+    int32_t *lens_out;
+    void *status;
+} cg_token_choice;
+
+cg_status cg_choose_tokens(const cg_token_choice *choice, cg_stream_t stream);
+
+/* cg_int4_compact: in layers [first_layer, first_layer + layers) of the cache, token
+ * kept[l][r][h][i] of request r (its place in head h) goes to place i, for i <
+ * new_lens[r]. kept is int32 [layers][requests][num_heads], rows of budget entries,
+ * adjacent, strides in elements, as cg_choose_tokens writes it. weights (NULL: none;
+ * float [layers][requests][num_heads], rows of weights_width floats) move along, and
+ * those from new_lens[r] to lens[r] become 0. The places from new_lens[r] on keep their
+ * bytes. A request with new_lens[r] = lens[r] is left as it is, whatever kept holds.
+ * Tokens whose place does not change are not written where a whole blob of 16 stays
+ * as it is, so pages that requests share may stand at the front of their tables as
+ * long as all of their tokens stay; no other page may belong to two requests.
+ *
+ * Errors in the cache's status, CG_ERR_CORRUPT: a length that is negative or beyond
+ * table_width pages or weights_width, new_lens[r] above lens[r] or (below it) above budget,
+ * entries of kept that do not ascend within [0, lens[r]) (that head's tokens, of that
+ * layer, or the whole request are left as they were); a page id outside the cache (what
+ * would be read or written there is not moved). Table entries from lens[r] on are not read.
+ * No two arrays may overlap. Asynchronous on stream. */
+typedef struct cg_compaction {
+    const int32_t *kept;
+    int64_t kept_layer_stride, kept_request_stride, kept_head_stride;
+    float *weights;
+    int64_t weights_layer_stride, weights_request_stride, weights_head_stride;
+    int32_t weights_width;
+    int32_t budget;
+    int32_t layers, requests;
+    const int32_t *lens;
+    const int32_t *new_lens;
+    const int32_t *block_table;
+    int64_t table_stride;
+    int32_t table_width;
+} cg_compaction;
+
+cg_status cg_int4_compact(const cg_int4_cache *cache, int32_t first_layer,
+                          const cg_compaction *args, cg_stream_t stream);
+
+/* cg_pages_release: the counterpart of cg_pages_grow. Request r holds lens[r] tokens and
+ * keeps new_lens[r] of them (0: the request ends); the pages behind those go to the
+ * end of the list free_pages[0 .. *free_count), by request and then by position, and
+ * their entries of block_table become -1. The call writes
+ *   free_pages      the ids released, from *free_count on
+ *   block_table     -1 for the pages released; no other entry
+ *   cu_out          int32 [requests + 1]: exclusive prefix sum of the pages released
+ *   lens_out        int32 [requests]: new_lens (may be lens or new_lens itself)
+ *   free_count_out  int32 [1]: pages on the list (may be free_count itself)
+ *   status          16 bytes, 16-byte aligned, always written: CG_OK, or
+ *                   CG_ERR_INVALID_ARG   a negative length, or new_lens[r] above lens[r]
+ *                   CG_ERR_CAPACITY      the list, or a table row, is too short
+ *                   CG_ERR_CORRUPT       free_count outside [0, free_capacity]
+ *                   or a released page id outside [0, num_pages)
+ *                   of several the greatest code (a page id counts where there is no
+ *                   other error)
+ * With an error nothing is released: block_table and free_pages are as they were, lens_out
+ * and free_count_out repeat lens and free_count, cu_out is 0 (a page id outside the cache
+ * is the exception: it goes to the list as it is, where cg_pages_grow will find it). A
+ * page that several requests share must not be released by more than one of them. No
+ * other two arrays may overlap. Limits as for cg_pages_grow. Asynchronous on stream. */
+typedef struct cg_page_release {
+    int32_t *block_table;
+    int64_t table_stride;
+    int32_t table_width;
+    int32_t requests;
+    const int32_t *lens;
+    const int32_t *new_lens;
+    int32_t *free_pages;
+    const int32_t *free_count;
+    int32_t free_capacity;
+    int32_t num_pages;
+    int32_t page_tokens;
+    int32_t *cu_out;
+    int32_t *lens_out;
+    int32_t *free_count_out;
+    void *status;
+} cg_page_release;
+
+cg_status cg_pages_release(const cg_page_release *batch, cg_stream_t stream);
+
 /* Per-kernel timing, for profiling. When enabled, each kernel that
  * cg_encode/cg_decode enqueue is bracketed by two CUDA events on the launch
  * stream (up to max_launches kernels are recorded; later ones are not).

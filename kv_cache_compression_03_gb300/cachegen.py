@@ -87,6 +87,42 @@ class cg_attention(ct.Structure):
                 ("sinks", ct.c_int32), ("scale", ct.c_float)]
 
 
+class cg_token_weights(ct.Structure):
+    _fields_ = [("in_", ct.c_void_p), ("out", ct.c_void_p)] + \
+        [(n, ct.c_int64) for n in ("in_request_stride", "in_head_stride", "out_request_stride",
+                                   "out_head_stride")] + [("width", ct.c_int32)]
+
+
+class cg_token_choice(ct.Structure):
+    _fields_ = [("weights", ct.c_void_p), ("layer_stride", ct.c_int64),
+                ("request_stride", ct.c_int64), ("head_stride", ct.c_int64),
+                ("layers", ct.c_int32), ("requests", ct.c_int32), ("heads", ct.c_int32),
+                ("width", ct.c_int32), ("lens", ct.c_void_p), ("budget", ct.c_int32),
+                ("recent", ct.c_int32), ("sinks", ct.c_int32), ("kept", ct.c_void_p),
+                ("lens_out", ct.c_void_p), ("status", ct.c_void_p)]
+
+
+class cg_compaction(ct.Structure):
+    _fields_ = [("kept", ct.c_void_p), ("kept_layer_stride", ct.c_int64),
+                ("kept_request_stride", ct.c_int64), ("kept_head_stride", ct.c_int64),
+                ("weights", ct.c_void_p), ("weights_layer_stride", ct.c_int64),
+                ("weights_request_stride", ct.c_int64), ("weights_head_stride", ct.c_int64),
+                ("weights_width", ct.c_int32), ("budget", ct.c_int32), ("layers", ct.c_int32),
+                ("requests", ct.c_int32), ("lens", ct.c_void_p), ("new_lens", ct.c_void_p),
+                ("block_table", ct.c_void_p), ("table_stride", ct.c_int64),
+                ("table_width", ct.c_int32)]
+
+
+class cg_page_release(ct.Structure):
+    _fields_ = [("block_table", ct.c_void_p), ("table_stride", ct.c_int64),
+                ("table_width", ct.c_int32), ("requests", ct.c_int32), ("lens", ct.c_void_p),
+                ("new_lens", ct.c_void_p), ("free_pages", ct.c_void_p),
+                ("free_count", ct.c_void_p), ("free_capacity", ct.c_int32),
+                ("num_pages", ct.c_int32), ("page_tokens", ct.c_int32), ("cu_out", ct.c_void_p),
+                ("lens_out", ct.c_void_p), ("free_count_out", ct.c_void_p),
+                ("status", ct.c_void_p)]
+
+
 class CacheGenError(RuntimeError):
     def __init__(self, status: int, what: str):
         super().__init__(f"{what}: {cg_status_string(status)} ({status})")
@@ -172,6 +208,15 @@ def _open(path: str) -> ct.CDLL:
         "cg_pages_grow": (st, [P, P]),
         "cg_int4_attention_workspace": (st, [ct.POINTER(cg_int4_cache), P, ct.POINTER(sz)]),
         "cg_int4_attention": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, P, P, sz, P]),
+        "cg_int4_attention_shared_workspace": (st, [ct.POINTER(cg_int4_cache), P, ct.c_int32,
+                                                    ct.POINTER(sz)]),
+        "cg_int4_attention_shared": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, P, ct.c_int32, P,
+                                          sz, P]),
+        "cg_int4_weigh_workspace": (st, [ct.POINTER(cg_int4_cache), P, P, ct.POINTER(sz)]),
+        "cg_int4_weigh": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, P, P, P, sz, P]),
+        "cg_choose_tokens": (st, [P, P]),
+        "cg_int4_compact": (st, [ct.POINTER(cg_int4_cache), ct.c_int32, P, P]),
+        "cg_pages_release": (st, [P, P]),
         "cg_profile_enable": (st, [P, ct.c_int32]),
         "cg_profile_read": (st, [P, ct.POINTER(cg_kernel_profile), ct.c_int32,
                                  ct.POINTER(ct.c_int32)]),
@@ -598,8 +643,14 @@ _torch = None   # the module, once one of these calls needs it
 _ROWS = struct.Struct("@PPqqqqqq")
 _BATCH = struct.Struct("@PqiiPPPPiiiPPPPqP")
 _ATTENTION = struct.Struct("@PqqPqqPPPqiiiiiiif")
-assert _ROWS.size == ct.sizeof(cg_kv_rows) and _BATCH.size == ct.sizeof(cg_page_batch) and \
-    -(-_ATTENTION.size // 8) * 8 == ct.sizeof(cg_attention)
+_WEIGHTS = struct.Struct("@PPqqqqi")
+_CHOICE = struct.Struct("@PqqqiiiiPiiiPPP")
+_COMPACTION = struct.Struct("@PqqqPqqqiiiiPPPqi")
+_RELEASE = struct.Struct("@PqiiPPPPiiiPPPP")
+assert all(-(-s.size // 8) * 8 == ct.sizeof(t) for s, t in (
+    (_ROWS, cg_kv_rows), (_BATCH, cg_page_batch), (_ATTENTION, cg_attention),
+    (_WEIGHTS, cg_token_weights), (_CHOICE, cg_token_choice), (_COMPACTION, cg_compaction),
+    (_RELEASE, cg_page_release)))
 
 
 def _need_torch():
@@ -620,7 +671,7 @@ def _on_stream(stream, fn, *args, **kw):
     owner = getattr(fn, "__self__", None)
     used = [owner.data, owner.status] if owner is not None else []
     for a in args:
-        used += [a.slots, a.cu, a.lens, a.free_count, a.status] if isinstance(a, PagePlan) else [a]
+        used += vars(a).values() if isinstance(a, (PagePlan, KeptTokens, ReleasePlan)) else [a]
     for t in used:
         if isinstance(t, torch.Tensor):
             t.record_stream(stream)
@@ -677,7 +728,7 @@ def _table(t, device, what: str):
     if isinstance(t, torch.Tensor) and t.dtype is torch.int32 and t.device == device and t.dim() == 2:
         n, width = t.shape
         s0, s1 = t.stride()
-        if (s1 == 1 or width <= 1) and (s0 >= width or n <= 1):
+        if n == 0 or ((s1 == 1 or width <= 1) and (s0 >= width or n <= 1)):
             return n, width, s0 if n > 1 else width
     raise ValueError(f"{what} must be an int32 tensor [requests, pages] on {device}, a row's "
                      f"entries adjacent")
@@ -712,6 +763,30 @@ def _bf16_rows(t, device, shape, what: str, written: bool):
             _need(s >= inner, f"{what}: rows overlap")
             inner += s * (n - 1)
     return ptr, strides
+
+
+def _floats(t, device, shape, what: str, written: bool):
+    """(address, strides but the last) of an fp32 tensor [.., n] of the given
+    shape with adjacent elements (and, when written, rows that do not overlap). A dimension of
+    one element counts stride 0. Sums of attention weights carry no gradient: a tensor that
+    autograd would follow is refused."""
+    torch = _torch or _need_torch()
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.shape == shape and
+            t.device == device):
+        raise ValueError(f"{what} must be an fp32 tensor of shape {list(shape)} on {device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires grad, and no gradient flows through it: pass {what}.detach(), "
+                         f"or call under torch.no_grad()")
+    strides = t.stride()
+    if shape[-1] > 1 and strides[-1] != 1 and t.numel():
+        raise ValueError(f"{what}: elements of a row must be adjacent")
+    strides = [s if n > 1 else 0 for s, n in zip(strides[:-1], shape)]
+    if written and t.numel():
+        inner = shape[-1]
+        for s, n in sorted((s, n) for s, n in zip(strides, shape) if n > 1):
+            _need(s >= inner, f"{what}: rows overlap")
+            inner += s * (n - 1)
+    return t.data_ptr(), strides
 
 
 @dataclass
@@ -782,6 +857,126 @@ def grow_pages(block_table, lens, counts, free_pages, free_count, page_tokens: i
     with _Launch(dev.index) as s:
         st = (_lib or load()).cg_pages_grow(b, s)
     _check(st, "cg_pages_grow")
+    return out
+
+
+@dataclass
+class ReleasePlan:
+    """What release_pages did: tensors on the device."""
+    cu: "object"           # int32 [requests + 1], exclusive sums of the pages released
+    lens: "object"         # int32 [requests], the new ones
+    free_count: "object"   # int32 [1]
+    status: "object"       # uint8 [16]
+
+    def check(self):
+        """Wait for the current stream; raise if nothing was released."""
+        import torch
+        with torch.cuda.device(self.status.device):
+            st, _ = cg_last_device_error(None, self.status)
+        _check(st, "cg_pages_release (device)")
+
+
+def release_pages(block_table, lens, new_lens, free_pages, free_count, page_tokens: int,
+                  num_pages: int | None = None, out: ReleasePlan | None = None,
+                  stream=None) -> ReleasePlan:
+    """The pages behind shorter requests back to the list of free pages
+    (cg_pages_release in include/cachegen.h), the counterpart of grow_pages:
+    request r holds lens[r] tokens and keeps new_lens[r] (0 where it ends). free_pages
+    (int32 [capacity], free_count of them in use) gets the ids at its end,
+    block_table -1 in their place. A page that several requests share may be
+    released by one of them only: give the others' new_lens the shared tokens. ``num_pages``
+    and ``stream`` as for grow_pages; ``out`` reuses the buffers of an earlier plan, whose
+    lens may be lens or new_lens and whose free_count may be free_count."""
+    if stream is not None:
+        return _on_stream(stream, release_pages, block_table, lens, new_lens, free_pages,
+                          free_count, page_tokens, num_pages, out)
+    torch = _torch or _need_torch()
+    _need(isinstance(lens, torch.Tensor) and lens.is_cuda, "lens must be a CUDA tensor")
+    dev = lens.device
+    n = lens.shape[0] if lens.dim() == 1 else -1
+    lens_at, new_at = _ints(lens, dev, (n,), "lens"), _ints(new_lens, dev, (n,), "new_lens")
+    rows, width, stride = _table(block_table, dev, "block_table")
+    _need(rows == n, "block_table must have one row per request")
+    capacity = free_pages.numel()
+    free_at = _ints(free_pages, dev, (capacity,), "free_pages")
+    nfree_at = _ints(free_count, dev, (1,), "free_count")
+    _need(page_tokens > 0, "page_tokens must be positive")
+    if out is None:
+        e, i32 = torch.empty, torch.int32
+        out = ReleasePlan(e(n + 1, dtype=i32, device=dev), e(n, dtype=i32, device=dev),
+                          e(1, dtype=i32, device=dev), e(16, dtype=torch.uint8, device=dev))
+    else:
+        _ints(out.cu, dev, (n + 1,), "out.cu")
+        _ints(out.lens, dev, (n,), "out.lens")
+        _ints(out.free_count, dev, (1,), "out.free_count")
+        _check_status_buffer(out.status, "release_pages")
+        _need(out.status.device == dev, "out.status must be on the same device")
+    try:
+        b = _RELEASE.pack(block_table.data_ptr(), stride, width, n, lens_at, new_at, free_at, nfree_at,
+                          capacity, 0x7FFFFFFF // page_tokens if num_pages is None else num_pages,
+                          page_tokens, out.cu.data_ptr(), out.lens.data_ptr(),
+                          out.free_count.data_ptr(), out.status.data_ptr())
+    except struct.error as e:
+        raise ValueError(f"a number does not fit its type: {e}") from None
+    with _Launch(dev.index) as s:
+        st = (_lib or load()).cg_pages_release(b, s)
+    _check(st, "cg_pages_release")
+    return out
+
+
+@dataclass
+class KeptTokens:
+    """What choose_tokens found: tensors on the device."""
+    kept: "object"     # int32 [.., requests, heads, budget], ascending, -1 behind the last
+    lens: "object"     # int32 [requests]: tokens that stay
+    status: "object"   # uint8 [16]
+
+    def check(self):
+        """Wait for the current stream; raise if a length was wrong."""
+        import torch
+        with torch.cuda.device(self.status.device):
+            st, _ = cg_last_device_error(None, self.status)
+        _check(st, "cg_choose_tokens (device)")
+
+
+def choose_tokens(weights, lens, budget: int, recent: int = 0, sinks: int = 0,
+                  out: KeptTokens | None = None, stream=None) -> KeptTokens:
+    """The tokens of each head that stay when requests are cut to ``budget``
+    tokens (cg_choose_tokens in include/cachegen.h): the first ``sinks``, the last
+    ``recent`` and those with the greatest weights (fp32 [requests, heads, n], or
+    [layers, requests, heads, n], as Int4Cache.weigh sums them; lens int32 [requests]).
+    Of equal weights the lower token stays. ``out`` reuses the buffers of an
+    earlier choice; its lens may be lens. With ``stream`` the call runs there."""
+    if stream is not None:
+        return _on_stream(stream, choose_tokens, weights, lens, budget, recent, sinks, out)
+    torch = _torch or _need_torch()
+    _need(isinstance(weights, torch.Tensor) and weights.is_cuda and weights.dim() in (3, 4),
+          "weights must be a CUDA tensor [requests, heads, tokens], with or without layers")
+    dev, shape = weights.device, tuple(weights.shape)
+    at, strides = _floats(weights, dev, shape, "weights", False)
+    layers = shape[0] if len(shape) == 4 else 1
+    if len(shape) == 3:
+        strides = [0] + strides
+    n, heads, width = shape[-3:]
+    lens_at = _ints(lens, dev, (n,), "lens")
+    _need(0 <= _int32(budget, "budget"), "budget must not be negative")
+    if out is None:
+        out = KeptTokens(torch.empty(shape[:-1] + (budget,), dtype=torch.int32, device=dev),
+                         torch.empty(n, dtype=torch.int32, device=dev),
+                         torch.empty(16, dtype=torch.uint8, device=dev))
+    else:
+        _ints(out.kept, dev, shape[:-1] + (budget,), "out.kept")
+        _ints(out.lens, dev, (n,), "out.lens")
+        _check_status_buffer(out.status, "choose_tokens")
+        _need(out.status.device == dev, "out.status must be on the same device")
+    try:
+        c = _CHOICE.pack(at, *strides, layers, n, heads, width, lens_at, budget, recent, sinks,
+                         out.kept.data_ptr(), out.lens.data_ptr(), out.status.data_ptr())
+    except struct.error as e:
+        raise ValueError(f"a number does not fit its type: {e}") from None
+    with _Launch(dev.index) as s:
+        st = (_lib or load()).cg_choose_tokens(c, s)
+    _check(st, "cg_choose_tokens")
     return out
 
 
@@ -884,7 +1079,7 @@ class Int4Cache:
 
     def attention(self, q, cu_q, kv_lens, block_table, layer: int = 0, window: int = 0,
                   sinks: int = 0, scale: float | None = None, max_q_len: int | None = None,
-                  out=None, stream=None):
+                  out=None, stream=None, shared: int = 0):
         """Attention of the new tokens' queries q (bf16 [tokens, q_heads,
         head_size]) over a layer of the cache: request r owns the rows
         cu_q[r]:cu_q[r + 1] and sees its first kv_lens[r] tokens through row r of
@@ -893,10 +1088,15 @@ class Int4Cache:
         max_q_len, the most rows that any request has, should be given where it is
         small (1 in a decode step): without it kernels for more rows are launched
         too, and a batch of single tokens takes up to 1.7 times as long. Returns
-        out, like q; rows from cu_q[-1] on are not written."""
+        out, like q; rows from cu_q[-1] on are not written.
+
+        With ``shared``, a multiple of page_tokens, the first ``shared`` tokens of every
+        request lie in the same pages (kv_lens counts them, every row of block_table names
+        them; those of its first row are read): they are read once for the whole batch. Not
+        with a window."""
         if stream is not None:
             return _on_stream(stream, self.attention, q, cu_q, kv_lens, block_table, layer, window,
-                              sinks, scale, max_q_len, out)
+                              sinks, scale, max_q_len, out, None, shared)
         torch, dev, D = _torch, self.device, self.head_size
         shape = q.shape
         _need(len(shape) == 3, "q must be [tokens, q_heads, head_size]")
@@ -923,23 +1123,138 @@ class Int4Cache:
         L = _lib or load()
         # the size depends on the most rows that a request can have per KV head, and on the cache
         rows = (min(max_q_len, tokens) if max_q_len else tokens) * q_heads // self.num_heads
+        if shared:
+            _int32(shared, "shared")
+            rows = (rows, tokens, q_heads)
+            _need(not window and 0 < shared <= width * self.page_tokens and
+                  shared % self.page_tokens == 0,
+                  "shared must be whole pages that a row of block_table can hold, without a window")
         size, ws, ws_at = self._sizes.get(rows), None, None
         if size is None:
             need = ct.c_size_t(0)
-            _check(L.cg_int4_attention_workspace(self._ref, a, ct.byref(need)),
-                   "cg_int4_attention_workspace")
-            if len(self._sizes) >= 1024:
-                self._sizes.clear()
-            size = self._sizes[rows] = need.value
+            if shared:
+                _check(L.cg_int4_attention_shared_workspace(self._ref, a, shared, ct.byref(need)),
+                       "cg_int4_attention_shared_workspace")
+            else:
+                _check(L.cg_int4_attention_workspace(self._ref, a, ct.byref(need)),
+                       "cg_int4_attention_workspace")
+            size = self._keep_size(rows, need.value)
         if size:
             # one per call, from the current stream's pool: calls on other
             # streams and captured graphs never share one
             ws = torch.empty(size, dtype=torch.uint8, device=dev)
             ws_at = ws.data_ptr()
         with _Launch(dev.index) as s:
-            st = L.cg_int4_attention(self._ref, layer, a, ws_at, size, s)
+            if shared:
+                st = L.cg_int4_attention_shared(self._ref, layer, a, shared, ws_at, size, s)
+            else:
+                st = L.cg_int4_attention(self._ref, layer, a, ws_at, size, s)
         _check(st, "cg_int4_attention")
         return out
+
+    def _keep_size(self, key, size: int) -> int:
+        if len(self._sizes) >= 1024:
+            self._sizes.clear()
+        self._sizes[key] = size
+        return size
+
+    def weigh(self, q, cu_q, kv_lens, block_table, weights=None, layer: int = 0, window: int = 0,
+              sinks: int = 0, scale: float | None = None, max_q_len: int | None = None, out=None,
+              stream=None):
+        """Add the attention weights that the cached tokens get from the new tokens'
+        queries, summed per KV head (cg_int4_weigh in include/cachegen.h), to
+        ``weights`` (fp32 [requests, heads, n], a row of it per row of block_table, n at
+        least every kv_lens[r]). The other arguments are those of attention, and so are the
+        weights. The sums go to ``out`` (like weights), or to weights itself;
+        without either a new tensor [requests, heads, pages of a row * page_tokens] is made of
+        zeros. Elements behind a request's last token are not written: a row starts as
+        zeros with its request. Returns what was written."""
+        if stream is not None:
+            return _on_stream(stream, self.weigh, q, cu_q, kv_lens, block_table, weights, layer, window,
+                              sinks, scale, max_q_len, out)
+        torch, dev, D = _torch, self.device, self.head_size
+        shape = q.shape
+        _need(len(shape) == 3, "q must be [tokens, q_heads, head_size]")
+        _int32(layer, "layer")
+        tokens, q_heads, _ = shape
+        if q_heads <= 0 or q_heads % self.num_heads:
+            raise ValueError(f"q_heads must be a multiple of {self.num_heads}")
+        q_at, (qs0, qs1) = _bf16_rows(q, dev, (tokens, q_heads, D), "q", False)
+        n, width, stride = _table(block_table, dev, "block_table")
+        lens_at = _ints(kv_lens, dev, (n,), "kv_lens (one entry per row of block_table)")
+        cu_at = _ints(cu_q, dev, (n + 1,), "cu_q")
+        if out is None and weights is None:
+            out = torch.zeros((n, self.num_heads, width * self.page_tokens), dtype=torch.float32, device=dev)
+        elif out is None:
+            out = weights
+        _need(isinstance(out, torch.Tensor) and out.dim() == 3, "weights must be [requests, heads, tokens]")
+        shape = (n, self.num_heads, out.shape[2])
+        out_at, (os0, os1) = _floats(out, dev, shape, "out" if out is not weights else "weights", True)
+        in_at = is0 = is1 = 0
+        if weights is out:
+            in_at, is0, is1 = out_at, os0, os1
+        elif weights is not None:
+            in_at, (is0, is1) = _floats(weights, dev, shape, "weights", False)
+        try:
+            a = _ATTENTION.pack(q_at, qs0, qs1, 0, 0, 0, cu_at, lens_at, block_table.data_ptr(), stride, width,
+                                n, tokens, q_heads, max_q_len or 0, window, sinks,
+                                D ** -0.5 if scale is None else scale)
+            w = _WEIGHTS.pack(in_at, out_at, is0, is1, os0, os1, shape[2])
+        except struct.error as e:
+            raise ValueError(f"a number does not fit its type: {e}") from None
+        L = _lib or load()
+        key = (tokens, q_heads, max_q_len, n, shape[2])
+        size = self._sizes.get(key)
+        if size is None:
+            need = ct.c_size_t(0)
+            _check(L.cg_int4_weigh_workspace(self._ref, a, w, ct.byref(need)), "cg_int4_weigh_workspace")
+            size = self._keep_size(key, need.value)
+        ws = torch.empty(size, dtype=torch.uint8, device=dev)   # one per call, as for attention
+        with _Launch(dev.index) as s:
+            st = L.cg_int4_weigh(self._ref, layer, a, w, ws.data_ptr(), size, s)
+        _check(st, "cg_int4_weigh")
+        return out
+
+    def compact(self, kept, new_lens, lens, block_table, weights=None, layer: int = 0, stream=None) -> None:
+        """Move the tokens that stay to the front of their request's pages
+        (cg_int4_compact in include/cachegen.h): token kept[r, h, i] of request r's head
+        h goes to place i < new_lens[r]. kept is int32 [requests, heads, budget] for one
+        layer, or [layers, requests, heads, budget] for the layers from ``layer`` on,
+        as choose_tokens gives it with new_lens. ``weights`` (fp32 [requests, heads, n], with
+        layers where kept has them) move along, and what is behind becomes 0. The pages behind
+        can then be given back with release_pages, once every layer has been compacted."""
+        if stream is not None:
+            return _on_stream(stream, self.compact, kept, new_lens, lens, block_table, weights, layer)
+        torch, dev = _torch, self.device
+        _need(isinstance(kept, torch.Tensor) and kept.dtype is torch.int32 and kept.device == dev and
+              kept.dim() in (3, 4), f"kept must be an int32 tensor [requests, heads, budget] on {dev}, with or "
+                                    f"without layers")
+        shape = tuple(kept.shape)
+        layers, budget = shape[0] if len(shape) == 4 else 1, shape[-1]
+        n, width, stride = _table(block_table, dev, "block_table")
+        _need(shape[-3:-1] == (n, self.num_heads), f"kept must be [requests, heads, budget] = [{n}, "
+                                                   f"{self.num_heads}, budget], with or without layers")
+        ks = kept.stride()
+        _need(budget <= 1 or ks[-1] == 1 or kept.numel() == 0, "kept: entries of a row must be adjacent")
+        ks = [s if m > 1 else 0 for s, m in zip(ks[:-1], shape)]
+        lens_at, new_at = _ints(lens, dev, (n,), "lens"), _ints(new_lens, dev, (n,), "new_lens")
+        w_at, wstr, w_width = 0, [0] * len(ks), 0
+        if weights is not None:
+            _need(isinstance(weights, torch.Tensor) and weights.dim() == len(shape), "weights must have kept's dimensions")
+            w_width = weights.shape[-1]
+            w_at, wstr = _floats(weights, dev, shape[:-1] + (w_width,), "weights", True)
+            w_at = w_at or 256   # (an empty tensor has no address: lengths are still held against its width)
+        if len(shape) == 3:
+            ks, wstr = [0] + ks, [0] + wstr
+        _int32(layer, "layer")
+        try:
+            c = _COMPACTION.pack(kept.data_ptr(), *ks, w_at, *wstr, w_width, budget, layers, n, lens_at,
+                                 new_at, block_table.data_ptr(), stride, width)
+        except struct.error as e:
+            raise ValueError(f"a number does not fit its type: {e}") from None
+        with _Launch(dev.index) as s:
+            st = (_lib or load()).cg_int4_compact(self._ref, layer, c, s)
+        _check(st, "cg_int4_compact")
 
     def check(self):
         """Wait for the current stream; raise the first error that the GPU

@@ -16,8 +16,41 @@ namespace {
 
 constexpr float kLog2E = 1.4426950408889634f;   // scores are taken in powers of two
 
-// The call's sizes (not its pointers).
-cg_status check_sizes(const cg_int4_cache *c, const cg_attention *a)
+// Requests with up to this many rows per KV head go to the kernel for few rows,
+// which works on 16 at a time and reads the tokens again for each 16; the other
+// expands them once for up to 256. Here and there, 8 KV heads of 128: 20 rows,
+// eight requests at 16K, 116 us and 127 us; 32 rows, four at 128K, 389 and 427,
+// 64 at 1K, 86 and 82; 48 rows, four at 128K, 569 and 428, 16 at 2K, 62 and 44.
+constexpr int kFewRows = 32;
+
+// Most rows of one KV head that a request can have (query heads times tokens).
+int64_t max_rows(const cg_int4_cache *c, const cg_attention *a)
+{
+    const int n = a->max_q_len > 0 && a->max_q_len < a->tokens ? a->max_q_len : a->tokens;
+    return (int64_t)n * (a->q_heads / c->num_heads);
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+// The workspace's part for the kernel for few rows.
+size_t few_bytes(const cg_int4_cache *c, int64_t rows)
+{
+    return align256(attn_few_workspace(c->head_size, (int)(rows < kFewRows ? rows : kFewRows)));
+}
+
+cg_status launch_passes(const cg_int4_cache *c, const AttnArgs &p, uint8_t *workspace, cudaStream_t s)
+{
+    const int64_t most = max_rows(c, &p.a);
+    cudaError_t err = attn_few_launch(p, c->head_size, c->group,
+                                      (int)(most < kFewRows ? most : kFewRows), workspace, s);
+    if (err == cudaSuccess && most > kFewRows)
+        err = attn_many_launch(p, c->head_size, c->group, workspace + few_bytes(c, most), s);
+    return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
+}
+
+}  // namespace
+
+cg_status attn_check_sizes(const cg_int4_cache *c, const cg_attention *a)
 {
     const cg_status st = int4_check_shape(c);
     if (st != CG_OK)
@@ -33,28 +66,37 @@ cg_status check_sizes(const cg_int4_cache *c, const cg_attention *a)
     return CG_OK;
 }
 
-// Requests with up to this many rows per KV head go to the kernel for few rows,
-// which works on 16 at a time and reads the tokens again for each 16; the other
-// expands them once for up to 256. Here and there, 8 KV heads of 128: 20 rows,
-// eight requests at 16K, 116 us and 127 us; 32 rows, four at 128K, 389 and 427,
-// 64 at 1K, 86 and 82; 48 rows, four at 128K, 569 and 428, 16 at 2K, 62 and 44.
-constexpr int kFewRows = 32;
-
-// Most rows of one KV head that a request can have (query heads times tokens).
-int64_t max_rows(const cg_int4_cache *c, const cg_attention *a)
+AttnArgs attn_args(const cg_int4_cache *c, int32_t layer, const cg_attention *a)
 {
-    const int n = a->max_q_len > 0 && a->max_q_len < a->tokens ? a->max_q_len : a->tokens;
-    return (int64_t)n * (a->q_heads / c->num_heads);
+    AttnArgs p = {};
+    p.layer = static_cast<const uint8_t *>(c->data) +
+              (size_t)layer * c->num_pages * int4_page_bytes(c);
+    p.status = c->status;
+    p.num_pages = c->num_pages;
+    p.page_tokens = c->page_tokens;
+    p.heads = c->num_heads;
+    p.ratio = p.pos_ratio = a->q_heads / c->num_heads;
+    p.few_rows = kFewRows;
+    p.scale2 = a->scale * kLog2E;
+    p.kv_limit = (int64_t)a->table_width * c->page_tokens;
+    p.a = *a;
+    return p;
 }
 
-// The workspace's part for the kernel for few rows.
-size_t few_bytes(const cg_int4_cache *c, int64_t rows)
+cg_status attn_check_arrays(const cg_attention *a, bool with_out)
 {
-    const size_t n = attn_few_workspace(c->head_size, (int)(rows < kFewRows ? rows : kFewRows));
-    return (n + 255) / 256 * 256;
+    if ((a->q == nullptr && a->tokens > 0) || a->cu_q == nullptr || a->kv_lens == nullptr ||
+        (a->block_table == nullptr && a->table_width > 0) || !int4_aligned(a->q, 16) ||
+        !int4_aligned(a->cu_q, 4) || !int4_aligned(a->kv_lens, 4) || !int4_aligned(a->block_table, 4) ||
+        (with_out && (a->out == nullptr || !int4_aligned(a->out, 16))))
+        return CG_ERR_INVALID_ARG;
+    const int64_t strides[4] = {a->q_token_stride, a->q_head_stride, with_out ? a->out_token_stride : 0,
+                                with_out ? a->out_head_stride : 0};
+    for (int64_t s : strides)
+        if (s < 0 || s % 8 != 0)
+            return CG_ERR_INVALID_ARG;
+    return CG_OK;
 }
-
-}  // namespace
 
 cudaError_t attn_sm_count(int *sms)
 {
@@ -78,7 +120,7 @@ extern "C" cg_status cg_int4_attention_workspace(const cg_int4_cache *c, const c
 {
     if (c == nullptr || a == nullptr || bytes == nullptr)
         return CG_ERR_INVALID_ARG;
-    const cg_status st = check_sizes(c, a);
+    const cg_status st = attn_check_sizes(c, a);
     if (st != CG_OK)
         return st;
     // a part each: the two kernels may run side by side
@@ -104,35 +146,89 @@ extern "C" cg_status cg_int4_attention(const cg_int4_cache *c, int32_t layer,
         return CG_ERR_INVALID_ARG;
     if (a->requests == 0 || a->tokens == 0)
         return CG_OK;
-    if (a->q == nullptr || a->out == nullptr || a->cu_q == nullptr || a->kv_lens == nullptr ||
-        (a->block_table == nullptr && a->table_width > 0) || !int4_aligned(a->q, 16) ||
-        !int4_aligned(a->out, 16) || !int4_aligned(a->cu_q, 4) || !int4_aligned(a->kv_lens, 4) ||
-        !int4_aligned(a->block_table, 4) || !int4_aligned(workspace, 256))
+    if (!int4_aligned(workspace, 256))
         return CG_ERR_INVALID_ARG;
-    const int64_t strides[4] = {a->q_token_stride, a->q_head_stride, a->out_token_stride,
-                                a->out_head_stride};
-    for (int64_t s : strides)
-        if (s < 0 || s % 8 != 0)
-            return CG_ERR_INVALID_ARG;
+    st = attn_check_arrays(a, true);
+    if (st != CG_OK)
+        return st;
     if (workspace_bytes < need || (need > 0 && workspace == nullptr))
         return CG_ERR_CAPACITY;
-    AttnArgs p;
-    p.layer = static_cast<const uint8_t *>(c->data) +
-              (size_t)layer * c->num_pages * int4_page_bytes(c);
-    p.status = c->status;
-    p.num_pages = c->num_pages;
-    p.page_tokens = c->page_tokens;
-    p.heads = c->num_heads;
-    p.ratio = a->q_heads / c->num_heads;
-    p.few_rows = kFewRows;
-    p.scale2 = a->scale * kLog2E;
-    p.a = *a;
+    const AttnArgs p = attn_args(c, layer, a);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t most = max_rows(c, a);
-    cudaError_t err = attn_few_launch(p, c->head_size, c->group,
-                                      (int)(most < kFewRows ? most : kFewRows), workspace, s);
-    if (err == cudaSuccess && most > kFewRows)
-        err = attn_many_launch(p, c->head_size, c->group,
-                               static_cast<uint8_t *>(workspace) + few_bytes(c, most), s);
-    return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
+    return launch_passes(c, p, static_cast<uint8_t *>(workspace), s);
+}
+
+// Shared tokens: one pass takes them for all rows of the batch, as one request's that all see
+// every token, and leaves its results and their sums in fp32; the other takes each
+// request's own tokens as ever and joins the two where it writes a row.
+//
+// 64 requests with a token each and 4 query heads to a KV head are 256 rows to the shared tokens:
+// they are read once, by the kernel for many rows, where a call for each request would read
+// them 64 times.
+
+extern "C" cg_status cg_int4_attention_shared_workspace(const cg_int4_cache *c, const cg_attention *a,
+                                                        int32_t shared, size_t *bytes)
+{
+    const cg_status st = cg_int4_attention_workspace(c, a, bytes);   // of the pass over own tokens
+    if (st != CG_OK)
+        return st;
+    if (shared < 0 || shared % c->page_tokens != 0 || shared / c->page_tokens > a->table_width ||
+        (shared > 0 && a->window > 0))
+        return CG_ERR_INVALID_ARG;
+    if (shared == 0)
+        return CG_OK;
+    // that of the other, which runs before it, may take more
+    cg_attention all = *a;
+    all.max_q_len = 0;
+    size_t first = 0;
+    cg_int4_attention_workspace(c, &all, &first);
+    if (first > *bytes)
+        *bytes = first;
+    const size_t rows = (size_t)a->tokens * a->q_heads;
+    *bytes = align256(*bytes) + align256(rows * c->head_size * sizeof(float)) + align256(rows * sizeof(float2));
+    return CG_OK;
+}
+
+extern "C" cg_status cg_int4_attention_shared(const cg_int4_cache *c, int32_t layer, const cg_attention *a,
+                                              int32_t shared, void *workspace, size_t workspace_bytes,
+                                              cg_stream_t stream)
+{
+    cg_status st = int4_check(c);
+    if (st != CG_OK)
+        return st;
+    size_t need = 0;
+    st = cg_int4_attention_shared_workspace(c, a, shared, &need);
+    if (st != CG_OK)
+        return st;
+    if (shared == 0)
+        return cg_int4_attention(c, layer, a, workspace, workspace_bytes, stream);
+    if (layer < 0 || layer >= c->num_layers)
+        return CG_ERR_INVALID_ARG;
+    if (a->requests == 0 || a->tokens == 0)
+        return CG_OK;
+    if (!int4_aligned(workspace, 256))
+        return CG_ERR_INVALID_ARG;
+    st = attn_check_arrays(a, true);
+    if (st != CG_OK)
+        return st;
+    if (workspace_bytes < need || (need > 0 && workspace == nullptr))
+        return CG_ERR_CAPACITY;
+    const size_t rows = (size_t)a->tokens * a->q_heads;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    AttnArgs p = attn_args(c, layer, a);
+    p.shared = shared;
+    p.row_stats = reinterpret_cast<float2 *>(ws + need - align256(rows * sizeof(float2)));
+    p.rows = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.row_stats) -
+                                       align256(rows * c->head_size * sizeof(float)));
+    AttnArgs first = p;
+    first.first = true;
+    first.pos_ratio = INT32_MAX;
+    first.a.cu_q += a->requests;
+    first.a.requests = 1;
+    first.a.max_q_len = 0;
+    p.a.block_table += shared / c->page_tokens;
+    p.a.table_width -= shared / c->page_tokens;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    st = launch_passes(c, first, ws, s);
+    return st == CG_OK ? launch_passes(c, p, ws, s) : st;
 }

@@ -301,8 +301,8 @@ __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t item, int s
         units_of(p, r, &q);
         // the last rows, which see most, first
         const int tile = (q.rows + kRows - 1) / kRows - 1 - off / p.heads;
-        const int row0 = tile * kRows, rows = min(kRows, q.rows - row0), x0 = q.kv - q.nq;
-        const int x_first = x0 + row0 / p.ratio, x_last = x0 + (row0 + rows - 1) / p.ratio;
+        const int row0 = tile * kRows, rows = min(kRows, q.rows - row0), x0 = q.x0;
+        const int x_first = x0 + row0 / p.pos_ratio, x_last = x0 + (row0 + rows - 1) / p.pos_ratio;
         const int end = x_last < 0 ? 0 : x_last / 16 + 1;
         int sink = 0, skip = 0;
         const int64_t low = (int64_t)x_first + 1 - p.a.window;
@@ -444,9 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
             const int tile = turns ? 0 : i, first = turns ? i : 0, step = turns ? 2 : 1;
             if (tile < u.tiles_q) {
                 const int rr = u.row0 + 128 * tile + 32 * (warp & 3) + lane;
-                const int x = rr < u.rows ? u.x0 + rr / p.ratio : -1;
+                const int x = rr < u.rows ? u.x0 + rr / p.pos_ratio : -1;
                 const int last_row = min(u.row0 + 128 * tile + 128, u.rows) - 1;
-                const int x_lo = u.x0 + (u.row0 + 128 * tile) / p.ratio, x_hi = u.x0 + last_row / p.ratio;
+                const int x_lo = u.x0 + (u.row0 + 128 * tile) / p.pos_ratio;
+                const int x_hi = u.x0 + last_row / p.pos_ratio;
                 float m = kNone, l = 0.0f;
                 bool alive = true;
                 for (int j = first; j < n; j += step) {
@@ -565,8 +566,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                 }
                 if (!alive)
                     break;
-                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
+                float *shared_row = nullptr, shared_f = 0.0f;
+                if (p.rows != nullptr && u.parts == 1 && rr < u.rows) {
+                    const int64_t row = (int64_t)(u.q_row0 + qt) * p.a.q_heads + qh;
+                    shared_row = p.rows + row * D;
+                    if (p.first) {
+                        p.row_stats[row] = make_float2(m, l);
+                    } else {
+                        const float2 f = join_factors(p, row, m, l);
+                        inv *= f.x;
+                        shared_f = f.y;
+                    }
+                }
                 __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(p.a.out) +
                                      (int64_t)(u.q_row0 + qt) * p.a.out_token_stride + qh * p.a.out_head_stride;
                 float *part = work.parts + u.item * kPartFloats<D>;
@@ -594,6 +607,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         for (int g = 0; g < 8; ++g)
                             *reinterpret_cast<float4 *>(part + (size_t)part_row * D + 32 * c + 4 * g) =
                                 make_float4(o[g], o[8 + g], o[16 + g], o[24 + g]);
+                    } else if (shared_row != nullptr) {
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) {
+                            float4 *there = reinterpret_cast<float4 *>(shared_row + 32 * c + 4 * g);
+                            float4 v = make_float4(o[g] * inv, o[8 + g] * inv, o[16 + g] * inv, o[24 + g] * inv);
+                            if (p.first) {
+                                *there = v;
+                            } else {
+                                const float4 b = *there;
+                                v = make_float4(fmaf(b.x, shared_f, v.x), fmaf(b.y, shared_f, v.y),
+                                                fmaf(b.z, shared_f, v.z), fmaf(b.w, shared_f, v.w));
+                                *reinterpret_cast<uint2 *>(out + 32 * c + 4 * g) =
+                                    make_uint2(pack_bf16(v.x, v.y), pack_bf16(v.z, v.w));
+                            }
+                        }
                     } else {
 #pragma unroll
                         for (int g = 0; g < 8; g += 2)
@@ -1017,14 +1045,33 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
             l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
+#pragma unroll
+        for (int c = 0; c < kC; ++c)
+            sum[c] *= inv;
+        if (p.rows != nullptr) {
+            const int64_t at_row = (int64_t)(u.q_row0 + qt) * p.a.q_heads + qh;
+            float *there = p.rows + at_row * D + kC * lane;
+            if (p.first) {
+#pragma unroll
+                for (int c = 0; c < kC; ++c)
+                    there[c] = sum[c];
+                if (lane == 0)
+                    p.row_stats[at_row] = make_float2(mx, l);
+                continue;
+            }
+            const float2 f = join_factors(p, at_row, mx, l);
+#pragma unroll
+            for (int c = 0; c < kC; ++c)
+                sum[c] = fmaf(there[c], f.y, sum[c] * f.x);
+        }
         uint32_t *out = reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(p.a.out) +
                                                      (int64_t)(u.q_row0 + qt) * p.a.out_token_stride +
                                                      qh * p.a.out_head_stride + kC * lane);
         if constexpr (kC == 4)
             *reinterpret_cast<uint2 *>(out) =
-                make_uint2(pack_bf16(sum[0] * inv, sum[1] * inv), pack_bf16(sum[2] * inv, sum[3] * inv));
+                make_uint2(pack_bf16(sum[0], sum[1]), pack_bf16(sum[2], sum[3]));
         else
-            *out = pack_bf16(sum[0] * inv, sum[1] * inv);
+            *out = pack_bf16(sum[0], sum[1]);
     }
 }
 

@@ -1,7 +1,7 @@
 // cg_pages_grow: pages and slots of a batch's new tokens from the requests'
-// lengths, on the GPU.
+// lengths, on the GPU; cg_pages_release: the pages behind shorter lengths back to the list.
 //
-// Two prefix sums over the requests (new tokens, pages needed) place every
+// Growing. Two prefix sums over the requests (new tokens, pages needed) place every
 // new token and page. The sums run in one block, so nothing waits on another
 // block and the in-place outputs have one writer. Pages and slots of small
 // batches are filled by the same block; larger ones take two more launches, over
@@ -219,6 +219,104 @@ __global__ void __launch_bounds__(kSlotThreads) k_page_slots(cg_page_batch b)
     }
 }
 
+// ------------------------------------------------------------------ release
+
+// A block of 1024 threads sums the pages that the requests release, in their order, and
+// writes all that is one to a request.
+__global__ void __launch_bounds__(kThreads) k_pages_release(cg_page_release b)
+{
+    __shared__ int64_t warp_sum[kWarps];
+    __shared__ uint32_t error;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int32_t P = b.page_tokens, nfree = *b.free_count;
+    if (tid == 0) {
+        error = CG_OK;
+        static_cast<uint4 *>(b.status)[0] = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    if (tid == 0 && (nfree < 0 || nfree > b.free_capacity))
+        atomicMax(&error, (uint32_t)CG_ERR_CORRUPT);
+    constexpr int kMost = (CG_MAX_REQUESTS + kThreads - 1) / kThreads;
+    const int each = (b.requests + kThreads - 1) / kThreads;
+    int32_t len[kMost], kept[kMost], pages[kMost];
+    int64_t own = 0;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int r = tid * each + i;
+        len[i] = kept[i] = pages[i] = 0;
+        if (i < each && r < b.requests) {
+            len[i] = b.lens[r];
+            kept[i] = b.new_lens[r];
+            if (kept[i] < 0 || kept[i] > len[i]) {
+                atomicMax(&error, (uint32_t)CG_ERR_INVALID_ARG);
+            } else {
+                const int64_t held = ((int64_t)len[i] + P - 1) / P;
+                if (held > b.table_width)
+                    atomicMax(&error, (uint32_t)CG_ERR_CAPACITY);
+                pages[i] = (int32_t)(held - ((int64_t)kept[i] + P - 1) / P);
+                own += pages[i];
+            }
+        }
+    }
+    int64_t inc = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
+        if (lane >= d)
+            inc += o;
+    }
+    if (lane == 31)
+        warp_sum[warp] = inc;
+    __syncthreads();
+    int64_t before = inc - own, total = 0;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        if (i < warp)
+            before += warp_sum[i];
+        total += warp_sum[i];
+    }
+    if (tid == 0 && total > (int64_t)b.free_capacity - nfree)
+        atomicMax(&error, (uint32_t)CG_ERR_CAPACITY);
+    __syncthreads();
+    const uint32_t err = error;
+#pragma unroll
+    for (int i = 0; i < kMost; ++i) {
+        const int r = tid * each + i;
+        if (i < each && r < b.requests) {
+            b.cu_out[r] = err ? 0 : (int32_t)before;
+            before += pages[i];
+            b.lens_out[r] = err ? len[i] : kept[i];
+        }
+    }
+    if (tid == 0) {
+        b.cu_out[b.requests] = err ? 0 : (int32_t)total;
+        *b.free_count_out = err ? nfree : nfree + (int32_t)total;
+        if (err)
+            static_cast<uint32_t *>(b.status)[0] = err;
+    }
+}
+
+// The page ids, a warp to a request.
+__global__ void __launch_bounds__(kSlotThreads) k_release_ids(cg_page_release b)
+{
+    const int lane = threadIdx.x & 31, r = (int)((blockIdx.x * kSlotThreads + threadIdx.x) >> 5);
+    if (r >= b.requests)
+        return;
+    const int32_t first = b.cu_out[r], n = b.cu_out[r + 1] - first;
+    if (n == 0)   // after an error too
+        return;
+    const int32_t nfree = *b.free_count_out - b.cu_out[b.requests];
+    const int32_t stays = (int32_t)(((int64_t)b.lens_out[r] + b.page_tokens - 1) / b.page_tokens);
+    int32_t *table = b.block_table + r * b.table_stride + stays;
+    for (int32_t i = lane; i < n; i += 32) {
+        const int32_t id = table[i];
+        if (id < 0 || id >= b.num_pages)
+            int4_set_status(b.status, CG_ERR_CORRUPT);
+        b.free_pages[nfree + first + i] = id;
+        table[i] = -1;
+    }
+}
+
 }  // namespace
 
 extern "C" cg_status cg_pages_grow(const cg_page_batch *b, cg_stream_t stream)
@@ -259,5 +357,32 @@ extern "C" cg_status cg_pages_grow(const cg_page_batch *b, cg_stream_t stream)
         k_page_slots<<<(unsigned)((b->tokens + kSlotTile - 1) / kSlotTile), kSlotThreads, 0,
                        s>>>(*b);
     }
+    return cudaGetLastError() == cudaSuccess ? CG_OK : CG_ERR_CUDA;
+}
+
+extern "C" cg_status cg_pages_release(const cg_page_release *b, cg_stream_t stream)
+{
+    if (b == nullptr || b->requests < 0 || b->table_width < 0 || b->table_stride < b->table_width ||
+        b->free_capacity < 0 || b->num_pages <= 0 || b->page_tokens <= 0)
+        return CG_ERR_INVALID_ARG;
+    if (b->page_tokens % 16 != 0 || b->page_tokens > 1024 ||
+        (int64_t)b->num_pages * b->page_tokens >= ((int64_t)1 << 31) || b->requests > CG_MAX_REQUESTS)
+        return CG_ERR_UNSUPPORTED;
+    if (b->status == nullptr || !int4_aligned(b->status, 16) || b->free_count == nullptr ||
+        b->cu_out == nullptr || b->free_count_out == nullptr)
+        return CG_ERR_INVALID_ARG;
+    if ((b->requests > 0 && (b->lens == nullptr || b->new_lens == nullptr || b->lens_out == nullptr)) ||
+        (b->requests > 0 && b->table_width > 0 && b->block_table == nullptr) ||
+        (b->free_capacity > 0 && b->free_pages == nullptr))
+        return CG_ERR_INVALID_ARG;
+    const void *words[] = {b->block_table, b->lens, b->new_lens, b->free_pages, b->free_count,
+                           b->cu_out, b->lens_out, b->free_count_out};
+    for (const void *p : words)
+        if (!int4_aligned(p, 4))
+            return CG_ERR_INVALID_ARG;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    k_pages_release<<<1, kThreads, 0, s>>>(*b);
+    if (b->requests > 0)
+        k_release_ids<<<(b->requests * 32 + kSlotThreads - 1) / kSlotThreads, kSlotThreads, 0, s>>>(*b);
     return cudaGetLastError() == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

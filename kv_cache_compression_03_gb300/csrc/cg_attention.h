@@ -10,13 +10,22 @@ struct AttnArgs {
     int32_t few_rows;       // requests with up to this many rows per KV head go to the
                             // kernel for few rows
     float scale2;           // scale * log2(e)
+    int64_t kv_limit;       // most tokens of a request
+    // Where all requests begin with the same `shared` tokens, one pass takes those, all rows
+    // of the batch as one request's, and leaves its results in rows; the other takes the
+    // tokens behind them (the table and the lengths begin there) and joins the two.
+    int32_t shared;         // 0: none
+    bool first;             // the pass over the shared tokens
+    int32_t pos_ratio;      // rows to a position: ratio; more than there are where all rows see alike
+    float *rows;            // [tokens * q_heads][head_size], normalised; nullptr: no shared tokens
+    float2 *row_stats;      // [tokens * q_heads]: maximum of the scores, sum
     cg_attention a;
 };
 
 // One request's rows and tokens.
 struct AttnRequest {
-    int32_t row0, nq, kv;   // first query row, query rows, cached tokens
-    int32_t rows;           // nq * ratio: rows of one KV head
+    int32_t row0, x0, kv;   // first query row, its position, cached tokens
+    int32_t rows;           // new tokens * ratio: rows of one KV head
 };
 
 // False for a request without rows and for an invalid one, which *error
@@ -24,17 +33,20 @@ struct AttnRequest {
 __device__ __forceinline__ bool attn_request(const AttnArgs &p, int r, AttnRequest *q,
                                              uint32_t *error)
 {
-    const int32_t c0 = p.a.cu_q[r], c1 = p.a.cu_q[r + 1], kv = p.a.kv_lens[r];
+    // in the pass over the shared tokens cu_q points at its last entry, the batch's rows
+    const int32_t c0 = p.first ? 0 : p.a.cu_q[r], c1 = p.a.cu_q[p.first ? 0 : r + 1];
+    const int32_t kv = p.first ? p.shared : p.a.kv_lens[r];
     *error = CG_OK;
-    if (c0 < 0 || c1 < c0 || c1 > p.a.tokens || kv < 0 ||
-        (int64_t)kv > (int64_t)p.a.table_width * p.page_tokens)
+    if (c0 < 0 || c1 < c0 || c1 > p.a.tokens || kv < 0 || kv > p.kv_limit)
         *error = CG_ERR_CORRUPT;
     else if (p.a.max_q_len > 0 && c1 - c0 > p.a.max_q_len)
         *error = CG_ERR_INVALID_ARG;
+    else if (!p.first && p.shared > 0 && c1 > c0 && kv - p.shared < c1 - c0)
+        *error = CG_ERR_INVALID_ARG;
     q->row0 = c0;
-    q->nq = c1 - c0;
-    q->kv = kv;
-    q->rows = q->nq * p.ratio;   // at most tokens * q_heads, which fits
+    q->kv = p.first ? kv : kv - p.shared;
+    q->x0 = p.first ? kv - 1 : q->kv - (c1 - c0);
+    q->rows = (c1 - c0) * p.ratio;   // at most tokens * q_heads, which fits
     return *error == CG_OK && c1 > c0;
 }
 
@@ -45,6 +57,16 @@ __device__ __forceinline__ float exp2_fast(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Row (token * q_heads + head) of the pass behind the shared tokens: the factors of its own
+// normalised result, whose scores had maximum m and sum l, and of the shared tokens'.
+__device__ __forceinline__ float2 join_factors(const AttnArgs &p, int64_t row, float m, float l)
+{
+    const float2 before = p.row_stats[row];
+    const float mx = fmaxf(m, before.x);
+    const float a = l * exp2_fast(m - mx), b = before.y * exp2_fast(before.x - mx), sum = a + b;
+    return sum == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(a / sum, b / sum);
 }
 
 // Product of bf16 pairs, rounded to bf16.
@@ -178,6 +200,12 @@ cudaError_t launch_under(void (*kernel)(Params...), dim3 grid, int threads, size
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
+
+// Checks of a call's sizes, and of its pointers and strides (out's where it has one); its
+// arguments for the kernels, without shared tokens.
+cg_status attn_check_sizes(const cg_int4_cache *c, const cg_attention *a);
+cg_status attn_check_arrays(const cg_attention *a, bool with_out);
+AttnArgs attn_args(const cg_int4_cache *c, int32_t layer, const cg_attention *a);
 
 // SM count of the current device, looked up once per device.
 cudaError_t attn_sm_count(int *sms);

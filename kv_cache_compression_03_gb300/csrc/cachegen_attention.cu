@@ -30,6 +30,12 @@ int64_t max_rows(const cg_int4_cache *c, const cg_attention *a)
     return (int64_t)n * (a->q_heads / c->num_heads);
 }
 
+// And all of a batch's rows of one KV head.
+int64_t all_rows(const cg_int4_cache *c, const cg_attention *a)
+{
+    return (int64_t)a->tokens * (a->q_heads / c->num_heads);
+}
+
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // The workspace's part for the kernel for few rows.
@@ -38,13 +44,24 @@ size_t few_bytes(const cg_int4_cache *c, int64_t rows)
     return align256(attn_few_workspace(c->head_size, (int)(rows < kFewRows ? rows : kFewRows)));
 }
 
-cg_status launch_passes(const cg_int4_cache *c, const AttnArgs &p, uint8_t *workspace, cudaStream_t s)
+size_t pass_bytes(const cg_int4_cache *c, int64_t rows, bool first)
+{
+    if (rows <= kFewRows)
+        return few_bytes(c, rows);
+    // a part each: the two kernels may run side by side
+    return (first ? 0 : few_bytes(c, rows)) + align256(attn_many_workspace(c->head_size, first));
+}
+
+cg_status launch_pass(const cg_int4_cache *c, const AttnArgs &p, uint8_t *workspace, cudaStream_t s)
 {
     const int64_t most = max_rows(c, &p.a);
-    cudaError_t err = attn_few_launch(p, c->head_size, c->group,
-                                      (int)(most < kFewRows ? most : kFewRows), workspace, s);
+    cudaError_t err = cudaSuccess;
+    if (most <= kFewRows || !p.first) {
+        err = attn_few_launch(p, c->head_size, c->group, (int)(most < kFewRows ? most : kFewRows), workspace, s);
+        workspace += few_bytes(c, most);
+    }
     if (err == cudaSuccess && most > kFewRows)
-        err = attn_many_launch(p, c->head_size, c->group, workspace + few_bytes(c, most), s);
+        err = attn_many_launch(p, c->head_size, c->group, workspace, s);
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }
 
@@ -123,11 +140,7 @@ extern "C" cg_status cg_int4_attention_workspace(const cg_int4_cache *c, const c
     const cg_status st = attn_check_sizes(c, a);
     if (st != CG_OK)
         return st;
-    // a part each: the two kernels may run side by side
-    const int64_t rows = max_rows(c, a);
-    *bytes = few_bytes(c, rows);
-    if (rows > kFewRows)
-        *bytes += attn_many_workspace(c->head_size);
+    *bytes = pass_bytes(c, max_rows(c, a), false);
     return CG_OK;
 }
 
@@ -155,7 +168,7 @@ extern "C" cg_status cg_int4_attention(const cg_int4_cache *c, int32_t layer,
         return CG_ERR_CAPACITY;
     const AttnArgs p = attn_args(c, layer, a);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return launch_passes(c, p, static_cast<uint8_t *>(workspace), s);
+    return launch_pass(c, p, static_cast<uint8_t *>(workspace), s);
 }
 
 // Shared tokens: one pass takes them for all rows of the batch, as one request's that all see
@@ -177,15 +190,10 @@ extern "C" cg_status cg_int4_attention_shared_workspace(const cg_int4_cache *c, 
         return CG_ERR_INVALID_ARG;
     if (shared == 0)
         return CG_OK;
-    // that of the other, which runs before it, may take more
-    cg_attention all = *a;
-    all.max_q_len = 0;
-    size_t first = 0;
-    cg_int4_attention_workspace(c, &all, &first);
-    if (first > *bytes)
-        *bytes = first;
+    // and that of the other, whose last kernels may still run when this one's first come up
+    *bytes += pass_bytes(c, all_rows(c, a), true);
     const size_t rows = (size_t)a->tokens * a->q_heads;
-    *bytes = align256(*bytes) + align256(rows * c->head_size * sizeof(float)) + align256(rows * sizeof(float2));
+    *bytes += align256(rows * c->head_size * sizeof(float)) + align256(rows * sizeof(float2));
     return CG_OK;
 }
 
@@ -226,9 +234,14 @@ extern "C" cg_status cg_int4_attention_shared(const cg_int4_cache *c, int32_t la
     first.a.cu_q += a->requests;
     first.a.requests = 1;
     first.a.max_q_len = 0;
+    // however many rows there are, they go to one kernel
+    first.few_rows = all_rows(c, a) <= kFewRows ? kFewRows : 0;
+    // a block begins and ends a unit for as long as it reads some 16 blobs: short ones are not strung
+    // together (4 requests of 7 to 65 tokens, 12 heads: 54 us with, FIG without)
+    p.least_unit = 16;
     p.a.block_table += shared / c->page_tokens;
     p.a.table_width -= shared / c->page_tokens;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    st = launch_passes(c, first, ws, s);
-    return st == CG_OK ? launch_passes(c, p, ws, s) : st;
+    st = launch_pass(c, first, ws, s);
+    return st == CG_OK ? launch_pass(c, p, ws + pass_bytes(c, all_rows(c, a), true), s) : st;
 }

@@ -131,8 +131,10 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
     int64_t total, chunk;
     const Place at = schedule<RU>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
     const int64_t begin = blockIdx.x * chunk;
-    if (begin >= total)
+    if (begin >= total) {
+        grid_wait();
         return;
+    }
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
 
     const int bpp = p.page_tokens / 16;
@@ -437,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 }
             }
         __syncthreads();
+        grid_wait();   // behind the shared tokens: nothing is written, and no row of theirs read, before
         const bool from_before = u.b0 > 0, goes_on = u.b1 < u.span.nb;
         float *part = parts + ((size_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * kPartFloats<D, RU>;
         const int rows_here = last_row - row_base + 1;
@@ -616,8 +619,12 @@ cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
     int blocks = (NT == 1 ? 3 : 2) * sms;
     if (blocks > kFewMaxBlocks)
         blocks = kFewMaxBlocks;
-    k_attention_few<B, NT><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
-    err = cudaGetLastError();
+    if (p.rows != nullptr && !p.first) {   // under the pass over the shared tokens
+        err = launch_under(k_attention_few<B, NT>, dim3(blocks), kThreads, sizeof(Sh), s, p, parts);
+    } else {
+        k_attention_few<B, NT><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
+        err = cudaGetLastError();
+    }
     if (err != cudaSuccess)
         return err;
     // launched while the main kernel still runs: its own schedule is worked out

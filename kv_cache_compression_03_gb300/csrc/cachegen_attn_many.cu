@@ -226,13 +226,15 @@ struct ManyShared {
     uint32_t gave_up;    // a wait ran out: everyone leaves
 };
 
-// Most blocks, hence most items of a batch that is cut.
-constexpr int kMaxBlocks = 160;
+// Most blocks, hence most items of a batch that is cut; and most items of shared tokens, whose units
+// are cut in more pieces than blocks.
+constexpr int kMaxBlocks = 160, kMaxItems = 640;
 
 // Workspace: how the batch was cut, the units, and of each item 256 rows of
 // { float o[D] }, then { float m }, { float l }. Where the softmax groups take
 // turns, rows 128 .. 255 are the second group's results for rows 0 .. 127.
 struct ManyWork {
+    int32_t items;       // that there is room for
     int32_t *cut;        // units, pieces of each
     Unit *heads;
     float *parts;
@@ -329,6 +331,23 @@ __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t item, int s
     }
 }
 
+// Units of shared tokens have n tiles each: as many pieces of each as make the longest block shortest,
+// a piece counting its tiles and what it costs to begin and end it (some 3 of them: 197 units of 256
+// tiles on 152 SMs take two turns whole, and 4/3 in three pieces). Every piece has two tiles at least,
+// so none is empty.
+__device__ __forceinline__ int split_of_equals(int units, int n, int items)
+{
+    const int lane = threadIdx.x & 31, whole = units > 0 ? (int)gridDim.x / units : 0;
+    const int s = lane < 31 ? lane + 1 : max(whole, 1);
+    const int64_t turns = ((int64_t)units * s + gridDim.x - 1) / gridDim.x;
+    const int64_t cost = turns * ((n + s - 1) / s + 3);
+    const bool can = s == 1 || (s <= n / 2 && (int64_t)units * s <= items);
+    // the least cost, and of equal ones the least s
+    const uint32_t least = __reduce_min_sync(0xFFFFFFFFu, can ? (uint32_t)min(cost, (int64_t)0x7FFFFFFF) : 0xFFFFFFFFu);
+    const bool mine = can && (uint32_t)min(cost, (int64_t)0x7FFFFFFF) == least;
+    return (int)__reduce_min_sync(0xFFFFFFFFu, mine ? (uint32_t)s : 0xFFFFFFFFu);
+}
+
 // -------------------------------------------------------------------- kernel
 
 template <typename B>
@@ -395,7 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
     tmem_fence_after();
     if (sm.tmem != 0 && tid == 0)   // never: the block took all of it
         int4_set_status(p.status, CG_ERR_CUDA);
-    const int split = sm.units > 0 && sm.units < gridDim.x ? gridDim.x / sm.units : 1;
+    const int split = p.first ? split_of_equals(sm.units, ((p.shared + 15) / 16 + kBlobs - 1) / kBlobs, work.items)
+                      : sm.units > 0 && sm.units < gridDim.x ? gridDim.x / sm.units : 1;
     if (blockIdx.x == 0 && tid == 0) {
         work.cut[0] = sm.units;
         work.cut[1] = split;
@@ -567,6 +587,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                 if (!alive)
                     break;
                 float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if (p.rows != nullptr && !p.first)   // for the rows of the shared tokens
+                    grid_wait();
                 const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
                 float *shared_row = nullptr, shared_f = 0.0f;
                 if (p.rows != nullptr && u.parts == 1 && rr < u.rows) {
@@ -997,6 +1019,7 @@ template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p, ManyWork work)
 {
     constexpr int kC = D / 32;   // channels of a lane
+    grid_next();   // the pass behind the shared tokens may come up
     grid_wait();
     if (work.cut[1] == 1)
         return;
@@ -1075,7 +1098,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
     }
 }
 
-constexpr size_t kHeadBytes = 256 + (sizeof(Unit) * kMaxBlocks + 255) / 256 * 256;
+constexpr size_t head_bytes(int items) { return 256 + (sizeof(Unit) * items + 255) / 256 * 256; }
+
+constexpr int most_items(bool first) { return first ? kMaxItems : kMaxBlocks; }
 
 template <typename B>
 cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
@@ -1087,10 +1112,15 @@ cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
         err = cudaFuncSetAttribute(k_attention_many<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess)
         return err;
-    const ManyWork work = {reinterpret_cast<int32_t *>(ws), reinterpret_cast<Unit *>(ws + 256),
-                           reinterpret_cast<float *>(ws + kHeadBytes)};
-    // under the kernels for few rows: it works on other rows, with a workspace of its own
-    err = launch_under(k_attention_many<B>, dim3(sms < kMaxBlocks ? sms : kMaxBlocks), kThreads, smem, s, p, work);
+    const int items = most_items(p.first), blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
+    const ManyWork work = {items, reinterpret_cast<int32_t *>(ws), reinterpret_cast<Unit *>(ws + 256),
+                           reinterpret_cast<float *>(ws + head_bytes(items))};
+    if (p.first) {   // the call's first kernel: it follows what is in the stream
+        k_attention_many<B><<<blocks, kThreads, smem, s>>>(p, work);
+        err = cudaGetLastError();
+    } else {   // under the kernels for few rows: it works on other rows, with a workspace of its own
+        err = launch_under(k_attention_many<B>, dim3(blocks), kThreads, smem, s, p, work);
+    }
     if (err == cudaSuccess)
         err = launch_under(k_attention_many_join<B::kD>, dim3(kJoinBlocks), kJoinThreads, 0, s, p, work);
     return err;
@@ -1098,9 +1128,10 @@ cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
 
 }  // namespace
 
-size_t attn_many_workspace(int head_size)
+size_t attn_many_workspace(int head_size, bool first)
 {
-    return kHeadBytes + kMaxBlocks * (size_t)kRows * (head_size + 2) * sizeof(float);
+    const int items = most_items(first);
+    return head_bytes(items) + items * (size_t)kRows * (head_size + 2) * sizeof(float);
 }
 
 cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, void *ws, cudaStream_t s)

@@ -5,7 +5,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "cg_int4.h"
+#include "cg_attention.h"
 
 namespace {
 
@@ -20,9 +20,192 @@ __device__ __forceinline__ uint32_t key_of(float w)
     return isnan(w) ? 0u : bits & 0x80000000u ? ~bits : bits | 0x80000000u;
 }
 
-// A block to a row: the threshold is found eight bits at a time, then the tokens above it, and
-// of those at it the lowest, are written in order.
-__global__ void __launch_bounds__(kChooseThreads) k_choose_tokens(cg_token_choice c)
+// ---- a row in the registers of a cluster
+
+constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
+constexpr int kDigits = 2048;                 // 11, 11 and 10 bits of a key
+constexpr int kMostCluster = 8;
+
+struct ChooseShared {
+    int32_t count[3][kDigits];
+    int32_t coarse[3][kDigits / 32];          // sums of 32
+    int32_t found[2];
+    int32_t over[kRowWarps], at[kRowWarps];   // of each warp
+    int32_t all[2];                           // of the block
+};
+
+__device__ __forceinline__ void cluster_sync(int size)
+{
+    if (size == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The value at `p`, a place in this block's shared memory, in that of the cluster's block `rank`.
+__device__ __forceinline__ int32_t cluster_load(const int32_t *p, int rank)
+{
+    uint32_t at;
+    int32_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at)
+                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// A cluster of `size` blocks to a row, each with an equal part of the tokens that are chosen among, and of
+// that each warp, up to E tokens a lane: the weights are read once. The threshold's key is found in three
+// digits, counted in shared memory: the first has sign, exponent and two bits, so that weights of a few
+// octaves fall into many places. Then every warp knows how many stay before its own.
+template <int E>
+__global__ void __launch_bounds__(kRowThreads, E > 4 ? 2 : 3) k_choose_tokens(cg_token_choice c, int size)
+{
+    __shared__ ChooseShared sm;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x / size;
+    const int rank = blockIdx.x % size;
+    const int h = (int)(row % c.heads), r = (int)(row / c.heads % c.requests);
+    const int64_t l = row / c.heads / c.requests;
+    const int32_t m = c.lens[r];
+    int32_t *kept = c.kept + row * c.budget;
+    const bool bad = m < 0 || m > c.width;
+    if (bad || m <= c.budget) {   // the whole cluster
+        for (int i = rank * kRowThreads + tid; i < c.budget; i += size * kRowThreads)
+            kept[i] = !bad && i < m ? i : -1;
+        return;
+    }
+    const float *w = c.weights + l * c.layer_stride + r * c.request_stride + h * c.head_stride;
+    // the choice is among [sinks, end), of which `pick` stay
+    const int32_t end = m - c.recent, pick = c.budget - c.sinks - c.recent, n = end - c.sinks;
+    const int32_t per_lane = (n + size * kRowThreads - 1) / (size * kRowThreads);   // at most E
+    const int32_t first = c.sinks + (rank * kRowWarps + warp) * per_lane * 32 + lane;
+    const int32_t mine = first < end ? min(per_lane, (end - first + 31) / 32) : 0;   // tokens of the lane
+    uint32_t key[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        key[e] = e < mine ? __float_as_uint(__ldg(w + first + 32 * e)) : 0u;
+    for (int i = tid; i < 3 * kDigits; i += kRowThreads)
+        sm.count[0][i] = 0;
+    for (int i = rank * kRowThreads + tid; i < c.sinks; i += size * kRowThreads)
+        kept[i] = i;
+    for (int i = rank * kRowThreads + tid; i < c.recent; i += size * kRowThreads)
+        kept[c.budget - c.recent + i] = end + i;
+    if (pick == 0)
+        return;
+    __syncthreads();
+    uint32_t prefix = 0;      // of the threshold's key
+    int32_t left = pick;      // to be taken from the tokens that begin with it
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
+        const uint32_t digits = d == 2 ? 1023u : 2047u;
+        int32_t *count = sm.count[d];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (d == 0)
+                key[e] = key_of(__uint_as_float(key[e]));
+            if (e < mine && (d == 0 || key[e] >> (d == 1 ? 21 : 10) == prefix))
+                atomicAdd(&count[key[e] >> shift & digits], 1);
+        }
+        __syncthreads();
+        for (int k = warp; k < kDigits / 32; k += kRowWarps) {
+            const int32_t sum = __reduce_add_sync(0xFFFFFFFFu, count[32 * k + lane]);
+            if (lane == 0)
+                sm.coarse[d][k] = sum;
+        }
+        cluster_sync(size);
+        // one warp finds the 32 digits of the threshold among the sums of all blocks, then the digit (a
+        // load from another block's memory goes lane by lane: all digits of all blocks were 180 us of 190
+        // for 256 rows of 65536)
+        if (warp == 0) {
+            int32_t above = 0, group = 0;   // tokens above the digit; where it is
+#pragma unroll
+            for (int step = 0; step < 3; ++step) {   // upper and lower half of the sums, then digits
+                const int32_t *from = step < 2 ? &sm.coarse[d][kDigits / 32 - 1 - 32 * step - lane]
+                                               : &count[32 * group + 31 - lane];
+                int32_t own = 0;
+                for (int k = 0; k < size; ++k)
+                    own += size == 1 ? *from : cluster_load(from, k);
+                int32_t inc = own;
+#pragma unroll
+                for (int s = 1; s < 32; s <<= 1) {
+                    const int32_t o = __shfl_up_sync(0xFFFFFFFFu, inc, s);
+                    if (lane >= s)
+                        inc += o;
+                }
+                const uint32_t reached = __ballot_sync(0xFFFFFFFFu, above + inc >= left);
+                const int at = reached ? __ffs(reached) - 1 : 32;
+                const int32_t before = __shfl_sync(0xFFFFFFFFu, at < 32 ? inc - own : inc, at < 32 ? at : 31);
+                if (step == 2) {
+                    if (lane == 0) {
+                        sm.found[0] = 32 * group + 31 - at;
+                        sm.found[1] = left - above - before;
+                    }
+                } else if (step == 0 || group < 0) {
+                    above += before;
+                    group = at < 32 ? kDigits / 32 - 1 - 32 * step - at : -1;
+                }
+            }
+        }
+        __syncthreads();
+        prefix = (d == 0 ? 0 : prefix << (d == 1 ? 11 : 10)) | (uint32_t)sm.found[0];
+        left = sm.found[1];
+    }
+    // ---- how many stay before each warp's
+    int32_t over = 0, at = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        over += e < mine && key[e] > prefix;
+        at += e < mine && key[e] == prefix;
+    }
+    over = __reduce_add_sync(0xFFFFFFFFu, over);
+    at = __reduce_add_sync(0xFFFFFFFFu, at);
+    if (lane == 0) {
+        sm.over[warp] = over;
+        sm.at[warp] = at;
+    }
+    __syncthreads();
+    if (tid < 2) {
+        const int32_t *from = tid ? sm.at : sm.over;
+        int32_t sum = 0;
+        for (int k = 0; k < kRowWarps; ++k)
+            sum += from[k];
+        sm.all[tid] = sum;
+    }
+    cluster_sync(size);
+    int32_t pos = c.sinks, taken = 0;
+    for (int k = 0; k < rank; ++k) {
+        pos += cluster_load(&sm.all[0], k);
+        taken += cluster_load(&sm.all[1], k);
+    }
+    for (int k = 0; k < warp; ++k) {
+        pos += sm.over[k];
+        taken += sm.at[k];
+    }
+    if (size > 1)   // no block's shared memory goes while another one reads it
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    pos += min(taken, left);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (e < per_lane) {
+            const bool there = e < mine;
+            const uint32_t eq = __ballot_sync(0xFFFFFFFFu, there && key[e] == prefix);
+            const int rank_eq = taken + __popc(eq & ((1u << lane) - 1));
+            const bool stays = there && (key[e] > prefix || (key[e] == prefix && rank_eq < left));
+            const uint32_t all = __ballot_sync(0xFFFFFFFFu, stays);
+            if (stays)
+                kept[pos + __popc(all & ((1u << lane) - 1))] = first + 32 * e;
+            pos += __popc(all);
+            taken += __popc(eq);
+        }
+    }
+    if (size > 1)
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Rows too long for the registers of a cluster: a block to a row, which it reads from memory each time.
+__global__ void __launch_bounds__(kChooseThreads) k_choose_long(cg_token_choice c)
 {
     __shared__ int32_t count[256];
     __shared__ int32_t sums[2][kChooseWarps];
@@ -35,8 +218,6 @@ __global__ void __launch_bounds__(kChooseThreads) k_choose_tokens(cg_token_choic
     int32_t *kept = c.kept + row * c.budget;
     const bool bad = m < 0 || m > c.width;
     if (bad || m <= c.budget) {
-        if (bad && tid == 0)
-            int4_set_status(c.status, CG_ERR_CORRUPT);
         for (int i = tid; i < c.budget; i += kChooseThreads)
             kept[i] = !bad && i < m ? i : -1;
         return;
@@ -126,19 +307,44 @@ __global__ void __launch_bounds__(kChooseThreads) k_choose_tokens(cg_token_choic
         kept[c.budget - c.recent + i] = end + i;
 }
 
-__global__ void __launch_bounds__(256) k_choose_lens(cg_token_choice c)
+// The lengths, once every row's kernel has read the old ones (they may be overwritten), and the status.
+constexpr int kLensThreads = 1024;
+
+__global__ void __launch_bounds__(kLensThreads) k_choose_lens(cg_token_choice c)
 {
-    const int r = blockIdx.x * 256 + threadIdx.x;
-    if (r < c.requests) {
+    bool bad = false;
+    grid_wait();
+    for (int r = threadIdx.x; r < c.requests; r += kLensThreads) {
         const int32_t m = c.lens[r];
+        bad |= m < 0 || m > c.width;
         c.lens_out[r] = m <= c.width && m > c.budget ? c.budget : m;
     }
+    bad = __syncthreads_or(bad);
+    if (threadIdx.x == 0)
+        *static_cast<uint4 *>(c.status) = make_uint4(bad ? CG_ERR_CORRUPT : CG_OK, 0, 0, 0);
+}
+
+template <int E>
+cudaError_t launch_choice(const cg_token_choice &c, int64_t rows, int size, cudaStream_t s)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * size));
+    cfg.blockDim = dim3(kRowThreads);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_choose_tokens<E>, c, size);
 }
 
 // ------------------------------------------------------------------ the move
 
 constexpr int kMoveThreads = 256;
-constexpr int kWave = 64;   // tokens moved at a time
+constexpr int kWave = 128;    // tokens moved at a time
+constexpr int kStages = 3;    // waves read ahead
 
 struct MoveArgs {
     uint8_t *data;        // the first layer
@@ -148,21 +354,42 @@ struct MoveArgs {
     cg_compaction c;
 };
 
-// A block to a (layer, request, head). Tokens move to lower places, in ascending order: a wave of
-// places is read whole, then written, and what later waves read lies behind it.
+// A wave's tokens in shared memory: of V the whole pair of which a token is half.
 template <typename B>
-__global__ void __launch_bounds__(kMoveThreads) k_int4_compact(MoveArgs a)
+struct alignas(16) MoveStage {
+    uint8_t k[kWave][B::kD / 2];
+    uint8_t v[kWave][B::kD];
+    uint8_t par[2][kWave][4 * B::kGroups];
+    const uint8_t *src[kWave];     // the blob that holds the token (nullptr: none)
+    uint8_t *dst[kWave / 16];
+    float weight[kWave];
+    uint8_t tok[kWave];            // in its blob
+};
+
+template <int N>
+__device__ __forceinline__ void copy_async(void *to, const void *from)
+{
+    const uint32_t at = (uint32_t)__cvta_generic_to_shared(to);
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(at), "l"(from), "n"(N) : "memory");
+}
+
+// A cluster to a (layer, request, head); its blocks take waves of places in turns. Tokens move to lower
+// places in ascending order, so the tokens of a wave lie at its own places or behind: a wave is written
+// once it and all before it have been read (a cluster barrier), and the next ones may be read long before.
+template <typename B>
+__global__ void __launch_bounds__(kMoveThreads, 2) k_int4_compact(MoveArgs a, int size)
 {
     constexpr int D = B::kD, NG = B::kGroups;
-    constexpr int kKUnits = D / 2, kUnits = 2 * kKUnits + 32;   // of a blob: K, V codes, parameters
-    constexpr int kMost = (kUnits * (kWave / 16) + kMoveThreads - 1) / kMoveThreads;
-    __shared__ const uint8_t *src[kWave];   // the blob of head h that holds the token
-    __shared__ uint8_t src_tok[kWave];
-    __shared__ uint8_t *dst[kWave / 16];
+    using Stage = MoveStage<B>;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    Stage *stages = reinterpret_cast<Stage *>(smem_raw);
     __shared__ int32_t first_moved;
     const cg_compaction &c = a.c;
-    const int tid = threadIdx.x;
-    const int64_t row = blockIdx.x;
+    const int tid = threadIdx.x, rank = blockIdx.x % size;
+    const int64_t row = blockIdx.x / size;
     const int h = (int)(row % a.heads), r = (int)(row / a.heads % c.requests);
     const int64_t l = row / a.heads / c.requests;
     const int32_t n = c.new_lens[r], m = c.lens[r];
@@ -174,16 +401,22 @@ __global__ void __launch_bounds__(kMoveThreads) k_int4_compact(MoveArgs a)
     if (tid == 0)
         first_moved = n;
     __syncthreads();
+    // every block looks at the whole list
     bool bad = !fits;
+    int32_t moved = n;
     if (fits)
+#pragma unroll 4
         for (int i = tid; i < n; i += kMoveThreads) {
             const int32_t j = kept[i], before = i ? kept[i - 1] : -1;
-            bad |= j <= before || j < 0 || j >= m;
+            bad |= j <= before || j >= m;
             if (j != i)
-                atomicMin(&first_moved, i);
+                moved = min(moved, i);
         }
-    if (__syncthreads_or(bad)) {
-        if (tid == 0)
+    moved = __reduce_min_sync(0xFFFFFFFFu, moved);
+    if ((tid & 31) == 0 && moved < n)
+        atomicMin(&first_moved, moved);
+    if (__syncthreads_or(bad)) {   // in every block of the cluster
+        if (tid == 0 && rank == 0)
             int4_set_status(a.status, CG_ERR_CORRUPT);
         return;
     }
@@ -201,92 +434,128 @@ __global__ void __launch_bounds__(kMoveThreads) k_int4_compact(MoveArgs a)
         return a.data + l * a.layer_bytes +
                (((size_t)id * a.heads + h) * bpp + (token - page * a.page_tokens) / 16) * B::kBytes;
     };
-    for (int32_t p0 = first_moved & ~15; p0 < n; p0 += kWave) {
-        float weight = 0.0f;
-        if (tid < kWave) {
-            const int32_t p = p0 + tid, j = p < n ? kept[p] : p;
+    const int32_t start = first_moved < n ? first_moved & ~15 : n;   // blobs before it stay as they are
+    const int waves = (int)(((int64_t)n - start + kWave - 1) / kWave);
+    // where the tokens of this block's wave i lie; then their bytes
+    auto read = [&](int i) {
+        const int64_t p0 = start + ((int64_t)i * size + rank) * kWave;
+        Stage &st = stages[i % kStages];
+        if (p0 < n && tid < kWave) {
+            const int32_t p = (int32_t)min(p0 + tid, (int64_t)INT32_MAX), j = p < n ? kept[p] : p;
             // a place behind the last shares its pair's bytes, and one whose token cannot be read keeps
             // its own: both are read where they are written
             const uint8_t *from = p < n ? blob_of(j) : nullptr;
             uint8_t *to = p <= n ? blob_of(p) : nullptr;
-            src[tid] = from != nullptr ? from : to;
-            src_tok[tid] = from != nullptr ? j & 15 : p & 15;
+            st.src[tid] = from != nullptr ? from : to;
+            st.tok[tid] = from != nullptr ? j & 15 : p & 15;
             if (tid % 16 == 0)
-                dst[tid / 16] = to;
+                st.dst[tid / 16] = to;
             if (w != nullptr && p < n)
-                weight = w[j];
+                st.weight[tid] = w[j];
         }
         __syncthreads();
-        uint4 x[kMost];
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-            const int u = tid + k * kMoveThreads, blob = u / kUnits, v = u - blob * kUnits;
-            x[k] = make_uint4(0, 0, 0, 0);
-            if (blob >= kWave / 16)
-                continue;
-            if (v < kKUnits) {
-                const int t = 16 * blob + v / (D / 32);
-                if (src[t] != nullptr)
-                    x[k] = *reinterpret_cast<const uint4 *>(src[t] + B::kKCodes + src_tok[t] * (D / 2) +
-                                                            v % (D / 32) * 16);
-            } else if (v < 2 * kKUnits) {
-                const int t = 16 * blob + (v - kKUnits) / (D / 16) * 2, part = (v - kKUnits) % (D / 16) * 16;
-                uint4 y[2];
-#pragma unroll
-                for (int b = 0; b < 2; ++b)
-                    y[b] = src[t + b] != nullptr ? *reinterpret_cast<const uint4 *>(src[t + b] + B::kVCodes +
-                                                                                    (src_tok[t + b] >> 1) * D + part)
-                                                 : make_uint4(0, 0, 0, 0);
-                const uint32_t sel = (src_tok[t] & 1 ? 0x0032u : 0x0010u) | (src_tok[t + 1] & 1 ? 0x7600u : 0x5400u);
-                x[k] = make_uint4(__byte_perm(y[0].x, y[1].x, sel), __byte_perm(y[0].y, y[1].y, sel),
-                                  __byte_perm(y[0].z, y[1].z, sel), __byte_perm(y[0].w, y[1].w, sel));
-            } else {
-                const int t = 16 * blob + (v & 15), is_v = (v - 2 * kKUnits) >> 4;
-                if (src[t] != nullptr) {
+        if (p0 < n) {
+            constexpr int kKParts = D / 32, kVParts = D / 16;
+#pragma unroll 4
+            for (int u = tid; u < kWave * kKParts; u += kMoveThreads) {
+                const int t = u / kKParts, part = u % kKParts * 16;
+                if (st.src[t] != nullptr)
+                    copy_async<16>(&st.k[t][part], st.src[t] + B::kKCodes + st.tok[t] * (D / 2) + part);
+            }
+#pragma unroll 4
+            for (int u = tid; u < kWave * kVParts; u += kMoveThreads) {
+                const int t = u / kVParts, part = u % kVParts * 16;
+                if (st.src[t] != nullptr)
+                    copy_async<16>(&st.v[t][part], st.src[t] + B::kVCodes + (st.tok[t] >> 1) * D + part);
+            }
+            for (int u = tid; u < 2 * kWave; u += kMoveThreads) {
+                const int t = u % kWave, v = u / kWave;
+                if (st.src[t] != nullptr)
+                    copy_async<4 * NG>(&st.par[v][t], st.src[t] + (v ? B::kVParams : B::kKParams) + st.tok[t] * 4 * NG);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const int rounds = (waves + size - 1) / size;
+    for (int i = 0; i < kStages; ++i)
+        read(i);
+    for (int i = 0; i < rounds; ++i) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        cluster_sync(size);   // this round's waves have been read, by all threads of all blocks
+        const int64_t p0 = start + ((int64_t)i * size + rank) * kWave;
+        const Stage &st = stages[i % kStages];
+        if (p0 < n) {
+            const int there = (int)min((int64_t)kWave, n - p0);   // places of the wave
+            constexpr int kUnits = D / 2;                         // 16 bytes each, of a blob's K or V codes
+#pragma unroll 4
+            for (int u = tid; u < kWave / 16 * kUnits; u += kMoveThreads) {
+                const int blob = u / kUnits, in = u % kUnits, t = 16 * blob + in / (D / 32);
+                if (t < there && st.dst[blob] != nullptr)
+                    *reinterpret_cast<uint4 *>(st.dst[blob] + B::kKCodes + in * 16) =
+                        *reinterpret_cast<const uint4 *>(&st.k[t][in % (D / 32) * 16]);
+            }
+#pragma unroll 4
+            for (int u = tid; u < kWave / 16 * kUnits; u += kMoveThreads) {
+                const int blob = u / kUnits, in = u % kUnits, t = 16 * blob + in / (D / 16) * 2, part = in % (D / 16) * 16;
+                if (t < there && st.dst[blob] != nullptr) {
+                    // halves of two tokens' words
+                    const uint4 x = *reinterpret_cast<const uint4 *>(&st.v[t][part]);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(&st.v[t + 1][part]);
+                    const uint32_t sel = (st.tok[t] & 1 ? 0x0032u : 0x0010u) | (st.tok[t + 1] & 1 ? 0x7600u : 0x5400u);
+                    *reinterpret_cast<uint4 *>(st.dst[blob] + B::kVCodes + in * 16) =
+                        make_uint4(__byte_perm(x.x, y.x, sel), __byte_perm(x.y, y.y, sel), __byte_perm(x.z, y.z, sel),
+                                   __byte_perm(x.w, y.w, sel));
+                }
+            }
+            for (int u = tid; u < 2 * kWave; u += kMoveThreads) {
+                const int t = u % kWave, v = u / kWave;
+                if (t < there && st.dst[t / 16] != nullptr) {
                     uint32_t par[NG];
-                    load_words(par, src[t] + (is_v ? B::kVParams : B::kKParams) + src_tok[t] * 4 * NG);
-                    x[k].x = par[0];
-                    x[k].y = par[NG > 1 ? 1 : 0];
-                    x[k].z = par[NG > 2 ? 2 : 0];
-                    x[k].w = par[NG > 2 ? 3 : 0];
-                }
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int k = 0; k < kMost; ++k) {
-            const int u = tid + k * kMoveThreads, blob = u / kUnits, v = u - blob * kUnits;
-            if (blob >= kWave / 16 || dst[blob] == nullptr)
-                continue;
-            uint8_t *to = dst[blob];
-            if (v < kKUnits) {
-                const int in = v / (D / 32), t = 16 * blob + in;
-                if (p0 + t < n && src[t] != nullptr)
-                    *reinterpret_cast<uint4 *>(to + B::kKCodes + in * (D / 2) + v % (D / 32) * 16) = x[k];
-            } else if (v < 2 * kKUnits) {
-                const int pair = (v - kKUnits) / (D / 16), t = 16 * blob + 2 * pair;
-                if (p0 + t < n && src[t] != nullptr && src[t + 1] != nullptr)
-                    *reinterpret_cast<uint4 *>(to + B::kVCodes + pair * D + (v - kKUnits) % (D / 16) * 16) = x[k];
-            } else {
-                const int in = v & 15, t = 16 * blob + in, is_v = (v - 2 * kKUnits) >> 4;
-                if (p0 + t < n && src[t] != nullptr) {
-                    uint8_t *par = to + (is_v ? B::kVParams : B::kKParams) + in * 4 * NG;
+                    load_words(par, st.par[v][t]);
+                    uint8_t *to = st.dst[t / 16] + (v ? B::kVParams : B::kKParams) + t % 16 * 4 * NG;
                     if constexpr (NG == 4)
-                        *reinterpret_cast<uint4 *>(par) = x[k];
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(par[0], par[1], par[2], par[3]);
                     else if constexpr (NG == 2)
-                        *reinterpret_cast<uint2 *>(par) = make_uint2(x[k].x, x[k].y);
+                        *reinterpret_cast<uint2 *>(to) = make_uint2(par[0], par[1]);
                     else
-                        *reinterpret_cast<uint32_t *>(par) = x[k].x;
+                        *reinterpret_cast<uint32_t *>(to) = par[0];
                 }
             }
+            if (w != nullptr && tid < there)
+                w[p0 + tid] = st.weight[tid];
         }
-        if (w != nullptr && tid < kWave && p0 + tid < n)
-            w[p0 + tid] = weight;
-        __syncthreads();
+        __syncthreads();   // the stage is free
+        read(i + kStages);
     }
-    if (w != nullptr)
-        for (int32_t i = n + tid; i < m; i += kMoveThreads)
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (w != nullptr)   // read by no wave any more
+        for (int64_t i = n + rank * kMoveThreads + tid; i < m; i += size * kMoveThreads)
             w[i] = 0.0f;
+}
+
+template <typename B>
+cudaError_t launch_move(const MoveArgs &a, int64_t lists, cudaStream_t s)
+{
+    const size_t smem = kStages * sizeof(MoveStage<B>);
+    const cudaError_t err = cudaFuncSetAttribute(k_int4_compact<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess)
+        return err;
+    // two blocks to an SM; few lists are shared by several
+    int size = 1;
+    while (size < kMostCluster && lists * size < 200)
+        size *= 2;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = size;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(lists * size));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_int4_compact<B>, a, size);
 }
 
 }  // namespace
@@ -307,13 +576,30 @@ extern "C" cg_status cg_choose_tokens(const cg_token_choice *c, cg_stream_t stre
         !int4_aligned(c->lens_out, 4))
         return CG_ERR_INVALID_ARG;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(c->status, 0, 16, s) != cudaSuccess)
-        return CG_ERR_CUDA;
-    if (lists * c->heads > 0)
-        k_choose_tokens<<<(unsigned)(lists * c->heads), kChooseThreads, 0, s>>>(*c);
-    if (c->requests > 0)
-        k_choose_lens<<<(c->requests + 255) / 256, 256, 0, s>>>(*c);
-    return cudaGetLastError() == cudaSuccess ? CG_OK : CG_ERR_CUDA;
+    const int64_t rows = lists * c->heads;
+    cudaError_t err = cudaSuccess;
+    if (rows > 0) {
+        // blocks to a row: as many as hold it, and more while there are SMs for them
+        int size = 1;
+        while (size < kMostCluster && c->width > 32 * kRowThreads * size)
+            size *= 2;
+        while (size < kMostCluster && rows * size < 152 && c->width > 8 * kRowThreads * size)
+            size *= 2;
+        const int64_t each = ((int64_t)c->width + size * kRowThreads - 1) / (size * kRowThreads);
+        if (rows * size >= limit || each > 32)
+            k_choose_long<<<(unsigned)rows, kChooseThreads, 0, s>>>(*c);
+        else
+            err = each <= 4    ? launch_choice<4>(*c, rows, size, s)
+                  : each <= 8  ? launch_choice<8>(*c, rows, size, s)
+                  : each <= 12 ? launch_choice<12>(*c, rows, size, s)
+                  : each <= 20 ? launch_choice<20>(*c, rows, size, s)
+                               : launch_choice<32>(*c, rows, size, s);
+    }
+    if (err == cudaSuccess)
+        err = cudaGetLastError();
+    if (err == cudaSuccess)
+        err = launch_under(k_choose_lens, dim3(1), kLensThreads, 0, s, *c);
+    return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }
 
 extern "C" cg_status cg_int4_compact(const cg_int4_cache *cache, int32_t first_layer, const cg_compaction *c,
@@ -349,8 +635,7 @@ extern "C" cg_status cg_int4_compact(const cg_int4_cache *cache, int32_t first_l
     a.c = *c;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t err = int4_dispatch(cache->head_size, cache->group, [&](auto blob) {
-        k_int4_compact<decltype(blob)><<<(unsigned)(lists * cache->num_heads), kMoveThreads, 0, s>>>(a);
-        return cudaGetLastError();
+        return launch_move<decltype(blob)>(a, lists * cache->num_heads, s);
     });
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

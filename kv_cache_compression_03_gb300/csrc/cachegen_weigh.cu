@@ -205,7 +205,7 @@ __device__ __forceinline__ Tile tile_of(const AttnArgs &p, const Unit &u)
     t.x_lo = u.q.x0 + t.row0 / p.ratio;
     t.x_hi = u.q.x0 + (t.row0 + t.rows - 1) / p.ratio;
     const int32_t end = t.x_hi < 0 ? 0 : t.x_hi / 16 + 1;
-    t.span = {end, 0, 0};
+    t.span = {end, 0, 0, end};
     const int64_t low = (int64_t)t.x_lo + 1 - p.a.window;
     if (p.a.window > 0 && low > 0) {
         const int32_t first = (int32_t)(low / 16);

@@ -11,6 +11,7 @@ struct AttnArgs {
                             // kernel for few rows
     float scale2;           // scale * log2(e)
     int64_t kv_limit;       // most tokens of a request
+    int32_t least_unit;     // few rows: blobs that a request and head count as at least (0: as they are)
     // Where all requests begin with the same `shared` tokens, one pass takes those, all rows
     // of the batch as one request's, and leaves its results in rows; the other takes the
     // tokens behind them (the table and the lengths begin there) and joins the two.
@@ -217,5 +218,5 @@ constexpr int kFewMaxBlocks = 480;
 size_t attn_few_workspace(int head_size, int max_rows);
 cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max_rows, void *ws,
                             cudaStream_t s);
-size_t attn_many_workspace(int head_size);
+size_t attn_many_workspace(int head_size, bool first);
 cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, void *ws, cudaStream_t s);

@@ -16,15 +16,17 @@ constexpr float kNone = -3.0e38f;   // no maximum yet; finite, so that differenc
 // ---------------------------------------------------------------- schedule
 
 // The blobs that a request's rows can see: [0, sink) and [sink + skip, ..),
-// nb of them (at least 1, so that every row gets its output).
+// nb of them (at least 1, so that every row gets its output). A unit counts as nb blobs of the line;
+// where it has to count as more than it has (p.least_unit), `real` of them are there and pieces of the
+// unit take as large a part of those.
 struct Span {
-    int32_t nb, sink, skip;
+    int32_t nb, sink, skip, real;
 };
 
 __device__ __forceinline__ Span span_of(const AttnArgs &p, const AttnRequest &q)
 {
     const int32_t end = (q.kv + 15) / 16;
-    Span s = {end, 0, 0};
+    Span s = {end, 0, 0, end};
     if (p.a.window > 0) {
         const int64_t low = (int64_t)q.x0 + 1 - p.a.window;   // the first row's
         if (low > 0) {
@@ -37,6 +39,9 @@ __device__ __forceinline__ Span span_of(const AttnArgs &p, const AttnRequest &q)
     }
     if (s.nb < 1)
         s.nb = 1;
+    s.real = s.nb;
+    if (s.nb < p.least_unit)
+        s.nb = p.least_unit;
     return s;
 }
 
@@ -201,9 +206,14 @@ __device__ __forceinline__ void unit_next(const AttnArgs &p, int64_t left, Unit 
 // A warp's stretch of a unit's blobs in this piece.
 __device__ __forceinline__ void warp_range(const Unit &u, int warp, int *b, int *e)
 {
-    const int n = u.b1 - u.b0;
-    *b = u.b0 + (int)((int64_t)n * warp / kWarps);
-    *e = u.b0 + (int)((int64_t)n * (warp + 1) / kWarps);
+    int b0 = u.b0, b1 = u.b1;
+    if (u.span.real != u.span.nb) {
+        b0 = (int)((int64_t)b0 * u.span.real / u.span.nb);
+        b1 = (int)((int64_t)b1 * u.span.real / u.span.nb);
+    }
+    const int n = b1 - b0;
+    *b = b0 + (int)((int64_t)n * warp / kWarps);
+    *e = b0 + (int)((int64_t)n * (warp + 1) / kWarps);
 }
 
 // ------------------------------------------------------------ instructions

@@ -13,24 +13,24 @@ namespace {
 
 constexpr int kChooseThreads = 1024, kChooseWarps = kChooseThreads / 32;
 
-// Ascending as the weights are: NaN first, -0 and +0 alike.
+// Ascending as the weights are, above 0: NaN first, -0 and +0 alike.
 __device__ __forceinline__ uint32_t key_of(float w)
 {
     const uint32_t bits = __float_as_uint(w + 0.0f);
-    return isnan(w) ? 0u : bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+    return w != w ? 1u : bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
 }
 
 // ---- a row in the registers of a cluster
 
-constexpr int kRowThreads = 512, kRowWarps = kRowThreads / 32;
 constexpr int kDigits = 2048;                 // 11, 11 and 10 bits of a key
 constexpr int kMostCluster = 8;
 
+template <int T>
 struct ChooseShared {
     int32_t count[3][kDigits];
     int32_t coarse[3][kDigits / 32];          // sums of 32
     int32_t found[2];
-    int32_t over[kRowWarps], at[kRowWarps];   // of each warp
+    int32_t over[T / 32], at[T / 32];         // of each warp
     int32_t all[2];                           // of the block
 };
 
@@ -54,14 +54,87 @@ __device__ __forceinline__ int32_t cluster_load(const int32_t *p, int rank)
     return v;
 }
 
-// A cluster of `size` blocks to a row, each with an equal part of the tokens that are chosen among, and of
-// that each warp, up to E tokens a lane: the weights are read once. The threshold's key is found in three
-// digits, counted in shared memory: the first has sign, exponent and two bits, so that weights of a few
-// octaves fall into many places. Then every warp knows how many stay before its own.
-template <int E>
-__global__ void __launch_bounds__(kRowThreads, E > 4 ? 2 : 3) k_choose_tokens(cg_token_choice c, int size)
+// One more at a place in shared memory, without a branch.
+__device__ __forceinline__ void count_if(bool yes, int32_t *at)
 {
-    __shared__ ChooseShared sm;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %0, 0;\n\t@p red.shared.add.u32 [%1], 1;\n\t}" ::"r"((uint32_t)yes),
+                 "r"((uint32_t)__cvta_generic_to_shared(at))
+                 : "memory");
+}
+
+// Bit j of lane i to bit i of lane j.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t m = 0x0000FFFFu;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1, m ^= m << s) {
+        const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, x, s);
+        x = lane & s ? (x & ~m) | ((y >> s) & m) : (x & m) | ((y & m) << s);
+    }
+    return x;
+}
+
+__device__ __forceinline__ int32_t warp_before(int32_t v, int lane)   // exclusive sum
+{
+    int32_t inc = v;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const int32_t o = __shfl_up_sync(0xFFFFFFFFu, inc, s);
+        if (lane >= s)
+            inc += o;
+    }
+    return inc - v;
+}
+
+// The digit of d's count that the threshold has, where `left` tokens are to be taken from above: by one
+// warp, which leaves it and what is left of them in sm.found. The sums of 32 places of all blocks are looked
+// at first (a load from another block's memory goes lane by lane: all places of all blocks were 180 us of 190
+// for 256 rows of 65536), all blocks' at once.
+template <int T>
+__device__ __forceinline__ void find_digit(ChooseShared<T> &sm, int d, int32_t left, int size)
+{
+    const int lane = threadIdx.x & 31;
+    auto sum_of = [&](const int32_t *from) {
+        if (size == 1)
+            return *from;
+        int32_t v[kMostCluster], sum = 0;
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k)
+            v[k] = k < size ? cluster_load(from, k) : 0;
+#pragma unroll
+        for (int k = 0; k < kMostCluster; ++k)
+            sum += v[k];
+        return sum;
+    };
+    // lane i: sums i and i + 32 from the top
+    const int32_t upper = sum_of(&sm.coarse[d][kDigits / 32 - 1 - lane]), lower = sum_of(&sm.coarse[d][31 - lane]);
+    const int32_t up_before = warp_before(upper, lane), up_all = __shfl_sync(0xFFFFFFFFu, up_before + upper, 31);
+    const bool in_upper = up_all >= left;
+    const int32_t own = in_upper ? upper : lower, before = in_upper ? up_before : up_all + warp_before(lower, lane);
+    const int at = __ffs(__ballot_sync(0xFFFFFFFFu, before + own >= left)) - 1;
+    const int group = (in_upper ? kDigits / 32 - 1 : 31) - at;
+    const int32_t above = __shfl_sync(0xFFFFFFFFu, before, at);
+    const int32_t place = sum_of(&sm.count[d][32 * group + 31 - lane]), place_before = above + warp_before(place, lane);
+    const int digit = __ffs(__ballot_sync(0xFFFFFFFFu, place_before + place >= left)) - 1;
+    if (lane == digit) {
+        sm.found[0] = 32 * group + 31 - lane;
+        sm.found[1] = left - place_before;
+    }
+}
+
+// A cluster of `size` blocks to a row, each with an equal part of the tokens that are chosen among, and of
+// that each warp, up to E tokens a lane (token 32 e + lane of the warp's), so the weights are read once. The
+// threshold's key is found in three digits, counted in shared memory. The first has sign, exponent and two
+// bits, so that weights of a few octaves fall into many places; what is above it stays, and only the few
+// tokens that share it (read again) are counted by the others. Every warp then knows how many stay before
+// its own. What bounds it is the work on a token, some 20 instructions. (All three digits over all tokens,
+// each token placed by a vote: 90, 82 us instead of FIG for 256 rows of 65536.)
+template <int T, int E>
+__global__ void __launch_bounds__(T, 1024 / T) k_choose_tokens(cg_token_choice c, int size)
+{
+    constexpr int kRowThreads = T, kRowWarps = T / 32;
+    __shared__ ChooseShared<T> sm;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x / size;
     const int rank = blockIdx.x % size;
@@ -79,14 +152,15 @@ __global__ void __launch_bounds__(kRowThreads, E > 4 ? 2 : 3) k_choose_tokens(cg
     // the choice is among [sinks, end), of which `pick` stay
     const int32_t end = m - c.recent, pick = c.budget - c.sinks - c.recent, n = end - c.sinks;
     const int32_t per_lane = (n + size * kRowThreads - 1) / (size * kRowThreads);   // at most E
-    const int32_t first = c.sinks + (rank * kRowWarps + warp) * per_lane * 32 + lane;
-    const int32_t mine = first < end ? min(per_lane, (end - first + 31) / 32) : 0;   // tokens of the lane
+    const int32_t first = c.sinks + (rank * kRowWarps + warp) * per_lane * 32;      // the warp's
+    w += first;
+    const int32_t mine = min(per_lane, (end - first - lane + 31) >> 5);             // tokens of the lane
     uint32_t key[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
-        key[e] = e < mine ? __float_as_uint(__ldg(w + first + 32 * e)) : 0u;
-    for (int i = tid; i < 3 * kDigits; i += kRowThreads)
-        sm.count[0][i] = 0;
+        key[e] = e < mine ? __float_as_uint(__ldg(w + 32 * e + lane)) : 0u;
+    for (int i = tid; i < 3 * kDigits / 4; i += kRowThreads)
+        reinterpret_cast<int4 *>(sm.count[0])[i] = make_int4(0, 0, 0, 0);
     for (int i = rank * kRowThreads + tid; i < c.sinks; i += size * kRowThreads)
         kept[i] = i;
     for (int i = rank * kRowThreads + tid; i < c.recent; i += size * kRowThreads)
@@ -94,73 +168,64 @@ __global__ void __launch_bounds__(kRowThreads, E > 4 ? 2 : 3) k_choose_tokens(cg
     if (pick == 0)
         return;
     __syncthreads();
+    // ---- the first digit of all tokens
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (e % 4 == 0 && e >= per_lane)   // for all lanes
+            break;
+        key[e] = e < mine ? key_of(__uint_as_float(key[e])) : 0u;   // 0: no token
+        count_if(key[e] != 0u, &sm.count[0][key[e] >> 21]);
+    }
     uint32_t prefix = 0;      // of the threshold's key
     int32_t left = pick;      // to be taken from the tokens that begin with it
+    uint32_t stays = 0, same = 0;   // bit e: the lane's token is above the threshold, begins as it does
 #pragma unroll
     for (int d = 0; d < 3; ++d) {
-        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0;
-        const uint32_t digits = d == 2 ? 1023u : 2047u;
-        int32_t *count = sm.count[d];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (d == 0)
-                key[e] = key_of(__uint_as_float(key[e]));
-            if (e < mine && (d == 0 || key[e] >> (d == 1 ? 21 : 10) == prefix))
-                atomicAdd(&count[key[e] >> shift & digits], 1);
-        }
         __syncthreads();
-        for (int k = warp; k < kDigits / 32; k += kRowWarps) {
-            const int32_t sum = __reduce_add_sync(0xFFFFFFFFu, count[32 * k + lane]);
+        for (int k = warp; k < (d == 2 ? 1024 : kDigits) / 32; k += kRowWarps) {
+            const int32_t sum = __reduce_add_sync(0xFFFFFFFFu, sm.count[d][32 * k + lane]);
             if (lane == 0)
                 sm.coarse[d][k] = sum;
         }
+        if (d == 2 && tid < 32)
+            sm.coarse[d][32 + tid] = 0;
         cluster_sync(size);
-        // one warp finds the 32 digits of the threshold among the sums of all blocks, then the digit (a
-        // load from another block's memory goes lane by lane: all digits of all blocks were 180 us of 190
-        // for 256 rows of 65536)
-        if (warp == 0) {
-            int32_t above = 0, group = 0;   // tokens above the digit; where it is
+        if (warp == 0)
+            find_digit(sm, d, left, size);
+        __syncthreads();
+        const uint32_t digit = (uint32_t)sm.found[0];
+        left = sm.found[1];
+        prefix = prefix << (d == 2 ? 10 : 11) | digit;
+        if (d == 0) {
+            // its keys: from .. below, and not 0
+            const uint32_t from = max(prefix << 21, 1u), below = prefix << 21 | ((1u << 21) - 1);
 #pragma unroll
-            for (int step = 0; step < 3; ++step) {   // upper and lower half of the sums, then digits
-                const int32_t *from = step < 2 ? &sm.coarse[d][kDigits / 32 - 1 - 32 * step - lane]
-                                               : &count[32 * group + 31 - lane];
-                int32_t own = 0;
-                for (int k = 0; k < size; ++k)
-                    own += size == 1 ? *from : cluster_load(from, k);
-                int32_t inc = own;
-#pragma unroll
-                for (int s = 1; s < 32; s <<= 1) {
-                    const int32_t o = __shfl_up_sync(0xFFFFFFFFu, inc, s);
-                    if (lane >= s)
-                        inc += o;
-                }
-                const uint32_t reached = __ballot_sync(0xFFFFFFFFu, above + inc >= left);
-                const int at = reached ? __ffs(reached) - 1 : 32;
-                const int32_t before = __shfl_sync(0xFFFFFFFFu, at < 32 ? inc - own : inc, at < 32 ? at : 31);
-                if (step == 2) {
-                    if (lane == 0) {
-                        sm.found[0] = 32 * group + 31 - at;
-                        sm.found[1] = left - above - before;
-                    }
-                } else if (step == 0 || group < 0) {
-                    above += before;
-                    group = at < 32 ? kDigits / 32 - 1 - 32 * step - at : -1;
-                }
+            for (int e = 0; e < E; ++e) {
+                if (e % 4 == 0 && e >= per_lane)
+                    break;
+                if (key[e] > below)
+                    stays |= 1u << e;
+                if (key[e] >= from)
+                    same |= 1u << e;
+            }
+            same &= ~stays;
+        }
+        // the tokens that share the digits so far
+        for (uint32_t rest = same; rest != 0; rest &= rest - 1) {
+            const int e = __ffs(rest) - 1;
+            const uint32_t k = key_of(__ldg(w + 32 * e + lane));
+            const uint32_t here = d == 0 ? prefix : d == 1 ? k >> 10 : k;
+            if (here == prefix) {
+                if (d < 2)
+                    atomicAdd(&sm.count[d + 1][d == 0 ? k >> 10 & 2047u : k & 1023u], 1);
+            } else {
+                same ^= 1u << e;
+                stays |= (uint32_t)(here > prefix) << e;
             }
         }
-        __syncthreads();
-        prefix = (d == 0 ? 0 : prefix << (d == 1 ? 11 : 10)) | (uint32_t)sm.found[0];
-        left = sm.found[1];
     }
     // ---- how many stay before each warp's
-    int32_t over = 0, at = 0;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        over += e < mine && key[e] > prefix;
-        at += e < mine && key[e] == prefix;
-    }
-    over = __reduce_add_sync(0xFFFFFFFFu, over);
-    at = __reduce_add_sync(0xFFFFFFFFu, at);
+    const int32_t over = __reduce_add_sync(0xFFFFFFFFu, __popc(stays)), at = __reduce_add_sync(0xFFFFFFFFu, __popc(same));
     if (lane == 0) {
         sm.over[warp] = over;
         sm.at[warp] = at;
@@ -186,18 +251,26 @@ __global__ void __launch_bounds__(kRowThreads, E > 4 ? 2 : 3) k_choose_tokens(cg
     if (size > 1)   // no block's shared memory goes while another one reads it
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     pos += min(taken, left);
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-        if (e < per_lane) {
-            const bool there = e < mine;
-            const uint32_t eq = __ballot_sync(0xFFFFFFFFu, there && key[e] == prefix);
-            const int rank_eq = taken + __popc(eq & ((1u << lane) - 1));
-            const bool stays = there && (key[e] > prefix || (key[e] == prefix && rank_eq < left));
-            const uint32_t all = __ballot_sync(0xFFFFFFFFu, stays);
-            if (stays)
-                kept[pos + __popc(all & ((1u << lane) - 1))] = first + 32 * e;
-            pos += __popc(all);
-            taken += __popc(eq);
+    // lane e: the tokens 32 e .. 32 e + 31 of the warp's
+    uint32_t word = transpose_bits(stays);
+    if (at > 0) {   // of those at the threshold the lowest, as many as are left
+        uint32_t eq = transpose_bits(same);
+        int32_t take = min(max(left - taken - warp_before(__popc(eq), lane), 0), 32);
+        for (; take > 0 && eq != 0; --take, eq &= eq - 1)
+            word |= eq & (0u - eq);
+    }
+    const int32_t here = __popc(word), before = warp_before(here, lane);
+    int32_t *to = kept + pos;
+    if (__reduce_add_sync(0xFFFFFFFFu, here) < 8 * per_lane) {   // few: each lane its own
+        to += before;
+        for (; word != 0; word &= word - 1)
+            *to++ = first + 32 * lane + __ffs(word) - 1;
+    } else {   // 32 tokens at a time, so that neighbours are written together
+        for (int e = 0; e < per_lane; ++e) {
+            const uint32_t all = __shfl_sync(0xFFFFFFFFu, word, e);
+            const int32_t at_e = __shfl_sync(0xFFFFFFFFu, before, e);
+            if (all >> lane & 1)
+                to[at_e + __popc(all & ((1u << lane) - 1))] = first + 32 * e + lane;
         }
     }
     if (size > 1)
@@ -324,7 +397,7 @@ __global__ void __launch_bounds__(kLensThreads) k_choose_lens(cg_token_choice c)
         *static_cast<uint4 *>(c.status) = make_uint4(bad ? CG_ERR_CORRUPT : CG_OK, 0, 0, 0);
 }
 
-template <int E>
+template <int T, int E>
 cudaError_t launch_choice(const cg_token_choice &c, int64_t rows, int size, cudaStream_t s)
 {
     cudaLaunchAttribute attr;
@@ -333,11 +406,11 @@ cudaError_t launch_choice(const cg_token_choice &c, int64_t rows, int size, cuda
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(rows * size));
-    cfg.blockDim = dim3(kRowThreads);
+    cfg.blockDim = dim3(T);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k_choose_tokens<E>, c, size);
+    return cudaLaunchKernelEx(&cfg, k_choose_tokens<T, E>, c, size);
 }
 
 // ------------------------------------------------------------------ the move
@@ -579,21 +652,26 @@ extern "C" cg_status cg_choose_tokens(const cg_token_choice *c, cg_stream_t stre
     const int64_t rows = lists * c->heads;
     cudaError_t err = cudaSuccess;
     if (rows > 0) {
-        // blocks to a row: as many as hold it, and more while there are SMs for them
+        // Blocks to a row: as many as hold it, and more while there are SMs for them. Short rows have small
+        // blocks, four on an SM: what bounds them is each block's chain of barriers.
+        constexpr int kSmall = 256, kLarge = 512, kMost = 32;   // threads; tokens of one
         int size = 1;
-        while (size < kMostCluster && c->width > 32 * kRowThreads * size)
+        while (size < kMostCluster && c->width > kMost * kLarge * size)
             size *= 2;
-        while (size < kMostCluster && rows * size < 152 && c->width > 8 * kRowThreads * size)
+        while (size < kMostCluster && rows * size < 152 && c->width > 8 * kSmall * size)
             size *= 2;
-        const int64_t each = ((int64_t)c->width + size * kRowThreads - 1) / (size * kRowThreads);
-        if (rows * size >= limit || each > 32)
+        const int64_t per_block = ((int64_t)c->width + size - 1) / size;
+        const bool small = per_block <= kMost * kSmall;
+        const int64_t each = (per_block + (small ? kSmall : kLarge) - 1) / (small ? kSmall : kLarge);
+        if (rows * size >= limit || each > kMost)
             k_choose_long<<<(unsigned)rows, kChooseThreads, 0, s>>>(*c);
+        else if (!small)
+            err = each <= 24 ? launch_choice<kLarge, 24>(*c, rows, size, s) : launch_choice<kLarge, 32>(*c, rows, size, s);
         else
-            err = each <= 4    ? launch_choice<4>(*c, rows, size, s)
-                  : each <= 8  ? launch_choice<8>(*c, rows, size, s)
-                  : each <= 12 ? launch_choice<12>(*c, rows, size, s)
-                  : each <= 20 ? launch_choice<20>(*c, rows, size, s)
-                               : launch_choice<32>(*c, rows, size, s);
+            err = each <= 4    ? launch_choice<kSmall, 4>(*c, rows, size, s)
+                  : each <= 8  ? launch_choice<kSmall, 8>(*c, rows, size, s)
+                  : each <= 20 ? launch_choice<kSmall, 20>(*c, rows, size, s)
+                               : launch_choice<kSmall, 32>(*c, rows, size, s);
     }
     if (err == cudaSuccess)
         err = cudaGetLastError();

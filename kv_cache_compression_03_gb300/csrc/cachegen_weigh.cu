@@ -15,9 +15,10 @@
 namespace {
 
 constexpr int kRing = 8;           // blobs in a warp's ring
-constexpr int kItemTokens = 128;   // of a block in the second pass, 32 to a warp
+constexpr int kItemTokens = 128;   // of a block in the second pass, 32 to a warp; or,
+constexpr int kManyRows = 128;     // from so many rows on, 32 to a block, whose warps share the rows
 constexpr int kApplyTokens = 512;  // of a block in the second pass over stored scores
-constexpr int kMaxBlocks = 960;    // of the first pass
+constexpr int kMaxBlocks = 640;    // of the first pass
 
 struct WeighArgs {
     cg_token_weights w;
@@ -141,35 +142,51 @@ __device__ __forceinline__ void load_keys(const uint8_t *blob, Keys<B> *to)
     }
 }
 
-// Scores in powers of two: z[j] are token g + 8 j's with rows 2t and 2t + 1.
-template <typename B>
-__device__ __forceinline__ void scores_of(const Keys<B> &k, const Queries<B> &q, float2 (&z)[2])
+// A product of the instruction that the compiler may move among others.
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t *a, uint32_t b0, uint32_t b1, const float *c)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// Scores in powers of two of NT row tiles: z[nt][j] are token g + 8 j's with rows 2t and 2t + 1.
+template <typename B, int NT>
+__device__ __forceinline__ void scores_of(const Keys<B> &k, const Queries<B> (&q)[NT], float2 (&z)[NT][2])
 {
     constexpr int NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
-    float2 y[2];
+    const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float2 y[NT][2];
 #pragma unroll
     for (int gi = 0; gi < NG; ++gi) {
-        float acc[4];
+        float acc[NT][4];
 #pragma unroll
         for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
 #pragma unroll
             for (int i = 0; i < 4; i += 2)
-                if (w == gi * WPG && i == 0)
-                    mma16816_first(acc, k.a[w][0], k.a[w][1], k.a[w][2], k.a[w][3], q.qf[w][0], q.qf[w][1]);
-                else
-                    mma16816(acc, k.a[w][2 * i], k.a[w][2 * i + 1], k.a[w][2 * i + 2], k.a[w][2 * i + 3], q.qf[w][i],
-                             q.qf[w][i + 1]);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float2 s = make_float2(k.s[j][gi], k.s[j][gi]), mid = make_float2(k.mid[j][gi], k.mid[j][gi]);
-            const float2 x = make_float2(acc[2 * j], acc[2 * j + 1]);
-            y[j] = gi ? fma2(s, x, y[j]) : make_float2(s.x * x.x, s.y * x.y);
-            z[j] = gi ? fma2(mid, q.sq[gi], z[j]) : make_float2(mid.x * q.sq[0].x, mid.y * q.sq[0].y);
-        }
+                for (int nt = 0; nt < NT; ++nt)
+                    mma(acc[nt], &k.a[w][2 * i], q[nt].qf[w][i], q[nt].qf[w][i + 1],
+                        w == gi * WPG && i == 0 ? zero : acc[nt]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float s = k.s[j][gi], mid = k.mid[j][gi], x0 = acc[nt][2 * j], x1 = acc[nt][2 * j + 1];
+                y[nt][j].x = gi ? fmaf(s, x0, y[nt][j].x) : s * x0;
+                y[nt][j].y = gi ? fmaf(s, x1, y[nt][j].y) : s * x1;
+                z[nt][j].x = gi ? fmaf(mid, q[nt].sq[gi].x, z[nt][j].x) : mid * q[nt].sq[0].x;
+                z[nt][j].y = gi ? fmaf(mid, q[nt].sq[gi].y, z[nt][j].y) : mid * q[nt].sq[0].y;
+            }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-        z[j] = fma2(y[j], q.rho, z[j]);
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            z[nt][j].x = fmaf(y[nt][j].x, q[nt].rho.x, z[nt][j].x);
+            z[nt][j].y = fmaf(y[nt][j].y, q[nt].rho.y, z[nt][j].y);
+        }
 }
 
 // Where not every token is seen by every row: -inf for those that are not. x: positions of the rows.
@@ -240,11 +257,10 @@ __device__ __forceinline__ float2 row_stats_of(float m, float l)
     return l == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(m, 1.0f / l);
 }
 
-// Blocks of the first pass on an SM.
-constexpr int stat_blocks(int NT) { return NT == 1 ? 4 : NT == 2 ? 3 : 2; }
+// Blocks on an SM.
+constexpr int stat_blocks(int NT) { return NT == 2 ? 3 : 2; }
 
-// kStored: scores are left for the second pass, else the queries.
-template <typename B, int NT, bool kStored>
+template <typename B, int NT>
 __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnArgs p, WeighArgs a)
 {
     using S = StatShared<B, NT>;
@@ -338,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
                 const int in = 8 * nt + 2 * t + j;
                 x[nt][j] = in < tile.rows ? u.q.x0 + (tile.row0 + in) / p.ratio : -1;
             }
-            if (!kStored && u.b0 == 0 && warp == 0 && 8 * nt < tile.rows) {   // by the unit's first piece
+            if (u.b0 == 0 && warp == 0 && 8 * nt < tile.rows) {   // by the unit's first piece, for the sums
                 const int64_t at_slot = (int64_t)u.h * a.slots + slot + nt;
                 uint4 *to = a.queries + at_slot * NW * 32 + lane;
 #pragma unroll
@@ -380,42 +396,34 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
                 load_keys<B>(sm.ring[warp][st], &k);
                 const int tok = 16 * (b < tile.span.sink ? b : b + tile.span.skip);
                 const bool whole = tok + 15 <= tile.x_lo && (tile.x_hi - tok < window || tok + 15 < p.a.sinks);
+                float2 z[NT][2];
+                scores_of<B, NT>(k, q, z);
+                if (!whole)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        hide(p, tok, x[nt], window, z[nt]);
+                // raised only when a score exceeds it by 2^8
+                float over = -INFINITY;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    over = fmaxf(fmaxf(over, fmaxf(z[nt][0].x, z[nt][1].x) - m[nt][0]),
+                                 fmaxf(z[nt][0].y, z[nt][1].y) - m[nt][1]);
+                if (over > 8.0f) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float m0 = fmaxf(m[nt][0], fmaxf(z[nt][0].x, z[nt][1].x));
+                        const float m1 = fmaxf(m[nt][1], fmaxf(z[nt][0].y, z[nt][1].y));
+                        l[nt][0] *= exp2_fast(m[nt][0] - m0);
+                        l[nt][1] *= exp2_fast(m[nt][1] - m1);
+                        m[nt][0] = m0;
+                        m[nt][1] = m1;
+                    }
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    float2 z[2];
-                    scores_of<B>(k, q[nt], z);
-                    if (!whole)
-                        hide(p, tok, x[nt], window, z);
-                    if (kStored) {
-                        float *to = a.scores + ((int64_t)u.r * p.heads + u.h) * a.rows * a.tokens + tok + g;
-                        const int row = 2 * t;
-                        if (row < tile.rows) {
-                            to[(int64_t)row * a.tokens] = z[0].x;
-                            to[(int64_t)row * a.tokens + 8] = z[1].x;
-                        }
-                        if (row + 1 < tile.rows) {
-                            to[(int64_t)(row + 1) * a.tokens] = z[0].y;
-                            to[(int64_t)(row + 1) * a.tokens + 8] = z[1].y;
-                        }
-                    }
-                    // raised only when a score exceeds it by 2^8
-                    const float2 top = make_float2(fmaxf(z[0].x, z[1].x), fmaxf(z[0].y, z[1].y));
-                    if (top.x > m[nt][0] + 8.0f) {
-                        l[nt][0] *= exp2_fast(m[nt][0] - top.x);
-                        m[nt][0] = top.x;
-                    }
-                    if (top.y > m[nt][1] + 8.0f) {
-                        l[nt][1] *= exp2_fast(m[nt][1] - top.y);
-                        m[nt][1] = top.y;
-                    }
-                    l[nt][0] += exp2_fast(z[0].x - m[nt][0]) + exp2_fast(z[1].x - m[nt][0]);
-                    l[nt][1] += exp2_fast(z[0].y - m[nt][1]) + exp2_fast(z[1].y - m[nt][1]);
+                    l[nt][0] += exp2_fast(z[nt][0].x - m[nt][0]) + exp2_fast(z[nt][1].x - m[nt][0]);
+                    l[nt][1] += exp2_fast(z[nt][0].y - m[nt][1]) + exp2_fast(z[nt][1].y - m[nt][1]);
                 }
-            } else if (kStored && alive) {   // a page that is not there
-                const int tok = 16 * (b < tile.span.sink ? b : b + tile.span.skip);
-                float *to = a.scores + ((int64_t)u.r * p.heads + u.h) * a.rows * a.tokens + tok;
-                for (int i = lane; i < 16 * tile.rows; i += 32)
-                    to[(int64_t)(i / 16) * a.tokens + i % 16] = -INFINITY;
             }
             __syncwarp();   // every lane has read the place
             if (alive)
@@ -467,6 +475,343 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
             bar_wait(&sm.full[warp][used % kRing], (used / kRing) & 1);
 }
 
+// ---- up to 8 rows: scores are stored
+
+// Half the words' instructions: a code enters as a bf16 whose bits are the code's, n 2^-133 or, for the
+// upper codes, n 2^-129 (against 1/16 of the query), and 8 times the sum of the queries comes off where the
+// products are summed, in each instruction by its own accumulator, so that no rounding comes between.
+template <typename B, int P>
+struct FewQueries {
+    uint32_t qf[P][B::kWords][4];
+    float2 off[B::kWords][2];        // -8 sum q of an instruction's 16 channels, as it counts them
+    float2 rho, sq[B::kGroups];
+};
+
+// P = 2: columns 4 .. 7 of the instruction have the rows 0 .. 3 again. A blob's products with the rows in
+// columns 0 .. 3 and the next one's with those in 4 .. 7 go to one accumulator, and all that follows is
+// done for both at once.
+template <typename B, int P>
+__device__ __forceinline__ void load_few(const AttnArgs &p, const AttnRequest &rq, int h, FewQueries<B, P> *to)
+{
+    constexpr int NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3, row = P == 2 ? g & 3 : g;
+    const bool there = row < rq.rows;
+    const int qt = there ? row / p.ratio : 0, qh = h * p.ratio + (there ? row - qt * p.ratio : 0);
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.a.q) +
+                             (int64_t)(rq.row0 + qt) * p.a.q_token_stride + qh * p.a.q_head_stride;
+    uint4 v[NW];
+    uint32_t top = 0;        // largest |q| of the row (as bf16 bits, in both halves)
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        v[w] = there ? *reinterpret_cast<const uint4 *>(q + 32 * w + 8 * t) : make_uint4(0, 0, 0, 0);
+        top = __vmaxu2(__vmaxu2(top, v[w].x & 0x7FFF7FFFu), v[w].y & 0x7FFF7FFFu);
+        top = __vmaxu2(__vmaxu2(top, v[w].z & 0x7FFF7FFFu), v[w].w & 0x7FFF7FFFu);
+    }
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    // exact: |q| 2^fe stays below 2^127; small rows (and 0) take the largest factor
+    const int fe = min(126 - ((int)(top >> 7) - 127), 127);
+    const float up = pow2(fe), up16 = pow2(fe - 4);
+    // scale2 2^(133 - fe) in two steps, both upwards: the power alone may pass 2^127, and what
+    // lies between passes fp32's range only where the result does
+    const float back = p.scale2 * pow2((133 - fe) >> 1) * pow2((134 - fe) >> 1);
+    const float o0 = pow2((fe - 130) >> 1), o1 = -pow2((fe - 129) >> 1);
+    to->rho = make_float2(__shfl_sync(0xFFFFFFFFu, back, 8 * t), __shfl_sync(0xFFFFFFFFu, back, 8 * t + 4));
+    float sum[NG] = {};
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const uint4 c = v[w];
+        // channels i and i + 4 side by side, as the codes of a word come
+        const uint32_t f[4] = {pack_bf16(par_s(c.x) * up, par_s(c.z) * up), pack_bf16(par_lo(c.x) * up16, par_lo(c.z) * up16),
+                               pack_bf16(par_s(c.y) * up, par_s(c.w) * up), pack_bf16(par_lo(c.y) * up16, par_lo(c.w) * up16)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            to->qf[0][w][i] = P == 2 && g >= 4 ? 0 : f[i];
+            if (P == 2)
+                to->qf[P - 1][w][i] = g >= 4 ? f[i] : 0;
+        }
+        float half[2] = {(par_s(c.x) + par_s(c.z)) + (par_lo(c.x) + par_lo(c.z)),
+                         (par_s(c.y) + par_s(c.w)) + (par_lo(c.y) + par_lo(c.w))};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            half[i] += __shfl_xor_sync(0xFFFFFFFFu, half[i], 1);
+            half[i] += __shfl_xor_sync(0xFFFFFFFFu, half[i], 2);
+            const float off = half[i] * o0 * o1;
+            to->off[w][i] = make_float2(__shfl_sync(0xFFFFFFFFu, off, 8 * t), __shfl_sync(0xFFFFFFFFu, off, 8 * t + 4));
+        }
+        sum[w / WPG] += half[0] + half[1];
+    }
+#pragma unroll
+    for (int i = 0; i < NG; ++i) {
+        const float mine = p.scale2 * sum[i];
+        to->sq[i] = make_float2(__shfl_sync(0xFFFFFFFFu, mine, 8 * t), __shfl_sync(0xFFFFFFFFu, mine, 8 * t + 4));
+    }
+}
+
+// z[j]: token g + 8 j with rows 2t and 2t + 1 (of their blob). `par`: the lane's blob, for its parameters.
+template <typename B, int P>
+__device__ __forceinline__ void few_scores(const uint8_t *const (&blob)[P], const uint8_t *par, const FewQueries<B, P> &q,
+                                           float2 (&z)[2])
+{
+    constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    uint32_t k[P][2][NW];
+#pragma unroll
+    for (int b = 0; b < P; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            load_words(k[b][j], blob[b] + B::kKCodes + (g + 8 * j) * (D / 2) + t * (D / 8));
+    uint32_t pw[2][NG];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        load_words(pw[j], par + B::kKParams + (g + 8 * j) * 4 * NG);
+    float2 y[2];
+#pragma unroll
+    for (int gi = 0; gi < NG; ++gi) {
+        float x[4] = {};
+#pragma unroll
+        for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float acc[4] = {q.off[w][i].x, q.off[w][i].y, q.off[w][i].x, q.off[w][i].y};
+#pragma unroll
+                for (int b = 0; b < P; ++b) {
+                    const uint32_t a[4] = {codes_of(k[b][0][w], 2 * i), codes_of(k[b][1][w], 2 * i),
+                                           codes_of(k[b][0][w], 2 * i + 1), codes_of(k[b][1][w], 2 * i + 1)};
+                    mma(acc, a, q.qf[b][w][2 * i], q.qf[b][w][2 * i + 1], acc);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = w == gi * WPG && i == 0 ? acc[e] : x[e] + acc[e];
+            }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float s = par_s(pw[j][gi]), mid = fmaf(8.0f, s, par_lo(pw[j][gi]));
+            y[j].x = gi ? fmaf(s, x[2 * j], y[j].x) : s * x[2 * j];
+            y[j].y = gi ? fmaf(s, x[2 * j + 1], y[j].y) : s * x[2 * j + 1];
+            z[j].x = gi ? fmaf(mid, q.sq[gi].x, z[j].x) : mid * q.sq[0].x;
+            z[j].y = gi ? fmaf(mid, q.sq[gi].y, z[j].y) : mid * q.sq[0].y;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        z[j].x = fmaf(y[j].x, q.rho.x, z[j].x);
+        z[j].y = fmaf(y[j].y, q.rho.y, z[j].y);
+    }
+}
+
+constexpr int kPairs = 4;        // pairs of blobs in a warp's ring
+constexpr int kFewBlocks = 3;    // on an SM
+
+template <typename B>
+struct FewShared {
+    uint8_t ring[kWarps][kPairs][2][B::kVCodes];
+    float m[kWarps][8], l[kWarps][8];
+    uint64_t full[kWarps][kPairs];
+};
+
+template <typename B, int P>
+__global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, WeighArgs a)
+{
+    using S = FewShared<B>;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    S &sm = *reinterpret_cast<S *>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t = lane & 3;
+
+    grid_next();
+    if (lane == 0)
+        for (int i = 0; i < kPairs; ++i)
+            bar_init(&sm.full[warp][i], 2);
+    bar_init_fence();
+    int64_t total, chunk;
+    const Place at = schedule<8>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
+    const int64_t begin = blockIdx.x * chunk;
+    if (begin >= total)
+        return;
+    const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
+    const int bpp = p.page_tokens / 16;
+    Unit first;
+    unit_at<8>(p, at, count, &first);
+    Unit fu = first;
+    Tile ft = tile_of<8>(p, fu);
+    int64_t f_pos = fu.b1 - fu.b0;
+    int f_b, f_e, f_i = 0, f_n = 0;
+    tile_range(fu, ft, warp, &f_b, &f_e);
+    uint32_t f_off = 0, f_ok = 0, issued = 0, ahead = 0;
+    auto feed = [&]() {
+        ahead >>= 2;
+        if (f_i >= f_n) {
+            while (f_b >= f_e) {
+                if (f_pos >= count)
+                    return;
+                unit_next<8>(p, count - f_pos, &fu);
+                ft = tile_of<8>(p, fu);
+                f_pos += fu.b1 - fu.b0;
+                tile_range(fu, ft, warp, &f_b, &f_e);
+            }
+            f_i = 0;
+            f_n = f_e - f_b < 32 ? f_e - f_b : 32;
+            int id = -1;
+            if (lane < f_n) {
+                const int vb = f_b + lane, ab = vb < ft.span.sink ? vb : vb + ft.span.skip;
+                const int page = ab / bpp;
+                id = p.a.block_table[fu.r * p.a.table_stride + page];
+                if ((unsigned)id >= (unsigned)p.num_pages)
+                    int4_set_status(p.status, CG_ERR_CORRUPT);
+                f_off = (((uint32_t)id * p.heads + fu.h) * bpp + (ab - page * bpp)) * (B::kBytes / 128);
+            }
+            f_ok = __ballot_sync(0xFFFFFFFFu, (unsigned)id < (unsigned)p.num_pages);
+            f_b += f_n;
+        }
+        const int st = issued % kPairs;
+        if ((unsigned)(lane - f_i) < 2u) {
+            uint64_t *bar = &sm.full[warp][st];
+            if (f_ok >> lane & 1) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_expect(bar, B::kVCodes);
+                bulk_copy(sm.ring[warp][st][lane - f_i], p.layer + (uint64_t)f_off * 128, B::kVCodes, bar);
+            } else {
+                bar_arrive(bar);
+            }
+        }
+        ahead |= (f_ok >> f_i & 3) << (2 * (kPairs - 1));
+        f_i += 2;
+        ++issued;
+    };
+    __syncwarp();
+    for (int i = 0; i < kPairs; ++i)
+        feed();
+
+    const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
+    const int side = P == 2 ? t >> 1 : 0;            // which blob of a pair the lane's columns are of
+    const int row = P == 2 ? 2 * (t & 1) : 2 * t;    // the first of the lane's two rows
+    bool alive = true;               // no wait has run out
+    uint32_t used = 0;
+    Unit u = first;
+    int64_t pos = 0;
+    for (;;) {
+        const Tile tile = tile_of<8>(p, u);
+        FewQueries<B, P> q;
+        load_few<B, P>(p, u.q, u.h, &q);
+        const int x[2] = {row < tile.rows ? u.q.x0 + row / p.ratio : -1, row + 1 < tile.rows ? u.q.x0 + (row + 1) / p.ratio : -1};
+        const bool has[2] = {row < tile.rows, row + 1 < tile.rows};
+        float *to0 = a.scores + (((int64_t)u.r * p.heads + u.h) * a.rows + row) * a.tokens + g;
+        float *to1 = to0 + a.tokens;
+        float2 m = make_float2(kNone, kNone), l = make_float2(0.0f, 0.0f);
+        // what the lane's rows make of two scores each
+        auto take = [&](float2 (&z)[2], int tok, bool whole, bool there, bool valid) {
+            if (!whole)
+                hide(p, tok, x, window, z);
+            if (!there)
+                z[0] = z[1] = make_float2(-INFINITY, -INFINITY);
+            if (valid && has[0]) {
+                to0[tok] = z[0].x;
+                to0[tok + 8] = z[1].x;
+            }
+            if (valid && has[1]) {
+                to1[tok] = z[0].y;
+                to1[tok + 8] = z[1].y;
+            }
+            // raised only when a score exceeds it by 2^8
+            const float top0 = fmaxf(z[0].x, z[1].x), top1 = fmaxf(z[0].y, z[1].y);
+            if (fmaxf(top0 - m.x, top1 - m.y) > 8.0f) {
+                const float m0 = fmaxf(m.x, top0), m1 = fmaxf(m.y, top1);
+                l.x *= exp2_fast(m.x - m0);
+                l.y *= exp2_fast(m.y - m1);
+                m = make_float2(m0, m1);
+            }
+            l.x += exp2_fast(z[0].x - m.x) + exp2_fast(z[1].x - m.x);
+            l.y += exp2_fast(z[0].y - m.y) + exp2_fast(z[1].y - m.y);
+        };
+        int b, e;
+        tile_range(u, tile, warp, &b, &e);
+        for (; b < e; b += 2) {
+            const int st = used % kPairs;
+            if (alive) {
+                const bool give_up = kTestTimeout && used == 1;
+                if (give_up || !__all_sync(0xFFFFFFFFu, bar_wait(&sm.full[warp][st], (used / kPairs) & 1))) {
+                    alive = false;   // `used` stays: the first pair not waited for
+                    int4_set_status(p.status, CG_ERR_TIMEOUT);
+                } else {
+                    ++used;
+                }
+            }
+            if (alive) {
+                auto token = [&](int vb) { return 16 * (vb < tile.span.sink ? vb : vb + tile.span.skip); };
+                auto all_see = [&](int tok) {
+                    return tok + 15 <= tile.x_lo && (tile.x_hi - tok < window || tok + 15 < p.a.sinks);
+                };
+                const uint8_t(&ring)[2][B::kVCodes] = sm.ring[warp][st];
+                if constexpr (P == 2) {
+                    const uint8_t *const blobs[P] = {ring[0], ring[1]};
+                    const int tok = token(b + side);
+                    const bool whole = all_see(token(b)) && all_see(token(b + 1));
+                    float2 z[2];
+                    few_scores<B, P>(blobs, ring[side], q, z);
+                    take(z, tok, whole, ahead >> side & 1, b + side < e);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        if (b + i >= e)
+                            break;
+                        const uint8_t *const blobs[P] = {ring[i]};
+                        float2 z[2];
+                        few_scores<B, P>(blobs, ring[i], q, z);
+                        take(z, token(b + i), all_see(token(b + i)), ahead >> i & 1, true);
+                    }
+                }
+            }
+            __syncwarp();   // every lane has read the place
+            if (alive)
+                feed();
+        }
+        // ---- joined over the lanes of a row, the warps, and with other pieces in a second kernel
+#pragma unroll
+        for (int d = P == 2 ? 2 : 4; d < 32; d <<= 1) {
+            const float2 om = make_float2(__shfl_xor_sync(0xFFFFFFFFu, m.x, d), __shfl_xor_sync(0xFFFFFFFFu, m.y, d));
+            const float2 ol = make_float2(__shfl_xor_sync(0xFFFFFFFFu, l.x, d), __shfl_xor_sync(0xFFFFFFFFu, l.y, d));
+            const float2 mx = make_float2(fmaxf(m.x, om.x), fmaxf(m.y, om.y));
+            l.x = l.x * exp2_fast(m.x - mx.x) + ol.x * exp2_fast(om.x - mx.x);
+            l.y = l.y * exp2_fast(m.y - mx.y) + ol.y * exp2_fast(om.y - mx.y);
+            m = mx;
+        }
+        if (g == 0 && side == 0) {
+            sm.m[warp][row] = m.x;
+            sm.m[warp][row + 1] = m.y;
+            sm.l[warp][row] = l.x;
+            sm.l[warp][row + 1] = l.y;
+        }
+        __syncthreads();
+        const bool from_before = u.b0 > 0, goes_on = u.b1 < u.span.nb;
+        if (tid < 8) {
+            float mx = kNone, ls = 0.0f;
+            if (tid < tile.rows) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    mx = fmaxf(mx, sm.m[w][tid]);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w)
+                    ls += sm.l[w][tid] * exp2_fast(sm.m[w][tid] - mx);
+            }
+            if (from_before || goes_on)
+                a.parts[((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * 8 + tid] = make_float2(mx, ls);
+            else
+                a.stats[((int64_t)u.h * a.slots + first_slot(p, u.r, u.q.row0)) * 8 + tid] = row_stats_of(mx, ls);
+        }
+        __syncthreads();
+        pos += u.b1 - u.b0;
+        if (pos >= count)
+            break;
+        unit_next<8>(p, count - pos, &u);
+    }
+    // a wait that ran out: the copies still in flight must land before the block's memory goes
+    if (!alive)
+        for (; used < issued; ++used)
+            bar_wait(&sm.full[warp][used % kPairs], (used / kPairs) & 1);
+}
+
 // Block c joins the unit that begins in block c of the first kernel and goes on behind it.
 template <int RU>
 __global__ void __launch_bounds__(kThreads) k_weigh_join(AttnArgs p, int pieces, WeighArgs a)
@@ -507,7 +852,7 @@ __global__ void __launch_bounds__(kThreads) k_weigh_join(AttnArgs p, int pieces,
 
 // -------------------------------------------------------------- sums of tokens
 
-// Items of `each` tokens of a (request, KV head), those of all heads of the first tokens first. One
+// Items of each(q) tokens of a (request, KV head), those of all heads of the first tokens first. One
 // warp finds its item, going on from where the last call stood (32 requests from r0 on, `before`
 // items ahead of them): false when there are no more. Requests without rows have items too.
 struct Items {
@@ -515,7 +860,8 @@ struct Items {
     int64_t before;
 };
 
-__device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, int each, Items *at, AttnRequest *q, int *r,
+template <typename F>
+__device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, F each, Items *at, AttnRequest *q, int *r,
                                           int *h, int *tok)
 {
     const int lane = threadIdx.x & 31;
@@ -527,7 +873,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, int e
         if (at->r0 + lane < p.a.requests) {
             attn_request(p, at->r0 + lane, q, &error);
             if (error == CG_OK)
-                w = (int64_t)((q->kv + each - 1) / each) * p.heads;
+                w = (int64_t)((q->kv + each(*q) - 1) / each(*q)) * p.heads;
         }
         int64_t inc = w;
 #pragma unroll
@@ -546,19 +892,21 @@ __device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, int e
         const int64_t off = __shfl_sync(0xFFFFFFFFu, item - start, src);
         *r = at->r0 + src;
         attn_request(p, *r, q, &error);
-        *h = (int)(off % p.heads);
-        *tok = (int)(off / p.heads) * each;
+        const int i = (int)(off / p.heads);
+        *h = (int)(off - (int64_t)i * p.heads);
+        *tok = i * each(*q);
         return true;
     }
 }
 
-// A block to 128 tokens of a (request, KV head), two blobs to a warp, over all rows that see any
-// of them.
+// A warp takes 32 tokens of a (request, KV head), two blobs whose keys stay in its registers, over the
+// rows that see any of them: all of those, or where there are many a quarter, every fourth tile of 8.
 template <typename B>
 __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArgs a)
 {
     constexpr int NW = B::kWords, NG = B::kGroups;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    __shared__ float parts[kWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
     const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
     const int bpp = p.page_tokens / 16;
     grid_wait();
@@ -566,11 +914,15 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
         AttnRequest q;
         int r, h, t0;
-        if (!find_item(p, item, kItemTokens, &items, &q, &r, &h, &t0))
+        if (!find_item(p, item, [](const AttnRequest &x) { return x.rows >= kManyRows ? 32 : kItemTokens; }, &items, &q,
+                       &r, &h, &t0))
             return;
-        t0 += 32 * warp;
-        if (t0 >= q.kv)
-            continue;
+        const bool shared = q.rows >= kManyRows;   // the block's warps have the same tokens
+        if (!shared) {
+            t0 += 32 * warp;
+            if (t0 >= q.kv)
+                continue;
+        }
         Keys<B> keys[2];
         bool there[2];
 #pragma unroll
@@ -584,45 +936,48 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
             const uint64_t blob = there[b] ? ((uint64_t)id * p.heads + h) * bpp + (tok - page * p.page_tokens) / 16 : 0;
             load_keys<B>(p.layer + blob * B::kBytes, &keys[b]);
         }
-        // ---- rows that see any of the warp's tokens
+        // ---- rows that see any of the tokens
         const int64_t lo = min((int64_t)max(0, t0 - q.x0) * p.ratio, (int64_t)q.rows);
         int64_t hi = q.rows;
         if (p.a.window > 0 && t0 >= p.a.sinks)
             hi = min(hi, ((int64_t)t0 + 31 + window - q.x0) * p.ratio);
-        const int i0 = (int)(lo / 8), i1 = hi < 0 ? 0 : (int)((hi + 7) / 8);
+        const int step = shared ? kWarps : 1, i0 = (int)(lo / 8) + (shared ? warp : 0);
+        const int i1 = hi < 0 ? 0 : (int)((hi + 7) / 8);
         const int64_t slot = (int64_t)h * a.slots + first_slot(p, r, q.row0);
         float total[2][2] = {}, sum[2][2] = {};
-        for (int i = i0; i < i1; ++i) {
-            Queries<B> rows;
+        int count = 0;
+        for (int i = i0; i < i1; i += step) {
+            Queries<B> rows[1];
             const uint4 *from = a.queries + (slot + i) * NW * 32 + lane;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const uint4 v = from[32 * w];
-                rows.qf[w][0] = v.x, rows.qf[w][1] = v.y, rows.qf[w][2] = v.z, rows.qf[w][3] = v.w;
+                rows[0].qf[w][0] = v.x, rows[0].qf[w][1] = v.y, rows[0].qf[w][2] = v.z, rows[0].qf[w][3] = v.w;
             }
             const float2 *f = reinterpret_cast<const float2 *>(a.factors + (slot + i) * (NG + 1) * 8) + t;
-            rows.rho = f[0];
+            rows[0].rho = f[0];
 #pragma unroll
             for (int k = 0; k < NG; ++k)
-                rows.sq[k] = f[4 * (k + 1)];
+                rows[0].sq[k] = f[4 * (k + 1)];
             const float4 st = *reinterpret_cast<const float4 *>(a.stats + (slot + i) * 8 + 2 * t);
             const int x_lo = q.x0 + 8 * i / p.ratio, x_hi = q.x0 + min(8 * i + 7, q.rows - 1) / p.ratio;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
                 const int tok = t0 + 16 * b;
-                float2 z[2];
-                scores_of<B>(keys[b], rows, z);
+                float2 z[1][2];
+                scores_of<B, 1>(keys[b], rows, z);
                 if (!(tok + 15 <= x_lo && (x_hi - tok < window || tok + 15 < p.a.sinks))) {
                     const int row = 8 * i + 2 * t;
                     const int x[2] = {row < q.rows ? q.x0 + row / p.ratio : -1,
                                       row + 1 < q.rows ? q.x0 + (row + 1) / p.ratio : -1};
-                    hide(p, tok, x, window, z);
+                    hide(p, tok, x, window, z[0]);
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    sum[b][j] = fmaf(exp2_fast(z[j].y - st.z), st.w, fmaf(exp2_fast(z[j].x - st.x), st.y, sum[b][j]));
+                    sum[b][j] = fmaf(exp2_fast(z[0][j].y - st.z), st.w,
+                                     fmaf(exp2_fast(z[0][j].x - st.x), st.y, sum[b][j]));
             }
-            if ((i & 31) == 31)   // sums of sums: their roundings grow with the root of either's length
+            if ((++count & 31) == 0)   // sums of sums: their roundings grow with the root of either's length
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -631,6 +986,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
                         sum[b][j] = 0.0f;
                     }
         }
+        float mine = 0.0f;   // of token t0 + lane
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -638,17 +994,25 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
                 float s = total[b][j] + sum[b][j];
                 s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
                 s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-                const int tok = t0 + 16 * b + 8 * j + g;
-                if (t == 0 && tok < q.kv) {
-                    const float had = a.w.in == nullptr ? 0.0f
-                                                        : a.w.in[r * a.w.in_request_stride + h * a.w.in_head_stride + tok];
-                    a.w.out[r * a.w.out_request_stride + h * a.w.out_head_stride + tok] = there[b] ? had + s : had;
-                }
+                s = __shfl_sync(0xFFFFFFFFu, s, 4 * (lane & 7));
+                if (lane >> 3 == 2 * b + j)
+                    mine = there[b] ? s : 0.0f;
             }
+        if (shared) {
+            parts[warp][lane] = mine;
+            __syncthreads();
+            mine = (parts[0][lane] + parts[1][lane]) + (parts[2][lane] + parts[3][lane]);
+            __syncthreads();
+        }
+        const int tok = t0 + lane;
+        if ((!shared || warp == 0) && tok < q.kv) {
+            const float had = a.w.in == nullptr ? 0.0f : a.w.in[r * a.w.in_request_stride + h * a.w.in_head_stride + tok];
+            a.w.out[r * a.w.out_request_stride + h * a.w.out_head_stride + tok] = had + mine;
+        }
     }
 }
 
-// The same from stored scores, a thread to a token.
+// The same from stored scores, four tokens to a thread.
 __global__ void __launch_bounds__(kThreads) k_weigh_apply(AttnArgs p, WeighArgs a)
 {
     constexpr int kEach = kApplyTokens / kThreads;
@@ -657,57 +1021,63 @@ __global__ void __launch_bounds__(kThreads) k_weigh_apply(AttnArgs p, WeighArgs 
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
         AttnRequest q;
         int r, h, t0;
-        if (!find_item(p, item, kApplyTokens, &items, &q, &r, &h, &t0))
+        if (!find_item(p, item, [](const AttnRequest &) { return kApplyTokens; }, &items, &q, &r, &h, &t0))
             return;
+        t0 += threadIdx.x;
         const float *in = a.w.in == nullptr ? nullptr : a.w.in + r * a.w.in_request_stride + h * a.w.in_head_stride;
         float *out = a.w.out + r * a.w.out_request_stride + h * a.w.out_head_stride;
-        const float *scores = a.scores + ((int64_t)r * p.heads + h) * a.rows * a.tokens;
-        const float2 *stats = a.stats + ((int64_t)h * a.slots + first_slot(p, r, q.row0)) * 8;
+        const float *scores = a.scores + ((int64_t)r * p.heads + h) * a.rows * a.tokens + t0;
+        const float4 *stats = reinterpret_cast<const float4 *>(a.stats + ((int64_t)h * a.slots + first_slot(p, r, q.row0)) * 8);
         // blobs that no row sees have no scores
         const int x_last = q.x0 + (q.rows > 0 ? (q.rows - 1) / p.ratio : 0);
         const int64_t low = p.a.window > 0 ? ((int64_t)q.x0 + 1 - p.a.window) / 16 * 16 : 0;
         const int64_t sinks = ((int64_t)p.a.sinks + 15) / 16 * 16;
-        float sum[kEach];
-#pragma unroll
-        for (int k = 0; k < kEach; ++k)
-            sum[k] = 0.0f;
-        for (int row = 0; row < q.rows; ++row) {
-            const float2 st = stats[row];
-#pragma unroll
-            for (int k = 0; k < kEach; ++k) {
-                const int tok = t0 + k * kThreads + threadIdx.x;
-                if (tok <= x_last && (tok >= low || tok < sinks))
-                    sum[k] = fmaf(exp2_fast(scores[(int64_t)row * a.tokens + tok] - st.x), st.y, sum[k]);
-            }
-        }
+        float had[kEach], sum[kEach];
+        bool seen[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
-            const int tok = t0 + k * kThreads + threadIdx.x;
-            if (tok < q.kv)
-                out[tok] = (in == nullptr ? 0.0f : in[tok]) + sum[k];
+            const int tok = t0 + k * kThreads;
+            seen[k] = tok <= x_last && (tok >= low || tok < sinks);
+            had[k] = in != nullptr && tok < q.kv ? in[tok] : 0.0f;
+            sum[k] = 0.0f;
         }
+        for (int row = 0; row < q.rows; row += 2) {
+            const float4 st = stats[row / 2];   // of two rows (a row that is not there: 0, 0)
+            float z[2][kEach];
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int k = 0; k < kEach; ++k)
+                    z[j][k] = seen[k] && row + j < q.rows ? scores[(int64_t)(row + j) * a.tokens + k * kThreads] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kEach; ++k)
+                sum[k] = fmaf(exp2_fast(z[1][k] - st.z), st.w, fmaf(exp2_fast(z[0][k] - st.x), st.y, sum[k]));
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            if (t0 + k * kThreads < q.kv)
+                out[t0 + k * kThreads] = had[k] + sum[k];
     }
 }
 
-template <typename B, int NT, bool kStored>
-cudaError_t launch(const AttnArgs &p, const WeighArgs &a, cudaStream_t s)
+template <int RU, typename Sh, typename B>
+cudaError_t launch(void (*kernel)(AttnArgs, WeighArgs), int per_sm, const AttnArgs &p, const WeighArgs &a, bool stored,
+                   cudaStream_t s)
 {
-    using Sh = StatShared<B, NT>;
     int sms = 0;
     cudaError_t err = attn_sm_count(&sms);
     if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(k_weigh_stats<B, NT, kStored>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   (int)sizeof(Sh));
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Sh));
     if (err != cudaSuccess)
         return err;
-    const int blocks = stat_blocks(NT) * sms < kMaxBlocks ? stat_blocks(NT) * sms : kMaxBlocks;
-    k_weigh_stats<B, NT, kStored><<<blocks, kThreads, sizeof(Sh), s>>>(p, a);
+    const int blocks = per_sm * sms < kMaxBlocks ? per_sm * sms : kMaxBlocks;
+    kernel<<<blocks, kThreads, sizeof(Sh), s>>>(p, a);
     err = cudaGetLastError();
     if (err == cudaSuccess)
-        err = launch_under(k_weigh_join<8 * NT>, dim3(blocks), kThreads, 0, s, p, blocks, a);
+        err = launch_under(k_weigh_join<RU>, dim3(blocks), kThreads, 0, s, p, blocks, a);
     if (err != cudaSuccess)
         return err;
-    if (kStored)
+    if (stored)
         return launch_under(k_weigh_apply, dim3(8 * sms), kThreads, 0, s, p, a);
     return launch_under(k_weigh_sums<B>, dim3(3 * sms), kThreads, 0, s, p, a);
 }
@@ -819,9 +1189,11 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
         using B = decltype(blob);
-        if (z.rows <= 8)
-            return z.stored ? launch<B, 1, true>(p, args, s) : launch<B, 1, false>(p, args, s);
-        return z.rows <= 16 ? launch<B, 2, false>(p, args, s) : launch<B, 4, false>(p, args, s);
+        if (z.stored)
+            return launch<8, FewShared<B>, B>(z.rows <= 4 ? k_weigh_few<B, 2> : k_weigh_few<B, 1>, kFewBlocks, p, args, true, s);
+        if (z.rows <= 16)
+            return launch<16, StatShared<B, 2>, B>(k_weigh_stats<B, 2>, stat_blocks(2), p, args, false, s);
+        return launch<32, StatShared<B, 4>, B>(k_weigh_stats<B, 4>, stat_blocks(4), p, args, false, s);
     });
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

@@ -16,7 +16,7 @@ namespace {
 
 constexpr int kRing = 8;           // blobs in a warp's ring
 constexpr int kItemTokens = 128;   // of a block in the second pass, 32 to a warp; or,
-constexpr int kManyRows = 128;     // from so many rows on, 32 to a block, whose warps share the rows
+constexpr int kManyRows = 512;     // from so many rows on, 32 to a block, whose warps share the rows
 constexpr int kApplyTokens = 512;  // of a block in the second pass over stored scores
 constexpr int kMaxBlocks = 640;    // of the first pass
 
@@ -38,6 +38,14 @@ struct WeighArgs {
 __device__ __forceinline__ int32_t first_slot(const AttnArgs &p, int r, int32_t row0)
 {
     return (int32_t)((int64_t)row0 * p.ratio / 8) + r;
+}
+
+// The lane, read once: kept, not read again wherever it is used.
+__device__ __forceinline__ int lane_once()
+{
+    int lane;
+    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
+    return lane;
 }
 
 // ------------------------------------------------------------------- scores
@@ -120,10 +128,10 @@ struct Keys {
 };
 
 template <typename B>
-__device__ __forceinline__ void load_keys(const uint8_t *blob, Keys<B> *to)
+__device__ __forceinline__ void load_keys(const uint8_t *blob, int lane, Keys<B> *to)
 {
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups;
-    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         uint32_t k[NW], par[NG];
@@ -173,26 +181,23 @@ __device__ __forceinline__ void scores_of(const Keys<B> &k, const Queries<B> (&q
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const float s = k.s[j][gi], mid = k.mid[j][gi], x0 = acc[nt][2 * j], x1 = acc[nt][2 * j + 1];
-                y[nt][j].x = gi ? fmaf(s, x0, y[nt][j].x) : s * x0;
-                y[nt][j].y = gi ? fmaf(s, x1, y[nt][j].y) : s * x1;
-                z[nt][j].x = gi ? fmaf(mid, q[nt].sq[gi].x, z[nt][j].x) : mid * q[nt].sq[0].x;
-                z[nt][j].y = gi ? fmaf(mid, q[nt].sq[gi].y, z[nt][j].y) : mid * q[nt].sq[0].y;
+                const float2 s = make_float2(k.s[j][gi], k.s[j][gi]), mid = make_float2(k.mid[j][gi], k.mid[j][gi]);
+                const float2 x = make_float2(acc[nt][2 * j], acc[nt][2 * j + 1]);
+                y[nt][j] = gi ? fma2(s, x, y[nt][j]) : make_float2(s.x * x.x, s.y * x.y);
+                z[nt][j] = gi ? fma2(mid, q[nt].sq[gi], z[nt][j]) : make_float2(mid.x * q[nt].sq[0].x, mid.y * q[nt].sq[0].y);
             }
     }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            z[nt][j].x = fmaf(y[nt][j].x, q[nt].rho.x, z[nt][j].x);
-            z[nt][j].y = fmaf(y[nt][j].y, q[nt].rho.y, z[nt][j].y);
+            z[nt][j] = fma2(y[nt][j], q[nt].rho, z[nt][j]);
         }
 }
 
 // Where not every token is seen by every row: -inf for those that are not. x: positions of the rows.
-__device__ __forceinline__ void hide(const AttnArgs &p, int tok, const int (&x)[2], int window, float2 (&z)[2])
+__device__ __forceinline__ void hide(const AttnArgs &p, int tok, int g, const int (&x)[2], int window, float2 (&z)[2])
 {
-    const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int at = tok + g + 8 * j;
@@ -243,13 +248,109 @@ __device__ __forceinline__ void tile_range(const Unit &u, const Tile &t, int war
     *e = b0 + (int)((int64_t)(b1 - b0) * (warp + 1) / kWarps);
 }
 
+// ------------------------------------------------------------------- copies
+
+// Where a warp stands in its block's piece: in shared memory, since it is looked at seldom and would
+// take a third of the registers.
+struct Stand {
+    Unit u;
+    Tile t;
+    int64_t pos;     // blobs of the piece up to the end of the unit
+    int32_t b, e;    // blobs of the tile that are left of the warp's stretch
+};
+
+// The warp's copies, HB blobs at a time and kStages of those ahead of it: 32 blobs are looked up at once,
+// one by each lane, which then issues its own blob's copy.
+template <typename B, int RU, int HB, int kStages>
+struct Feeder {
+    uint8_t (*ring)[HB][B::kVCodes];
+    uint64_t *full;                // barriers, HB arrivals each
+    Stand *at;
+    int32_t i, n;                  // blobs issued and looked up of the current 32
+    uint32_t off, ok;              // the lane's blob (in 128-byte units of the layer); valid lanes
+    uint32_t issued, ahead;        // steps issued; which blobs of the steps in flight are there
+
+    __device__ __forceinline__ void start(const AttnArgs &p, int64_t count, const Unit &u, int warp, int lane)
+    {
+        const Tile t = tile_of<RU>(p, u);
+        int b, e;
+        tile_range(u, t, warp, &b, &e);
+        if (lane == 0)
+            *at = {u, t, u.b1 - u.b0, b, e};
+        i = n = 0;
+        off = ok = issued = ahead = 0;
+        __syncwarp();
+        for (int k = 0; k < kStages; ++k)
+            feed(p, count, warp, lane);
+    }
+
+    __device__ __forceinline__ bool look(const AttnArgs &p, int64_t count, int warp, int lane)
+    {
+        int b = at->b, e = at->e;
+        if (b >= e) {
+            Unit u = at->u;
+            Tile t;
+            int64_t pos = at->pos;
+            do {
+                if (pos >= count)
+                    return false;
+                unit_next<RU>(p, count - pos, &u);
+                t = tile_of<RU>(p, u);
+                pos += u.b1 - u.b0;
+                tile_range(u, t, warp, &b, &e);
+            } while (b >= e);
+            __syncwarp();
+            if (lane == 0)
+                *at = {u, t, pos, b, e};
+            __syncwarp();
+        }
+        i = 0;
+        n = e - b < 32 ? e - b : 32;
+        int id = -1;
+        if (lane < n) {
+            const int bpp = p.page_tokens / 16, vb = b + lane, ab = vb < at->t.span.sink ? vb : vb + at->t.span.skip;
+            const int page = ab / bpp;
+            id = p.a.block_table[at->u.r * p.a.table_stride + page];
+            if ((unsigned)id >= (unsigned)p.num_pages)
+                int4_set_status(p.status, CG_ERR_CORRUPT);
+            off = (((uint32_t)id * p.heads + at->u.h) * bpp + (ab - page * bpp)) * (B::kBytes / 128);
+        }
+        ok = __ballot_sync(0xFFFFFFFFu, (unsigned)id < (unsigned)p.num_pages);
+        if (lane == 0)
+            at->b = b + n;
+        __syncwarp();
+        return true;
+    }
+
+    __device__ __forceinline__ void feed(const AttnArgs &p, int64_t count, int warp, int lane)
+    {
+        ahead >>= HB;
+        if (i >= n && !look(p, count, warp, lane))
+            return;
+        const int st = issued % kStages;
+        if ((unsigned)(lane - i) < (unsigned)HB) {
+            if (ok >> lane & 1) {
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_expect(&full[st], B::kVCodes);
+                bulk_copy(ring[st][lane - i], p.layer + (uint64_t)off * 128, B::kVCodes, &full[st]);
+            } else {
+                bar_arrive(&full[st]);
+            }
+        }
+        ahead |= (ok >> i & ((1u << HB) - 1)) << (HB * (kStages - 1));
+        i += HB;
+        ++issued;
+    }
+};
+
 // -------------------------------------------------------- maximum and sum
 
 template <typename B, int NT>
 struct StatShared {
-    uint8_t ring[kWarps][kRing][B::kVCodes];   // the K half of blobs
+    uint8_t ring[kWarps][kRing][1][B::kVCodes];   // the K half of blobs
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
     uint64_t full[kWarps][kRing];
+    Stand feed[kWarps], now[kWarps];
 };
 
 __device__ __forceinline__ float2 row_stats_of(float m, float l)
@@ -267,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
     constexpr int NW = B::kWords, NG = B::kGroups, RU = 8 * NT;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = lane_once(), warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
 
     grid_next();
@@ -281,68 +382,24 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
     if (begin >= total)
         return;
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
-    const int bpp = p.page_tokens / 16;
-    // ---- the warp's copies, some blobs ahead of it: 32 are looked up at once, one by each lane,
-    // which then issues its own blob's copy
     Unit first;
     unit_at<RU>(p, at, count, &first);
-    Unit fu = first;
-    Tile ft = tile_of<RU>(p, fu);
-    int64_t f_pos = fu.b1 - fu.b0;
-    int f_b, f_e, f_i = 0, f_n = 0;
-    tile_range(fu, ft, warp, &f_b, &f_e);
-    uint32_t f_off = 0, f_ok = 0, issued = 0, ahead = 0;
-    auto feed = [&]() {
-        ahead >>= 1;
-        if (f_i >= f_n) {
-            while (f_b >= f_e) {
-                if (f_pos >= count)
-                    return;
-                unit_next<RU>(p, count - f_pos, &fu);
-                ft = tile_of<RU>(p, fu);
-                f_pos += fu.b1 - fu.b0;
-                tile_range(fu, ft, warp, &f_b, &f_e);
-            }
-            f_i = 0;
-            f_n = f_e - f_b < 32 ? f_e - f_b : 32;
-            int id = -1;
-            if (lane < f_n) {
-                const int vb = f_b + lane, ab = vb < ft.span.sink ? vb : vb + ft.span.skip;
-                const int page = ab / bpp;
-                id = p.a.block_table[fu.r * p.a.table_stride + page];
-                if ((unsigned)id >= (unsigned)p.num_pages)
-                    int4_set_status(p.status, CG_ERR_CORRUPT);
-                f_off = (((uint32_t)id * p.heads + fu.h) * bpp + (ab - page * bpp)) * (B::kBytes / 128);
-            }
-            f_ok = __ballot_sync(0xFFFFFFFFu, (unsigned)id < (unsigned)p.num_pages);
-            f_b += f_n;
-        }
-        const int st = issued % kRing;
-        if (lane == f_i) {
-            uint64_t *bar = &sm.full[warp][st];
-            if (f_ok >> lane & 1) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                bar_expect(bar, B::kVCodes);
-                bulk_copy(sm.ring[warp][st], p.layer + (uint64_t)f_off * 128, B::kVCodes, bar);
-            } else {
-                bar_arrive(bar);
-            }
-        }
-        ahead |= (f_ok >> f_i & 1) << (kRing - 1);
-        ++f_i;
-        ++issued;
-    };
+    Feeder<B, RU, 1, kRing> feeder;
+    feeder.ring = sm.ring[warp];
+    feeder.full = sm.full[warp];
+    feeder.at = &sm.feed[warp];
+    feeder.start(p, count, first, warp, lane);
+    Stand &now = sm.now[warp];
+    if (lane == 0)
+        now = {first, tile_of<RU>(p, first), 0, 0, 0};
     __syncwarp();
-    for (int i = 0; i < kRing; ++i)
-        feed();
 
     const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
     bool alive = true;               // no wait has run out
     uint32_t used = 0;
-    Unit u = first;
-    int64_t pos = 0;
     for (;;) {
-        const Tile tile = tile_of<RU>(p, u);
+        const Unit u = now.u;
+        const Tile tile = now.t;
         const int slot = first_slot(p, u.r, u.q.row0) + tile.row0 / 8;
         Queries<B> q[NT];
         int x[NT][2];
@@ -391,9 +448,9 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
                     ++used;
                 }
             }
-            if (alive && (ahead & 1)) {
+            if (alive && (feeder.ahead & 1)) {
                 Keys<B> k;
-                load_keys<B>(sm.ring[warp][st], &k);
+                load_keys<B>(sm.ring[warp][st][0], lane, &k);
                 const int tok = 16 * (b < tile.span.sink ? b : b + tile.span.skip);
                 const bool whole = tok + 15 <= tile.x_lo && (tile.x_hi - tok < window || tok + 15 < p.a.sinks);
                 float2 z[NT][2];
@@ -401,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
                 if (!whole)
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        hide(p, tok, x[nt], window, z[nt]);
+                        hide(p, tok, g, x[nt], window, z[nt]);
                 // raised only when a score exceeds it by 2^8
                 float over = -INFINITY;
 #pragma unroll
@@ -427,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
             }
             __syncwarp();   // every lane has read the place
             if (alive)
-                feed();
+                feeder.feed(p, count, warp, lane);
         }
         // ---- joined over the lanes of a row, the warps, and with other pieces in a second kernel
 #pragma unroll
@@ -447,31 +504,37 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
                 }
             }
         __syncthreads();
-        const bool from_before = u.b0 > 0, goes_on = u.b1 < u.span.nb;
-        if (tid < RU) {
+        Unit end = now.u;
+        const bool from_before = end.b0 > 0, goes_on = end.b1 < end.span.nb;
+        if (threadIdx.x < RU) {
+            const int row = threadIdx.x, rows = now.t.rows;
             float mx = kNone, ls = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                mx = fmaxf(mx, sm.m[w][tid]);
+                mx = fmaxf(mx, sm.m[w][row]);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w)
-                ls += sm.l[w][tid] * exp2_fast(sm.m[w][tid] - mx);
-            if (tid >= tile.rows)
+                ls += sm.l[w][row] * exp2_fast(sm.m[w][row] - mx);
+            if (row >= rows)
                 ls = 0.0f;
             if (from_before || goes_on)
-                a.parts[((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * RU + tid] = make_float2(mx, ls);
-            else if (tid < (tile.rows + 7) / 8 * 8)
-                a.stats[((int64_t)u.h * a.slots + slot) * 8 + tid] = row_stats_of(mx, ls);
+                a.parts[((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * RU + row] = make_float2(mx, ls);
+            else if (row < (rows + 7) / 8 * 8)
+                a.stats[((int64_t)end.h * a.slots + first_slot(p, end.r, end.q.row0) + now.t.row0 / 8) * 8 + row] =
+                    row_stats_of(mx, ls);
         }
+        const int64_t pos = now.pos + end.b1 - end.b0;
         __syncthreads();
-        pos += u.b1 - u.b0;
         if (pos >= count)
             break;
-        unit_next<RU>(p, count - pos, &u);
+        unit_next<RU>(p, count - pos, &end);
+        if (lane == 0)
+            now = {end, tile_of<RU>(p, end), pos, 0, 0};
+        __syncwarp();
     }
     // a wait that ran out: the copies still in flight must land before the block's memory goes
     if (!alive)
-        for (; used < issued; ++used)
+        for (; used < feeder.issued; ++used)
             bar_wait(&sm.full[warp][used % kRing], (used / kRing) & 1);
 }
 
@@ -552,10 +615,10 @@ __device__ __forceinline__ void load_few(const AttnArgs &p, const AttnRequest &r
 // z[j]: token g + 8 j with rows 2t and 2t + 1 (of their blob). `par`: the lane's blob, for its parameters.
 template <typename B, int P>
 __device__ __forceinline__ void few_scores(const uint8_t *const (&blob)[P], const uint8_t *par, const FewQueries<B, P> &q,
-                                           float2 (&z)[2])
+                                           int lane, float2 (&z)[2])
 {
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
-    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const int g = lane >> 2, t = lane & 3;
     uint32_t k[P][2][NW];
 #pragma unroll
     for (int b = 0; b < P; ++b)
@@ -609,6 +672,7 @@ struct FewShared {
     uint8_t ring[kWarps][kPairs][2][B::kVCodes];
     float m[kWarps][8], l[kWarps][8];
     uint64_t full[kWarps][kPairs];
+    Stand feed[kWarps], now[kWarps];
 };
 
 template <typename B, int P>
@@ -617,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
     using S = FewShared<B>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int lane = lane_once(), warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
 
     grid_next();
@@ -631,68 +695,26 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
     if (begin >= total)
         return;
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
-    const int bpp = p.page_tokens / 16;
     Unit first;
     unit_at<8>(p, at, count, &first);
-    Unit fu = first;
-    Tile ft = tile_of<8>(p, fu);
-    int64_t f_pos = fu.b1 - fu.b0;
-    int f_b, f_e, f_i = 0, f_n = 0;
-    tile_range(fu, ft, warp, &f_b, &f_e);
-    uint32_t f_off = 0, f_ok = 0, issued = 0, ahead = 0;
-    auto feed = [&]() {
-        ahead >>= 2;
-        if (f_i >= f_n) {
-            while (f_b >= f_e) {
-                if (f_pos >= count)
-                    return;
-                unit_next<8>(p, count - f_pos, &fu);
-                ft = tile_of<8>(p, fu);
-                f_pos += fu.b1 - fu.b0;
-                tile_range(fu, ft, warp, &f_b, &f_e);
-            }
-            f_i = 0;
-            f_n = f_e - f_b < 32 ? f_e - f_b : 32;
-            int id = -1;
-            if (lane < f_n) {
-                const int vb = f_b + lane, ab = vb < ft.span.sink ? vb : vb + ft.span.skip;
-                const int page = ab / bpp;
-                id = p.a.block_table[fu.r * p.a.table_stride + page];
-                if ((unsigned)id >= (unsigned)p.num_pages)
-                    int4_set_status(p.status, CG_ERR_CORRUPT);
-                f_off = (((uint32_t)id * p.heads + fu.h) * bpp + (ab - page * bpp)) * (B::kBytes / 128);
-            }
-            f_ok = __ballot_sync(0xFFFFFFFFu, (unsigned)id < (unsigned)p.num_pages);
-            f_b += f_n;
-        }
-        const int st = issued % kPairs;
-        if ((unsigned)(lane - f_i) < 2u) {
-            uint64_t *bar = &sm.full[warp][st];
-            if (f_ok >> lane & 1) {
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                bar_expect(bar, B::kVCodes);
-                bulk_copy(sm.ring[warp][st][lane - f_i], p.layer + (uint64_t)f_off * 128, B::kVCodes, bar);
-            } else {
-                bar_arrive(bar);
-            }
-        }
-        ahead |= (f_ok >> f_i & 3) << (2 * (kPairs - 1));
-        f_i += 2;
-        ++issued;
-    };
+    Feeder<B, 8, 2, kPairs> feeder;
+    feeder.ring = sm.ring[warp];
+    feeder.full = sm.full[warp];
+    feeder.at = &sm.feed[warp];
+    feeder.start(p, count, first, warp, lane);
+    Stand &now = sm.now[warp];
+    if (lane == 0)
+        now = {first, tile_of<8>(p, first), 0, 0, 0};
     __syncwarp();
-    for (int i = 0; i < kPairs; ++i)
-        feed();
 
     const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
     const int side = P == 2 ? t >> 1 : 0;            // which blob of a pair the lane's columns are of
     const int row = P == 2 ? 2 * (t & 1) : 2 * t;    // the first of the lane's two rows
     bool alive = true;               // no wait has run out
     uint32_t used = 0;
-    Unit u = first;
-    int64_t pos = 0;
     for (;;) {
-        const Tile tile = tile_of<8>(p, u);
+        const Unit u = now.u;
+        const Tile tile = now.t;
         FewQueries<B, P> q;
         load_few<B, P>(p, u.q, u.h, &q);
         const int x[2] = {row < tile.rows ? u.q.x0 + row / p.ratio : -1, row + 1 < tile.rows ? u.q.x0 + (row + 1) / p.ratio : -1};
@@ -703,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
         // what the lane's rows make of two scores each
         auto take = [&](float2 (&z)[2], int tok, bool whole, bool there, bool valid) {
             if (!whole)
-                hide(p, tok, x, window, z);
+                hide(p, tok, g, x, window, z);
             if (!there)
                 z[0] = z[1] = make_float2(-INFINITY, -INFINITY);
             if (valid && has[0]) {
@@ -749,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
                     const int tok = token(b + side);
                     const bool whole = all_see(token(b)) && all_see(token(b + 1));
                     float2 z[2];
-                    few_scores<B, P>(blobs, ring[side], q, z);
-                    take(z, tok, whole, ahead >> side & 1, b + side < e);
+                    few_scores<B, P>(blobs, ring[side], q, lane, z);
+                    take(z, tok, whole, feeder.ahead >> side & 1, b + side < e);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
@@ -758,14 +780,14 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
                             break;
                         const uint8_t *const blobs[P] = {ring[i]};
                         float2 z[2];
-                        few_scores<B, P>(blobs, ring[i], q, z);
-                        take(z, token(b + i), all_see(token(b + i)), ahead >> i & 1, true);
+                        few_scores<B, P>(blobs, ring[i], q, lane, z);
+                        take(z, token(b + i), all_see(token(b + i)), feeder.ahead >> i & 1, true);
                     }
                 }
             }
             __syncwarp();   // every lane has read the place
             if (alive)
-                feed();
+                feeder.feed(p, count, warp, lane);
         }
         // ---- joined over the lanes of a row, the warps, and with other pieces in a second kernel
 #pragma unroll
@@ -784,31 +806,36 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
             sm.l[warp][row + 1] = l.y;
         }
         __syncthreads();
-        const bool from_before = u.b0 > 0, goes_on = u.b1 < u.span.nb;
-        if (tid < 8) {
+        Unit end = now.u;
+        const bool from_before = end.b0 > 0, goes_on = end.b1 < end.span.nb;
+        if (threadIdx.x < 8) {
+            const int i = threadIdx.x;
             float mx = kNone, ls = 0.0f;
-            if (tid < tile.rows) {
+            if (i < now.t.rows) {
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    mx = fmaxf(mx, sm.m[w][tid]);
+                    mx = fmaxf(mx, sm.m[w][i]);
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w)
-                    ls += sm.l[w][tid] * exp2_fast(sm.m[w][tid] - mx);
+                    ls += sm.l[w][i] * exp2_fast(sm.m[w][i] - mx);
             }
             if (from_before || goes_on)
-                a.parts[((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * 8 + tid] = make_float2(mx, ls);
+                a.parts[((int64_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * 8 + i] = make_float2(mx, ls);
             else
-                a.stats[((int64_t)u.h * a.slots + first_slot(p, u.r, u.q.row0)) * 8 + tid] = row_stats_of(mx, ls);
+                a.stats[((int64_t)end.h * a.slots + first_slot(p, end.r, end.q.row0)) * 8 + i] = row_stats_of(mx, ls);
         }
+        const int64_t pos = now.pos + end.b1 - end.b0;
         __syncthreads();
-        pos += u.b1 - u.b0;
         if (pos >= count)
             break;
-        unit_next<8>(p, count - pos, &u);
+        unit_next<8>(p, count - pos, &end);
+        if (lane == 0)
+            now = {end, tile_of<8>(p, end), pos, 0, 0};
+        __syncwarp();
     }
     // a wait that ran out: the copies still in flight must land before the block's memory goes
     if (!alive)
-        for (; used < issued; ++used)
+        for (; used < feeder.issued; ++used)
             bar_wait(&sm.full[warp][used % kPairs], (used / kPairs) & 1);
 }
 
@@ -906,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
 {
     constexpr int NW = B::kWords, NG = B::kGroups;
     __shared__ float parts[kWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
+    const int lane = lane_once(), warp = threadIdx.x >> 5, t = lane & 3;
     const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
     const int bpp = p.page_tokens / 16;
     grid_wait();
@@ -934,7 +961,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
                 int4_set_status(p.status, CG_ERR_CORRUPT);
             // (a blob behind the last token is the one before it again: its sums are not written)
             const uint64_t blob = there[b] ? ((uint64_t)id * p.heads + h) * bpp + (tok - page * p.page_tokens) / 16 : 0;
-            load_keys<B>(p.layer + blob * B::kBytes, &keys[b]);
+            load_keys<B>(p.layer + blob * B::kBytes, lane, &keys[b]);
         }
         // ---- rows that see any of the tokens
         const int64_t lo = min((int64_t)max(0, t0 - q.x0) * p.ratio, (int64_t)q.rows);
@@ -943,34 +970,54 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
             hi = min(hi, ((int64_t)t0 + 31 + window - q.x0) * p.ratio);
         const int step = shared ? kWarps : 1, i0 = (int)(lo / 8) + (shared ? warp : 0);
         const int i1 = hi < 0 ? 0 : (int)((hi + 7) / 8);
-        const int64_t slot = (int64_t)h * a.slots + first_slot(p, r, q.row0);
+        const int64_t slot = (int64_t)h * a.slots + first_slot(p, r, q.row0) + i0;
+        const uint4 *from = a.queries + slot * NW * 32 + lane;
+        const float2 *factors = reinterpret_cast<const float2 *>(a.factors + slot * (NG + 1) * 8) + t;
+        const float4 *stats = reinterpret_cast<const float4 *>(a.stats + slot * 8 + 2 * t);
+        // Whether a row sees a token goes by rows: position x0 + row / ratio is at least x from row
+        // (x - x0) ratio on. All 8 rows of a tile see a whole blob from row `from_row` on, up to `to_row`.
+        auto row_of = [&](int64_t x) {   // (a tile's rows end at 2^31 - 8 at most)
+            return (int)max(min((x - q.x0) * p.ratio, (int64_t)INT32_MAX), (int64_t)-1);
+        };
+        int from_row[2], to_row[2];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const int64_t tok = t0 + 16 * b;
+            from_row[b] = row_of(tok + 15);
+            to_row[b] = p.a.window == 0 || tok + 15 < p.a.sinks ? INT32_MAX : row_of(tok + window);
+        }
         float total[2][2] = {}, sum[2][2] = {};
         int count = 0;
         for (int i = i0; i < i1; i += step) {
             Queries<B> rows[1];
-            const uint4 *from = a.queries + (slot + i) * NW * 32 + lane;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const uint4 v = from[32 * w];
                 rows[0].qf[w][0] = v.x, rows[0].qf[w][1] = v.y, rows[0].qf[w][2] = v.z, rows[0].qf[w][3] = v.w;
             }
-            const float2 *f = reinterpret_cast<const float2 *>(a.factors + (slot + i) * (NG + 1) * 8) + t;
-            rows[0].rho = f[0];
+            rows[0].rho = factors[0];
 #pragma unroll
             for (int k = 0; k < NG; ++k)
-                rows[0].sq[k] = f[4 * (k + 1)];
-            const float4 st = *reinterpret_cast<const float4 *>(a.stats + (slot + i) * 8 + 2 * t);
-            const int x_lo = q.x0 + 8 * i / p.ratio, x_hi = q.x0 + min(8 * i + 7, q.rows - 1) / p.ratio;
+                rows[0].sq[k] = factors[4 * (k + 1)];
+            const float4 st = *stats;
+            from += step * NW * 32;
+            factors += step * (NG + 1) * 4;
+            stats += step * 4;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
-                const int tok = t0 + 16 * b;
                 float2 z[1][2];
                 scores_of<B, 1>(keys[b], rows, z);
-                if (!(tok + 15 <= x_lo && (x_hi - tok < window || tok + 15 < p.a.sinks))) {
+                if (8 * i < from_row[b] || 8 * i + 7 >= to_row[b]) {
                     const int row = 8 * i + 2 * t;
-                    const int x[2] = {row < q.rows ? q.x0 + row / p.ratio : -1,
-                                      row + 1 < q.rows ? q.x0 + (row + 1) / p.ratio : -1};
-                    hide(p, tok, x, window, z[0]);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int64_t tok = t0 + 16 * b + 8 * j + (lane >> 2);
+                        const int first = row_of(tok), end = p.a.window == 0 || tok < p.a.sinks ? INT32_MAX : row_of(tok + window);
+                        if (row < first || row >= end)
+                            z[0][j].x = -INFINITY;
+                        if (row + 1 < first || row + 1 >= end)
+                            z[0][j].y = -INFINITY;
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < 2; ++j)

@@ -15,8 +15,8 @@
 namespace {
 
 constexpr int kRing = 8;           // blobs in a warp's ring
-constexpr int kItemTokens = 128;   // of a block in the second pass, 32 to a warp; or,
-constexpr int kManyRows = 512;     // from so many rows on, 32 to a block, whose warps share the rows
+constexpr int kItemTokens = 64;    // of a block in the second pass, a blob to a warp; or,
+constexpr int kManyRows = 512;     // from so many rows on, a blob to a block, whose warps share the rows
 constexpr int kApplyTokens = 512;  // of a block in the second pass over stored scores
 constexpr int kMaxBlocks = 640;    // of the first pass
 
@@ -159,40 +159,32 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t *a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Scores in powers of two of NT row tiles: z[nt][j] are token g + 8 j's with rows 2t and 2t + 1.
-template <typename B, int NT>
-__device__ __forceinline__ void scores_of(const Keys<B> &k, const Queries<B> (&q)[NT], float2 (&z)[NT][2])
+// Scores in powers of two, less m, of a row tile: z[j] are token g + 8 j with rows 2t and 2t + 1.
+template <typename B>
+__device__ __forceinline__ void scores_of(const Keys<B> &k, const Queries<B> &q, float2 m, float2 (&z)[2])
 {
     constexpr int NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
     const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float2 y[NT][2];
+    float2 y[2];
 #pragma unroll
     for (int gi = 0; gi < NG; ++gi) {
-        float acc[NT][4];
+        float acc[4];
 #pragma unroll
         for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
 #pragma unroll
             for (int i = 0; i < 4; i += 2)
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma(acc[nt], &k.a[w][2 * i], q[nt].qf[w][i], q[nt].qf[w][i + 1],
-                        w == gi * WPG && i == 0 ? zero : acc[nt]);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 s = make_float2(k.s[j][gi], k.s[j][gi]), mid = make_float2(k.mid[j][gi], k.mid[j][gi]);
-                const float2 x = make_float2(acc[nt][2 * j], acc[nt][2 * j + 1]);
-                y[nt][j] = gi ? fma2(s, x, y[nt][j]) : make_float2(s.x * x.x, s.y * x.y);
-                z[nt][j] = gi ? fma2(mid, q[nt].sq[gi], z[nt][j]) : make_float2(mid.x * q[nt].sq[0].x, mid.y * q[nt].sq[0].y);
-            }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+                mma(acc, &k.a[w][2 * i], q.qf[w][i], q.qf[w][i + 1], w == gi * WPG && i == 0 ? zero : acc);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            z[nt][j] = fma2(y[nt][j], q[nt].rho, z[nt][j]);
+            const float2 s = make_float2(k.s[j][gi], k.s[j][gi]), mid = make_float2(k.mid[j][gi], k.mid[j][gi]);
+            const float2 x = make_float2(acc[2 * j], acc[2 * j + 1]);
+            y[j] = gi ? fma2(s, x, y[j]) : mul2(s, x);
+            z[j] = fma2(mid, q.sq[gi], gi ? z[j] : make_float2(-m.x, -m.y));
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+        z[j] = fma2(y[j], q.rho, z[j]);
 }
 
 // Where not every token is seen by every row: -inf for those that are not. x: positions of the rows.
@@ -348,6 +340,8 @@ struct Feeder {
 template <typename B, int NT>
 struct StatShared {
     uint8_t ring[kWarps][kRing][1][B::kVCodes];   // the K half of blobs
+    uint4 qf[NT][B::kWords][32];                  // the rows' second factors, as the lanes have them
+    float2 factors[NT][B::kGroups + 1][4];        // rho, sq
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
     uint64_t full[kWarps][kRing];
     Stand feed[kWarps], now[kWarps];
@@ -359,10 +353,10 @@ __device__ __forceinline__ float2 row_stats_of(float m, float l)
 }
 
 // Blocks on an SM.
-constexpr int stat_blocks(int NT) { return NT == 2 ? 3 : 2; }
+constexpr int kStatBlocks = 4;
 
 template <typename B, int NT>
-__global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnArgs p, WeighArgs a)
+__global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs p, WeighArgs a)
 {
     using S = StatShared<B, NT>;
     constexpr int NW = B::kWords, NG = B::kGroups, RU = 8 * NT;
@@ -401,40 +395,48 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
         const Unit u = now.u;
         const Tile tile = now.t;
         const int slot = first_slot(p, u.r, u.q.row0) + tile.row0 / 8;
-        Queries<B> q[NT];
+        // a warp to a tile of 8 rows; the unit's first piece leaves them for the sums too
+        if (warp < NT && 8 * warp < tile.rows) {
+            Queries<B> q;
+            load_rows<B>(p, u.q, u.h, tile.row0 + 8 * warp, &q);
+            const int64_t at_slot = (int64_t)u.h * a.slots + slot + warp;
+            uint4 *to = a.queries + at_slot * NW * 32 + lane;
+            float2 *f = reinterpret_cast<float2 *>(a.factors + at_slot * (NG + 1) * 8) + t;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) {
+                sm.qf[warp][w][lane] = make_uint4(q.qf[w][0], q.qf[w][1], q.qf[w][2], q.qf[w][3]);
+                if (u.b0 == 0)
+                    to[32 * w] = sm.qf[warp][w][lane];
+            }
+            if (g == 0) {
+#pragma unroll
+                for (int i = 0; i <= NG; ++i) {
+                    sm.factors[warp][i][t] = i ? q.sq[i ? i - 1 : 0] : q.rho;
+                    if (u.b0 == 0)
+                        f[4 * i] = sm.factors[warp][i][t];
+                }
+            }
+        }
+        __syncthreads();
         int x[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            load_rows<B>(p, u.q, u.h, tile.row0 + 8 * nt, &q[nt]);
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int in = 8 * nt + 2 * t + j;
                 x[nt][j] = in < tile.rows ? u.q.x0 + (tile.row0 + in) / p.ratio : -1;
             }
-            if (u.b0 == 0 && warp == 0 && 8 * nt < tile.rows) {   // by the unit's first piece, for the sums
-                const int64_t at_slot = (int64_t)u.h * a.slots + slot + nt;
-                uint4 *to = a.queries + at_slot * NW * 32 + lane;
+        const int tiles = (tile.rows + 7) / 8;
+        // Each lane keeps a maximum (0 before the first score) and a sum of its own, over tokens g and g + 8
+        // of the blobs. The maximum is set by a row's first score, and raised only when a score exceeds it by
+        // 2^8: `limit` is below every score while a row of the lane waits for its first.
+        float2 m[NT], l[NT];
+        float limit[NT];
 #pragma unroll
-                for (int w = 0; w < NW; ++w)
-                    to[32 * w] = make_uint4(q[nt].qf[w][0], q[nt].qf[w][1], q[nt].qf[w][2], q[nt].qf[w][3]);
-                if (g == 0) {
-                    float2 *f = reinterpret_cast<float2 *>(a.factors + at_slot * (NG + 1) * 8) + t;
-                    f[0] = q[nt].rho;
-#pragma unroll
-                    for (int i = 0; i < NG; ++i)
-                        f[4 * (i + 1)] = q[nt].sq[i];
-                }
-            }
+        for (int nt = 0; nt < NT; ++nt) {
+            m[nt] = l[nt] = make_float2(0.0f, 0.0f);
+            limit[nt] = kNone;
         }
-        // each lane keeps a maximum and a sum of its own, over tokens g and g + 8 of the blobs
-        float m[NT][2], l[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                m[nt][j] = kNone;
-                l[nt][j] = 0.0f;
-            }
         int b, e;
         tile_range(u, tile, warp, &b, &e);
         for (; b < e; ++b) {
@@ -453,33 +455,46 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
                 load_keys<B>(sm.ring[warp][st][0], lane, &k);
                 const int tok = 16 * (b < tile.span.sink ? b : b + tile.span.skip);
                 const bool whole = tok + 15 <= tile.x_lo && (tile.x_hi - tok < window || tok + 15 < p.a.sinks);
-                float2 z[NT][2];
-                scores_of<B, NT>(k, q, z);
-                if (!whole)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        hide(p, tok, g, x[nt], window, z[nt]);
-                // raised only when a score exceeds it by 2^8
-                float over = -INFINITY;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    over = fmaxf(fmaxf(over, fmaxf(z[nt][0].x, z[nt][1].x) - m[nt][0]),
-                                 fmaxf(z[nt][0].y, z[nt][1].y) - m[nt][1]);
-                if (over > 8.0f) {
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        const float m0 = fmaxf(m[nt][0], fmaxf(z[nt][0].x, z[nt][1].x));
-                        const float m1 = fmaxf(m[nt][1], fmaxf(z[nt][0].y, z[nt][1].y));
-                        l[nt][0] *= exp2_fast(m[nt][0] - m0);
-                        l[nt][1] *= exp2_fast(m[nt][1] - m1);
-                        m[nt][0] = m0;
-                        m[nt][1] = m1;
-                    }
-                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    l[nt][0] += exp2_fast(z[nt][0].x - m[nt][0]) + exp2_fast(z[nt][1].x - m[nt][0]);
-                    l[nt][1] += exp2_fast(z[nt][0].y - m[nt][1]) + exp2_fast(z[nt][1].y - m[nt][1]);
+                    if (nt >= tiles)
+                        break;
+                    Queries<B> q;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) {
+                        const uint4 v = sm.qf[nt][w][lane];
+                        q.qf[w][0] = v.x, q.qf[w][1] = v.y, q.qf[w][2] = v.z, q.qf[w][3] = v.w;
+                    }
+                    q.rho = sm.factors[nt][0][t];
+#pragma unroll
+                    for (int i = 0; i < NG; ++i)
+                        q.sq[i] = sm.factors[nt][i + 1][t];
+                    float2 z[2];
+                    scores_of<B>(k, q, m[nt], z);
+                    if (!whole)
+                        hide(p, tok, g, x[nt], window, z);
+                    const float2 top = make_float2(fmaxf(z[0].x, z[1].x), fmaxf(z[0].y, z[1].y));
+                    if (fmaxf(top.x, top.y) > limit[nt]) {
+                        const bool none_x = l[nt].x == 0.0f, none_y = l[nt].y == 0.0f;
+                        const float up_x = none_x ? fmaxf(top.x, kNone) : fmaxf(top.x, 0.0f);
+                        const float up_y = none_y ? fmaxf(top.y, kNone) : fmaxf(top.y, 0.0f);
+                        if (up_x > kNone) {
+                            m[nt].x += up_x;
+                            l[nt].x = none_x ? 0.0f : l[nt].x * exp2_fast(-up_x);
+                            z[0].x -= up_x;
+                            z[1].x -= up_x;
+                        }
+                        if (up_y > kNone) {
+                            m[nt].y += up_y;
+                            l[nt].y = none_y ? 0.0f : l[nt].y * exp2_fast(-up_y);
+                            z[0].y -= up_y;
+                            z[1].y -= up_y;
+                        }
+                        if ((up_x > kNone || x[nt][0] < 0) && (up_y > kNone || x[nt][1] < 0))
+                            limit[nt] = 8.0f;
+                    }
+                    l[nt].x += exp2_fast(z[0].x) + exp2_fast(z[1].x);
+                    l[nt].y += exp2_fast(z[0].y) + exp2_fast(z[1].y);
                 }
             }
             __syncwarp();   // every lane has read the place
@@ -491,16 +506,17 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
+                float lj = j ? l[nt].y : l[nt].x, mj = lj == 0.0f ? kNone : j ? m[nt].y : m[nt].x;
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) {
-                    const float om = __shfl_xor_sync(0xFFFFFFFFu, m[nt][j], d);
-                    const float ol = __shfl_xor_sync(0xFFFFFFFFu, l[nt][j], d), mx = fmaxf(m[nt][j], om);
-                    l[nt][j] = l[nt][j] * exp2_fast(m[nt][j] - mx) + ol * exp2_fast(om - mx);
-                    m[nt][j] = mx;
+                    const float om = __shfl_xor_sync(0xFFFFFFFFu, mj, d);
+                    const float ol = __shfl_xor_sync(0xFFFFFFFFu, lj, d), mx = fmaxf(mj, om);
+                    lj = lj * exp2_fast(mj - mx) + ol * exp2_fast(om - mx);
+                    mj = mx;
                 }
                 if (g == 0) {
-                    sm.m[warp][8 * nt + 2 * t + j] = m[nt][j];
-                    sm.l[warp][8 * nt + 2 * t + j] = l[nt][j];
+                    sm.m[warp][8 * nt + 2 * t + j] = mj;
+                    sm.l[warp][8 * nt + 2 * t + j] = lj;
                 }
             }
         __syncthreads();
@@ -542,11 +558,11 @@ __global__ void __launch_bounds__(kThreads, stat_blocks(NT)) k_weigh_stats(AttnA
 
 // Half the words' instructions: a code enters as a bf16 whose bits are the code's, n 2^-133 or, for the
 // upper codes, n 2^-129 (against 1/16 of the query), and 8 times the sum of the queries comes off where the
-// products are summed, in each instruction by its own accumulator, so that no rounding comes between.
+// products of a group are summed: its accumulator begins with that.
 template <typename B, int P>
 struct FewQueries {
     uint32_t qf[P][B::kWords][4];
-    float2 off[B::kWords][2];        // -8 sum q of an instruction's 16 channels, as it counts them
+    float2 off[B::kGroups];          // -8 sum q of a group, as the products count them
     float2 rho, sq[B::kGroups];
 };
 
@@ -594,20 +610,15 @@ __device__ __forceinline__ void load_few(const AttnArgs &p, const AttnRequest &r
             if (P == 2)
                 to->qf[P - 1][w][i] = g >= 4 ? f[i] : 0;
         }
-        float half[2] = {(par_s(c.x) + par_s(c.z)) + (par_lo(c.x) + par_lo(c.z)),
-                         (par_s(c.y) + par_s(c.w)) + (par_lo(c.y) + par_lo(c.w))};
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            half[i] += __shfl_xor_sync(0xFFFFFFFFu, half[i], 1);
-            half[i] += __shfl_xor_sync(0xFFFFFFFFu, half[i], 2);
-            const float off = half[i] * o0 * o1;
-            to->off[w][i] = make_float2(__shfl_sync(0xFFFFFFFFu, off, 8 * t), __shfl_sync(0xFFFFFFFFu, off, 8 * t + 4));
-        }
-        sum[w / WPG] += half[0] + half[1];
+        sum[w / WPG] += ((par_s(c.x) + par_s(c.z)) + (par_lo(c.x) + par_lo(c.z))) +
+                        ((par_s(c.y) + par_s(c.w)) + (par_lo(c.y) + par_lo(c.w)));
     }
 #pragma unroll
     for (int i = 0; i < NG; ++i) {
-        const float mine = p.scale2 * sum[i];
+        sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 1);
+        sum[i] += __shfl_xor_sync(0xFFFFFFFFu, sum[i], 2);
+        const float off = sum[i] * o0 * o1, mine = p.scale2 * sum[i];
+        to->off[i] = make_float2(__shfl_sync(0xFFFFFFFFu, off, 8 * t), __shfl_sync(0xFFFFFFFFu, off, 8 * t + 4));
         to->sq[i] = make_float2(__shfl_sync(0xFFFFFFFFu, mine, 8 * t), __shfl_sync(0xFFFFFFFFu, mine, 8 * t + 4));
     }
 }
@@ -632,36 +643,28 @@ __device__ __forceinline__ void few_scores(const uint8_t *const (&blob)[P], cons
     float2 y[2];
 #pragma unroll
     for (int gi = 0; gi < NG; ++gi) {
-        float x[4] = {};
+        float x[4] = {q.off[gi].x, q.off[gi].y, q.off[gi].x, q.off[gi].y};
 #pragma unroll
-        for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
+        for (int b = 0; b < P; ++b)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                float acc[4] = {q.off[w][i].x, q.off[w][i].y, q.off[w][i].x, q.off[w][i].y};
+            for (int w = gi * WPG; w < (gi + 1) * WPG; ++w)
 #pragma unroll
-                for (int b = 0; b < P; ++b) {
-                    const uint32_t a[4] = {codes_of(k[b][0][w], 2 * i), codes_of(k[b][1][w], 2 * i),
-                                           codes_of(k[b][0][w], 2 * i + 1), codes_of(k[b][1][w], 2 * i + 1)};
-                    mma(acc, a, q.qf[b][w][2 * i], q.qf[b][w][2 * i + 1], acc);
+                for (int i = 0; i < 4; i += 2) {
+                    const uint32_t a[4] = {codes_of(k[b][0][w], i), codes_of(k[b][1][w], i),
+                                           codes_of(k[b][0][w], i + 1), codes_of(k[b][1][w], i + 1)};
+                    mma(x, a, q.qf[b][w][i], q.qf[b][w][i + 1], x);
                 }
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = w == gi * WPG && i == 0 ? acc[e] : x[e] + acc[e];
-            }
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const float s = par_s(pw[j][gi]), mid = fmaf(8.0f, s, par_lo(pw[j][gi]));
-            y[j].x = gi ? fmaf(s, x[2 * j], y[j].x) : s * x[2 * j];
-            y[j].y = gi ? fmaf(s, x[2 * j + 1], y[j].y) : s * x[2 * j + 1];
-            z[j].x = gi ? fmaf(mid, q.sq[gi].x, z[j].x) : mid * q.sq[0].x;
-            z[j].y = gi ? fmaf(mid, q.sq[gi].y, z[j].y) : mid * q.sq[0].y;
+            const float2 s2 = make_float2(s, s), mid2 = make_float2(mid, mid), x2 = make_float2(x[2 * j], x[2 * j + 1]);
+            y[j] = gi ? fma2(s2, x2, y[j]) : mul2(s2, x2);
+            z[j] = gi ? fma2(mid2, q.sq[gi], z[j]) : mul2(mid2, q.sq[0]);
         }
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        z[j].x = fmaf(y[j].x, q.rho.x, z[j].x);
-        z[j].y = fmaf(y[j].y, q.rho.y, z[j].y);
-    }
+    for (int j = 0; j < 2; ++j)
+        z[j] = fma2(y[j], q.rho, z[j]);
 }
 
 constexpr int kPairs = 4;        // pairs of blobs in a warp's ring
@@ -926,13 +929,13 @@ __device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, F eac
     }
 }
 
-// A warp takes 32 tokens of a (request, KV head), two blobs whose keys stay in its registers, over the
-// rows that see any of them: all of those, or where there are many a quarter, every fourth tile of 8.
+// A warp takes a blob of a (request, KV head), whose keys stay in its registers, over the rows that see any
+// of its tokens: all of those, or where there are many a quarter, every fourth tile of 8.
 template <typename B>
-__global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArgs a)
+__global__ void __launch_bounds__(kThreads, 4) k_weigh_sums(AttnArgs p, WeighArgs a)
 {
     constexpr int NW = B::kWords, NG = B::kGroups;
-    __shared__ float parts[kWarps][32];
+    __shared__ float parts[kWarps][16];
     const int lane = lane_once(), warp = threadIdx.x >> 5, t = lane & 3;
     const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
     const int bpp = p.page_tokens / 16;
@@ -941,33 +944,27 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
         AttnRequest q;
         int r, h, t0;
-        if (!find_item(p, item, [](const AttnRequest &x) { return x.rows >= kManyRows ? 32 : kItemTokens; }, &items, &q,
+        if (!find_item(p, item, [](const AttnRequest &x) { return x.rows >= kManyRows ? 16 : kItemTokens; }, &items, &q,
                        &r, &h, &t0))
             return;
         const bool shared = q.rows >= kManyRows;   // the block's warps have the same tokens
         if (!shared) {
-            t0 += 32 * warp;
+            t0 += 16 * warp;
             if (t0 >= q.kv)
                 continue;
         }
-        Keys<B> keys[2];
-        bool there[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int tok = min(t0 + 16 * b, q.kv - 1) & ~15, page = tok / p.page_tokens;
-            const int id = p.a.block_table[r * p.a.table_stride + page];
-            there[b] = (unsigned)id < (unsigned)p.num_pages;
-            if (!there[b])
-                int4_set_status(p.status, CG_ERR_CORRUPT);
-            // (a blob behind the last token is the one before it again: its sums are not written)
-            const uint64_t blob = there[b] ? ((uint64_t)id * p.heads + h) * bpp + (tok - page * p.page_tokens) / 16 : 0;
-            load_keys<B>(p.layer + blob * B::kBytes, lane, &keys[b]);
-        }
+        const int page = t0 / p.page_tokens, id = p.a.block_table[r * p.a.table_stride + page];
+        const bool there = (unsigned)id < (unsigned)p.num_pages;
+        if (!there)
+            int4_set_status(p.status, CG_ERR_CORRUPT);
+        const uint64_t blob = there ? ((uint64_t)id * p.heads + h) * bpp + (t0 - page * p.page_tokens) / 16 : 0;
+        Keys<B> keys;
+        load_keys<B>(p.layer + blob * B::kBytes, lane, &keys);
         // ---- rows that see any of the tokens
         const int64_t lo = min((int64_t)max(0, t0 - q.x0) * p.ratio, (int64_t)q.rows);
         int64_t hi = q.rows;
         if (p.a.window > 0 && t0 >= p.a.sinks)
-            hi = min(hi, ((int64_t)t0 + 31 + window - q.x0) * p.ratio);
+            hi = min(hi, ((int64_t)t0 + 15 + window - q.x0) * p.ratio);
         const int step = shared ? kWarps : 1, i0 = (int)(lo / 8) + (shared ? warp : 0);
         const int i1 = hi < 0 ? 0 : (int)((hi + 7) / 8);
         const int64_t slot = (int64_t)h * a.slots + first_slot(p, r, q.row0) + i0;
@@ -975,84 +972,73 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
         const float2 *factors = reinterpret_cast<const float2 *>(a.factors + slot * (NG + 1) * 8) + t;
         const float4 *stats = reinterpret_cast<const float4 *>(a.stats + slot * 8 + 2 * t);
         // Whether a row sees a token goes by rows: position x0 + row / ratio is at least x from row
-        // (x - x0) ratio on. All 8 rows of a tile see a whole blob from row `from_row` on, up to `to_row`.
+        // (x - x0) ratio on. All 8 rows of a tile see the whole blob from row `from_row` on, up to `to_row`.
         auto row_of = [&](int64_t x) {   // (a tile's rows end at 2^31 - 8 at most)
             return (int)max(min((x - q.x0) * p.ratio, (int64_t)INT32_MAX), (int64_t)-1);
         };
-        int from_row[2], to_row[2];
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int64_t tok = t0 + 16 * b;
-            from_row[b] = row_of(tok + 15);
-            to_row[b] = p.a.window == 0 || tok + 15 < p.a.sinks ? INT32_MAX : row_of(tok + window);
-        }
-        float total[2][2] = {}, sum[2][2] = {};
+        const int from_row = row_of((int64_t)t0 + 15);
+        const int to_row = p.a.window == 0 || t0 + 15 < p.a.sinks ? INT32_MAX : row_of((int64_t)t0 + window);
+        float total[2] = {}, sum[2] = {};
         int count = 0;
         for (int i = i0; i < i1; i += step) {
-            Queries<B> rows[1];
+            Queries<B> rows;
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 const uint4 v = from[32 * w];
-                rows[0].qf[w][0] = v.x, rows[0].qf[w][1] = v.y, rows[0].qf[w][2] = v.z, rows[0].qf[w][3] = v.w;
+                rows.qf[w][0] = v.x, rows.qf[w][1] = v.y, rows.qf[w][2] = v.z, rows.qf[w][3] = v.w;
             }
-            rows[0].rho = factors[0];
+            rows.rho = factors[0];
 #pragma unroll
             for (int k = 0; k < NG; ++k)
-                rows[0].sq[k] = factors[4 * (k + 1)];
+                rows.sq[k] = factors[4 * (k + 1)];
             const float4 st = *stats;
             from += step * NW * 32;
             factors += step * (NG + 1) * 4;
             stats += step * 4;
+            float2 z[2];
+            scores_of<B>(keys, rows, make_float2(st.x, st.z), z);
+            if (8 * i < from_row || 8 * i + 7 >= to_row) {
+                const int row = 8 * i + 2 * t;
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                float2 z[1][2];
-                scores_of<B, 1>(keys[b], rows, z);
-                if (8 * i < from_row[b] || 8 * i + 7 >= to_row[b]) {
-                    const int row = 8 * i + 2 * t;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int64_t tok = t0 + 16 * b + 8 * j + (lane >> 2);
-                        const int first = row_of(tok), end = p.a.window == 0 || tok < p.a.sinks ? INT32_MAX : row_of(tok + window);
-                        if (row < first || row >= end)
-                            z[0][j].x = -INFINITY;
-                        if (row + 1 < first || row + 1 >= end)
-                            z[0][j].y = -INFINITY;
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t tok = t0 + 8 * j + (lane >> 2);
+                    const int first = row_of(tok), end = p.a.window == 0 || tok < p.a.sinks ? INT32_MAX : row_of(tok + window);
+                    if (row < first || row >= end)
+                        z[j].x = -INFINITY;
+                    if (row + 1 < first || row + 1 >= end)
+                        z[j].y = -INFINITY;
                 }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    sum[b][j] = fmaf(exp2_fast(z[0][j].y - st.z), st.w,
-                                     fmaf(exp2_fast(z[0][j].x - st.x), st.y, sum[b][j]));
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                sum[j] = fmaf(exp2_fast(z[j].y), st.w, fmaf(exp2_fast(z[j].x), st.y, sum[j]));
             if ((++count & 31) == 0)   // sums of sums: their roundings grow with the root of either's length
 #pragma unroll
-                for (int b = 0; b < 2; ++b)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        total[b][j] += sum[b][j];
-                        sum[b][j] = 0.0f;
-                    }
+                for (int j = 0; j < 2; ++j) {
+                    total[j] += sum[j];
+                    sum[j] = 0.0f;
+                }
         }
         float mine = 0.0f;   // of token t0 + lane
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float s = total[b][j] + sum[b][j];
-                s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-                s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-                s = __shfl_sync(0xFFFFFFFFu, s, 4 * (lane & 7));
-                if (lane >> 3 == 2 * b + j)
-                    mine = there[b] ? s : 0.0f;
-            }
+        for (int j = 0; j < 2; ++j) {
+            float s = total[j] + sum[j];
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+            s = __shfl_sync(0xFFFFFFFFu, s, 4 * (lane & 7));
+            if (lane >> 3 == j)
+                mine = there ? s : 0.0f;
+        }
         if (shared) {
-            parts[warp][lane] = mine;
+            if (lane < 16)
+                parts[warp][lane] = mine;
             __syncthreads();
-            mine = (parts[0][lane] + parts[1][lane]) + (parts[2][lane] + parts[3][lane]);
+            if (lane < 16)
+                mine = (parts[0][lane] + parts[1][lane]) + (parts[2][lane] + parts[3][lane]);
             __syncthreads();
         }
         const int tok = t0 + lane;
-        if ((!shared || warp == 0) && tok < q.kv) {
+        if ((!shared || warp == 0) && lane < 16 && tok < q.kv) {
             const float had = a.w.in == nullptr ? 0.0f : a.w.in[r * a.w.in_request_stride + h * a.w.in_head_stride + tok];
             a.w.out[r * a.w.out_request_stride + h * a.w.out_head_stride + tok] = had + mine;
         }
@@ -1126,7 +1112,7 @@ cudaError_t launch(void (*kernel)(AttnArgs, WeighArgs), int per_sm, const AttnAr
         return err;
     if (stored)
         return launch_under(k_weigh_apply, dim3(8 * sms), kThreads, 0, s, p, a);
-    return launch_under(k_weigh_sums<B>, dim3(3 * sms), kThreads, 0, s, p, a);
+    return launch_under(k_weigh_sums<B>, dim3(4 * sms), kThreads, 0, s, p, a);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
@@ -1239,8 +1225,8 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
         if (z.stored)
             return launch<8, FewShared<B>, B>(z.rows <= 4 ? k_weigh_few<B, 2> : k_weigh_few<B, 1>, kFewBlocks, p, args, true, s);
         if (z.rows <= 16)
-            return launch<16, StatShared<B, 2>, B>(k_weigh_stats<B, 2>, stat_blocks(2), p, args, false, s);
-        return launch<32, StatShared<B, 4>, B>(k_weigh_stats<B, 4>, stat_blocks(4), p, args, false, s);
+            return launch<16, StatShared<B, 2>, B>(k_weigh_stats<B, 2>, kStatBlocks, p, args, false, s);
+        return launch<32, StatShared<B, 4>, B>(k_weigh_stats<B, 4>, kStatBlocks, p, args, false, s);
     });
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

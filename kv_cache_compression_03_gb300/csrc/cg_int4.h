@@ -60,6 +60,16 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return d;
 }
 
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
 // lo + s n for the codes i and i + 4 of a word, rounded once: n comes exact out
 // of the mantissa of 128 + n.
 __device__ __forceinline__ uint32_t expand(uint32_t w, int i, uint32_t s, uint32_t lo)

@@ -347,13 +347,26 @@ struct StatShared {
     Stand feed[kWarps], now[kWarps];
 };
 
+// A row's maximum set by its first score or raised by a later one, `top` above it: by how much. *limit
+// stays below every score while a row that is there waits for its first.
+__device__ __forceinline__ float raise(float top, bool no_row, float *m, float *l, float *limit)
+{
+    const bool none = *l == 0.0f;
+    const float up = none ? (top > kNone ? top : 0.0f) : fmaxf(top, 0.0f);
+    *m += up;
+    *l = none ? 0.0f : *l * exp2_fast(-up);
+    if (none && !(top > kNone) && !no_row)
+        *limit = kNone;
+    return up;
+}
+
 __device__ __forceinline__ float2 row_stats_of(float m, float l)
 {
     return l == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(m, 1.0f / l);
 }
 
 // Blocks on an SM.
-constexpr int kStatBlocks = 4;
+constexpr int kStatBlocks = 3;
 
 template <typename B, int NT>
 __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs p, WeighArgs a)
@@ -396,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
         const Tile tile = now.t;
         const int slot = first_slot(p, u.r, u.q.row0) + tile.row0 / 8;
         // a warp to a tile of 8 rows; the unit's first piece leaves them for the sums too
-        if (warp < NT && 8 * warp < tile.rows) {
+        if (warp < NT) {
             Queries<B> q;
             load_rows<B>(p, u.q, u.h, tile.row0 + 8 * warp, &q);
             const int64_t at_slot = (int64_t)u.h * a.slots + slot + warp;
@@ -405,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 sm.qf[warp][w][lane] = make_uint4(q.qf[w][0], q.qf[w][1], q.qf[w][2], q.qf[w][3]);
-                if (u.b0 == 0)
+                if (u.b0 == 0 && 8 * warp < tile.rows)
                     to[32 * w] = sm.qf[warp][w][lane];
             }
             if (g == 0) {
 #pragma unroll
                 for (int i = 0; i <= NG; ++i) {
                     sm.factors[warp][i][t] = i ? q.sq[i ? i - 1 : 0] : q.rho;
-                    if (u.b0 == 0)
+                    if (u.b0 == 0 && 8 * warp < tile.rows)
                         f[4 * i] = sm.factors[warp][i][t];
                 }
             }
@@ -426,17 +439,14 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
                 const int in = 8 * nt + 2 * t + j;
                 x[nt][j] = in < tile.rows ? u.q.x0 + (tile.row0 + in) / p.ratio : -1;
             }
-        const int tiles = (tile.rows + 7) / 8;
         // Each lane keeps a maximum (0 before the first score) and a sum of its own, over tokens g and g + 8
         // of the blobs. The maximum is set by a row's first score, and raised only when a score exceeds it by
         // 2^8: `limit` is below every score while a row of the lane waits for its first.
         float2 m[NT], l[NT];
-        float limit[NT];
+        float limit = kNone;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+        for (int nt = 0; nt < NT; ++nt)
             m[nt] = l[nt] = make_float2(0.0f, 0.0f);
-            limit[nt] = kNone;
-        }
         int b, e;
         tile_range(u, tile, warp, &b, &e);
         for (; b < e; ++b) {
@@ -455,10 +465,10 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
                 load_keys<B>(sm.ring[warp][st][0], lane, &k);
                 const int tok = 16 * (b < tile.span.sink ? b : b + tile.span.skip);
                 const bool whole = tok + 15 <= tile.x_lo && (tile.x_hi - tok < window || tok + 15 < p.a.sinks);
+                // rows that are not there have q = 0: what they get is dropped at the end
+                float2 z[NT][2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    if (nt >= tiles)
-                        break;
                     Queries<B> q;
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
@@ -469,32 +479,33 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
 #pragma unroll
                     for (int i = 0; i < NG; ++i)
                         q.sq[i] = sm.factors[nt][i + 1][t];
-                    float2 z[2];
-                    scores_of<B>(k, q, m[nt], z);
-                    if (!whole)
-                        hide(p, tok, g, x[nt], window, z);
-                    const float2 top = make_float2(fmaxf(z[0].x, z[1].x), fmaxf(z[0].y, z[1].y));
-                    if (fmaxf(top.x, top.y) > limit[nt]) {
-                        const bool none_x = l[nt].x == 0.0f, none_y = l[nt].y == 0.0f;
-                        const float up_x = none_x ? fmaxf(top.x, kNone) : fmaxf(top.x, 0.0f);
-                        const float up_y = none_y ? fmaxf(top.y, kNone) : fmaxf(top.y, 0.0f);
-                        if (up_x > kNone) {
-                            m[nt].x += up_x;
-                            l[nt].x = none_x ? 0.0f : l[nt].x * exp2_fast(-up_x);
-                            z[0].x -= up_x;
-                            z[1].x -= up_x;
-                        }
-                        if (up_y > kNone) {
-                            m[nt].y += up_y;
-                            l[nt].y = none_y ? 0.0f : l[nt].y * exp2_fast(-up_y);
-                            z[0].y -= up_y;
-                            z[1].y -= up_y;
-                        }
-                        if ((up_x > kNone || x[nt][0] < 0) && (up_y > kNone || x[nt][1] < 0))
-                            limit[nt] = 8.0f;
+                    scores_of<B>(k, q, m[nt], z[nt]);
+                }
+                if (!whole)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        hide(p, tok, g, x[nt], window, z[nt]);
+                float top = -INFINITY;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    top = fmaxf(fmaxf(top, z[nt][0].x), z[nt][0].y);
+                    top = fmaxf(fmaxf(top, z[nt][1].x), z[nt][1].y);
+                }
+                if (top > limit) {
+                    limit = 8.0f;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float up_x = raise(fmaxf(z[nt][0].x, z[nt][1].x), x[nt][0] < 0, &m[nt].x, &l[nt].x, &limit);
+                        const float up_y = raise(fmaxf(z[nt][0].y, z[nt][1].y), x[nt][1] < 0, &m[nt].y, &l[nt].y, &limit);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            z[nt][j] = make_float2(z[nt][j].x - up_x, z[nt][j].y - up_y);
                     }
-                    l[nt].x += exp2_fast(z[0].x) + exp2_fast(z[1].x);
-                    l[nt].y += exp2_fast(z[0].y) + exp2_fast(z[1].y);
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    l[nt].x += exp2_fast(z[nt][0].x) + exp2_fast(z[nt][1].x);
+                    l[nt].y += exp2_fast(z[nt][0].y) + exp2_fast(z[nt][1].y);
                 }
             }
             __syncwarp();   // every lane has read the place
@@ -932,7 +943,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, F eac
 // A warp takes a blob of a (request, KV head), whose keys stay in its registers, over the rows that see any
 // of its tokens: all of those, or where there are many a quarter, every fourth tile of 8.
 template <typename B>
-__global__ void __launch_bounds__(kThreads, 4) k_weigh_sums(AttnArgs p, WeighArgs a)
+__global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArgs a)
 {
     constexpr int NW = B::kWords, NG = B::kGroups;
     __shared__ float parts[kWarps][16];
@@ -967,7 +978,7 @@ __global__ void __launch_bounds__(kThreads, 4) k_weigh_sums(AttnArgs p, WeighArg
             hi = min(hi, ((int64_t)t0 + 15 + window - q.x0) * p.ratio);
         const int step = shared ? kWarps : 1, i0 = (int)(lo / 8) + (shared ? warp : 0);
         const int i1 = hi < 0 ? 0 : (int)((hi + 7) / 8);
-        const int64_t slot = (int64_t)h * a.slots + first_slot(p, r, q.row0) + i0;
+        const int64_t slot = (int64_t)h * a.slots + first_slot(p, r, q.row0);
         const uint4 *from = a.queries + slot * NW * 32 + lane;
         const float2 *factors = reinterpret_cast<const float2 *>(a.factors + slot * (NG + 1) * 8) + t;
         const float4 *stats = reinterpret_cast<const float4 *>(a.stats + slot * 8 + 2 * t);
@@ -980,24 +991,54 @@ __global__ void __launch_bounds__(kThreads, 4) k_weigh_sums(AttnArgs p, WeighArg
         const int to_row = p.a.window == 0 || t0 + 15 < p.a.sinks ? INT32_MAX : row_of((int64_t)t0 + window);
         float total[2] = {}, sum[2] = {};
         int count = 0;
-        for (int i = i0; i < i1; i += step) {
+        auto scores = [&](int i, float4 *st, float2 (&z)[2]) {   // of row tile i
             Queries<B> rows;
+            const uint4 *qi = from + (int64_t)i * (NW * 32);
+            const float2 *fi = factors + (int64_t)i * ((NG + 1) * 4);
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const uint4 v = from[32 * w];
+                const uint4 v = qi[32 * w];
                 rows.qf[w][0] = v.x, rows.qf[w][1] = v.y, rows.qf[w][2] = v.z, rows.qf[w][3] = v.w;
             }
-            rows.rho = factors[0];
+            rows.rho = fi[0];
 #pragma unroll
             for (int k = 0; k < NG; ++k)
-                rows.sq[k] = factors[4 * (k + 1)];
-            const float4 st = *stats;
-            from += step * NW * 32;
-            factors += step * (NG + 1) * 4;
-            stats += step * 4;
+                rows.sq[k] = fi[4 * (k + 1)];
+            *st = stats[4 * (int64_t)i];
+            scores_of<B>(keys, rows, make_float2(st->x, st->z), z);
+        };
+        auto add = [&](const float4 &st, const float2 (&z)[2]) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                sum[j] = fmaf(exp2_fast(z[j].y), st.w, fmaf(exp2_fast(z[j].x), st.y, sum[j]));
+        };
+        auto carry = [&]() {   // sums of sums: their roundings grow with the root of either's length
+            if ((++count & 31) == 0)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    total[j] += sum[j];
+                    sum[j] = 0.0f;
+                }
+        };
+        // tiles [f0, f1) see the whole blob: two at a time, whose instructions mix
+        const int f0 = from_row < 0 ? i0 : from_row > 8 * (int64_t)i1 ? i1 : max(i0, (from_row + 7) / 8);
+        const int f1 = min(i1, to_row < 0 ? 0 : to_row / 8);
+        for (int i = i0; i < i1; i += step) {
+            if (i >= f0 && i + step < f1) {
+                float4 st[2];
+                float2 z[2][2];
+                scores(i, &st[0], z[0]);
+                scores(i + step, &st[1], z[1]);
+                add(st[0], z[0]);
+                add(st[1], z[1]);
+                carry();
+                i += step;
+                continue;
+            }
+            float4 st;
             float2 z[2];
-            scores_of<B>(keys, rows, make_float2(st.x, st.z), z);
-            if (8 * i < from_row || 8 * i + 7 >= to_row) {
+            scores(i, &st, z);
+            if (i < f0 || i >= f1) {
                 const int row = 8 * i + 2 * t;
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -1009,15 +1050,8 @@ __global__ void __launch_bounds__(kThreads, 4) k_weigh_sums(AttnArgs p, WeighArg
                         z[j].y = -INFINITY;
                 }
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                sum[j] = fmaf(exp2_fast(z[j].y), st.w, fmaf(exp2_fast(z[j].x), st.y, sum[j]));
-            if ((++count & 31) == 0)   // sums of sums: their roundings grow with the root of either's length
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    total[j] += sum[j];
-                    sum[j] = 0.0f;
-                }
+            add(st, z);
+            carry();
         }
         float mine = 0.0f;   // of token t0 + lane
 #pragma unroll
@@ -1112,7 +1146,7 @@ cudaError_t launch(void (*kernel)(AttnArgs, WeighArgs), int per_sm, const AttnAr
         return err;
     if (stored)
         return launch_under(k_weigh_apply, dim3(8 * sms), kThreads, 0, s, p, a);
-    return launch_under(k_weigh_sums<B>, dim3(4 * sms), kThreads, 0, s, p, a);
+    return launch_under(k_weigh_sums<B>, dim3(3 * sms), kThreads, 0, s, p, a);
 }
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }

@@ -866,7 +866,7 @@ class ReleasePlan:
     cu: "object"           # int32 [requests + 1], exclusive sums of the pages released
     lens: "object"         # int32 [requests], the new ones
     free_count: "object"   # int32 [1]
-    status: "object"       # uint8 [16]
+    status: "object"       # 16 bytes
 
     def check(self):
         """Wait for the current stream; raise if nothing was released."""
@@ -904,7 +904,7 @@ def release_pages(block_table, lens, new_lens, free_pages, free_count, page_toke
     if out is None:
         e, i32 = torch.empty, torch.int32
         out = ReleasePlan(e(n + 1, dtype=i32, device=dev), e(n, dtype=i32, device=dev),
-                          e(1, dtype=i32, device=dev), e(16, dtype=torch.uint8, device=dev))
+                          e(1, dtype=i32, device=dev), e(4, dtype=i32, device=dev))
     else:
         _ints(out.cu, dev, (n + 1,), "out.cu")
         _ints(out.lens, dev, (n,), "out.lens")
@@ -929,7 +929,7 @@ class KeptTokens:
     """What choose_tokens found: tensors on the device."""
     kept: "object"     # int32 [.., requests, heads, budget], ascending, -1 behind the last
     lens: "object"     # int32 [requests]: tokens that stay
-    status: "object"   # uint8 [16]
+    status: "object"   # 16 bytes
 
     def check(self):
         """Wait for the current stream; raise if a length was wrong."""
@@ -961,9 +961,9 @@ def choose_tokens(weights, lens, budget: int, recent: int = 0, sinks: int = 0,
     lens_at = _ints(lens, dev, (n,), "lens")
     _need(0 <= _int32(budget, "budget"), "budget must not be negative")
     if out is None:
-        out = KeptTokens(torch.empty(shape[:-1] + (budget,), dtype=torch.int32, device=dev),
-                         torch.empty(n, dtype=torch.int32, device=dev),
-                         torch.empty(16, dtype=torch.uint8, device=dev))
+        e, i32 = torch.empty, torch.int32
+        out = KeptTokens(e(shape[:-1] + (budget,), dtype=i32, device=dev), e(n, dtype=i32, device=dev),
+                         e(4, dtype=i32, device=dev))
     else:
         _ints(out.kept, dev, shape[:-1] + (budget,), "out.kept")
         _ints(out.lens, dev, (n,), "out.lens")

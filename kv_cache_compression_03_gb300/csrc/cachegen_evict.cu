@@ -509,22 +509,39 @@ __global__ void __launch_bounds__(kMoveThreads, 2) k_int4_compact(MoveArgs a, in
     };
     const int32_t start = first_moved < n ? first_moved & ~15 : n;   // blobs before it stay as they are
     const int waves = (int)(((int64_t)n - start + kWave - 1) / kWave);
-    // where the tokens of this block's wave i lie; then their bytes
-    auto read = [&](int i) {
-        const int64_t p0 = start + ((int64_t)i * size + rank) * kWave;
+    // Of this block's wave i, in steps that a dependent load each ends: the token that comes to a thread's
+    // place, where both lie, and its bytes.
+    auto place_of = [&](int i) { return start + ((int64_t)i * size + rank) * kWave + tid; };
+    auto token_of = [&](int i) {
+        const int64_t p = place_of(i);
+        return tid < kWave && p < n ? kept[p] : -1;
+    };
+    struct Found {
+        const uint8_t *from;
+        uint8_t *to;
+        float weight;
+    };
+    auto find = [&](int i, int32_t j) -> Found {
+        const int64_t p = place_of(i);
+        Found f = {nullptr, nullptr, 0.0f};
+        if (tid < kWave && p <= n && p - tid < n) {
+            f.from = j >= 0 ? blob_of(j) : nullptr;
+            f.to = blob_of((int32_t)p);
+            f.weight = w != nullptr && j >= 0 ? w[j] : 0.0f;
+        }
+        return f;
+    };
+    auto fetch = [&](int i, int32_t j, const Found &f) {
+        const int64_t p0 = place_of(i) - tid;
         Stage &st = stages[i % kStages];
         if (p0 < n && tid < kWave) {
-            const int32_t p = (int32_t)min(p0 + tid, (int64_t)INT32_MAX), j = p < n ? kept[p] : p;
             // a place behind the last shares its pair's bytes, and one whose token cannot be read keeps
             // its own: both are read where they are written
-            const uint8_t *from = p < n ? blob_of(j) : nullptr;
-            uint8_t *to = p <= n ? blob_of(p) : nullptr;
-            st.src[tid] = from != nullptr ? from : to;
-            st.tok[tid] = from != nullptr ? j & 15 : p & 15;
+            st.src[tid] = f.from != nullptr ? f.from : f.to;
+            st.tok[tid] = f.from != nullptr ? j & 15 : tid & 15;
             if (tid % 16 == 0)
-                st.dst[tid / 16] = to;
-            if (w != nullptr && p < n)
-                st.weight[tid] = w[j];
+                st.dst[tid / 16] = p0 + tid < n ? f.to : nullptr;
+            st.weight[tid] = f.weight;
         }
         __syncthreads();
         if (p0 < n) {
@@ -550,12 +567,18 @@ __global__ void __launch_bounds__(kMoveThreads, 2) k_int4_compact(MoveArgs a, in
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     const int rounds = (waves + size - 1) / size;
-    for (int i = 0; i < kStages; ++i)
-        read(i);
+    for (int i = 0; i < kStages; ++i) {
+        const int32_t j = token_of(i);
+        fetch(i, j, find(i, j));
+    }
+    int32_t ahead = token_of(kStages);   // of the wave that is fetched next
     for (int i = 0; i < rounds; ++i) {
         asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
         cluster_sync(size);   // this round's waves have been read, by all threads of all blocks
-        const int64_t p0 = start + ((int64_t)i * size + rank) * kWave;
+        const int32_t j = ahead;
+        const Found found = find(i + kStages, j);   // (its loads end under the writes)
+        ahead = token_of(i + kStages + 1);
+        const int64_t p0 = place_of(i) - tid;
         const Stage &st = stages[i % kStages];
         if (p0 < n) {
             const int there = (int)min((int64_t)kWave, n - p0);   // places of the wave
@@ -598,7 +621,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) k_int4_compact(MoveArgs a, in
                 w[p0 + tid] = st.weight[tid];
         }
         __syncthreads();   // the stage is free
-        read(i + kStages);
+        fetch(i + kStages, j, found);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if (w != nullptr)   // read by no wave any more
@@ -656,7 +679,7 @@ extern "C" cg_status cg_choose_tokens(const cg_token_choice *c, cg_stream_t stre
         // blocks, four on an SM: what bounds them is each block's chain of barriers.
         constexpr int kSmall = 256, kLarge = 512, kMost = 32;   // threads; tokens of one
         int size = 1;
-        while (size < kMostCluster && c->width > kMost * kLarge * size)
+        while (size < kMostCluster && c->width > kMost * kSmall * size)
             size *= 2;
         while (size < kMostCluster && rows * size < 152 && c->width > 8 * kSmall * size)
             size *= 2;

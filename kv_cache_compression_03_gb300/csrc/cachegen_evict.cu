@@ -636,9 +636,11 @@ cudaError_t launch_move(const MoveArgs &a, int64_t lists, cudaStream_t s)
     const cudaError_t err = cudaFuncSetAttribute(k_int4_compact<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess)
         return err;
-    // two blocks to an SM; few lists are shared by several
+    // Two blocks to an SM. Lists that do not fill the SMs are shared by the blocks of a cluster (128 lists of
+    // 2048: 28 us with two, 20 with four); more are not, a barrier of the cluster to each wave costs more
+    // than it gives (256 of 8192: 179 us, with two blocks 228).
     int size = 1;
-    while (size < kMostCluster && lists * size < 200)
+    while (size < kMostCluster && lists < 152 && lists * size < 400)
         size *= 2;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;

@@ -17,7 +17,6 @@ namespace {
 constexpr int kRing = 8;           // blobs in a warp's ring
 constexpr int kItemTokens = 64;    // of a block in the second pass, a blob to a warp; or,
 constexpr int kManyRows = 512;     // from so many rows on, a blob to a block, whose warps share the rows
-constexpr int kApplyTokens = 512;  // of a block in the second pass over stored scores
 constexpr int kMaxBlocks = 640;    // of the first pass
 
 struct WeighArgs {
@@ -368,7 +367,8 @@ __device__ __forceinline__ float2 row_stats_of(float m, float l)
 // Blocks on an SM.
 constexpr int kStatBlocks = 3;
 
-template <typename B, int NT>
+// kStored: scores are left for the sums, else the queries.
+template <typename B, int NT, bool kStored>
 __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs p, WeighArgs a)
 {
     using S = StatShared<B, NT>;
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
         const Unit u = now.u;
         const Tile tile = now.t;
         const int slot = first_slot(p, u.r, u.q.row0) + tile.row0 / 8;
-        // a warp to a tile of 8 rows; the unit's first piece leaves them for the sums too
+        // a warp to a tile of 8 rows; the unit's first piece leaves them for the sums
         if (warp < NT) {
             Queries<B> q;
             load_rows<B>(p, u.q, u.h, tile.row0 + 8 * warp, &q);
@@ -418,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
                 sm.qf[warp][w][lane] = make_uint4(q.qf[w][0], q.qf[w][1], q.qf[w][2], q.qf[w][3]);
-                if (u.b0 == 0 && 8 * warp < tile.rows)
+                if (!kStored && u.b0 == 0 && 8 * warp < tile.rows)
                     to[32 * w] = sm.qf[warp][w][lane];
             }
             if (g == 0) {
 #pragma unroll
                 for (int i = 0; i <= NG; ++i) {
                     sm.factors[warp][i][t] = i ? q.sq[i ? i - 1 : 0] : q.rho;
-                    if (u.b0 == 0 && 8 * warp < tile.rows)
+                    if (!kStored && u.b0 == 0 && 8 * warp < tile.rows)
                         f[4 * i] = sm.factors[warp][i][t];
                 }
             }
@@ -485,6 +485,20 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
                         hide(p, tok, g, x[nt], window, z[nt]);
+                if (kStored) {
+                    float *to = a.scores + (((int64_t)u.r * p.heads + u.h) * a.rows + tile.row0 + 2 * t) * a.tokens + tok + g;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const int row = 8 * nt + 2 * t;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            if (row < tile.rows)
+                                to[(int64_t)(8 * nt) * a.tokens + 8 * j] = z[nt][j].x + m[nt].x;
+                            if (row + 1 < tile.rows)
+                                to[(int64_t)(8 * nt + 1) * a.tokens + 8 * j] = z[nt][j].y + m[nt].y;
+                        }
+                    }
+                }
                 float top = -INFINITY;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -507,6 +521,12 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
                     l[nt].x += exp2_fast(z[nt][0].x) + exp2_fast(z[nt][1].x);
                     l[nt].y += exp2_fast(z[nt][0].y) + exp2_fast(z[nt][1].y);
                 }
+            }
+            if (kStored && alive && !(feeder.ahead & 1)) {   // a page that is not there
+                const int tok = 16 * (b < tile.span.sink ? b : b + tile.span.skip);
+                float *to = a.scores + (((int64_t)u.r * p.heads + u.h) * a.rows + tile.row0) * a.tokens + tok;
+                for (int i = lane; i < 16 * tile.rows; i += 32)
+                    to[(int64_t)(i / 16) * a.tokens + i % 16] = -INFINITY;
             }
             __syncwarp();   // every lane has read the place
             if (alive)
@@ -859,7 +879,7 @@ __global__ void __launch_bounds__(kThreads) k_weigh_join(AttnArgs p, int pieces,
 {
     grid_next();
     int64_t total, chunk;
-    const int c = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = blockIdx.x;
     const Place at = schedule<RU>(p, pieces, c + 1, 0, false, &total, &chunk);
     const int64_t border = (c + 1) * chunk;
     Unit u;
@@ -872,22 +892,27 @@ __global__ void __launch_bounds__(kThreads) k_weigh_join(AttnArgs p, int pieces,
     const int n = (int)((end + chunk - 1) / chunk) - c;
     const Tile tile = tile_of<RU>(p, u);
     const int slot = first_slot(p, u.r, u.q.row0) + tile.row0 / 8;
-    for (int row = warp; row < (tile.rows + 7) / 8 * 8; row += kWarps) {
-        float mx = kNone, l = 0.0f;
-        for (int k = lane; k < n; k += 32)
-            mx = fmaxf(mx, a.parts[((int64_t)(c + k) * 2 + (k == 0)) * RU + row].x);
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1)
-            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, d));
-        for (int k = lane; k < n; k += 32) {
-            const float2 part = a.parts[((int64_t)(c + k) * 2 + (k == 0)) * RU + row];
-            l = fmaf(part.y, exp2_fast(part.x - mx), l);
-        }
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1)
-            l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-        if (lane == 0)
-            a.stats[((int64_t)u.h * a.slots + slot) * 8 + row] = row_stats_of(mx, l);
+    // rows side by side, the parts shared by slices of the block
+    constexpr int kSlices = kThreads / RU;
+    __shared__ float2 slices[kSlices][RU];
+    const int row = threadIdx.x % RU, slice = threadIdx.x / RU;
+    float mx = kNone, l = 0.0f;
+#pragma unroll 4
+    for (int k = slice; k < n; k += kSlices) {
+        const float2 part = a.parts[((int64_t)(c + k) * 2 + (k == 0)) * RU + row];
+        const float up = fmaxf(mx, part.x);
+        l = l * exp2_fast(mx - up) + part.y * exp2_fast(part.x - up);
+        mx = up;
+    }
+    slices[slice][row] = make_float2(mx, l);
+    __syncthreads();
+    if (threadIdx.x < (tile.rows + 7) / 8 * 8) {
+        for (int k = 0; k < kSlices; ++k)
+            mx = fmaxf(mx, slices[k][row].x);
+        l = 0.0f;
+        for (int k = 0; k < kSlices; ++k)
+            l = fmaf(slices[k][row].y, exp2_fast(slices[k][row].x - mx), l);
+        a.stats[((int64_t)u.h * a.slots + slot) * 8 + row] = row_stats_of(mx, l);
     }
 }
 
@@ -1079,51 +1104,66 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
     }
 }
 
-// The same from stored scores, four tokens to a thread.
+// The same from stored scores, kEach tokens to a thread, kRows rows at a time: as many loads in flight as a
+// thread has registers for, whether a request has few rows and many tokens or the other way round.
+template <int kEach, int kRows>
 __global__ void __launch_bounds__(kThreads) k_weigh_apply(AttnArgs p, WeighArgs a)
 {
-    constexpr int kEach = kApplyTokens / kThreads;
+    constexpr int kTokens = kEach * kThreads;
     grid_wait();
     Items items = {0, 0};
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
         AttnRequest q;
         int r, h, t0;
-        if (!find_item(p, item, [](const AttnRequest &) { return kApplyTokens; }, &items, &q, &r, &h, &t0))
+        if (!find_item(p, item, [](const AttnRequest &) { return kTokens; }, &items, &q, &r, &h, &t0))
             return;
         t0 += threadIdx.x;
         const float *in = a.w.in == nullptr ? nullptr : a.w.in + r * a.w.in_request_stride + h * a.w.in_head_stride;
         float *out = a.w.out + r * a.w.out_request_stride + h * a.w.out_head_stride;
         const float *scores = a.scores + ((int64_t)r * p.heads + h) * a.rows * a.tokens + t0;
         const float4 *stats = reinterpret_cast<const float4 *>(a.stats + ((int64_t)h * a.slots + first_slot(p, r, q.row0)) * 8);
-        // blobs that no row sees have no scores
-        const int x_last = q.x0 + (q.rows > 0 ? (q.rows - 1) / p.ratio : 0);
-        const int64_t low = p.a.window > 0 ? ((int64_t)q.x0 + 1 - p.a.window) / 16 * 16 : 0;
+        // A blob has scores for the rows of a tile (of 8, 16 or 32, where the first pass has several) that
+        // sees it, whose own rows may see less of it.
         const int64_t sinks = ((int64_t)p.a.sinks + 15) / 16 * 16;
-        float had[kEach], sum[kEach];
-        bool seen[kEach];
+        float had[kEach], sum[kEach], total[kEach];
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
             const int tok = t0 + k * kThreads;
-            seen[k] = tok <= x_last && (tok >= low || tok < sinks);
             had[k] = in != nullptr && tok < q.kv ? in[tok] : 0.0f;
-            sum[k] = 0.0f;
+            sum[k] = total[k] = 0.0f;
         }
-        for (int row = 0; row < q.rows; row += 2) {
-            const float4 st = stats[row / 2];   // of two rows (a row that is not there: 0, 0)
-            float z[2][kEach];
+        for (int row = 0; row < q.rows; row += kRows) {
+            // the tokens from `low` on (or below sinks) up to x_last: those of these rows
+            const int x_first = q.x0 + row / p.ratio, x_last = q.x0 + min(row + kRows - 1, q.rows - 1) / p.ratio;
+            const int64_t low = p.a.window > 0 ? (int64_t)x_first + 1 - p.a.window : 0;
+            float z[kRows][kEach];
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+            for (int j = 0; j < kRows; ++j)
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) {
+                    const int tok = t0 + k * kThreads;
+                    const bool seen = tok <= x_last && (tok >= low || tok < sinks) && row + j < q.rows;
+                    z[j][k] = seen ? scores[(int64_t)(row + j) * a.tokens + k * kThreads] : -INFINITY;
+                }
+#pragma unroll
+            for (int j = 0; j < kRows; j += 2) {
+                // of two rows (0, 0 where only the second is not there)
+                const float4 st = row + j < q.rows ? stats[(row + j) / 2] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int k = 0; k < kEach; ++k)
-                    z[j][k] = seen[k] && row + j < q.rows ? scores[(int64_t)(row + j) * a.tokens + k * kThreads] : -INFINITY;
+                    sum[k] = fmaf(exp2_fast(z[j + 1][k] - st.z), st.w, fmaf(exp2_fast(z[j][k] - st.x), st.y, sum[k]));
+            }
+            if (row % 256 == 256 - kRows)   // sums of sums: their roundings grow with the root of either's length
 #pragma unroll
-            for (int k = 0; k < kEach; ++k)
-                sum[k] = fmaf(exp2_fast(z[1][k] - st.z), st.w, fmaf(exp2_fast(z[0][k] - st.x), st.y, sum[k]));
+                for (int k = 0; k < kEach; ++k) {
+                    total[k] += sum[k];
+                    sum[k] = 0.0f;
+                }
         }
 #pragma unroll
         for (int k = 0; k < kEach; ++k)
             if (t0 + k * kThreads < q.kv)
-                out[t0 + k * kThreads] = had[k] + sum[k];
+                out[t0 + k * kThreads] = had[k] + (total[k] + sum[k]);
     }
 }
 
@@ -1144,8 +1184,10 @@ cudaError_t launch(void (*kernel)(AttnArgs, WeighArgs), int per_sm, const AttnAr
         err = launch_under(k_weigh_join<RU>, dim3(blocks), kThreads, 0, s, p, blocks, a);
     if (err != cudaSuccess)
         return err;
+    if (stored && RU == 8)
+        return launch_under(k_weigh_apply<4, 4>, dim3(8 * sms), kThreads, 0, s, p, a);
     if (stored)
-        return launch_under(k_weigh_apply, dim3(8 * sms), kThreads, 0, s, p, a);
+        return launch_under(k_weigh_apply<1, 16>, dim3(16 * sms), kThreads, 0, s, p, a);
     return launch_under(k_weigh_sums<B>, dim3(3 * sms), kThreads, 0, s, p, a);
 }
 
@@ -1170,10 +1212,11 @@ WeighSizes sizes_of(const cg_int4_cache *c, const cg_attention *a, const cg_toke
     z.slots = (int32_t)((int64_t)a->tokens * ratio / 8 + a->requests + 1);
     z.rows = (int32_t)(rows < INT32_MAX ? rows : INT32_MAX);
     z.tokens = (int32_t)(((limit < w->width ? limit : w->width) + 15) / 16 * 16);
-    // of up to 8 rows a token's scores are fewer bytes than its keys and are not computed again; a batch
-    // with more room in its tables than this goes without
+    // Scores are stored, and not computed again, where there is room for those that the batch can have (128
+    // rows at 32768 tokens, 8 heads: FIGA us so, 123 computed again; more than the L2 holds would be
+    // read from memory at no gain: 8192 rows at 2048, two requests, 1 GB).
     const size_t lists = (size_t)a->requests * c->num_heads;
-    z.stored = z.rows <= 8 && (lists == 0 || (size_t)z.rows * z.tokens <= kMostScores / sizeof(float) / lists);
+    z.stored = lists == 0 || (size_t)z.rows * z.tokens <= kMostScores / sizeof(float) / lists;
     z.parts = align256((size_t)kMaxBlocks * 2 * 32 * sizeof(float2));
     z.stats = align256((size_t)c->num_heads * z.slots * 8 * sizeof(float2));
     if (z.stored) {
@@ -1256,11 +1299,12 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
         using B = decltype(blob);
-        if (z.stored)
+        if (z.stored && z.rows <= 8)
             return launch<8, FewShared<B>, B>(z.rows <= 4 ? k_weigh_few<B, 2> : k_weigh_few<B, 1>, kFewBlocks, p, args, true, s);
-        if (z.rows <= 16)
-            return launch<16, StatShared<B, 2>, B>(k_weigh_stats<B, 2>, kStatBlocks, p, args, false, s);
-        return launch<32, StatShared<B, 4>, B>(k_weigh_stats<B, 4>, kStatBlocks, p, args, false, s);
+        if (z.stored && z.rows <= 16)
+            return launch<16, StatShared<B, 2>, B>(k_weigh_stats<B, 2, true>, kStatBlocks, p, args, true, s);
+        return launch<32, StatShared<B, 4>, B>(z.stored ? k_weigh_stats<B, 4, true> : k_weigh_stats<B, 4, false>,
+                                               kStatBlocks, p, args, z.stored, s);
     });
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

@@ -578,11 +578,13 @@ cg_status cg_int4_attention_shared(const cg_int4_cache *cache, int32_t layer,
  * p is computed in fp32, the sum over i and g in an order that does not depend on timing.
  *
  * args are those of cg_int4_attention (out and its strides are not looked at), with
- * the same limits and device errors; a kv_len beyond width is CG_ERR_CORRUPT. in (NULL:
+ * the same limits and device errors (and tokens of a row, or width, at most 2^31 - 2^16); a
+ * kv_len beyond width is CG_ERR_CORRUPT. in (NULL:
  * zeros) and out have rows of width floats, elements adjacent, strides in elements; in
  * may be out (with the same strides) and otherwise must not overlap it. Rows of out must not
  * overlap, nor out q or the cache. workspace as for attention; its size depends on the
- * cache's shape, tokens, requests, q_heads, max_q_len and width. */
+ * cache's shape, tokens, requests, q_heads, max_q_len, table_width and width: room for the
+ * scores where they are below 256 MB, for the queries again where they are not. */
 typedef struct cg_token_weights {
     const float *in;
     float *out;

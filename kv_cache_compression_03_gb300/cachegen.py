@@ -1203,7 +1203,7 @@ class Int4Cache:
         except struct.error as e:
             raise ValueError(f"a number does not fit its type: {e}") from None
         L = _lib or load()
-        key = (tokens, q_heads, max_q_len, n, shape[2])
+        key = (tokens, q_heads, max_q_len, n, width, shape[2])
         size = self._sizes.get(key)
         if size is None:
             need = ct.c_size_t(0)

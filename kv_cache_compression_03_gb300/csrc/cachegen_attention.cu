@@ -49,7 +49,9 @@ size_t pass_bytes(const cg_int4_cache *c, int64_t rows, bool first)
     if (rows <= kFewRows)
         return few_bytes(c, rows);
     // a part each: the two kernels may run side by side
-    return (first ? 0 : few_bytes(c, rows)) + align256(attn_many_workspace(c->head_size, first));
+    if (first)
+        return align256(attn_many_workspace(c->head_size, attn_many_items(rows, c->num_heads)));
+    return few_bytes(c, rows) + align256(attn_many_workspace(c->head_size, 0));
 }
 
 cg_status launch_pass(const cg_int4_cache *c, const AttnArgs &p, uint8_t *workspace, cudaStream_t s)
@@ -230,6 +232,7 @@ extern "C" cg_status cg_int4_attention_shared(const cg_int4_cache *c, int32_t la
                                        align256(rows * c->head_size * sizeof(float)));
     AttnArgs first = p;
     first.first = true;
+    first.items = attn_many_items(all_rows(c, a), c->num_heads);
     first.pos_ratio = INT32_MAX;
     first.a.cu_q += a->requests;
     first.a.requests = 1;
@@ -237,7 +240,7 @@ extern "C" cg_status cg_int4_attention_shared(const cg_int4_cache *c, int32_t la
     // however many rows there are, they go to one kernel
     first.few_rows = all_rows(c, a) <= kFewRows ? kFewRows : 0;
     // a block begins and ends a unit for as long as it reads some 16 blobs: short ones are not strung
-    // together (4 requests of 7 to 65 tokens, 12 heads: 54 us with, FIG without)
+    // together (4 requests of 7 to 65 tokens, 12 heads: 54 us with, 14 without)
     p.least_unit = 16;
     p.a.block_table += shared / c->page_tokens;
     p.a.table_width -= shared / c->page_tokens;

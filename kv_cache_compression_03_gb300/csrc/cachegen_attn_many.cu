@@ -228,7 +228,7 @@ struct ManyShared {
 
 // Most blocks, hence most items of a batch that is cut; and most items of shared tokens, whose units
 // are cut in more pieces than blocks.
-constexpr int kMaxBlocks = 160, kMaxItems = 640;
+constexpr int kMaxBlocks = 160, kMaxItems = 640, kMaxSplit = 31;
 
 // Workspace: how the batch was cut, the units, and of each item 256 rows of
 // { float o[D] }, then { float m }, { float l }. Where the softmax groups take
@@ -338,7 +338,7 @@ __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t item, int s
 __device__ __forceinline__ int split_of_equals(int units, int n, int items)
 {
     const int lane = threadIdx.x & 31, whole = units > 0 ? (int)gridDim.x / units : 0;
-    const int s = lane < 31 ? lane + 1 : max(whole, 1);
+    const int s = lane < kMaxSplit ? lane + 1 : max(whole, 1);
     const int64_t turns = ((int64_t)units * s + gridDim.x - 1) / gridDim.x;
     const int64_t cost = turns * ((n + s - 1) / s + 3);
     const bool can = s == 1 || (s <= n / 2 && (int64_t)units * s <= items);
@@ -1013,7 +1013,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
 
 // Rows of units that were cut, a warp to a row: the parts' accumulators, weighted by
 // 2^(m - max m), in the order of the parts.
-constexpr int kJoinBlocks = 608, kJoinThreads = 128;   // four blocks on each of 152 SMs
+constexpr int kJoinThreads = 128;
+
+// Blocks: four on each of 152 SMs, and ten for shared tokens, where there may be 50000 rows and what counts is
+// how many loads are under way (25200 rows in three parts: 30 us with ten, 64 with four).
+constexpr int join_blocks(bool first) { return first ? 1520 : 608; }
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p, ManyWork work)
@@ -1024,7 +1028,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
     if (work.cut[1] == 1)
         return;
     const int lane = threadIdx.x & 31, rows = work.cut[0] * kRows;   // fewer units than blocks
-    for (int at = (blockIdx.x * kJoinThreads + threadIdx.x) >> 5; at < rows; at += kJoinBlocks * kJoinThreads / 32) {
+    for (int at = (blockIdx.x * kJoinThreads + threadIdx.x) >> 5; at < rows; at += gridDim.x * kJoinThreads / 32) {
         const Unit &u = work.heads[at / kRows];
         const int row = at % kRows, rr = u.row0 + row;
         if (u.parts == 1 || rr >= u.rows)
@@ -1100,8 +1104,6 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
 
 constexpr size_t head_bytes(int items) { return 256 + (sizeof(Unit) * items + 255) / 256 * 256; }
 
-constexpr int most_items(bool first) { return first ? kMaxItems : kMaxBlocks; }
-
 template <typename B>
 cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
 {
@@ -1112,7 +1114,7 @@ cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
         err = cudaFuncSetAttribute(k_attention_many<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess)
         return err;
-    const int items = most_items(p.first), blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
+    const int items = p.first ? p.items : kMaxBlocks, blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
     const ManyWork work = {items, reinterpret_cast<int32_t *>(ws), reinterpret_cast<Unit *>(ws + 256),
                            reinterpret_cast<float *>(ws + head_bytes(items))};
     if (p.first) {   // the call's first kernel: it follows what is in the stream
@@ -1122,15 +1124,21 @@ cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
         err = launch_under(k_attention_many<B>, dim3(blocks), kThreads, smem, s, p, work);
     }
     if (err == cudaSuccess)
-        err = launch_under(k_attention_many_join<B::kD>, dim3(kJoinBlocks), kJoinThreads, 0, s, p, work);
+        err = launch_under(k_attention_many_join<B::kD>, dim3(join_blocks(p.first)), kJoinThreads, 0, s, p, work);
     return err;
 }
 
 }  // namespace
 
-size_t attn_many_workspace(int head_size, bool first)
+int attn_many_items(int64_t rows, int heads)
 {
-    const int items = most_items(first);
+    const int64_t most = (rows + kRows - 1) / kRows * heads * kMaxSplit;
+    return most < kMaxBlocks ? kMaxBlocks : most < kMaxItems ? (int)most : kMaxItems;
+}
+
+size_t attn_many_workspace(int head_size, int items)
+{
+    items = items > 0 ? items : kMaxBlocks;
     return head_bytes(items) + items * (size_t)kRows * (head_size + 2) * sizeof(float);
 }
 

@@ -1202,6 +1202,7 @@ struct WeighSizes {
 };
 
 constexpr size_t kMostScores = (size_t)256 << 20;   // bytes
+constexpr int32_t kMostTokens = INT32_MAX - 65535;
 
 WeighSizes sizes_of(const cg_int4_cache *c, const cg_attention *a, const cg_token_weights *w)
 {
@@ -1213,7 +1214,7 @@ WeighSizes sizes_of(const cg_int4_cache *c, const cg_attention *a, const cg_toke
     z.rows = (int32_t)(rows < INT32_MAX ? rows : INT32_MAX);
     z.tokens = (int32_t)(((limit < w->width ? limit : w->width) + 15) / 16 * 16);
     // Scores are stored, and not computed again, where there is room for those that the batch can have (128
-    // rows at 32768 tokens, 8 heads: FIGA us so, 123 computed again; more than the L2 holds would be
+    // rows at 32768 tokens, 8 heads: 115 us so, 123 computed again; more than the L2 holds would be
     // read from memory at no gain: 8192 rows at 2048, two requests, 1 GB).
     const size_t lists = (size_t)a->requests * c->num_heads;
     z.stored = lists == 0 || (size_t)z.rows * z.tokens <= kMostScores / sizeof(float) / lists;
@@ -1246,6 +1247,9 @@ extern "C" cg_status cg_int4_weigh_workspace(const cg_int4_cache *c, const cg_at
     cg_status st = attn_check_sizes(c, a);
     if (st == CG_OK)
         st = check_weights(w);
+    // (a block's last tokens count past a request's)
+    if (st == CG_OK && (int64_t)a->table_width * c->page_tokens > kMostTokens && w->width > kMostTokens)
+        st = CG_ERR_UNSUPPORTED;
     if (st == CG_OK)
         *bytes = sizes_of(c, a, w).bytes();
     return st;

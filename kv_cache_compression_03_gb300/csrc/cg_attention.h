@@ -17,6 +17,7 @@ struct AttnArgs {
     // tokens behind them (the table and the lengths begin there) and joins the two.
     int32_t shared;         // 0: none
     bool first;             // the pass over the shared tokens
+    int32_t items;          // its items that the workspace holds
     int32_t pos_ratio;      // rows to a position: ratio; more than there are where all rows see alike
     float *rows;            // [tokens * q_heads][head_size], normalised; nullptr: no shared tokens
     float2 *row_stats;      // [tokens * q_heads]: maximum of the scores, sum
@@ -218,5 +219,8 @@ constexpr int kFewMaxBlocks = 480;
 size_t attn_few_workspace(int head_size, int max_rows);
 cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max_rows, void *ws,
                             cudaStream_t s);
-size_t attn_many_workspace(int head_size, bool first);
+// Items that the shared tokens of `rows` rows of each KV head may be cut into; bytes for so many (0: for a
+// pass over own tokens).
+int attn_many_items(int64_t rows, int heads);
+size_t attn_many_workspace(int head_size, int items);
 cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, void *ws, cudaStream_t s);

@@ -202,6 +202,45 @@ def test_weigh_without_rows_or_requests():
     assert torch.equal(a, b)
 
 
+def test_weigh_with_tables_and_rows_of_other_widths():
+    """The same call but for how far its table and its weights reach."""
+    rng = np.random.default_rng(21)
+    nkv = [40, 33]
+    table, want, got, cu, q = _weigh_case(rng, [1, 1], nkv, 4, 64, 32, 16)
+    exact, tol = evict.weigh(want, 0, q, cu, nkv, table, 0, 0, 0.125, 64)
+    for wide, width in ((3, 40), (3, 64), (200, 40), (4000, 64), (4000, 60000), (3, 40)):
+        t = np.full((2, wide), -1, np.int32)
+        t[:, :3] = table[:, :3]
+        w = torch.zeros(2, 2, width, device="cuda")
+        got.weigh(_dev(q), _ints(cu), _ints(nkv), _ints(t), w, max_q_len=1)
+        got.check()
+        out = w.cpu().numpy()
+        for r, m in enumerate(nkv):
+            assert (np.abs(out[r, :, :m] - exact[r, :, :m]) <= tol[r, :, :m] + 2.0 ** -23).all()
+            assert not out[r, :, m:].any()
+
+
+@pytest.mark.parametrize("nq,ratio", [(1, 4), (2, 4), (9, 1), (30, 2), (300, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 5)])
+def test_weigh_with_and_without_room_for_scores(nq, ratio, window, sinks):
+    """Rows of weights so wide that scores cannot be stored for the batch: computed twice instead, with the same result."""
+    rng = np.random.default_rng(nq)
+    nkv = [nq + 700, nq, nq + 33]
+    table, want, got, cu, q = _weigh_case(rng, [nq] * 3, nkv, ratio, 128, 64, 16)
+    wide = np.full((3, 1 << 18), -1, np.int32)     # 2^22 tokens a row: 400 MB of scores for 6 lists and 4 rows
+    wide[:, :table.shape[1]] = table
+    exact, tol = evict.weigh(want, 0, q, cu, nkv, table, window, sinks, 128 ** -0.5, table.shape[1] * 16)
+    kw = dict(window=window, sinks=sinks, max_q_len=nq)
+    few = got.weigh(_dev(q), _ints(cu), _ints(nkv), _ints(table), **kw).cpu().numpy()
+    base = torch.zeros(3, 2, 1 << 22, device="cuda")
+    got.weigh(_dev(q), _ints(cu), _ints(nkv), _ints(wide), base, **kw)
+    got.check()
+    many = base[..., :few.shape[-1]].cpu().numpy()
+    assert not base[..., few.shape[-1]:].any()
+    for out in (few, many):
+        _check_weights(out, np.zeros_like(out), exact, tol)
+
+
 @pytest.mark.parametrize("n", [33, 300])
 def test_weigh_many_requests(n):
     rng = np.random.default_rng(n)

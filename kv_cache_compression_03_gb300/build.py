@@ -17,9 +17,11 @@ LIB = os.path.join(OUT_DIR, "libcachegen.so")
 
 SOURCES = ["cachegen_kernels.cu", "cachegen_api.cu", "cachegen_noalloc.cu", "cachegen_int8.cu",
            "cachegen_int4.cu", "cachegen_pages.cu", "cachegen_attention.cu",
-           "cachegen_attn_few.cu", "cachegen_attn_many.cu", "cachegen_weigh.cu", "cachegen_evict.cu"]
+           "cachegen_attn_few.cu", "cachegen_attn_many.cu", "cachegen_weigh.cu",
+           "cachegen_weigh_many.cu", "cachegen_evict.cu"]
 HEADERS = [os.path.join(CSRC, "cg_internal.h"), os.path.join(CSRC, "cg_int4.h"),
            os.path.join(CSRC, "cg_attention.h"), os.path.join(CSRC, "cg_few.h"),
+           os.path.join(CSRC, "cg_tiles.h"), os.path.join(CSRC, "cg_weigh.h"),
            os.path.join(INCLUDE, "cachegen.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",

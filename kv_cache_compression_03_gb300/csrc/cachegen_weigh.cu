@@ -10,7 +10,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "cg_few.h"
+#include "cg_weigh.h"
 
 namespace {
 
@@ -19,49 +19,12 @@ constexpr int kItemTokens = 64;    // of a block in the second pass, a blob to a
 constexpr int kManyRows = 512;     // from so many rows on, a blob to a block, whose warps share the rows
 constexpr int kMaxBlocks = 640;    // of the first pass
 
-struct WeighArgs {
-    cg_token_weights w;
-    float2 *parts;       // [block][2][rows of a tile]: m, l of pieces; slot 0 began in an earlier block
-    float2 *stats;       // [heads][slots][8]: m, 1 / l (0, 0: no such row, or it sees nothing)
-    int32_t slots;       // row tiles of 8 of all requests
-    // what the second pass works from, either
-    uint4 *queries;      // [heads][slots][words][32]: the second factor, as a lane of the warp has it
-    float *factors;      // [heads][slots][groups + 1][8]: rho, sq
-    // or
-    float *scores;       // [requests][heads][rows][tokens]
-    int32_t rows, tokens;
-};
-
-// Row tiles of 8 of request r lie from here on. (Of a rows before it and b of its own, ceil(b / 8)
-// is at most floor((a + b) / 8) - floor(a / 8) + 1.)
-__device__ __forceinline__ int32_t first_slot(const AttnArgs &p, int r, int32_t row0)
-{
-    return (int32_t)((int64_t)row0 * p.ratio / 8) + r;
-}
-
-// The lane, read once: kept, not read again wherever it is used.
-__device__ __forceinline__ int lane_once()
-{
-    int lane;
-    asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));
-    return lane;
-}
-
 // ------------------------------------------------------------------- scores
 
 // With mid = lo + 8 s and m = n - 8 in [-8, 7], q.k^ = sum_g s_g (q.m)_g + mid_g (sum q)_g. Where a
 // few channels of a group are large, s and lo follow those and the others' codes lie near 8:
 // q.n and lo (sum q) would be large and cancel (an error of 1.3e-5 in the weights, of 2e-7 so). The
 // products of bf16 pairs are exact, everything else is fp32.
-
-// Codes i and i + 4 of a word, less 8, as a bf16 pair: exact out of the mantissa of 128 + n.
-__device__ __forceinline__ uint32_t centred(uint32_t w, int i)
-{
-    const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    uint32_t y;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x43084308u));
-    return y;
-}
 
 // The queries of 8 rows of a KV head, from row0 on. qf: the second factor of the instruction, column
 // g is the row row0 + g times a power of two that brings it below 2^-7 (so that no s (q.m) overflows
@@ -357,11 +320,6 @@ __device__ __forceinline__ float raise(float top, bool no_row, float *m, float *
     if (none && !(top > kNone) && !no_row)
         *limit = kNone;
     return up;
-}
-
-__device__ __forceinline__ float2 row_stats_of(float m, float l)
-{
-    return l == 0.0f ? make_float2(0.0f, 0.0f) : make_float2(m, 1.0f / l);
 }
 
 // Blocks on an SM.
@@ -918,53 +876,6 @@ __global__ void __launch_bounds__(kThreads) k_weigh_join(AttnArgs p, int pieces,
 
 // -------------------------------------------------------------- sums of tokens
 
-// Items of each(q) tokens of a (request, KV head), those of all heads of the first tokens first. One
-// warp finds its item, going on from where the last call stood (32 requests from r0 on, `before`
-// items ahead of them): false when there are no more. Requests without rows have items too.
-struct Items {
-    int r0;
-    int64_t before;
-};
-
-template <typename F>
-__device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, F each, Items *at, AttnRequest *q, int *r,
-                                          int *h, int *tok)
-{
-    const int lane = threadIdx.x & 31;
-    for (;; at->r0 += 32) {
-        if (at->r0 >= p.a.requests)
-            return false;
-        uint32_t error;
-        int64_t w = 0;
-        if (at->r0 + lane < p.a.requests) {
-            attn_request(p, at->r0 + lane, q, &error);
-            if (error == CG_OK)
-                w = (int64_t)((q->kv + each(*q) - 1) / each(*q)) * p.heads;
-        }
-        int64_t inc = w;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, inc, d);
-            if (lane >= d)
-                inc += o;
-        }
-        const int64_t start = at->before + inc - w;
-        const uint32_t mine = __ballot_sync(0xFFFFFFFFu, item >= start && item < start + w);
-        if (mine == 0) {
-            at->before += __shfl_sync(0xFFFFFFFFu, inc, 31);
-            continue;
-        }
-        const int src = __ffs(mine) - 1;
-        const int64_t off = __shfl_sync(0xFFFFFFFFu, item - start, src);
-        *r = at->r0 + src;
-        attn_request(p, *r, q, &error);
-        const int i = (int)(off / p.heads);
-        *h = (int)(off - (int64_t)i * p.heads);
-        *tok = i * each(*q);
-        return true;
-    }
-}
-
 // A warp takes a blob of a (request, KV head), whose keys stay in its registers, over the rows that see any
 // of its tokens: all of those, or where there are many a quarter, every fourth tile of 8.
 template <typename B>
@@ -980,7 +891,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
         AttnRequest q;
         int r, h, t0;
-        if (!find_item(p, item, [](const AttnRequest &x) { return x.rows >= kManyRows ? 16 : kItemTokens; }, &items, &q,
+        if (!find_item(p, item, [&](const AttnRequest &x) { return x.rows > p.few_rows ? 0 : x.rows >= kManyRows ? 16 : kItemTokens; }, &items, &q,
                        &r, &h, &t0))
             return;
         const bool shared = q.rows >= kManyRows;   // the block's warps have the same tokens
@@ -1115,7 +1026,7 @@ __global__ void __launch_bounds__(kThreads) k_weigh_apply(AttnArgs p, WeighArgs 
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
         AttnRequest q;
         int r, h, t0;
-        if (!find_item(p, item, [](const AttnRequest &) { return kTokens; }, &items, &q, &r, &h, &t0))
+        if (!find_item(p, item, [&](const AttnRequest &x) { return x.rows > p.few_rows ? 0 : kTokens; }, &items, &q, &r, &h, &t0))
             return;
         t0 += threadIdx.x;
         const float *in = a.w.in == nullptr ? nullptr : a.w.in + r * a.w.in_request_stride + h * a.w.in_head_stride;
@@ -1196,10 +1107,15 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // How a call goes, and the parts of its workspace.
 struct WeighSizes {
     int32_t slots, rows, tokens;   // rows of a request's KV head, and tokens, at most
-    bool stored;
-    size_t parts, stats, queries, factors, scores;
-    size_t bytes() const { return parts + stats + queries + factors + scores; }
+    bool stored, tiles;            // scores are stored; requests with many rows go by tiles
+    size_t parts, stats, queries, factors, scores, many;
+    size_t bytes() const { return parts + stats + queries + factors + scores + many; }
 };
+
+// Requests with more rows than this go to the kernels for many (cachegen_weigh_many.cu), where there is room
+// for their sums by row tiles.
+constexpr int kTileRows = 64;
+constexpr size_t kMostSums = (size_t)1 << 30;   // bytes
 
 constexpr size_t kMostScores = (size_t)256 << 20;   // bytes
 constexpr int32_t kMostTokens = INT32_MAX - 65535;
@@ -1211,8 +1127,13 @@ WeighSizes sizes_of(const cg_int4_cache *c, const cg_attention *a, const cg_toke
     const int n = a->max_q_len > 0 && a->max_q_len < a->tokens ? a->max_q_len : a->tokens;
     const int64_t rows = (int64_t)n * ratio, limit = (int64_t)a->table_width * c->page_tokens;
     z.slots = (int32_t)((int64_t)a->tokens * ratio / 8 + a->requests + 1);
-    z.rows = (int32_t)(rows < INT32_MAX ? rows : INT32_MAX);
     z.tokens = (int32_t)(((limit < w->width ? limit : w->width) + 15) / 16 * 16);
+    if (rows > kTileRows) {
+        z.many = weigh_many_workspace(c, a, z.tokens);
+        z.tiles = z.many <= kMostSums;
+        z.many = z.tiles ? align256(z.many) : 0;
+    }
+    z.rows = (int32_t)(z.tiles ? kTileRows : rows);
     // Scores are stored, and not computed again, where there is room for those that the batch can have (128
     // rows at 32768 tokens, 8 heads: 115 us so, 123 computed again; more than the L2 holds would be
     // read from memory at no gain: 8192 rows at 2048, two requests, 1 GB).
@@ -1280,10 +1201,10 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
     if (workspace_bytes < need || workspace == nullptr)
         return CG_ERR_CAPACITY;
     AttnArgs p = attn_args(c, layer, a);
-    p.few_rows = INT32_MAX;
+    const WeighSizes z = sizes_of(c, a, w);
+    p.few_rows = z.tiles ? kTileRows : INT32_MAX;
     if (p.kv_limit > w->width)
         p.kv_limit = w->width;
-    const WeighSizes z = sizes_of(c, a, w);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     auto take = [&](size_t n) {
         uint8_t *at = ws;
@@ -1300,8 +1221,10 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
     args.queries = reinterpret_cast<uint4 *>(take(z.queries));
     args.factors = reinterpret_cast<float *>(take(z.factors));
     args.scores = reinterpret_cast<float *>(take(z.scores));
+    args.sums = nullptr;
+    args.tiles = 0;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
+    cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
         using B = decltype(blob);
         if (z.stored && z.rows <= 8)
             return launch<8, FewShared<B>, B>(z.rows <= 4 ? k_weigh_few<B, 2> : k_weigh_few<B, 1>, kFewBlocks, p, args, true, s);
@@ -1310,5 +1233,7 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
         return launch<32, StatShared<B, 4>, B>(z.stored ? k_weigh_stats<B, 4, true> : k_weigh_stats<B, 4, false>,
                                                kStatBlocks, p, args, z.stored, s);
     });
+    if (err == cudaSuccess && z.tiles)
+        err = weigh_many_launch(p, args, c, ws, s);
     return err == cudaSuccess ? CG_OK : CG_ERR_CUDA;
 }

@@ -30,7 +30,7 @@ namespace {
 
 constexpr int kSoftWarps = 8, kExpandWarps = 8;
 constexpr int kAllWarps = kSoftWarps + kExpandWarps + 2, kAllThreads = 32 * kAllWarps;
-constexpr int kPlaces = 8;       // blobs copied ahead
+constexpr int kPlaces = 24;      // blobs copied ahead
 constexpr int kIssue = 4;        // of those, copied at once
 constexpr int kTile = 128;       // rows, and tokens
 constexpr int kBlobs = kTile / 16;
@@ -58,9 +58,9 @@ constexpr int kGroupSteps = B::kGroups == 4 ? 2 : 1;
 template <typename B>
 struct TileShared {
     uint8_t q[kTile * B::kD * 2];
-    uint8_t qx[kTile * 128];
+    uint8_t qx[kTile * 64];
     uint8_t k[2][2][kTile * B::kD * 2];     // high and low parts
-    uint8_t kx[2][kTile * 128];
+    uint8_t kx[2][kTile * 64];
     uint8_t ring[kPlaces][B::kVCodes];
     float4 row[kKnown][kTile / 2];          // of two rows: rho, rho, -m, -m
     float2 inv[kKnown][kTile / 2];          // and 1 / l
@@ -165,11 +165,13 @@ __device__ __forceinline__ void find_piece(const AttnArgs &p, int64_t item, int 
     }
 }
 
-__device__ __forceinline__ uint32_t fma2_bf16(uint32_t a, uint32_t b, uint32_t c)
+// c s - hi of bf16 pairs, exact where hi is the product rounded.
+__device__ __forceinline__ uint32_t rest_of(uint32_t c, uint32_t s, uint32_t hi)
 {
-    uint32_t d;
-    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
-    return d;
+    const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&c),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&s),
+                                     __hneg2(*reinterpret_cast<const __nv_bfloat162 *>(&hi)));
+    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // x in three bf16 values (the high halves): 24 bits.
@@ -435,6 +437,10 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
         auto put = [&](uint8_t *tile, int row, int c, uint4 v) {
             *reinterpret_cast<uint4 *>(tile + (c >> 3) * kSub + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v;
         };
+        // and of a row of 64 bytes
+        auto put_group = [&](uint8_t *tile, int row, int c, uint4 v) {
+            *reinterpret_cast<uint4 *>(tile + row * 64 + ((c ^ (row >> 1 & 3)) << 4)) = v;
+        };
         uint32_t seq = 0;            // blobs of earlier pieces
         while (const Piece *up = next_piece()) {
             const Piece &u = *up;
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                     uint32_t part[3];
                     three_parts(mine, part);
                     if (t < kGroupChunks)   // 0 1 2 0 1 0 beside 0 0 0 1 1 2 of the keys
-                        put(sm.qx, in, t, make_uint4(part[0] >> 16 | part[1], part[2] >> 16 | part[0], part[1] >> 16 | part[0], 0));
+                        put_group(sm.qx, in, t, make_uint4(part[0] >> 16 | part[1], part[2] >> 16 | part[0], part[1] >> 16 | part[0], 0));
                     if (t == 0) {
                         float *f = reinterpret_cast<float *>(&sm.row[qn % kKnown][in >> 1]) + (in & 1);
                         f[0] = rho;
@@ -538,7 +544,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                         for (int k = 0; k < 4; ++k) {
                             const uint32_t c = centred(code[w], k);
                             hi[k] = mul_bf16x2(c, s2);
-                            lo[k] = fma2_bf16(c, s2, hi[k] ^ 0x80008000u);   // exact
+                            lo[k] = rest_of(c, s2, hi[k]);
                         }
                         put(sm.k[sl][0], row, 4 * w + t, make_uint4(hi[0], hi[1], hi[2], hi[3]));
                         put(sm.k[sl][1], row, 4 * w + t, make_uint4(lo[0], lo[1], lo[2], lo[3]));
@@ -551,7 +557,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                                 mine = par[k];
                         uint32_t part[3];
                         three_parts(fmaf(8.0f, par_s(mine), par_lo(mine)), part);
-                        put(sm.kx[sl], row, t, make_uint4(part[0] >> 16 | part[0], part[0] >> 16 | part[1],
+                        put_group(sm.kx[sl], row, t, make_uint4(part[0] >> 16 | part[0], part[0] >> 16 | part[1],
                                                           part[1] >> 16 | part[2], 0));
                     }
                 }
@@ -654,13 +660,15 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                         const uint32_t dq = smem_desc(q) + off, dk = smem_desc(k) + off;
                         mma_ss(tmem + 128 * sl, kSums ? dk : dq, kSums ? dq : dk, mma_desc(kTile), add);
                     };
+                    const uint32_t dqx = smem_desc(qx_at), dkx = smem_desc(kx_at + sl * (kTile * 64));
                     // the small parts first: an accumulator loses most where it is large
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         product(q_at, k_at + (2 * sl + 1) * kHalf, ((kk >> 2) * kSub + (kk & 3) * 32) >> 4, kk > 0);
 #pragma unroll
                     for (int kk = 0; kk < kGroupSteps<B>; ++kk)
-                        product(qx_at, kx_at + sl * kSub, kk * 32 >> 4, true);
+                        mma_ss<kDescHigh64>(tmem + 128 * sl, (kSums ? dkx : dqx) + 2 * kk, (kSums ? dqx : dkx) + 2 * kk,
+                                            mma_desc(kTile), true);
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk)
                         product(q_at, k_at + 2 * sl * kHalf, ((kk >> 2) * kSub + (kk & 3) * 32) >> 4, true);
@@ -700,28 +708,39 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
     grid_wait();
 }
 
-// A row's parts: of each piece of its unit, either half of the tiles.
-__global__ void __launch_bounds__(kTile) k_weigh_tiles_join(AttnArgs p, WeighArgs a, TileWork work)
+// A row's parts: of each piece of its unit, either half of the tiles. Slices of the block take them in turns.
+constexpr int kJoinSlices = 4, kJoinThreads = kTile * kJoinSlices;
+
+__global__ void __launch_bounds__(kJoinThreads) k_weigh_tiles_join(AttnArgs p, WeighArgs a, TileWork work)
 {
+    __shared__ float2 slices[kJoinSlices][kTile];
+    const int row = threadIdx.x % kTile, slice = threadIdx.x / kTile;
     grid_next();
     grid_wait();
     for (int at = blockIdx.x; at < work.cut[0]; at += gridDim.x) {
         const Piece &u = work.heads[at];
-        const int row = threadIdx.x, n = 2 * u.parts;
-        if (row >= (min(kTile, u.rows - u.row0) + 7) / 8 * 8)
-            continue;
+        const int n = 2 * u.parts;
         const float2 *parts = work.parts + (int64_t)u.item * 2 * kTile + row;
         float mx = kNone, l = 0.0f;
 #pragma unroll 8
-        for (int k = 0; k < n; ++k)
-            mx = fmaxf(mx, parts[(int64_t)k * kTile].x);
-#pragma unroll 8
-        for (int k = 0; k < n; ++k) {
+        for (int k = slice; k < n; k += kJoinSlices) {
             const float2 part = parts[(int64_t)k * kTile];
-            l = fmaf(part.y, exp2_fast(part.x - mx), l);
+            const float up = fmaxf(mx, part.x);
+            l = l * exp2_fast(mx - up) + part.y * exp2_fast(part.x - up);
+            mx = up;
         }
-        a.stats[((int64_t)u.h * a.slots + first_slot(p, u.r, u.q_row0) + u.row0 / 8) * 8 + row] =
-            u.row0 + row < u.rows ? row_stats_of(mx, l) : make_float2(0.0f, 0.0f);
+        slices[slice][row] = make_float2(mx, l);
+        __syncthreads();
+        if (slice == 0 && row < (min(kTile, u.rows - u.row0) + 7) / 8 * 8) {
+            for (int k = 1; k < kJoinSlices; ++k)
+                mx = fmaxf(mx, slices[k][row].x);
+            l = 0.0f;
+            for (int k = 0; k < kJoinSlices; ++k)
+                l = fmaf(slices[k][row].y, exp2_fast(slices[k][row].x - mx), l);
+            a.stats[((int64_t)u.h * a.slots + first_slot(p, u.r, u.q_row0) + u.row0 / 8) * 8 + row] =
+                u.row0 + row < u.rows ? row_stats_of(mx, l) : make_float2(0.0f, 0.0f);
+        }
+        __syncthreads();
     }
 }
 
@@ -741,16 +760,21 @@ __global__ void __launch_bounds__(kAddThreads) k_weigh_add(AttnArgs p, WeighArgs
         const int tok = t0 + threadIdx.x, blob = tok / 16;
         if (tok >= q.kv)
             continue;
-        const int tiles = (q.rows + kTile - 1) / kTile;
+        // Row tile i sees the blob from where its last row reaches position 16 blob on: row (16 blob - x0) ratio;
+        // under a window, if the blob is not of the first tokens, up to where its first row leaves the blob's
+        // last token behind: position 16 blob + 15 + window.
+        const int64_t from = (16 * (int64_t)blob - q.x0) * p.ratio, tiles = (q.rows + kTile - 1) / kTile;
+        const int64_t i0 = from > 0 ? from / kTile : 0;
+        int64_t i1 = tiles;
+        if (p.a.window > 0 && blob >= ((int64_t)p.a.sinks + 15) / 16) {
+            const int64_t rows = (16 * (int64_t)blob + 15 + p.a.window - q.x0) * p.ratio;   // that begin before
+            i1 = rows <= 0 ? 0 : min(i1, (rows + kTile - 1) / kTile);
+        }
         const float *sums = a.sums + ((int64_t)h * a.tiles + first_tile(p, r, q.row0)) * a.tokens + tok;
         float total = 0.0f;
-#pragma unroll 4
-        for (int i = 0; i < tiles; ++i) {
-            int nb, sink, skip;
-            blobs_of(p, q.x0, i * kTile, min(kTile, q.rows - i * kTile), &nb, &sink, &skip);
-            if (blob < nb + skip && (blob < sink || blob >= sink + skip))
-                total += sums[(int64_t)i * a.tokens];
-        }
+#pragma unroll 8
+        for (int64_t i = i0; i < i1; ++i)
+            total += sums[i * a.tokens];
         const float had = a.w.in == nullptr ? 0.0f : a.w.in[r * a.w.in_request_stride + h * a.w.in_head_stride + tok];
         a.w.out[r * a.w.out_request_stride + h * a.w.out_head_stride + tok] = had + total;
     }
@@ -807,7 +831,7 @@ cudaError_t weigh_many_launch(const AttnArgs &p, WeighArgs a, const cg_int4_cach
         if (e == cudaSuccess)
             e = launch_under(k_weigh_tiles<B, false>, dim3(blocks), kAllThreads, smem, s, p, a, work);
         if (e == cudaSuccess)
-            e = launch_under(k_weigh_tiles_join, dim3(8 * blocks), kTile, 0, s, p, a, work);
+            e = launch_under(k_weigh_tiles_join, dim3(2 * blocks), kJoinThreads, 0, s, p, a, work);
         if (e == cudaSuccess)
             e = launch_under(k_weigh_tiles<B, true>, dim3(blocks), kAllThreads, smem, s, p, a, work);
         if (e == cudaSuccess)

@@ -11,6 +11,8 @@
 // varies; it is passed as 32 bits, so that a product takes few registers over to
 // the uniform file (what the issuing thread spends its time on).
 constexpr uint32_t kDescHigh = 64u | 1u << 14 | 2u << 29;
+// The same of rows of 64 bytes, 64-byte swizzle, groups of 8 rows 512 bytes apart.
+constexpr uint32_t kDescHigh64 = 32u | 1u << 14 | 4u << 29;
 __device__ __forceinline__ uint32_t smem_desc(uint32_t at) { return (at >> 4 & 0x3FFF) | 1u << 16; }
 
 // bf16 x bf16 -> fp32, both operands K-major, M = 128.
@@ -19,12 +21,14 @@ __host__ __device__ constexpr uint32_t mma_desc(int n)
     return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | (uint32_t)(128 >> 4) << 24;
 }
 
+// kHigh: the descriptors' high word.
+template <uint32_t kHigh = kDescHigh>
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t desc, bool add)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 a, {%1, %5};\n\t"
         "mov.b64 b, {%2, %5};\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kDescHigh)
+        "r"(a), "r"(b), "r"(desc), "r"((uint32_t)add), "r"(kHigh)
         : "memory");
 }
 

@@ -121,6 +121,68 @@ def test_weigh_of_channels_that_differ():
     assert np.linalg.norm(out - exact) / np.linalg.norm(exact) < 2.0 ** -19
 
 
+@pytest.mark.parametrize("nq,nkv,ratio,heads", [([200] * 4, [250, 200, 777, 201], 7, 8),    # 352 units of 128 rows
+                                                 ([129], [3000], 1, 1),                     # 2 units, cut in pieces
+                                                 ([65, 1, 0, 90], [65, 900, 30, 40], 3, 2),  # rows before the first token
+                                                 ([33] * 3, [40, 1033, 129], 2, 3),          # 66 rows, few beside
+                                                 ([700], [700], 5, 2)])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (1, 0), (100, 17), (257, 3)])
+@pytest.mark.parametrize("dim,group,page", [(128, 32, 64), (64, 32, 16), (128, 128, 48)])
+def test_weigh_of_many_rows(nq, nkv, ratio, heads, window, sinks, dim, group, page):
+    rng = np.random.default_rng(sum(nkv) + window + dim)
+    table, want, got, cu, q = _weigh_case(rng, nq, nkv, ratio, dim, group, page, heads=heads)
+    width = table.shape[1] * page
+    exact, tol = evict.weigh(want, 0, q, cu, nkv, table, window, sinks, dim ** -0.5, width)
+    out = torch.zeros(len(nq), heads, width, device="cuda")
+    args = (_dev(q), _ints(cu), _ints(nkv), _ints(table))
+    got.weigh(*args, out, window=window, sinks=sinks, max_q_len=max(nq))
+    got.check()
+    got_w = out.cpu().numpy()
+    _check_weights(got_w, np.zeros_like(got_w), exact, tol)
+    assert not got_w[np.isnan(exact)].any()
+    # the weights of each row sum to one
+    for r, m in enumerate(nkv):
+        assert np.allclose(got_w[r].sum(-1), ratio * min(nq[r], m), rtol=2.0 ** -12, atol=0)
+    norm = np.linalg.norm(np.nan_to_num(exact))
+    assert np.linalg.norm(got_w - np.nan_to_num(exact)) / norm < 2.0 ** -19
+
+
+def test_weigh_of_many_rows_reports_bad_pages():
+    rng = np.random.default_rng(31)
+    nq, m, page = 150, 900, 16
+    table, want, got, cu, q = _weigh_case(rng, [nq], [m], 2, 64, 32, page)
+    bad = table.copy()
+    bad[0, [3, 20, 21]] = [1 << 20, -1, 1 << 30]
+    out = got.weigh(_dev(q), _ints(cu), _ints([m]), _ints(bad)).cpu().numpy()
+    _status(got.check, cg.CG_ERR_CORRUPT)
+    gone = np.r_[48:64, 320:352]
+    assert not out[0, :, gone].any() and np.isfinite(out).all()
+    assert np.allclose(out[0].sum(-1), 2 * nq, rtol=2.0 ** -12)
+    # as if those tokens were not there: the others' weights, renormalised row by row
+    keep = np.delete(np.arange(m), gone)
+    k, _, _ = want.values(0, table[0][keep // page] * page + keep % page)
+    for h in range(2):
+        exact = np.zeros(len(keep))
+        for g in range(2):
+            z = q[:, 2 * h + g].astype(np.float64) @ k[:, h].T * 0.125
+            z = np.where(keep[None, :] <= (m - nq + np.arange(nq))[:, None], z, -np.inf)
+            e = np.exp(z - z.max(1, keepdims=True))
+            exact += (e / e.sum(1, keepdims=True)).sum(0)
+        assert np.abs(out[0, h, keep] - exact).max() <= 2.0 ** -17 * exact.max()
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.3])
+@pytest.mark.parametrize("qscale", [1.0, 2.0 ** -100, 2.0 ** 60])
+def test_weigh_of_many_rows_scales(scale, qscale):
+    rng = np.random.default_rng(32)
+    table, want, got, cu, q = _weigh_case(rng, [90], [300], 2, 64, 32, 16)
+    q = ref.bf16_round(q * np.float32(qscale))
+    exact, tol = evict.weigh(want, 0, q, cu, [300], table, 0, 0, scale / qscale, 300)
+    out = got.weigh(_dev(q), _ints(cu), _ints([300]), _ints(table), scale=scale / qscale)
+    got.check()
+    _check_weights(out.cpu().numpy()[..., :300], np.zeros(exact.shape, np.float32), exact, tol)
+
+
 def test_weigh_strides_layers_and_streams():
     rng = np.random.default_rng(9)
     nq, nkv, ratio, heads, dim, page = [1, 2], [300, 77], 4, 3, 64, 16
@@ -582,6 +644,56 @@ def test_release_pages_reports_page_ids_outside_the_cache():
 
 
 # ------------------------------------------------------------ all together
+
+def test_requests_that_share_a_front_are_cut_and_attended():
+    """Three requests on 64 shared tokens, cut to a budget that keeps those, and attended with shared=:
+    the shared pages are read by all and written by none."""
+    rng = np.random.default_rng(13)
+    heads, ratio, dim, group, page, shared = 2, 4, 64, 64, 16, 64
+    own = [200, 90, 130]
+    lens = [shared + n for n in own]
+    held = [-(-n // page) for n in own]
+    pages = 4 + sum(held) + 1
+    want, got = _pair(1, pages, page, heads, dim, group)
+    ids = rng.permutation(pages)
+    table = np.full((3, 4 + max(held)), -1, np.int32)
+    table[:, :4], at = ids[:4], 4
+    for r, n in enumerate(held):
+        table[r, 4:4 + n] = ids[at:at + n]
+        at += n
+        x = np.arange(lens[r])[0 if r == 0 else shared:]
+        want.store(0, _rand(rng, len(x), heads, dim), _rand(rng, len(x), heads, dim), table[r][x // page] * page + x % page)
+    _copy(want, got)
+    q, cu = _rand(rng, 3, heads * ratio, dim), np.arange(4)
+    tab, dq, dcu = _ints(table), _dev(q), _ints(cu)
+    w = got.weigh(dq, dcu, _ints(lens), tab, max_q_len=1)
+    exact, tol = evict.weigh(want, 0, q, cu, lens, table, 0, 0, dim ** -0.5, w.shape[2])
+    _check_weights(w.cpu().numpy(), np.zeros(w.shape, np.float32), exact, tol)
+    before = w.cpu().numpy()[None].copy()
+    c = cg.choose_tokens(w, _ints(lens), 150, recent=20, sinks=shared)
+    kept, new = evict.choose(before, lens, 150, 20, shared)
+    assert np.array_equal(c.kept.cpu().numpy(), kept[0]) and np.array_equal(c.lens.cpu().numpy(), new)
+    got.compact(c.kept, c.lens, _ints(lens), tab, weights=w)
+    got.check()
+    front = want.data[0, table[0, :4]].copy()
+    evict.compact(want, 0, kept, new, lens, table, before)
+    assert np.array_equal(want.data[0, table[0, :4]], front)
+    _same_bytes(want, got)
+    out = got.attention(dq, dcu, c.lens, tab, max_q_len=1, shared=shared)
+    got.check()
+    o, tol = ref.attention(want, 0, q, cu, new, table, 0, 0, dim ** -0.5)
+    assert (np.abs(_np(out) - o) <= tol).all()
+    free, count = _ints([-7] * pages), _ints([0])
+    rel = cg.release_pages(tab, _ints(lens), c.lens, free, count, page, num_pages=pages)
+    rel.check()
+    # at its end a request gives back its own pages, the last one all of them
+    for r in range(3):
+        ends = [0 if i == r == 2 else shared if i <= r else n for i, n in enumerate(new)]
+        was = rel.lens.clone()
+        rel = cg.release_pages(tab, was, _ints(ends), free, rel.free_count, page, num_pages=pages)
+        rel.check()
+    assert sorted(free[:int(rel.free_count)].tolist()) == sorted(ids[:at].tolist())
+
 
 def test_a_cache_is_kept_to_its_budget():
     """grow -> store -> attention and weigh, step by step in a graph; then choose -> compact -> release in

@@ -614,7 +614,7 @@ __device__ __forceinline__ void load_few(const AttnArgs &p, const AttnRequest &r
 
 // z[j]: token g + 8 j with rows 2t and 2t + 1 (of their blob). `par`: the lane's blob, for its parameters.
 template <typename B, int P>
-__device__ __forceinline__ void few_scores(const uint8_t *const (&blob)[P], const uint8_t *par, const FewQueries<B, P> &q,
+__device__ __forceinline__ void few_scores(const uint8_t *(&blob)[P], const uint8_t *par, const FewQueries<B, P> &q,
                                            int lane, float2 (&z)[2])
 {
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
@@ -656,21 +656,24 @@ __device__ __forceinline__ void few_scores(const uint8_t *const (&blob)[P], cons
         z[j] = fma2(y[j], q.rho, z[j]);
 }
 
-constexpr int kPairs = 4;        // pairs of blobs in a warp's ring
 constexpr int kFewBlocks = 3;    // on an SM
 
-template <typename B>
+// A warp takes two accumulators' blobs in one step, two P: their chains mix, and what a step costs
+// besides (waits, copies, the look at the maximum) is halved.
+template <typename B, int P>
 struct FewShared {
-    uint8_t ring[kWarps][kPairs][2][B::kVCodes];
+    static constexpr int HB = 2 * P, kSteps = P == 2 ? 3 : 4;
+    uint8_t ring[kWarps][kSteps][HB][B::kVCodes];
     float m[kWarps][8], l[kWarps][8];
-    uint64_t full[kWarps][kPairs];
+    uint64_t full[kWarps][kSteps];
     Stand feed[kWarps], now[kWarps];
 };
 
 template <typename B, int P>
 __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, WeighArgs a)
 {
-    using S = FewShared<B>;
+    using S = FewShared<B, P>;
+    constexpr int HB = S::HB, kSteps = S::kSteps;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     S &sm = *reinterpret_cast<S *>(smem_raw);
     const int lane = lane_once(), warp = threadIdx.x >> 5;
@@ -678,8 +681,8 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
 
     grid_next();
     if (lane == 0)
-        for (int i = 0; i < kPairs; ++i)
-            bar_init(&sm.full[warp][i], 2);
+        for (int i = 0; i < kSteps; ++i)
+            bar_init(&sm.full[warp][i], HB);
     bar_init_fence();
     int64_t total, chunk;
     const Place at = schedule<8>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
@@ -689,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
     Unit first;
     unit_at<8>(p, at, count, &first);
-    Feeder<B, 8, 2, kPairs> feeder;
+    Feeder<B, 8, HB, kSteps> feeder;
     feeder.ring = sm.ring[warp];
     feeder.full = sm.full[warp];
     feeder.at = &sm.feed[warp];
@@ -714,39 +717,14 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
         float *to0 = a.scores + (((int64_t)u.r * p.heads + u.h) * a.rows + row) * a.tokens + g;
         float *to1 = to0 + a.tokens;
         float2 m = make_float2(kNone, kNone), l = make_float2(0.0f, 0.0f);
-        // what the lane's rows make of two scores each
-        auto take = [&](float2 (&z)[2], int tok, bool whole, bool there, bool valid) {
-            if (!whole)
-                hide(p, tok, g, x, window, z);
-            if (!there)
-                z[0] = z[1] = make_float2(-INFINITY, -INFINITY);
-            if (valid && has[0]) {
-                to0[tok] = z[0].x;
-                to0[tok + 8] = z[1].x;
-            }
-            if (valid && has[1]) {
-                to1[tok] = z[0].y;
-                to1[tok + 8] = z[1].y;
-            }
-            // raised only when a score exceeds it by 2^8
-            const float top0 = fmaxf(z[0].x, z[1].x), top1 = fmaxf(z[0].y, z[1].y);
-            if (fmaxf(top0 - m.x, top1 - m.y) > 8.0f) {
-                const float m0 = fmaxf(m.x, top0), m1 = fmaxf(m.y, top1);
-                l.x *= exp2_fast(m.x - m0);
-                l.y *= exp2_fast(m.y - m1);
-                m = make_float2(m0, m1);
-            }
-            l.x += exp2_fast(z[0].x - m.x) + exp2_fast(z[1].x - m.x);
-            l.y += exp2_fast(z[0].y - m.y) + exp2_fast(z[1].y - m.y);
-        };
         int b, e;
         tile_range(u, tile, warp, &b, &e);
-        for (; b < e; b += 2) {
-            const int st = used % kPairs;
+        for (; b < e; b += HB) {
+            const int st = used % kSteps;
             if (alive) {
                 const bool give_up = kTestTimeout && used == 1;
-                if (give_up || !__all_sync(0xFFFFFFFFu, bar_wait(&sm.full[warp][st], (used / kPairs) & 1))) {
-                    alive = false;   // `used` stays: the first pair not waited for
+                if (give_up || !__all_sync(0xFFFFFFFFu, bar_wait(&sm.full[warp][st], (used / kSteps) & 1))) {
+                    alive = false;   // `used` stays: the first step not waited for
                     int4_set_status(p.status, CG_ERR_TIMEOUT);
                 } else {
                     ++used;
@@ -757,24 +735,49 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
                 auto all_see = [&](int tok) {
                     return tok + 15 <= tile.x_lo && (tile.x_hi - tok < window || tok + 15 < p.a.sinks);
                 };
-                const uint8_t(&ring)[2][B::kVCodes] = sm.ring[warp][st];
-                if constexpr (P == 2) {
-                    const uint8_t *const blobs[P] = {ring[0], ring[1]};
-                    const int tok = token(b + side);
-                    const bool whole = all_see(token(b)) && all_see(token(b + 1));
-                    float2 z[2];
-                    few_scores<B, P>(blobs, ring[side], q, lane, z);
-                    take(z, tok, whole, feeder.ahead >> side & 1, b + side < e);
-                } else {
+                const uint8_t(&ring)[HB][B::kVCodes] = sm.ring[warp][st];
+                float2 z[2][2];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (b + i >= e)
-                            break;
-                        const uint8_t *const blobs[P] = {ring[i]};
-                        float2 z[2];
-                        few_scores<B, P>(blobs, ring[i], q, lane, z);
-                        take(z, token(b + i), all_see(token(b + i)), feeder.ahead >> i & 1, true);
+                for (int k = 0; k < 2; ++k) {
+                    const uint8_t *blobs[P];
+#pragma unroll
+                    for (int i = 0; i < P; ++i)
+                        blobs[i] = ring[P * k + i];
+                    few_scores<B, P>(blobs, ring[P * k + side], q, lane, z[k]);
+                }
+                // what all rows see of the first and the last blob they see of those between, unless blobs
+                // are left out there
+                const bool whole = all_see(token(b)) && all_see(token(b + HB - 1)) &&
+                                   (b >= tile.span.sink || b + HB <= tile.span.sink);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int vb = b + P * k + side, tok = token(vb);
+                    if (!whole)
+                        hide(p, tok, g, x, window, z[k]);
+                    if (!(feeder.ahead >> (P * k + side) & 1))
+                        z[k][0] = z[k][1] = make_float2(-INFINITY, -INFINITY);
+                    if (vb < e && has[0]) {
+                        to0[tok] = z[k][0].x;
+                        to0[tok + 8] = z[k][1].x;
                     }
+                    if (vb < e && has[1]) {
+                        to1[tok] = z[k][0].y;
+                        to1[tok + 8] = z[k][1].y;
+                    }
+                }
+                // the maximum is raised only when a score exceeds it by 2^8
+                const float top0 = fmaxf(fmaxf(z[0][0].x, z[0][1].x), fmaxf(z[1][0].x, z[1][1].x));
+                const float top1 = fmaxf(fmaxf(z[0][0].y, z[0][1].y), fmaxf(z[1][0].y, z[1][1].y));
+                if (fmaxf(top0 - m.x, top1 - m.y) > 8.0f) {
+                    const float m0 = fmaxf(m.x, top0), m1 = fmaxf(m.y, top1);
+                    l.x *= exp2_fast(m.x - m0);
+                    l.y *= exp2_fast(m.y - m1);
+                    m = make_float2(m0, m1);
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    l.x += exp2_fast(z[k][0].x - m.x) + exp2_fast(z[k][1].x - m.x);
+                    l.y += exp2_fast(z[k][0].y - m.y) + exp2_fast(z[k][1].y - m.y);
                 }
             }
             __syncwarp();   // every lane has read the place
@@ -828,7 +831,7 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
     // a wait that ran out: the copies still in flight must land before the block's memory goes
     if (!alive)
         for (; used < feeder.issued; ++used)
-            bar_wait(&sm.full[warp][used % kPairs], (used / kPairs) & 1);
+            bar_wait(&sm.full[warp][used % kSteps], (used / kSteps) & 1);
 }
 
 // Block c joins the unit that begins in block c of the first kernel and goes on behind it.
@@ -1227,7 +1230,8 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
     cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
         using B = decltype(blob);
         if (z.stored && z.rows <= 8)
-            return launch<8, FewShared<B>, B>(z.rows <= 4 ? k_weigh_few<B, 2> : k_weigh_few<B, 1>, kFewBlocks, p, args, true, s);
+            return z.rows <= 4 ? launch<8, FewShared<B, 2>, B>(k_weigh_few<B, 2>, kFewBlocks, p, args, true, s)
+                               : launch<8, FewShared<B, 1>, B>(k_weigh_few<B, 1>, kFewBlocks, p, args, true, s);
         if (z.stored && z.rows <= 16)
             return launch<16, StatShared<B, 2>, B>(k_weigh_stats<B, 2, true>, kStatBlocks, p, args, true, s);
         return launch<32, StatShared<B, 4>, B>(z.stored ? k_weigh_stats<B, 4, true> : k_weigh_stats<B, 4, false>,

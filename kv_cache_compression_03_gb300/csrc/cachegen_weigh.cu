@@ -2,8 +2,17 @@
 // request's new tokens i and the query heads g of a KV head of p_igj = 2^(z_igj - m_ig) / l_ig,
 // z the scores in powers of two.
 //
-// The maximum m and the sum l of a row are over all of its tokens, so K is met twice: once for
-// m and l of every row, once for the sums over the rows of every token.
+// The maximum m and the sum l of a row are over all of its tokens, so a first kernel goes over K
+// for m and l of every row (a running maximum and sum, pieces joined by k_weigh_join), and a second one sums
+// over the rows of every token: from the scores, which the first one left in the workspace (k_weigh_apply),
+// or, where there is no room for them, from K again (k_weigh_sums). Requests with more than kTileRows rows of
+// a KV head go to tcgen05 (cachegen_weigh_many.cu), those with fewer come here:
+//   1 .. 8 rows    k_weigh_few. K is read once at 80 bytes a token and head of 128 channels in groups of 32, and
+//                  what bounds it is the work on a blob of 16 tokens, some 700 instructions a warp: 64 requests
+//                  of up to 8192 tokens, 4 rows: 59 us for 278 MB, with join 5 and apply 20 88 us in all; a
+//                  floor of 42 at the copy rate. (mma.sync: 16 tokens by 8 rows is all that there are.)
+//   9 .. 64 rows   k_weigh_stats, 16 or 32 rows at a time, which read K again for each 32.
+// Sums go by rows in a fixed order, 256 or so to a partial sum, so the same call gives the same bits.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -16,14 +25,16 @@ namespace {
 
 constexpr int kRing = 8;           // blobs in a warp's ring
 constexpr int kItemTokens = 64;    // of a block in the second pass, a blob to a warp; or,
-constexpr int kManyRows = 512;     // from so many rows on, a blob to a block, whose warps share the rows
+// from so many rows on, a blob to a block, whose warps share the rows. (Without stored scores and without room
+// for the sums of kTileRows' kernel, so with tables of millions of tokens.)
+constexpr int kManyRows = 512;
 constexpr int kMaxBlocks = 640;    // of the first pass
 
 // ------------------------------------------------------------------- scores
 
 // With mid = lo + 8 s and m = n - 8 in [-8, 7], q.k^ = sum_g s_g (q.m)_g + mid_g (sum q)_g. Where a
 // few channels of a group are large, s and lo follow those and the others' codes lie near 8:
-// q.n and lo (sum q) would be large and cancel (an error of 1.3e-5 in the weights, of 2e-7 so). The
+// q.n and lo (sum q) would be large and cancel (an error of 1.3e-5 in the weights, of 3e-8 so). The
 // products of bf16 pairs are exact, everything else is fp32.
 
 // The queries of 8 rows of a KV head, from row0 on. qf: the second factor of the instruction, column
@@ -325,6 +336,10 @@ __device__ __forceinline__ float raise(float top, bool no_row, float *m, float *
 // Blocks on an SM.
 constexpr int kStatBlocks = 3;
 
+// For 8 NT rows of a (request, KV head) at a time. 32 rows of 32768 tokens, 8 KV heads: 46 us with all that
+// follows, 64 rows 67. What bounds it is instructions: a blob's keys are made once (4 a pair of codes) and
+// meet NT tiles of 8 rows, each of whose scores takes an exponential and a store.
+//
 // kStored: scores are left for the sums, else the queries.
 template <typename B, int NT, bool kStored>
 __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs p, WeighArgs a)
@@ -732,9 +747,6 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
             }
             if (alive) {
                 auto token = [&](int vb) { return 16 * (vb < tile.span.sink ? vb : vb + tile.span.skip); };
-                auto all_see = [&](int tok) {
-                    return tok + 15 <= tile.x_lo && (tile.x_hi - tok < window || tok + 15 < p.a.sinks);
-                };
                 const uint8_t(&ring)[HB][B::kVCodes] = sm.ring[warp][st];
                 float2 z[2][2];
 #pragma unroll
@@ -745,10 +757,9 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
                         blobs[i] = ring[P * k + i];
                     few_scores<B, P>(blobs, ring[P * k + side], q, lane, z[k]);
                 }
-                // what all rows see of the first and the last blob they see of those between, unless blobs
-                // are left out there
-                const bool whole = all_see(token(b)) && all_see(token(b + HB - 1)) &&
-                                   (b >= tile.span.sink || b + HB <= tile.span.sink);
+                // every row sees all of the step's tokens: from the first to the last, or to the last of the sinks
+                const int t0 = token(b), t1 = token(b + HB - 1) + 15;
+                const bool whole = t1 <= tile.x_lo && (tile.x_hi - t0 < window || t1 < p.a.sinks);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     const int vb = b + P * k + side, tok = token(vb);
@@ -1116,7 +1127,9 @@ struct WeighSizes {
 };
 
 // Requests with more rows than this go to the kernels for many (cachegen_weigh_many.cu), where there is room
-// for their sums by row tiles.
+// for their sums by row tiles. Here and there, 8 KV heads of 128: one request of 32768 tokens with 32 rows 46 us and
+// 76, 48 rows 62 and 76, 64 rows 67 and 76; eight of 16384 with 64 rows 209 and 237, 64 of 1024 with 64 rows 124
+// and 148. (More rows here would read K again for each 32.)
 constexpr int kTileRows = 64;
 constexpr size_t kMostSums = (size_t)1 << 30;   // bytes
 
@@ -1137,9 +1150,9 @@ WeighSizes sizes_of(const cg_int4_cache *c, const cg_attention *a, const cg_toke
         z.many = z.tiles ? align256(z.many) : 0;
     }
     z.rows = (int32_t)(z.tiles ? kTileRows : rows);
-    // Scores are stored, and not computed again, where there is room for those that the batch can have (128
-    // rows at 32768 tokens, 8 heads: 115 us so, 123 computed again; more than the L2 holds would be
-    // read from memory at no gain: 8192 rows at 2048, two requests, 1 GB).
+    // Scores are stored, and not computed again, where there is room for those that the batch can have: one
+    // request of 32768 tokens, 128 rows and 8 heads (134 MB) took 115 us so and 123 computed again; with two of
+    // 2048 tokens and 8192 rows each (1 GB), which the L2 does not hold, either took as long.
     const size_t lists = (size_t)a->requests * c->num_heads;
     z.stored = lists == 0 || (size_t)z.rows * z.tokens <= kMostScores / sizeof(float) / lists;
     z.parts = align256((size_t)kMaxBlocks * 2 * 32 * sizeof(float2));
@@ -1192,10 +1205,10 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
         return st;
     if (layer < 0 || layer >= c->num_layers)
         return CG_ERR_INVALID_ARG;
-    if (a->requests == 0 || w->width == 0)
+    if (a->requests == 0)
         return CG_OK;
     st = attn_check_arrays(a, false);
-    if (st != CG_OK || w->out == nullptr || !int4_aligned(w->in, 4) || !int4_aligned(w->out, 4) ||
+    if (st != CG_OK || (w->out == nullptr && w->width > 0) || !int4_aligned(w->in, 4) || !int4_aligned(w->out, 4) ||
         !int4_aligned(workspace, 256))
         return CG_ERR_INVALID_ARG;
     if (w->in == w->out &&

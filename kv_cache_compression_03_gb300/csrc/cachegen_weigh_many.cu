@@ -75,6 +75,7 @@ struct TileShared {
 };
 
 struct TileWork {
+    int32_t most;        // units that there is room for
     int32_t *cut;        // units, pieces of each
     Piece *heads;        // [units]: their first pieces
     float2 *parts;       // [items][2][128]: m, l of either half of an item's tiles
@@ -112,13 +113,13 @@ __device__ __forceinline__ void blobs_of(const AttnArgs &p, int32_t x0, int32_t 
 
 // One warp: piece `item` of the batch into *u. It goes on from where the last call stood.
 __device__ __forceinline__ void find_piece(const AttnArgs &p, int64_t item, int split, int *r0, int64_t *before, Piece *u,
-                                           Piece *heads)
+                                           const TileWork &work, Piece *heads)
 {
     const int lane = threadIdx.x & 31;
     const int64_t want = item / split;
     const int piece = (int)(item - want * split);
     for (;; *r0 += 32) {
-        if (*r0 >= p.a.requests) {
+        if (*r0 >= p.a.requests || want >= work.most) {
             if (lane == 0)
                 u->there = 0;
             __syncwarp();
@@ -243,8 +244,10 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
     const uint32_t tmem = sm.tmem;
     const int split = sm.units > 0 && sm.units < gridDim.x ? gridDim.x / sm.units : 1;
     if (!kSums && blockIdx.x == 0 && tid == 0) {
-        work.cut[0] = sm.units;
+        work.cut[0] = min(sm.units, work.most);
         work.cut[1] = split;
+        if (sm.units > work.most)   // more than a batch of so many tokens has: requests that share rows of q
+            int4_set_status(p.status, CG_ERR_CORRUPT);
     }
     if (kSums)
         grid_wait();   // for the rows' maxima and sums
@@ -582,7 +585,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
             if (!wait_all(&sm.u_empty[slot], (which / kKnown & 1) ^ 1))
                 return false;
             find_piece(p, blockIdx.x + (int64_t)which * gridDim.x, split, &u_r0, &u_before, &sm.piece[slot],
-                       kSums ? nullptr : work.heads);
+                       work, kSums ? nullptr : work.heads);
             if (lane == 0)
                 bar_arrive(&sm.u_full[slot]);
             __syncwarp();
@@ -812,6 +815,7 @@ cudaError_t weigh_many_launch(const AttnArgs &p, WeighArgs a, const cg_int4_cach
     const TileSizes z = sizes_of(c, &p.a, a.tokens);
     uint8_t *at = static_cast<uint8_t *>(ws);
     TileWork work;
+    work.most = z.tiles * c->num_heads;   // (fits: their sums are within the bound on those)
     work.cut = reinterpret_cast<int32_t *>(at);
     work.heads = reinterpret_cast<Piece *>(at += z.cut);
     work.parts = reinterpret_cast<float2 *>(at += z.heads);

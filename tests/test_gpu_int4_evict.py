@@ -121,6 +121,24 @@ def test_weigh_of_channels_that_differ():
     assert np.linalg.norm(out - exact) / np.linalg.norm(exact) < 2.0 ** -19
 
 
+@pytest.mark.parametrize("low", [13, 14, 15, 79])
+@pytest.mark.parametrize("more", [-1, 0, 1, 16])
+@pytest.mark.parametrize("nq,ratio", [(4, 1), (2, 2), (8, 1), (20, 1)])
+def test_weigh_where_the_windows_begin_at_the_last_of_the_first_tokens(low, more, nq, ratio):
+    """The first row's window begins with token `low`, at a blob's end, the others' behind it; the tokens
+    between, if they are not of the first ones, are seen by some rows only."""
+    rng = np.random.default_rng(low)
+    window, sinks = 400, low // 16 * 16 + 16 + more
+    nkv = [window + nq - 1 + low]
+    table, want, got, cu, q = _weigh_case(rng, [nq], nkv, ratio, 64, 32, 16)
+    width = table.shape[1] * 16
+    exact, tol = evict.weigh(want, 0, q, cu, nkv, table, window, sinks, 0.125, width)
+    out = torch.zeros(1, 2, width, device="cuda")
+    got.weigh(_dev(q), _ints(cu), _ints(nkv), _ints(table), out, window=window, sinks=sinks, max_q_len=nq)
+    got.check()
+    _check_weights(out.cpu().numpy(), np.zeros(out.shape, np.float32), exact, tol)
+
+
 @pytest.mark.parametrize("nq,nkv,ratio,heads", [([200] * 4, [250, 200, 777, 201], 7, 8),    # 352 units of 128 rows
                                                  ([129], [3000], 1, 1),                     # 2 units, cut in pieces
                                                  ([65, 1, 0, 90], [65, 900, 30, 40], 3, 2),  # rows before the first token
@@ -169,6 +187,21 @@ def test_weigh_of_many_rows_reports_bad_pages():
             e = np.exp(z - z.max(1, keepdims=True))
             exact += (e / e.sum(1, keepdims=True)).sum(0)
         assert np.abs(out[0, h, keep] - exact).max() <= 2.0 ** -17 * exact.max()
+
+
+def test_weigh_of_many_rows_reports_requests_that_share_rows():
+    """Bounds of rows that go back and forth: every other request has all of them, more tiles of 128 than
+    a batch of so many tokens."""
+    rng = np.random.default_rng(41)
+    nq, n = 600, 61
+    table, want, got, cu, q = _weigh_case(rng, [nq], [nq], 2, 64, 32, 16)
+    to_and_fro = [0, nq] * (n // 2) + [0, nq]
+    w = torch.zeros(n, 2, table.shape[1] * 16, device="cuda")
+    got.weigh(_dev(q), _ints(to_and_fro), _ints([nq] * n), _ints(np.repeat(table, n, 0)), w)
+    _status(got.check, cg.CG_ERR_CORRUPT)
+    a = got.weigh(_dev(q), _ints(cu), _ints([nq]), _ints(table))     # and the next call is right
+    got.check()
+    assert torch.allclose(a.sum(-1), torch.full((1, 2), 2.0 * nq, device="cuda"), rtol=2.0 ** -12)
 
 
 @pytest.mark.parametrize("scale", [0.0, -0.3])
@@ -256,6 +289,12 @@ def test_weigh_without_rows_or_requests():
     assert torch.equal(out[0, :, :40], w[0, :, :40]) and (out[0, :, 40:] == -7.0).all() and (out[1] == -7.0).all()
     none = got.weigh(empty, _ints([0]), _ints([]), _ints(np.empty((0, 3))))
     assert none.shape == (0, 2, 48)
+    # rows without room for a token: a request that has one is reported, whatever else there is
+    no_room = torch.empty(2, 2, 0, device="cuda")
+    got.weigh(_dev(q[:0]), _ints([0, 0, 0]), _ints([0, 0]), _ints(table), no_room)
+    got.check()
+    got.weigh(_dev(q[:0]), _ints([0, 0, 0]), _ints([40, 0]), _ints(table), no_room)
+    _status(got.check, cg.CG_ERR_CORRUPT)
     # padding: rows of q behind the last request's, pages that are not there
     q = _dev(_rand(rng, 5, 4, 64))
     a = got.weigh(q[:2], _ints([0, 2, 2]), _ints([40, 0]), _ints(table))
@@ -289,12 +328,12 @@ def test_weigh_with_and_without_room_for_scores(nq, ratio, window, sinks):
     rng = np.random.default_rng(nq)
     nkv = [nq + 700, nq, nq + 33]
     table, want, got, cu, q = _weigh_case(rng, [nq] * 3, nkv, ratio, 128, 64, 16)
-    wide = np.full((3, 1 << 18), -1, np.int32)     # 2^22 tokens a row: 400 MB of scores for 6 lists and 4 rows
-    wide[:, :table.shape[1]] = table
+    wide = np.full((3, 1 << 19), -1, np.int32)     # 2^23 tokens a row: 800 MB of scores for 6 lists and 4 rows,
+    wide[:, :table.shape[1]] = table               # 1.2 GB of sums for 36 tiles of 128 rows
     exact, tol = evict.weigh(want, 0, q, cu, nkv, table, window, sinks, 128 ** -0.5, table.shape[1] * 16)
     kw = dict(window=window, sinks=sinks, max_q_len=nq)
     few = got.weigh(_dev(q), _ints(cu), _ints(nkv), _ints(table), **kw).cpu().numpy()
-    base = torch.zeros(3, 2, 1 << 22, device="cuda")
+    base = torch.zeros(3, 2, 1 << 23, device="cuda")
     got.weigh(_dev(q), _ints(cu), _ints(nkv), _ints(wide), base, **kw)
     got.check()
     many = base[..., :few.shape[-1]].cpu().numpy()

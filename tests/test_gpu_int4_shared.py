@@ -69,6 +69,20 @@ def test_shared_tokens_other_formats(dim, group, i):
     test_shared_tokens(i, dim, group, 32)
 
 
+@pytest.mark.parametrize("scale,qscale", [(0.0, 1.0), (-0.2, 1.0), (2.0 ** -26, 2.0 ** 23)])
+@pytest.mark.parametrize("i", [0, 5, 6, 8])
+def test_scales(scale, qscale, i):
+    """Scales that the kernel for many rows takes into Q: the two passes' maxima are still of one kind."""
+    nq, own, shared, ratio = SHAPES[i]
+    rng = np.random.default_rng(i)
+    table, want, got, cu, q, lens = _case(rng, nq, own, shared, 2, ratio, 64, 32, 16)
+    q = ref.bf16_round(q * np.float32(qscale))
+    o, tol = ref.attention(want, 0, q, cu, lens, table, 0, 0, scale)
+    out = got.attention(_dev(q), _ints(cu), _ints(lens), _ints(table), scale=scale, max_q_len=max(nq), shared=shared)
+    got.check()
+    assert (np.abs(_np(out) - o) <= tol).all()
+
+
 @pytest.mark.parametrize("nq,n", [(1, 3), (1, 40), (70, 2)])
 def test_weights_on_either_side(nq, n):
     """Scores that put nearly all weight on the shared tokens, or nearly none."""

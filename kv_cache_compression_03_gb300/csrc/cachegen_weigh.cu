@@ -352,6 +352,8 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
     const int g = lane >> 2, t = lane & 3;
 
     grid_next();
+    if (a.taken != nullptr && blockIdx.x == 0 && threadIdx.x < 2)
+        a.taken[threadIdx.x] = 0;
     if (lane == 0)
         for (int i = 0; i < kRing; ++i)
             bar_init(&sm.full[warp][i], 1);
@@ -900,6 +902,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_weigh_sums(AttnArgs p, WeighArg
     const int lane = lane_once(), warp = threadIdx.x >> 5, t = lane & 3;
     const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
     const int bpp = p.page_tokens / 16;
+    grid_next();   // the kernels for many rows may come up: they work on other rows
     grid_wait();
     Items items = {0, 0};
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
@@ -1035,6 +1038,7 @@ template <int kEach, int kRows>
 __global__ void __launch_bounds__(kThreads) k_weigh_apply(AttnArgs p, WeighArgs a)
 {
     constexpr int kTokens = kEach * kThreads;
+    grid_next();   // as there
     grid_wait();
     Items items = {0, 0};
     for (int64_t item = blockIdx.x;; item += gridDim.x) {
@@ -1239,6 +1243,7 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
     args.scores = reinterpret_cast<float *>(take(z.scores));
     args.sums = nullptr;
     args.tiles = 0;
+    args.taken = z.tiles ? weigh_many_taken(ws) : nullptr;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t err = int4_dispatch(c->head_size, c->group, [&](auto blob) {
         using B = decltype(blob);

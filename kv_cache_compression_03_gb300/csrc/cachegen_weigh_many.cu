@@ -16,7 +16,16 @@
 //   warps 8-15       queries of a unit; keys of a blob at a time
 //   warp 16          finds the units and copies the K half of their blobs into a ring
 //   warp 17          one thread issues all products
-// With fewer units than blocks each is cut along its tokens; more are dealt in turns, the longest first.
+// With fewer units than blocks each is cut along its tokens; of more, whichever block is free takes the next, the
+// longest of a request first (two prompts of 2048: 195 us so, 210 dealt in turns).
+//
+// What bounds it: a tile takes some 2300 cycles in the first pass and 3000 in the second. Its products are 1280,
+// which the shared memory's rate sets (two operands of 4 KB in 64 cycles), the expansion of its keys and its
+// exponentials about as much each; they overlap, but hand the two buffers of keys and scores on by barriers.
+// One request of 32768 tokens, 128 rows, 32 query and 8 KV heads: 28 + 31 us, with all else 76; two prompts of
+// 2048 at 4 rows to a token: 188. Products alone would be 9 of the 28. (Built, and not better: 256 rows to a block,
+// whose low parts had one buffer, 183 for the prompts and 88 for the 128 rows; 16 expanding warps of half a blob,
+// 224 and 84.)
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,7 +40,7 @@ namespace {
 constexpr int kSoftWarps = 8, kExpandWarps = 8;
 constexpr int kAllWarps = kSoftWarps + kExpandWarps + 2, kAllThreads = 32 * kAllWarps;
 constexpr int kPlaces = 24;      // blobs copied ahead
-constexpr int kIssue = 4;        // of those, copied at once
+constexpr int kIssue = 8;        // of those, copied at once
 constexpr int kTile = 128;       // rows, and tokens
 constexpr int kBlobs = kTile / 16;
 constexpr int kKnown = 4;        // units known at a time, and their rows' factors kept
@@ -76,7 +85,7 @@ struct TileShared {
 
 struct TileWork {
     int32_t most;        // units that there is room for
-    int32_t *cut;        // units, pieces of each
+    int32_t *cut;        // units, pieces of each; then, of either pass, items taken behind the blocks' first
     Piece *heads;        // [units]: their first pieces
     float2 *parts;       // [items][2][128]: m, l of either half of an item's tiles
 };
@@ -199,7 +208,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
     grid_next();
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            bar_init(&sm.k_full[i], kBlobs);
+            bar_init(&sm.k_full[i], kExpandWarps);
             bar_init(&sm.k_empty[i], 1);
             bar_init(&sm.s_full[i], 1);
             bar_init(&sm.s_empty[i], 128);
@@ -249,8 +258,6 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
         if (sm.units > work.most)   // more than a batch of so many tokens has: requests that share rows of q
             int4_set_status(p.status, CG_ERR_CORRUPT);
     }
-    if (kSums)
-        grid_wait();   // for the rows' maxima and sums
     const int bpp = p.page_tokens / 16;
     // Every role walks the block's pieces on its own and meets the others at the barriers only.
     uint32_t un = 0;             // pieces begun
@@ -449,23 +456,33 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
             const Piece &u = *up;
             const int n = u.n;
             auto queries = [&]() {   // false: a wait ran out
-                if (!wait_all(&sm.q_empty, (qn & 1) ^ 1))   // the last piece's scores are done
-                    return false;
                 const int64_t slot = (int64_t)u.h * a.slots + first_slot(p, u.r, u.q_row0) + u.row0 / 8;
-#pragma unroll 1
-                for (int in0 = 8 * wi; in0 < kTile; in0 += 8 * kExpandWarps) {
-                    const int in = in0 + k8, row = u.row0 + in;
+                constexpr int kRounds = kTile / 8 / kExpandWarps;
+                uint4 v[kRounds][NW];      // on their way while the last piece's products end
+#pragma unroll
+                for (int i = 0; i < kRounds; ++i) {
+                    const int row = u.row0 + 8 * (wi + kExpandWarps * i) + k8;
                     const bool there = row < u.rows;
                     const int qt = there ? row / p.ratio : 0, qh = u.h * p.ratio + (there ? row - qt * p.ratio : 0);
                     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(p.a.q) +
                                              (int64_t)(u.q_row0 + qt) * p.a.q_token_stride + qh * p.a.q_head_stride;
-                    uint4 v[NW];
+#pragma unroll
+                    for (int w = 0; w < NW; ++w)
+                        v[i][w] = there ? *reinterpret_cast<const uint4 *>(q + 32 * w + 8 * t) : make_uint4(0, 0, 0, 0);
+                }
+                if (!wait_all(&sm.q_empty, (qn & 1) ^ 1))   // the last piece's scores are done
+                    return false;
+                if (kSums)
+                    grid_wait();   // for the rows' maxima and sums
+#pragma unroll
+                for (int i = 0; i < kRounds; ++i) {
+                    const int in = 8 * (wi + kExpandWarps * i) + k8;
+                    const bool there = u.row0 + in < u.rows;
                     uint32_t top = 0;        // largest |q| of the row (as bf16 bits, in both halves)
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
-                        v[w] = there ? *reinterpret_cast<const uint4 *>(q + 32 * w + 8 * t) : make_uint4(0, 0, 0, 0);
-                        top = __vmaxu2(__vmaxu2(top, v[w].x & 0x7FFF7FFFu), v[w].y & 0x7FFF7FFFu);
-                        top = __vmaxu2(__vmaxu2(top, v[w].z & 0x7FFF7FFFu), v[w].w & 0x7FFF7FFFu);
+                        top = __vmaxu2(__vmaxu2(top, v[i][w].x & 0x7FFF7FFFu), v[i][w].y & 0x7FFF7FFFu);
+                        top = __vmaxu2(__vmaxu2(top, v[i][w].z & 0x7FFF7FFFu), v[i][w].w & 0x7FFF7FFFu);
                     }
                     top = max(top & 0xFFFFu, top >> 16);
                     top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
@@ -477,7 +494,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                     float sum[NG] = {};
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
-                        const uint4 c = v[w];
+                        const uint4 c = v[i][w];
                         // channels i and i + 4 side by side, as the codes of a word come
                         const float f[8] = {par_s(c.x), par_s(c.z), par_lo(c.x), par_lo(c.z),
                                             par_s(c.y), par_s(c.w), par_lo(c.y), par_lo(c.w)};
@@ -518,8 +535,8 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                 return true;
             };
             bool alive = n == 0 || queries();
-            int b = (int)((wi + kExpandWarps - seq % kExpandWarps) % kExpandWarps);
-            for (; b < n * kBlobs && alive; b += kExpandWarps) {
+            static_assert(kExpandWarps == kBlobs);
+            for (int b = wi; b < n * kBlobs && alive; b += kBlobs) {   // a blob of each tile
                 const uint32_t use = tiles_done + (uint32_t)b / kBlobs, sl = use & 1, at = seq + b;
                 const uint32_t slot = at % kPlaces;
                 const int in_tile = b % kBlobs;
@@ -584,7 +601,15 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
             const uint32_t slot = which % kKnown;
             if (!wait_all(&sm.u_empty[slot], (which / kKnown & 1) ^ 1))
                 return false;
-            find_piece(p, blockIdx.x + (int64_t)which * gridDim.x, split, &u_r0, &u_before, &sm.piece[slot],
+            int64_t item = blockIdx.x;
+            if (which > 0) {   // the next one that no block has
+                grid_wait();   // for the counter's 0
+                int32_t taken = 0;
+                if (lane == 0)
+                    taken = atomicAdd(a.taken + kSums, 1);
+                item = gridDim.x + (int64_t)__shfl_sync(0xFFFFFFFFu, taken, 0);
+            }
+            find_piece(p, item, split, &u_r0, &u_before, &sm.piece[slot],
                        work, kSums ? nullptr : work.heads);
             if (lane == 0)
                 bar_arrive(&sm.u_full[slot]);
@@ -809,6 +834,8 @@ size_t weigh_many_workspace(const cg_int4_cache *c, const cg_attention *a, int32
 {
     return sizes_of(c, a, tokens).bytes();
 }
+
+int32_t *weigh_many_taken(void *ws) { return static_cast<int32_t *>(ws) + 2; }
 
 cudaError_t weigh_many_launch(const AttnArgs &p, WeighArgs a, const cg_int4_cache *c, void *ws, cudaStream_t s)
 {

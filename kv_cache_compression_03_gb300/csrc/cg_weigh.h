@@ -17,6 +17,7 @@ struct WeighArgs {
     // requests with more rows than p.few_rows: their sums by row tiles of 128
     float *sums;         // [heads][tiles][tokens]
     int32_t tiles;
+    int32_t *taken;      // [2], which the first kernel sets to 0; nullptr where there are no such requests
 };
 
 namespace {
@@ -103,4 +104,5 @@ __device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, F eac
 // The kernels for many rows: bytes that they need besides the others' (for `rows` rows of a request's KV head
 // at most), and the launch behind those.
 size_t weigh_many_workspace(const cg_int4_cache *c, const cg_attention *a, int32_t tokens);
+int32_t *weigh_many_taken(void *ws);
 cudaError_t weigh_many_launch(const AttnArgs &p, WeighArgs a, const cg_int4_cache *c, void *ws, cudaStream_t s);

@@ -546,16 +546,18 @@ cg_status cg_int4_attention(const cg_int4_cache *cache, int32_t layer, const cg_
 /* The same where every request begins with the same cached tokens (an instruction
  * or a document that a batch shares): the first shared_tokens of each request's tokens
  * lie in the same pages, the first shared_tokens / page_tokens entries of its row of
- * block_table. They are read once for all queries, by way of the first row of
- * block_table; the other rows' entries there are not read. kv_lens counts the shared
- * tokens too. The result is that of cg_int4_attention but for the order of fp32 sums.
+ * block_table. They are read by way of the first row of block_table (the other rows' entries
+ * there are not read), and where there are enough of them once for all queries. kv_lens
+ * counts the shared tokens too. The result is that of cg_int4_attention but for the order of
+ * fp32 sums.
  *
  * shared_tokens is a multiple of page_tokens and window is 0 (CG_ERR_INVALID_ARG; what
  * of the first tokens is in a window depends on the query); shared_tokens = 0 is
  * cg_int4_attention. A request whose new tokens do not all lie behind the shared ones
  * sets CG_ERR_INVALID_ARG in the cache's status (its rows are left as they were).
  * A page id outside the cache among the shared ones hides its tokens from every query.
- * The workspace holds tokens * q_heads * (head_size + 2) floats more. */
+ * The workspace's size depends on requests and shared_tokens too, and is at most tokens * q_heads *
+ * (head_size + 2) floats and 86 MB larger. */
 cg_status cg_int4_attention_shared_workspace(const cg_int4_cache *cache, const cg_attention *args,
                                              int32_t shared_tokens, size_t *bytes);
 cg_status cg_int4_attention_shared(const cg_int4_cache *cache, int32_t layer,
@@ -584,7 +586,9 @@ cg_status cg_int4_attention_shared(const cg_int4_cache *cache, int32_t layer,
  * may be out (with the same strides) and otherwise must not overlap it. Rows of out must not
  * overlap, nor out q or the cache. workspace as for attention; its size depends on the
  * cache's shape, tokens, requests, q_heads, max_q_len, table_width and width: room for the
- * scores where they are below 256 MB, for the queries again where they are not. */
+ * scores where they are below 256 MB, for the queries again where they are not; and where a
+ * request may have more than 64 rows (query heads of a KV head times new tokens), for sums of each 128
+ * rows, a float a token, where those are below 1 GB. */
 typedef struct cg_token_weights {
     const float *in;
     float *out;
@@ -606,7 +610,8 @@ cg_status cg_int4_weigh(const cg_int4_cache *cache, int32_t layer, const cg_atte
  * lower token, and NaN is below every other weight.
  *   kept      int32 [layers][requests][heads][budget], contiguous: the tokens that
  *             stay, ascending; -1 behind the last
- *   lens_out  int32 [requests]: min(m, budget) (may be lens itself)
+ *   lens_out  int32 [requests]: min(m, budget) (may be lens itself; cg_int4_compact
+ *             wants both)
  *   status    16 bytes, 16-byte aligned, always written: CG_OK, or CG_ERR_CORRUPT for a
  *             length that is negative or beyond width (its row of kept is -1,
  *             lens_out repeats it)

@@ -946,7 +946,8 @@ def choose_tokens(weights, lens, budget: int, recent: int = 0, sinks: int = 0,
     ``recent`` and those with the greatest weights (fp32 [requests, heads, n], or
     [layers, requests, heads, n], as Int4Cache.weigh sums them; lens int32 [requests]).
     Of equal weights the lower token stays. ``out`` reuses the buffers of an
-    earlier choice; its lens may be lens. With ``stream`` the call runs there."""
+    earlier choice; its lens may be lens (Int4Cache.compact wants both). With ``stream`` the call
+    runs there."""
     if stream is not None:
         return _on_stream(stream, choose_tokens, weights, lens, budget, recent, sinks, out)
     torch = _torch or _need_torch()
@@ -1125,7 +1126,7 @@ class Int4Cache:
         rows = (min(max_q_len, tokens) if max_q_len else tokens) * q_heads // self.num_heads
         if shared:
             _int32(shared, "shared")
-            rows = (rows, tokens, q_heads)
+            rows = (rows, tokens, q_heads, n, shared)
             _need(not window and 0 < shared <= width * self.page_tokens and
                   shared % self.page_tokens == 0,
                   "shared must be whole pages that a row of block_table can hold, without a window")

@@ -54,6 +54,59 @@ size_t pass_bytes(const cg_int4_cache *c, int64_t rows, bool first)
     return few_bytes(c, rows) + align256(attn_many_workspace(c->head_size, 0));
 }
 
+// Shared tokens: whether a pass of their own pays. Each request reading them costs instructions and the L2's
+// rate, not memory's, and what it costs more than two passes' launches, joins, starts and ends must be there
+// first. Estimates in us, from measurements (152 SMs; 32 query heads of 128, 500 tokens of a request's own):
+//   requests, queries, KV heads    shared    one pass    two
+//   32, 1, 8                         2048        35       43
+//                                    8192        80       49
+//   8, 1, 8                          8192        33       45
+//                                   32768        76       64
+//   16, 4, 2 (64 rows)               8192        51       68
+//                                   32768       119       88
+//   8, 100, 8 (400 rows)             8192       157      192
+//                                   32768       531      481
+#ifdef CG_TEST_SHARED_TWO
+constexpr bool kTestTwoPasses = true;   // test builds: whatever the sizes
+#else
+constexpr bool kTestTwoPasses = kTestTimeout;
+#endif
+
+bool two_passes(const cg_int4_cache *c, const cg_attention *a, int32_t shared)
+{
+    if (kTestTwoPasses)
+        return true;
+    const int64_t requests = a->requests > 0 ? a->requests : 1, all = all_rows(c, a), heads = c->num_heads;
+    const int64_t most = max_rows(c, a), each = most < all / requests + 1 ? most : all / requests + 1;
+    const int64_t tiles = (shared + 127) / 128;   // of 128 tokens; rows come in units of 256
+    const double bytes = (double)shared * heads * (int4_blob_bytes(c->head_size, c->group) / 16);
+    // bytes a us out of the L2, of blobs that take as many instructions with half the channels
+    const double rate = c->head_size == 128 ? 5.8e6 : 3.9e6, tile = c->head_size == 128 ? 2.25 : 1.35;
+    auto by_few = [&](int64_t rows) { return rows <= 8 ? bytes / rate : (double)((rows + 15) / 16) * bytes / (0.53 * rate); };
+    auto by_many = [&](int64_t units, int64_t split, double ends) {
+        return (double)((units * split + 151) / 152) * ((double)((tiles + split - 1) / split) + ends) * tile;
+    };
+    double one, two;    // what the shared tokens cost in one pass, and in two
+    if (each <= kFewRows) {
+        one = (double)requests * by_few(each);
+        two = all <= kFewRows ? 20.0 : 10.0;
+    } else {
+        const int64_t units = (all / 256 + requests < requests * ((most + 255) / 256) ? all / 256 + requests
+                                                                                      : requests * ((most + 255) / 256)) * heads;
+        one = by_many(units, units <= 76 ? 152 / units : 1, 0.0) * (each <= 128 ? 0.7 : 1.0);
+        two = 35.0;
+    }
+    if (all <= kFewRows)
+        return two + by_few(all) < one;
+    const int64_t units = (all + 255) / 256 * heads, items = attn_many_items(all, c->num_heads);
+    double first = by_many(units, 1, 3.0);
+    for (int64_t split = 2; split <= 31 && split <= tiles / 2 && units * split <= items; ++split) {
+        const double cut = by_many(units, split, 3.0);
+        first = cut < first ? cut : first;
+    }
+    return two + first < one;
+}
+
 cg_status launch_pass(const cg_int4_cache *c, const AttnArgs &p, uint8_t *workspace, cudaStream_t s)
 {
     const int64_t most = max_rows(c, &p.a);
@@ -173,13 +226,17 @@ extern "C" cg_status cg_int4_attention(const cg_int4_cache *c, int32_t layer,
     return launch_pass(c, p, static_cast<uint8_t *>(workspace), s);
 }
 
-// Shared tokens: one pass takes them for all rows of the batch, as one request's that all see
-// every token, and leaves its results and their sums in fp32; the other takes each
-// request's own tokens as ever and joins the two where it writes a row.
+// Shared tokens, where they are many: one pass takes them for all rows of the batch, as one request's
+// that all see every token, and leaves its results and their sums in fp32; the other takes each
+// request's own tokens as ever and joins the two where it writes a row (o = sum of l_i 2^(m_i - m) o_i
+// over the sum of l_i 2^(m_i - m)). Where they are few, one pass in which every request reads
+// them itself, out of the L2.
 //
 // 64 requests with a token each and 4 query heads to a KV head are 256 rows to the shared tokens:
-// they are read once, by the kernel for many rows, where a call for each request would read
-// them 64 times.
+// they are read once, by the kernel for many rows, where each request would read
+// them itself, 64 times. 16384 shared and up to 1024 own tokens, 8 KV heads: 80 us and 268 (36 the first
+// pass, 13 its join, 30 the second, 8 its join; of the floor of 10 us the shared tokens are 3). 8 requests of 300
+// queries, 32 query and 2 KV heads, 32768 shared: 880 and 1046.
 
 extern "C" cg_status cg_int4_attention_shared_workspace(const cg_int4_cache *c, const cg_attention *a,
                                                         int32_t shared, size_t *bytes)
@@ -190,7 +247,7 @@ extern "C" cg_status cg_int4_attention_shared_workspace(const cg_int4_cache *c, 
     if (shared < 0 || shared % c->page_tokens != 0 || shared / c->page_tokens > a->table_width ||
         (shared > 0 && a->window > 0))
         return CG_ERR_INVALID_ARG;
-    if (shared == 0)
+    if (shared == 0 || !two_passes(c, a, shared))
         return CG_OK;
     // and that of the other, whose last kernels may still run when this one's first come up
     *bytes += pass_bytes(c, all_rows(c, a), true);
@@ -225,7 +282,15 @@ extern "C" cg_status cg_int4_attention_shared(const cg_int4_cache *c, int32_t la
         return CG_ERR_CAPACITY;
     const size_t rows = (size_t)a->tokens * a->q_heads;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     AttnArgs p = attn_args(c, layer, a);
+    // a block begins and ends a unit for as long as it reads some 16 blobs: short ones are not strung
+    // together (4 requests of 7 to 65 tokens, 12 heads: 54 us with, 14 without)
+    p.least_unit = 16;
+    if (!two_passes(c, a, shared)) {
+        p.front = shared;
+        return launch_pass(c, p, ws, s);
+    }
     p.shared = shared;
     p.row_stats = reinterpret_cast<float2 *>(ws + need - align256(rows * sizeof(float2)));
     p.rows = reinterpret_cast<float *>(reinterpret_cast<uint8_t *>(p.row_stats) -
@@ -239,12 +304,8 @@ extern "C" cg_status cg_int4_attention_shared(const cg_int4_cache *c, int32_t la
     first.a.max_q_len = 0;
     // however many rows there are, they go to one kernel
     first.few_rows = all_rows(c, a) <= kFewRows ? kFewRows : 0;
-    // a block begins and ends a unit for as long as it reads some 16 blobs: short ones are not strung
-    // together (4 requests of 7 to 65 tokens, 12 heads: 54 us with, 14 without)
-    p.least_unit = 16;
     p.a.block_table += shared / c->page_tokens;
     p.a.table_width -= shared / c->page_tokens;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     st = launch_pass(c, first, ws, s);
     return st == CG_OK ? launch_pass(c, p, ws + pass_bytes(c, all_rows(c, a), true), s) : st;
 }

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             if (lane < f_n && fu.q.kv > 0) {
                 const int vb = f_b + lane, ab = vb < fu.span.sink ? vb : vb + fu.span.skip;
                 const int page = ab / bpp;
-                id = p.a.block_table[fu.r * p.a.table_stride + page];
+                id = p.a.block_table[(16 * ab < p.front ? 0 : fu.r) * p.a.table_stride + page];
                 if ((unsigned)id >= (unsigned)p.num_pages)
                     int4_set_status(p.status, CG_ERR_CORRUPT);
                 // at most num_pages * heads * page_tokens / 16 blobs: below 2^32 such units (cg_int4.h)

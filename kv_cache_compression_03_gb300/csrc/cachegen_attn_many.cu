@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                     const int vb = u.v0 + b0 + lane;
                     const bool wanted = b0 + lane < n * kBlobs && vb < u.nb;
                     const int blob = wanted ? u.blob(vb) : 0, page = blob / bpp;
-                    const int id = wanted ? table[page] : -1;
+                    const int id = wanted ? (16 * blob < p.front ? p.a.block_table : table)[page] : -1;
                     const bool there = (unsigned)id < (unsigned)p.num_pages;
                     const uint32_t bad = __ballot_sync(0xFFFFFFFFu, wanted && !there);
                     if (bad && lane == 0)

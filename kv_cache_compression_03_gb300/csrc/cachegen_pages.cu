@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(kThreads) k_pages_release(cg_page_release b)
     }
 }
 
-// The page ids, a warp to a request.
+// The page ids, a warp to a request: a load and two stores a page, whose latency is what it takes (4096
+// requests, 450 thousand pages: 19 us with the sums; 64 requests 8.6).
 __global__ void __launch_bounds__(kSlotThreads) k_release_ids(cg_page_release b)
 {
     const int lane = threadIdx.x & 31, r = (int)((blockIdx.x * kSlotThreads + threadIdx.x) >> 5);

@@ -12,9 +12,11 @@ struct AttnArgs {
     float scale2;           // scale * log2(e)
     int64_t kv_limit;       // most tokens of a request
     int32_t least_unit;     // few rows: blobs that a request and head count as at least (0: as they are)
-    // Where all requests begin with the same `shared` tokens, one pass takes those, all rows
-    // of the batch as one request's, and leaves its results in rows; the other takes the
+    // Where all requests begin with the same tokens, either each of them reads those, the first
+    // `front`, by way of the table's first row; or one pass takes the first `shared`, all rows
+    // of the batch as one request's, and leaves its results in rows, and the other takes the
     // tokens behind them (the table and the lengths begin there) and joins the two.
+    int32_t front;          // 0: none
     int32_t shared;         // 0: none
     bool first;             // the pass over the shared tokens
     int32_t items;          // its items that the workspace holds
@@ -43,7 +45,7 @@ __device__ __forceinline__ bool attn_request(const AttnArgs &p, int r, AttnReque
         *error = CG_ERR_CORRUPT;
     else if (p.a.max_q_len > 0 && c1 - c0 > p.a.max_q_len)
         *error = CG_ERR_INVALID_ARG;
-    else if (!p.first && p.shared > 0 && c1 > c0 && kv - p.shared < c1 - c0)
+    else if (!p.first && p.shared + p.front > 0 && c1 > c0 && kv - (p.shared + p.front) < c1 - c0)
         *error = CG_ERR_INVALID_ARG;
     q->row0 = c0;
     q->kv = p.first ? kv : kv - p.shared;

@@ -13,6 +13,16 @@ from kv_cache_compression_03_gb300 import build, cachegen as cg  # noqa: E402
 from test_gpu_int4 import FORMATS, _copy, _dev, _ints, _np, _pair, _rand  # noqa: E402
 
 
+@pytest.fixture(autouse=True, params=["by size", "two passes"])
+def passes(request):
+    """As the sizes have it (the shared tokens here are few), and the shared tokens always in a pass of their own."""
+    if request.param == "by size":
+        yield
+    else:
+        with cg.use_library(build.build_test_variant("test_cg_test_shared_two", ["CG_TEST_SHARED_TWO"])):
+            yield
+
+
 def _case(rng, nq, own, shared, heads, ratio, dim, group, page, layers=1, layer=0, scale=1.0, fill=0xFF):
     """Requests with `own` tokens behind `shared` common ones; unused places hold bytes that are no numbers."""
     held = [-(-k // page) for k in own]
@@ -190,6 +200,7 @@ def test_a_wait_that_runs_out_is_reported():
     args = (_dev(q), _ints(cu), _ints(lens), _ints(table))
     before = got.attention(*args, max_q_len=1, shared=9600)
     got.check()
+    got._sizes.clear()                 # this variant takes two passes, and room for them
     with cg.use_library(variant):
         got.attention(*args, max_q_len=1, shared=9600)
         with pytest.raises(cg.CacheGenError) as e:

@@ -133,9 +133,10 @@ __device__ __forceinline__ void find_digit(ChooseShared<T> &sm, int d, int32_t l
 // What bounds it: 56 instructions for a token (7 make its key, 5 count it, 5 tell whether it stays, the rest
 // are what a block does for its 2048 places and its barriers), of which 1.7 a cycle are issued since blocks
 // wait for one another four times; the weights are read at 1.1 TB/s. 256 rows of 65536: 60 us, 512 rows of
-// 4608: 11. (All three digits over all tokens, each token placed by a vote: 90, 82 us instead of 60.)
+// 4608: 11. Up to 8 tokens a lane need 40 registers, so six blocks of 256 share an SM (6144 rows of 1308: 58 us, 70
+// with four). (All three digits over all tokens, each token placed by a vote: 90, 82 us instead of 60.)
 template <int T, int E>
-__global__ void __launch_bounds__(T, 1024 / T) k_choose_tokens(cg_token_choice c, int size)
+__global__ void __launch_bounds__(T, E <= 8 ? 1536 / T : 1024 / T) k_choose_tokens(cg_token_choice c, int size)
 {
     constexpr int kRowThreads = T, kRowWarps = T / 32;
     __shared__ ChooseShared<T> sm;

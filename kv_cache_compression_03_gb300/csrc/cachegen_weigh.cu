@@ -1134,7 +1134,11 @@ struct WeighSizes {
 // for their sums by row tiles. Here and there, 8 KV heads of 128: one request of 32768 tokens with 32 rows 46 us and
 // 76, 48 rows 62 and 76, 64 rows 67 and 76; eight of 16384 with 64 rows 209 and 237, 64 of 1024 with 64 rows 124
 // and 148. (More rows here would read K again for each 32.)
+// Their seven launches take 31 us where there is little to do, so small batches stay here up to twice the rows: of 80
+// rows, one head of 1024 tokens 25 and 31, eight of 4096 29 and 37, of 16384 55 and 53; of 128 rows, eight heads of
+// 1024 tokens 31 and 35, of 4096 41 and 39.
 constexpr int kTileRows = 64;
+constexpr int64_t kFewPairs = 1 << 21;   // of a row and a token
 constexpr size_t kMostSums = (size_t)1 << 30;   // bytes
 
 constexpr size_t kMostScores = (size_t)256 << 20;   // bytes
@@ -1148,7 +1152,8 @@ WeighSizes sizes_of(const cg_int4_cache *c, const cg_attention *a, const cg_toke
     const int64_t rows = (int64_t)n * ratio, limit = (int64_t)a->table_width * c->page_tokens;
     z.slots = (int32_t)((int64_t)a->tokens * ratio / 8 + a->requests + 1);
     z.tokens = (int32_t)(((limit < w->width ? limit : w->width) + 15) / 16 * 16);
-    if (rows > kTileRows) {
+    const size_t lists = (size_t)a->requests * c->num_heads;
+    if (rows > kTileRows && (rows > 2 * kTileRows || (double)lists * rows * z.tokens > kFewPairs)) {
         z.many = weigh_many_workspace(c, a, z.tokens);
         z.tiles = z.many <= kMostSums;
         z.many = z.tiles ? align256(z.many) : 0;
@@ -1157,7 +1162,6 @@ WeighSizes sizes_of(const cg_int4_cache *c, const cg_attention *a, const cg_toke
     // Scores are stored, and not computed again, where there is room for those that the batch can have: one
     // request of 32768 tokens, 128 rows and 8 heads (134 MB) took 115 us so and 123 computed again; with two of
     // 2048 tokens and 8192 rows each (1 GB), which the L2 does not hold, either took as long.
-    const size_t lists = (size_t)a->requests * c->num_heads;
     z.stored = lists == 0 || (size_t)z.rows * z.tokens <= kMostScores / sizeof(float) / lists;
     z.parts = align256((size_t)kMaxBlocks * 2 * 32 * sizeof(float2));
     z.stats = align256((size_t)c->num_heads * z.slots * 8 * sizeof(float2));
@@ -1223,6 +1227,9 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
     AttnArgs p = attn_args(c, layer, a);
     const WeighSizes z = sizes_of(c, a, w);
     p.few_rows = z.tiles ? kTileRows : INT32_MAX;
+    // short units are not strung together, as behind shared tokens (3 requests of 11 queries and 12 tokens, 8
+    // heads: 103 us with, 17 without)
+    p.least_unit = 16;
     if (p.kv_limit > w->width)
         p.kv_limit = w->width;
     uint8_t *ws = static_cast<uint8_t *>(workspace);

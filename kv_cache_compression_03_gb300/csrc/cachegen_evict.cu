@@ -20,40 +20,6 @@ __device__ __forceinline__ uint32_t key_of(float w)
     return w != w ? 1u : bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
 }
 
-// ---- a row in the registers of a cluster
-
-constexpr int kDigits = 2048;                 // 11, 11 and 10 bits of a key
-constexpr int kMostCluster = 8;
-
-template <int T>
-struct ChooseShared {
-    int32_t count[3][kDigits];
-    int32_t coarse[3][kDigits / 32];          // sums of 32
-    int32_t found[2];
-    int32_t over[T / 32], at[T / 32];         // of each warp
-    int32_t all[2];                           // of the block
-};
-
-__device__ __forceinline__ void cluster_sync(int size)
-{
-    if (size == 1)
-        __syncthreads();
-    else
-        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// The value at `p`, a place in this block's shared memory, in that of the cluster's block `rank`.
-__device__ __forceinline__ int32_t cluster_load(const int32_t *p, int rank)
-{
-    uint32_t at;
-    int32_t v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                 : "=r"(at)
-                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-    return v;
-}
-
 // One more at a place in shared memory, without a branch.
 __device__ __forceinline__ void count_if(bool yes, int32_t *at)
 {
@@ -85,6 +51,177 @@ __device__ __forceinline__ int32_t warp_before(int32_t v, int lane)   // exclusi
             inc += o;
     }
     return inc - v;
+}
+
+// A warp's tokens that stay, from kept[0] on: of its token 32 e + lane, counted from `first` on, bit e of `stays`
+// says that it does, and of `same` that it is at the threshold, where the lowest `take` stay.
+__device__ __forceinline__ void put_kept(int32_t *kept, uint32_t stays, uint32_t same, bool any_same, int32_t take,
+                                         int32_t first, int32_t per_lane, int lane)
+{
+    // lane e: the tokens 32 e .. 32 e + 31 of the warp's
+    uint32_t word = transpose_bits(stays);
+    if (any_same) {
+        uint32_t eq = transpose_bits(same);
+        take = min(max(take - warp_before(__popc(eq), lane), 0), 32);
+        for (; take > 0 && eq != 0; --take, eq &= eq - 1)
+            word |= eq & (0u - eq);
+    }
+    const int32_t here = __popc(word), before = warp_before(here, lane);
+    if (__reduce_add_sync(0xFFFFFFFFu, here) < 8 * per_lane) {   // few: each lane its own
+        kept += before;
+        for (; word != 0; word &= word - 1)
+            *kept++ = first + 32 * lane + __ffs(word) - 1;
+    } else {   // 32 tokens at a time, so that neighbours are written together
+        for (int e = 0; e < per_lane; ++e) {
+            const uint32_t all = __shfl_sync(0xFFFFFFFFu, word, e);
+            const int32_t at_e = __shfl_sync(0xFFFFFFFFu, before, e);
+            if (all >> lane & 1)
+                kept[at_e + __popc(all & ((1u << lane) - 1))] = first + 32 * e + lane;
+        }
+    }
+}
+
+// ---- a row in the registers of a warp or a block
+
+// W warps to a row, each with an equal part of the tokens that are chosen among, up to E a lane (token
+// 32 e + lane of the warp's). The threshold is the largest key that `pick` tokens reach; its bits are found
+// from the top, by counting the tokens that reach each candidate, until exactly `pick` do: some 20 steps of
+// 2 instructions a token, whose sums go through shared memory and one barrier each.
+//
+// What bounds it: those instructions where there are many rows, the steps' chain where there are few. Against digits
+// counted in shared memory, as below, whose places cost a block 5000 instructions however short its row is: 4352
+// rows of 7 tokens 8 us and 37, 3456 of 117 8 and 31, 6144 of 1308 43 and 58; 60 rows of 3669 10 and 14, 56 of
+// 6306 12 and 14. But 512 rows of 4608 17 and 14, 1440 of 7361 42 and 29: from 152 rows on, more than 2048 tokens go
+// by digits.
+constexpr int kBitsThreads = 128;   // where a warp has a row
+
+template <int W, int E>
+__global__ void __launch_bounds__(W == 1 ? kBitsThreads : 32 * W, W == 1 ? 8 : 32 / W) k_choose_bits(cg_token_choice c)
+{
+    __shared__ int32_t sums[2][W], over[W], at[W];
+    const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5, tid = 32 * warp + lane;
+    const int64_t row = W == 1 ? (int64_t)blockIdx.x * (kBitsThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
+    if (W == 1 && row >= (int64_t)c.layers * c.requests * c.heads)
+        return;
+    const int h = (int)(row % c.heads), r = (int)(row / c.heads % c.requests);
+    const int64_t l = row / c.heads / c.requests;
+    const int32_t m = c.lens[r];
+    int32_t *kept = c.kept + row * c.budget;
+    const bool bad = m < 0 || m > c.width;
+    if (bad || m <= c.budget) {   // all of the row's warps
+        for (int64_t i = tid; i < c.budget; i += 32 * W)
+            kept[i] = !bad && i < m ? (int32_t)i : -1;
+        return;
+    }
+    const float *w = c.weights + l * c.layer_stride + r * c.request_stride + h * c.head_stride;
+    // the choice is among [sinks, end), of which `pick` stay
+    const int32_t end = m - c.recent, pick = c.budget - c.sinks - c.recent, n = end - c.sinks;
+    const int32_t per_lane = (n + 32 * W - 1) / (32 * W);            // at most E
+    const int32_t first = c.sinks + warp * per_lane * 32;            // the warp's
+    w += first;
+    const int32_t mine = min(per_lane, (end - first - lane + 31) >> 5);   // tokens of the lane
+    uint32_t key[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        key[e] = e < mine ? __float_as_uint(__ldg(w + 32 * e + lane)) : 0u;
+    for (int i = tid; i < c.sinks; i += 32 * W)
+        kept[i] = i;
+    for (int i = tid; i < c.recent; i += 32 * W)
+        kept[c.budget - c.recent + i] = end + i;
+    if (pick == 0)
+        return;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (e % 4 == 0 && e >= per_lane)   // for all lanes
+            break;
+        key[e] = e < mine ? key_of(__uint_as_float(key[e])) : 0u;   // 0: no token
+    }
+    uint32_t threshold = 0;
+    int32_t reach = n;        // tokens at or above it, always `pick` at least
+    for (int bit = 31; bit >= 0 && reach != pick; --bit) {
+        const uint32_t tried = threshold | 1u << bit;
+        int32_t count = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            if (e % 4 == 0 && e >= per_lane)
+                break;
+            count += key[e] >= tried;
+        }
+        count = __reduce_add_sync(0xFFFFFFFFu, count);
+        if (W > 1) {
+            if (lane == 0)
+                sums[bit & 1][warp] = count;
+            __syncthreads();
+            count = __reduce_add_sync(0xFFFFFFFFu, lane < W ? sums[bit & 1][lane] : 0);
+        }
+        if (count >= pick) {
+            threshold = tried;
+            reach = count;
+        }
+    }
+    const bool exact = reach == pick;   // all of them stay, else those above the threshold and the first at it
+    uint32_t stays = 0, same = 0;       // bit e: of the lane's token
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        if (e % 4 == 0 && e >= per_lane)
+            break;
+        if (key[e] > threshold)
+            stays |= 1u << e;
+        if (key[e] == threshold && key[e] != 0u)
+            same |= 1u << e;
+    }
+    if (exact) {
+        stays |= same;
+        same = 0;
+    }
+    const int32_t above = __reduce_add_sync(0xFFFFFFFFu, __popc(stays)), level = __reduce_add_sync(0xFFFFFFFFu, __popc(same));
+    int32_t pos = c.sinks, taken = 0, left = pick - above;
+    if (W > 1) {
+        if (lane == 0) {
+            over[warp] = above;
+            at[warp] = level;
+        }
+        __syncthreads();
+        const int32_t o = lane < W ? over[lane] : 0, a = lane < W ? at[lane] : 0;
+        left = pick - __reduce_add_sync(0xFFFFFFFFu, o);
+        pos += __reduce_add_sync(0xFFFFFFFFu, lane < warp ? o : 0);
+        taken = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? a : 0);
+    }
+    put_kept(kept + pos + min(taken, left), stays, same, level > 0, left - taken, first, per_lane, lane);
+}
+
+// ---- a row in the registers of a block or a cluster
+
+constexpr int kDigits = 2048;                 // 11, 11 and 10 bits of a key
+constexpr int kMostCluster = 8;
+
+template <int T>
+struct ChooseShared {
+    int32_t count[3][kDigits];
+    int32_t coarse[3][kDigits / 32];          // sums of 32
+    int32_t found[2];
+    int32_t over[T / 32], at[T / 32];         // of each warp
+    int32_t all[2];                           // of the block
+};
+
+__device__ __forceinline__ void cluster_sync(int size)
+{
+    if (size == 1)
+        __syncthreads();
+    else
+        asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The value at `p`, a place in this block's shared memory, in that of the cluster's block `rank`.
+__device__ __forceinline__ int32_t cluster_load(const int32_t *p, int rank)
+{
+    uint32_t at;
+    int32_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at)
+                 : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
 }
 
 // The digit of d's count that the threshold has, where `left` tokens are to be taken from above: by one
@@ -123,7 +260,7 @@ __device__ __forceinline__ void find_digit(ChooseShared<T> &sm, int d, int32_t l
     }
 }
 
-// A cluster of `size` blocks to a row, each with an equal part of the tokens that are chosen among, and of
+// A block or a cluster of `size` blocks to a row, each with an equal part of the tokens that are chosen among, and of
 // that each warp, up to E tokens a lane (token 32 e + lane of the warp's), so the weights are read once. The
 // threshold's key is found in three digits, counted in shared memory. The first has sign, exponent and two
 // bits, so that weights of a few octaves fall into many places; what is above it stays, and only the few
@@ -133,10 +270,9 @@ __device__ __forceinline__ void find_digit(ChooseShared<T> &sm, int d, int32_t l
 // What bounds it: 56 instructions for a token (7 make its key, 5 count it, 5 tell whether it stays, the rest
 // are what a block does for its 2048 places and its barriers), of which 1.7 a cycle are issued since blocks
 // wait for one another four times; the weights are read at 1.1 TB/s. 256 rows of 65536: 60 us, 512 rows of
-// 4608: 11. Up to 8 tokens a lane need 40 registers, so six blocks of 256 share an SM (6144 rows of 1308: 58 us, 70
-// with four). (All three digits over all tokens, each token placed by a vote: 90, 82 us instead of 60.)
+// 4608: 11. (All three digits over all tokens, each token placed by a vote: 90, 82 us instead of 60.)
 template <int T, int E>
-__global__ void __launch_bounds__(T, E <= 8 ? 1536 / T : 1024 / T) k_choose_tokens(cg_token_choice c, int size)
+__global__ void __launch_bounds__(T, 1024 / T) k_choose_tokens(cg_token_choice c, int size)
 {
     constexpr int kRowThreads = T, kRowWarps = T / 32;
     __shared__ ChooseShared<T> sm;
@@ -255,29 +391,7 @@ __global__ void __launch_bounds__(T, E <= 8 ? 1536 / T : 1024 / T) k_choose_toke
     }
     if (size > 1)   // no block's shared memory goes while another one reads it
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    pos += min(taken, left);
-    // lane e: the tokens 32 e .. 32 e + 31 of the warp's
-    uint32_t word = transpose_bits(stays);
-    if (at > 0) {   // of those at the threshold the lowest, as many as are left
-        uint32_t eq = transpose_bits(same);
-        int32_t take = min(max(left - taken - warp_before(__popc(eq), lane), 0), 32);
-        for (; take > 0 && eq != 0; --take, eq &= eq - 1)
-            word |= eq & (0u - eq);
-    }
-    const int32_t here = __popc(word), before = warp_before(here, lane);
-    int32_t *to = kept + pos;
-    if (__reduce_add_sync(0xFFFFFFFFu, here) < 8 * per_lane) {   // few: each lane its own
-        to += before;
-        for (; word != 0; word &= word - 1)
-            *to++ = first + 32 * lane + __ffs(word) - 1;
-    } else {   // 32 tokens at a time, so that neighbours are written together
-        for (int e = 0; e < per_lane; ++e) {
-            const uint32_t all = __shfl_sync(0xFFFFFFFFu, word, e);
-            const int32_t at_e = __shfl_sync(0xFFFFFFFFu, before, e);
-            if (all >> lane & 1)
-                to[at_e + __popc(all & ((1u << lane) - 1))] = first + 32 * e + lane;
-        }
-    }
+    put_kept(kept + pos + min(taken, left), stays, same, at > 0, left - taken, first, per_lane, lane);
     if (size > 1)
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -417,6 +531,14 @@ cudaError_t launch_choice(const cg_token_choice &c, int64_t rows, int size, cuda
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, k_choose_tokens<T, E>, c, size);
+}
+
+template <int W, int E>
+cudaError_t launch_bits(const cg_token_choice &c, int64_t rows, cudaStream_t s)
+{
+    constexpr int kRows = W == 1 ? kBitsThreads / 32 : 1;
+    k_choose_bits<W, E><<<(unsigned)((rows + kRows - 1) / kRows), W == 1 ? kBitsThreads : 32 * W, 0, s>>>(c);
+    return cudaGetLastError();
 }
 
 // ------------------------------------------------------------------ the move
@@ -688,8 +810,8 @@ extern "C" cg_status cg_choose_tokens(const cg_token_choice *c, cg_stream_t stre
     const int64_t rows = lists * c->heads;
     cudaError_t err = cudaSuccess;
     if (rows > 0) {
-        // Blocks to a row: as many as hold it, and more while there are SMs for them. Short rows have small
-        // blocks, four on an SM: what bounds them is each block's chain of barriers.
+        // Blocks to a row that go by digits: as many as hold it, and more while there are SMs for them. Small blocks,
+        // four on an SM, where they do: what bounds them is each block's chain of barriers.
         constexpr int kSmall = 256, kLarge = 512, kMost = 32;   // threads; tokens of one
         int size = 1;
         while (size < kMostCluster && c->width > kMost * kSmall * size)
@@ -699,13 +821,18 @@ extern "C" cg_status cg_choose_tokens(const cg_token_choice *c, cg_stream_t stre
         const int64_t per_block = ((int64_t)c->width + size - 1) / size;
         const bool small = per_block <= kMost * kSmall;
         const int64_t each = (per_block + (small ? kSmall : kLarge) - 1) / (small ? kSmall : kLarge);
-        if (rows * size >= limit || each > kMost)
+        if (c->width <= 2048)
+            err = c->width <= 128   ? launch_bits<1, 4>(*c, rows, s)
+                  : c->width <= 512 ? launch_bits<1, 16>(*c, rows, s)
+                                    : launch_bits<4, 16>(*c, rows, s);
+        else if (c->width <= 8192 && rows < 152)
+            err = c->width <= 5120 ? launch_bits<8, 20>(*c, rows, s) : launch_bits<8, 32>(*c, rows, s);
+        else if (rows * size >= limit || each > kMost)
             k_choose_long<<<(unsigned)rows, kChooseThreads, 0, s>>>(*c);
         else if (!small)
             err = each <= 24 ? launch_choice<kLarge, 24>(*c, rows, size, s) : launch_choice<kLarge, 32>(*c, rows, size, s);
         else
-            err = each <= 4    ? launch_choice<kSmall, 4>(*c, rows, size, s)
-                  : each <= 8  ? launch_choice<kSmall, 8>(*c, rows, size, s)
+            err = each <= 8    ? launch_choice<kSmall, 8>(*c, rows, size, s)
                   : each <= 20 ? launch_choice<kSmall, 20>(*c, rows, size, s)
                                : launch_choice<kSmall, 32>(*c, rows, size, s);
     }

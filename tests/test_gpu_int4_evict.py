@@ -402,7 +402,11 @@ def test_a_wait_of_weigh_that_runs_out_is_reported(nq, ratio):
 @pytest.mark.parametrize("layers,lens,width,budget,recent,sinks", [
     (None, [0, 1, 5, 40], 40, 5, 2, 1), (None, [3000, 100, 2999], 3100, 100, 0, 0), (2, [5000, 4096], 5000, 1024, 1020, 4),
     (3, [65, 64, 63, 1], 65, 64, 8, 3), (1, [70000], 70001, 3000, 64, 16), (2, [500, 7], 600, 0, 0, 0),
-    (2, [20000], 20000, 19999, 5, 5), (None, [33], 33, 200, 100, 7), (4, [9000] * 3, 9000, 1, 0, 0)])
+    (2, [20000], 20000, 19999, 5, 5), (None, [33], 33, 200, 100, 7), (4, [9000] * 3, 9000, 1, 0, 0),
+    # by a warp, four and eight of them; by a block's digits from 152 rows on; by a cluster; from memory
+    (7, [128, 127, 1], 128, 31, 1, 2), (3, [512, 290, 511], 512, 100, 0, 37), (2, [2048, 1500, 513], 2048, 700, 64, 0),
+    (None, [5120, 2049], 5120, 2000, 3, 3), (None, [8192, 5121], 8192, 100, 0, 1), (38, [2500, 2049], 2600, 1000, 7, 4),
+    (39, [8192, 6000], 8192, 64, 0, 0), (None, [98304], 98304, 500, 20, 2), (None, [140000, 9], 150000, 1024, 100, 4)])
 @pytest.mark.parametrize("kind", ["random", "ties", "odd"])
 def test_choose(layers, lens, width, budget, recent, sinks, kind):
     rng = np.random.default_rng(sum(lens) + budget)

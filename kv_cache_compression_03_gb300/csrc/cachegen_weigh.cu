@@ -1133,12 +1133,12 @@ struct WeighSizes {
 // Requests with more rows than this go to the kernels for many (cachegen_weigh_many.cu), where there is room
 // for their sums by row tiles. Here and there, 8 KV heads of 128: one request of 32768 tokens with 32 rows 46 us and
 // 76, 48 rows 62 and 76, 64 rows 67 and 76; eight of 16384 with 64 rows 209 and 237, 64 of 1024 with 64 rows 124
-// and 148. (More rows here would read K again for each 32.)
+// and 148 (there some 3 % more since). More rows here would read K again for each 32.
 // Their seven launches take 31 us where there is little to do, so small batches stay here up to twice the rows: of 80
-// rows, one head of 1024 tokens 25 and 31, eight of 4096 29 and 37, of 16384 55 and 53; of 128 rows, eight heads of
+// rows, one head of 1024 tokens 25 and 31, eight of 4096 29 and 39, of 16384 55 and 53; of 128 rows, eight heads of
 // 1024 tokens 31 and 35, of 4096 41 and 39.
 constexpr int kTileRows = 64;
-constexpr int64_t kFewPairs = 1 << 21;   // of a row and a token
+constexpr int64_t kFewPairs = 3 << 20;   // of a row and a token
 constexpr size_t kMostSums = (size_t)1 << 30;   // bytes
 
 constexpr size_t kMostScores = (size_t)256 << 20;   // bytes

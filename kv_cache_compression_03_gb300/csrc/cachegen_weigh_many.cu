@@ -1,11 +1,14 @@
 // cg_int4_weigh for requests with many query rows: their scores by tcgen05, twice, once for the maximum
 // and sum of every row and once for the sums of every token over the rows.
 //
-// Exact products of 16-bit operands. With m = n - 8 and mid = lo + 8 s, q.k^ = sum_c q_c (s m)_c + sum_g
-// mid_g (sum q)_g. s m has 12 bits: two bf16 values hold it. mid and sum q are fp32, three bf16 values
-// each, of whose nine products the six largest count (the others are below 2^-24). So a tile of scores is
-// 2 D / 16 instructions for the codes and one or two for the groups, all into one accumulator, and
-// differs from the sums in 64 bits by fp32 roundings alone.
+// Exact products of 16-bit operands. With c the code whose value is nearest to 0, m = n - c and mid = lo + c s,
+// q.k^ = sum q (s m) + sum mid (sum q), over channels and over groups. (Where a few channels of a group are
+// large, s follows them and the others' codes lie at c: so their terms are small and none cancel. With 8
+// for c the error was 3e-7 to 1e-6 of the prompts' weights, so 1.5e-7, for 4 % of the time.) s m has 13
+// bits: two bf16 values hold it. mid and sum q are fp32, three bf16 values each, of whose nine products
+// the six largest count (the others are below 2^-24). So a tile of scores is 2 D / 16 instructions for the
+// codes and one or two for the groups, all into one accumulator, and differs from the sums in 64 bits by
+// fp32 roundings alone.
 //
 // One block per 128 rows of a (request, KV head), which stay in shared memory, and tiles of 128 tokens, whose
 // keys eight warps expand, 16 tokens each. Either pass is 128 x 128 x (2 D + 16 or 32):
@@ -22,10 +25,10 @@
 // What bounds it: a tile takes some 2300 cycles in the first pass and 3000 in the second. Its products are 1280,
 // which the shared memory's rate sets (two operands of 4 KB in 64 cycles), the expansion of its keys and its
 // exponentials about as much each; they overlap, but hand the two buffers of keys and scores on by barriers.
-// One request of 32768 tokens, 128 rows, 32 query and 8 KV heads: 28 + 31 us, with all else 76; two prompts of
-// 2048 at 4 rows to a token: 188. Products alone would be 9 of the 28. (Built, and not better: 256 rows to a block,
-// whose low parts had one buffer, 183 for the prompts and 88 for the 128 rows; 16 expanding warps of half a blob,
-// 224 and 84.)
+// One request of 32768 tokens, 128 rows, 32 query and 8 KV heads: 29 + 32 us, with all else 78; two prompts of
+// 2048 at 4 rows to a token: 192. Products alone would be 9 of the 29. (Built, and not better, when those two took
+// 76 and 188: 256 rows to a block, whose low parts had one buffer, 88 and 183; 16 expanding warps of half a blob, 84 and
+// 224; two accumulators for a tile of scores, 81 and 208, for a fifth less of error.)
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -182,6 +185,12 @@ __device__ __forceinline__ uint32_t rest_of(uint32_t c, uint32_t s, uint32_t hi)
                                      *reinterpret_cast<const __nv_bfloat162 *>(&s),
                                      __hneg2(*reinterpret_cast<const __nv_bfloat162 *>(&hi)));
     return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// The code whose value is nearest to 0 (0 where s is; any code gives the same score but for roundings).
+__device__ __forceinline__ float code_of_zero(uint32_t par)
+{
+    return fminf(fmaxf(rintf(__fdividef(-par_lo(par), par_s(par))), 0.0f), 15.0f);
 }
 
 // x in three bf16 values (the high halves): 24 bits.
@@ -555,6 +564,14 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                     uint32_t code[NW], par[NG];
                     load_words(code, blob + B::kKCodes + tok * (D / 2) + t * (D / 8));
                     load_words(par, blob + B::kKParams + tok * 4 * NG);
+                    // a lane of the token's four finds c of group t % NG; 128 + c, twice, for all
+                    const uint32_t own = *reinterpret_cast<const uint32_t *>(blob + B::kKParams + (tok * NG + t % NG) * 4);
+                    const float c_own = code_of_zero(own);
+                    const uint32_t own_from = (0x4300u + (uint32_t)c_own) * 0x10001u;
+                    uint32_t from[NG];
+#pragma unroll
+                    for (int k = 0; k < NG; ++k)
+                        from[k] = NG == 1 ? own_from : __shfl_sync(0xFFFFFFFFu, own_from, (lane & ~3) | k);
 #pragma unroll
                     for (int w = 0; w < NW; ++w) {
                         const uint32_t q = there ? par[w / WPG] : 0;
@@ -562,7 +579,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                         uint32_t hi[4], lo[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            const uint32_t c = centred(code[w], k);
+                            const uint32_t c = centred(code[w], k, from[w / WPG]);
                             hi[k] = mul_bf16x2(c, s2);
                             lo[k] = rest_of(c, s2, hi[k]);
                         }
@@ -570,13 +587,8 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
                         put(sm.k[sl][1], row, 4 * w + t, make_uint4(lo[0], lo[1], lo[2], lo[3]));
                     }
                     if (t < kGroupChunks) {
-                        uint32_t mine = 0;       // the parameters of group t
-#pragma unroll
-                        for (int k = 0; k < NG; ++k)
-                            if (t == k && there)
-                                mine = par[k];
                         uint32_t part[3];
-                        three_parts(fmaf(8.0f, par_s(mine), par_lo(mine)), part);
+                        three_parts(t < NG && there ? fmaf(c_own, par_s(own), par_lo(own)) : 0.0f, part);
                         put_group(sm.kx[sl], row, t, make_uint4(part[0] >> 16 | part[0], part[0] >> 16 | part[1],
                                                           part[1] >> 16 | part[2], 0));
                     }

@@ -37,12 +37,13 @@ __device__ __forceinline__ int lane_once()
     return lane;
 }
 
-// Codes i and i + 4 of a word, less 8, as a bf16 pair: exact out of the mantissa of 128 + n.
-__device__ __forceinline__ uint32_t centred(uint32_t w, int i)
+// Codes i and i + 4 of a word, less c (8), as a bf16 pair: exact out of the mantissa of 128 + n. `from` is 128 + c,
+// twice.
+__device__ __forceinline__ uint32_t centred(uint32_t w, int i, uint32_t from = 0x43084308u)
 {
     const uint32_t x = ((w >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
     uint32_t y;
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0x43084308u));
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(from));
     return y;
 }
 

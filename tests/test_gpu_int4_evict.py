@@ -102,7 +102,8 @@ def test_weigh_scales(scale, qscale, nq):
     _check_weights(out.cpu().numpy()[..., :400], np.zeros(exact.shape, np.float32), exact, tol)
 
 
-def test_weigh_of_channels_that_differ():
+@pytest.mark.parametrize("nq", [1, 70])
+def test_weigh_of_channels_that_differ(nq):
     """Keys as models have them: a few channels many times as large as the others, which lo and s
     follow; the scores are sums of far smaller terms."""
     rng = np.random.default_rng(11)
@@ -112,10 +113,10 @@ def test_weigh_of_channels_that_differ():
     k = ref.bf16_round((_rand(rng, m, heads, dim) * size).astype(np.float32))
     want.store(0, k, k, np.arange(m))
     _copy(want, got)
-    q = ref.bf16_round((_rand(rng, 1, 4, dim) / size).astype(np.float32))
+    q = ref.bf16_round((_rand(rng, nq, 4, dim) / size).astype(np.float32))
     table = np.arange(125)[None]
-    exact, _ = evict.weigh(want, 0, q, [0, 1], [m], table, 0, 0, dim ** -0.5, m)
-    out = got.weigh(_dev(q), _ints([0, 1]), _ints([m]), _ints(table)).cpu().numpy()
+    exact, _ = evict.weigh(want, 0, q, [0, nq], [m], table, 0, 0, dim ** -0.5, m)
+    out = got.weigh(_dev(q), _ints([0, nq]), _ints([m]), _ints(table)).cpu().numpy()
     # no sum here passes 2^7, so what cancels costs 2^-17 at most of the 30 roundings of 2^-24 each
     assert np.abs(out - exact).max() / exact.max() < 30 * 2.0 ** -17
     assert np.linalg.norm(out - exact) / np.linalg.norm(exact) < 2.0 ** -19

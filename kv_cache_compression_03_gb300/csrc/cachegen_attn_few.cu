@@ -71,13 +71,13 @@ constexpr int kPartFloats = RU *(D + 4);
 constexpr int kRoom = 16;
 
 // Four channels of a row's result, sum times inv; m and l are the maximum and the sum of its scores.
-template <int D>
+template <int D, bool kPasses>
 __device__ __forceinline__ void put_row(const AttnArgs &p, const Unit &u, int rr, int ch, float4 sum, float inv,
                                         float m, float l)
 {
     const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
     float4 v = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-    if (p.rows != nullptr) {
+    if (kPasses) {
         const int64_t row = (int64_t)(u.q.row0 + qt) * p.a.q_heads + qh;
         float4 *there = reinterpret_cast<float4 *>(p.rows + row * D + ch);
         if (p.first) {
@@ -111,7 +111,8 @@ struct FewShared {
     uint64_t full[kWarps][kStages];
 };
 
-template <typename B, int NT>
+// kPasses: shared tokens have a pass of their own, and this is one of the two.
+template <typename B, int NT, bool kPasses>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(AttnArgs p, float *parts)
 {
     using S = FewShared<B, NT>;
@@ -132,7 +133,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
     const Place at = schedule<RU>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
     const int64_t begin = blockIdx.x * chunk;
     if (begin >= total) {
-        grid_wait();
+        if (kPasses)
+            grid_wait();
         return;
     }
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
@@ -439,7 +441,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 }
             }
         __syncthreads();
-        grid_wait();   // behind the shared tokens: nothing is written, and no row of theirs read, before
+        if (kPasses)
+            grid_wait();   // behind the shared tokens: nothing is written, and no row of theirs read, before
         const bool from_before = u.b0 > 0, goes_on = u.b1 < u.span.nb;
         float *part = parts + ((size_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * kPartFloats<D, RU>;
         const int rows_here = last_row - row_base + 1;
@@ -508,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                     }
                 } else {
                     const float inv = ls == 0.0f ? 0.0f : pow2(kRoom - v_least) / ls;
-                    put_row<D>(p, u, row_base + row, ch, sum, inv, mx, ls);
+                    put_row<D, kPasses>(p, u, row_base + row, ch, sum, inv, mx, ls);
                 }
             }
             __syncthreads();
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 
 // Block c joins the unit that begins in block c of the main kernel and goes
 // on behind it, if there is one.
-template <int D, int RU>
+template <int D, int RU, bool kPasses>
 __global__ void __launch_bounds__(kThreads, 8) k_attention_join(AttnArgs p, int pieces, const float *parts)
 {
     grid_next();
@@ -598,39 +601,39 @@ __global__ void __launch_bounds__(kThreads, 8) k_attention_join(AttnArgs p, int 
             sum.z = fmaf(v.z, e, sum.z);
             sum.w = fmaf(v.w, e, sum.w);
         }
-        put_row<D>(p, u, row_base + row, ch, sum, inv[row], stat[row].x, stat[row].y);
+        put_row<D, kPasses>(p, u, row_base + row, ch, sum, inv[row], stat[row].x, stat[row].y);
     }
 }
 
 // Row tiles of 8 or 16 query rows, by the most rows that a request can have.
 int tile_rows(int max_rows) { return max_rows <= 8 ? 8 : 16; }
 
-template <typename B, int NT>
+template <typename B, int NT, bool kPasses>
 cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
 {
     using Sh = FewShared<B, NT>;
     int sms = 0;
     cudaError_t err = attn_sm_count(&sms);
     if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(k_attention_few<B, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        err = cudaFuncSetAttribute(k_attention_few<B, NT, kPasses>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)sizeof(Sh));
     if (err != cudaSuccess)
         return err;
     int blocks = (NT == 1 ? 3 : 2) * sms;
     if (blocks > kFewMaxBlocks)
         blocks = kFewMaxBlocks;
-    if (p.rows != nullptr && !p.first) {   // under the pass over the shared tokens
-        err = launch_under(k_attention_few<B, NT>, dim3(blocks), kThreads, sizeof(Sh), s, p, parts);
+    if (kPasses && !p.first) {   // under the pass over the shared tokens
+        err = launch_under(k_attention_few<B, NT, kPasses>, dim3(blocks), kThreads, sizeof(Sh), s, p, parts);
     } else {
-        k_attention_few<B, NT><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
+        k_attention_few<B, NT, kPasses><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
         err = cudaGetLastError();
     }
     if (err != cudaSuccess)
         return err;
     // launched while the main kernel still runs: its own schedule is worked out
     // meanwhile, and it waits for the main kernel before it reads the parts
-    return launch_under(k_attention_join<B::kD, 8 * NT>, dim3(blocks), kThreads, 8 * NT * blocks * sizeof(float), s,
-                        p, blocks, parts);
+    return launch_under(k_attention_join<B::kD, 8 * NT, kPasses>, dim3(blocks), kThreads, 8 * NT * blocks * sizeof(float),
+                        s, p, blocks, parts);
 }
 
 }  // namespace
@@ -647,6 +650,8 @@ cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max
     float *parts = static_cast<float *>(ws);
     return int4_dispatch(head_size, group, [&](auto blob) {
         using B = decltype(blob);
-        return tile_rows(max_rows) == 8 ? launch<B, 1>(p, parts, s) : launch<B, 2>(p, parts, s);
+        if (p.rows == nullptr)
+            return tile_rows(max_rows) == 8 ? launch<B, 1, false>(p, parts, s) : launch<B, 2, false>(p, parts, s);
+        return tile_rows(max_rows) == 8 ? launch<B, 1, true>(p, parts, s) : launch<B, 2, true>(p, parts, s);
     });
 }

@@ -237,7 +237,8 @@ __device__ __forceinline__ int split_of_equals(int units, int n, int items)
 
 // -------------------------------------------------------------------- kernel
 
-template <typename B>
+// kPasses: shared tokens have a pass of their own, and this is one of the two.
+template <typename B, bool kPasses>
 __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, ManyWork work)
 {
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
     tmem_fence_after();
     if (sm.tmem != 0 && tid == 0)   // never: the block took all of it
         int4_set_status(p.status, CG_ERR_CUDA);
-    const int split = p.first ? split_of_equals(sm.units, ((p.shared + 15) / 16 + kBlobs - 1) / kBlobs, work.items)
+    const int split = kPasses && p.first ? split_of_equals(sm.units, ((p.shared + 15) / 16 + kBlobs - 1) / kBlobs, work.items)
                       : sm.units > 0 && sm.units < gridDim.x ? gridDim.x / sm.units : 1;
     if (blockIdx.x == 0 && tid == 0) {
         work.cut[0] = sm.units;
@@ -474,11 +475,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                 if (!alive)
                     break;
                 float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                if (p.rows != nullptr && !p.first)   // for the rows of the shared tokens
+                if (kPasses && !p.first)   // for the rows of the shared tokens
                     grid_wait();
                 const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
                 float *shared_row = nullptr, shared_f = 0.0f;
-                if (p.rows != nullptr && u.parts == 1 && rr < u.rows) {
+                if (kPasses && u.parts == 1 && rr < u.rows) {
                     const int64_t row = (int64_t)(u.q_row0 + qt) * p.a.q_heads + qh;
                     shared_row = p.rows + row * D;
                     if (p.first) {
@@ -516,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         for (int g = 0; g < 8; ++g)
                             *reinterpret_cast<float4 *>(part + (size_t)part_row * D + 32 * c + 4 * g) =
                                 make_float4(o[g], o[8 + g], o[16 + g], o[24 + g]);
-                    } else if (shared_row != nullptr) {
+                    } else if (kPasses && shared_row != nullptr) {
 #pragma unroll
                         for (int g = 0; g < 8; ++g) {
                             float4 *there = reinterpret_cast<float4 *>(shared_row + 32 * c + 4 * g);
@@ -906,11 +907,12 @@ constexpr int kJoinThreads = 128;
 // how many loads are under way (25200 rows in three parts: 30 us with ten, 64 with four).
 constexpr int join_blocks(bool first) { return first ? 1520 : 608; }
 
-template <int D>
+template <int D, bool kPasses>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p, ManyWork work)
 {
     constexpr int kC = D / 32;   // channels of a lane
-    grid_next();   // the pass behind the shared tokens may come up
+    if (kPasses)
+        grid_next();   // the pass behind the shared tokens may come up
     grid_wait();
     if (work.cut[1] == 1)
         return;
@@ -962,7 +964,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
 #pragma unroll
         for (int c = 0; c < kC; ++c)
             sum[c] *= inv;
-        if (p.rows != nullptr) {
+        if (kPasses) {
             const int64_t at_row = (int64_t)(u.q_row0 + qt) * p.a.q_heads + qh;
             float *there = p.rows + at_row * D + kC * lane;
             if (p.first) {
@@ -991,27 +993,27 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
 
 constexpr size_t head_bytes(int items) { return 256 + (sizeof(Unit) * items + 255) / 256 * 256; }
 
-template <typename B>
+template <typename B, bool kPasses>
 cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
 {
     int sms = 0;
     cudaError_t err = attn_sm_count(&sms);
     const int smem = (int)sizeof(ManyShared<B>);
     if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(k_attention_many<B>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        err = cudaFuncSetAttribute(k_attention_many<B, kPasses>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess)
         return err;
     const int items = p.first ? p.items : kMaxBlocks, blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
     const ManyWork work = {items, reinterpret_cast<int32_t *>(ws), reinterpret_cast<Unit *>(ws + 256),
                            reinterpret_cast<float *>(ws + head_bytes(items))};
     if (p.first) {   // the call's first kernel: it follows what is in the stream
-        k_attention_many<B><<<blocks, kThreads, smem, s>>>(p, work);
+        k_attention_many<B, kPasses><<<blocks, kThreads, smem, s>>>(p, work);
         err = cudaGetLastError();
     } else {   // under the kernels for few rows: it works on other rows, with a workspace of its own
-        err = launch_under(k_attention_many<B>, dim3(blocks), kThreads, smem, s, p, work);
+        err = launch_under(k_attention_many<B, kPasses>, dim3(blocks), kThreads, smem, s, p, work);
     }
     if (err == cudaSuccess)
-        err = launch_under(k_attention_many_join<B::kD>, dim3(join_blocks(p.first)), kJoinThreads, 0, s, p, work);
+        err = launch_under(k_attention_many_join<B::kD, kPasses>, dim3(join_blocks(p.first)), kJoinThreads, 0, s, p, work);
     return err;
 }
 
@@ -1031,6 +1033,9 @@ size_t attn_many_workspace(int head_size, int items)
 
 cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, void *ws, cudaStream_t s)
 {
-    return int4_dispatch(head_size, group,
-                         [&](auto blob) { return launch<decltype(blob)>(p, static_cast<uint8_t *>(ws), s); });
+    return int4_dispatch(head_size, group, [&](auto blob) {
+        using B = decltype(blob);
+        uint8_t *at = static_cast<uint8_t *>(ws);
+        return p.rows == nullptr ? launch<B, false>(p, at, s) : launch<B, true>(p, at, s);
+    });
 }

@@ -90,7 +90,7 @@ struct TileWork {
     int32_t most;        // units that there is room for
     int32_t *cut;        // units, pieces of each; then, of either pass, items taken behind the blocks' first
     Piece *heads;        // [units]: their first pieces
-    float2 *parts;       // [items][2][128]: m, l of either half of an item's tiles
+    float2 *parts;       // [items][2][128]: m, l of an item's even tiles and of its odd ones
 };
 
 __device__ __forceinline__ int32_t units_of(const AttnArgs &p, int r, AttnRequest *q)
@@ -316,7 +316,10 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
             float rho = 0.0f;
             if (!kSums && n > 0 && alive)
                 rho = my & 1 ? row_f[my >> 1].y : row_f[my >> 1].x;
-            for (int j = (int)((i - tiles_done) & 1u); j < n && alive; j += 2) {
+            // which of the piece's tiles are in the accumulator goes by how many the block has had, hence by timing;
+            // the parts go by the tiles, so that the join adds in the same order whatever block had the piece
+            const int half = (int)((i - tiles_done) & 1u);
+            for (int j = half; j < n && alive; j += 2) {
                 const uint32_t use = tiles_done + j;
                 alive = wait_all(&sm.s_full[i], use >> 1 & 1, gives_up(0) && use == 2);
                 if (!alive)
@@ -426,7 +429,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
             if (!alive)
                 break;
             if (!kSums)
-                work.parts[((int64_t)u.item * 2 + i) * kTile + my] = make_float2(m, l);
+                work.parts[((int64_t)u.item * 2 + half) * kTile + my] = make_float2(m, l);
             piece_over(n);
         }
     } else if (warp < kSoftWarps + kExpandWarps) {
@@ -748,7 +751,7 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
     grid_wait();
 }
 
-// A row's parts: of each piece of its unit, either half of the tiles. Slices of the block take them in turns.
+// A row's parts: of each piece of its unit, its even tiles and its odd ones. Slices of the block take them in turns.
 constexpr int kJoinSlices = 4, kJoinThreads = kTile * kJoinSlices;
 
 __global__ void __launch_bounds__(kJoinThreads) k_weigh_tiles_join(AttnArgs p, WeighArgs a, TileWork work)

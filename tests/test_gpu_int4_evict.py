@@ -383,6 +383,24 @@ def test_weigh_gives_the_same_bits_in_graphs_and_on_streams(nq, ratio):
     got.check()
 
 
+def test_weigh_of_more_units_than_blocks_gives_the_same_bits():
+    """672 units of 128 rows, of odd and even numbers of tiles: whichever blocks take them, and in whatever order."""
+    rng = np.random.default_rng(17)
+    nq, nkv, heads, ratio = [700, 333, 512, 90, 1000], [1100, 333, 900, 700, 1000], 8, 4
+    table, want, got, cu, q = _weigh_case(rng, nq, nkv, ratio, 64, 32, 16, heads=heads)
+    assert sum(-(-n * ratio // 128) for n in nq) * heads > 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    args = (_dev(q), _ints(cu), _ints(nkv), _ints(table))
+    first = got.weigh(*args, max_q_len=max(nq))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for i in range(40):   # one at a time, and beside one another
+        outs = [got.weigh(*args, max_q_len=max(nq), stream=s) for s in streams[:1 + i % 3]]
+        torch.cuda.synchronize()
+        for o in outs:
+            assert torch.equal(o, first)
+    got.check()
+
+
 @pytest.mark.parametrize("nq,ratio", [(1, 4), (40, 4)])
 def test_a_wait_of_weigh_that_runs_out_is_reported(nq, ratio):
     variant = build.build_test_variant("test_cg_test_attn_timeout", ["CG_TEST_ATTN_TIMEOUT"])

@@ -554,7 +554,8 @@ cg_status cg_int4_attention(const cg_int4_cache *cache, int32_t layer, const cg_
  * shared_tokens is a multiple of page_tokens and window is 0 (CG_ERR_INVALID_ARG; what
  * of the first tokens is in a window depends on the query); shared_tokens = 0 is
  * cg_int4_attention. A request whose new tokens do not all lie behind the shared ones
- * sets CG_ERR_INVALID_ARG in the cache's status (its rows are left as they were).
+ * sets CG_ERR_INVALID_ARG in the cache's status, and one whose rows do not all lie before
+ * cu_q[requests] CG_ERR_CORRUPT (their rows are left as they were).
  * A page id outside the cache among the shared ones hides its tokens from every query.
  * The workspace's size depends on requests and shared_tokens too, and is at most tokens * q_heads *
  * (head_size + 2) floats and 86 MB larger. */

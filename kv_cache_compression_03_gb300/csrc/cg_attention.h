@@ -37,15 +37,20 @@ struct AttnRequest {
 __device__ __forceinline__ bool attn_request(const AttnArgs &p, int r, AttnRequest *q,
                                              uint32_t *error)
 {
-    // in the pass over the shared tokens cu_q points at its last entry, the batch's rows
-    const int32_t c0 = p.first ? 0 : p.a.cu_q[r], c1 = p.a.cu_q[p.first ? 0 : r + 1];
+    // in the pass over the shared tokens cu_q points at its last entry, the batch's rows (all that
+    // there can be where it is beyond them: the other pass, whose requests lie before it, reports it)
+    const int32_t c0 = p.first ? 0 : p.a.cu_q[r];
+    const int32_t c1 = p.first ? min(p.a.cu_q[0], p.a.tokens) : p.a.cu_q[r + 1];
+    const bool shares = !p.first && p.shared + p.front > 0;
     const int32_t kv = p.first ? p.shared : p.a.kv_lens[r];
     *error = CG_OK;
     if (c0 < 0 || c1 < c0 || c1 > p.a.tokens || kv < 0 || kv > p.kv_limit)
         *error = CG_ERR_CORRUPT;
+    else if (shares && c1 > c0 && c1 > p.a.cu_q[p.a.requests])   // rows that the pass over the shared tokens had not
+        *error = CG_ERR_CORRUPT;
     else if (p.a.max_q_len > 0 && c1 - c0 > p.a.max_q_len)
         *error = CG_ERR_INVALID_ARG;
-    else if (!p.first && p.shared + p.front > 0 && c1 > c0 && kv - (p.shared + p.front) < c1 - c0)
+    else if (shares && c1 > c0 && kv - (p.shared + p.front) < c1 - c0)
         *error = CG_ERR_INVALID_ARG;
     q->row0 = c0;
     q->kv = p.first ? kv : kv - p.shared;

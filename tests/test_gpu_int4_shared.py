@@ -167,6 +167,38 @@ def test_errors(nq):
             got.attention(_dev(q), _ints(cu), _ints(lens), _ints(table), **kw)
 
 
+@pytest.mark.parametrize("nq", [1, 40])
+def test_bounds_of_rows_that_do_not_ascend(nq, monkeypatch):
+    """Whichever requests they leave without fault are right, the rows of the others stay as they were, also where
+    the workspace held something else before."""
+    rng = np.random.default_rng(nq)
+    table, want, got, cu, q, lens = _case(rng, [nq] * 4, [nq + 5, nq, nq + 30, nq + 1], 960, 2, 2, 64, 32, 16)
+    o, tol = ref.attention(want, 0, q, cu, lens, table, 0, 0, 0.125)
+    empty = torch.empty
+
+    def of_no_numbers(*a, **k):
+        t = empty(*a, **k)
+        return t.fill_(0xFF) if t.dtype is torch.uint8 else t
+
+    monkeypatch.setattr(torch, "empty", of_no_numbers)
+    # the bounds, in rows of a request, and the requests that they leave
+    for at, right in (([0, 1, 2, 3, 5], [0, 1, 2]), ([0, 1, 2, 3, 2], [0, 1]), ([0, 1, 2, 3, -1], []),
+                      ([0, 9, 2, 3, 4], [2, 3]), ([0, 1, -3, 3, 4], [0, 3]), ([0, 1, 2, 1 << 25, 4], [0, 1]),
+                      ([0, 1, 2, 3, 0], [])):
+        out = torch.full((4 * nq, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+        got.attention(_dev(q), _ints(np.array(at) * nq), _ints(lens), _ints(table), out=out, shared=960)
+        with pytest.raises(cg.CacheGenError) as e:
+            got.check()
+        assert e.value.status == cg.CG_ERR_CORRUPT
+        out = _np(out)
+        for r in range(4):
+            rows = slice(r * nq, (r + 1) * nq)
+            if r in right:
+                assert (np.abs(out[rows] - o[rows]) <= tol[rows]).all(), (at, r)
+            else:
+                assert (out[rows] == 3.0).all(), (at, r)
+
+
 @pytest.mark.parametrize("nq,n", [(1, 5), (1, 30), (50, 3)])
 def test_the_same_bits_in_graphs_and_on_streams(nq, n):
     rng = np.random.default_rng(2)

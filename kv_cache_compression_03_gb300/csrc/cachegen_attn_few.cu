@@ -71,13 +71,13 @@ constexpr int kPartFloats = RU *(D + 4);
 constexpr int kRoom = 16;
 
 // Four channels of a row's result, sum times inv; m and l are the maximum and the sum of its scores.
-template <int D, bool kPasses>
+template <int D, bool kShared>
 __device__ __forceinline__ void put_row(const AttnArgs &p, const Unit &u, int rr, int ch, float4 sum, float inv,
                                         float m, float l)
 {
     const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
     float4 v = make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
-    if (kPasses) {
+    if (kShared && p.rows != nullptr) {
         const int64_t row = (int64_t)(u.q.row0 + qt) * p.a.q_heads + qh;
         float4 *there = reinterpret_cast<float4 *>(p.rows + row * D + ch);
         if (p.first) {
@@ -111,11 +111,12 @@ struct FewShared {
     uint64_t full[kWarps][kStages];
 };
 
-// kPasses: shared tokens have a pass of their own, and this is one of the two.
-template <typename B, int NT, bool kPasses>
+// kShared: there are shared tokens, and where they have a pass of their own (p.rows), this is one of the two.
+template <typename B, int NT, bool kShared>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(AttnArgs p, float *parts)
 {
     using S = FewShared<B, NT>;
+    using K = BatchOf<kShared, kShared>;
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG, RU = S::RU;
     constexpr int HB = S::HB, kStages = S::kStages;
     extern __shared__ __align__(128) uint8_t smem_raw[];
@@ -130,25 +131,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             bar_init(&sm.full[warp][i], HB);   // one arrival per blob of the step
     bar_init_fence();
     int64_t total, chunk;
-    const Place at = schedule<RU>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
+    const Place at = schedule<RU, K>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
     const int64_t begin = blockIdx.x * chunk;
     if (begin >= total) {
-        if (kPasses)
+        if (kShared)
             grid_wait();
         return;
     }
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
 
-    const int bpp = p.page_tokens / 16;
+    const int bpp = p.page_tokens / 16, pos_ratio = kShared ? p.pos_ratio : p.ratio;
     // ---- the warp's feeder: copies some steps ahead of the warp, through the same units.
     // Up to 32 blobs of the stretch are looked up at once, one by each lane, which then
     // issues its own blob's copy.
     Unit first;
-    unit_at<RU>(p, at, count, &first);
+    unit_at<RU, K>(p, at, count, &first);
     Unit fu = first;
     int64_t f_pos = fu.b1 - fu.b0;   // blobs of the piece up to the end of the feeder's unit
     int f_b, f_e;                    // blobs of the stretch not looked up yet
-    warp_range(fu, warp, &f_b, &f_e);
+    warp_range<K>(fu, warp, &f_b, &f_e);
     int f_i = 0, f_n = 0;            // blobs issued and looked up of the current 32
     uint32_t f_off = 0, f_ok = 0;    // the lane's blob (in 128-byte units of the layer); valid lanes
     uint32_t issued = 0;
@@ -159,9 +160,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             while (f_b >= f_e) {
                 if (f_pos >= count)
                     return;
-                unit_next<RU>(p, count - f_pos, &fu);
+                unit_next<RU, K>(p, count - f_pos, &fu);
                 f_pos += fu.b1 - fu.b0;
-                warp_range(fu, warp, &f_b, &f_e);
+                warp_range<K>(fu, warp, &f_b, &f_e);
             }
             f_i = 0;
             f_n = f_e - f_b < 32 ? f_e - f_b : 32;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             if (lane < f_n && fu.q.kv > 0) {
                 const int vb = f_b + lane, ab = vb < fu.span.sink ? vb : vb + fu.span.skip;
                 const int page = ab / bpp;
-                id = p.a.block_table[(16 * ab < p.front ? 0 : fu.r) * p.a.table_stride + page];
+                id = p.a.block_table[(kShared && 16 * ab < p.front ? 0 : fu.r) * p.a.table_stride + page];
                 if ((unsigned)id >= (unsigned)p.num_pages)
                     int4_set_status(p.status, CG_ERR_CORRUPT);
                 // at most num_pages * heads * page_tokens / 16 blobs: below 2^32 such units (cg_int4.h)
@@ -214,13 +215,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int rr = row_base + 8 * nt + 2 * t + j;
-                x[nt][j] = rr < u.q.rows ? u.q.x0 + rr / p.pos_ratio : -1;
+                x[nt][j] = rr < u.q.rows ? u.q.x0 + rr / pos_ratio : -1;
             }
         }
         // positions of the tile's first and last row: blobs that both see whole need no mask
         const int last_row = (row_base + RU < u.q.rows ? row_base + RU : u.q.rows) - 1;
-        const int x_lo = u.q.x0 + row_base / p.pos_ratio;
-        const int x_hi = u.q.x0 + last_row / p.pos_ratio;
+        const int x_lo = u.q.x0 + row_base / pos_ratio;
+        const int x_hi = u.q.x0 + last_row / pos_ratio;
         const int window = p.a.window > 0 ? p.a.window : INT32_MAX;
 
         float o[NW * 2][NT][4] = {};
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
             m[nt][0] = m[nt][1] = kNone;
 
         int b, e;
-        warp_range(u, warp, &b, &e);
+        warp_range<K>(u, warp, &b, &e);
         for (; b < e; b += HB) {
             const int st = used & (kStages - 1);
             if (alive) {
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                 }
             }
         __syncthreads();
-        if (kPasses)
+        if (kShared)
             grid_wait();   // behind the shared tokens: nothing is written, and no row of theirs read, before
         const bool from_before = u.b0 > 0, goes_on = u.b1 < u.span.nb;
         float *part = parts + ((size_t)blockIdx.x * 2 + (from_before ? 0 : 1)) * kPartFloats<D, RU>;
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
                     }
                 } else {
                     const float inv = ls == 0.0f ? 0.0f : pow2(kRoom - v_least) / ls;
-                    put_row<D, kPasses>(p, u, row_base + row, ch, sum, inv, mx, ls);
+                    put_row<D, kShared>(p, u, row_base + row, ch, sum, inv, mx, ls);
                 }
             }
             __syncthreads();
@@ -519,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
         pos += u.b1 - u.b0;
         if (pos >= count)
             break;
-        unit_next<RU>(p, count - pos, &u);
+        unit_next<RU, K>(p, count - pos, &u);
     }
     // a wait that ran out: the copies still in flight, of the steps from that one on, must
     // land before the block's memory goes
@@ -532,18 +533,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) k_attention_few(Att
 
 // Block c joins the unit that begins in block c of the main kernel and goes
 // on behind it, if there is one.
-template <int D, int RU, bool kPasses>
+template <int D, int RU, bool kShared>
 __global__ void __launch_bounds__(kThreads, 8) k_attention_join(AttnArgs p, int pieces, const float *parts)
 {
+    using K = BatchOf<kShared, kShared>;
     grid_next();
     int64_t total, chunk;
     const int c = blockIdx.x;
     // where the next piece starts: inside the unit, if one goes on
-    const Place at = schedule<RU>(p, pieces, c + 1, 0, false, &total, &chunk);
+    const Place at = schedule<RU, K>(p, pieces, c + 1, 0, false, &total, &chunk);
     const int64_t border = (c + 1) * chunk;
     Unit u;
     if (border < total)
-        unit_at<RU>(p, at, 1, &u);
+        unit_at<RU, K>(p, at, 1, &u);
     grid_wait();   // for the main kernel's parts
     if (border >= total || u.b0 == 0 || u.b0 > chunk)
         return;   // nothing there, or begins at the border, or before block c
@@ -601,38 +603,38 @@ __global__ void __launch_bounds__(kThreads, 8) k_attention_join(AttnArgs p, int 
             sum.z = fmaf(v.z, e, sum.z);
             sum.w = fmaf(v.w, e, sum.w);
         }
-        put_row<D, kPasses>(p, u, row_base + row, ch, sum, inv[row], stat[row].x, stat[row].y);
+        put_row<D, kShared>(p, u, row_base + row, ch, sum, inv[row], stat[row].x, stat[row].y);
     }
 }
 
 // Row tiles of 8 or 16 query rows, by the most rows that a request can have.
 int tile_rows(int max_rows) { return max_rows <= 8 ? 8 : 16; }
 
-template <typename B, int NT, bool kPasses>
+template <typename B, int NT, bool kShared>
 cudaError_t launch(const AttnArgs &p, float *parts, cudaStream_t s)
 {
     using Sh = FewShared<B, NT>;
     int sms = 0;
     cudaError_t err = attn_sm_count(&sms);
     if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(k_attention_few<B, NT, kPasses>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        err = cudaFuncSetAttribute(k_attention_few<B, NT, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    (int)sizeof(Sh));
     if (err != cudaSuccess)
         return err;
     int blocks = (NT == 1 ? 3 : 2) * sms;
     if (blocks > kFewMaxBlocks)
         blocks = kFewMaxBlocks;
-    if (kPasses && !p.first) {   // under the pass over the shared tokens
-        err = launch_under(k_attention_few<B, NT, kPasses>, dim3(blocks), kThreads, sizeof(Sh), s, p, parts);
+    if (kShared && p.rows != nullptr && !p.first) {   // under the pass over the shared tokens
+        err = launch_under(k_attention_few<B, NT, kShared>, dim3(blocks), kThreads, sizeof(Sh), s, p, parts);
     } else {
-        k_attention_few<B, NT, kPasses><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
+        k_attention_few<B, NT, kShared><<<blocks, kThreads, sizeof(Sh), s>>>(p, parts);
         err = cudaGetLastError();
     }
     if (err != cudaSuccess)
         return err;
     // launched while the main kernel still runs: its own schedule is worked out
     // meanwhile, and it waits for the main kernel before it reads the parts
-    return launch_under(k_attention_join<B::kD, 8 * NT, kPasses>, dim3(blocks), kThreads, 8 * NT * blocks * sizeof(float),
+    return launch_under(k_attention_join<B::kD, 8 * NT, kShared>, dim3(blocks), kThreads, 8 * NT * blocks * sizeof(float),
                         s, p, blocks, parts);
 }
 
@@ -650,7 +652,7 @@ cudaError_t attn_few_launch(const AttnArgs &p, int head_size, int group, int max
     float *parts = static_cast<float *>(ws);
     return int4_dispatch(head_size, group, [&](auto blob) {
         using B = decltype(blob);
-        if (p.rows == nullptr)
+        if (p.shared + p.front == 0)
             return tile_rows(max_rows) == 8 ? launch<B, 1, false>(p, parts, s) : launch<B, 2, false>(p, parts, s);
         return tile_rows(max_rows) == 8 ? launch<B, 1, true>(p, parts, s) : launch<B, 2, true>(p, parts, s);
     });

@@ -146,16 +146,19 @@ struct ManyWork {
 template <int D>
 constexpr size_t kPartFloats = (size_t)kRows * (D + 2);
 
+// (kShared as attn_request has it)
+template <bool kShared>
 __device__ __forceinline__ int32_t units_of(const AttnArgs &p, int r, AttnRequest *q)
 {
     uint32_t error;
-    if (r >= p.a.requests || !attn_request(p, r, q, &error) || q->rows <= p.few_rows)
+    if (r >= p.a.requests || !attn_request<kShared>(p, r, q, &error) || q->rows <= p.few_rows)
         return 0;
     return (q->rows + kRows - 1) / kRows * p.heads;   // at most tokens * q_heads
 }
 
 // One warp: unit `want` of the batch into *u. It goes on from where the last
 // call stood (32 requests from *r0 on, `*before` units ahead of them).
+template <bool kShared>
 __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t item, int split, int *r0, int64_t *before,
                                           Unit *u, Unit *heads)
 {
@@ -170,7 +173,7 @@ __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t item, int s
             return;
         }
         AttnRequest q;
-        const int w = units_of(p, *r0 + lane, &q);
+        const int w = units_of<kShared>(p, *r0 + lane, &q);
         int64_t inc = w;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -187,11 +190,12 @@ __device__ __forceinline__ void find_unit(const AttnArgs &p, int64_t item, int s
         const int src = __ffs(mine) - 1;
         const int off = __shfl_sync(0xFFFFFFFFu, (int)(want - start), src);
         const int r = *r0 + src;
-        units_of(p, r, &q);
+        units_of<kShared>(p, r, &q);
         // the last rows, which see most, first
         const int tile = (q.rows + kRows - 1) / kRows - 1 - off / p.heads;
         const int row0 = tile * kRows, rows = min(kRows, q.rows - row0), x0 = q.x0;
-        const int x_first = x0 + row0 / p.pos_ratio, x_last = x0 + (row0 + rows - 1) / p.pos_ratio;
+        const int pos_ratio = kShared ? p.pos_ratio : p.ratio;
+        const int x_first = x0 + row0 / pos_ratio, x_last = x0 + (row0 + rows - 1) / pos_ratio;
         const int end = x_last < 0 ? 0 : x_last / 16 + 1;
         int sink = 0, skip = 0;
         const int64_t low = (int64_t)x_first + 1 - p.a.window;
@@ -237,8 +241,8 @@ __device__ __forceinline__ int split_of_equals(int units, int n, int items)
 
 // -------------------------------------------------------------------- kernel
 
-// kPasses: shared tokens have a pass of their own, and this is one of the two.
-template <typename B, bool kPasses>
+// kShared: there are shared tokens, and where they have a pass of their own (p.rows), this is one of the two.
+template <typename B, bool kShared>
 __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, ManyWork work)
 {
     constexpr int D = B::kD, NW = B::kWords, NG = B::kGroups, WPG = NW / NG;
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
         int64_t mine = 0;
         for (int r = tid; r < p.a.requests; r += kThreads) {
             AttnRequest q;
-            mine += units_of(p, r, &q);
+            mine += units_of<kShared>(p, r, &q);
         }
         // only whether there are fewer than blocks matters
         const int few = __reduce_add_sync(0xFFFFFFFFu, (int)min(mine, (int64_t)(1 << 20)));
@@ -302,13 +306,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
     tmem_fence_after();
     if (sm.tmem != 0 && tid == 0)   // never: the block took all of it
         int4_set_status(p.status, CG_ERR_CUDA);
-    const int split = kPasses && p.first ? split_of_equals(sm.units, ((p.shared + 15) / 16 + kBlobs - 1) / kBlobs, work.items)
+    const int split = kShared && p.first ? split_of_equals(sm.units, ((p.shared + 15) / 16 + kBlobs - 1) / kBlobs, work.items)
                       : sm.units > 0 && sm.units < gridDim.x ? gridDim.x / sm.units : 1;
     if (blockIdx.x == 0 && tid == 0) {
         work.cut[0] = sm.units;
         work.cut[1] = split;
     }
     const int bpp = p.page_tokens / 16;
+    const int pos_ratio = kShared ? p.pos_ratio : p.ratio;
+    const bool passes = kShared && p.rows != nullptr;
     // Every role walks the block's units on its own and meets the others at the barriers only,
     // so that the next unit's queries, keys and values come in under the last one's products.
     uint32_t un = 0;             // units begun
@@ -352,10 +358,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
             const int tile = turns ? 0 : i, first = turns ? i : 0, step = turns ? 2 : 1;
             if (tile < u.tiles_q) {
                 const int rr = u.row0 + 128 * tile + 32 * (warp & 3) + lane;
-                const int x = rr < u.rows ? u.x0 + rr / p.pos_ratio : -1;
+                const int x = rr < u.rows ? u.x0 + rr / pos_ratio : -1;
                 const int last_row = min(u.row0 + 128 * tile + 128, u.rows) - 1;
-                const int x_lo = u.x0 + (u.row0 + 128 * tile) / p.pos_ratio;
-                const int x_hi = u.x0 + last_row / p.pos_ratio;
+                const int x_lo = u.x0 + (u.row0 + 128 * tile) / pos_ratio;
+                const int x_hi = u.x0 + last_row / pos_ratio;
                 float m = kNone, l = 0.0f;
                 bool alive = true;
                 for (int j = first; j < n; j += step) {
@@ -475,11 +481,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                 if (!alive)
                     break;
                 float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                if (kPasses && !p.first)   // for the rows of the shared tokens
+                if (passes && !p.first)   // for the rows of the shared tokens
                     grid_wait();
                 const int qt = rr / p.ratio, qh = u.h * p.ratio + rr - qt * p.ratio;
                 float *shared_row = nullptr, shared_f = 0.0f;
-                if (kPasses && u.parts == 1 && rr < u.rows) {
+                if (passes && u.parts == 1 && rr < u.rows) {
                     const int64_t row = (int64_t)(u.q_row0 + qt) * p.a.q_heads + qh;
                     shared_row = p.rows + row * D;
                     if (p.first) {
@@ -517,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                         for (int g = 0; g < 8; ++g)
                             *reinterpret_cast<float4 *>(part + (size_t)part_row * D + 32 * c + 4 * g) =
                                 make_float4(o[g], o[8 + g], o[16 + g], o[24 + g]);
-                    } else if (kPasses && shared_row != nullptr) {
+                    } else if (passes && shared_row != nullptr) {
 #pragma unroll
                         for (int g = 0; g < 8; ++g) {
                             float4 *there = reinterpret_cast<float4 *>(shared_row + 32 * c + 4 * g);
@@ -716,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                 const uint32_t slot = which % kUnits;
                 if (!wait_all(&sm.u_empty[slot], (which / kUnits & 1) ^ 1))
                     return false;
-                find_unit(p, blockIdx.x + (int64_t)which * gridDim.x, split, &u_r0, &u_before, &sm.unit[slot],
+                find_unit<kShared>(p, blockIdx.x + (int64_t)which * gridDim.x, split, &u_r0, &u_before, &sm.unit[slot],
                           work.heads);
                 if (lane == 0)
                     bar_arrive(&sm.u_full[slot]);
@@ -734,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attention_many(AttnArgs p, Many
                     const int vb = u.v0 + b0 + lane;
                     const bool wanted = b0 + lane < n * kBlobs && vb < u.nb;
                     const int blob = wanted ? u.blob(vb) : 0, page = blob / bpp;
-                    const int id = wanted ? (16 * blob < p.front ? p.a.block_table : table)[page] : -1;
+                    const int id = wanted ? (kShared && 16 * blob < p.front ? p.a.block_table : table)[page] : -1;
                     const bool there = (unsigned)id < (unsigned)p.num_pages;
                     const uint32_t bad = __ballot_sync(0xFFFFFFFFu, wanted && !there);
                     if (bad && lane == 0)
@@ -907,11 +913,11 @@ constexpr int kJoinThreads = 128;
 // how many loads are under way (25200 rows in three parts: 30 us with ten, 64 with four).
 constexpr int join_blocks(bool first) { return first ? 1520 : 608; }
 
-template <int D, bool kPasses>
+template <int D, bool kShared>
 __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p, ManyWork work)
 {
     constexpr int kC = D / 32;   // channels of a lane
-    if (kPasses)
+    if (kShared)
         grid_next();   // the pass behind the shared tokens may come up
     grid_wait();
     if (work.cut[1] == 1)
@@ -964,7 +970,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
 #pragma unroll
         for (int c = 0; c < kC; ++c)
             sum[c] *= inv;
-        if (kPasses) {
+        if (kShared && p.rows != nullptr) {
             const int64_t at_row = (int64_t)(u.q_row0 + qt) * p.a.q_heads + qh;
             float *there = p.rows + at_row * D + kC * lane;
             if (p.first) {
@@ -993,27 +999,27 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
 
 constexpr size_t head_bytes(int items) { return 256 + (sizeof(Unit) * items + 255) / 256 * 256; }
 
-template <typename B, bool kPasses>
+template <typename B, bool kShared>
 cudaError_t launch(const AttnArgs &p, uint8_t *ws, cudaStream_t s)
 {
     int sms = 0;
     cudaError_t err = attn_sm_count(&sms);
     const int smem = (int)sizeof(ManyShared<B>);
     if (err == cudaSuccess)
-        err = cudaFuncSetAttribute(k_attention_many<B, kPasses>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        err = cudaFuncSetAttribute(k_attention_many<B, kShared>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess)
         return err;
     const int items = p.first ? p.items : kMaxBlocks, blocks = sms < kMaxBlocks ? sms : kMaxBlocks;
     const ManyWork work = {items, reinterpret_cast<int32_t *>(ws), reinterpret_cast<Unit *>(ws + 256),
                            reinterpret_cast<float *>(ws + head_bytes(items))};
     if (p.first) {   // the call's first kernel: it follows what is in the stream
-        k_attention_many<B, kPasses><<<blocks, kThreads, smem, s>>>(p, work);
+        k_attention_many<B, kShared><<<blocks, kThreads, smem, s>>>(p, work);
         err = cudaGetLastError();
     } else {   // under the kernels for few rows: it works on other rows, with a workspace of its own
-        err = launch_under(k_attention_many<B, kPasses>, dim3(blocks), kThreads, smem, s, p, work);
+        err = launch_under(k_attention_many<B, kShared>, dim3(blocks), kThreads, smem, s, p, work);
     }
     if (err == cudaSuccess)
-        err = launch_under(k_attention_many_join<B::kD, kPasses>, dim3(join_blocks(p.first)), kJoinThreads, 0, s, p, work);
+        err = launch_under(k_attention_many_join<B::kD, kShared>, dim3(join_blocks(p.first)), kJoinThreads, 0, s, p, work);
     return err;
 }
 
@@ -1036,6 +1042,6 @@ cudaError_t attn_many_launch(const AttnArgs &p, int head_size, int group, void *
     return int4_dispatch(head_size, group, [&](auto blob) {
         using B = decltype(blob);
         uint8_t *at = static_cast<uint8_t *>(ws);
-        return p.rows == nullptr ? launch<B, false>(p, at, s) : launch<B, true>(p, at, s);
+        return p.shared + p.front > 0 ? launch<B, true>(p, at, s) : launch<B, false>(p, at, s);
     });
 }

@@ -259,7 +259,7 @@ struct Feeder {
             do {
                 if (pos >= count)
                     return false;
-                unit_next<RU>(p, count - pos, &u);
+                unit_next<RU, WeighBatch>(p, count - pos, &u);
                 t = tile_of<RU>(p, u);
                 pos += u.b1 - u.b0;
                 tile_range(u, t, warp, &b, &e);
@@ -359,13 +359,13 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
             bar_init(&sm.full[warp][i], 1);
     bar_init_fence();
     int64_t total, chunk;
-    const Place at = schedule<RU>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
+    const Place at = schedule<RU, WeighBatch>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
     const int64_t begin = blockIdx.x * chunk;
     if (begin >= total)
         return;
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
     Unit first;
-    unit_at<RU>(p, at, count, &first);
+    unit_at<RU, WeighBatch>(p, at, count, &first);
     Feeder<B, RU, 1, kRing> feeder;
     feeder.ring = sm.ring[warp];
     feeder.full = sm.full[warp];
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, kStatBlocks) k_weigh_stats(AttnArgs 
         __syncthreads();
         if (pos >= count)
             break;
-        unit_next<RU>(p, count - pos, &end);
+        unit_next<RU, WeighBatch>(p, count - pos, &end);
         if (lane == 0)
             now = {end, tile_of<RU>(p, end), pos, 0, 0};
         __syncwarp();
@@ -702,13 +702,13 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
             bar_init(&sm.full[warp][i], HB);
     bar_init_fence();
     int64_t total, chunk;
-    const Place at = schedule<8>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
+    const Place at = schedule<8, WeighBatch>(p, gridDim.x, blockIdx.x, 0, blockIdx.x == 0, &total, &chunk);
     const int64_t begin = blockIdx.x * chunk;
     if (begin >= total)
         return;
     const int64_t count = (begin + chunk < total ? begin + chunk : total) - begin;
     Unit first;
-    unit_at<8>(p, at, count, &first);
+    unit_at<8, WeighBatch>(p, at, count, &first);
     Feeder<B, 8, HB, kSteps> feeder;
     feeder.ring = sm.ring[warp];
     feeder.full = sm.full[warp];
@@ -836,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, kFewBlocks) k_weigh_few(AttnArgs p, 
         __syncthreads();
         if (pos >= count)
             break;
-        unit_next<8>(p, count - pos, &end);
+        unit_next<8, WeighBatch>(p, count - pos, &end);
         if (lane == 0)
             now = {end, tile_of<8>(p, end), pos, 0, 0};
         __syncwarp();
@@ -854,11 +854,11 @@ __global__ void __launch_bounds__(kThreads) k_weigh_join(AttnArgs p, int pieces,
     grid_next();
     int64_t total, chunk;
     const int c = blockIdx.x;
-    const Place at = schedule<RU>(p, pieces, c + 1, 0, false, &total, &chunk);
+    const Place at = schedule<RU, WeighBatch>(p, pieces, c + 1, 0, false, &total, &chunk);
     const int64_t border = (c + 1) * chunk;
     Unit u;
     if (border < total)
-        unit_at<RU>(p, at, 1, &u);
+        unit_at<RU, WeighBatch>(p, at, 1, &u);
     grid_wait();
     if (border >= total || u.b0 == 0 || u.b0 > chunk)
         return;   // nothing there, or begins at the border, or before block c

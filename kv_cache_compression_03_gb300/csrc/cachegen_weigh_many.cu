@@ -96,7 +96,7 @@ struct TileWork {
 __device__ __forceinline__ int32_t units_of(const AttnArgs &p, int r, AttnRequest *q)
 {
     uint32_t error;
-    if (r >= p.a.requests || !attn_request(p, r, q, &error) || q->rows <= p.few_rows)
+    if (r >= p.a.requests || !attn_request<WeighBatch::kShared>(p, r, q, &error) || q->rows <= p.few_rows)
         return 0;
     return (q->rows + kTile - 1) / kTile * p.heads;
 }

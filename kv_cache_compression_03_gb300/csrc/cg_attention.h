@@ -11,7 +11,7 @@ struct AttnArgs {
                             // kernel for few rows
     float scale2;           // scale * log2(e)
     int64_t kv_limit;       // most tokens of a request
-    int32_t least_unit;     // few rows: blobs that a request and head count as at least (0: as they are)
+    int32_t least_unit;     // few rows, shared tokens and weights: blobs that a request and head count as at least
     // Where all requests begin with the same tokens, either each of them reads those, the first
     // `front`, by way of the table's first row; or one pass takes the first `shared`, all rows
     // of the batch as one request's, and leaves its results in rows, and the other takes the
@@ -33,28 +33,30 @@ struct AttnRequest {
 };
 
 // False for a request without rows and for an invalid one, which *error
-// then names.
+// then names. kShared: there may be shared tokens (p.first, p.shared, p.front).
+template <bool kShared>
 __device__ __forceinline__ bool attn_request(const AttnArgs &p, int r, AttnRequest *q,
                                              uint32_t *error)
 {
     // in the pass over the shared tokens cu_q points at its last entry, the batch's rows (all that
     // there can be where it is beyond them: the other pass, whose requests lie before it, reports it)
-    const int32_t c0 = p.first ? 0 : p.a.cu_q[r];
-    const int32_t c1 = p.first ? min(p.a.cu_q[0], p.a.tokens) : p.a.cu_q[r + 1];
-    const bool shares = !p.first && p.shared + p.front > 0;
-    const int32_t kv = p.first ? p.shared : p.a.kv_lens[r];
+    const bool first = kShared && p.first;
+    const int32_t c0 = first ? 0 : p.a.cu_q[r];
+    const int32_t c1 = first ? min(p.a.cu_q[0], p.a.tokens) : p.a.cu_q[r + 1];
+    const bool shares = kShared && !first && p.shared + p.front > 0;
+    // (of rows from there on the pass over the shared tokens left nothing)
+    const int32_t most = shares ? min(p.a.cu_q[p.a.requests], p.a.tokens) : p.a.tokens;
+    const int32_t kv = first ? p.shared : p.a.kv_lens[r];
     *error = CG_OK;
-    if (c0 < 0 || c1 < c0 || c1 > p.a.tokens || kv < 0 || kv > p.kv_limit)
-        *error = CG_ERR_CORRUPT;
-    else if (shares && c1 > c0 && c1 > p.a.cu_q[p.a.requests])   // rows that the pass over the shared tokens had not
+    if (c0 < 0 || c1 < c0 || c1 > most || kv < 0 || kv > p.kv_limit)
         *error = CG_ERR_CORRUPT;
     else if (p.a.max_q_len > 0 && c1 - c0 > p.a.max_q_len)
         *error = CG_ERR_INVALID_ARG;
     else if (shares && c1 > c0 && kv - (p.shared + p.front) < c1 - c0)
         *error = CG_ERR_INVALID_ARG;
     q->row0 = c0;
-    q->kv = p.first ? kv : kv - p.shared;
-    q->x0 = p.first ? kv - 1 : q->kv - (c1 - c0);
+    q->kv = first || !kShared ? kv : kv - p.shared;
+    q->x0 = first ? kv - 1 : q->kv - (c1 - c0);
     q->rows = (c1 - c0) * p.ratio;   // at most tokens * q_heads, which fits
     return *error == CG_OK && c1 > c0;
 }

@@ -15,14 +15,23 @@ constexpr float kNone = -3.0e38f;   // no maximum yet; finite, so that differenc
 
 // ---------------------------------------------------------------- schedule
 
+// What a kernel's batch has besides: shared tokens (as attn_request has it), and units that have to count as
+// more blobs than they have (p.least_unit). Known to the compiler: looked at when a call runs, the two cost attention
+// that has neither up to 1 us of its smallest call and 1 % of a prompt of 8192 tokens (558 us, 554 so).
+template <bool kSharedTokens, bool kLeastUnit>
+struct BatchOf {
+    static constexpr bool kShared = kSharedTokens, kLeast = kLeastUnit;
+};
+
 // The blobs that a request's rows can see: [0, sink) and [sink + skip, ..),
 // nb of them (at least 1, so that every row gets its output). A unit counts as nb blobs of the line;
-// where it has to count as more than it has (p.least_unit), `real` of them are there and pieces of the
+// where it has to count as more than it has, `real` of them are there and pieces of the
 // unit take as large a part of those.
 struct Span {
     int32_t nb, sink, skip, real;
 };
 
+template <typename K>
 __device__ __forceinline__ Span span_of(const AttnArgs &p, const AttnRequest &q)
 {
     const int32_t end = (q.kv + 15) / 16;
@@ -40,17 +49,17 @@ __device__ __forceinline__ Span span_of(const AttnArgs &p, const AttnRequest &q)
     if (s.nb < 1)
         s.nb = 1;
     s.real = s.nb;
-    if (s.nb < p.least_unit)
+    if (K::kLeast && s.nb < p.least_unit)
         s.nb = p.least_unit;
     return s;
 }
 
-template <int RU>
+template <int RU, typename K>
 __device__ __forceinline__ int64_t work_of(const AttnArgs &p, int r, AttnRequest *q, uint32_t *error)
 {
-    if (!attn_request(p, r, q, error) || q->rows > p.few_rows)
+    if (!attn_request<K::kShared>(p, r, q, error) || q->rows > p.few_rows)
         return 0;
-    return (int64_t)((q->rows + RU - 1) / RU) * p.heads * span_of(p, *q).nb;
+    return (int64_t)((q->rows + RU - 1) / RU) * p.heads * span_of<K>(p, *q).nb;
 }
 
 struct Place {   // a point of the line
@@ -69,7 +78,7 @@ __device__ __forceinline__ int64_t piece_of(int64_t total, int pieces)
 
 // Block-wide: the line's length, the blobs of a piece, and the place of
 // piece `piece` plus `plus`. Block 0 of the main kernel reports bad requests.
-template <int RU>
+template <int RU, typename K>
 __device__ __forceinline__ Place schedule(const AttnArgs &p, int pieces, int piece, int plus, bool report,
                                           int64_t *total_out, int64_t *chunk_out)
 {
@@ -78,7 +87,7 @@ __device__ __forceinline__ Place schedule(const AttnArgs &p, int pieces, int pie
         if (r >= p.a.requests)
             return 0;
         uint32_t error;
-        const int64_t w = work_of<RU>(p, r, q, &error);
+        const int64_t w = work_of<RU, K>(p, r, q, &error);
         if (say && error != CG_OK)
             int4_set_status(p.status, error);
         return w;
@@ -165,12 +174,12 @@ struct Unit {
 };
 
 // Finds the unit at a place; `left` blobs of the piece remain.
-template <int RU>
+template <int RU, typename K>
 __device__ __forceinline__ void unit_at(const AttnArgs &p, const Place &at, int64_t left, Unit *u)
 {
     u->q = at.q;
     u->r = at.r;
-    u->span = span_of(p, u->q);
+    u->span = span_of<K>(p, u->q);
     u->tiles = (u->q.rows + RU - 1) / RU;
     const int32_t i = at.off >> 31 ? (int32_t)(at.off / u->span.nb) : (int32_t)at.off / u->span.nb;
     u->h = i / u->tiles;
@@ -181,7 +190,7 @@ __device__ __forceinline__ void unit_at(const AttnArgs &p, const Place &at, int6
 }
 
 // The next unit of the line (the caller knows that there is one).
-template <int RU>
+template <int RU, typename K>
 __device__ __forceinline__ void unit_next(const AttnArgs &p, int64_t left, Unit *u)
 {
     if (++u->rt == u->tiles) {
@@ -189,13 +198,13 @@ __device__ __forceinline__ void unit_next(const AttnArgs &p, int64_t left, Unit 
         if (++u->h == p.heads) {
             u->h = 0;
             uint32_t error;
-            while (++u->r < p.a.requests && work_of<RU>(p, u->r, &u->q, &error) == 0)
+            while (++u->r < p.a.requests && work_of<RU, K>(p, u->r, &u->q, &error) == 0)
                 ;
             if (u->r >= p.a.requests) {   // not reached while blobs are left
                 u->b0 = u->b1 = 0;
                 return;
             }
-            u->span = span_of(p, u->q);
+            u->span = span_of<K>(p, u->q);
             u->tiles = (u->q.rows + RU - 1) / RU;
         }
     }
@@ -204,10 +213,11 @@ __device__ __forceinline__ void unit_next(const AttnArgs &p, int64_t left, Unit 
 }
 
 // A warp's stretch of a unit's blobs in this piece.
+template <typename K>
 __device__ __forceinline__ void warp_range(const Unit &u, int warp, int *b, int *e)
 {
     int b0 = u.b0, b1 = u.b1;
-    if (u.span.real != u.span.nb) {
+    if (K::kLeast && u.span.real != u.span.nb) {
         b0 = (int)((int64_t)b0 * u.span.real / u.span.nb);
         b1 = (int)((int64_t)b1 * u.span.real / u.span.nb);
     }

@@ -22,6 +22,8 @@ struct WeighArgs {
 
 namespace {
 
+using WeighBatch = BatchOf<false, true>;
+
 // Row tiles of 8 of request r lie from here on. (Of a rows before it and b of its own, ceil(b / 8)
 // is at most floor((a + b) / 8) - floor(a / 8) + 1.)
 __device__ __forceinline__ int32_t first_slot(const AttnArgs &p, int r, int32_t row0)
@@ -72,7 +74,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, F eac
         uint32_t error;
         int64_t w = 0;
         if (at->r0 + lane < p.a.requests) {
-            attn_request(p, at->r0 + lane, q, &error);
+            attn_request<WeighBatch::kShared>(p, at->r0 + lane, q, &error);
             if (error == CG_OK && each(*q) > 0)
                 w = (int64_t)((q->kv + each(*q) - 1) / each(*q)) * p.heads;
         }
@@ -92,7 +94,7 @@ __device__ __forceinline__ bool find_item(const AttnArgs &p, int64_t item, F eac
         const int src = __ffs(mine) - 1;
         const int64_t off = __shfl_sync(0xFFFFFFFFu, item - start, src);
         *r = at->r0 + src;
-        attn_request(p, *r, q, &error);
+        attn_request<WeighBatch::kShared>(p, *r, q, &error);
         const int i = (int)(off / p.heads);
         *h = (int)(off - (int64_t)i * p.heads);
         *tok = i * each(*q);

@@ -1219,7 +1219,7 @@ extern "C" cg_status cg_int4_weigh(const cg_int4_cache *c, int32_t layer, const 
     if (st != CG_OK || (w->out == nullptr && w->width > 0) || !int4_aligned(w->in, 4) || !int4_aligned(w->out, 4) ||
         !int4_aligned(workspace, 256))
         return CG_ERR_INVALID_ARG;
-    if (w->in == w->out &&
+    if (w->in != nullptr && w->in == w->out &&
         (w->in_request_stride != w->out_request_stride || w->in_head_stride != w->out_head_stride))
         return CG_ERR_INVALID_ARG;
     if (workspace_bytes < need || workspace == nullptr)

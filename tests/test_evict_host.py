@@ -103,6 +103,17 @@ def test_weigh_refusals(lib):
     assert go(args=_args(out=0, out_token_stride=3), size=0) == cg.CG_ERR_CAPACITY
 
 
+def test_weigh_of_no_earlier_weights_into_rows_without_room(lib):
+    """in and out are both none, and are not the same rows: in's strides are not looked at."""
+    n = ct.c_size_t(0)
+    w = _weights(in_=0, out=0, in_request_stride=0, in_head_stride=0, out_request_stride=4, out_head_stride=1, width=0)
+    assert lib.cg_int4_weigh_workspace(ct.byref(_cache()), ct.byref(_args()), ct.byref(w), ct.byref(n)) == cg.CG_OK
+    # all arguments are looked at before the workspace
+    assert lib.cg_int4_weigh(ct.byref(_cache()), 0, ct.byref(_args()), ct.byref(w), None, 0, None) == cg.CG_ERR_CAPACITY
+    w = _weights(in_=0, out=FAKE, in_request_stride=-1, in_head_stride=7)
+    assert lib.cg_int4_weigh(ct.byref(_cache()), 0, ct.byref(_args()), ct.byref(w), None, 0, None) == cg.CG_ERR_CAPACITY
+
+
 def _choice(**kw):
     return _make(cg.cg_token_choice, dict(weights=FAKE, layer_stride=4096, request_stride=1024, head_stride=256, layers=2,
                                           requests=3, heads=4, width=200, lens=FAKE, budget=50, recent=8, sinks=4,

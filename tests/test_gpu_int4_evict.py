@@ -304,6 +304,17 @@ def test_weigh_without_rows_or_requests():
     assert torch.equal(a, b)
 
 
+def test_weigh_from_nothing_into_rows_without_room():
+    rng = np.random.default_rng(3)
+    _, _, got, _, _ = _weigh_case(rng, [0, 0], [40, 0], 2, 64, 32, 16)
+    q, lens = torch.empty(0, 4, 64, dtype=torch.bfloat16, device="cuda"), _ints([0, 0])
+    none = got.weigh(q, _ints([0, 0, 0]), lens, _ints(np.empty((2, 0))))          # a table of no pages
+    assert none.shape == (2, 2, 0)
+    out = torch.empty(2, 2, 0, device="cuda")
+    assert got.weigh(q, _ints([0, 0, 0]), lens, _ints([[1], [0]]), out=out) is out
+    got.check()
+
+
 def test_weigh_with_tables_and_rows_of_other_widths():
     """The same call but for how far its table and its weights reach."""
     rng = np.random.default_rng(21)

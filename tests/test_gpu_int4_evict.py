@@ -639,6 +639,80 @@ def test_compact_reports_pages_outside_the_cache():
     _same_bytes(want, got)
 
 
+def _move(cache, first_layer, kept, new_lens, lens, table, weights):
+    """evict.compact, all tokens of a list at once."""
+    D, g, page = cache.dim, cache.dim // cache.group, cache.page
+    a = 8 * D + 64 * g
+
+    def places(r, j):   # page, blob, bytes of the tokens
+        slot = table[r][j // page].astype(np.int64) * page + j % page
+        tok = slot[:, None] % 16
+        v = a + tok // 2 * D + 2 * (tok % 2) + np.arange(D).reshape(-1, 4)[:, :2].reshape(-1)
+        at = np.concatenate([tok * (D // 2) + np.arange(D // 2), 8 * D + tok * 4 * g + np.arange(4 * g), v,
+                             a + 8 * D + tok * 4 * g + np.arange(4 * g)], 1)
+        return slot[:, None] // page, slot[:, None] % page // 16, at
+
+    for l, r, h in np.ndindex(*kept.shape[:3]):
+        n, m = int(new_lens[r]), int(lens[r])
+        if n == m:
+            continue
+        data, src = cache.data[first_layer + l], kept[l, r, h, :n].astype(np.int64)
+        p, b, at = places(r, src)
+        got = data[p, h, b, at].copy()
+        p, b, at = places(r, np.arange(n))
+        data[p, h, b, at] = got
+        w = weights[l, r, h, src].copy()
+        weights[l, r, h, :m] = 0
+        weights[l, r, h, :n] = w
+
+
+def test_numpy_moves_agree():
+    rng = np.random.default_rng(1)
+    want, got, table = _random_cache(rng, 1, [70, 40], 2, 64, 32, 16)
+    kept, new = _random_kept(rng, 1, [70, 40], 2, 33)
+    a, b = rng.random((1, 2, 2, 70)), None
+    b, other = a.copy(), ref.Cache(*want.shape)
+    other.data[:] = want.data
+    evict.compact(want, 0, kept, new, [70, 40], table, a)
+    _move(other, 0, kept, new, [70, 40], table, b)
+    assert np.array_equal(want.data, other.data) and np.array_equal(a, b)
+
+
+# layers, requests, heads, tokens, those that stay: a block to a list, and clusters of two, four and eight to one, each in
+# more rounds of 128 tokens to a block than it reads ahead; lists of odd lengths
+@pytest.mark.parametrize("layers,requests,heads,top,budget,blocks", [
+    (5, 8, 4, 1500, 1301, 1), (1, 10, 12, 3100, 2700, 4), (2, 2, 1, 9000, 7999, 8), (1, 1, 1, 9000, 8000, 8),
+    (1, 152, 1, 700, 655, 1), (1, 151, 1, 2800, 2577, 4), (1, 100, 1, 2300, 2100, 4), (1, 99, 1, 4500, 4201, 8)])
+@pytest.mark.parametrize("how", ["random", "one goes early", "one goes late", "from within a blob"])
+def test_compact_in_rounds(layers, requests, heads, top, budget, blocks, how):
+    rng = np.random.default_rng(top + budget)
+    dim, group, page = 64, 32, 48
+    lists, size = layers * requests * heads, 1
+    while size < 8 and lists < 152 and lists * size < 400:
+        size *= 2
+    assert size == blocks and budget > 4 * 128 * blocks   # the case is what it says: five rounds at least
+    lens = [top - (i * 37) % max(1, (top - budget) // 2) for i in range(requests)]
+    want, got, table = _random_cache(rng, layers, lens, heads, dim, group, page)
+    if how in ("random", "from within a blob"):
+        kept, new = _random_kept(rng, layers, lens, heads, budget)
+        if how == "from within a blob":   # the first stay in place, 13 of a blob's tokens among them
+            first = 16 * 40 + 13
+            for l, r, h in np.ndindex(*kept.shape[:3]):
+                kept[l, r, h, :first] = np.arange(first)
+                kept[l, r, h, first:] = first + 1 + np.sort(rng.permutation(lens[r] - first - 1)[:budget - first])
+    else:
+        at = 5 if how == "one goes early" else budget - 70
+        kept = np.broadcast_to(np.delete(np.arange(budget + 1, dtype=np.int32), at), (layers, requests, heads, budget)).copy()
+        new = np.full(requests, budget, np.int32)
+    w = rng.random((layers, requests, heads, top + 3)).astype(np.float32)
+    wt = _floats(w)
+    got.compact(_ints(kept), _ints(new), _ints(lens), _ints(table), weights=wt)
+    got.check()
+    _move(want, 0, kept, new, lens, table, w)
+    _same_bytes(want, got)
+    assert np.array_equal(wt.cpu().numpy(), w)
+
+
 def test_compact_and_choose_of_nothing():
     rng = np.random.default_rng(8)
     want, got, table = _random_cache(rng, 1, [20], 2, 64, 32, 16)

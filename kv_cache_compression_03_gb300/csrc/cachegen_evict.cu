@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(T, 1024 / T) k_choose_tokens(cg_token_choice c
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Rows too long for the registers of a cluster (131072 tokens and more): a block to a row, which it reads from
+// Rows too long for the registers of a cluster (more than 131072 tokens): a block to a row, which it reads from
 // memory for each of four digits of 8 bits, to count what stays before each warp, and to write.
 __global__ void __launch_bounds__(kChooseThreads) k_choose_long(cg_token_choice c)
 {

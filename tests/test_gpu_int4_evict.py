@@ -454,6 +454,15 @@ def test_choose(layers, lens, width, budget, recent, sinks, kind):
     assert np.array_equal(got.kept.cpu().numpy(), kept)
 
 
+# the widest rows that a cluster holds (131072: 8 blocks of 512 threads, 32 tokens each), and the next
+@pytest.mark.parametrize("lens,width,budget,recent,sinks", [
+    ([98305, 90001], 98305, 4096, 64, 4), ([131072, 131071], 131072, 4000, 256, 16), ([131072], 131072, 130000, 0, 0),
+    ([131073, 131072], 131073, 4096, 64, 4)])
+@pytest.mark.parametrize("kind", ["random", "ties", "odd"])
+def test_choose_from_the_widest_rows(lens, width, budget, recent, sinks, kind):
+    test_choose(None, lens, width, budget, recent, sinks, kind)
+
+
 def test_choose_strides_out_graph_and_bad_lengths():
     rng = np.random.default_rng(1)
     base = _floats(rng.random((3, 4, 2, 210)))

@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_attention_many_join(AttnArgs p
     grid_wait();
     if (work.cut[1] == 1)
         return;
-    const int lane = threadIdx.x & 31, rows = work.cut[0] * kRows;   // fewer units than blocks
+    const int lane = threadIdx.x & 31, rows = work.cut[0] * kRows;   // (units that are cut are no more than items)
     for (int at = (blockIdx.x * kJoinThreads + threadIdx.x) >> 5; at < rows; at += gridDim.x * kJoinThreads / 32) {
         const Unit &u = work.heads[at / kRows];
         const int row = at % kRows, rr = u.row0 + row;

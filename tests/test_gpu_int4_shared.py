@@ -199,6 +199,34 @@ def test_bounds_of_rows_that_do_not_ascend(nq, monkeypatch):
                 assert (out[rows] == 3.0).all(), (at, r)
 
 
+def _pieces(units, tiles, items, blocks):
+    """Into how many pieces each unit of shared tokens is cut: the longest block's time counts, a piece's being its
+    tiles and three more."""
+    can = [s for s in range(1, 32) if s == 1 or (s <= tiles // 2 and units * s <= items)]
+    return min(can, key=lambda s: (-(-units * s // blocks) * (-(-tiles // s) + 3), s))
+
+
+# new tokens of each request, KV heads, shared tokens: 100 units of 256 rows each, cut in three. Two full row
+# tiles to a unit; one row tile, whose softmax groups take turns at five tiles; the two kinds by turns
+@pytest.mark.parametrize("nq,heads,shared", [([640, 640], 20, 1536), ([50, 50], 100, 1920), ([100, 200], 50, 1920)])
+def test_more_pieces_than_blocks(nq, heads, shared):
+    rng = np.random.default_rng(heads)
+    blocks = min(torch.cuda.get_device_properties(0).multi_processor_count, 160)
+    units = -(-sum(nq) // 256) * heads
+    pieces = _pieces(units, shared // 128, min(max(units * 31, 160), 640), blocks)
+    assert pieces == 3 and units * pieces > blocks
+    table, want, got, cu, q, lens = _case(rng, nq, [n + 9 for n in nq], shared, heads, 1, 64, 32, 64)
+    o, tol = ref.attention(want, 0, q, cu, lens, table, 0, 0, 0.125)
+    args = (_dev(q), _ints(cu), _ints(lens), _ints(table))
+    out = got.attention(*args, shared=shared, max_q_len=max(nq))
+    got.check()
+    over = np.abs(_np(out) - o) - tol
+    assert (over <= 0).all(), float(over.max())
+    for _ in range(5):
+        assert torch.equal(got.attention(*args, shared=shared, max_q_len=max(nq)), out)
+    got.check()
+
+
 @pytest.mark.parametrize("nq,n", [(1, 5), (1, 30), (50, 3)])
 def test_the_same_bits_in_graphs_and_on_streams(nq, n):
     rng = np.random.default_rng(2)

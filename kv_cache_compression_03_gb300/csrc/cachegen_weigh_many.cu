@@ -88,7 +88,7 @@ struct TileShared {
 
 struct TileWork {
     int32_t most;        // units that there is room for
-    int32_t *cut;        // units, pieces of each; then, of either pass, items taken behind the blocks' first
+    int32_t *cut;        // units; then, of either pass, items taken behind the blocks' first
     Piece *heads;        // [units]: their first pieces
     float2 *parts;       // [items][2][128]: m, l of an item's even tiles and of its odd ones
 };
@@ -246,7 +246,8 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
             AttnRequest q;
             mine += units_of(p, r, &q);
         }
-        // only whether there are fewer than blocks matters
+        // exact where the batch is right: parts of 2 KB a unit are within the bound on the workspace, so units are
+        // fewer than 2^20; of more, only that they are too many matters
         const int few = __reduce_add_sync(0xFFFFFFFFu, (int)min(mine, (int64_t)(1 << 20)));
         if (lane == 0)
             atomicAdd(&sm.units, few);
@@ -263,7 +264,6 @@ __global__ void __launch_bounds__(kAllThreads, 1) k_weigh_tiles(AttnArgs p, Weig
     const int split = sm.units > 0 && sm.units < gridDim.x ? gridDim.x / sm.units : 1;
     if (!kSums && blockIdx.x == 0 && tid == 0) {
         work.cut[0] = min(sm.units, work.most);
-        work.cut[1] = split;
         if (sm.units > work.most)   // more than a batch of so many tokens has: requests that share rows of q
             int4_set_status(p.status, CG_ERR_CORRUPT);
     }
@@ -850,7 +850,7 @@ size_t weigh_many_workspace(const cg_int4_cache *c, const cg_attention *a, int32
     return sizes_of(c, a, tokens).bytes();
 }
 
-int32_t *weigh_many_taken(void *ws) { return static_cast<int32_t *>(ws) + 2; }
+int32_t *weigh_many_taken(void *ws) { return static_cast<int32_t *>(ws) + 1; }
 
 cudaError_t weigh_many_launch(const AttnArgs &p, WeighArgs a, const cg_int4_cache *c, void *ws, cudaStream_t s)
 {

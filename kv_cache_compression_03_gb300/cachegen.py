@@ -1094,7 +1094,8 @@ class Int4Cache:
         With ``shared``, a multiple of page_tokens, the first ``shared`` tokens of every
         request lie in the same pages (kv_lens counts them, every row of block_table names
         them; those of its first row are read): where there are enough of them they are read
-        once for the whole batch. Not with a window."""
+        once for the whole batch. Not with a window. Requests with few rows may then have the
+        roundings and the limit on V of those with many (the header names them)."""
         if stream is not None:
             return _on_stream(stream, self.attention, q, cu_q, kv_lens, block_table, layer, window,
                               sinks, scale, max_q_len, out, None, shared)

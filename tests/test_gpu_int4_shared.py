@@ -227,6 +227,26 @@ def test_more_pieces_than_blocks(nq, heads, shared):
     got.check()
 
 
+@pytest.mark.parametrize("nq,n", [(1, 3), (1, 40), (70, 2)])
+@pytest.mark.parametrize("vscale", [2.0 ** 92, 2.0 ** -100])
+def test_values_to_the_ends_of_the_range(nq, n, vscale):
+    """V below 2^96 (2^92 times what no normal draw of these few passes), and small ones."""
+    rng = np.random.default_rng(nq + n)
+    heads, dim, page, shared = 2, 64, 16, 960
+    table, want, got, cu, q, lens = _case(rng, [nq] * n, [nq + 9] * n, shared, heads, 2, dim, 32, page)
+    for r, m in enumerate(lens):
+        x = np.arange(m)[0 if r == 0 else shared:]
+        v = _rand(rng, len(x), heads, dim, scale=vscale)
+        assert np.abs(v).max() < 16 * vscale
+        want.store(0, _rand(rng, len(x), heads, dim), v, table[r][x // page] * page + x % page)
+    _copy(want, got)
+    o, tol = ref.attention(want, 0, q, cu, lens, table, 0, 0, 0.125)
+    out = got.attention(_dev(q), _ints(cu), _ints(lens), _ints(table), max_q_len=nq, shared=shared)
+    got.check()
+    # small values: the codes of the kernel for few rows are summed in units that end at 2^-106
+    assert (np.abs(_np(out) - o) <= tol + 2.0 ** -108 * max(lens)).all()
+
+
 @pytest.mark.parametrize("nq,n", [(1, 5), (1, 30), (50, 3)])
 def test_the_same_bits_in_graphs_and_on_streams(nq, n):
     rng = np.random.default_rng(2)

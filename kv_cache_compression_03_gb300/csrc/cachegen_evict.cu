@@ -812,6 +812,9 @@ extern "C" cg_status cg_choose_tokens(const cg_token_choice *c, cg_stream_t stre
     if (rows > 0) {
         // Blocks to a row that go by digits: as many as hold it, and more while there are SMs for them. Small blocks,
         // four on an SM, where they do: what bounds them is each block's chain of barriers.
+        // It goes by the rows' room, lengths being known to the GPU alone: 512 rows of 4608 tokens with room for as many
+        // 14 us, for 32768 30, for 131072 98 (clusters of eight large blocks, most of which find no token), for
+        // 140000 21 (the kernel that reads from memory).
         constexpr int kSmall = 256, kLarge = 512, kMost = 32;   // threads; tokens of one
         int size = 1;
         while (size < kMostCluster && c->width > kMost * kSmall * size)

@@ -26,7 +26,7 @@ namespace {
 constexpr int kRing = 8;           // blobs in a warp's ring
 constexpr int kItemTokens = 64;    // of a block in the second pass, a blob to a warp; or,
 // from so many rows on, a blob to a block, whose warps share the rows. (Without stored scores and without room
-// for the sums of kTileRows' kernel, so with tables of millions of tokens.)
+// for the sums of kTileRows' kernel: a prompt of 32768 tokens, say, or a chunk of 8192 under a table for 131072.)
 constexpr int kManyRows = 512;
 constexpr int kMaxBlocks = 640;    // of the first pass
 
@@ -336,8 +336,8 @@ __device__ __forceinline__ float raise(float top, bool no_row, float *m, float *
 // Blocks on an SM.
 constexpr int kStatBlocks = 3;
 
-// For 8 NT rows of a (request, KV head) at a time. 32 rows of 32768 tokens, 8 KV heads: 46 us with all that
-// follows, 64 rows 67. What bounds it is instructions: a blob's keys are made once (4 a pair of codes) and
+// For 8 NT rows of a (request, KV head) at a time. 12 rows of 32768 tokens, 8 KV heads: 31 us with all that
+// follows, 32 rows 41, 64 rows 63. What bounds it is instructions: a blob's keys are made once (4 a pair of codes) and
 // meet NT tiles of 8 rows, each of whose scores takes an exponential and a store.
 //
 // kStored: scores are left for the sums, else the queries.
@@ -1131,17 +1131,22 @@ struct WeighSizes {
 };
 
 // Requests with more rows than this go to the kernels for many (cachegen_weigh_many.cu), where there is room
-// for their sums by row tiles. Here and there, 8 KV heads of 128: one request of 32768 tokens with 32 rows 46 us and
-// 76, 48 rows 62 and 76, 64 rows 67 and 76; eight of 16384 with 64 rows 209 and 237, 64 of 1024 with 64 rows 124
-// and 148 (there some 3 % more since). More rows here would read K again for each 32.
+// for their sums by row tiles. Here and there, 8 KV heads of 128: one request of 32768 tokens with 32 rows 41 us and
+// 75, 48 rows 58 and 75, 64 rows 63 and 76; eight of 16384 with 64 rows 199 and 231, 64 of 1024 with 64 rows 118
+// and 138. More rows here would read K again for each 32.
 // Their seven launches take 31 us where there is little to do, so small batches stay here up to twice the rows: of 80
 // rows, one head of 1024 tokens 25 and 31, eight of 4096 29 and 39, of 16384 55 and 53; of 128 rows, eight heads of
 // 1024 tokens 31 and 35, of 4096 41 and 39.
 constexpr int kTileRows = 64;
 constexpr int64_t kFewPairs = 3 << 20;   // of a row and a token
-constexpr size_t kMostSums = (size_t)1 << 30;   // bytes
+// Bytes. Both bound the workspace and cost time: they go by what the table may hold (its rows are not known
+// when the workspace is taken), and what passes them is read and computed again instead. Here and with room for
+// them, 32 query and 8 KV heads of 128: a prompt of 32768 tokens (1.02 GB of sums) 49 ms and 18.7, one of 16384 has
+// the room and takes 4.8; a chunk of 8192 of 16384 tokens under a table for 131072 9.1 ms and 3.7. 64 requests of
+// 4096 to 8192 tokens, a query each, under a table for 65536 (537 MB of scores) 462 us and 88.
+constexpr size_t kMostSums = (size_t)1 << 30;
 
-constexpr size_t kMostScores = (size_t)256 << 20;   // bytes
+constexpr size_t kMostScores = (size_t)256 << 20;
 constexpr int32_t kMostTokens = INT32_MAX - 65535;
 
 WeighSizes sizes_of(const cg_int4_cache *c, const cg_attention *a, const cg_token_weights *w)

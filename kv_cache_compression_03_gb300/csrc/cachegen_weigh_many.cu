@@ -25,8 +25,8 @@
 // What bounds it: a tile takes some 2300 cycles in the first pass and 3000 in the second. Its products are 1280,
 // which the shared memory's rate sets (two operands of 4 KB in 64 cycles), the expansion of its keys and its
 // exponentials about as much each; they overlap, but hand the two buffers of keys and scores on by barriers.
-// One request of 32768 tokens, 128 rows, 32 query and 8 KV heads: 29 + 32 us, with all else 78; two prompts of
-// 2048 at 4 rows to a token: 192. Products alone would be 9 of the 29. (Built, and not better, when those two took
+// One request of 32768 tokens, 128 rows, 32 query and 8 KV heads: 29 + 32 us, with all else 76; two prompts of
+// 2048 at 4 rows to a token: 190. Products alone would be 9 of the 29. (Built, and not better, when those two took
 // 76 and 188: 256 rows to a block, whose low parts had one buffer, 88 and 183; 16 expanding warps of half a blob, 84 and
 // 224; two accumulators for a tile of scores, 81 and 208, for a fifth less of error.)
 

@@ -1014,7 +1014,7 @@ class Int4Cache:
         self._c.data, self._c.status = data.data_ptr(), self.status.data_ptr()
         self.num_layers, self.num_pages, self.page_tokens = num_layers, num_pages, page_tokens
         self.num_heads, self.head_size, self.group = num_heads, head_size, group
-        self._sizes = {}   # workspace of attention calls, by their rows
+        self._sizes = {}   # workspaces of attention and weigh, by the sizes that they go by
 
     def _rows(self, k, v, tokens, layers, written):
         shape = (tokens, self.num_heads, self.head_size)

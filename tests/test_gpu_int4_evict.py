@@ -279,6 +279,29 @@ def test_weigh_reports_bad_requests_and_pages(nq):
     assert np.allclose(out[1, :, :200].sum(-1), 2 * nq, rtol=2.0 ** -12)
 
 
+@pytest.mark.parametrize("nq", [1, 40, 150])
+def test_weigh_of_bounds_of_rows_that_do_not_ascend(nq):
+    """The requests that they leave, whose rows follow one another, are right; the others' weights stay as they were."""
+    rng = np.random.default_rng(nq)
+    nkv = [nq + 300, nq + 7, nq + 500, nq]
+    table, want, got, cu, q = _weigh_case(rng, [nq] * 4, nkv, 2, 64, 32, 16)
+    width = table.shape[1] * 16
+    exact, tol = evict.weigh(want, 0, q, cu, nkv, table, 0, 0, 0.125, width)
+    for at, right in (([0, 1, 2, 3, 5], [0, 1, 2]), ([0, 1, 2, 3, 2], [0, 1, 2]), ([0, 1, 2, 3, -1], [0, 1, 2]),
+                      ([0, 9, 2, 3, 4], [2, 3]), ([0, 1, -3, 3, 4], [0, 3]), ([0, 1, 2, 1 << 22, 4], [0, 1])):
+        out = torch.full((4, 2, width), -7.0, device="cuda")
+        got.weigh(_dev(q), _ints(np.array(at) * nq), _ints(nkv), _ints(table), out=out)
+        _status(got.check, cg.CG_ERR_CORRUPT)
+        o = out.cpu().numpy()
+        for r in range(4):
+            if r in right:
+                m = nkv[r]
+                assert (np.abs(o[r, :, :m] - exact[r, :, :m]) <= tol[r, :, :m] + 2.0 ** -23 * o[r, :, :m]).all(), (at, r)
+                assert (o[r, :, m:] == -7.0).all()
+            else:
+                assert (o[r] == -7.0).all(), (at, r)
+
+
 def test_weigh_without_rows_or_requests():
     rng = np.random.default_rng(3)
     table, want, got, cu, q = _weigh_case(rng, [0, 0], [40, 0], 2, 64, 32, 16)
@@ -720,6 +743,46 @@ def test_compact_in_rounds(layers, requests, heads, top, budget, blocks, how):
     _move(want, 0, kept, new, lens, table, w)
     _same_bytes(want, got)
     assert np.array_equal(wt.cpu().numpy(), w)
+
+
+def test_pages_of_a_layer_behind_4_gib():
+    """Offsets into a layer that pass 32 bits, second layer of two: weights, attention with shared tokens and the move."""
+    rng = np.random.default_rng(15)
+    heads, dim, group, page, shared, lens, budget = 8, 128, 32, 64, 128, [700, 260], 400
+    table, pages = _batch(rng, [1, 1], lens, page)
+    table[1, :shared // page] = table[0, :shared // page]
+    want, _ = _filled(rng, lens, table, pages, page, heads, dim, group)
+    bytes_of_page = want.data[0, 0].size
+    far = (1 << 32) // bytes_of_page + 3                     # pages of a layer before the first of these
+    got = cg.Int4Cache(2, far + pages, page, heads, dim, group,
+                       data=torch.empty(2 * (far + pages) * bytes_of_page, dtype=torch.uint8, device="cuda"))
+    there = got.data.view(2, far + pages, -1)[1, far:]
+    there.copy_(torch.from_numpy(want.data[0].reshape(pages, -1)))
+    at = np.where(table >= 0, table + far, -1)
+    q, cu, kw = _rand(rng, 2, 4 * heads, dim), np.arange(3), dict(layer=1, max_q_len=1)
+    args = (_dev(q), _ints(cu), _ints(lens), _ints(at))
+    w = got.weigh(*args, **kw)
+    exact, tol = evict.weigh(want, 0, q, cu, lens, table, 0, 0, dim ** -0.5, w.shape[2])
+    _check_weights(w.cpu().numpy(), np.zeros(w.shape, np.float32), exact, tol)
+    out = got.attention(*args, shared=shared, **kw)
+    o, tol = ref.attention(want, 0, q, cu, lens, table, 0, 0, dim ** -0.5)
+    assert (np.abs(_np(out) - o) <= tol).all()
+    many = _rand(rng, 260, 4 * heads, dim)                   # and of many rows
+    out = got.attention(_dev(many), _ints([0, 130, 260]), _ints(lens), _ints(at), shared=shared, layer=1)
+    o, tol = ref.attention(want, 0, many, [0, 130, 260], lens, table, 0, 0, dim ** -0.5)
+    assert (np.abs(_np(out) - o) <= tol).all()
+    w = got.weigh(_dev(many), _ints([0, 130, 260]), _ints(lens), _ints(at), layer=1)
+    exact, tol = evict.weigh(want, 0, many, [0, 130, 260], lens, table, 0, 0, dim ** -0.5, w.shape[2])
+    _check_weights(w.cpu().numpy(), np.zeros(w.shape, np.float32), exact, tol)
+    kept, new = _random_kept(rng, 1, lens, heads, budget)
+    kept[..., :shared] = np.arange(shared)                   # the shared pages stay as they are
+    for h in range(heads):
+        kept[0, 0, h, shared:] = shared + np.sort(rng.permutation(lens[0] - shared)[:budget - shared])
+    kept[0, 1, :, :lens[1]] = np.arange(lens[1])
+    got.compact(_ints(kept[0]), _ints(new), _ints(lens), _ints(at), layer=1)
+    got.check()
+    _move(want, 0, kept, new, lens, table, np.zeros((1, 2, heads, 700)))
+    assert np.array_equal(there.cpu().numpy(), want.data[0].reshape(pages, -1))
 
 
 def test_compact_and_choose_of_nothing():

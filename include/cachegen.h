@@ -552,7 +552,8 @@ cg_status cg_int4_attention(const cg_int4_cache *cache, int32_t layer, const cg_
  *
  * Limits and roundings are those of cg_int4_attention for requests with more than 32 rows per KV
  * head, however few a request has: where the shared tokens are read for all queries at once, those
- * may be taken by the kernel for many rows. So V values have to stay below 2^96, and k, v and the
+ * may be taken by the kernel for many rows. So V values have to stay below 2^96 (small ones may have
+ * the error that they have for few rows all the same), and k, v and the
  * probabilities may each be rounded to bf16 (2^-8 relative at most), where for few rows
  * cg_int4_attention rounds the probabilities' products with the groups' steps alone. 64 requests of one
  * token each and 16384 shared ones: the result is off by 0.0028 of its norm, by 0.0019 in a call without

@@ -1139,8 +1139,8 @@ struct WeighSizes {
 // 1024 tokens 31 and 35, of 4096 41 and 39.
 constexpr int kTileRows = 64;
 constexpr int64_t kFewPairs = 3 << 20;   // of a row and a token
-// Bytes. Both bound the workspace and cost time: they go by what the table may hold (its rows are not known
-// when the workspace is taken), and what passes them is read and computed again instead. Here and with room for
+// Bytes. Both bound the workspace and cost time: they go by what the table may hold (lengths are known to the GPU
+// alone), and what passes them is read and computed again instead. Here and with room for
 // them, 32 query and 8 KV heads of 128: a prompt of 32768 tokens (1.02 GB of sums) 49 ms and 18.7, one of 16384 has
 // the room and takes 4.8; a chunk of 8192 of 16384 tokens under a table for 131072 9.1 ms and 3.7. 64 requests of
 // 4096 to 8192 tokens, a query each, under a table for 65536 (537 MB of scores) 462 us and 88.
